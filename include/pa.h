@@ -396,6 +396,136 @@ pa_status pa_gather_rows(const void* src, int64_t src_rows, int64_t row_bytes,
                          const int32_t* rows, int32_t n, void* dst, pa_stream_t stream);
 
 /*
+ * The latent path: layers that cache one shared latent vector per token.
+ *
+ * Such a layer keeps, per token, a latent row c [latent_dim] and one rotary
+ * key row k_r [rope_dim]; the key and the value of head h are products of c,
+ *     k[h] = [ W_k[h] c ; k_r ],    v[h] = W_v[h] c.
+ * Scores and outputs can be taken in two forms that give the same result:
+ *   expanded   k and v of every head are made and attended to as usual
+ *              (pa_latent_prefill; fewest operations for long chunks);
+ *   absorbed   W_k[h]^T moves into the query and W_v[h] behind the output,
+ *              so that every head attends straight to the cache, with key
+ *              [c ; k_r] and value c (pa_latent_forward; a token's cache is
+ *              read once for all heads).
+ * The products with W are the caller's. pa_rope turns the queries' rotary
+ * part, pa_write_latent turns and stores a step's new rows, pa_read_latent
+ * fetches cached rows back for the expanded form.
+ */
+
+/*
+ * pa_rope — rotary positions. The first rot_dim dims of every head of every
+ * token are turned in pairs: pair i of token t by the angle
+ * positions[t] * inv_freq[i] (radians),
+ *     (x, y) -> factor * (x cos - y sin, y cos + x sin);
+ * the dims past rot_dim are copied unchanged.
+ *
+ *   x, out          dev bf16 [T][num_heads][head_dim], innermost dims
+ *                   contiguous, the token and head strides given in elements
+ *                   (>= 0; x may repeat rows with stride 0, rows of out must
+ *                   not overlap). out may be x itself, with the same strides
+ *                   (then turned in place); otherwise the two must not overlap.
+ *                   A rotary part at the end of a wider head is reached by
+ *                   pointing at it.
+ *   positions       dev int32 [T], any value
+ *   inv_freq        dev fp32 [rot_dim / 2]
+ *   rot_dim         even, 0 .. min(head_dim, 256)
+ *   layout          PA_ROPE_HALF: pair i is dims (i, i + rot_dim / 2);
+ *                   PA_ROPE_INTERLEAVED: dims (2i, 2i + 1)
+ *   factor          finite and positive (long-context scalings change inv_freq and this factor)
+ *
+ * Angles are exact to about 2^-24 of a turn at any position; fp32 arithmetic, one
+ * rounding to bf16 (nearest-even). The inverse turn is the same call with
+ * negated positions and 1 / factor. Errors: PA_ERR_INVALID (sizes, strides,
+ * NULL or misaligned pointers), PA_ERR_UNSUPPORTED (odd rot_dim or above 256).
+ */
+typedef enum pa_rope_layout { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
+
+pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                  int64_t out_token_stride, int64_t out_head_stride, const int32_t* positions,
+                  int32_t T, int32_t num_heads, int32_t head_dim, const float* inv_freq,
+                  int32_t rot_dim, int32_t layout, float factor, pa_stream_t stream);
+
+/*
+ * The latent block pool (caller-owned device memory, 16-byte aligned). Blocks,
+ * block tables and slots are those of pa_kv_pool; a cell is one token:
+ *     latent[num_blocks][block_size][latent_dim]   bf16, or E4M3 codes
+ *     rope  [num_blocks][block_size][rope_dim]     bf16
+ *     scales[num_blocks][block_size]               fp32, E4M3 pools only
+ * A code of token n stands for decode(code) * scales[n].
+ *
+ * Supported: latent_dim in {256, 512}; rope_dim 64; block_size in {16, 32, 64}.
+ */
+typedef struct pa_latent_pool {
+  void* latent;          /* dev */
+  void* rope;            /* dev */
+  float* scales;         /* dev; NULL for bf16 pools */
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t latent_dim;
+  int32_t rope_dim;
+  int32_t dtype;         /* pa_kv_dtype */
+} pa_latent_pool;
+
+/*
+ * pa_write_latent — scatter this step's latent rows and rotary keys into the
+ * pool by slot, as pa_write_kv does for keys and values.
+ *
+ *   latent        dev bf16 [T][latent_dim], token stride latent_stride
+ *                 (elements, a multiple of 8), 16-byte aligned
+ *   k_rope        dev bf16 [T][rope_dim], token stride rope_stride
+ *   positions     dev int32 [T], inv_freq dev fp32 [rope_dim / 2], layout and
+ *                 factor: k_rope is turned as pa_rope does before it is
+ *                 stored. Both NULL: stored as it comes.
+ *   slot_mapping  dev int64 [T]; slot < 0 marks a padding token (skipped)
+ *
+ * bf16 pools copy latent's bits. E4M3 pools store, per token,
+ *   scale = 2^e, the smallest with max |latent| <= 448 * 2^e over the finite
+ *           elements (e >= -60; 1 for a row of zeros),
+ *   code  = e4m3(latent / scale), nearest-even, saturating; NaN stores 0x7F,
+ * so that decode(code) * scale is exact in bf16 (up to bf16's range).
+ * A slot >= num_blocks*block_size sets PA_ERR_DEVICE_BOUNDS and is skipped.
+ * Duplicate slots within one call leave the cell unspecified.
+ */
+pa_status pa_write_latent(const pa_latent_pool* pool, const void* latent, int64_t latent_stride,
+                          const void* k_rope, int64_t rope_stride, const int32_t* positions,
+                          const float* inv_freq, int32_t layout, float factor,
+                          const int64_t* slot_mapping, int32_t T, pa_stream_t stream);
+
+/*
+ * pa_read_latent — cached rows of a batch of requests, gathered through their
+ * block tables into one ragged array and widened to bf16 (the input of the
+ * products that make the expanded keys and values of a context).
+ *
+ *   block_tables  dev int32 [num_reqs][max_blocks]
+ *   kv_start_loc  dev int32 [num_reqs+1], from 0, non-decreasing: request r's
+ *                 tokens are rows kv_start_loc[r] .. kv_start_loc[r+1]-1
+ *   first         dev int32 [num_reqs]: position of the request's first token
+ *                 that is read (NULL: 0), for contexts read in windows
+ *   num_tokens    rows of the outputs; rows past kv_start_loc[num_reqs] are
+ *                 left as they are
+ *   latent_out    dev bf16 [num_tokens][latent_dim], stride latent_stride
+ *                 (a multiple of 8), 16-byte aligned
+ *   rope_out      dev bf16 [num_tokens][rope_dim], stride rope_stride (even),
+ *                 4-byte aligned
+ *
+ * A position outside the table, a block outside the pool, kv_start_loc[0] != 0
+ * or more rows than num_tokens set PA_ERR_DEVICE_BOUNDS; such rows are skipped.
+ */
+pa_status pa_read_latent(const pa_latent_pool* pool, const int32_t* block_tables,
+                         int32_t max_blocks, const int32_t* kv_start_loc, const int32_t* first,
+                         int32_t num_reqs, int32_t num_tokens, void* latent_out,
+                         int64_t latent_stride, void* rope_out, int64_t rope_stride,
+                         pa_stream_t stream);
+
+/*
+ * pa_copy_latent_blocks — pa_copy_blocks for a latent pool (latents, rotary
+ * parts and scales); the same rules for src and dst.
+ */
+pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src,
+                                const int32_t* dst, int32_t n, pa_stream_t stream);
+
+/*
  * pa_get_error — synchronise `stream`, then return and clear the sticky
  * device error word of the current device: PA_ERR_TIMEOUT if a bounded wait
  * gave up, else PA_ERR_DEVICE_BOUNDS if an index was out of range, else

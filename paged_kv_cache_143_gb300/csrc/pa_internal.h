@@ -39,6 +39,7 @@ inline pa_status launch_status() {
 
 // Shape checks shared by every entry point that takes a pool.
 pa_status check_pool(const pa_kv_pool* pool);
+pa_status check_latent_pool(const pa_latent_pool* pool);
 
 // The driver's cuTensorMapEncodeTiled (looked up once); nullptr if the driver
 // does not provide it.

@@ -1,0 +1,232 @@
+// rope.cu — pa_rope: rotary positions applied to the leading part of each head.
+//
+// Pair i of a head at position p is turned by the angle p * inv_freq[i]:
+//   (x, y) -> factor * (x cos - y sin, y cos + x sin),
+// the pair being dims (2i, 2i + 1) or (i, i + rot / 2). The work is one read
+// and one write of every element (HBM-bound when large, launch latency when
+// small); the angles depend on (token, pair) only, so a CTA computes its
+// tokens' cosines and sines once into shared memory, while the first vectors of
+// x are already on their way, and every head reuses them. fp32 arithmetic, one
+// rounding to bf16.
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "rope_angle.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnits = 512;      // units a CTA aims at: two per thread, both loaded before the angles
+constexpr int kMaxPairs = 128;   // rot_dim <= 256
+constexpr int kMaxTokens = 64;   // tokens of one CTA
+constexpr int kMaxAngles = 2048; // (token, pair) angles of one CTA
+
+struct RopeParams {
+  const __nv_bfloat16* x;
+  __nv_bfloat16* out;
+  const int32_t* positions;
+  const float* inv_freq;
+  int64_t x_ts, x_hs, o_ts, o_hs;  // token and head strides, elements
+  int32_t T, H, pairs, interleaved;
+  int32_t units;                   // units per head (rotated ones first, then copied ones)
+  int32_t rot_units;
+  int32_t tokens, heads;           // of one CTA
+  float factor;
+};
+
+// A unit of the vector form: 8 dims (4 pairs) of the interleaved layout; 8 + 8
+// dims (8 pairs) of the half layout; 8 dims passed through.
+struct VecUnit {
+  uint4 a, b;
+  __device__ __forceinline__ static int64_t dim(const RopeParams& p, int u) {
+    if (u < p.rot_units || p.interleaved) return u * 8;
+    return 2 * p.pairs + (u - p.rot_units) * 8;
+  }
+  __device__ __forceinline__ void load(const RopeParams& p, const __nv_bfloat16* x, int u) {
+    const __nv_bfloat16* src = x + dim(p, u);
+    a = *reinterpret_cast<const uint4*>(src);
+    if (!p.interleaved && u < p.rot_units) b = *reinterpret_cast<const uint4*>(src + p.pairs);
+  }
+  __device__ __forceinline__ static uint4 pack(const float (&f)[8]) {
+    uint4 v;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return v;
+  }
+  __device__ __forceinline__ void store(const RopeParams& p, __nv_bfloat16* out, int u,
+                                        const float2* cs) const {
+    __nv_bfloat16* dst = out + dim(p, u);
+    if (u >= p.rot_units) {
+      *reinterpret_cast<uint4*>(dst) = a;
+      return;
+    }
+    float f[8];
+    pa::bf16x8_to_f32(a, f);
+    if (p.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = cs[u * 4 + i];
+        pa::rope_turn(f[2 * i], f[2 * i + 1], t.x, t.y);
+      }
+      *reinterpret_cast<uint4*>(dst) = pack(f);
+    } else {
+      float g[8];
+      pa::bf16x8_to_f32(b, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 t = cs[u * 8 + i];
+        pa::rope_turn(f[i], g[i], t.x, t.y);
+      }
+      *reinterpret_cast<uint4*>(dst) = pack(f);
+      *reinterpret_cast<uint4*>(dst + p.pairs) = pack(g);
+    }
+  }
+};
+
+// A unit of the scalar form (odd sizes, strides or addresses): one pair, or
+// one dim passed through.
+struct ScalarUnit {
+  __nv_bfloat16 a, b;
+  __device__ __forceinline__ void load(const RopeParams& p, const __nv_bfloat16* x, int u) {
+    if (u >= p.pairs) {
+      a = x[p.pairs + u];
+    } else {
+      a = x[p.interleaved ? 2 * u : u];
+      b = x[p.interleaved ? 2 * u + 1 : u + p.pairs];
+    }
+  }
+  __device__ __forceinline__ void store(const RopeParams& p, __nv_bfloat16* out, int u,
+                                        const float2* cs) const {
+    if (u >= p.pairs) {
+      out[p.pairs + u] = a;
+      return;
+    }
+    float f = __bfloat162float(a), g = __bfloat162float(b);
+    pa::rope_turn(f, g, cs[u].x, cs[u].y);
+    out[p.interleaved ? 2 * u : u] = __float2bfloat16_rn(f);
+    out[p.interleaved ? 2 * u + 1 : u + p.pairs] = __float2bfloat16_rn(g);
+  }
+};
+
+// grid (token groups, head groups). In place (out == x) is safe: a unit's dims
+// are read and written by one thread, and its loads come first.
+template <typename Unit>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  __shared__ float2 cs[kMaxAngles];
+  const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
+  const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.H - h0);
+  const int per_token = nh * p.units, n = nt * per_token;
+  auto place = [&](int i, int& t, int& h, int& u) {
+    t = i / per_token;
+    const int j = i - t * per_token;
+    h = j / p.units;
+    u = j - h * p.units;
+  };
+  auto src = [&](int t, int h) { return p.x + (t0 + t) * p.x_ts + (h0 + h) * p.x_hs; };
+  auto dst = [&](int t, int h) { return p.out + (t0 + t) * p.o_ts + (h0 + h) * p.o_hs; };
+  Unit first[2];
+  int t[2], h[2], u[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    if (i < n) {
+      place(i, t[k], h[k], u[k]);
+      first[k].load(p, src(t[k], h[k]), u[k]);
+    }
+  }
+  for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
+    const int tok = i / p.pairs;
+    float c, s;
+    pa::rope_cos_sin(__ldg(p.positions + t0 + tok), __ldg(p.inv_freq + i - tok * p.pairs),
+                     p.factor, c, s);
+    cs[i] = make_float2(c, s);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if ((int)threadIdx.x + k * kThreads < n)
+      first[k].store(p, dst(t[k], h[k]), u[k], cs + t[k] * p.pairs);
+  for (int i = threadIdx.x + 2 * kThreads; i < n; i += kThreads) {
+    int tt, hh, uu;
+    place(i, tt, hh, uu);
+    Unit v;
+    v.load(p, src(tt, hh), uu);
+    v.store(p, dst(tt, hh), uu, cs + tt * p.pairs);
+  }
+}
+
+}  // namespace
+
+extern "C" pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride,
+                             void* out, int64_t out_token_stride, int64_t out_head_stride,
+                             const int32_t* positions, int32_t T, int32_t num_heads,
+                             int32_t head_dim, const float* inv_freq, int32_t rot_dim,
+                             int32_t layout, float factor, pa_stream_t stream) {
+  if (T < 0 || num_heads <= 0 || head_dim <= 0 || rot_dim < 0 || rot_dim > head_dim)
+    return PA_ERR_INVALID;
+  if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_INVALID;
+  if (!(factor > 0.f) || factor > 3.0e38f) return PA_ERR_INVALID;
+  if (rot_dim % 2 != 0 || rot_dim > 2 * kMaxPairs) return PA_ERR_UNSUPPORTED;
+  if (T == 0) return PA_OK;
+  if (!x || !out || !positions || (rot_dim > 0 && !inv_freq)) return PA_ERR_INVALID;
+  // rows [token][head] of out must not share elements: heads inside tokens, or
+  // tokens inside heads
+  // (the stride of a dimension of one entry is never used)
+  const int64_t D = head_dim, xt = T > 1 ? x_token_stride : 0, ot = T > 1 ? out_token_stride : 0;
+  const int64_t xh = num_heads > 1 ? x_head_stride : 0, oh = num_heads > 1 ? out_head_stride : 0;
+  if (xt < 0 || xh < 0 || ot < 0 || oh < 0) return PA_ERR_INVALID;
+  const bool heads_inside = (num_heads == 1 || oh >= D) &&
+                            (T == 1 || ot >= (num_heads - 1) * oh + D);
+  const bool tokens_inside = (T == 1 || ot >= D) &&
+                             (num_heads == 1 || oh >= (int64_t)(T - 1) * ot + D);
+  if (!heads_inside && !tokens_inside) return PA_ERR_INVALID;
+  if (x == out && ((T > 1 && xt != ot) || (num_heads > 1 && xh != oh))) return PA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(x) & 1u) || (reinterpret_cast<uintptr_t>(out) & 1u) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(inv_freq) & 3u))
+    return PA_ERR_INVALID;
+
+  RopeParams p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.x_ts = xt; p.x_hs = xh; p.o_ts = ot; p.o_hs = oh;
+  p.T = T;
+  p.H = num_heads;
+  p.pairs = rot_dim / 2;
+  p.interleaved = layout == PA_ROPE_INTERLEAVED;
+  p.factor = factor;
+  // 16-byte vectors where every row and every half starts on 16 bytes
+  const bool vec = pa::aligned16(x) && pa::aligned16(out) && (xt | xh | ot | oh | D) % 8 == 0 &&
+                   (p.interleaved ? rot_dim : p.pairs) % 8 == 0;
+  const int pass = x == out ? 0 : head_dim - rot_dim;  // dims copied
+  p.rot_units = vec ? (p.interleaved ? rot_dim / 8 : p.pairs / 8) : p.pairs;
+  p.units = p.rot_units + (vec ? pass / 8 : pass);
+  if (p.units == 0) return PA_OK;  // in place, nothing turned
+  // CTAs of about kUnits units: several tokens of few heads, or some heads of one token
+  const int64_t per_token = (int64_t)num_heads * p.units;
+  p.tokens = 1;
+  p.heads = num_heads;
+  if (per_token > kUnits) {
+    const int groups = (int)((per_token + kUnits - 1) / kUnits);
+    p.heads = (num_heads + groups - 1) / groups;
+  } else {
+    p.tokens = (int)(kUnits / per_token);
+    if (p.tokens > kMaxTokens) p.tokens = kMaxTokens;
+    if (p.pairs > 0 && p.tokens > kMaxAngles / p.pairs) p.tokens = kMaxAngles / p.pairs;
+    // no fewer CTAs than SMs while there are tokens to spread
+    const int spread = (T + pa::num_sms() - 1) / pa::num_sms();
+    if (p.tokens > spread) p.tokens = spread;
+  }
+  const dim3 grid((unsigned)((T + p.tokens - 1) / p.tokens),
+                  (unsigned)((num_heads + p.heads - 1) / p.heads));
+  if (grid.y > 65535u) return PA_ERR_UNSUPPORTED;
+  if (vec)
+    rope_kernel<VecUnit><<<grid, kThreads, 0, pa::as_stream(stream)>>>(p);
+  else
+    rope_kernel<ScalarUnit><<<grid, kThreads, 0, pa::as_stream(stream)>>>(p);
+  return pa::launch_status();
+}

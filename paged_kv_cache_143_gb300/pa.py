@@ -28,6 +28,7 @@ EXPORTS = ("pa_write_kv", "pa_forward_workspace_size", "pa_forward", "pa_apply_s
            "pa_forward_noalloc", "pa_selftest_wait_timeout", "pa_forward_shared_prefix",
            "pa_prepare_inputs", "pa_decode_graph_create", "pa_decode_graph_launch",
            "pa_decode_graph_destroy", "pa_decode_graph_kernels",
+           "pa_rope", "pa_write_latent", "pa_read_latent", "pa_copy_latent_blocks",
            # include/pa_sched.h
            "pa_sched_create", "pa_sched_destroy", "pa_sched_add_request", "pa_sched_fork",
            "pa_sched_abort", "pa_sched_step", "pa_sched_commit", "pa_sched_get_stats",
@@ -46,6 +47,13 @@ class _Pool(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float)]
+
+
+class _LatentPool(ctypes.Structure):
+    _fields_ = [("latent", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("num_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class _DecodeGraphDesc(ctypes.Structure):
@@ -116,6 +124,15 @@ def lib():
         L.pa_copy_blocks.argtypes = [PP, P, P, I32, P]
         L.pa_gather_rows.restype = ctypes.c_int
         L.pa_gather_rows.argtypes = [P, I64, I64, P, I32, P, P]
+        LP = ctypes.POINTER(_LatentPool)
+        L.pa_rope.restype = ctypes.c_int
+        L.pa_rope.argtypes = [P, I64, I64, P, I64, I64, P, I32, I32, I32, P, I32, I32, F32, P]
+        L.pa_write_latent.restype = ctypes.c_int
+        L.pa_write_latent.argtypes = [LP, P, I64, P, I64, P, P, I32, F32, P, I32, P]
+        L.pa_read_latent.restype = ctypes.c_int
+        L.pa_read_latent.argtypes = [LP, P, I32, P, P, I32, I32, P, I64, P, I64, P]
+        L.pa_copy_latent_blocks.restype = ctypes.c_int
+        L.pa_copy_latent_blocks.argtypes = [LP, P, P, I32, P]
         L.pa_get_error.restype = ctypes.c_int
         L.pa_get_error.argtypes = [P]
         L.pa_status_string.restype = ctypes.c_char_p
@@ -558,6 +575,197 @@ def gather_rows(src: torch.Tensor, rows: torch.Tensor, dst: torch.Tensor, stream
     row_bytes = src[0].numel() * src.element_size() if src.shape[0] else 16
     _check(lib().pa_gather_rows(_dptr(src), src.shape[0], row_bytes, _dptr(rows, torch.int32), n,
                                 _dptr(dst), _stream(stream)), "pa_gather_rows")
+
+
+# ---------------------------------------------------------------- latent path
+
+PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
+LATENT_ROPE_DIM = 64  # rotary dims of a latent cell
+
+
+def _strided(t: torch.Tensor, what: str, dtype=torch.bfloat16) -> Optional[int]:
+    """Device pointer of a tensor whose innermost dimension is contiguous, on
+    the current device."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, not on the current device")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: the innermost dimension must be contiguous")
+    return t.data_ptr() if t.numel() else None
+
+
+def _flat(t: Optional[torch.Tensor], what: str, dtype) -> Optional[int]:
+    """Device pointer of a contiguous tensor on the current device (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return _strided(t.view(-1), what, dtype)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+                     stretch: float = 1.0, original_context: int = 4096, fast: float = 32.0,
+                     slow: float = 1.0, device=None):
+    """(inv_freq fp32 [rot_dim / 2], factor) for `rope` and `write_latent`.
+
+    base ** (-2 i / rot_dim), and for contexts `stretch` times longer than
+    `original_context`:
+      None         as they are;
+      "linear"     every frequency divided by `stretch` (positions interpolated);
+      "base"       the base raised so that the slowest pair is stretched by
+                   `stretch` and the fastest not at all;
+      "by_parts"   pairs that turn less than `slow` times over the original
+                   context are divided by `stretch`, those that turn more than
+                   `fast` times are kept, a linear ramp between; the factor is
+                   1 + 0.1 ln(stretch).
+    """
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be positive and even")
+    if not (stretch >= 1.0 and base > 1.0):
+        raise ValueError("stretch must be at least 1 and base above 1")
+    i = np.arange(rot_dim // 2, dtype=np.float64)
+    factor = 1.0
+    if scaling == "base":
+        if rot_dim == 2:
+            raise ValueError("one pair has no slowest and fastest frequency")
+        base = base * stretch ** (rot_dim / (rot_dim - 2.0))
+    f = base ** (-2.0 * i / rot_dim)
+    if scaling == "linear":
+        f = f / stretch
+    elif scaling == "by_parts":
+        if not fast > slow:
+            raise ValueError("fast must be above slow")
+        turns = original_context * f / (2 * np.pi)
+        keep = np.clip((turns - slow) / (fast - slow), 0.0, 1.0)
+        f = f * keep + f / stretch * (1 - keep)
+        factor = 1.0 + 0.1 * float(np.log(stretch))
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.from_numpy(f.astype(np.float32)).to(device or "cpu"), factor
+
+
+def rope(x: torch.Tensor, out: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+         interleaved: bool = False, factor: float = 1.0, stream=None) -> None:
+    """Turns the first 2 * len(inv_freq) dims of every head of x [T][H][D] by
+    positions * inv_freq into out (which may be x); the other dims are copied."""
+    if x.dim() != 3 or out.shape != x.shape:
+        raise ValueError("x and out must be [T][H][D] of one shape")
+    T, H, D = x.shape
+    if positions.numel() != T:
+        raise ValueError("positions must have one entry per token")
+    _check(lib().pa_rope(
+        _strided(x, "x"), x.stride(0), x.stride(1), _strided(out, "out"), out.stride(0),
+        out.stride(1), _flat(positions, "positions", torch.int32), T, H, D,
+        _flat(inv_freq, "inv_freq", torch.float32), 2 * inv_freq.numel(),
+        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor, _stream(stream)), "pa_rope")
+
+
+class LatentPool:
+    """Caller-owned latent cache: latent [num_blocks][B][L] (bf16, or uint8
+    E4M3 codes with fp32 scales [num_blocks][B]) and rope bf16
+    [num_blocks][B][64]."""
+
+    def __init__(self, latent: torch.Tensor, rope: torch.Tensor,
+                 scales: Optional[torch.Tensor] = None):
+        if latent.dim() != 3 or rope.dim() != 3 or latent.shape[:2] != rope.shape[:2]:
+            raise ValueError("latent and rope must be [num_blocks][B][dim] over the same cells")
+        if latent.dtype == torch.bfloat16:
+            self.dtype = PA_KV_BF16
+            if scales is not None:
+                raise ValueError("a bf16 pool has no scales")
+        elif latent.dtype == torch.uint8:
+            self.dtype = PA_KV_FP8_E4M3
+            if scales is None or scales.shape != latent.shape[:2]:
+                raise ValueError("an E4M3 pool needs scales [num_blocks][B]")
+        else:
+            raise TypeError("latent dtype must be bfloat16 or uint8 (E4M3 codes)")
+        self.latent, self.rope, self.scales = latent, rope, scales
+        self.num_blocks, self.block_size, self.latent_dim = latent.shape
+        self.rope_dim = rope.shape[2]
+
+    def struct(self) -> _LatentPool:
+        return _LatentPool(_flat(self.latent, "latent", self.latent.dtype),
+                           _flat(self.rope, "rope", torch.bfloat16),
+                           _flat(self.scales, "scales", torch.float32), self.num_blocks,
+                           self.block_size, self.latent_dim, self.rope_dim, self.dtype)
+
+    def ref(self):
+        """ctypes reference to the pool's C struct, built once per set of
+        device pointers (storage may move under a tensor)."""
+        t = (self.latent.data_ptr(), self.rope.data_ptr(),
+             None if self.scales is None else self.scales.data_ptr(),
+             torch.cuda.current_device())
+        c = self.__dict__.get("_c")
+        if c is None or c[2] != t:
+            st = self.struct()
+            c = self.__dict__["_c"] = (st, ctypes.byref(st), t)
+        return c[1]
+
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_c", None)
+        object.__setattr__(self, name, value)
+
+
+def _tokens(t: torch.Tensor, width: int, what: str) -> int:
+    """Token stride of rows [T][width]."""
+    if t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{what} must be [tokens][{width}]")
+    return t.stride(0) if t.shape[0] > 1 else (width + 7) // 8 * 8
+
+
+def write_latent(pool: LatentPool, latent: torch.Tensor, k_rope: torch.Tensor,
+                 slot_mapping: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                 inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 factor: float = 1.0, stream=None) -> None:
+    """Stores a step's latent rows and rotary keys by slot; with positions and
+    inv_freq the rotary keys are turned first."""
+    T = slot_mapping.numel()
+    ls, rs = _tokens(latent, pool.latent_dim, "latent"), _tokens(k_rope, pool.rope_dim, "k_rope")
+    if latent.shape[0] != T or k_rope.shape[0] != T or (positions is not None and
+                                                        positions.numel() != T):
+        raise ValueError("latent, k_rope and positions must have one row per slot")
+    if inv_freq is not None and 2 * inv_freq.numel() != pool.rope_dim:
+        raise ValueError("inv_freq must have rope_dim / 2 entries")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq come together")
+    if T == 0:
+        return
+    _check(lib().pa_write_latent(
+        pool.ref(), _strided(latent, "latent"), ls, _strided(k_rope, "k_rope"), rs,
+        _flat(positions, "positions", torch.int32), _flat(inv_freq, "inv_freq", torch.float32),
+        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor,
+        _flat(slot_mapping, "slot_mapping", torch.int64), T, _stream(stream)), "pa_write_latent")
+
+
+def read_latent(pool: LatentPool, block_tables: torch.Tensor, kv_start_loc: torch.Tensor,
+                latent_out: torch.Tensor, rope_out: torch.Tensor,
+                first: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Cached rows of the requests, ragged by kv_start_loc, widened to bf16."""
+    R, max_blocks = block_tables.shape
+    N = latent_out.shape[0]
+    ls, rs = _tokens(latent_out, pool.latent_dim, "latent_out"), _tokens(rope_out, pool.rope_dim,
+                                                                         "rope_out")
+    if kv_start_loc.numel() != R + 1 or (first is not None and first.numel() != R):
+        raise ValueError("kv_start_loc must have num_reqs + 1 entries and first num_reqs")
+    if rope_out.shape[0] != N:
+        raise ValueError("latent_out and rope_out must have the same rows")
+    _check(lib().pa_read_latent(
+        pool.ref(), _flat(block_tables, "block_tables", torch.int32), max_blocks,
+        _flat(kv_start_loc, "kv_start_loc", torch.int32), _flat(first, "first", torch.int32), R, N,
+        _strided(latent_out, "latent_out"), ls, _strided(rope_out, "rope_out"), rs,
+        _stream(stream)), "pa_read_latent")
+
+
+def copy_latent_blocks(pool: LatentPool, src: torch.Tensor, dst: torch.Tensor,
+                       stream=None) -> None:
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must pair up")
+    _check(lib().pa_copy_latent_blocks(
+        pool.ref(), _flat(src, "src", torch.int32), _flat(dst, "dst", torch.int32), src.numel(),
+        _stream(stream)), "pa_copy_latent_blocks")
 
 
 def selftest_wait_timeout(stream=None) -> None:
