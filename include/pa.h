@@ -526,6 +526,47 @@ pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src,
                                 const int32_t* dst, int32_t n, pa_stream_t stream);
 
 /*
+ * pa_latent_forward — attention in the absorbed form over the paged latent
+ * cache, for a mixed batch of decode tokens and chunks, as pa_forward:
+ *   s[t][h][n] = scale * q[t][h] . [c_n ; k_r_n],
+ *   out[t][h]  = sum_n softmax_n(s[t][h]) c_n    over the visible keys.
+ *
+ *   q            dev bf16 [T][num_q_heads][latent_dim + rope_dim], 16-byte
+ *                aligned: the absorbed query, then its turned rotary part
+ *   out          dev bf16 [T][num_q_heads][latent_dim], 16-byte aligned
+ *   query_start_loc, seq_lens, qsl_host, seq_lens_host, block_tables,
+ *   max_blocks, num_reqs, num_tokens, causal
+ *                as pa_forward (the step's own rows are already written)
+ *   num_q_heads  any positive number (all heads read the same cache)
+ *   workspace    dev scratch, required: pa_latent_workspace_size bytes serve
+ *                every batch; 16-byte aligned. Calls that may run at the same
+ *                time (other streams, captured graphs that overlap) need
+ *                workspaces of their own.
+ *
+ * Computed in fp32 (the softmax weights enter the second product rounded to
+ * 16 bits), rounded once to bf16. Rows of requests with q_len == 0 and rows
+ * past query_start_loc[num_reqs] are not touched.
+ * The work is divided from the device arrays at every launch; the host mirrors
+ * only size the launch. A captured call therefore follows device lengths that
+ * change between replays, with exact results, as long as query_start_loc
+ * stays within num_tokens and each seq_len within max_blocks * block_size.
+ * Host checks as pa_forward, and PA_ERR_INVALID for a workspace too small.
+ * Device checks: a request whose device entries leave those bounds (or with
+ * q_len > seq_len) sets PA_ERR_DEVICE_BOUNDS and is skipped; a block id
+ * outside the pool sets it too. Nothing is read or written outside the
+ * buffers.
+ */
+size_t pa_latent_workspace_size(int32_t num_q_heads, int32_t latent_dim);
+
+pa_status pa_latent_forward(const void* q, void* out, const int32_t* query_start_loc,
+                            const int32_t* seq_lens, const int32_t* qsl_host,
+                            const int32_t* seq_lens_host, const int32_t* block_tables,
+                            int32_t max_blocks, int32_t num_reqs, int32_t num_tokens,
+                            int32_t num_q_heads, const pa_latent_pool* pool, float scale,
+                            int32_t causal, void* workspace, size_t workspace_bytes,
+                            pa_stream_t stream);
+
+/*
  * pa_get_error — synchronise `stream`, then return and clear the sticky
  * device error word of the current device: PA_ERR_TIMEOUT if a bounded wait
  * gave up, else PA_ERR_DEVICE_BOUNDS if an index was out of range, else

@@ -29,6 +29,7 @@ EXPORTS = ("pa_write_kv", "pa_forward_workspace_size", "pa_forward", "pa_apply_s
            "pa_prepare_inputs", "pa_decode_graph_create", "pa_decode_graph_launch",
            "pa_decode_graph_destroy", "pa_decode_graph_kernels",
            "pa_rope", "pa_write_latent", "pa_read_latent", "pa_copy_latent_blocks",
+           "pa_latent_workspace_size", "pa_latent_forward",
            # include/pa_sched.h
            "pa_sched_create", "pa_sched_destroy", "pa_sched_add_request", "pa_sched_fork",
            "pa_sched_abort", "pa_sched_step", "pa_sched_commit", "pa_sched_get_stats",
@@ -133,6 +134,11 @@ def lib():
         L.pa_read_latent.argtypes = [LP, P, I32, P, P, I32, I32, P, I64, P, I64, P]
         L.pa_copy_latent_blocks.restype = ctypes.c_int
         L.pa_copy_latent_blocks.argtypes = [LP, P, P, I32, P]
+        L.pa_latent_workspace_size.restype = SZ
+        L.pa_latent_workspace_size.argtypes = [I32, I32]
+        L.pa_latent_forward.restype = ctypes.c_int
+        L.pa_latent_forward.argtypes = [P, P, P, P, P, P, P, I32, I32, I32, I32, LP, F32, I32, P,
+                                        SZ, P]
         L.pa_get_error.restype = ctypes.c_int
         L.pa_get_error.argtypes = [P]
         L.pa_status_string.restype = ctypes.c_char_p
@@ -766,6 +772,38 @@ def copy_latent_blocks(pool: LatentPool, src: torch.Tensor, dst: torch.Tensor,
     _check(lib().pa_copy_latent_blocks(
         pool.ref(), _flat(src, "src", torch.int32), _flat(dst, "dst", torch.int32), src.numel(),
         _stream(stream)), "pa_copy_latent_blocks")
+
+
+def latent_workspace_size(num_q_heads: int, latent_dim: int) -> int:
+    """Bytes of the workspace that latent_forward needs, whatever the batch."""
+    return int(lib().pa_latent_workspace_size(num_q_heads, latent_dim))
+
+
+def latent_forward(q: torch.Tensor, out: torch.Tensor, query_start_loc: torch.Tensor,
+                   seq_lens: torch.Tensor, qsl_host, seq_lens_host, block_tables: torch.Tensor,
+                   pool: LatentPool, scale: float, causal: int = 1,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Absorbed attention: q [T][H][L + 64] over the latent cache, out [T][H][L]."""
+    qh = _host_i32(qsl_host)
+    sh = _host_i32(seq_lens_host)
+    R = sh.size
+    if qh.size != R + 1 or query_start_loc.numel() != R + 1 or seq_lens.numel() != R:
+        raise ValueError("query_start_loc must have num_reqs + 1 entries and seq_lens num_reqs")
+    T, H, D = q.shape
+    if D != pool.latent_dim + pool.rope_dim or out.shape != (T, H, pool.latent_dim):
+        raise ValueError("q must be [T][H][latent_dim + rope_dim] and out [T][H][latent_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != R:
+        raise ValueError("block_tables must be [num_reqs][max_blocks]")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().pa_latent_forward(
+        _flat(q, "q", torch.bfloat16), _flat(out, "out", torch.bfloat16),
+        _flat(query_start_loc, "query_start_loc", torch.int32),
+        _flat(seq_lens, "seq_lens", torch.int32), _np_addr(qh), _np_addr(sh),
+        _flat(block_tables, "block_tables", torch.int32), block_tables.shape[1], R, T, H,
+        pool.ref(), float(scale), int(causal),
+        None if workspace is None else _flat(workspace, "workspace", workspace.dtype), ws_bytes,
+        _stream(stream))
+    _check(st, "pa_latent_forward")
 
 
 def selftest_wait_timeout(stream=None) -> None:

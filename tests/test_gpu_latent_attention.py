@@ -1,0 +1,271 @@
+"""GPU tests of pa_latent_forward (absorbed attention over the paged latent
+cache) against the 64-bit reference on the cells' own values.
+
+Tolerance of an output element o = sum_n p_n v_n:
+  * p is rounded to bf16 before the product (half a step, relative 2^-8 by the
+    count used here) while the sum of p is not: at most 2^-8 sum_n p_n |v_n|;
+  * the scores are fp32 sums of bf16 products: for scores of magnitude up to
+    S = scale * sum |q||k| the error is below 2^-20 S (576 terms, fp32
+    accumulation), and a score error d moves o by at most 2 d sum p |v|;
+  * one rounding of o to bf16: 2^-8 |o|.
+The bound below sums these per element, from the reference's own p and v."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_143_gb300 import pa
+from tests import latent_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(a, dev):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=dev)
+
+
+class Batch:
+    """A filled cache, its tables and a step's queries. Cells past each
+    request's length, and blocks of nobody, stay poisoned with NaN."""
+
+    def __init__(self, seqs, q_lens, H, L, B, fp8, dev, seed=0, mult=1.0, causal=1, spare_rows=0):
+        rng = np.random.default_rng(seed)
+        self.seqs, self.q_lens, self.H, self.L, self.B = seqs, q_lens, H, L, B
+        self.dev, self.causal, self.scale = dev, causal, (128 + 64) ** -0.5
+        live = [s if q else 0 for s, q in zip(seqs, q_lens)]
+        self.tab, blocks = ref.tables(rng, live, B)
+        self.pool = ref.new_pool(pa, blocks, B, L, fp8, dev)
+        n = sum(live)
+        if n:
+            c = torch.from_numpy(rng.standard_normal((n, L)).astype(np.float32)).to(dev).bfloat16()
+            kr = torch.from_numpy(rng.standard_normal((n, 64)).astype(np.float32)).to(dev).bfloat16()
+            slots = np.concatenate([ref.slots_of(self.tab, r, s, B) for r, s in enumerate(live)])
+            pa.write_latent(self.pool, c, kr, torch.from_numpy(slots).to(dev))
+        self.qsl = np.cumsum([0] + list(q_lens)).astype(np.int32)
+        self.T = int(self.qsl[-1]) + spare_rows
+        self.q = torch.from_numpy((rng.standard_normal((self.T, H, L + 64)) * mult).astype(
+            np.float32)).to(dev).bfloat16()
+        self.out = torch.full((self.T, H, L), 9.0, dtype=torch.bfloat16, device=dev)
+        self.ws = torch.full((pa.latent_workspace_size(H, L),), 0xFF, dtype=torch.uint8, device=dev)
+        self.seq_dev, self.qsl_dev, self.tab_dev = (i32(seqs, dev), i32(self.qsl, dev),
+                                                    i32(self.tab, dev))
+
+    def run(self, out=None, qsl_host=None, seq_host=None, ws=None, stream=None):
+        pa.latent_forward(self.q, self.out if out is None else out, self.qsl_dev, self.seq_dev,
+                          self.qsl if qsl_host is None else qsl_host,
+                          np.array(self.seqs, np.int32) if seq_host is None else seq_host,
+                          self.tab_dev, self.pool, self.scale, self.causal,
+                          workspace=self.ws if ws is None else ws, stream=stream)
+        return self.out if out is None else out
+
+    def check(self, out=None, seqs=None, reqs=None):
+        out = self.out if out is None else out
+        seqs = self.seqs if seqs is None else seqs
+        lat, rot = ref.pool_rows(self.pool)
+        p_half = ref.BF16_HALF
+        worst = 0.0
+        for r in range(len(seqs)) if reqs is None else reqs:
+            a, b = self.qsl[r], self.qsl[r + 1]
+            if a == b:
+                continue
+            at = ref.slots_of(self.tab, r, seqs[r], self.B)
+            q = ref.f64(self.q[a:b])
+            want, p = ref.absorbed(q, lat[at], rot[at], self.scale, self.causal)
+            size = np.einsum("thn,nl->thl", p, np.abs(lat[at]))
+            k = np.concatenate((lat[at], rot[at]), -1)
+            s_mag = self.scale * np.einsum("thd,nd->thn", np.abs(q), np.abs(k)).max(-1)[..., None]
+            tol = size * (p_half + 2 * 2.0 ** -20 * s_mag) + p_half * np.abs(want) + 1e-30
+            got = ref.f64(out[a:b])
+            assert np.isfinite(got).all()
+            err = np.abs(got - want)
+            assert (err <= tol).all(), (r, err.max(), (err / tol).max())
+            worst = max(worst, (err / tol).max())
+        return worst
+
+
+SHAPES = [  # seq_lens, q_lens, H, L, B
+    ([1], [1], 1, 512, 16),
+    ([1, 63, 64, 65, 127, 128, 129], [1] * 7, 16, 512, 16),
+    ([200, 7, 1000], [1, 1, 1], 5, 256, 32),
+    ([333, 64, 2049], [1, 1, 1], 32, 512, 64),
+    ([90, 400], [1, 1], 40, 512, 16),
+    ([511, 3000], [1, 1], 128, 512, 64),
+    ([700, 65], [1, 1], 128, 256, 16),
+    ([130, 77, 300], [1, 4, 2], 16, 512, 32),      # drafted tokens among decodes
+    ([50, 64, 65], [50, 64, 33], 3, 512, 16),      # whole prompts and a chunk
+    ([900], [130], 24, 256, 64),                   # many row tiles
+    ([40, 10, 70], [1, 0, 1], 4, 512, 16),         # an empty request
+    ([5000], [1], 20, 256, 16),                    # one request cut over every CTA
+    ([12000, 1, 1, 12000], [1, 1, 1, 3], 64, 512, 64),
+    ([17] * 400, [1] * 400, 16, 256, 16),          # more requests than threads
+    ([64] * 152 + [1], [1] * 153, 8, 512, 32),
+]
+
+
+@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+@pytest.mark.parametrize("case", range(len(SHAPES)))
+def test_shapes(cuda_device, case, fp8):
+    seqs, q_lens, H, L, B = SHAPES[case]
+    b = Batch(seqs, q_lens, H, L, B, fp8, cuda_device, seed=case)
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check()
+
+
+@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+@pytest.mark.parametrize("mult", [0.0, 0.05, 6.0])
+def test_flat_and_peaked_scores(cuda_device, mult, fp8):
+    """Equal weights, nearly equal ones, and rows that one key owns (the
+    reference maximum moves and O is rescaled)."""
+    b = Batch([3000, 70, 640], [1, 1, 5], 16, 512, 16, fp8, cuda_device, seed=3, mult=mult)
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check()
+
+
+@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+def test_rising_scores_rescale_every_tile(cuda_device, fp8):
+    """Keys that grow along the context: the maximum rises tile after tile."""
+    dev = cuda_device
+    b = Batch([1500], [2], 24, 256, 16, fp8, dev, seed=4)
+    n = 1500
+    ramp = torch.linspace(0, 60, n, device=dev)[:, None]
+    one = torch.ones(1, 64, device=dev)
+    rng = np.random.default_rng(8)
+    c = torch.from_numpy(rng.standard_normal((n, 256)).astype(np.float32)).to(dev).bfloat16()
+    slots = torch.from_numpy(ref.slots_of(b.tab, 0, n, 16)).to(dev)
+    pa.write_latent(b.pool, c, (ramp * one).bfloat16(), slots)
+    b.q[..., 256:] = 0.25
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check()
+
+
+@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+def test_not_causal(cuda_device, fp8):
+    b = Batch([100, 64, 7], [30, 1, 7], 6, 512, 16, fp8, cuda_device, seed=5, causal=0)
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check()
+
+
+def test_rows_past_the_last_sequence_stay(cuda_device):
+    """A padded batch: query_start_loc ends before the rows do (the device
+    array; the host mirror sizes the launch for all rows)."""
+    dev = cuda_device
+    b = Batch([100, 40], [1, 3], 16, 512, 16, False, dev, seed=6, spare_rows=5)
+    host = b.qsl.copy()
+    host[-1] = b.T  # as planned for a larger step
+    b.run(qsl_host=host, seq_host=np.array([100, 64], np.int32))
+    assert pa.get_error() == pa.PA_OK
+    b.check()
+    assert (b.out[4:] == 9).all()
+
+
+@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+def test_deterministic_and_independent_of_placement(cuda_device, fp8):
+    dev = cuda_device
+    b = Batch([777, 2000, 33], [1, 2, 1], 20, 512, 32, fp8, dev, seed=7)
+    first = b.run().clone()
+    again = b.run(out=torch.empty_like(first))
+    assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+    perm = torch.from_numpy(np.random.default_rng(1).permutation(b.pool.num_blocks)).to(dev)
+
+    def moved(t):
+        if t is None:
+            return None
+        u = torch.empty_like(t)
+        u[perm] = t
+        return u
+
+    b.pool = pa.LatentPool(moved(b.pool.latent), moved(b.pool.rope), moved(b.pool.scales))
+    b.tab_dev = torch.where(b.tab_dev >= 0, perm[b.tab_dev.clamp(min=0).long()].int(), b.tab_dev)
+    third = b.run(out=torch.empty_like(first))
+    assert torch.equal(first.view(torch.int16), third.view(torch.int16))
+    assert pa.get_error() == pa.PA_OK
+
+
+def test_captured_call_follows_the_device_lengths(cuda_device):
+    """One captured call replayed while the contexts grow (the cache holds the
+    longer contexts from the start; the lengths on the device change)."""
+    dev = cuda_device
+    seqs = [900, 130, 64, 2000]
+    b = Batch(seqs, [1] * 4, 16, 512, 16, False, dev, seed=9)
+    b.seq_dev.copy_(i32([10, 130, 1, 65], dev))
+    b.run(seq_host=np.array([10, 130, 1, 65], np.int32))  # warm: attributes, module
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        b.run(seq_host=np.array([10, 130, 1, 65], np.int32))
+    for lens in ([10, 130, 1, 65], [11, 64, 2, 66], [900, 129, 63, 1999], seqs):
+        b.seq_dev.copy_(i32(lens, dev))
+        b.out.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert pa.get_error() == pa.PA_OK
+        b.check(seqs=lens)
+
+
+def test_two_streams_with_workspaces_of_their_own(cuda_device):
+    dev = cuda_device
+    batches = [Batch([3000 + i, 500], [1, 1], 16, 512, 16, False, dev, seed=20 + i)
+               for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for b, s in zip(batches, streams):
+            b.run(stream=s)
+    torch.cuda.synchronize()
+    for b in batches:
+        b.check()
+    assert pa.get_error() == pa.PA_OK
+
+
+def test_cells_past_32_bits_of_bytes(cuda_device):
+    """A cache whose request lies more than 2^32 bytes into the pool."""
+    dev = cuda_device
+    b = Batch([200], [1], 16, 512, 64, False, dev, seed=11)
+    far = (1 << 32) // (64 * 512 * 2) + 5
+    latent = torch.zeros(far + b.pool.num_blocks, 64, 512, dtype=torch.bfloat16, device=dev)
+    rope = torch.zeros(far + b.pool.num_blocks, 64, 64, dtype=torch.bfloat16, device=dev)
+    latent[far:], rope[far:] = b.pool.latent, b.pool.rope
+    near = b.run().clone()
+    b.pool = pa.LatentPool(latent, rope)
+    b.tab_dev = torch.where(b.tab_dev >= 0, b.tab_dev + far, b.tab_dev)
+    assert torch.equal(b.run(out=torch.empty_like(near)).view(torch.int16), near.view(torch.int16))
+    assert pa.get_error() == pa.PA_OK
+
+
+def test_bad_blocks_and_lengths_are_flagged(cuda_device):
+    dev = cuda_device
+    b = Batch([100, 40, 64], [1, 1, 2], 16, 256, 16, False, dev, seed=12)
+    good = b.run().clone()
+    assert pa.get_error() == pa.PA_OK
+    tab = b.tab_dev.clone()
+    for bad in (b.pool.num_blocks, -1, 1 << 30, -(1 << 31)):
+        b.tab_dev = tab.clone()
+        b.tab_dev[1, 0] = bad
+        b.run()
+        assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS
+    b.tab_dev = tab
+    host = np.array(b.seqs, np.int32)
+    for r, n in ((0, 10 ** 6), (2, 1), (1, 0), (1, -5)):  # past the table; q_len > seq_len
+        b.seq_dev = i32(b.seqs, dev)
+        b.seq_dev[r] = n
+        b.out.fill_(9.0)
+        b.run(seq_host=host)
+        assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS
+        for o in range(3):  # the others are right, the bad one is left alone
+            a, e = b.qsl[o], b.qsl[o + 1]
+            if o != r:
+                b.check(reqs=[o])
+            else:
+                assert (b.out[a:e] == 9).all()
+    b.seq_dev = i32(b.seqs, dev)
+    for q in ([0, 1, 2, 5], [-1, 1, 2, 4], [0, 3, 2, 4]):  # rows that leave q
+        b.qsl_dev = i32(q, dev)
+        b.run()
+        assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS
+    b.qsl_dev = i32(b.qsl, dev)
+    assert torch.equal(b.run().view(torch.int16), good.view(torch.int16))
+    assert pa.get_error() == pa.PA_OK

@@ -169,3 +169,34 @@ def test_reference_absorbed_equals_expanded():
     qa = np.concatenate((np.einsum("thd,hdl->thl", q[..., :dn], wk), q[..., dn:]), -1)
     o, _ = ref.absorbed(qa, c, kr, 0.2)
     np.testing.assert_allclose(np.einsum("thl,hdl->thd", o, wv), full, atol=1e-12)
+
+
+def test_latent_forward_refusals():
+    L = pa.lib()
+    qsl, seq = np.array([0, 1, 3], np.int32), np.array([40, 50], np.int32)
+    ptr = lambda a: None if a is None else a.ctypes.data_as(ctypes.c_void_p)
+    ok = dict(q=P, out=P, qsl=P, seq=P, qh=qsl, sh=seq, tab=P, mb=4, R=2, T=3, H=16, pool={},
+              scale=0.1, causal=1, ws=None, wb=0)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return L.pa_latent_forward(a["q"], a["out"], a["qsl"], a["seq"], ptr(a["qh"]),
+                                   ptr(a["sh"]), a["tab"], a["mb"], a["R"], a["T"], a["H"],
+                                   latent_pool(**a["pool"]), a["scale"], a["causal"], a["ws"],
+                                   a["wb"], None)
+
+    i = lambda *v: np.array(v, np.int32)
+    for bad in (dict(), dict(ws=P, wb=4096),  # a workspace is required, of the whole size
+                dict(ws=24, wb=1 << 30), dict(ws=None, wb=1 << 30), dict(q=None), dict(q=24),
+                dict(out=None), dict(out=40), dict(qsl=None), dict(seq=None), dict(qh=None),
+                dict(sh=None), dict(tab=None), dict(mb=-1), dict(mb=3), dict(R=-1), dict(T=-1),
+                dict(T=4), dict(H=0), dict(scale=0.0), dict(scale=-1.0),
+                dict(scale=float("inf")), dict(scale=float("nan")), dict(causal=2),
+                dict(qh=i(1, 1, 3)), dict(qh=i(0, 4, 3)), dict(sh=i(40, 1)), dict(sh=i(0, 50)),
+                dict(sh=i(65, 50)), dict(pool=dict(num_blocks=0)), dict(R=0)):
+        assert call(**bad) == pa.PA_ERR_INVALID, bad
+    assert call(R=0, T=0) == pa.PA_OK
+    assert call(T=0, qh=i(0, 0, 0)) == pa.PA_OK
+    assert call(pool=dict(latent_dim=128)) == pa.PA_ERR_UNSUPPORTED
+    assert call(H=1 << 30) == pa.PA_ERR_UNSUPPORTED  # rows past 32-bit coordinates
+    assert pa.latent_workspace_size(0, 512) == 0 and pa.latent_workspace_size(16, 100) == 0
