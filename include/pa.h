@@ -567,6 +567,48 @@ pa_status pa_latent_forward(const void* q, void* out, const int32_t* query_start
                             pa_stream_t stream);
 
 /*
+ * pa_latent_prefill — attention in the expanded form: ragged query chunks
+ * against keys and values that the caller has made from the latents of each
+ * request's whole context (cached tokens, from pa_read_latent, and the
+ * chunk's own):
+ *   s[i][h][n] = scale * (q[i][h][:nope_dim] . k_nope[n][h]
+ *                         + q[i][h][nope_dim:] . k_rope[n]),
+ *   out[i][h]  = sum_n softmax_n(s[i][h]) v[n][h]   over the visible keys.
+ *
+ *   q        dev bf16 [num_tokens][num_heads][nope_dim + rope_dim]
+ *   k_nope   dev bf16 [num_kv_tokens][num_heads][nope_dim]
+ *   k_rope   dev bf16 [num_kv_tokens][rope_dim], shared by the heads
+ *   v        dev bf16 [num_kv_tokens][num_heads][v_dim]
+ *            16-byte aligned, innermost dims contiguous, token and head
+ *            strides in elements, multiples of 8 (k_nope and v may be the
+ *            two parts of one projection's output)
+ *   out      dev bf16 [num_tokens][num_heads][v_dim], contiguous, 16-byte aligned
+ *   query_start_loc, kv_start_loc
+ *            dev int32 [num_reqs+1], from 0, non-decreasing; qsl_host and
+ *            ksl_host their host mirrors (same values)
+ *   causal   1: query j of a request sees keys 0 .. k_len - q_len + j; 0: all
+ *            k_len keys. A row without a visible key is zero.
+ *
+ * Computed in fp32 (the softmax weights enter the second product rounded to
+ * bf16), rounded once to bf16. Rows past query_start_loc[num_reqs] are not
+ * touched. Supported: nope_dim 128, rope_dim 64, v_dim 128.
+ * Host checks: PA_ERR_INVALID (sizes, mirrors that do not end at num_tokens
+ * and num_kv_tokens, strides, pointers), PA_ERR_UNSUPPORTED (other dims, more
+ * than 32767 requests). Device checks: start arrays that leave the buffers or
+ * need more query tiles than the mirrors set PA_ERR_DEVICE_BOUNDS; nothing
+ * outside the buffers is read or written.
+ */
+pa_status pa_latent_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                            const void* k_nope, int64_t k_token_stride, int64_t k_head_stride,
+                            const void* k_rope, int64_t rope_token_stride, const void* v,
+                            int64_t v_token_stride, int64_t v_head_stride, void* out,
+                            const int32_t* query_start_loc, const int32_t* kv_start_loc,
+                            const int32_t* qsl_host, const int32_t* ksl_host, int32_t num_reqs,
+                            int32_t num_tokens, int32_t num_kv_tokens, int32_t num_heads,
+                            int32_t nope_dim, int32_t rope_dim, int32_t v_dim, float scale,
+                            int32_t causal, pa_stream_t stream);
+
+/*
  * pa_get_error — synchronise `stream`, then return and clear the sticky
  * device error word of the current device: PA_ERR_TIMEOUT if a bounded wait
  * gave up, else PA_ERR_DEVICE_BOUNDS if an index was out of range, else

@@ -29,7 +29,7 @@ EXPORTS = ("pa_write_kv", "pa_forward_workspace_size", "pa_forward", "pa_apply_s
            "pa_prepare_inputs", "pa_decode_graph_create", "pa_decode_graph_launch",
            "pa_decode_graph_destroy", "pa_decode_graph_kernels",
            "pa_rope", "pa_write_latent", "pa_read_latent", "pa_copy_latent_blocks",
-           "pa_latent_workspace_size", "pa_latent_forward",
+           "pa_latent_workspace_size", "pa_latent_forward", "pa_latent_prefill",
            # include/pa_sched.h
            "pa_sched_create", "pa_sched_destroy", "pa_sched_add_request", "pa_sched_fork",
            "pa_sched_abort", "pa_sched_step", "pa_sched_commit", "pa_sched_get_stats",
@@ -139,6 +139,9 @@ def lib():
         L.pa_latent_forward.restype = ctypes.c_int
         L.pa_latent_forward.argtypes = [P, P, P, P, P, P, P, I32, I32, I32, I32, LP, F32, I32, P,
                                         SZ, P]
+        L.pa_latent_prefill.restype = ctypes.c_int
+        L.pa_latent_prefill.argtypes = [P, I64, I64, P, I64, I64, P, I64, P, I64, I64, P, P, P, P,
+                                        P, I32, I32, I32, I32, I32, I32, I32, F32, I32, P]
         L.pa_get_error.restype = ctypes.c_int
         L.pa_get_error.argtypes = [P]
         L.pa_status_string.restype = ctypes.c_char_p
@@ -589,27 +592,53 @@ PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
 LATENT_ROPE_DIM = 64  # rotary dims of a latent cell
 
 
-def _strided(t: torch.Tensor, what: str, dtype=torch.bfloat16) -> Optional[int]:
-    """Device pointer of a tensor whose innermost dimension is contiguous, on
-    the current device."""
+def _device_of(t: torch.Tensor, what: str) -> int:
+    """The current device, on which a call's first tensor must be."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    # (what torch.cuda.current_device() and, below, current_stream() return,
+    # without their Python layers: a decode step's calls are small enough for
+    # the difference to show)
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} is on {t.device}, not on the current device")
+    return dev
+
+
+def _on(dev: int, stream) -> int:
+    """The raw stream of a call on device `dev`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def _refuse(t: torch.Tensor, what: str, dtype, dev: int) -> None:
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, not on the current device")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    raise ValueError(f"{what} is on {t.device}, the call on cuda:{dev}")
+
+
+def _strided(t: torch.Tensor, what: str, dev: int, dtype=torch.bfloat16) -> int:
+    """Device pointer of a tensor on device `dev` whose innermost dimension is
+    contiguous (0 for an empty one)."""
+    if t.get_device() != dev or t.dtype is not dtype:
+        _refuse(t, what, dtype, dev)
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"{what}: the innermost dimension must be contiguous")
-    return t.data_ptr() if t.numel() else None
+    return t.data_ptr()
 
 
-def _flat(t: Optional[torch.Tensor], what: str, dtype) -> Optional[int]:
-    """Device pointer of a contiguous tensor on the current device (None stays None)."""
+def _flat(t: Optional[torch.Tensor], what: str, dev: int, dtype) -> Optional[int]:
+    """Device pointer of a contiguous tensor on device `dev` (None stays None)."""
     if t is None:
         return None
+    if t.get_device() != dev or t.dtype is not dtype:
+        _refuse(t, what, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
-    return _strided(t.view(-1), what, dtype)
+    return t.data_ptr()
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
@@ -662,11 +691,12 @@ def rope(x: torch.Tensor, out: torch.Tensor, positions: torch.Tensor, inv_freq: 
     T, H, D = x.shape
     if positions.numel() != T:
         raise ValueError("positions must have one entry per token")
+    dev = _device_of(x, "x")
     _check(lib().pa_rope(
-        _strided(x, "x"), x.stride(0), x.stride(1), _strided(out, "out"), out.stride(0),
-        out.stride(1), _flat(positions, "positions", torch.int32), T, H, D,
-        _flat(inv_freq, "inv_freq", torch.float32), 2 * inv_freq.numel(),
-        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor, _stream(stream)), "pa_rope")
+        _strided(x, "x", dev), x.stride(0), x.stride(1), _strided(out, "out", dev), out.stride(0),
+        out.stride(1), _flat(positions, "positions", dev, torch.int32), T, H, D,
+        _flat(inv_freq, "inv_freq", dev, torch.float32), 2 * inv_freq.numel(),
+        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor, _on(dev, stream)), "pa_rope")
 
 
 class LatentPool:
@@ -692,23 +722,22 @@ class LatentPool:
         self.num_blocks, self.block_size, self.latent_dim = latent.shape
         self.rope_dim = rope.shape[2]
 
-    def struct(self) -> _LatentPool:
-        return _LatentPool(_flat(self.latent, "latent", self.latent.dtype),
-                           _flat(self.rope, "rope", torch.bfloat16),
-                           _flat(self.scales, "scales", torch.float32), self.num_blocks,
+    def struct(self, dev: int) -> _LatentPool:
+        return _LatentPool(_flat(self.latent, "latent", dev, self.latent.dtype),
+                           _flat(self.rope, "rope", dev, torch.bfloat16),
+                           _flat(self.scales, "scales", dev, torch.float32), self.num_blocks,
                            self.block_size, self.latent_dim, self.rope_dim, self.dtype)
 
-    def ref(self):
-        """ctypes reference to the pool's C struct, built once per set of
-        device pointers (storage may move under a tensor)."""
-        t = (self.latent.data_ptr(), self.rope.data_ptr(),
-             None if self.scales is None else self.scales.data_ptr(),
-             torch.cuda.current_device())
+    def ref(self, dev: int):
+        """ctypes reference to the pool's C struct, built once per device and
+        set of pointers (storage may move under a tensor)."""
+        at = (dev, self.latent.data_ptr(), self.rope.data_ptr(),
+              None if self.scales is None else self.scales.data_ptr())
         c = self.__dict__.get("_c")
-        if c is None or c[2] != t:
-            st = self.struct()
-            c = self.__dict__["_c"] = (st, ctypes.byref(st), t)
-        return c[1]
+        if c is None or c[1] != at:
+            c = (ctypes.byref(self.struct(dev)), at)
+            self.__dict__["_c"] = c
+        return c[0]
 
     def __setattr__(self, name, value):
         self.__dict__.pop("_c", None)
@@ -739,11 +768,14 @@ def write_latent(pool: LatentPool, latent: torch.Tensor, k_rope: torch.Tensor,
         raise ValueError("positions and inv_freq come together")
     if T == 0:
         return
+    dev = _device_of(pool.latent, "the pool")
     _check(lib().pa_write_latent(
-        pool.ref(), _strided(latent, "latent"), ls, _strided(k_rope, "k_rope"), rs,
-        _flat(positions, "positions", torch.int32), _flat(inv_freq, "inv_freq", torch.float32),
+        pool.ref(dev), _strided(latent, "latent", dev), ls, _strided(k_rope, "k_rope", dev), rs,
+        _flat(positions, "positions", dev, torch.int32),
+        _flat(inv_freq, "inv_freq", dev, torch.float32),
         PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor,
-        _flat(slot_mapping, "slot_mapping", torch.int64), T, _stream(stream)), "pa_write_latent")
+        _flat(slot_mapping, "slot_mapping", dev, torch.int64), T, _on(dev, stream)),
+        "pa_write_latent")
 
 
 def read_latent(pool: LatentPool, block_tables: torch.Tensor, kv_start_loc: torch.Tensor,
@@ -758,20 +790,23 @@ def read_latent(pool: LatentPool, block_tables: torch.Tensor, kv_start_loc: torc
         raise ValueError("kv_start_loc must have num_reqs + 1 entries and first num_reqs")
     if rope_out.shape[0] != N:
         raise ValueError("latent_out and rope_out must have the same rows")
+    dev = _device_of(pool.latent, "the pool")
     _check(lib().pa_read_latent(
-        pool.ref(), _flat(block_tables, "block_tables", torch.int32), max_blocks,
-        _flat(kv_start_loc, "kv_start_loc", torch.int32), _flat(first, "first", torch.int32), R, N,
-        _strided(latent_out, "latent_out"), ls, _strided(rope_out, "rope_out"), rs,
-        _stream(stream)), "pa_read_latent")
+        pool.ref(dev), _flat(block_tables, "block_tables", dev, torch.int32), max_blocks,
+        _flat(kv_start_loc, "kv_start_loc", dev, torch.int32),
+        _flat(first, "first", dev, torch.int32), R, N,
+        _strided(latent_out, "latent_out", dev), ls, _strided(rope_out, "rope_out", dev), rs,
+        _on(dev, stream)), "pa_read_latent")
 
 
 def copy_latent_blocks(pool: LatentPool, src: torch.Tensor, dst: torch.Tensor,
                        stream=None) -> None:
     if src.numel() != dst.numel():
         raise ValueError("src and dst must pair up")
+    dev = _device_of(pool.latent, "the pool")
     _check(lib().pa_copy_latent_blocks(
-        pool.ref(), _flat(src, "src", torch.int32), _flat(dst, "dst", torch.int32), src.numel(),
-        _stream(stream)), "pa_copy_latent_blocks")
+        pool.ref(dev), _flat(src, "src", dev, torch.int32), _flat(dst, "dst", dev, torch.int32),
+        src.numel(), _on(dev, stream)), "pa_copy_latent_blocks")
 
 
 def latent_workspace_size(num_q_heads: int, latent_dim: int) -> int:
@@ -795,15 +830,45 @@ def latent_forward(q: torch.Tensor, out: torch.Tensor, query_start_loc: torch.Te
     if block_tables.dim() != 2 or block_tables.shape[0] != R:
         raise ValueError("block_tables must be [num_reqs][max_blocks]")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    dev = _device_of(q, "q")
     st = lib().pa_latent_forward(
-        _flat(q, "q", torch.bfloat16), _flat(out, "out", torch.bfloat16),
-        _flat(query_start_loc, "query_start_loc", torch.int32),
-        _flat(seq_lens, "seq_lens", torch.int32), _np_addr(qh), _np_addr(sh),
-        _flat(block_tables, "block_tables", torch.int32), block_tables.shape[1], R, T, H,
-        pool.ref(), float(scale), int(causal),
-        None if workspace is None else _flat(workspace, "workspace", workspace.dtype), ws_bytes,
-        _stream(stream))
+        _flat(q, "q", dev, torch.bfloat16), _flat(out, "out", dev, torch.bfloat16),
+        _flat(query_start_loc, "query_start_loc", dev, torch.int32),
+        _flat(seq_lens, "seq_lens", dev, torch.int32), _np_addr(qh), _np_addr(sh),
+        _flat(block_tables, "block_tables", dev, torch.int32), block_tables.shape[1], R, T, H,
+        pool.ref(dev), float(scale), int(causal),
+        None if workspace is None else _flat(workspace, "workspace", dev, workspace.dtype),
+        ws_bytes, _on(dev, stream))
     _check(st, "pa_latent_forward")
+
+
+def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
+                   out: torch.Tensor, query_start_loc: torch.Tensor, kv_start_loc: torch.Tensor,
+                   qsl_host, ksl_host, scale: float, causal: int = 1, stream=None) -> None:
+    """Expanded attention: q [T][H][192] against k_nope [Tk][H][128] and the
+    shared k_rope [Tk][64], values v [Tk][H][128], into out [T][H][128];
+    requests ragged on both sides."""
+    qh = _host_i32(qsl_host)
+    kh = _host_i32(ksl_host)
+    R = qh.size - 1
+    if kh.size != R + 1 or query_start_loc.numel() != R + 1 or kv_start_loc.numel() != R + 1:
+        raise ValueError("the start arrays must have num_reqs + 1 entries")
+    T, H, D = q.shape
+    Tk, Hk, Dn = k_nope.shape
+    Dr, Dv = k_rope.shape[-1], v.shape[-1]
+    if Hk != H or D != Dn + Dr or v.shape != (Tk, H, Dv) or k_rope.shape != (Tk, Dr) or \
+            out.shape != (T, H, Dv):
+        raise ValueError("q [T][H][Dn + Dr], k_nope [Tk][H][Dn], k_rope [Tk][Dr], v [Tk][H][Dv] "
+                         "and out [T][H][Dv] must agree")
+    dev = _device_of(q, "q")
+    st = lib().pa_latent_prefill(
+        _strided(q, "q", dev), q.stride(0), q.stride(1), _strided(k_nope, "k_nope", dev),
+        k_nope.stride(0), k_nope.stride(1), _strided(k_rope, "k_rope", dev), k_rope.stride(0),
+        _strided(v, "v", dev), v.stride(0), v.stride(1), _flat(out, "out", dev, torch.bfloat16),
+        _flat(query_start_loc, "query_start_loc", dev, torch.int32),
+        _flat(kv_start_loc, "kv_start_loc", dev, torch.int32), _np_addr(qh), _np_addr(kh), R, T,
+        Tk, H, Dn, Dr, Dv, float(scale), int(causal), _on(dev, stream))
+    _check(st, "pa_latent_prefill")
 
 
 def selftest_wait_timeout(stream=None) -> None:

@@ -101,7 +101,7 @@ SHAPES = [  # seq_lens, q_lens, H, L, B
 ]
 
 
-@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("case", range(len(SHAPES)))
 def test_shapes(cuda_device, case, fp8):
     seqs, q_lens, H, L, B = SHAPES[case]
@@ -111,7 +111,7 @@ def test_shapes(cuda_device, case, fp8):
     b.check()
 
 
-@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("mult", [0.0, 0.05, 6.0])
 def test_flat_and_peaked_scores(cuda_device, mult, fp8):
     """Equal weights, nearly equal ones, and rows that one key owns (the
@@ -122,7 +122,7 @@ def test_flat_and_peaked_scores(cuda_device, mult, fp8):
     b.check()
 
 
-@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 def test_rising_scores_rescale_every_tile(cuda_device, fp8):
     """Keys that grow along the context: the maximum rises tile after tile."""
     dev = cuda_device
@@ -140,7 +140,7 @@ def test_rising_scores_rescale_every_tile(cuda_device, fp8):
     b.check()
 
 
-@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 def test_not_causal(cuda_device, fp8):
     b = Batch([100, 64, 7], [30, 1, 7], 6, 512, 16, fp8, cuda_device, seed=5, causal=0)
     b.run()
@@ -161,7 +161,7 @@ def test_rows_past_the_last_sequence_stay(cuda_device):
     assert (b.out[4:] == 9).all()
 
 
-@pytest.mark.parametrize("fp8", [False], ids=["bf16"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 def test_deterministic_and_independent_of_placement(cuda_device, fp8):
     dev = cuda_device
     b = Batch([777, 2000, 33], [1, 2, 1], 20, 512, 32, fp8, dev, seed=7)

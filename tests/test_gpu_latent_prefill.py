@@ -1,0 +1,200 @@
+"""GPU tests of pa_latent_prefill (expanded attention) against the 64-bit
+reference. The tolerance is that of the absorbed form's tests: half a bf16 step
+of every softmax weight and of the output, and the fp32 scores' error."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_143_gb300 import pa
+from tests import latent_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DN, DR, DV = 128, 64, 128
+
+
+def i32(a, dev):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=dev)
+
+
+class Chunks:
+    def __init__(self, q_lens, k_lens, H, dev, seed=0, mult=1.0, causal=1, spare=0, split=True):
+        rng = np.random.default_rng(seed)
+
+        def rand(*shape, m=1.0):
+            x = rng.standard_normal(shape, dtype=np.float32) * np.float32(m)
+            return torch.from_numpy(x).to(dev).bfloat16()
+
+        self.q_lens, self.k_lens, self.H, self.causal = q_lens, k_lens, H, causal
+        self.qsl, self.ksl = (np.cumsum([0] + list(x)).astype(np.int32) for x in (q_lens, k_lens))
+        T, Tk = int(self.qsl[-1]) + spare, int(self.ksl[-1]) + spare
+        self.q = rand(T, H, DN + DR, m=mult)
+        kv = rand(Tk, H, DN + DV)
+        self.k, self.v = (kv[..., :DN], kv[..., DN:])
+        if not split:
+            self.k, self.v = self.k.contiguous(), self.v.contiguous()
+        self.kr = rand(Tk, DR)
+        self.scale = (DN + DR) ** -0.5
+        self.out = torch.full((T, H, DV), 9.0, dtype=torch.bfloat16, device=dev)
+        self.qsl_dev, self.ksl_dev = i32(self.qsl, dev), i32(self.ksl, dev)
+        # the mirrors plan for every row of the buffers, the spare ones too
+        self.qsl_host, self.ksl_host = self.qsl.copy(), self.ksl.copy()
+        self.qsl_host[-1] += spare
+        self.ksl_host[-1] += spare
+
+    def run(self):
+        pa.latent_prefill(self.q, self.k, self.kr, self.v, self.out, self.qsl_dev, self.ksl_dev,
+                          self.qsl_host, self.ksl_host, self.scale, self.causal)
+        return self.out
+
+    def check(self, reqs=None, rows=None):
+        for r in range(len(self.q_lens)) if reqs is None else reqs:
+            a, b, c, d = self.qsl[r], self.qsl[r + 1], self.ksl[r], self.ksl[r + 1]
+            if a == b:
+                continue
+            q = ref.f64(self.q[a:b])
+            k, kr, v = ref.f64(self.k[c:d]), ref.f64(self.kr[c:d]), ref.f64(self.v[c:d])
+            want, p = ref.expanded(q, k, kr, v, self.scale, self.causal)
+            size = np.einsum("thn,nhd->thd", p, np.abs(v))
+            s_mag = np.zeros((b - a, self.H, 1))
+            if d > c:
+                s_mag = self.scale * (
+                    np.einsum("thd,nhd->thn", np.abs(q[..., :DN]), np.abs(k))
+                    + np.einsum("thd,nd->thn", np.abs(q[..., DN:]), np.abs(kr))).max(-1)[..., None]
+            tol = size * (ref.BF16_HALF + 2 * 2.0 ** -20 * s_mag) + ref.BF16_HALF * np.abs(want)
+            got = ref.f64(self.out[a:b])
+            assert np.isfinite(got).all()
+            err = np.abs(got - want)
+            assert (err <= tol + 1e-30).all(), (r, err.max(), (err / (tol + 1e-30)).max())
+
+
+SHAPES = [  # q_lens, k_lens, H
+    ([1], [1], 1),
+    ([1, 1, 1], [1, 128, 1000], 3),
+    ([127, 128, 129, 255, 256, 257], [127, 128, 129, 255, 256, 257], 2),
+    ([64, 300], [64 + 500, 300 + 77], 5),
+    ([5, 0, 130], [40, 9, 130], 4),
+    ([700], [2100], 2),
+    ([33, 520], [33, 520], 16),
+    ([2] * 70, [3] * 70, 1),
+]
+
+
+@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("case", range(len(SHAPES)))
+def test_shapes(cuda_device, case, causal):
+    q, k, H = SHAPES[case]
+    b = Chunks(q, k, H, cuda_device, seed=case, causal=causal)
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check()
+
+
+@pytest.mark.parametrize("mult", [0.0, 8.0])
+def test_flat_and_peaked_scores(cuda_device, mult):
+    b = Chunks([200, 300], [900, 300], 2, cuda_device, seed=1, mult=mult)
+    b.run()
+    b.check()
+
+
+def test_rows_without_a_visible_key_are_zero(cuda_device):
+    """Fewer keys than queries: the first queries see nothing; a request
+    without keys is all zeros."""
+    for causal in (1, 0):
+        b = Chunks([300, 40, 200], [100, 0, 200], 3, cuda_device, seed=2, causal=causal)
+        b.run()
+        assert pa.get_error() == pa.PA_OK
+        b.check()
+        assert (b.out[300:340] == 0).all()
+        if causal:
+            assert (b.out[:200] == 0).all()
+    empty = Chunks([7], [0], 2, cuda_device, seed=2)  # no key at all
+    empty.run()
+    assert pa.get_error() == pa.PA_OK and (empty.out == 0).all()
+
+
+def test_foreign_rows_may_hold_nan(cuda_device):
+    """Keys and values of other requests, and rows past the last request,
+    never reach a request's rows."""
+    dev = cuda_device
+    b = Chunks([90, 150, 64], [90, 150 + 33, 64], 2, dev, seed=3, spare=40)
+    b.run()
+    want = b.out[90:240].clone()
+    nan = float("nan")
+    for t in (b.k, b.v, b.kr):
+        t[:90] = nan
+        t[90 + 183:] = nan
+    b.out.fill_(9.0)
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    assert torch.equal(b.out[90:240].view(torch.int16), want.view(torch.int16))
+    assert (b.out[304:] == 9).all()  # rows past the last sequence stay
+    b.check(reqs=[1])
+
+
+def test_strides(cuda_device):
+    """Contiguous keys and values, heads outside tokens, a padded query row."""
+    dev = cuda_device
+    b = Chunks([130, 20], [200, 50], 4, dev, seed=4)
+    want = b.run().clone()
+    for form in ("contiguous", "heads_outside"):
+        k, v, q, kr = b.k, b.v, b.q, b.kr
+        if form == "contiguous":
+            k, v = k.contiguous(), v.contiguous()
+            q = torch.nn.functional.pad(q, (0, 8))[..., :192]
+            kr = torch.nn.functional.pad(kr, (0, 16))[..., :64]
+        else:
+            k, v, q = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (k, v, q))
+        out = torch.empty_like(want)
+        pa.latent_prefill(q, k, kr, v, out, b.qsl_dev, b.ksl_dev, b.qsl, b.ksl, b.scale)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    assert pa.get_error() == pa.PA_OK
+    bad = torch.zeros(b.k.shape[0], 4, DN + 4, dtype=torch.bfloat16, device=dev)[..., :DN]
+    with pytest.raises(pa.PaError):
+        pa.latent_prefill(b.q, bad, b.kr, b.v, out, b.qsl_dev, b.ksl_dev, b.qsl, b.ksl, b.scale)
+
+
+def test_more_units_than_the_list_holds(cuda_device):
+    """1100 one-token requests: the grid walks every request."""
+    n = 1100
+    b = Chunks([1] * n, [2] * n, 1, cuda_device, seed=5)
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check(reqs=range(0, n, 37))
+
+
+def test_deterministic(cuda_device):
+    b = Chunks([400, 31], [1000, 31], 3, cuda_device, seed=6)
+    first = b.run().clone()
+    assert torch.equal(b.run().view(torch.int16), first.view(torch.int16))
+
+
+def test_captured_and_on_another_stream(cuda_device):
+    b = Chunks([140, 31], [500, 31], 3, cuda_device, seed=7)
+    first = b.run().clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        b.run()
+    b.out.fill_(9.0)
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(b.out.view(torch.int16), first.view(torch.int16))
+    assert pa.get_error() == pa.PA_OK
+
+
+def test_device_starts_that_disagree_are_flagged(cuda_device):
+    dev = cuda_device
+    b = Chunks([300, 40], [300, 40], 2, dev, seed=8)
+    good = b.run().clone()
+    assert pa.get_error() == pa.PA_OK
+    for q, k in (([0, 300, 341], None), ([0, 30, 340], None), ([0, -1, 340], None),
+                 (None, [0, 300, 341]), (None, [0, 400, 340]), (None, [-3, 300, 340])):
+        b.qsl_dev = i32(b.qsl if q is None else q, dev)
+        b.ksl_dev = i32(b.ksl if k is None else k, dev)
+        b.run()
+        assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS, (q, k)
+    b.qsl_dev, b.ksl_dev = i32(b.qsl, dev), i32(b.ksl, dev)
+    assert torch.equal(b.run().view(torch.int16), good.view(torch.int16))
+    assert pa.get_error() == pa.PA_OK

@@ -200,3 +200,35 @@ def test_latent_forward_refusals():
     assert call(pool=dict(latent_dim=128)) == pa.PA_ERR_UNSUPPORTED
     assert call(H=1 << 30) == pa.PA_ERR_UNSUPPORTED  # rows past 32-bit coordinates
     assert pa.latent_workspace_size(0, 512) == 0 and pa.latent_workspace_size(16, 100) == 0
+
+
+def test_latent_prefill_refusals():
+    L = pa.lib()
+    i = lambda *v: np.array(v, np.int32)
+    ptr = lambda a: None if a is None else a.ctypes.data_as(ctypes.c_void_p)
+    ok = dict(q=P, qt=768, qh=192, k=P, kt=512, kh=128, kr=P, rt=64, v=P, vt=512, vh=128, out=P,
+              qsl=P, ksl=P, qhost=i(0, 1, 3), khost=i(0, 4, 9), R=2, T=3, Tk=9, H=4, dn=128,
+              dr=64, dv=128, scale=0.1, causal=1)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return L.pa_latent_prefill(
+            a["q"], a["qt"], a["qh"], a["k"], a["kt"], a["kh"], a["kr"], a["rt"], a["v"], a["vt"],
+            a["vh"], a["out"], a["qsl"], a["ksl"], ptr(a["qhost"]), ptr(a["khost"]), a["R"],
+            a["T"], a["Tk"], a["H"], a["dn"], a["dr"], a["dv"], a["scale"], a["causal"], None)
+
+    for bad in (dict(R=-1), dict(T=-1), dict(Tk=-1), dict(H=0), dict(scale=0.0),
+                dict(scale=float("nan")), dict(causal=3), dict(qhost=None), dict(khost=None),
+                dict(qsl=None), dict(ksl=None), dict(T=4), dict(Tk=8), dict(qhost=i(0, 4, 3)),
+                dict(khost=i(0, 10, 9)), dict(qhost=i(1, 1, 3)), dict(q=None), dict(q=24),
+                dict(out=None), dict(out=24), dict(k=None), dict(v=None), dict(kr=None),
+                dict(k=24), dict(v=24), dict(kr=24), dict(qt=770), dict(qh=0), dict(kt=-8),
+                dict(kh=132), dict(vt=0), dict(vh=4), dict(rt=60), dict(R=0)):
+        assert call(**bad) == pa.PA_ERR_INVALID, bad
+    assert call(R=0, T=0, Tk=0) == pa.PA_OK
+    assert call(T=0, qhost=i(0, 0, 0)) == pa.PA_OK
+    for bad in (dict(dn=64), dict(dr=32), dict(dv=64)):
+        assert call(**bad) == pa.PA_ERR_UNSUPPORTED, bad
+    n = 40000
+    assert call(R=n, T=n, Tk=0, qhost=np.arange(n + 1, dtype=np.int32),
+                khost=np.zeros(n + 1, np.int32)) == pa.PA_ERR_UNSUPPORTED
