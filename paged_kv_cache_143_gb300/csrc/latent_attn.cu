@@ -10,22 +10,27 @@
 // operations on it; up to about 128 rows per request that is less tensor time
 // than the cell takes from HBM, so the design is laid out for streaming.
 //
-// One CTA per SM walks an equal share of all (row tile, 64-key tile) pairs
+// One CTA per SM walks an equal share of all (row tile, 32-key tile) pairs
 // (pa::LatentParams). Both products run on the 5th-generation tensor cores:
-//   S [64 rows x 64 keys] = Q K^T     Q and the cells K-major in shared memory
+//   S [64 rows x 32 keys] = Q K^T     Q and the cells K-major in shared memory
 //   O^T [L x NR]        += c^T P^T    the same cells read again, MN-major, as
 //                                     the A operand; P from shared memory
 // O is kept transposed (lane = latent dim, column = row) because a row of O is
 // L fp32 values: NR x 512 of them as [dim][row] take 4 NR TMEM columns, and the
 // products stay full 128-row instructions for few query rows, where rows
-// down the lanes would leave most of the tensor core (and 16 of every 32 lanes)
-// idle. NR is 16, 32 or 64.
-//   warp 0      TMA producer: the Q tile, then per key tile one box per physical
-//               block and 64-column chunk into a ring of stages
-//   warp 1      TMEM, and one thread that issues the MMAs: S(j + 1) goes in
-//               before PV(j), so the tensor core works while softmax(j) does
+// down the lanes would leave most of the tensor core idle. NR is 16, 32 or 64.
+// Tiles are 32 keys (36 KB at L 512) so that four of them fit beside 64 rows of
+// Q: a stage is loading for about 2000 cycles and in use (S, softmax, PV and
+// their hand-overs) for 2700, and what HBM delivers a tile in is 1570.
+//   warp 0      TMA producer: the Q tile, then the key tiles into a ring of stages,
+//               whole rows at once, one box per physical block and 64 columns
+//   warp 1      TMEM and, one elected lane, the MMAs: whichever is ready of the
+//               next S (up to three tiles ahead) and the next PV
 //   warps 4-7   softmax of 16 rows each (S read as 16 x 256-bit fragments: a row
 //               in four lanes), P written by stmatrix; then the output
+// The softmax warps share nothing tile by tile. A warp that moves a row's
+// reference maximum says so beside P; the MMA warp then asks all four to rescale
+// their dims of O before it issues that PV (rare: growth by more than 2^8).
 // Every wait is bounded; a timeout sets the error word and the CTA unwinds.
 #include <cudaTypedefs.h>
 
@@ -43,9 +48,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRope = 64;
 constexpr int KT = kLatentKeys;
-constexpr int kChunk = KT * 128;   // one 64-column bf16 chunk of a key tile
+constexpr int kChunk = KT * 128;   // 64 bf16 columns of a key tile
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 256;   // S buffers at columns 256, 320
+constexpr uint32_t kTmemS = 256;   // S buffers at columns 256, 288, 320, 352
+constexpr int kSBufs = 4, kMaxStages = 10;
 constexpr float kRescaleLog2 = 8.f;
 
 template <int L, int NR>
@@ -53,14 +59,15 @@ struct Smem {
   static constexpr int kChunks = L / 64 + 1;          // the last one is the rotary part
   static constexpr int kQBytes = kChunks * NR * 128;
   static constexpr int kStage = kChunks * kChunk;
-  static constexpr int kPBytes = NR * 128;
+  static constexpr int kPBytes = NR * 128;            // two tiles of P side by side
   static constexpr int kTail = 2048;                  // barriers and row statistics
-  static constexpr int kStages = (232448 - 1024 - kTail - kQBytes - kPBytes) / kStage;
+  static constexpr int kFit = (232448 - 1024 - kTail - kQBytes - kPBytes) / kStage;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kOffK = kQBytes;
   static constexpr int kOffP = kOffK + kStages * kStage;
   static constexpr int kOffTail = kOffP + kPBytes;
   static constexpr int kAlloc = kOffTail + kTail + 1024;  // the base is rounded up to 1024 B
-  static_assert(kStages >= 2, "needs two key tiles in flight");
+  static_assert(kStages >= 4, "needs four key tiles in flight");
   static_assert(kAlloc <= 232448, "dynamic shared memory above the 227 KB per-block limit");
   static_assert(kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzled tiles start on 1024 bytes");
   // S always reads 64 rows of Q: the rows past NR are whatever follows in
@@ -68,17 +75,19 @@ struct Smem {
   static_assert(kQBytes + (64 - NR) * 128 <= kAlloc - 1024, "Q over-read leaves the allocation");
 };
 
-constexpr int kMaxStages = 5;
 struct Tail {
   uint64_t q_full, q_empty;
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
-  uint64_t s_full[2];
-  uint64_t p_full, pv_done, o_empty, final_mma;
-  float alpha[2][kLatentRows];
-  float l[kLatentRows];
-  int fail[3];         // a softmax warp gave up: tiles by parity, then outputs
+  uint64_t s_full[kSBufs];
+  uint64_t p_full[2], pv_done[2];
+  uint64_t fix, fixed;           // O is to be rescaled for tile fix_tile; it has been
+  uint64_t o_empty, final_mma;
+  float alpha[2][kLatentRows];   // by tile: factors of the rows of a warp that asks
+  float l[2][kLatentRows];       // by piece: 1 / sum
+  uint8_t ask[2][4];             // by tile: softmax warps that ask for a rescale
+  int32_t fix_tile;
   int64_t warp_sum[kThreads / 32];
-  int64_t base;        // flat start of the request that holds the CTA's first tile
+  int32_t base;        // flat start of the request that holds the CTA's first tile
   int32_t req;         // that request
   uint32_t tmem;
   int abort;
@@ -89,26 +98,16 @@ __device__ __forceinline__ bool aborted(Tail* t) {
   return *reinterpret_cast<volatile int*>(&t->abort) != 0;
 }
 
-// The softmax warps meet at named barriers, so they must leave together: one
-// that gave up (bad) says so before the barrier, and all read it after. The
-// flag read behind one barrier is not written again before the next.
-__device__ __forceinline__ bool agreed_to_stop(Tail* t, int which) {
-  return *reinterpret_cast<volatile int*>(&t->fail[which]) != 0;
-}
-
-// 16 lanes x 64 columns as mma-style fragments: of each 8-column group i,
+// 16 lanes x 32 columns as mma-style fragments: of each 8-column group i,
 // r[4 i], r[4 i + 1] are columns 2 (lane % 4), + 1 of row lane / 4, and
 // r[4 i + 2], r[4 i + 3] those of row lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 
@@ -148,8 +147,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // ------------------------------------------------------------ the flat space
 
 struct Request {
-  int32_t q_begin, q_len, seq, tiles, keys;  // row tiles, key tiles
-  int64_t weight;                            // tiles * keys; 0 for one without work
+  int32_t q_begin, q_len, seq, rows, keys;  // query rows, key tiles
+  int64_t weight;                           // row tiles * keys; 0 for one without work
 };
 
 // Reads request r; one whose device entries do not fit the buffers has no
@@ -166,9 +165,9 @@ __device__ __forceinline__ Request load_request(const LatentParams& p, int r, bo
     if (report) raise_error(p.err, kErrBounds);
     return q;
   }
-  q.tiles = (int)(((int64_t)q.q_len * p.Hq + NR - 1) / NR);
+  q.rows = q.q_len * p.Hq;  // (T * Hq fits 32 bits)
   q.keys = (q.seq + KT - 1) / KT;
-  q.weight = (int64_t)q.tiles * q.keys;
+  q.weight = (int64_t)((q.rows + NR - 1) / NR) * q.keys;
   return q;
 }
 
@@ -180,14 +179,14 @@ struct Piece {
   int32_t slot;        // partial slot 0 / 1 of the CTA, or -1: the whole unit
 };
 
+// (The whole flat space fits 31 bits, so do all positions.)
 template <int NR>
 struct Walk {
-  int64_t pos, end, base;
-  int r;
+  int32_t pos, end, base, r;
   bool loaded;
   Request q;
 
-  __device__ Walk(const Tail* t, int64_t begin, int64_t stop)
+  __device__ Walk(const Tail* t, int32_t begin, int32_t stop)
       : pos(begin), end(stop), base(t->base), r(t->req), loaded(false), q{} {}
 
   __device__ bool next(const LatentParams& p, Piece& out) {
@@ -196,24 +195,24 @@ struct Walk {
       q = load_request<NR>(p, r, false);
       loaded = true;
     }
-    while (pos >= base + q.weight) {
-      base += q.weight;
+    while (pos - base >= (int32_t)q.weight) {
+      base += (int32_t)q.weight;
       if (++r >= p.R) return false;
       q = load_request<NR>(p, r, false);
     }
-    const int64_t off = pos - base;
+    const unsigned off = pos - base;
     out.r = r;
-    out.tile = (int)(off / q.keys);
-    out.k0 = (int)(off - (int64_t)out.tile * q.keys);
-    const int64_t left = end - pos;
-    const int k1 = left < q.keys - out.k0 ? out.k0 + (int)left : q.keys;
+    out.tile = (int)(off / (unsigned)q.keys);
+    out.k0 = (int)off - out.tile * q.keys;
+    const int k1 = min(q.keys, out.k0 + (end - pos));
     pos += k1 - out.k0;
     out.slot = out.k0 > 0 ? 0 : k1 < q.keys ? 1 : -1;
-    const int64_t row0 = (int64_t)out.tile * NR;
-    const int64_t left_rows = (int64_t)q.q_len * p.Hq - row0;
-    out.rows = left_rows < NR ? (int)left_rows : NR;
-    const int last_tok = (int)((row0 + out.rows - 1) / p.Hq);
-    out.n_keys = p.causal ? q.seq - q.q_len + last_tok + 1 : q.seq;
+    out.rows = min(NR, q.rows - out.tile * NR);
+    out.n_keys = q.seq;
+    if (p.causal && q.q_len > 1) {  // up to the last row's token
+      const unsigned last_row = out.tile * NR + out.rows - 1;
+      out.n_keys = q.seq - q.q_len + (int)(last_row / (unsigned)p.Hq) + 1;
+    }
     out.k1 = min(k1, (out.n_keys + KT - 1) / KT);
     return true;
   }
@@ -226,7 +225,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmap_r, const LatentParams p) {
   using S = Smem<L, NR>;
   constexpr int kStages = S::kStages;
-  static_assert(kStages <= kMaxStages, "");
   constexpr int kBlocks = L / 128;  // 128-dim blocks of O^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -248,14 +246,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tail->k_full[s], 1);
       mbar_init(&tail->k_empty[s], 1);
     }
-    mbar_init(&tail->s_full[0], 1);
-    mbar_init(&tail->s_full[1], 1);
-    mbar_init(&tail->p_full, 4);   // one arrival per softmax warp
-    mbar_init(&tail->pv_done, 1);
+    for (int s = 0; s < kSBufs; ++s) mbar_init(&tail->s_full[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tail->p_full[s], 4);   // one arrival per softmax warp
+      mbar_init(&tail->pv_done[s], 1);
+    }
+    mbar_init(&tail->fix, 1);
+    mbar_init(&tail->fixed, 4);
     mbar_init(&tail->o_empty, 4);
     mbar_init(&tail->final_mma, 1);
     tail->abort = 0;
-    tail->fail[0] = tail->fail[1] = tail->fail[2] = 0;
     tail->req = p.R;
     tail->base = 0;
     fence_mbar_init();
@@ -289,8 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     kept_before = W + scan(kept_w, total);
     W += total;
   }
-  const int64_t Q = (W + gridDim.x - 1) / gridDim.x;
-  const int64_t begin = min(W, cta * Q), end = min(W, begin + Q);
+  if (W > INT32_MAX) {  // (the host has checked its mirrors)
+    if (cta == 0 && threadIdx.x == 0) raise_error(p.err, kErrBounds);
+    W = 0;
+  }
+  const unsigned Q = ((unsigned)W + gridDim.x - 1) / gridDim.x;
+  const int begin = (int)min((int64_t)W, (int64_t)cta * Q), end = (int)min(W, (int64_t)begin + Q);
   if (p.R > kThreads) {  // the sums of all but the last step are taken again
     int64_t sum = 0;
     for (int r0 = 0; r0 < p.R; r0 += kThreads) {
@@ -301,27 +305,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum += total;
       if (begin >= before && begin < before + w) {
         tail->req = r;
-        tail->base = before;
+        tail->base = (int)before;
       }
     }
   } else if (begin >= kept_before && begin < kept_before + kept_w) {
     tail->req = threadIdx.x;
-    tail->base = kept_before;
+    tail->base = (int)kept_before;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tail->tmem;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 64) {
     // the unit cut at this CTA's start, for the join: handled at its first cut
     LatentJoin j{};
     if (begin < end) {
       const Request q = load_request<NR>(p, tail->req, false);
-      const int64_t tile = (begin - tail->base) / q.keys;
-      const int64_t a = tail->base + tile * q.keys;  // the unit's start
-      if (begin > a && a / Q + 1 == cta) {
-        const int64_t rows = (int64_t)q.q_len * p.Hq - tile * NR;
-        j.rows = (int32_t)min(rows, (int64_t)NR);
+      const int tile = (begin - tail->base) / q.keys;
+      const unsigned a = tail->base + tile * q.keys;  // the unit's start
+      if ((unsigned)begin > a && a / Q + 1 == (unsigned)cta) {
+        j.rows = min(q.rows - tile * NR, NR);
         j.last = (int32_t)((a + q.keys - 1) / Q);
         j.out_row = (int64_t)q.q_begin * p.Hq + tile * NR;
       }
@@ -338,61 +341,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::prefetch_tensormap(&tmap_c);
         tc::prefetch_tensormap(&tmap_r);
       }
-      const int bpt = KT / p.B;  // blocks per key tile: 4, 2 or 1
+      const int rows = min(p.B, KT);             // rows of one box
+      const int bpt = KT / rows;                 // boxes down a tile: 2 or 1
+      const int b = lane / S::kChunks, c = lane - b * S::kChunks;  // the lane's box
       Walk<NR> walk(tail, begin, end);
       Piece pc;
-      int g = 0, pieces = 0;     // key tiles and pieces so far
+      int g = 0, pieces = 0;                     // key tiles and pieces so far
+      int st = 0, phase = 1;                     // stage, and the parity its emptying waits for
       bool ok = true;
       while (ok && walk.next(p, pc)) {
         if (pc.k0 >= pc.k1) continue;  // no row of the tile sees these keys
-        if (pieces > 0) {
-          if (lane == 0) ok = mbar_wait(&tail->q_empty, (pieces - 1) & 1, p.err);
-          ok = __shfl_sync(full, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-        }
+        ok = pieces == 0 ||
+             __all_sync(full, mbar_wait(&tail->q_empty, (pieces - 1) & 1, p.err));
+        if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&tail->q_full, S::kQBytes);
         __syncwarp();
-        const int row = walk.q.q_begin * p.Hq + pc.tile * NR;
+        const int q_row = walk.q.q_begin * p.Hq + pc.tile * NR;
         if (lane < S::kChunks)
-          tc::tma_load_2d(smem + lane * NR * 128, &tmap_q, lane * 64, row, &tail->q_full);
+          tc::tma_load_2d(smem + lane * NR * 128, &tmap_q, lane * 64, q_row, &tail->q_full);
         ++pieces;
         const int32_t* table = p.block_tables + (int64_t)pc.r * p.max_blocks;
-        auto fetch = [&](int j) -> int {  // block `lane` of key tile j
-          const int lb = j * bpt + lane;
-          return (j < pc.k1 && lane < bpt && (int64_t)lb * p.B < pc.n_keys) ? __ldg(table + lb) : 0;
+        auto loads = [&](int j) {  // the lane has a box in key tile j
+          return j < pc.k1 && b < bpt && j * KT + b * rows < pc.n_keys;
         };
-        int ids = fetch(pc.k0);
+        auto fetch = [&](int j) -> int {  // its physical block
+          return loads(j) ? __ldg(table + (j * KT + b * rows) / p.B) : 0;
+        };
+        int id = fetch(pc.k0);
         for (int j = pc.k0; j < pc.k1; ++j, ++g) {
           const int next = fetch(j + 1);
-          const int st = g % kStages;
-          int nload = 0;
-          while (nload < bpt && (j * bpt + nload) * p.B < pc.n_keys) ++nload;
-          const bool bad = lane < nload && (ids < 0 || ids >= p.num_blocks);
+          const bool mine = loads(j);
+          const bool bad = mine && (id < 0 || id >= p.num_blocks);
           if (__any_sync(full, bad) && lane == 0) raise_error(p.err, kErrBounds);
-          const int blk_lane = bad ? 0 : ids;  // a valid block; the output is then unspecified
-          if (lane == 0 && g >= kStages)
-            ok = mbar_wait(&tail->k_empty[st], (g / kStages - 1) & 1, p.err);
-          if (!__shfl_sync(full, ok ? 1 : 0, 0) || aborted(tail)) {
-            ok = false;
-            break;
-          }
-          uint8_t* stage = smem + S::kOffK + st * S::kStage;
+          const int blk = bad ? 0 : id;  // a valid block; the output is then unspecified
+          const int boxes = __popc(__ballot_sync(full, mine));
+          ok = (g < kStages || __all_sync(full, mbar_wait(&tail->k_empty[st], phase, p.err))) &&
+               !__any_sync(full, aborted(tail));
+          if (!ok) break;
           if (lane == 0)
-            mbar_arrive_expect_tx(&tail->k_full[st], (uint32_t)(nload * p.B * 128 * S::kChunks));
+            mbar_arrive_expect_tx(&tail->k_full[st], (uint32_t)(boxes * rows * 128));
           __syncwarp();
-          for (int i0 = 0; i0 < nload * S::kChunks; i0 += 32) {
-            const int i = i0 + lane;
-            const int b = i / S::kChunks, c = i - b * S::kChunks;
-            const int y = __shfl_sync(full, blk_lane, b & 3) * p.B;
-            if (b < nload) {
-              uint8_t* dst = stage + c * kChunk + b * p.B * 128;
-              if (c < L / 64)
-                tc::tma_load_2d(dst, &tmap_c, c * 64, y, &tail->k_full[st]);
-              else
-                tc::tma_load_2d(dst, &tmap_r, 0, y, &tail->k_full[st]);
-            }
+          if (mine) {
+            uint8_t* dst = smem + S::kOffK + st * S::kStage + c * kChunk + b * rows * 128;
+            const int y = blk * p.B + (j * KT + b * rows) % p.B;
+            if (c < L / 64)
+              tc::tma_load_2d(dst, &tmap_c, c * 64, y, &tail->k_full[st]);
+            else
+              tc::tma_load_2d(dst, &tmap_r, 0, y, &tail->k_full[st]);
           }
-          ids = next;
+          if (++st == kStages) {
+            st = 0;
+            phase ^= 1;
+          }
+          id = next;
         }
       }
       // every issued copy lands before the CTA may leave
@@ -405,63 +406,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMA issuer
-      if (lane == 0) {
+      if (tc::elect_one()) {
         constexpr uint32_t idesc_s = tc::idesc_16bit_f32(64, KT, false, false, false);
         constexpr uint32_t idesc_o = tc::idesc_16bit_f32(128, NR, true, false, false);
-        const uint8_t* ps = smem + S::kOffP;
-        Walk<NR> walk(tail, begin, end);
-        Piece pc;
-        int g = 0, pieces = 0;
-        bool ok = true;
-        auto issue_s = [&](int i, bool last) -> bool {  // S of the CTA's key tile i
-          const int st = i % kStages;
-          if (!mbar_wait(&tail->k_full[st], (i / kStages) & 1, p.err) || aborted(tail))
-            return false;
-          tc::fence_after_sync();
-          const uint8_t* ks = smem + S::kOffK + st * S::kStage;
-#pragma unroll
-          for (int k = 0; k < S::kChunks * 4; ++k) {
-            const uint64_t a =
-                tc::smem_desc_sw128(smem + (k >> 2) * NR * 128 + (k & 3) * 32, 16, 1024);
-            const uint64_t b = tc::smem_desc_sw128(ks + (k >> 2) * kChunk + (k & 3) * 32, 16, 1024);
-            tc::mma_bf16_ss(tmem + kTmemS + (i & 1) * KT, a, b, idesc_s, k > 0);
-          }
-          tc::mma_commit(&tail->s_full[i & 1]);
-          if (last) tc::mma_commit(&tail->q_empty);
-          return true;
+        const uint64_t q_desc = tc::smem_desc_sw128(smem, 16, 1024);
+        const uint64_t p_desc = tc::smem_desc_sw128(smem + S::kOffP, 16, 1024);
+        const uint64_t k_desc = tc::smem_desc_sw128(smem + S::kOffK, 16, 1024);
+        const uint64_t v_desc = tc::smem_desc_sw128(smem + S::kOffK, kChunk, 1024);
+        // Two walks over the same pieces: tile `s` is the next to be scored, `v`
+        // the next whose P is taken; s runs ahead by at most three tiles.
+        Walk<NR> s_walk(tail, begin, end), v_walk(tail, begin, end);
+        Piece sp, vp;
+        auto advance = [&](Walk<NR>& w, Piece& x) {  // to the next piece with keys
+          while (w.next(p, x))
+            if (x.k0 < x.k1) return true;
+          return false;
         };
-        while (ok && walk.next(p, pc)) {
-          if (pc.k0 >= pc.k1) continue;
-          const int n = pc.k1 - pc.k0;
-          ok = mbar_wait(&tail->q_full, pieces & 1, p.err);
-          ok = ok && issue_s(g, n == 1);
-          for (int j = 0; ok && j < n; ++j, ++g) {
-            if (j + 1 < n && !issue_s(g + 1, j + 2 == n)) ok = false;
-            if (!ok || !mbar_wait(&tail->p_full, g & 1, p.err) || aborted(tail)) {
-              ok = false;
-              break;
+        bool s_more = advance(s_walk, sp), v_more = advance(v_walk, vp);
+        int s = 0, s_st = 0, s_phase = 0, s_piece = 0, sj = sp.k0;
+        int v = 0, v_st = 0, v_piece = 0, vj = vp.k0;
+        int fixes = 0;
+        bool ok = true;
+        int idle = 0;
+        unsigned long long t0 = 0;
+        while (ok && v_more) {
+          if (s_more && s - v < kSBufs - 1 && mbar_test_wait(&tail->k_full[s_st], s_phase) &&
+              (sj > sp.k0 || mbar_test_wait(&tail->q_full, s_piece & 1))) {
+            tc::fence_after_sync();
+            const uint64_t ks = tc::desc_at(k_desc, s_st * S::kStage);
+            const uint32_t d = tmem + kTmemS + (s % kSBufs) * KT;
+#pragma unroll
+            for (int k = 0; k < S::kChunks * 4; ++k)
+              tc::mma_bf16_ss(d, tc::desc_at(q_desc, (k >> 2) * NR * 128 + (k & 3) * 32),
+                              tc::desc_at(ks, (k >> 2) * kChunk + (k & 3) * 32), idesc_s, k > 0);
+            tc::mma_commit(&tail->s_full[s % kSBufs]);
+            ++s;
+            if (++s_st == kStages) {
+              s_st = 0;
+              s_phase ^= 1;
             }
-            // the first product of a piece overwrites O: the last piece is out
-            if (j == 0 && pieces > 0 && !mbar_wait(&tail->o_empty, (pieces - 1) & 1, p.err)) {
-              ok = false;
-              break;
+            if (++sj == sp.k1) {
+              tc::mma_commit(&tail->q_empty);
+              ++s_piece;
+              s_more = advance(s_walk, sp);
+              sj = sp.k0;
+            }
+            idle = 0;
+          }
+          // (the first product of a piece overwrites O: the last piece is out)
+          if (v < s && mbar_test_wait(&tail->p_full[v & 1], (v >> 1) & 1) &&
+              (vj > vp.k0 || v_piece == 0 ||
+               mbar_test_wait(&tail->o_empty, (v_piece - 1) & 1))) {
+            if (*reinterpret_cast<volatile uint32_t*>(&tail->ask[v & 1][0]) != 0) {
+              // rows of this tile have a new reference: O, complete up to the
+              // tile before, is rescaled first
+              *reinterpret_cast<volatile int32_t*>(&tail->fix_tile) = v;
+              ok = mbar_wait(&tail->pv_done[(v - 1) & 1], ((v - 1) >> 1) & 1, p.err);
+              mbar_arrive(&tail->fix);
+              ok = ok && mbar_wait(&tail->fixed, fixes & 1, p.err);
+              if (!ok) break;
+              ++fixes;
             }
             tc::fence_after_sync();
-            const int st = g % kStages;
-            const uint8_t* ks = smem + S::kOffK + st * S::kStage;
+            const uint64_t vs = tc::desc_at(v_desc, v_st * S::kStage);
+            const uint64_t ps = tc::desc_at(p_desc, (v & 1) * 64);
+            const bool first = vj == vp.k0;
 #pragma unroll
             for (int m = 0; m < kBlocks; ++m)
 #pragma unroll
-              for (int k = 0; k < KT / 16; ++k) {
-                const uint64_t a =
-                    tc::smem_desc_sw128(ks + 2 * m * kChunk + k * 16 * 128, kChunk, 1024);
-                const uint64_t b = tc::smem_desc_sw128(ps + k * 32, 16, 1024);
-                tc::mma_bf16_ss(tmem + m * NR, a, b, idesc_o, j > 0 || k > 0);
-              }
-            tc::mma_commit(&tail->k_empty[st]);
-            tc::mma_commit(&tail->pv_done);
+              for (int k = 0; k < KT / 16; ++k)
+                tc::mma_bf16_ss(tmem + m * NR, tc::desc_at(vs, 2 * m * kChunk + k * 16 * 128),
+                                tc::desc_at(ps, k * 32), idesc_o, !first || k > 0);
+            tc::mma_commit(&tail->k_empty[v_st]);
+            tc::mma_commit(&tail->pv_done[v & 1]);
+            ++v;
+            if (++v_st == kStages) v_st = 0;
+            if (++vj == vp.k1) {
+              ++v_piece;
+              v_more = advance(v_walk, vp);
+              vj = vp.k0;
+            }
+            idle = 0;
           }
-          ++pieces;
+          // nothing came for long: give up after the usual limit
+          if (++idle == 4096) t0 = global_timer_ns();
+          if (idle > 4096 && (idle & 1023) == 0) {
+            if (aborted(tail)) ok = false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+              raise_error(p.err, kErrTimeout);
+              ok = false;
+            }
+          }
         }
         if (!ok) tail->abort = 1;
         tc::mma_commit(&tail->final_mma);
@@ -476,12 +511,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
       uint8_t* ps = smem + S::kOffP;
       const int tid = threadIdx.x - 128;
+      int fixes = 0;
+      // this warp's dims of O times the new factors of the rows that ask
+      auto rescale = [&]() {
+        tc::fence_after_sync();
+        const int slot = *reinterpret_cast<volatile int32_t*>(&tail->fix_tile) & 1;
+        const uint32_t asked = *reinterpret_cast<volatile uint32_t*>(&tail->ask[slot][0]);
+#pragma unroll 1
+        for (int c = 0; c < kBlocks * NR; c += 16) {
+          const int r = c % NR;  // the rows of softmax warp r / 16
+          if (((asked >> (r / 2)) & 0xFF) == 0) continue;
+          uint32_t o[16];
+          tmem_ld16(tmem + lanes + c, o);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * tail->alpha[slot][r + i]);
+          tmem_st16(tmem + lanes + c, o);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->fixed);
+        ++fixes;
+      };
+      // Waits for a barrier, doing the rescales that are asked for meanwhile.
+      auto wait = [&](uint64_t* bar, int parity) -> bool {
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
+        unsigned long long t0 = 0;
+        for (int spin = 1;; ++spin) {
+          if (__all_sync(0xffffffffu, mbar_test_wait(&tail->fix, fixes & 1))) rescale();
+          if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
+          if ((spin & 1023) == 0) {
+            const unsigned long long now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+              if (lane == 0) raise_error(p.err, kErrTimeout);
+              return false;
+            }
+          }
+        }
+      };
       Walk<NR> walk(tail, begin, end);
       Piece pc;
-      int g = 0;
-      bool bad = false, stop = false;
-      while (!stop && walk.next(p, pc)) {
-        const bool none = pc.k0 >= pc.k1;
+      int g = 0, pieces = 0;
+      bool ok = true;
+      while (ok && walk.next(p, pc)) {
         const int row0 = pc.tile * NR;
         int lim_a = 0, lim_b = 0;  // keys the rows see
         if (scores) {
@@ -491,32 +566,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
         for (int j = pc.k0; j < pc.k1; ++j, ++g) {
-          bad = bad ||
-                !__all_sync(0xffffffffu, mbar_wait(&tail->s_full[g & 1], (g >> 1) & 1, p.err)) ||
-                aborted(tail);
-          if (bad && lane == 0) tail->fail[g & 1] = 1;
-          tc::fence_after_sync();
-          uint32_t sr[32];
+          uint32_t sr[16];
           float* s = reinterpret_cast<float*>(sr);
           float aa = 1.f, ab = 1.f;
-          bool rescale = false;
           const int key0 = j * KT;
-          if (scores && !bad) {
-            tmem_ld_16x64(tmem + kTmemS + (g & 1) * KT + lanes, sr);
+          if (scores) {
+            if (!(ok = wait(&tail->s_full[g % kSBufs], g / kSBufs))) break;
+            tc::fence_after_sync();
+            tmem_ld_16x32(tmem + kTmemS + (g % kSBufs) * KT + lanes, sr);
             tc::tmem_wait_ld();
             if (key0 + KT > min(lim_a, lim_b)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
+              for (int i = 0; i < 16; ++i) {
                 const int key = key0 + (i >> 2) * 8 + 2 * (lane & 3) + (i & 1);
                 if (key >= ((i & 2) ? lim_b : lim_a)) s[i] = -INFINITY;
               }
             }
-            float ta = -INFINITY, tb = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              ta = fmax3(ta, s[i], s[i + 1]);
-              tb = fmax3(tb, s[i + 2], s[i + 3]);
-            }
+            float ta = fmax3(fmaxf(s[0], s[1]), s[4], s[5]);
+            float tb = fmax3(fmaxf(s[2], s[3]), s[6], s[7]);
+            ta = fmax3(ta, fmaxf(s[8], s[9]), fmaxf(s[12], s[13]));
+            tb = fmax3(tb, fmaxf(s[10], s[11]), fmaxf(s[14], s[15]));
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
               ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
@@ -531,19 +600,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if (ta > ma + kRescaleLog2) {
               aa = ex2_ftz(ma - ta);
               ma = ta;
-              rescale = true;
             }
             if (mb == -INFINITY) {
               mb = tb;
             } else if (tb > mb + kRescaleLog2) {
               ab = ex2_ftz(mb - tb);
               mb = tb;
-              rescale = true;
             }
             const float na = ma == -INFINITY ? 0.f : -ma, nb = mb == -INFINITY ? 0.f : -mb;
             float sa = 0.f, sb = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < 16; i += 4) {
               s[i] = ex2_ftz(fmaf(s[i], p.scale_log2, na));
               s[i + 1] = ex2_ftz(fmaf(s[i + 1], p.scale_log2, na));
               s[i + 2] = ex2_ftz(fmaf(s[i + 2], p.scale_log2, nb));
@@ -553,123 +620,143 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             la = la * aa + sa;
             lb = lb * ab + sb;
-            if ((lane & 3) == 0) {
-              tail->alpha[g & 1][ra] = aa;
-              tail->alpha[g & 1][rb] = ab;
-            }
           }
-          // O is rescaled by all four warps (a warp holds 32 latent dims of
-          // every row) when any row asks for it
-          const bool any = named_bar_or(1, 128, rescale);
-          if (agreed_to_stop(tail, g & 1)) {
-            stop = true;
-            break;
-          }
-          if (g > 0 && (any || scores)) {
-            // P is free, and O complete, once PV(g - 1) is done
-            if (!__all_sync(0xffffffffu, mbar_wait(&tail->pv_done, (g - 1) & 1, p.err))) {
-              bad = true;
-              continue;
-            }
-          }
-          if (any) {
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int c = 0; c < kBlocks * NR; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(tmem + lanes + c, o);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * tail->alpha[g & 1][c % NR + i]);
-              tmem_st16(tmem + lanes + c, o);
-            }
-            tc::tmem_wait_st();
-          }
+          // PV(g - 2) has read this half of P, and what was published with it
+          if (g >= 2 && !(ok = wait(&tail->pv_done[g & 1], (g >> 1) - 1))) break;
           if (scores) {
             const int mi = lane >> 3;  // the 8x8 matrix whose row this lane addresses
             const int row = w4 * 16 + (mi & 1) * 8 + (lane & 7);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int gran = 2 * i + (mi >> 1);
+            for (int i = 0; i < 2; ++i) {
+              const int gran = (g & 1) * 4 + 2 * i + (mi >> 1);
               stmatrix_x4(ps + row * 128 + ((gran ^ (row & 7)) << 4),
                           pack_bf16(s[8 * i], s[8 * i + 1]), pack_bf16(s[8 * i + 2], s[8 * i + 3]),
                           pack_bf16(s[8 * i + 4], s[8 * i + 5]),
                           pack_bf16(s[8 * i + 6], s[8 * i + 7]));
             }
           }
+          const bool ask = __any_sync(0xffffffffu, aa < 1.f || ab < 1.f);
+          if (ask && (lane & 3) == 0) {
+            tail->alpha[g & 1][ra] = aa;
+            tail->alpha[g & 1][rb] = ab;
+          }
+          if (lane == 0) tail->ask[g & 1][w4] = ask;
           if (key0 + KT > pc.n_keys) {
             // the tile holds keys past the last visible one (unloaded blocks,
-            // unwritten cells): zero them, so that P = 0 never meets a NaN
-            uint8_t* ks = smem + S::kOffK + (g % kStages) * S::kStage;
-            for (int i = tid; i < (L / 64) * KT * 8; i += 128) {
-              const int c = i / (KT * 8), n = (i / 8) % KT;
-              if (key0 + n >= pc.n_keys)
-                *reinterpret_cast<uint4*>(ks + c * kChunk + n * 128 + (i & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
+            // unwritten cells): zero them, so that P = 0 never meets a NaN (S of
+            // this tile has read them: every warp waits for it)
+            if (!scores && !(ok = wait(&tail->s_full[g % kSBufs], g / kSBufs))) break;
+            constexpr int kCols = L / 64;  // chunks: the thread's is (tid / 8) % kCols
+            uint8_t* ks = smem + S::kOffK + (g % kStages) * S::kStage +
+                          ((tid >> 3) & (kCols - 1)) * kChunk + (tid & 7) * 16;
+            for (int n = pc.n_keys - key0 + tid / (8 * kCols); n < KT; n += 16 / kCols)
+              *reinterpret_cast<uint4*>(ks + n * 128) = make_uint4(0, 0, 0, 0);
+          }
+          if (j == pc.k1 - 1 && scores) {
+            // the piece's sums, before the arrival that its output waits behind
+            float ua = la, ub = lb;
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+              ua += __shfl_xor_sync(0xffffffffu, ua, o);
+              ub += __shfl_xor_sync(0xffffffffu, ub, o);
+            }
+            if ((lane & 3) == 0) {
+              tail->l[pieces & 1][ra] = ua > 0.f ? 1.f / ua : 0.f;
+              tail->l[pieces & 1][rb] = ub > 0.f ? 1.f / ub : 0.f;
+              if (pc.slot >= 0) {
+                float2* ml = p.part_ml + (int64_t)(2 * cta + pc.slot) * NR;
+                ml[ra] = make_float2(ma, ua);
+                ml[rb] = make_float2(mb, ub);
+              }
             }
           }
           tc::fence_proxy_async_smem();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tail->p_full);
+          if (lane == 0) mbar_arrive(&tail->p_full[g & 1]);
         }
-        if (stop) break;
+        if (!ok) break;
 
+        if (pc.k0 >= pc.k1) {  // no key for any row: sums of zero, which the join skips
+          if (scores && pc.slot >= 0 && (lane & 3) == 0) {
+            float2* ml = p.part_ml + (int64_t)(2 * cta + pc.slot) * NR;
+            ml[ra] = ml[rb] = make_float2(-INFINITY, 0.f);
+          }
+          continue;
+        }
         // ---- the piece's rows: normalised to out, or a partial
-        if (scores) {
-#pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            la += __shfl_xor_sync(0xffffffffu, la, o);
-            lb += __shfl_xor_sync(0xffffffffu, lb, o);
-          }
-          if ((lane & 3) == 0) {
-            if (pc.slot < 0) {
-              tail->l[ra] = la > 0.f ? 1.f / la : 0.f;
-              tail->l[rb] = lb > 0.f ? 1.f / lb : 0.f;
-            } else {
-              float2* ml = p.part_ml + (int64_t)(2 * cta + pc.slot) * NR;
-              ml[ra] = make_float2(ma, la);
-              ml[rb] = make_float2(mb, lb);
-            }
-          }
-        }
-        if (none) continue;  // sums of zero: the join skips it
-        bad = bad ||
-              !__all_sync(0xffffffffu, mbar_wait(&tail->pv_done, (g - 1) & 1, p.err)) ||
-              aborted(tail);
-        if (bad && lane == 0) tail->fail[2] = 1;
-        named_bar_sync(1, 128);
-        if (agreed_to_stop(tail, 2)) {
-          stop = true;
-          break;
-        }
+        if (!(ok = wait(&tail->pv_done[(g - 1) & 1], (g - 1) >> 1))) break;
         tc::fence_after_sync();
         const int64_t out_row = (int64_t)walk.q.q_begin * p.Hq + row0;
-        __nv_bfloat16* orow = p.out + out_row * L + w4 * 32 + lane;
-        float* prow = p.part_o + (int64_t)(2 * cta + max(pc.slot, 0)) * NR * L + w4 * 32 + lane;
-#pragma unroll 1
-        for (int m = 0; m < kBlocks; ++m)
+        if (pc.slot < 0) {
+          // lane = dim, register = row: three exchanges between lanes whose
+          // numbers differ in one bit leave 8 dims of two rows in each lane
+          __nv_bfloat16* orow = p.out + out_row * L + w4 * 32 + (lane >> 3) * 8;
 #pragma unroll 1
           for (int c = 0; c < NR; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(tmem + lanes + m * NR + c, o);
-            tc::tmem_wait_ld();
+            if (c >= pc.rows) break;
+            float inv[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (c + i >= pc.rows) break;
-              const float v = __uint_as_float(o[i]);
-              if (pc.slot < 0)
-                orow[(int64_t)(c + i) * L + m * 128] = __float2bfloat16_rn(v * tail->l[c + i]);
-              else
-                prow[(c + i) * L + m * 128] = v;
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(inv + i) =
+                  *reinterpret_cast<const float4*>(&tail->l[pieces & 1][c + i]);
+            // row of the lane's first output: bit 0, 1, 2 of the lane pick bits
+            // 3, 2, 1 of the row
+            const int row = c + (lane & 1) * 8 + (lane & 2) * 2 + ((lane & 4) >> 1);
+#pragma unroll 1
+            for (int m = 0; m < kBlocks; ++m) {
+              uint32_t o[16];
+              tmem_ld16(tmem + lanes + m * NR + c, o);
+              tc::tmem_wait_ld();
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {  // lane pairs: bf16 of two dims, 8 rows each
+                const float x = __uint_as_float(o[i]) * inv[i];
+                const float y = __uint_as_float(o[i + 8]) * inv[i + 8];
+                const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
+                w[i] = (lane & 1) ? pack_bf16(got, y) : pack_bf16(x, got);
+              }
+              uint32_t u[4][2];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {  // four dims, 4 rows each
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & 2) ? w[i] : w[i + 4], 2);
+                u[i][0] = (lane & 2) ? got : w[i];
+                u[i][1] = (lane & 2) ? w[i + 4] : got;
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {  // eight dims, 2 rows each
+                const bool up = (lane & 4) != 0;
+                const uint32_t g0 = __shfl_xor_sync(0xffffffffu, up ? u[i][0] : u[i + 2][0], 4);
+                const uint32_t g1 = __shfl_xor_sync(0xffffffffu, up ? u[i][1] : u[i + 2][1], 4);
+                if (row + i < pc.rows)
+                  *reinterpret_cast<uint4*>(orow + (int64_t)(row + i) * L + m * 128) =
+                      up ? make_uint4(g0, g1, u[i + 2][0], u[i + 2][1])
+                         : make_uint4(u[i][0], u[i][1], g0, g1);
+              }
             }
           }
+        } else {
+          float* prow = p.part_o + (int64_t)(2 * cta + pc.slot) * NR * L + w4 * 32 + lane;
+#pragma unroll 1
+          for (int c = 0; c < NR; c += 16) {
+            if (c >= pc.rows) break;
+#pragma unroll 1
+            for (int m = 0; m < kBlocks; ++m) {
+              uint32_t o[16];
+              tmem_ld16(tmem + lanes + m * NR + c, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)  // (rows past the unit's are scratch)
+                prow[(c + i) * L + m * 128] = __uint_as_float(o[i]);
+            }
+          }
+        }
+        ++pieces;
         tc::fence_before_sync();
-        named_bar_sync(1, 128);  // tail->l is free again
+        __syncwarp();
         if (lane == 0) mbar_arrive(&tail->o_empty);
       }
-      if (stop) tail->abort = 1;
+      if (!ok) tail->abort = 1;
     }
   }
   tc::fence_before_sync();
@@ -772,10 +859,11 @@ pa_status launch(const LatentParams& p, const void* q, const pa_latent_pool* poo
   using S = Smem<L, NR>;
   CUtensorMap tq, tc, tr;
   const int64_t cells = (int64_t)pool->num_blocks * pool->block_size;
+  const int box_rows = std::min(p.B, KT);
   if (!encode_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, L + kRope, (int64_t)p.T * p.Hq, 64,
                  NR) ||
-      !encode_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->latent, L, cells, 64, p.B) ||
-      !encode_2d(&tr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->rope, kRope, cells, 64, p.B))
+      !encode_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->latent, L, cells, 64, box_rows) ||
+      !encode_2d(&tr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->rope, kRope, cells, 64, box_rows))
     return PA_ERR_CUDA;
   if (cudaFuncSetAttribute(latent_attn_kernel<L, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            S::kAlloc) != cudaSuccess)
@@ -848,6 +936,7 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
     if (rows > 0)
       W += (rows + NR - 1) / NR * ((seq_lens_host[r] + pa::kLatentKeys - 1) / pa::kLatentKeys);
   }
+  if (W > INT32_MAX) return PA_ERR_UNSUPPORTED;
   const int grid = (int)std::min<int64_t>(W, std::min(pa::num_sms(), pa::kLatentMaxCtas));
   if (workspace_bytes < pa::scratch_bytes(grid, NR, L)) return PA_ERR_INVALID;
 

@@ -8,12 +8,12 @@
 
 namespace pa {
 
-constexpr int kLatentKeys = 64;     // keys per tile
+constexpr int kLatentKeys = 32;     // keys per tile
 constexpr int kLatentRows = 64;     // most query rows (token, head) per row tile
 constexpr int kLatentMaxCtas = 1024;
 
-// The work of one call is laid out as one sequence of 64-key tiles, the "flat
-// space": unit (request r, row tile i) holds the C_r = ceil(seq_len / 64) key
+// The work of one call is laid out as one sequence of 32-key tiles, the "flat
+// space": unit (request r, row tile i) holds the C_r = ceil(seq_len / 32) key
 // tiles that the NR query rows i NR .. of the request are scored against, at
 // pref[r] + i C_r, pref the exclusive running sum of tiles_r C_r. CTA b of the
 // grid takes the tiles [b Q, b Q + Q), Q = ceil(W / grid): equal shares

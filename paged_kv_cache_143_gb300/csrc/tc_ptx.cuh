@@ -154,6 +154,23 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(const void* smem, uint32_t l
   return d;
 }
 
+// The same descriptor `bytes` further on (a multiple of 16): the address field
+// is its low bits, and shared memory ends long before they carry over.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+  return desc + (bytes >> 4);
+}
+
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      :
+      : "memory");
+  return r != 0;
+}
+
 // Instruction descriptor for kind::f16 with A and B both bf16 (or both f16),
 // fp32 accumulate.
 __host__ __device__ constexpr uint32_t idesc_16bit_f32(int M, int N, bool a_mn_major,
