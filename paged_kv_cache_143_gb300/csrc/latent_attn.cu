@@ -22,14 +22,14 @@
 // Tiles are 32 keys (36 KB at L 512) so that four of them fit beside 64 rows of
 // Q: a stage is loading for about 2000 cycles and in use (S, softmax, PV and
 // their hand-overs) for 2700, and what HBM delivers a tile in is 1570.
-//   warp 0      TMA producer: the Q tile, then the key tiles into a ring of stages,
-//               whole rows at once, one box per physical block and 64 columns
-//   warp 1      TMEM and, one elected lane, the MMAs: whichever is ready of the
-//               next S (up to three tiles ahead) and the next PV
+//   warp 0      TMA producer: the Q tile, then the key tiles into a ring of stages
+//   warp 1      TMEM and, one elected lane, S, up to four tiles ahead
+//   warp 2      one elected lane, PV. (One lane for both spent a third of a tile's
+//               time between the two batches of products.)
 //   warps 4-7   softmax of 16 rows each (S read as 16 x 256-bit fragments: a row
 //               in four lanes), P written by stmatrix; then the output
 // The softmax warps share nothing tile by tile. A warp that moves a row's
-// reference maximum says so beside P; the MMA warp then asks all four to rescale
+// reference maximum says so beside P; warp 2 then asks all four to rescale
 // their dims of O before it issues that PV (rare: growth by more than 2^8).
 // Every wait is bounded; a timeout sets the error word and the CTA unwinds.
 #include <cudaTypedefs.h>
@@ -78,7 +78,7 @@ struct Smem {
 struct Tail {
   uint64_t q_full, q_empty;
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
-  uint64_t s_full[kSBufs];
+  uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t p_full[2], pv_done[2];
   uint64_t fix, fixed;           // O is to be rescaled for tile fix_tile; it has been
   uint64_t o_empty, final_mma;
@@ -148,7 +148,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 struct Request {
   int32_t q_begin, q_len, seq, rows, keys;  // query rows, key tiles
-  int64_t weight;                           // row tiles * keys; 0 for one without work
+  int64_t weight;                           // passes * keys; 0 for one without work
 };
 
 // Reads request r; one whose device entries do not fit the buffers has no
@@ -167,27 +167,28 @@ __device__ __forceinline__ Request load_request(const LatentParams& p, int r, bo
   }
   q.rows = q.q_len * p.Hq;  // (T * Hq fits 32 bits)
   q.keys = (q.seq + KT - 1) / KT;
-  q.weight = (int64_t)((q.rows + NR - 1) / NR) * q.keys;
+  const int tiles = (q.rows + NR - 1) / NR;
+  q.weight = (int64_t)((tiles + p.lanes - 1) / p.lanes) * q.keys;
   return q;
 }
 
-// A CTA's part of one unit: key tiles [k0, k1) of row tile `tile` of request r.
+// A CTA's part of one pass: key tiles [k0, k1) for row tile `tile` of request r.
 struct Piece {
   int32_t r, tile, k0, k1;
   int32_t n_keys;      // keys any row of the tile sees (k1 is cut to it)
-  int32_t rows;        // valid query rows of the tile
-  int32_t slot;        // partial slot 0 / 1 of the CTA, or -1: the whole unit
+  int32_t rows;        // valid query rows of the tile (none: the pass has fewer tiles)
+  int32_t slot;        // partial slot 0 / 1 of the CTA, or -1: the whole pass
 };
 
 // (The whole flat space fits 31 bits, so do all positions.)
 template <int NR>
 struct Walk {
-  int32_t pos, end, base, r;
+  int32_t pos, end, base, r, lane;
   bool loaded;
   Request q;
 
-  __device__ Walk(const Tail* t, int32_t begin, int32_t stop)
-      : pos(begin), end(stop), base(t->base), r(t->req), loaded(false), q{} {}
+  __device__ Walk(const Tail* t, int32_t begin, int32_t stop, int32_t in_group)
+      : pos(begin), end(stop), base(t->base), r(t->req), lane(in_group), loaded(false), q{} {}
 
   __device__ bool next(const LatentParams& p, Piece& out) {
     if (pos >= end) return false;
@@ -202,12 +203,18 @@ struct Walk {
     }
     const unsigned off = pos - base;
     out.r = r;
-    out.tile = (int)(off / (unsigned)q.keys);
-    out.k0 = (int)off - out.tile * q.keys;
+    const int pass = (int)(off / (unsigned)q.keys);
+    out.tile = pass * p.lanes + lane;
+    out.k0 = (int)off - pass * q.keys;
     const int k1 = min(q.keys, out.k0 + (end - pos));
     pos += k1 - out.k0;
     out.slot = out.k0 > 0 ? 0 : k1 < q.keys ? 1 : -1;
     out.rows = min(NR, q.rows - out.tile * NR);
+    if (out.rows <= 0) {
+      out.rows = 0;
+      out.k1 = out.k0;
+      return true;
+    }
     out.n_keys = q.seq;
     if (p.causal && q.q_len > 1) {  // up to the last row's token
       const unsigned last_row = out.tile * NR + out.rows - 1;
@@ -231,10 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Tail* tail = reinterpret_cast<Tail*>(smem + S::kOffTail);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = blockIdx.x;
+  const int cta = blockIdx.x, group = cta / p.lanes, in_group = cta - group * p.lanes;
+  const int groups = gridDim.x / p.lanes;
   launch_dependents();  // the join that follows may be scheduled now
 
-  // ---- this CTA's range: W, then the request that holds tile cta * Q
+  // ---- this group's range: W, then the request that holds tile group * Q
   if (warp == 1) {
     tc::tmem_alloc(&tail->tmem, kTmemCols);
     tc::tmem_relinquish();
@@ -246,7 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tail->k_full[s], 1);
       mbar_init(&tail->k_empty[s], 1);
     }
-    for (int s = 0; s < kSBufs; ++s) mbar_init(&tail->s_full[s], 1);
+    for (int s = 0; s < kSBufs; ++s) {
+      mbar_init(&tail->s_full[s], 1);
+      mbar_init(&tail->s_empty[s], NR / 16);  // the warps that read S
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tail->p_full[s], 4);   // one arrival per softmax warp
       mbar_init(&tail->pv_done[s], 1);
@@ -254,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&tail->fix, 1);
     mbar_init(&tail->fixed, 4);
     mbar_init(&tail->o_empty, 4);
-    mbar_init(&tail->final_mma, 1);
+    mbar_init(&tail->final_mma, 2);
     tail->abort = 0;
     tail->req = p.R;
     tail->base = 0;
@@ -293,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (cta == 0 && threadIdx.x == 0) raise_error(p.err, kErrBounds);
     W = 0;
   }
-  const unsigned Q = ((unsigned)W + gridDim.x - 1) / gridDim.x;
-  const int begin = (int)min((int64_t)W, (int64_t)cta * Q), end = (int)min(W, (int64_t)begin + Q);
+  const unsigned Q = ((unsigned)W + groups - 1) / groups;
+  const int begin = (int)min(W, (int64_t)group * Q), end = (int)min(W, (int64_t)begin + Q);
   if (p.R > kThreads) {  // the sums of all but the last step are taken again
     int64_t sum = 0;
     for (int r0 = 0; r0 < p.R; r0 += kThreads) {
@@ -316,17 +327,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tail->tmem;
-  if (threadIdx.x == 64) {
-    // the unit cut at this CTA's start, for the join: handled at its first cut
+  if (threadIdx.x == 96) {
+    // the pass cut at this group's start, for the join: handled at its first cut
     LatentJoin j{};
     if (begin < end) {
       const Request q = load_request<NR>(p, tail->req, false);
-      const int tile = (begin - tail->base) / q.keys;
-      const unsigned a = tail->base + tile * q.keys;  // the unit's start
-      if ((unsigned)begin > a && a / Q + 1 == (unsigned)cta) {
-        j.rows = min(q.rows - tile * NR, NR);
-        j.last = (int32_t)((a + q.keys - 1) / Q);
-        j.out_row = (int64_t)q.q_begin * p.Hq + tile * NR;
+      const int pass = (begin - tail->base) / q.keys;
+      const unsigned a = tail->base + pass * q.keys;  // the pass's start
+      const int row0 = (pass * p.lanes + in_group) * NR;
+      if ((unsigned)begin > a && a / Q + 1 == (unsigned)group && row0 < q.rows) {
+        j.rows = min(q.rows - row0, NR);
+        j.pieces = (int32_t)((a + q.keys - 1) / Q - a / Q) + 1;
+        j.out_row = (int64_t)q.q_begin * p.Hq + row0;
       }
     }
     p.joins[cta] = j;
@@ -335,69 +347,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (begin < end) {
     if (warp == 0) {
       // --------------------------------------------------------- TMA producer
-      const unsigned full = 0xffffffffu;
-      if (lane == 0) {
+      // (one lane: a copy instruction with several lanes active costs about
+      // 120 cycles a lane, and the ring then waits for its producer)
+      if (tc::elect_one()) {
         tc::prefetch_tensormap(&tmap_q);
         tc::prefetch_tensormap(&tmap_c);
         tc::prefetch_tensormap(&tmap_r);
-      }
-      const int rows = min(p.B, KT);             // rows of one box
-      const int bpt = KT / rows;                 // boxes down a tile: 2 or 1
-      const int b = lane / S::kChunks, c = lane - b * S::kChunks;  // the lane's box
-      Walk<NR> walk(tail, begin, end);
-      Piece pc;
-      int g = 0, pieces = 0;                     // key tiles and pieces so far
-      int st = 0, phase = 1;                     // stage, and the parity its emptying waits for
-      bool ok = true;
-      while (ok && walk.next(p, pc)) {
-        if (pc.k0 >= pc.k1) continue;  // no row of the tile sees these keys
-        ok = pieces == 0 ||
-             __all_sync(full, mbar_wait(&tail->q_empty, (pieces - 1) & 1, p.err));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&tail->q_full, S::kQBytes);
-        __syncwarp();
-        const int q_row = walk.q.q_begin * p.Hq + pc.tile * NR;
-        if (lane < S::kChunks)
-          tc::tma_load_2d(smem + lane * NR * 128, &tmap_q, lane * 64, q_row, &tail->q_full);
-        ++pieces;
-        const int32_t* table = p.block_tables + (int64_t)pc.r * p.max_blocks;
-        auto loads = [&](int j) {  // the lane has a box in key tile j
-          return j < pc.k1 && b < bpt && j * KT + b * rows < pc.n_keys;
-        };
-        auto fetch = [&](int j) -> int {  // its physical block
-          return loads(j) ? __ldg(table + (j * KT + b * rows) / p.B) : 0;
-        };
-        int id = fetch(pc.k0);
-        for (int j = pc.k0; j < pc.k1; ++j, ++g) {
-          const int next = fetch(j + 1);
-          const bool mine = loads(j);
-          const bool bad = mine && (id < 0 || id >= p.num_blocks);
-          if (__any_sync(full, bad) && lane == 0) raise_error(p.err, kErrBounds);
-          const int blk = bad ? 0 : id;  // a valid block; the output is then unspecified
-          const int boxes = __popc(__ballot_sync(full, mine));
-          ok = (g < kStages || __all_sync(full, mbar_wait(&tail->k_empty[st], phase, p.err))) &&
-               !__any_sync(full, aborted(tail));
-          if (!ok) break;
-          if (lane == 0)
-            mbar_arrive_expect_tx(&tail->k_full[st], (uint32_t)(boxes * rows * 128));
-          __syncwarp();
-          if (mine) {
-            uint8_t* dst = smem + S::kOffK + st * S::kStage + c * kChunk + b * rows * 128;
-            const int y = blk * p.B + (j * KT + b * rows) % p.B;
-            if (c < L / 64)
-              tc::tma_load_2d(dst, &tmap_c, c * 64, y, &tail->k_full[st]);
-            else
-              tc::tma_load_2d(dst, &tmap_r, 0, y, &tail->k_full[st]);
+        Walk<NR> walk(tail, begin, end, in_group);
+        Piece pc;
+        int g = 0, pieces = 0;     // key tiles and pieces so far
+        int st = 0, phase = 1;     // stage, and the parity its emptying waits for
+        bool ok = true;
+        while (ok && walk.next(p, pc)) {
+          if (pc.k0 >= pc.k1) continue;  // no row of the tile sees these keys
+          if (pieces > 0 && !mbar_wait(&tail->q_empty, (pieces - 1) & 1, p.err)) {
+            ok = false;
+            break;
           }
-          if (++st == kStages) {
-            st = 0;
-            phase ^= 1;
+          mbar_arrive_expect_tx(&tail->q_full, S::kQBytes);
+          tc::tma_load_3d(smem, &tmap_q, 0, walk.q.q_begin * p.Hq + pc.tile * NR, 0, &tail->q_full);
+          ++pieces;
+          const int32_t* table = p.block_tables + (int64_t)pc.r * p.max_blocks;
+          // physical row of the first key of half i of tile j (16-token blocks
+          // fill a tile in two halves)
+          auto fetch = [&](int j, int i) -> int {
+            const int key = j * KT + i * 16;
+            return j < pc.k1 && key < pc.n_keys ? __ldg(table + (key >> p.b_shift)) : 0;
+          };
+          const bool halves = p.b_shift == 4;
+          int id0 = fetch(pc.k0, 0), id1 = halves ? fetch(pc.k0, 1) : 0;
+          for (int j = pc.k0; j < pc.k1; ++j, ++g) {
+            const int next0 = fetch(j + 1, 0), next1 = halves ? fetch(j + 1, 1) : 0;
+            if (id0 < 0 || id0 >= p.num_blocks || id1 < 0 || id1 >= p.num_blocks) {
+              raise_error(p.err, kErrBounds);  // a valid block; the output is then unspecified
+              if (id0 < 0 || id0 >= p.num_blocks) id0 = 0;
+              if (id1 < 0 || id1 >= p.num_blocks) id1 = 0;
+            }
+            if (g >= kStages && (!mbar_wait(&tail->k_empty[st], phase, p.err) || aborted(tail))) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = smem + S::kOffK + st * S::kStage;
+            uint64_t* bar = &tail->k_full[st];
+            if (!halves) {
+              const int y = (id0 << p.b_shift) + ((j * KT) & ((1 << p.b_shift) - 1));
+              mbar_arrive_expect_tx(bar, S::kStage);
+              tc::tma_load_3d(dst, &tmap_c, 0, y, 0, bar);
+              tc::tma_load_2d(dst + (L / 64) * kChunk, &tmap_r, 0, y, bar);
+            } else {
+              const bool both = j * KT + 16 < pc.n_keys;
+              mbar_arrive_expect_tx(bar, both ? S::kStage : S::kStage / 2);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (i == 1 && !both) break;
+                const int y = (i ? id1 : id0) << 4;
+#pragma unroll
+                for (int c = 0; c < L / 64; ++c)
+                  tc::tma_load_3d(dst + c * kChunk + i * 2048, &tmap_c, 0, y, c, bar);
+                tc::tma_load_2d(dst + (L / 64) * kChunk + i * 2048, &tmap_r, 0, y, bar);
+              }
+            }
+            if (++st == kStages) {
+              st = 0;
+              phase ^= 1;
+            }
+            id0 = next0;
+            id1 = next1;
           }
-          id = next;
         }
-      }
-      // every issued copy lands before the CTA may leave
-      if (lane == 0) {
+        // every issued copy lands before the CTA may leave
         if (!ok) tail->abort = 1;
         if (pieces > 0) mbar_wait(&tail->q_full, (pieces - 1) & 1, p.err);
         for (int i = max(0, g - kStages); i < g; ++i)
@@ -405,98 +423,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // ----------------------------------------------------------- MMA issuer
+      // ------------------------------------------------------------------- S
       if (tc::elect_one()) {
-        constexpr uint32_t idesc_s = tc::idesc_16bit_f32(64, KT, false, false, false);
-        constexpr uint32_t idesc_o = tc::idesc_16bit_f32(128, NR, true, false, false);
+        constexpr uint32_t idesc = tc::idesc_16bit_f32(64, KT, false, false, false);
         const uint64_t q_desc = tc::smem_desc_sw128(smem, 16, 1024);
-        const uint64_t p_desc = tc::smem_desc_sw128(smem + S::kOffP, 16, 1024);
         const uint64_t k_desc = tc::smem_desc_sw128(smem + S::kOffK, 16, 1024);
-        const uint64_t v_desc = tc::smem_desc_sw128(smem + S::kOffK, kChunk, 1024);
-        // Two walks over the same pieces: tile `s` is the next to be scored, `v`
-        // the next whose P is taken; s runs ahead by at most three tiles.
-        Walk<NR> s_walk(tail, begin, end), v_walk(tail, begin, end);
-        Piece sp, vp;
-        auto advance = [&](Walk<NR>& w, Piece& x) {  // to the next piece with keys
-          while (w.next(p, x))
-            if (x.k0 < x.k1) return true;
-          return false;
-        };
-        bool s_more = advance(s_walk, sp), v_more = advance(v_walk, vp);
-        int s = 0, s_st = 0, s_phase = 0, s_piece = 0, sj = sp.k0;
-        int v = 0, v_st = 0, v_piece = 0, vj = vp.k0;
-        int fixes = 0;
+        Walk<NR> walk(tail, begin, end, in_group);
+        Piece pc;
+        int g = 0, st = 0, phase = 0, pieces = 0;
         bool ok = true;
-        int idle = 0;
-        unsigned long long t0 = 0;
-        while (ok && v_more) {
-          if (s_more && s - v < kSBufs - 1 && mbar_test_wait(&tail->k_full[s_st], s_phase) &&
-              (sj > sp.k0 || mbar_test_wait(&tail->q_full, s_piece & 1))) {
+        while (ok && walk.next(p, pc)) {
+          if (pc.k0 >= pc.k1) continue;
+          if (!(ok = mbar_wait(&tail->q_full, pieces & 1, p.err))) break;
+          ++pieces;
+          for (int j = pc.k0; j < pc.k1; ++j, ++g) {
+            const int buf = g % kSBufs;
+            ok = (g < kSBufs || mbar_wait(&tail->s_empty[buf], (g / kSBufs - 1) & 1, p.err)) &&
+                 mbar_wait(&tail->k_full[st], phase, p.err);
+            if (!ok) break;
             tc::fence_after_sync();
-            const uint64_t ks = tc::desc_at(k_desc, s_st * S::kStage);
-            const uint32_t d = tmem + kTmemS + (s % kSBufs) * KT;
+            const uint64_t ks = tc::desc_at(k_desc, st * S::kStage);
+            const uint32_t d = tmem + kTmemS + buf * KT;
 #pragma unroll
             for (int k = 0; k < S::kChunks * 4; ++k)
               tc::mma_bf16_ss(d, tc::desc_at(q_desc, (k >> 2) * NR * 128 + (k & 3) * 32),
-                              tc::desc_at(ks, (k >> 2) * kChunk + (k & 3) * 32), idesc_s, k > 0);
-            tc::mma_commit(&tail->s_full[s % kSBufs]);
-            ++s;
-            if (++s_st == kStages) {
-              s_st = 0;
-              s_phase ^= 1;
+                              tc::desc_at(ks, (k >> 2) * kChunk + (k & 3) * 32), idesc, k > 0);
+            tc::mma_commit(&tail->s_full[buf]);
+            if (++st == kStages) {
+              st = 0;
+              phase ^= 1;
             }
-            if (++sj == sp.k1) {
-              tc::mma_commit(&tail->q_empty);
-              ++s_piece;
-              s_more = advance(s_walk, sp);
-              sj = sp.k0;
-            }
-            idle = 0;
           }
-          // (the first product of a piece overwrites O: the last piece is out)
-          if (v < s && mbar_test_wait(&tail->p_full[v & 1], (v >> 1) & 1) &&
-              (vj > vp.k0 || v_piece == 0 ||
-               mbar_test_wait(&tail->o_empty, (v_piece - 1) & 1))) {
-            if (*reinterpret_cast<volatile uint32_t*>(&tail->ask[v & 1][0]) != 0) {
+          tc::mma_commit(&tail->q_empty);
+        }
+        if (!ok) tail->abort = 1;
+        tc::mma_commit(&tail->final_mma);
+        mbar_wait(&tail->final_mma, 0, p.err);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------------ PV
+      if (tc::elect_one()) {
+        constexpr uint32_t idesc = tc::idesc_16bit_f32(128, NR, true, false, false);
+        const uint64_t p_desc = tc::smem_desc_sw128(smem + S::kOffP, 16, 1024);
+        const uint64_t v_desc = tc::smem_desc_sw128(smem + S::kOffK, kChunk, 1024);
+        Walk<NR> walk(tail, begin, end, in_group);
+        Piece pc;
+        int g = 0, st = 0, pieces = 0, fixes = 0;
+        bool ok = true;
+        while (ok && walk.next(p, pc)) {
+          if (pc.k0 >= pc.k1) continue;
+          for (int j = pc.k0; j < pc.k1; ++j, ++g) {
+            if (!(ok = mbar_wait(&tail->p_full[g & 1], (g >> 1) & 1, p.err))) break;
+            if (j == pc.k0) {
+              // the first product of a piece overwrites O: the last piece is out
+              if (pieces > 0 && !(ok = mbar_wait(&tail->o_empty, (pieces - 1) & 1, p.err))) break;
+            } else if (*reinterpret_cast<volatile uint32_t*>(&tail->ask[g & 1][0]) != 0) {
               // rows of this tile have a new reference: O, complete up to the
               // tile before, is rescaled first
-              *reinterpret_cast<volatile int32_t*>(&tail->fix_tile) = v;
-              ok = mbar_wait(&tail->pv_done[(v - 1) & 1], ((v - 1) >> 1) & 1, p.err);
+              *reinterpret_cast<volatile int32_t*>(&tail->fix_tile) = g;
+              ok = mbar_wait(&tail->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err);
               mbar_arrive(&tail->fix);
               ok = ok && mbar_wait(&tail->fixed, fixes & 1, p.err);
               if (!ok) break;
               ++fixes;
             }
             tc::fence_after_sync();
-            const uint64_t vs = tc::desc_at(v_desc, v_st * S::kStage);
-            const uint64_t ps = tc::desc_at(p_desc, (v & 1) * 64);
-            const bool first = vj == vp.k0;
+            const uint64_t vs = tc::desc_at(v_desc, st * S::kStage);
+            const uint64_t ps = tc::desc_at(p_desc, (g & 1) * 64);
 #pragma unroll
             for (int m = 0; m < kBlocks; ++m)
 #pragma unroll
               for (int k = 0; k < KT / 16; ++k)
                 tc::mma_bf16_ss(tmem + m * NR, tc::desc_at(vs, 2 * m * kChunk + k * 16 * 128),
-                                tc::desc_at(ps, k * 32), idesc_o, !first || k > 0);
-            tc::mma_commit(&tail->k_empty[v_st]);
-            tc::mma_commit(&tail->pv_done[v & 1]);
-            ++v;
-            if (++v_st == kStages) v_st = 0;
-            if (++vj == vp.k1) {
-              ++v_piece;
-              v_more = advance(v_walk, vp);
-              vj = vp.k0;
-            }
-            idle = 0;
+                                tc::desc_at(ps, k * 32), idesc, j > pc.k0 || k > 0);
+            tc::mma_commit(&tail->k_empty[st]);
+            tc::mma_commit(&tail->pv_done[g & 1]);
+            if (++st == kStages) st = 0;
           }
-          // nothing came for long: give up after the usual limit
-          if (++idle == 4096) t0 = global_timer_ns();
-          if (idle > 4096 && (idle & 1023) == 0) {
-            if (aborted(tail)) ok = false;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-              raise_error(p.err, kErrTimeout);
-              ok = false;
-            }
-          }
+          ++pieces;
         }
         if (!ok) tail->abort = 1;
         tc::mma_commit(&tail->final_mma);
@@ -552,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      Walk<NR> walk(tail, begin, end);
+      Walk<NR> walk(tail, begin, end, in_group);
       Piece pc;
       int g = 0, pieces = 0;
       bool ok = true;
@@ -575,6 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_after_sync();
             tmem_ld_16x32(tmem + kTmemS + (g % kSBufs) * KT + lanes, sr);
             tc::tmem_wait_ld();
+            tc::fence_before_sync();
+            if (lane == 0) mbar_arrive(&tail->s_empty[g % kSBufs]);
             if (key0 + KT > min(lim_a, lim_b)) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -778,9 +785,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
   const LatentJoin j = p.joins[b];
   const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= j.rows) return;
-  // piece i: slot 2 b - 1 for i = 0, then slots 2 (b + i - 1)
-  const int n = j.last - b + 2;
-  auto slot = [&](int i) -> int64_t { return i == 0 ? 2 * b - 1 : 2 * (b + i - 1); };
+  // piece 0 is slot 1 of the CTA one group back, piece i slot 0 of the CTA
+  // i - 1 groups on
+  const int n = j.pieces;
+  auto slot = [&](int i) -> int64_t { return 2 * (b + (i - 1) * p.lanes) + (i == 0 ? 1 : 0); };
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) {
     const float2 ml = p.part_ml[slot(i) * NR + row];
@@ -839,16 +847,32 @@ size_t scratch_bytes(int n, int NR, int L) {
          (size_t)2 * n * NR * L * sizeof(float);
 }
 
-bool encode_2d(CUtensorMap* m, CUtensorMapDataType type, int elt, const void* base, int64_t cols,
-               int64_t rows, int box_cols, int box_rows) {
+// Rows of `chunks` times 64 bf16 columns, row_bytes apart, as [chunk][row][64]:
+// one box is `box_rows` rows of `box_chunks` chunks, chunk after chunk in shared
+// memory, each 128-byte swizzled.
+bool encode_chunks(CUtensorMap* m, const void* base, int chunks, int64_t row_bytes, int64_t rows,
+                   int box_rows, int box_chunks) {
   auto encode = tensor_map_encoder();
   if (!encode) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * elt};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)chunks};
+  const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_rope(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {kRope, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {kRope * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   const cuuint32_t es[2] = {1, 1};
-  return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, es,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+                es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -859,18 +883,18 @@ pa_status launch(const LatentParams& p, const void* q, const pa_latent_pool* poo
   using S = Smem<L, NR>;
   CUtensorMap tq, tc, tr;
   const int64_t cells = (int64_t)pool->num_blocks * pool->block_size;
-  const int box_rows = std::min(p.B, KT);
-  if (!encode_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, L + kRope, (int64_t)p.T * p.Hq, 64,
-                 NR) ||
-      !encode_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->latent, L, cells, 64, box_rows) ||
-      !encode_2d(&tr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->rope, kRope, cells, 64, box_rows))
+  const int box_rows = std::min(pool->block_size, KT);
+  if (!encode_chunks(&tq, q, L / 64 + 1, (L + kRope) * 2, (int64_t)p.T * p.Hq, NR, L / 64 + 1) ||
+      !encode_chunks(&tc, pool->latent, L / 64, L * 2, cells, box_rows,
+                     box_rows == KT ? L / 64 : 1) ||
+      !encode_rope(&tr, pool->rope, cells, box_rows))
     return PA_ERR_CUDA;
   if (cudaFuncSetAttribute(latent_attn_kernel<L, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            S::kAlloc) != cudaSuccess)
     return PA_ERR_CUDA;
   latent_attn_kernel<L, NR><<<grid, kThreads, S::kAlloc, s>>>(tq, tc, tr, p);
   pa_status st = launch_status();
-  if (st != PA_OK || grid == 1) return st;  // one CTA cuts nothing
+  if (st != PA_OK || grid == p.lanes) return st;  // one group cuts nothing
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, NR / kJoinWarps);
   cfg.blockDim = dim3(kJoinWarps * 32);
@@ -927,17 +951,34 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
 
   // Row tiles: the smallest of 16, 32 and 64 rows that covers the widest
   // request in one pass over its cells; 64 past that.
-  int64_t widest = 0, W = 0;
+  int64_t widest = 0;
   for (int r = 0; r < R; ++r)
     widest = std::max<int64_t>(widest, (int64_t)(qsl_host[r + 1] - qsl_host[r]) * Hq);
   const int NR = widest <= 16 ? 16 : widest <= 32 ? 32 : 64;
-  for (int r = 0; r < R; ++r) {
-    const int64_t rows = (int64_t)(qsl_host[r + 1] - qsl_host[r]) * Hq;
-    if (rows > 0)
-      W += (rows + NR - 1) / NR * ((seq_lens_host[r] + pa::kLatentKeys - 1) / pa::kLatentKeys);
+  // CTAs side by side (LatentParams): a tile of keys costs a CTA about 1300
+  // cycles of products and HBM 1570 cycles of an SM's share; two CTAs on the same
+  // keys share the latter (more would gain nothing: the products then bound).
+  const int sms = std::min(pa::num_sms(), pa::kLatentMaxCtas);
+  int64_t W = 0, best = INT64_MAX;
+  int G = 1;
+  for (int lanes = 1; lanes <= 2; ++lanes) {
+    int64_t w = 0;
+    for (int r = 0; r < R; ++r) {
+      const int64_t rows = (int64_t)(qsl_host[r + 1] - qsl_host[r]) * Hq;
+      if (rows > 0)
+        w += ((rows + NR - 1) / NR + lanes - 1) / lanes *
+             ((seq_lens_host[r] + pa::kLatentKeys - 1) / pa::kLatentKeys);
+    }
+    const int64_t cost = w * std::max(1570, 1300 * lanes);
+    if (lanes <= sms && cost < best) {
+      best = cost;
+      W = w;
+      G = lanes;
+    }
+    if (w > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (widest <= NR) break;  // one row tile each
   }
-  if (W > INT32_MAX) return PA_ERR_UNSUPPORTED;
-  const int grid = (int)std::min<int64_t>(W, std::min(pa::num_sms(), pa::kLatentMaxCtas));
+  const int grid = G * (int)std::min<int64_t>(W, sms / G);
   if (workspace_bytes < pa::scratch_bytes(grid, NR, L)) return PA_ERR_INVALID;
 
   pa::LatentParams p{};
@@ -952,7 +993,9 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
   p.max_blocks = max_blocks;
   p.num_blocks = pool->num_blocks;
   p.B = pool->block_size;
+  p.b_shift = p.B == 16 ? 4 : p.B == 32 ? 5 : 6;
   p.causal = causal;
+  p.lanes = G;
   p.scale_log2 = scale * 1.4426950408889634f;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.joins = reinterpret_cast<pa::LatentJoin*>(ws);

@@ -13,23 +13,28 @@ constexpr int kLatentRows = 64;     // most query rows (token, head) per row til
 constexpr int kLatentMaxCtas = 1024;
 
 // The work of one call is laid out as one sequence of 32-key tiles, the "flat
-// space": unit (request r, row tile i) holds the C_r = ceil(seq_len / 32) key
-// tiles that the NR query rows i NR .. of the request are scored against, at
-// pref[r] + i C_r, pref the exclusive running sum of tiles_r C_r. CTA b of the
-// grid takes the tiles [b Q, b Q + Q), Q = ceil(W / grid): equal shares
-// whatever the lengths. Its pieces are the parts of units inside that range; a
-// piece that is a whole unit writes its rows, the others (at most the first
-// and the last of a CTA) write partials, joined by log-sum-exp:
-//   slot 2 b      the piece that begins inside a unit
-//   slot 2 b + 1  the piece that begins a unit and does not end it
-// so the partials of a unit cut at CTA boundaries c0 + 1 .. c1 are slot
-// 2 c0 + 1 and the slots 2 c of c = c0 + 1 .. c1, and the scratch depends on the
-// grid alone, not on the batch. Everything is computed from the device arrays
-// at every launch, so a captured call follows lengths that change.
-struct LatentJoin {       // what the join needs of CTA b's first piece
-  int32_t rows;           // query rows of the unit cut at b Q; 0: none, or joined at an earlier cut
-  int32_t last;           // c1
-  int64_t out_row;        // first row of the unit in out
+// space". The grid is NG groups of G CTAs (G 1 or 2) that walk it side by
+// side: a pass (request r, row tiles i G .. i G + G - 1 of NR query rows, one to
+// each CTA of the group) takes the C_r = ceil(seq_len / 32) key tiles of the
+// request, at pref[r] + i C_r, pref the exclusive running sum of passes_r C_r.
+// Group b takes the tiles [b Q, b Q + Q), Q = ceil(W / NG): equal shares whatever
+// the lengths, and a cell that several row tiles need is read from HBM once,
+// by the first of the group's CTAs that comes to it. A CTA's pieces are the parts
+// of passes inside its group's range; a piece that is a whole pass writes its
+// rows, the others (at most the first and the last) write partials, joined by
+// log-sum-exp:
+//   slot 2 c      the piece of CTA c that begins inside a pass
+//   slot 2 c + 1  the piece that begins a pass and does not end it
+// so the partials of a row tile cut at group boundaries b0 + 1 .. b1 are slot
+// 2 c + 1 of its CTA in group b0 and the slots 2 c of those in b0 + 1 .. b1, and
+// the scratch depends on the grid alone, not on the batch. Everything is
+// computed from the device arrays at every launch, so a captured call follows
+// lengths that change.
+struct LatentJoin {       // what the join needs of a CTA's first piece
+  int32_t rows;           // query rows of the tile cut at its start; 0: none, or
+                          // joined at an earlier cut
+  int32_t pieces;         // partials of that tile
+  int64_t out_row;        // its first row in out
 };
 
 struct LatentParams {
@@ -38,8 +43,9 @@ struct LatentParams {
   const int32_t* seq_lens;     // [R]
   const int32_t* block_tables; // [R][max_blocks]
   const float* scales;         // E4M3 pools: [num_blocks][B]
-  int32_t T, R, Hq, max_blocks, num_blocks, B;
+  int32_t T, R, Hq, max_blocks, num_blocks, B, b_shift;  // B = 1 << b_shift
   int32_t causal;
+  int32_t lanes;               // G
   float scale_log2;            // softmax scale * log2(e)
   LatentJoin* joins;           // [grid]
   float2* part_ml;             // [2 grid][NR] (max in log2 units, sum)
