@@ -6,9 +6,9 @@
 // its rows: s = scale * (q_c . c + q_r . k_r), o = softmax(s) c, the softmax
 // running over key tiles with a reference maximum and sum per row.
 //
-// What bounds it: a cell is (L + 64) * 2 bytes and each row spends 2 (2 L + 64)
-// operations on it; up to about 128 rows per request that is less tensor time
-// than the cell takes from HBM, so the design is laid out for streaming.
+// What bounds it: a bf16 cell is (L + 64) * 2 bytes and each row spends
+// 2 (2 L + 64) operations on it; up to about 64 rows per request that is less
+// tensor time than the cell takes from HBM, so the design is laid out for streaming.
 //
 // One CTA per SM walks an equal share of all (row tile, 32-key tile) pairs
 // (pa::LatentParams). Both products run on the 5th-generation tensor cores:
@@ -22,20 +22,38 @@
 // Tiles are 32 keys (36 KB at L 512) so that four of them fit beside 64 rows of
 // Q: a stage is loading for about 2000 cycles and in use (S, softmax, PV and
 // their hand-overs) for 2700, and what HBM delivers a tile in is 1570.
-//   warp 0      TMA producer: the Q tile, then the key tiles into a ring of stages
-//   warp 1      TMEM and, one elected lane, S, up to four tiles ahead
-//   warp 2      one elected lane, PV. (One lane for both spent a third of a tile's
-//               time between the two batches of products.)
-//   warps 4-7   softmax of 16 rows each (S read as 16 x 256-bit fragments: a row
-//               in four lanes), P written by stmatrix; then the output
+//   warp 0      TMA producer (one lane): the key tiles into a ring of stages, and
+//               the Q tile
+//   warp 1      TMEM and, one lane, S, up to four tiles ahead
+//   warp 2      one lane, PV. (One lane for both products spent a third of a
+//               tile's time between the two batches of them.)
+//   warp 3      the CTA's pieces, found once and handed to the others through a
+//               ring of four; it also asks L2 for a coming piece's first cells
+//   warps 4-7   softmax (S read as 16 x 256-bit fragments: a row in four lanes),
+//               P to shared memory; then the output
+//   warps 8-11  (E4M3) the query tile as E4M3 parts
 // The softmax warps share nothing tile by tile. A warp that moves a row's
 // reference maximum says so beside P; warp 2 then asks all four to rescale
 // their dims of O before it issues that PV (rare: growth by more than 2^8).
 // Every wait is bounded; a timeout sets the error word and the CTA unwinds.
+//
+// E4M3 pools: both products take the codes as they are stored (kind::f8f6f4),
+// nothing is widened. The other operand is a sum of two E4M3 numbers, hi + lo:
+//   q 2^e = hi + lo, 2^e bringing the row's largest magnitude to [2^7, 2^8). A
+//     bf16 number has 8 significant bits and each part 4, so the sum is exact
+//     down to E4M3's smallest step, 2^-17 of the row's maximum.
+//   p s_n = hi + lo for key n of scale s_n, below 2^-8 of the weight off (as
+//     bf16), no less than 2^-14 of the row's largest weight. The reference
+//     maximum is that of p s_n, placed at 2^4, so weights stay below 2^8.
+// For 32 rows or fewer the parts of q are stacked in the 64 rows of S: the lane
+// that reads a row's hi scores reads its lo scores too. The rotary part of q
+// and k stays bf16 and has S columns of its own, since s_n does not apply to it.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cmath>
+
+#include <cuda_fp8.h>
 
 #include "latent_attn.h"
 #include "pa_device.cuh"
@@ -45,22 +63,33 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kRope = 64;
 constexpr int KT = kLatentKeys;
-constexpr int kChunk = KT * 128;   // 64 bf16 columns of a key tile
+constexpr int kChunk = KT * 128;   // 128 bytes of each row of a key tile: 64 bf16 or 128 codes
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;   // S buffers at columns 256, 288, 320, 352
-constexpr int kSBufs = 4, kMaxStages = 10;
-constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kTmemR = 384;   // E4M3: the rotary part of S at 384 ..
+constexpr int kSBufs = 4, kMaxStages = 10, kPieces = 4;
+// The reference maximum moves when it grows by more than 2^kRescaleLog2; weights
+// of the maximum are placed at 2^kTargetLog2 (E4M3 weights must stay below 448).
+template <bool F8> constexpr float kRescaleLog2 = F8 ? 3.f : 8.f;
+template <bool F8> constexpr float kTargetLog2 = F8 ? 4.f : 0.f;
 
-template <int L, int NR>
+template <int L, int NR, bool F8>
 struct Smem {
-  static constexpr int kChunks = L / 64 + 1;          // the last one is the rotary part
-  static constexpr int kQBytes = kChunks * NR * 128;
-  static constexpr int kStage = kChunks * kChunk;
+  static constexpr int kThreads = F8 ? 384 : 256;
+  static constexpr bool kStacked = F8 && NR <= 32;    // hi and lo rows of q in one S
+  static constexpr int kCols = F8 ? L / 128 : L / 64; // 128-byte chunks of a latent row
+  static constexpr int kQRows = kStacked ? 2 * NR : NR;
+  static constexpr int kQChunk = kQRows * 128;
+  // bf16: the latent chunks, then the rotary part. E4M3: the chunks of hi (and
+  // lo, stacked), those of lo if apart, then the rotary part.
+  static constexpr int kQParts = F8 && !kStacked ? 2 : 1;
+  static constexpr int kOffQR = kQParts * kCols * kQChunk;
+  static constexpr int kQBytes = kOffQR + kQChunk;
+  static constexpr int kStage = (kCols + 1) * kChunk; // the last chunk is the rotary part
   static constexpr int kPBytes = NR * 128;            // two tiles of P side by side
-  static constexpr int kTail = 2048;                  // barriers and row statistics
+  static constexpr int kTail = F8 ? 5120 : 2048;      // barriers, pieces, row statistics
   static constexpr int kFit = (232448 - 1024 - kTail - kQBytes - kPBytes) / kStage;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kOffK = kQBytes;
@@ -70,31 +99,49 @@ struct Smem {
   static_assert(kStages >= 4, "needs four key tiles in flight");
   static_assert(kAlloc <= 232448, "dynamic shared memory above the 227 KB per-block limit");
   static_assert(kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzled tiles start on 1024 bytes");
-  // S always reads 64 rows of Q: the rows past NR are whatever follows in
-  // shared memory (their scores are never looked at)
-  static_assert(kQBytes + (64 - NR) * 128 <= kAlloc - 1024, "Q over-read leaves the allocation");
+  // S always reads 64 rows of Q: the rows past the tile's are whatever follows
+  // in shared memory (their scores are never looked at)
+  static_assert(kQBytes + 64 * 128 <= kAlloc - 1024, "Q over-read leaves the allocation");
 };
 
+// A CTA's part of one pass, as the roles need it.
+struct Piece {
+  int32_t r;           // request; -1: no more pieces
+  int32_t k0, k1;      // key tiles [k0, k1)
+  int32_t n_keys;      // keys any row of the tile sees (k1 is cut to it)
+  int32_t rows;        // valid query rows of the tile
+  int32_t slot;        // partial slot 0 / 1 of the CTA, or -1: the whole pass
+  int32_t row;         // the tile's first row in q and out
+  int32_t first;       // the same within the request; -1: every row sees n_keys
+  int32_t sees;        // keys that the request's first token sees
+};
+
+template <bool F8>
 struct Tail {
   uint64_t q_full, q_empty;
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
   uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t p_full[2], pv_done[2];
   uint64_t fix, fixed;           // O is to be rescaled for tile fix_tile; it has been
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t o_empty, final_mma;
-  float alpha[2][kLatentRows];   // by tile: factors of the rows of a warp that asks
-  float l[2][kLatentRows];       // by piece: 1 / sum
-  uint8_t ask[2][4];             // by tile: softmax warps that ask for a rescale
+  Piece piece[kPieces];
+  alignas(16) float alpha[2][kLatentRows];   // by tile: factors of the rows of a warp that asks
+  alignas(16) float l[2][kLatentRows];       // by piece: 1 / sum
+  alignas(16) float scale[F8 ? kMaxStages : 1][KT];      // E4M3: of the stage's keys
+  float q_scale[F8 ? kPieces : 1][kLatentRows];          // E4M3: 2^-e of the rows
+  alignas(4) uint8_t ask[2][4];  // by tile: softmax warps that ask for a rescale
   int32_t fix_tile;
-  int64_t warp_sum[kThreads / 32];
+  int64_t warp_sum[12];
   int32_t base;        // flat start of the request that holds the CTA's first tile
   int32_t req;         // that request
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Tail) <= 2048, "Tail overruns its slot");
+static_assert(sizeof(Tail<true>) <= 5120 && sizeof(Tail<false>) <= 2048, "Tail overruns its slot");
 
-__device__ __forceinline__ bool aborted(Tail* t) {
+template <bool F8>
+__device__ __forceinline__ bool aborted(Tail<F8>* t) {
   return *reinterpret_cast<volatile int*>(&t->abort) != 0;
 }
 
@@ -144,6 +191,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// Two fp32 to E4M3 (nearest even), x in the low byte, and what they stand for.
+__device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+
 // ------------------------------------------------------------ the flat space
 
 struct Request {
@@ -172,14 +224,6 @@ __device__ __forceinline__ Request load_request(const LatentParams& p, int r, bo
   return q;
 }
 
-// A CTA's part of one pass: key tiles [k0, k1) for row tile `tile` of request r.
-struct Piece {
-  int32_t r, tile, k0, k1;
-  int32_t n_keys;      // keys any row of the tile sees (k1 is cut to it)
-  int32_t rows;        // valid query rows of the tile (none: the pass has fewer tiles)
-  int32_t slot;        // partial slot 0 / 1 of the CTA, or -1: the whole pass
-};
-
 // (The whole flat space fits 31 bits, so do all positions.)
 template <int NR>
 struct Walk {
@@ -187,8 +231,9 @@ struct Walk {
   bool loaded;
   Request q;
 
-  __device__ Walk(const Tail* t, int32_t begin, int32_t stop, int32_t in_group)
-      : pos(begin), end(stop), base(t->base), r(t->req), lane(in_group), loaded(false), q{} {}
+  __device__ Walk(int32_t begin, int32_t stop, int32_t first_req, int32_t first_base,
+                  int32_t in_group)
+      : pos(begin), end(stop), base(first_base), r(first_req), lane(in_group), loaded(false), q{} {}
 
   __device__ bool next(const LatentParams& p, Piece& out) {
     if (pos >= end) return false;
@@ -202,53 +247,56 @@ struct Walk {
       q = load_request<NR>(p, r, false);
     }
     const unsigned off = pos - base;
+    const int pass = (int)(off / (unsigned)q.keys), tile = pass * p.lanes + lane;
     out.r = r;
-    const int pass = (int)(off / (unsigned)q.keys);
-    out.tile = pass * p.lanes + lane;
     out.k0 = (int)off - pass * q.keys;
     const int k1 = min(q.keys, out.k0 + (end - pos));
     pos += k1 - out.k0;
     out.slot = out.k0 > 0 ? 0 : k1 < q.keys ? 1 : -1;
-    out.rows = min(NR, q.rows - out.tile * NR);
-    if (out.rows <= 0) {
-      out.rows = 0;
-      out.k1 = out.k0;
-      return true;
-    }
+    out.row = q.q_begin * p.Hq + tile * NR;
+    out.rows = max(0, min(NR, q.rows - tile * NR));  // 0: the pass has fewer tiles
     out.n_keys = q.seq;
-    if (p.causal && q.q_len > 1) {  // up to the last row's token
-      const unsigned last_row = out.tile * NR + out.rows - 1;
-      out.n_keys = q.seq - q.q_len + (int)(last_row / (unsigned)p.Hq) + 1;
+    out.first = -1;
+    out.sees = q.seq - q.q_len + 1;
+    if (p.causal && q.q_len > 1 && out.rows > 0) {  // up to the last row's token
+      out.first = tile * NR;
+      out.n_keys = out.sees + (int)((unsigned)(out.first + out.rows - 1) / (unsigned)p.Hq);
     }
-    out.k1 = min(k1, (out.n_keys + KT - 1) / KT);
+    out.k1 = out.rows > 0 ? min(k1, (out.n_keys + KT - 1) / KT) : out.k0;
     return true;
   }
 };
 
-template <int L, int NR>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int L, int NR, bool F8>
+__global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_c,
                        const __grid_constant__ CUtensorMap tmap_r, const LatentParams p) {
-  using S = Smem<L, NR>;
-  constexpr int kStages = S::kStages;
-  constexpr int kBlocks = L / 128;  // 128-dim blocks of O^T
+  using S = Smem<L, NR, F8>;
+  constexpr int kThreads = S::kThreads, kStages = S::kStages, kCols = S::kCols;
+  constexpr bool kStacked = S::kStacked;
+  constexpr int kBlocks = L / 128;              // 128-dim blocks of O^T
+  constexpr int RT = kStacked ? 1 : 2;          // query rows of a softmax thread
+  constexpr int kWarpRows = 8 * RT;             // and of its warp
+  constexpr int kScoreWarps = NR / kWarpRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Tail* tail = reinterpret_cast<Tail*>(smem + S::kOffTail);
+  Tail<F8>* tail = reinterpret_cast<Tail<F8>*>(smem + S::kOffTail);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, group = cta / p.lanes, in_group = cta - group * p.lanes;
   const int groups = gridDim.x / p.lanes;
   launch_dependents();  // the join that follows may be scheduled now
 
   // ---- this group's range: W, then the request that holds tile group * Q
+  int64_t kept_w = 0, kept_before = 0;
+  if ((int)threadIdx.x < p.R) kept_w = load_request<NR>(p, threadIdx.x, cta == 0).weight;
   if (warp == 1) {
     tc::tmem_alloc(&tail->tmem, kTmemCols);
     tc::tmem_relinquish();
   }
   if (threadIdx.x == 0) {
-    mbar_init(&tail->q_full, 1);
+    mbar_init(&tail->q_full, F8 ? 4 : 1);  // E4M3: the warps that convert
     mbar_init(&tail->q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&tail->k_full[s], 1);
@@ -256,11 +304,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kSBufs; ++s) {
       mbar_init(&tail->s_full[s], 1);
-      mbar_init(&tail->s_empty[s], NR / 16);  // the warps that read S
+      mbar_init(&tail->s_empty[s], kScoreWarps);  // the warps that read S
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tail->p_full[s], 4);   // one arrival per softmax warp
       mbar_init(&tail->pv_done[s], 1);
+    }
+    for (int s = 0; s < kPieces; ++s) {
+      mbar_init(&tail->piece_full[s], 1);
+      mbar_init(&tail->piece_empty[s], F8 ? 11 : 7);  // one arrival per reading warp
     }
     mbar_init(&tail->fix, 1);
     mbar_init(&tail->fixed, 4);
@@ -271,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tail->base = 0;
     fence_mbar_init();
   }
-  // running sum over the requests, kThreads at a time (one step up to 256)
+  // running sum over the requests, kThreads at a time (one step for most batches)
   auto scan = [&](int64_t w, int64_t& total) -> int64_t {  // exclusive sum of w
     int64_t x = w;
 #pragma unroll
@@ -292,12 +344,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return before + x - w;
   };
-  int64_t W = 0, kept_w = 0, kept_before = 0;
-  for (int r0 = 0; r0 < p.R; r0 += kThreads) {
+  int64_t W = 0;
+  kept_before = scan(kept_w, W);
+  for (int r0 = kThreads; r0 < p.R; r0 += kThreads) {
     const int r = r0 + threadIdx.x;
-    kept_w = r < p.R ? load_request<NR>(p, r, cta == 0).weight : 0;
     int64_t total;
-    kept_before = W + scan(kept_w, total);
+    scan(r < p.R ? load_request<NR>(p, r, cta == 0).weight : 0, total);
     W += total;
   }
   if (W > INT32_MAX) {  // (the host has checked its mirrors)
@@ -306,43 +358,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const unsigned Q = ((unsigned)W + groups - 1) / groups;
   const int begin = (int)min(W, (int64_t)group * Q), end = (int)min(W, (int64_t)begin + Q);
-  if (p.R > kThreads) {  // the sums of all but the last step are taken again
+  {
     int64_t sum = 0;
-    for (int r0 = 0; r0 < p.R; r0 += kThreads) {
+    for (int r0 = 0; r0 < p.R; r0 += kThreads) {  // the request, from the sums of each step
       const int r = r0 + threadIdx.x;
-      const int64_t w = r < p.R ? load_request<NR>(p, r, false).weight : 0;
-      int64_t total;
-      const int64_t before = sum + scan(w, total);
+      int64_t w = kept_w, before = kept_before, total = 0;
+      if (p.R > kThreads) {
+        w = r < p.R ? load_request<NR>(p, r, false).weight : 0;
+        before = sum + scan(w, total);
+      }
       sum += total;
       if (begin >= before && begin < before + w) {
         tail->req = r;
         tail->base = (int)before;
       }
     }
-  } else if (begin >= kept_before && begin < kept_before + kept_w) {
-    tail->req = threadIdx.x;
-    tail->base = (int)kept_before;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tail->tmem;
-  if (threadIdx.x == 96) {
-    // the pass cut at this group's start, for the join: handled at its first cut
-    LatentJoin j{};
-    if (begin < end) {
-      const Request q = load_request<NR>(p, tail->req, false);
-      const int pass = (begin - tail->base) / q.keys;
-      const unsigned a = tail->base + pass * q.keys;  // the pass's start
-      const int row0 = (pass * p.lanes + in_group) * NR;
-      if ((unsigned)begin > a && a / Q + 1 == (unsigned)group && row0 < q.rows) {
-        j.rows = min(q.rows - row0, NR);
-        j.pieces = (int32_t)((a + q.keys - 1) / Q - a / Q) + 1;
-        j.out_row = (int64_t)q.q_begin * p.Hq + row0;
-      }
-    }
-    p.joins[cta] = j;
-  }
+
+  // the next piece (n-th of the CTA) for one thread; r < 0 at the end
+  auto piece = [&](int n, bool& ok) -> Piece {
+    Piece pc;
+    ok = mbar_wait(&tail->piece_full[n % kPieces], (n / kPieces) & 1, p.err);
+    if (ok)
+      pc = tail->piece[n % kPieces];
+    else
+      pc.r = -1;
+    return pc;
+  };
+  auto release = [&](int n) { mbar_arrive(&tail->piece_empty[n % kPieces]); };
 
   if (begin < end) {
     if (warp == 0) {
@@ -350,24 +397,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (one lane: a copy instruction with several lanes active costs about
       // 120 cycles a lane, and the ring then waits for its producer)
       if (tc::elect_one()) {
-        tc::prefetch_tensormap(&tmap_q);
         tc::prefetch_tensormap(&tmap_c);
         tc::prefetch_tensormap(&tmap_r);
-        Walk<NR> walk(tail, begin, end, in_group);
-        Piece pc;
-        int g = 0, pieces = 0;     // key tiles and pieces so far
+        if (!F8) tc::prefetch_tensormap(&tmap_q);
+        int g = 0, queries = 0;    // key tiles so far; pieces whose Q is on its way
         int st = 0, phase = 1;     // stage, and the parity its emptying waits for
         bool ok = true;
-        while (ok && walk.next(p, pc)) {
-          if (pc.k0 >= pc.k1) continue;  // no row of the tile sees these keys
-          if (pieces > 0 && !mbar_wait(&tail->q_empty, (pieces - 1) & 1, p.err)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&tail->q_full, S::kQBytes);
-          tc::tma_load_3d(smem, &tmap_q, 0, walk.q.q_begin * p.Hq + pc.tile * NR, 0, &tail->q_full);
-          ++pieces;
+        for (int n = 0;; ++n) {
+          const Piece pc = piece(n, ok);
+          if (pc.r < 0) break;
           const int32_t* table = p.block_tables + (int64_t)pc.r * p.max_blocks;
+          // the Q tile as soon as the last piece's S are done; its keys need not
+          // wait for that
+          auto load_q = [&](bool may_wait) -> bool {
+            if (F8 || queries > n) return true;
+            if (n > 0) {
+              uint64_t* bar = &tail->q_empty;
+              if (may_wait) {
+                if (!mbar_wait(bar, (n - 1) & 1, p.err)) return false;
+              } else if (!mbar_test_wait(bar, (n - 1) & 1)) {
+                return true;
+              }
+            }
+            mbar_arrive_expect_tx(&tail->q_full, S::kQBytes);
+            tc::tma_load_3d(smem, &tmap_q, 0, pc.row, 0, &tail->q_full);
+            queries = n + 1;
+            return true;
+          };
           // physical row of the first key of half i of tile j (16-token blocks
           // fill a tile in two halves)
           auto fetch = [&](int j, int i) -> int {
@@ -376,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           const bool halves = p.b_shift == 4;
           int id0 = fetch(pc.k0, 0), id1 = halves ? fetch(pc.k0, 1) : 0;
+          load_q(false);
           for (int j = pc.k0; j < pc.k1; ++j, ++g) {
             const int next0 = fetch(j + 1, 0), next1 = halves ? fetch(j + 1, 1) : 0;
             if (id0 < 0 || id0 >= p.num_blocks || id1 < 0 || id1 >= p.num_blocks) {
@@ -383,28 +440,33 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (id0 < 0 || id0 >= p.num_blocks) id0 = 0;
               if (id1 < 0 || id1 >= p.num_blocks) id1 = 0;
             }
-            if (g >= kStages && (!mbar_wait(&tail->k_empty[st], phase, p.err) || aborted(tail))) {
-              ok = false;
-              break;
+            if (g >= kStages && !mbar_test_wait(&tail->k_empty[st], phase)) {
+              // the stage may be waiting for products that wait for this Q
+              ok = load_q(true) && mbar_wait(&tail->k_empty[st], phase, p.err) && !aborted(tail);
+              if (!ok) break;
             }
+            load_q(false);
             uint8_t* dst = smem + S::kOffK + st * S::kStage;
             uint64_t* bar = &tail->k_full[st];
+            constexpr int kBytes = S::kStage + (F8 ? KT * 4 : 0);
             if (!halves) {
               const int y = (id0 << p.b_shift) + ((j * KT) & ((1 << p.b_shift) - 1));
-              mbar_arrive_expect_tx(bar, S::kStage);
+              mbar_arrive_expect_tx(bar, kBytes);
               tc::tma_load_3d(dst, &tmap_c, 0, y, 0, bar);
-              tc::tma_load_2d(dst + (L / 64) * kChunk, &tmap_r, 0, y, bar);
+              tc::tma_load_2d(dst + kCols * kChunk, &tmap_r, 0, y, bar);
+              if (F8) bulk_g2s(tail->scale[st], p.scales + y, KT * 4, bar);
             } else {
               const bool both = j * KT + 16 < pc.n_keys;
-              mbar_arrive_expect_tx(bar, both ? S::kStage : S::kStage / 2);
+              mbar_arrive_expect_tx(bar, both ? kBytes : kBytes / 2);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 if (i == 1 && !both) break;
                 const int y = (i ? id1 : id0) << 4;
 #pragma unroll
-                for (int c = 0; c < L / 64; ++c)
+                for (int c = 0; c < kCols; ++c)
                   tc::tma_load_3d(dst + c * kChunk + i * 2048, &tmap_c, 0, y, c, bar);
-                tc::tma_load_2d(dst + (L / 64) * kChunk + i * 2048, &tmap_r, 0, y, bar);
+                tc::tma_load_2d(dst + kCols * kChunk + i * 2048, &tmap_r, 0, y, bar);
+                if (F8) bulk_g2s(tail->scale[st] + i * 16, p.scales + y, 64, bar);
               }
             }
             if (++st == kStages) {
@@ -414,10 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             id0 = next0;
             id1 = next1;
           }
+          ok = ok && load_q(true);
+          if (!ok) break;
+          release(n);
         }
         // every issued copy lands before the CTA may leave
         if (!ok) tail->abort = 1;
-        if (pieces > 0) mbar_wait(&tail->q_full, (pieces - 1) & 1, p.err);
+        if (queries > 0) mbar_wait(&tail->q_full, (queries - 1) & 1, p.err);
         for (int i = max(0, g - kStages); i < g; ++i)
           mbar_wait(&tail->k_full[i % kStages], (i / kStages) & 1, p.err);
       }
@@ -426,16 +491,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------------- S
       if (tc::elect_one()) {
         constexpr uint32_t idesc = tc::idesc_16bit_f32(64, KT, false, false, false);
+        constexpr uint32_t idesc8 = tc::idesc_e4m3_f32(64, KT);
         const uint64_t q_desc = tc::smem_desc_sw128(smem, 16, 1024);
         const uint64_t k_desc = tc::smem_desc_sw128(smem + S::kOffK, 16, 1024);
-        Walk<NR> walk(tail, begin, end, in_group);
-        Piece pc;
-        int g = 0, st = 0, phase = 0, pieces = 0;
+        int g = 0, st = 0, phase = 0;
         bool ok = true;
-        while (ok && walk.next(p, pc)) {
-          if (pc.k0 >= pc.k1) continue;
-          if (!(ok = mbar_wait(&tail->q_full, pieces & 1, p.err))) break;
-          ++pieces;
+        for (int n = 0;; ++n) {
+          const Piece pc = piece(n, ok);
+          if (pc.r < 0) break;
+          if (!(ok = mbar_wait(&tail->q_full, n & 1, p.err))) break;
           for (int j = pc.k0; j < pc.k1; ++j, ++g) {
             const int buf = g % kSBufs;
             ok = (g < kSBufs || mbar_wait(&tail->s_empty[buf], (g / kSBufs - 1) & 1, p.err)) &&
@@ -443,18 +507,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t ks = tc::desc_at(k_desc, st * S::kStage);
-            const uint32_t d = tmem + kTmemS + buf * KT;
+            const uint32_t d = tmem + kTmemS + buf * KT, dr = F8 ? tmem + kTmemR + buf * KT : d;
 #pragma unroll
-            for (int k = 0; k < S::kChunks * 4; ++k)
-              tc::mma_bf16_ss(d, tc::desc_at(q_desc, (k >> 2) * NR * 128 + (k & 3) * 32),
-                              tc::desc_at(ks, (k >> 2) * kChunk + (k & 3) * 32), idesc, k > 0);
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16_ss(dr, tc::desc_at(q_desc, S::kOffQR + k * 32),
+                              tc::desc_at(ks, kCols * kChunk + k * 32), idesc, k > 0);
+#pragma unroll
+            for (int q = 0; q < S::kQParts; ++q)
+#pragma unroll
+              for (int k = 0; k < kCols * 4; ++k) {
+                const uint64_t qa =
+                    tc::desc_at(q_desc, (q * kCols + (k >> 2)) * S::kQChunk + (k & 3) * 32);
+                const uint64_t kb = tc::desc_at(ks, (k >> 2) * kChunk + (k & 3) * 32);
+                if (F8)
+                  tc::mma_e4m3_ss(d, qa, kb, idesc8, q > 0 || k > 0);
+                else
+                  tc::mma_bf16_ss(d, qa, kb, idesc, true);
+              }
             tc::mma_commit(&tail->s_full[buf]);
             if (++st == kStages) {
               st = 0;
               phase ^= 1;
             }
           }
+          if (!ok) break;
           tc::mma_commit(&tail->q_empty);
+          release(n);
         }
         if (!ok) tail->abort = 1;
         tc::mma_commit(&tail->final_mma);
@@ -464,20 +542,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
       // ------------------------------------------------------------------ PV
       if (tc::elect_one()) {
+        // first the pass cut at this group's start, for the join: handled at its first cut
+        LatentJoin join{};
+        {
+          const Request q = load_request<NR>(p, tail->req, false);
+          const int pass = (begin - tail->base) / q.keys;
+          const unsigned a = tail->base + pass * q.keys;  // the pass's start
+          const int row0 = (pass * p.lanes + in_group) * NR;
+          if ((unsigned)begin > a && a / Q + 1 == (unsigned)group && row0 < q.rows) {
+            join.rows = min(q.rows - row0, NR);
+            join.pieces = (int32_t)((a + q.keys - 1) / Q - a / Q) + 1;
+            join.out_row = (int64_t)q.q_begin * p.Hq + row0;
+          }
+        }
+        p.joins[cta] = join;
         constexpr uint32_t idesc = tc::idesc_16bit_f32(128, NR, true, false, false);
+        constexpr uint32_t idesc8 = tc::idesc_e4m3_f32(128, NR) | (1u << 15);  // A MN-major
         const uint64_t p_desc = tc::smem_desc_sw128(smem + S::kOffP, 16, 1024);
         const uint64_t v_desc = tc::smem_desc_sw128(smem + S::kOffK, kChunk, 1024);
-        Walk<NR> walk(tail, begin, end, in_group);
-        Piece pc;
-        int g = 0, st = 0, pieces = 0, fixes = 0;
+        int g = 0, st = 0, fixes = 0;
         bool ok = true;
-        while (ok && walk.next(p, pc)) {
-          if (pc.k0 >= pc.k1) continue;
+        for (int n = 0;; ++n) {
+          const Piece pc = piece(n, ok);
+          if (pc.r < 0) break;
           for (int j = pc.k0; j < pc.k1; ++j, ++g) {
             if (!(ok = mbar_wait(&tail->p_full[g & 1], (g >> 1) & 1, p.err))) break;
             if (j == pc.k0) {
               // the first product of a piece overwrites O: the last piece is out
-              if (pieces > 0 && !(ok = mbar_wait(&tail->o_empty, (pieces - 1) & 1, p.err))) break;
+              if (n > 0 && !(ok = mbar_wait(&tail->o_empty, (n - 1) & 1, p.err))) break;
             } else if (*reinterpret_cast<volatile uint32_t*>(&tail->ask[g & 1][0]) != 0) {
               // rows of this tile have a new reference: O, complete up to the
               // tile before, is rescaled first
@@ -491,28 +583,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_after_sync();
             const uint64_t vs = tc::desc_at(v_desc, st * S::kStage);
             const uint64_t ps = tc::desc_at(p_desc, (g & 1) * 64);
+            const bool add = j > pc.k0;
+            // two products per 128-dim block: bf16, 16 keys each; E4M3, the hi
+            // and the lo weights of all 32 keys
 #pragma unroll
             for (int m = 0; m < kBlocks; ++m)
 #pragma unroll
-              for (int k = 0; k < KT / 16; ++k)
-                tc::mma_bf16_ss(tmem + m * NR, tc::desc_at(vs, 2 * m * kChunk + k * 16 * 128),
-                                tc::desc_at(ps, k * 32), idesc, j > pc.k0 || k > 0);
+              for (int k = 0; k < 2; ++k) {
+                const uint64_t pb = tc::desc_at(ps, k * 32);
+                if (F8)
+                  tc::mma_e4m3_ss(tmem + m * NR, tc::desc_at(vs, m * kChunk), pb, idesc8,
+                                  add || k > 0);
+                else
+                  tc::mma_bf16_ss(tmem + m * NR, tc::desc_at(vs, 2 * m * kChunk + k * 16 * 128),
+                                  pb, idesc, add || k > 0);
+              }
             tc::mma_commit(&tail->k_empty[st]);
             tc::mma_commit(&tail->pv_done[g & 1]);
             if (++st == kStages) st = 0;
           }
-          ++pieces;
+          if (!ok) break;
+          release(n);
         }
         if (!ok) tail->abort = 1;
         tc::mma_commit(&tail->final_mma);
         mbar_wait(&tail->final_mma, 0, p.err);
       }
       __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+      // -------------------------------------------------------------- pieces
+      Walk<NR> walk(begin, end, tail->req, tail->base, in_group);
+      Piece pc;
+      int n = 0;
+      bool ok = true;
+      for (bool more = true; ok && more;) {
+        more = walk.next(p, pc);
+        if (!more) {
+          pc.r = -1;
+        } else if (pc.k0 >= pc.k1) {
+          // no row of the tile sees these keys: sums of zero, which the join skips
+          if (pc.slot >= 0) {
+            float2* ml = p.part_ml + (int64_t)(2 * cta + pc.slot) * NR;
+            for (int i = lane; i < NR; i += 32) ml[i] = make_float2(-INFINITY, 0.f);
+          }
+          continue;
+        }
+        if (n >= kPieces)
+          ok = __all_sync(0xffffffffu, mbar_wait(&tail->piece_empty[n % kPieces],
+                                                 (n / kPieces - 1) & 1, p.err));
+        if (!ok) break;
+        if (lane == 0) {
+          tail->piece[n % kPieces] = pc;
+          mbar_arrive(&tail->piece_full[n % kPieces]);
+        }
+        __syncwarp();
+        // a later piece's first tiles and queries, towards L2 while the ones
+        // before are worked on (16 keys a lane)
+        if (more && n > 0) {
+          const int key = pc.k0 * KT + lane * 16;
+          if (lane < 8 && key < pc.n_keys) {
+            const int32_t id = __ldg(p.block_tables + (int64_t)pc.r * p.max_blocks +
+                                     (key >> p.b_shift));
+            if (id >= 0 && id < p.num_blocks) {
+              const int64_t cell = ((int64_t)id << p.b_shift) + (key & ((1 << p.b_shift) - 1));
+              prefetch_l2(p.latent + cell * L * (F8 ? 1 : 2), 16 * L * (F8 ? 1 : 2));
+              prefetch_l2(p.rope + cell * kRope * 2, 16 * kRope * 2);
+            }
+          } else if (lane == 8) {
+            prefetch_l2(reinterpret_cast<const uint8_t*>(p.q) + (int64_t)pc.row * (L + kRope) * 2,
+                        pc.rows * (L + kRope) * 2);
+          }
+        }
+        ++n;
+      }
+      if (!ok && lane == 0) tail->abort = 1;
+      __syncwarp();
+    } else if (warp < 8) {
       // ---------------------------------------------------- softmax and output
       const int w4 = warp - 4;
-      const bool scores = w4 * 16 < NR;          // this warp's rows w4 * 16 .. + 15
-      const int ra = w4 * 16 + (lane >> 2), rb = ra + 8;  // the thread's two rows
+      const bool scores = w4 < kScoreWarps;
+      int row[RT];                               // the thread's rows of the tile
+#pragma unroll
+      for (int t = 0; t < RT; ++t) row[t] = w4 * kWarpRows + t * 8 + (lane >> 2);
       const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
       uint8_t* ps = smem + S::kOffP;
       const int tid = threadIdx.x - 128;
@@ -524,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t asked = *reinterpret_cast<volatile uint32_t*>(&tail->ask[slot][0]);
 #pragma unroll 1
         for (int c = 0; c < kBlocks * NR; c += 16) {
-          const int r = c % NR;  // the rows of softmax warp r / 16
-          if (((asked >> (r / 2)) & 0xFF) == 0) continue;
+          const int r = c % NR;  // the rows of softmax warp r / kWarpRows (and the next)
+          if (((asked >> (r / kWarpRows * 8)) & (RT == 1 ? 0xFFFF : 0xFF)) == 0) continue;
           uint32_t o[16];
           tmem_ld16(tmem + lanes + c, o);
           tc::tmem_wait_ld();
@@ -557,95 +709,171 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      Walk<NR> walk(tail, begin, end, in_group);
-      Piece pc;
-      int g = 0, pieces = 0;
+      int g = 0;
       bool ok = true;
-      while (ok && walk.next(p, pc)) {
-        const int row0 = pc.tile * NR;
-        int lim_a = 0, lim_b = 0;  // keys the rows see
-        if (scores) {
-          const int vis = walk.q.seq - walk.q.q_len + 1;
-          if (ra < pc.rows) lim_a = p.causal ? vis + (row0 + ra) / p.Hq : walk.q.seq;
-          if (rb < pc.rows) lim_b = p.causal ? vis + (row0 + rb) / p.Hq : walk.q.seq;
+      for (int n = 0;; ++n) {
+        const Piece pc = piece(n, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok || pc.r < 0) break;
+        int lim[RT];                 // keys the rows see
+        float m[RT], l[RT], qs[RT];  // reference (log2), sum; E4M3: 2^-e of the query
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          lim[t] = !scores || row[t] >= pc.rows ? 0
+                   : pc.first < 0
+                       ? pc.n_keys
+                       : pc.sees + (int)((unsigned)(pc.first + row[t]) / (unsigned)p.Hq);
+          m[t] = -INFINITY;
+          l[t] = 0.f;
+          qs[t] = 1.f;
         }
-        float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
+        const int lim_min = RT == 2 ? min(lim[0], lim[RT - 1]) : lim[0];
         for (int j = pc.k0; j < pc.k1; ++j, ++g) {
-          uint32_t sr[16];
-          float* s = reinterpret_cast<float*>(sr);
-          float aa = 1.f, ab = 1.f;
+          float x[RT][8];            // key 8 i + 2 (lane % 4) + b of the tile at [2 i + b]
+          float alpha[RT];
+#pragma unroll
+          for (int t = 0; t < RT; ++t) alpha[t] = 1.f;
+          float sc[8];               // E4M3: scales of those keys
           const int key0 = j * KT;
           if (scores) {
-            if (!(ok = wait(&tail->s_full[g % kSBufs], g / kSBufs))) break;
+            const int buf = g % kSBufs;
+            if (!(ok = wait(&tail->s_full[buf], g / kSBufs))) break;
             tc::fence_after_sync();
-            tmem_ld_16x32(tmem + kTmemS + (g % kSBufs) * KT + lanes, sr);
-            tc::tmem_wait_ld();
-            tc::fence_before_sync();
-            if (lane == 0) mbar_arrive(&tail->s_empty[g % kSBufs]);
-            if (key0 + KT > min(lim_a, lim_b)) {
+            uint32_t sr[16];
+            const float* s = reinterpret_cast<const float*>(sr);
+            tmem_ld_16x32(tmem + kTmemS + buf * KT + lanes, sr);
+            if constexpr (F8) {
+              // (the stage's scales came with its keys)
+              if (!(ok = wait(&tail->k_full[g % kStages], g / kStages))) break;
+              uint32_t rr[16];
+              const float* rs = reinterpret_cast<const float*>(rr);
+              tmem_ld_16x32(tmem + kTmemR + buf * KT + lanes, rr);
+              if (j == pc.k0) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int key = key0 + (i >> 2) * 8 + 2 * (lane & 3) + (i & 1);
-                if (key >= ((i & 2) ? lim_b : lim_a)) s[i] = -INFINITY;
+                for (int t = 0; t < RT; ++t) qs[t] = tail->q_scale[n % kPieces][row[t]];
+              }
+              const float2* st = reinterpret_cast<const float2*>(tail->scale[g % kStages]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = st[4 * i + (lane & 3)];
+                sc[2 * i] = v.x;
+                sc[2 * i + 1] = v.y;
+              }
+              if (key0 + KT > pc.n_keys) {  // unwritten cells' scales may be anything
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (key0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1) >= pc.n_keys) sc[i] = 0.f;
+              }
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int a = (i >> 1) * 4 + (i & 1);
+                if constexpr (kStacked) {
+                  x[0][i] = p.scale_log2 * fmaf((s[a] + s[a + 2]) * qs[0], sc[i], rs[a]);
+                } else {
+                  x[0][i] = p.scale_log2 * fmaf(s[a] * qs[0], sc[i], rs[a]);
+                  x[RT - 1][i] = p.scale_log2 * fmaf(s[a + 2] * qs[RT - 1], sc[i], rs[a + 2]);
+                }
+              }
+            } else {
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                x[0][i] = s[(i >> 1) * 4 + (i & 1)];
+                x[RT - 1][i] = s[(i >> 1) * 4 + (i & 1) + 2];
               }
             }
-            float ta = fmax3(fmaxf(s[0], s[1]), s[4], s[5]);
-            float tb = fmax3(fmaxf(s[2], s[3]), s[6], s[7]);
-            ta = fmax3(ta, fmaxf(s[8], s[9]), fmaxf(s[12], s[13]));
-            tb = fmax3(tb, fmaxf(s[10], s[11]), fmaxf(s[14], s[15]));
+            tc::fence_before_sync();
+            if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
+            if (key0 + KT > lim_min) {
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-              ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
-              tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
-            }
-            ta *= p.scale_log2;
-            tb *= p.scale_log2;
-            // the reference maximum moves only when it grows by more than 2^8
-            // (any reference gives the same softmax; P stays below 2^8)
-            if (ma == -INFINITY) {
-              ma = ta;
-            } else if (ta > ma + kRescaleLog2) {
-              aa = ex2_ftz(ma - ta);
-              ma = ta;
-            }
-            if (mb == -INFINITY) {
-              mb = tb;
-            } else if (tb > mb + kRescaleLog2) {
-              ab = ex2_ftz(mb - tb);
-              mb = tb;
-            }
-            const float na = ma == -INFINITY ? 0.f : -ma, nb = mb == -INFINITY ? 0.f : -mb;
-            float sa = 0.f, sb = 0.f;
+              for (int i = 0; i < 8; ++i) {
+                const int key = key0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1);
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              s[i] = ex2_ftz(fmaf(s[i], p.scale_log2, na));
-              s[i + 1] = ex2_ftz(fmaf(s[i + 1], p.scale_log2, na));
-              s[i + 2] = ex2_ftz(fmaf(s[i + 2], p.scale_log2, nb));
-              s[i + 3] = ex2_ftz(fmaf(s[i + 3], p.scale_log2, nb));
-              sa += s[i] + s[i + 1];
-              sb += s[i + 2] + s[i + 3];
+                for (int t = 0; t < RT; ++t)
+                  if (key >= lim[t]) x[t][i] = -INFINITY;
+              }
             }
-            la = la * aa + sa;
-            lb = lb * ab + sb;
+            // the row's maximum (E4M3: of the weight p s, s by its exponent)
+            float top[RT];
+            float lift[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              lift[i] = F8 ? (float)((int)(__float_as_uint(sc[i]) >> 23) - 127) : 0.f;
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+              float y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = F8 ? x[t][i] + lift[i] : x[t][i];
+              top[t] = fmax3(fmax3(y[0], y[1], y[2]), fmax3(y[3], y[4], y[5]), fmaxf(y[6], y[7]));
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+              for (int t = 0; t < RT; ++t)
+                top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], o));
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+              if (!F8) top[t] *= p.scale_log2;
+              // the reference moves only when it grows by more than 2^kRescaleLog2
+              // (any reference gives the same softmax)
+              if (m[t] == -INFINITY) {
+                m[t] = top[t];
+              } else if (top[t] > m[t] + kRescaleLog2<F8>) {
+                alpha[t] = ex2_ftz(m[t] - top[t]);
+                m[t] = top[t];
+              }
+              const float neg = m[t] == -INFINITY ? 0.f : kTargetLog2<F8> - m[t];
+              float sum = 0.f;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                x[t][i] = ex2_ftz(F8 ? x[t][i] + neg : fmaf(x[t][i], p.scale_log2, neg));
+                sum += x[t][i];
+              }
+              l[t] = l[t] * alpha[t] + sum;
+            }
           }
           // PV(g - 2) has read this half of P, and what was published with it
           if (g >= 2 && !(ok = wait(&tail->pv_done[g & 1], (g >> 1) - 1))) break;
           if (scores) {
-            const int mi = lane >> 3;  // the 8x8 matrix whose row this lane addresses
-            const int row = w4 * 16 + (mi & 1) * 8 + (lane & 7);
+            if constexpr (F8) {
+              // weights p s as hi + lo, 32 bytes each of the row's half
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int gran = (g & 1) * 4 + 2 * i + (mi >> 1);
-              stmatrix_x4(ps + row * 128 + ((gran ^ (row & 7)) << 4),
-                          pack_bf16(s[8 * i], s[8 * i + 1]), pack_bf16(s[8 * i + 2], s[8 * i + 3]),
-                          pack_bf16(s[8 * i + 4], s[8 * i + 5]),
-                          pack_bf16(s[8 * i + 6], s[8 * i + 7]));
+              for (int t = 0; t < RT; ++t) {
+                uint8_t* prow = ps + row[t] * 128 + (lane & 3) * 2;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float a = x[t][2 * i] * sc[2 * i], b = x[t][2 * i + 1] * sc[2 * i + 1];
+                  const uint32_t hi = e4m3_pair(a, b);
+                  float ha, hb;
+                  e4m3x2_to_f32((uint16_t)hi, ha, hb);
+                  const uint32_t lo = e4m3_pair(a - ha, b - hb);
+                  const int gran = (g & 1) * 4 + (i >> 1);  // 16 keys a granule
+                  uint8_t* at = prow + (i & 1) * 8;
+                  *reinterpret_cast<uint16_t*>(at + ((gran ^ (row[t] & 7)) << 4)) = (uint16_t)hi;
+                  *reinterpret_cast<uint16_t*>(at + (((gran + 2) ^ (row[t] & 7)) << 4)) =
+                      (uint16_t)lo;
+                }
+              }
+            } else {
+              const int mi = lane >> 3;  // the 8x8 matrix whose row this lane addresses
+              const int prow = w4 * 16 + (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int gran = (g & 1) * 4 + 2 * i + (mi >> 1);
+                stmatrix_x4(ps + prow * 128 + ((gran ^ (prow & 7)) << 4),
+                            pack_bf16(x[0][4 * i], x[0][4 * i + 1]),
+                            pack_bf16(x[RT - 1][4 * i], x[RT - 1][4 * i + 1]),
+                            pack_bf16(x[0][4 * i + 2], x[0][4 * i + 3]),
+                            pack_bf16(x[RT - 1][4 * i + 2], x[RT - 1][4 * i + 3]));
+              }
             }
           }
-          const bool ask = __any_sync(0xffffffffu, aa < 1.f || ab < 1.f);
-          if (ask && (lane & 3) == 0) {
-            tail->alpha[g & 1][ra] = aa;
-            tail->alpha[g & 1][rb] = ab;
+          const bool ask = __any_sync(0xffffffffu, alpha[0] < 1.f || alpha[RT - 1] < 1.f);
+          // (stacked: a rescale takes the rows of two warps, either may have asked)
+          if (scores && (ask || RT == 1) && (lane & 3) == 0) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) tail->alpha[g & 1][row[t]] = alpha[t];
           }
           if (lane == 0) tail->ask[g & 1][w4] = ask;
           if (key0 + KT > pc.n_keys) {
@@ -653,27 +881,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             // unwritten cells): zero them, so that P = 0 never meets a NaN (S of
             // this tile has read them: every warp waits for it)
             if (!scores && !(ok = wait(&tail->s_full[g % kSBufs], g / kSBufs))) break;
-            constexpr int kCols = L / 64;  // chunks: the thread's is (tid / 8) % kCols
+            // the thread's chunk is (tid / 8) % kCols
             uint8_t* ks = smem + S::kOffK + (g % kStages) * S::kStage +
                           ((tid >> 3) & (kCols - 1)) * kChunk + (tid & 7) * 16;
-            for (int n = pc.n_keys - key0 + tid / (8 * kCols); n < KT; n += 16 / kCols)
-              *reinterpret_cast<uint4*>(ks + n * 128) = make_uint4(0, 0, 0, 0);
+            for (int i = pc.n_keys - key0 + tid / (8 * kCols); i < KT; i += 16 / kCols)
+              *reinterpret_cast<uint4*>(ks + i * 128) = make_uint4(0, 0, 0, 0);
           }
           if (j == pc.k1 - 1 && scores) {
             // the piece's sums, before the arrival that its output waits behind
-            float ua = la, ub = lb;
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-              ua += __shfl_xor_sync(0xffffffffu, ua, o);
-              ub += __shfl_xor_sync(0xffffffffu, ub, o);
-            }
-            if ((lane & 3) == 0) {
-              tail->l[pieces & 1][ra] = ua > 0.f ? 1.f / ua : 0.f;
-              tail->l[pieces & 1][rb] = ub > 0.f ? 1.f / ub : 0.f;
-              if (pc.slot >= 0) {
-                float2* ml = p.part_ml + (int64_t)(2 * cta + pc.slot) * NR;
-                ml[ra] = make_float2(ma, ua);
-                ml[rb] = make_float2(mb, ub);
+            for (int t = 0; t < RT; ++t) {
+              float u = l[t];
+#pragma unroll
+              for (int o = 1; o < 4; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+              if ((lane & 3) == 0) {
+                tail->l[n & 1][row[t]] = u > 0.f ? 1.f / u : 0.f;
+                if (pc.slot >= 0)
+                  p.part_ml[(int64_t)(2 * cta + pc.slot) * NR + row[t]] = make_float2(m[t], u);
               }
             }
           }
@@ -684,44 +908,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
 
-        if (pc.k0 >= pc.k1) {  // no key for any row: sums of zero, which the join skips
-          if (scores && pc.slot >= 0 && (lane & 3) == 0) {
-            float2* ml = p.part_ml + (int64_t)(2 * cta + pc.slot) * NR;
-            ml[ra] = ml[rb] = make_float2(-INFINITY, 0.f);
-          }
-          continue;
-        }
         // ---- the piece's rows: normalised to out, or a partial
         if (!(ok = wait(&tail->pv_done[(g - 1) & 1], (g - 1) >> 1))) break;
         tc::fence_after_sync();
-        const int64_t out_row = (int64_t)walk.q.q_begin * p.Hq + row0;
         if (pc.slot < 0) {
           // lane = dim, register = row: three exchanges between lanes whose
           // numbers differ in one bit leave 8 dims of two rows in each lane
-          __nv_bfloat16* orow = p.out + out_row * L + w4 * 32 + (lane >> 3) * 8;
+          __nv_bfloat16* orow = p.out + (int64_t)pc.row * L + w4 * 32 + (lane >> 3) * 8;
 #pragma unroll 1
           for (int c = 0; c < NR; c += 16) {
             if (c >= pc.rows) break;
+            uint32_t o[kBlocks][16];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) tmem_ld16(tmem + lanes + b * NR + c, o[b]);
             float inv[16];
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
               *reinterpret_cast<float4*>(inv + i) =
-                  *reinterpret_cast<const float4*>(&tail->l[pieces & 1][c + i]);
+                  *reinterpret_cast<const float4*>(&tail->l[n & 1][c + i]);
+            tc::tmem_wait_ld();
             // row of the lane's first output: bit 0, 1, 2 of the lane pick bits
             // 3, 2, 1 of the row
-            const int row = c + (lane & 1) * 8 + (lane & 2) * 2 + ((lane & 4) >> 1);
-#pragma unroll 1
-            for (int m = 0; m < kBlocks; ++m) {
-              uint32_t o[16];
-              tmem_ld16(tmem + lanes + m * NR + c, o);
-              tc::tmem_wait_ld();
+            const int r0 = c + (lane & 1) * 8 + (lane & 2) * 2 + ((lane & 4) >> 1);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
               uint32_t w[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {  // lane pairs: bf16 of two dims, 8 rows each
-                const float x = __uint_as_float(o[i]) * inv[i];
-                const float y = __uint_as_float(o[i + 8]) * inv[i + 8];
-                const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
-                w[i] = (lane & 1) ? pack_bf16(got, y) : pack_bf16(x, got);
+                const float u = __uint_as_float(o[b][i]) * inv[i];
+                const float v = __uint_as_float(o[b][i + 8]) * inv[i + 8];
+                const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? u : v, 1);
+                w[i] = (lane & 1) ? pack_bf16(got, v) : pack_bf16(u, got);
               }
               uint32_t u[4][2];
 #pragma unroll
@@ -735,8 +952,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool up = (lane & 4) != 0;
                 const uint32_t g0 = __shfl_xor_sync(0xffffffffu, up ? u[i][0] : u[i + 2][0], 4);
                 const uint32_t g1 = __shfl_xor_sync(0xffffffffu, up ? u[i][1] : u[i + 2][1], 4);
-                if (row + i < pc.rows)
-                  *reinterpret_cast<uint4*>(orow + (int64_t)(row + i) * L + m * 128) =
+                if (r0 + i < pc.rows)
+                  *reinterpret_cast<uint4*>(orow + (int64_t)(r0 + i) * L + b * 128) =
                       up ? make_uint4(g0, g1, u[i + 2][0], u[i + 2][1])
                          : make_uint4(u[i][0], u[i][1], g0, g1);
               }
@@ -747,24 +964,108 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < NR; c += 16) {
             if (c >= pc.rows) break;
-#pragma unroll 1
-            for (int m = 0; m < kBlocks; ++m) {
-              uint32_t o[16];
-              tmem_ld16(tmem + lanes + m * NR + c, o);
-              tc::tmem_wait_ld();
+            uint32_t o[kBlocks][16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i)  // (rows past the unit's are scratch)
-                prow[(c + i) * L + m * 128] = __uint_as_float(o[i]);
-            }
+            for (int b = 0; b < kBlocks; ++b) tmem_ld16(tmem + lanes + b * NR + c, o[b]);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)  // (rows past the tile's are scratch)
+                prow[(c + i) * L + b * 128] = __uint_as_float(o[b][i]);
           }
         }
-        ++pieces;
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tail->o_empty);
+        if (lane == 0) {
+          mbar_arrive(&tail->o_empty);
+          release(n);
+        }
+      }
+      if (!ok) tail->abort = 1;
+    } else if constexpr (F8) {
+      // ------------------------------------------------------- query as E4M3
+      const int w4 = warp - 8;
+      bool ok = true;
+      constexpr int kPer = L / 32;               // dims of a lane: 16 or 8
+      for (int n = 0;; ++n) {
+        const Piece pc = piece(n, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok || pc.r < 0) break;
+        if (n > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&tail->q_empty, (n - 1) & 1, p.err))))
+          break;
+#pragma unroll 2
+        for (int i = 0; i < NR / 4; ++i) {
+          const int row = i * 4 + w4;
+          // (rows past the tile's are zeros)
+          uint4 v[kPer / 8], r = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < kPer / 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
+          if (row < pc.rows) {
+            const __nv_bfloat16* src = p.q + (int64_t)(pc.row + row) * (L + kRope);
+#pragma unroll
+            for (int k = 0; k < kPer / 8; ++k)
+              v[k] = __ldg(reinterpret_cast<const uint4*>(src + lane * kPer) + k);
+            if (lane < 8) r = __ldg(reinterpret_cast<const uint4*>(src + L) + lane);
+          }
+          float f[kPer], amax = 0.f;
+#pragma unroll
+          for (int k = 0; k < kPer / 8; ++k) bf16x8_to_f32(v[k], f + 8 * k);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) amax = fmaxf(amax, fabsf(f[k]));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // 2^e brings the largest magnitude to [2^7, 2^8); exact
+          const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+          const int e = amax > 0.f ? min(100, max(-120, 7 - ex)) : 0;
+          const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+          uint32_t hi[kPer / 4], lo[kPer / 4];
+#pragma unroll
+          for (int k = 0; k < kPer / 4; ++k) {
+            hi[k] = lo[k] = 0u;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float x = f[4 * k + 2 * b] * up, y = f[4 * k + 2 * b + 1] * up;
+              const uint32_t h = e4m3_pair(x, y);
+              float hx, hy;
+              e4m3x2_to_f32((uint16_t)h, hx, hy);
+              hi[k] |= h << (16 * b);
+              lo[k] |= e4m3_pair(x - hx, y - hy) << (16 * b);
+            }
+          }
+          const int qrow = kStacked ? (row >> 3) * 16 + (row & 7) : row;
+          const int lrow = kStacked ? qrow + 8 : row;
+          const int block = lane * kPer / 128, byte = lane * kPer % 128;
+          auto place = [&](int off, int at) {
+            return smem + off + at * 128 + (((byte >> 4) ^ (at & 7)) << 4) + (byte & 15);
+          };
+          uint8_t* dh = place(block * S::kQChunk, qrow);
+          uint8_t* dl = place(((kStacked ? 0 : kCols) + block) * S::kQChunk, lrow);
+          if constexpr (kPer == 16) {
+            *reinterpret_cast<uint4*>(dh) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint2*>(dh) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dl) = make_uint2(lo[0], lo[1]);
+          }
+          if (lane < 8)
+            *reinterpret_cast<uint4*>(smem + S::kOffQR + qrow * 128 +
+                                      ((lane ^ (qrow & 7)) << 4)) = r;
+          if (lane == 0)
+            tail->q_scale[n % kPieces][row] = __uint_as_float((uint32_t)(127 - e) << 23);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&tail->q_full);
+          release(n);
+        }
       }
       if (!ok) tail->abort = 1;
     }
+  } else if (threadIdx.x == 64) {
+    p.joins[cta] = LatentJoin{};
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -774,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the partials of the units cut at CTA boundaries: grid (attention CTAs,
+// Joins the partials of the row tiles cut at group boundaries: grid (attention CTAs,
 // row groups), one warp per row. o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
 constexpr int kJoinWarps = 8;
 
@@ -847,20 +1148,21 @@ size_t scratch_bytes(int n, int NR, int L) {
          (size_t)2 * n * NR * L * sizeof(float);
 }
 
-// Rows of `chunks` times 64 bf16 columns, row_bytes apart, as [chunk][row][64]:
-// one box is `box_rows` rows of `box_chunks` chunks, chunk after chunk in shared
-// memory, each 128-byte swizzled.
-bool encode_chunks(CUtensorMap* m, const void* base, int chunks, int64_t row_bytes, int64_t rows,
-                   int box_rows, int box_chunks) {
+// Rows of `chunks` times 128 bytes (64 bf16 or 128 codes), row_bytes apart, as
+// [chunk][row][128 bytes]: one box is `box_rows` rows of `box_chunks` chunks, chunk
+// after chunk in shared memory, each 128-byte swizzled.
+bool encode_chunks(CUtensorMap* m, const void* base, bool codes, int chunks, int64_t row_bytes,
+                   int64_t rows, int box_rows, int box_chunks) {
   auto encode = tensor_map_encoder();
   if (!encode) return false;
-  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)chunks};
+  const cuuint32_t cols = codes ? 128 : 64;
+  const cuuint64_t dims[3] = {cols, (cuuint64_t)rows, (cuuint64_t)chunks};
   const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, 128};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
+  const cuuint32_t box[3] = {cols, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
   const cuuint32_t es[3] = {1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-                es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return encode(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -877,22 +1179,24 @@ bool encode_rope(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int L, int NR>
+template <int L, int NR, bool F8>
 pa_status launch(const LatentParams& p, const void* q, const pa_latent_pool* pool, int grid,
                  cudaStream_t s) {
-  using S = Smem<L, NR>;
+  using S = Smem<L, NR, F8>;
   CUtensorMap tq, tc, tr;
   const int64_t cells = (int64_t)pool->num_blocks * pool->block_size;
   const int box_rows = std::min(pool->block_size, KT);
-  if (!encode_chunks(&tq, q, L / 64 + 1, (L + kRope) * 2, (int64_t)p.T * p.Hq, NR, L / 64 + 1) ||
-      !encode_chunks(&tc, pool->latent, L / 64, L * 2, cells, box_rows,
-                     box_rows == KT ? L / 64 : 1) ||
+  // (E4M3: the queries are converted, not copied)
+  if (!encode_chunks(&tq, q, false, L / 64 + 1, (L + kRope) * 2, (int64_t)p.T * p.Hq, NR,
+                     L / 64 + 1) ||
+      !encode_chunks(&tc, pool->latent, F8, S::kCols, S::kCols * 128, cells, box_rows,
+                     box_rows == KT ? S::kCols : 1) ||
       !encode_rope(&tr, pool->rope, cells, box_rows))
     return PA_ERR_CUDA;
-  if (cudaFuncSetAttribute(latent_attn_kernel<L, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           S::kAlloc) != cudaSuccess)
+  if (cudaFuncSetAttribute(latent_attn_kernel<L, NR, F8>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc) != cudaSuccess)
     return PA_ERR_CUDA;
-  latent_attn_kernel<L, NR><<<grid, kThreads, S::kAlloc, s>>>(tq, tc, tr, p);
+  latent_attn_kernel<L, NR, F8><<<grid, S::kThreads, S::kAlloc, s>>>(tq, tc, tr, p);
   pa_status st = launch_status();
   if (st != PA_OK || grid == p.lanes) return st;  // one group cuts nothing
   cudaLaunchConfig_t cfg{};
@@ -914,7 +1218,8 @@ pa_status launch(const LatentParams& p, const void* q, const pa_latent_pool* poo
 
 extern "C" size_t pa_latent_workspace_size(int32_t num_q_heads, int32_t latent_dim) {
   if (num_q_heads <= 0 || (latent_dim != 256 && latent_dim != 512)) return 0;
-  return pa::scratch_bytes(std::min(pa::num_sms(), pa::kLatentMaxCtas), pa::kLatentRows, latent_dim);
+  return pa::scratch_bytes(std::min(pa::num_sms(), pa::kLatentMaxCtas), pa::kLatentRows,
+                           latent_dim);
 }
 
 extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* query_start_loc,
@@ -945,7 +1250,6 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
     if (seq < ql || (int64_t)seq > (int64_t)max_blocks * pool->block_size) return PA_ERR_INVALID;
   }
   if (T == 0) return PA_OK;
-  if (pool->dtype != PA_KV_BF16) return PA_ERR_UNSUPPORTED;
   // rows are addressed by 32-bit tensor-map coordinates
   if ((int64_t)T * Hq > INT32_MAX - pa::kLatentRows) return PA_ERR_UNSUPPORTED;
 
@@ -986,6 +1290,9 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
   p.qsl = query_start_loc;
   p.seq_lens = seq_lens;
   p.block_tables = block_tables;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.latent = static_cast<const uint8_t*>(pool->latent);
+  p.rope = static_cast<const uint8_t*>(pool->rope);
   p.scales = pool->scales;
   p.T = T;
   p.R = R;
@@ -1006,11 +1313,16 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
   p.err = pa::error_word();
   if (!p.err) return PA_ERR_CUDA;
   cudaStream_t s = pa::as_stream(stream);
-  auto go = [&](auto l) {
+  auto go = [&](auto l, auto f8) {
     constexpr int kL = decltype(l)::value;
-    return NR == 16   ? pa::launch<kL, 16>(p, q, pool, grid, s)
-           : NR == 32 ? pa::launch<kL, 32>(p, q, pool, grid, s)
-                      : pa::launch<kL, 64>(p, q, pool, grid, s);
+    constexpr bool kF8 = decltype(f8)::value;
+    return NR == 16   ? pa::launch<kL, 16, kF8>(p, q, pool, grid, s)
+           : NR == 32 ? pa::launch<kL, 32, kF8>(p, q, pool, grid, s)
+                      : pa::launch<kL, 64, kF8>(p, q, pool, grid, s);
   };
-  return L == 512 ? go(std::integral_constant<int, 512>{}) : go(std::integral_constant<int, 256>{});
+  const auto L512 = std::integral_constant<int, 512>{};
+  const auto L256 = std::integral_constant<int, 256>{};
+  if (pool->dtype == PA_KV_FP8_E4M3)
+    return L == 512 ? go(L512, std::true_type{}) : go(L256, std::true_type{});
+  return L == 512 ? go(L512, std::false_type{}) : go(L256, std::false_type{});
 }

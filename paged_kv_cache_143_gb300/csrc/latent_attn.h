@@ -38,6 +38,9 @@ struct LatentJoin {       // what the join needs of a CTA's first piece
 };
 
 struct LatentParams {
+  const __nv_bfloat16* q;      // [T * Hq][L + 64]
+  const uint8_t* latent;       // the pool's cells
+  const uint8_t* rope;
   __nv_bfloat16* out;          // [T * Hq][L]
   const int32_t* qsl;          // [R+1]
   const int32_t* seq_lens;     // [R]

@@ -136,6 +136,11 @@ __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gmem_src, u
       : "memory");
 }
 
+// Asks L2 for `bytes` contiguous bytes (address and size multiples of 16).
+__device__ __forceinline__ void prefetch_l2(const void* gmem, unsigned bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gmem), "r"(bytes) : "memory");
+}
+
 // 16 bytes global -> shared through L2 only (cp.async.cg), tracked by the
 // executing thread's async-copy groups.
 __device__ __forceinline__ void cp_async16(void* smem_dst, const void* gmem_src) {

@@ -8,6 +8,13 @@ Tolerance of an output element o = sum_n p_n v_n:
     S = scale * sum |q||k| the error is below 2^-20 S (576 terms, fp32
     accumulation), and a score error d moves o by at most 2 d sum p |v|;
   * one rounding of o to bf16: 2^-8 |o|.
+On E4M3 pools, besides:
+  * the latent part of q is hi + lo in E4M3 after a power of two that brings the
+    row's maximum to [2^7, 2^8): at most half of E4M3's smallest step, 2^-10, off,
+    so 2^-17 of the row's maximum, and a score by scale 2^-17 max|q| sum |c|;
+  * the weights p_n s_n are hi + lo in E4M3, within 2^-4 2^-4 = 2^-8 relative
+    (the count above) or 2^-10 absolute where the row's largest weight is at
+    least 2^4: 2^-14 max_n(p_n s_n) for every key, on codes v_n / s_n.
 The bound below sums these per element, from the reference's own p and v."""
 import numpy as np
 import pytest
@@ -73,7 +80,16 @@ class Batch:
             size = np.einsum("thn,nl->thl", p, np.abs(lat[at]))
             k = np.concatenate((lat[at], rot[at]), -1)
             s_mag = self.scale * np.einsum("thd,nd->thn", np.abs(q), np.abs(k)).max(-1)[..., None]
-            tol = size * (p_half + 2 * 2.0 ** -20 * s_mag) + p_half * np.abs(want) + 1e-30
+            s_err = 2.0 ** -20 * s_mag
+            floor = 0.0
+            if self.pool.scales is not None:
+                s = ref.f64(self.pool.scales).reshape(-1)[at]
+                q_max = np.abs(q[..., :self.L]).max(-1)[..., None]
+                s_err = s_err + self.scale * 2.0 ** -17 * q_max * np.abs(lat[at]).sum(-1).max()
+                seen = (p > 0).astype(np.float64)
+                floor = 2.0 ** -14 * (p * s).max(-1)[..., None] * np.einsum(
+                    "thn,nl->thl", seen, np.abs(lat[at]) / s[:, None])
+            tol = size * (p_half + 2 * s_err) + floor + p_half * np.abs(want) + 1e-30
             got = ref.f64(out[a:b])
             assert np.isfinite(got).all()
             err = np.abs(got - want)
