@@ -38,13 +38,16 @@
 // Every wait is bounded; a timeout sets the error word and the CTA unwinds.
 //
 // E4M3 pools: both products take the codes as they are stored (kind::f8f6f4),
-// nothing is widened. The other operand is a sum of two E4M3 numbers, hi + lo:
-//   q 2^e = hi + lo, 2^e bringing the row's largest magnitude to [2^7, 2^8). A
-//     bf16 number has 8 significant bits and each part 4, so the sum is exact
-//     down to E4M3's smallest step, 2^-17 of the row's maximum.
-//   p s_n = hi + lo for key n of scale s_n, below 2^-8 of the weight off (as
-//     bf16), no less than 2^-14 of the row's largest weight. The reference
-//     maximum is that of p s_n, placed at 2^4, so weights stay below 2^8.
+// nothing is widened. The other operand is a sum of 8-bit numbers:
+//   q 2^e = hi + lo in E4M3, 2^e bringing the row's largest magnitude to
+//     [2^7, 2^8). A bf16 number has 8 significant bits and each part 4, so the sum
+//     is exact down to half of E4M3's smallest step, 2^-17 of the row's maximum.
+//   p s_n, the weight of key n of scale s_n, = three parts in E5M2 (3 bits each):
+//     below 2^-9 of the weight off, or 2^-17 absolute. The reference maximum is
+//     that of p s_n, placed at 2^7, so that is 2^-24 of the row's largest weight:
+//     a long context's many small weights keep their share beside one large one.
+//     (Two E4M3 parts would do for weights within 2^-8 of the largest, but lose
+//     every weight below 2^-14 of it; PV is a fifth of the tensor time.)
 // For 32 rows or fewer the parts of q are stacked in the 64 rows of S: the lane
 // that reads a row's hi scores reads its lo scores too. The rotary part of q
 // and k stays bf16 and has S columns of its own, since s_n does not apply to it.
@@ -71,9 +74,9 @@ constexpr uint32_t kTmemS = 256;   // S buffers at columns 256, 288, 320, 352
 constexpr uint32_t kTmemR = 384;   // E4M3: the rotary part of S at 384 ..
 constexpr int kSBufs = 4, kMaxStages = 10, kPieces = 4;
 // The reference maximum moves when it grows by more than 2^kRescaleLog2; weights
-// of the maximum are placed at 2^kTargetLog2 (E4M3 weights must stay below 448).
-template <bool F8> constexpr float kRescaleLog2 = F8 ? 3.f : 8.f;
-template <bool F8> constexpr float kTargetLog2 = F8 ? 4.f : 0.f;
+// of the maximum are placed at 2^kTargetLog2 (E5M2 weights must stay below 57344).
+template <bool F8> constexpr float kRescaleLog2 = F8 ? 7.f : 8.f;
+template <bool F8> constexpr float kTargetLog2 = F8 ? 7.f : 0.f;
 
 template <int L, int NR, bool F8>
 struct Smem {
@@ -88,7 +91,10 @@ struct Smem {
   static constexpr int kOffQR = kQParts * kCols * kQChunk;
   static constexpr int kQBytes = kOffQR + kQChunk;
   static constexpr int kStage = (kCols + 1) * kChunk; // the last chunk is the rotary part
-  static constexpr int kPBytes = NR * 128;            // two tiles of P side by side
+  // P of two tiles: bf16 side by side in 128-byte rows; E5M2 in rows of their own
+  // (three parts of 32 bytes)
+  static constexpr int kPTile = F8 ? NR * 128 : 64;
+  static constexpr int kPBytes = F8 ? 2 * kPTile : NR * 128;
   static constexpr int kTail = F8 ? 5120 : 2048;      // barriers, pieces, row statistics
   static constexpr int kFit = (232448 - 1024 - kTail - kQBytes - kPBytes) / kStage;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -191,9 +197,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Two fp32 to E4M3 (nearest even), x in the low byte, and what they stand for.
+// Two fp32 to E4M3 or E5M2 (nearest even), x in the low byte.
 __device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e5m2_pair(float x, float y) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E5M2);
+}
+// What two E5M2 codes stand for: the high bytes of two f16 numbers.
+__device__ __forceinline__ float2 e5m2_values(uint32_t pair) {
+  const uint32_t h = __byte_perm(pair, 0u, 0x1404);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // ------------------------------------------------------------ the flat space
@@ -557,7 +571,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         }
         p.joins[cta] = join;
         constexpr uint32_t idesc = tc::idesc_16bit_f32(128, NR, true, false, false);
-        constexpr uint32_t idesc8 = tc::idesc_e4m3_f32(128, NR) | (1u << 15);  // A MN-major
+        // A the codes, MN-major (bit 15); B E5M2 (type 1 in bits 10..)
+        constexpr uint32_t idesc8 = tc::idesc_e4m3_f32(128, NR) | (1u << 15) | (1u << 10);
         const uint64_t p_desc = tc::smem_desc_sw128(smem + S::kOffP, 16, 1024);
         const uint64_t v_desc = tc::smem_desc_sw128(smem + S::kOffK, kChunk, 1024);
         int g = 0, st = 0, fixes = 0;
@@ -582,14 +597,14 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             }
             tc::fence_after_sync();
             const uint64_t vs = tc::desc_at(v_desc, st * S::kStage);
-            const uint64_t ps = tc::desc_at(p_desc, (g & 1) * 64);
+            const uint64_t ps = tc::desc_at(p_desc, (g & 1) * S::kPTile);
             const bool add = j > pc.k0;
-            // two products per 128-dim block: bf16, 16 keys each; E4M3, the hi
-            // and the lo weights of all 32 keys
+            // products per 128-dim block: bf16, two of 16 keys each; codes, three,
+            // one for each part of the weights of all 32 keys
 #pragma unroll
             for (int m = 0; m < kBlocks; ++m)
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
+              for (int k = 0; k < (F8 ? 3 : 2); ++k) {
                 const uint64_t pb = tc::desc_at(ps, k * 32);
                 if (F8)
                   tc::mma_e4m3_ss(tmem + m * NR, tc::desc_at(vs, m * kChunk), pb, idesc8,
@@ -837,22 +852,24 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           if (g >= 2 && !(ok = wait(&tail->pv_done[g & 1], (g >> 1) - 1))) break;
           if (scores) {
             if constexpr (F8) {
-              // weights p s as hi + lo, 32 bytes each of the row's half
+              // weights p s in three parts, 32 bytes of the row each
 #pragma unroll
               for (int t = 0; t < RT; ++t) {
-                uint8_t* prow = ps + row[t] * 128 + (lane & 3) * 2;
+                uint8_t* prow = ps + (g & 1) * S::kPTile + row[t] * 128 + (lane & 3) * 2;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const float a = x[t][2 * i] * sc[2 * i], b = x[t][2 * i + 1] * sc[2 * i + 1];
-                  const uint32_t hi = e4m3_pair(a, b);
-                  float ha, hb;
-                  e4m3x2_to_f32((uint16_t)hi, ha, hb);
-                  const uint32_t lo = e4m3_pair(a - ha, b - hb);
-                  const int gran = (g & 1) * 4 + (i >> 1);  // 16 keys a granule
+                  float a = x[t][2 * i] * sc[2 * i], b = x[t][2 * i + 1] * sc[2 * i + 1];
                   uint8_t* at = prow + (i & 1) * 8;
-                  *reinterpret_cast<uint16_t*>(at + ((gran ^ (row[t] & 7)) << 4)) = (uint16_t)hi;
-                  *reinterpret_cast<uint16_t*>(at + (((gran + 2) ^ (row[t] & 7)) << 4)) =
-                      (uint16_t)lo;
+#pragma unroll
+                  for (int part = 0; part < 3; ++part) {
+                    const uint32_t code = e5m2_pair(a, b);
+                    const int gran = part * 2 + (i >> 1);  // 16 keys a granule
+                    *reinterpret_cast<uint16_t*>(at + ((gran ^ (row[t] & 7)) << 4)) =
+                        (uint16_t)code;
+                    const float2 v = e5m2_values(code);
+                    a -= v.x;
+                    b -= v.y;
+                  }
                 }
               }
             } else {

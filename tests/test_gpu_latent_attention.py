@@ -12,9 +12,9 @@ On E4M3 pools, besides:
   * the latent part of q is hi + lo in E4M3 after a power of two that brings the
     row's maximum to [2^7, 2^8): at most half of E4M3's smallest step, 2^-10, off,
     so 2^-17 of the row's maximum, and a score by scale 2^-17 max|q| sum |c|;
-  * the weights p_n s_n are hi + lo in E4M3, within 2^-4 2^-4 = 2^-8 relative
-    (the count above) or 2^-10 absolute where the row's largest weight is at
-    least 2^4: 2^-14 max_n(p_n s_n) for every key, on codes v_n / s_n.
+  * the weights p_n s_n are three parts in E5M2, within 2^-9 relative (below the
+    count above) or half of its smallest step, 2^-17, where the row's largest
+    weight is at least 2^7: 2^-24 max_n(p_n s_n) for every key, on codes v_n / s_n.
 The bound below sums these per element, from the reference's own p and v."""
 import numpy as np
 import pytest
@@ -87,7 +87,7 @@ class Batch:
                 q_max = np.abs(q[..., :self.L]).max(-1)[..., None]
                 s_err = s_err + self.scale * 2.0 ** -17 * q_max * np.abs(lat[at]).sum(-1).max()
                 seen = (p > 0).astype(np.float64)
-                floor = 2.0 ** -14 * (p * s).max(-1)[..., None] * np.einsum(
+                floor = 2.0 ** -24 * (p * s).max(-1)[..., None] * np.einsum(
                     "thn,nl->thl", seen, np.abs(lat[at]) / s[:, None])
             tol = size * (p_half + 2 * s_err) + floor + p_half * np.abs(want) + 1e-30
             got = ref.f64(out[a:b])
@@ -151,6 +151,25 @@ def test_rising_scores_rescale_every_tile(cuda_device, fp8):
     slots = torch.from_numpy(ref.slots_of(b.tab, 0, n, 16)).to(dev)
     pa.write_latent(b.pool, c, (ramp * one).bfloat16(), slots)
     b.q[..., 256:] = 0.25
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_one_large_weight_beside_many_small_ones(cuda_device, fp8):
+    """A first key that holds a third of the weight, and 20000 others, each
+    2^-13 of it and less, that hold the rest."""
+    dev = cuda_device
+    n = 20000
+    b = Batch([n], [1], 16, 512, 16, fp8, dev, seed=14)
+    rng = np.random.default_rng(15)
+    c = torch.from_numpy(rng.standard_normal((n, 512)).astype(np.float32)).to(dev).bfloat16()
+    rope = torch.zeros(n, 64, device=dev)
+    rope[0] = 1.0
+    pa.write_latent(b.pool, c, rope.bfloat16(), torch.from_numpy(ref.slots_of(b.tab, 0, n, 16)).to(dev))
+    b.q.mul_(0.02)
+    b.q[..., 512:] = float(np.log(n / 2.0) / 64 / b.scale)
     b.run()
     assert pa.get_error() == pa.PA_OK
     b.check()
