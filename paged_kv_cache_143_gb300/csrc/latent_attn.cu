@@ -67,12 +67,10 @@ namespace pa {
 namespace {
 
 constexpr int kRope = 64;
-constexpr int KT = kLatentKeys;
-constexpr int kChunk = KT * 128;   // 128 bytes of each row of a key tile: 64 bf16 or 128 codes
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 256;   // S buffers at columns 256, 288, 320, 352
-constexpr uint32_t kTmemR = 384;   // E4M3: the rotary part of S at 384 ..
-constexpr int kSBufs = 4, kMaxStages = 10, kPieces = 4;
+constexpr uint32_t kTmemS = 256;   // S buffers from column 256 on
+constexpr uint32_t kTmemR = 384;   // E4M3: the rotary part of S from 384 on
+constexpr int kMaxStages = 8, kPieces = 4;
 // The reference maximum moves when it grows by more than 2^kRescaleLog2; weights
 // of the maximum are placed at 2^kTargetLog2 (E5M2 weights must stay below 57344).
 template <bool F8> constexpr float kRescaleLog2 = F8 ? 7.f : 8.f;
@@ -81,6 +79,9 @@ template <bool F8> constexpr float kTargetLog2 = F8 ? 7.f : 0.f;
 template <int L, int NR, bool F8>
 struct Smem {
   static constexpr int kThreads = F8 ? 384 : 256;
+  static constexpr int KT = latent_tile_keys(L, F8);
+  static constexpr int kChunk = KT * 128;             // 128 bytes of each row of a key tile
+  static constexpr int kSBufs = F8 ? 2 : 4;           // S buffers of KT columns
   static constexpr bool kStacked = F8 && NR <= 32;    // hi and lo rows of q in one S
   static constexpr int kCols = F8 ? L / 128 : L / 64; // 128-byte chunks of a latent row
   static constexpr int kQRows = kStacked ? 2 * NR : NR;
@@ -91,10 +92,15 @@ struct Smem {
   static constexpr int kOffQR = kQParts * kCols * kQChunk;
   static constexpr int kQBytes = kOffQR + kQChunk;
   static constexpr int kStage = (kCols + 1) * kChunk; // the last chunk is the rotary part
-  // P of two tiles: bf16 side by side in 128-byte rows; E5M2 in rows of their own
-  // (three parts of 32 bytes)
-  static constexpr int kPTile = F8 ? NR * 128 : 64;
-  static constexpr int kPBytes = F8 ? 2 * kPTile : NR * 128;
+  // P of two tiles in 128-byte rows, a tile's part (bf16: all of it) in 64 bytes
+  // of a row (bf16 with 64 keys: 128); part `i` of tile g starts at p_part
+  static constexpr int kPartBytes = F8 ? KT : KT * 2;
+  static constexpr int kPartsP = F8 ? 3 : 1;
+  static constexpr int kPBytes = 2 * kPartsP * kPartBytes * NR;
+  __host__ __device__ static constexpr int p_part(int g, int part) {
+    const int u = (g & 1) * kPartsP + part;
+    return kPartBytes == 128 ? u * NR * 128 : (u >> 1) * NR * 128 + (u & 1) * 64;
+  }
   static constexpr int kTail = F8 ? 5120 : 2048;      // barriers, pieces, row statistics
   static constexpr int kFit = (232448 - 1024 - kTail - kQBytes - kPBytes) / kStage;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -102,7 +108,7 @@ struct Smem {
   static constexpr int kOffP = kOffK + kStages * kStage;
   static constexpr int kOffTail = kOffP + kPBytes;
   static constexpr int kAlloc = kOffTail + kTail + 1024;  // the base is rounded up to 1024 B
-  static_assert(kStages >= 4, "needs four key tiles in flight");
+  static_assert(kStages * KT >= 128 && kStages >= 3, "needs several key tiles in flight");
   static_assert(kAlloc <= 232448, "dynamic shared memory above the 227 KB per-block limit");
   static_assert(kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzled tiles start on 1024 bytes");
   // S always reads 64 rows of Q: the rows past the tile's are whatever follows
@@ -126,7 +132,7 @@ template <bool F8>
 struct Tail {
   uint64_t q_full, q_empty;
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
-  uint64_t s_full[kSBufs], s_empty[kSBufs];
+  uint64_t s_full[4], s_empty[4];
   uint64_t p_full[2], pv_done[2];
   uint64_t fix, fixed;           // O is to be rescaled for tile fix_tile; it has been
   uint64_t piece_full[kPieces], piece_empty[kPieces];
@@ -134,13 +140,10 @@ struct Tail {
   Piece piece[kPieces];
   alignas(16) float alpha[2][kLatentRows];   // by tile: factors of the rows of a warp that asks
   alignas(16) float l[2][kLatentRows];       // by piece: 1 / sum
-  alignas(16) float scale[F8 ? kMaxStages : 1][KT];      // E4M3: of the stage's keys
+  alignas(16) float scale[F8 ? kMaxStages : 1][64];      // E4M3: of the stage's keys
   float q_scale[F8 ? kPieces : 1][kLatentRows];          // E4M3: 2^-e of the rows
   alignas(4) uint8_t ask[2][4];  // by tile: softmax warps that ask for a rescale
   int32_t fix_tile;
-  int64_t warp_sum[12];
-  int32_t base;        // flat start of the request that holds the CTA's first tile
-  int32_t req;         // that request
   uint32_t tmem;
   int abort;
 };
@@ -154,7 +157,7 @@ __device__ __forceinline__ bool aborted(Tail<F8>* t) {
 // 16 lanes x 32 columns as mma-style fragments: of each 8-column group i,
 // r[4 i], r[4 i + 1] are columns 2 (lane % 4), + 1 of row lane / 4, and
 // r[4 i + 2], r[4 i + 3] those of row lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -214,12 +217,12 @@ __device__ __forceinline__ float2 e5m2_values(uint32_t pair) {
 
 struct Request {
   int32_t q_begin, q_len, seq, rows, keys;  // query rows, key tiles
-  int64_t weight;                           // passes * keys; 0 for one without work
+  int32_t weight;                           // passes * keys; 0 for one without work
 };
 
 // Reads request r; one whose device entries do not fit the buffers has no
 // work (and is reported once).
-template <int NR>
+template <int NR, int KT>
 __device__ __forceinline__ Request load_request(const LatentParams& p, int r, bool report) {
   Request q{};
   q.q_begin = __ldg(p.qsl + r);
@@ -234,12 +237,11 @@ __device__ __forceinline__ Request load_request(const LatentParams& p, int r, bo
   q.rows = q.q_len * p.Hq;  // (T * Hq fits 32 bits)
   q.keys = (q.seq + KT - 1) / KT;
   const int tiles = (q.rows + NR - 1) / NR;
-  q.weight = (int64_t)((tiles + p.lanes - 1) / p.lanes) * q.keys;
+  q.weight = (p.lanes == 1 ? tiles : (tiles + 1) / 2) * q.keys;  // (the host bounds the sum)
   return q;
 }
 
-// (The whole flat space fits 31 bits, so do all positions.)
-template <int NR>
+template <int NR, int KT>
 struct Walk {
   int32_t pos, end, base, r, lane;
   bool loaded;
@@ -252,13 +254,13 @@ struct Walk {
   __device__ bool next(const LatentParams& p, Piece& out) {
     if (pos >= end) return false;
     if (!loaded) {
-      q = load_request<NR>(p, r, false);
+      q = load_request<NR, KT>(p, r, false);
       loaded = true;
     }
-    while (pos - base >= (int32_t)q.weight) {
-      base += (int32_t)q.weight;
+    while (pos - base >= q.weight) {
+      base += q.weight;
       if (++r >= p.R) return false;
-      q = load_request<NR>(p, r, false);
+      q = load_request<NR, KT>(p, r, false);
     }
     const unsigned off = pos - base;
     const int pass = (int)(off / (unsigned)q.keys), tile = pass * p.lanes + lane;
@@ -288,6 +290,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                        const __grid_constant__ CUtensorMap tmap_r, const LatentParams p) {
   using S = Smem<L, NR, F8>;
   constexpr int kThreads = S::kThreads, kStages = S::kStages, kCols = S::kCols;
+  constexpr int KT = S::KT, kChunk = S::kChunk, kSBufs = S::kSBufs;
+  constexpr int VT = KT / 4;                    // scores of a row in one thread
   constexpr bool kStacked = S::kStacked;
   constexpr int kBlocks = L / 128;              // 128-dim blocks of O^T
   constexpr int RT = kStacked ? 1 : 2;          // query rows of a softmax thread
@@ -298,13 +302,23 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Tail<F8>* tail = reinterpret_cast<Tail<F8>*>(smem + S::kOffTail);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = blockIdx.x, group = cta / p.lanes, in_group = cta - group * p.lanes;
-  const int groups = gridDim.x / p.lanes;
+  const int cta = blockIdx.x;
   launch_dependents();  // the join that follows may be scheduled now
 
-  // ---- this group's range: W, then the request that holds tile group * Q
-  int64_t kept_w = 0, kept_before = 0;
-  if ((int)threadIdx.x < p.R) kept_w = load_request<NR>(p, threadIdx.x, cta == 0).weight;
+  // ---- the weights of the requests, summed by thread over consecutive ones (the
+  // ring is still empty). What runs before the first copy is kept short: cold
+  // instructions cost as much as cold data.
+  int32_t* weights = reinterpret_cast<int32_t*>(smem + S::kOffK);
+  const int per_thread = (p.R + kThreads - 1) / kThreads;
+  {
+    int32_t w = 0;
+#pragma unroll 1
+    for (int i = 0; i < per_thread; ++i) {
+      const int r = threadIdx.x * per_thread + i;
+      if (r < p.R) w += load_request<NR, KT>(p, r, cta == 0).weight;
+    }
+    weights[threadIdx.x] = w;
+  }
   if (warp == 1) {
     tc::tmem_alloc(&tail->tmem, kTmemCols);
     tc::tmem_relinquish();
@@ -333,61 +347,9 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
     mbar_init(&tail->o_empty, 4);
     mbar_init(&tail->final_mma, 2);
     tail->abort = 0;
-    tail->req = p.R;
-    tail->base = 0;
     fence_mbar_init();
   }
-  // running sum over the requests, kThreads at a time (one step for most batches)
-  auto scan = [&](int64_t w, int64_t& total) -> int64_t {  // exclusive sum of w
-    int64_t x = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) tail->warp_sum[warp] = x;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      const int64_t s = tail->warp_sum[i];
-      if (i < warp) before += s;
-      total += s;
-    }
-    return before + x - w;
-  };
-  int64_t W = 0;
-  kept_before = scan(kept_w, W);
-  for (int r0 = kThreads; r0 < p.R; r0 += kThreads) {
-    const int r = r0 + threadIdx.x;
-    int64_t total;
-    scan(r < p.R ? load_request<NR>(p, r, cta == 0).weight : 0, total);
-    W += total;
-  }
-  if (W > INT32_MAX) {  // (the host has checked its mirrors)
-    if (cta == 0 && threadIdx.x == 0) raise_error(p.err, kErrBounds);
-    W = 0;
-  }
-  const unsigned Q = ((unsigned)W + groups - 1) / groups;
-  const int begin = (int)min(W, (int64_t)group * Q), end = (int)min(W, (int64_t)begin + Q);
-  {
-    int64_t sum = 0;
-    for (int r0 = 0; r0 < p.R; r0 += kThreads) {  // the request, from the sums of each step
-      const int r = r0 + threadIdx.x;
-      int64_t w = kept_w, before = kept_before, total = 0;
-      if (p.R > kThreads) {
-        w = r < p.R ? load_request<NR>(p, r, false).weight : 0;
-        before = sum + scan(w, total);
-      }
-      sum += total;
-      if (begin >= before && begin < before + w) {
-        tail->req = r;
-        tail->base = (int)before;
-      }
-    }
-  }
+  tc::fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -405,7 +367,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
   };
   auto release = [&](int n) { mbar_arrive(&tail->piece_empty[n % kPieces]); };
 
-  if (begin < end) {
+  {
     if (warp == 0) {
       // --------------------------------------------------------- TMA producer
       // (one lane: a copy instruction with several lanes active costs about
@@ -438,22 +400,28 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             queries = n + 1;
             return true;
           };
-          // physical row of the first key of half i of tile j (16-token blocks
-          // fill a tile in two halves)
-          auto fetch = [&](int j, int i) -> int {
-            const int key = j * KT + i * 16;
-            return j < pc.k1 && key < pc.n_keys ? __ldg(table + (key >> p.b_shift)) : 0;
+          // physical block of part i of tile j (a tile is 1, 2 or 4 parts of
+          // min(block, tile) keys, each in one block)
+          const int part_shift = min(p.b_shift, KT == 64 ? 6 : 5), parts = KT >> part_shift;
+          auto fetch = [&](int j, int (&id)[KT / 16]) {
+#pragma unroll
+            for (int i = 0; i < KT / 16; ++i) {
+              const int key = j * KT + (i << part_shift);
+              id[i] = i < parts && j < pc.k1 && key < pc.n_keys ? __ldg(table + (key >> p.b_shift))
+                                                                 : 0;
+            }
           };
-          const bool halves = p.b_shift == 4;
-          int id0 = fetch(pc.k0, 0), id1 = halves ? fetch(pc.k0, 1) : 0;
+          int ids[KT / 16], next[KT / 16];
+          fetch(pc.k0, ids);
           load_q(false);
           for (int j = pc.k0; j < pc.k1; ++j, ++g) {
-            const int next0 = fetch(j + 1, 0), next1 = halves ? fetch(j + 1, 1) : 0;
-            if (id0 < 0 || id0 >= p.num_blocks || id1 < 0 || id1 >= p.num_blocks) {
-              raise_error(p.err, kErrBounds);  // a valid block; the output is then unspecified
-              if (id0 < 0 || id0 >= p.num_blocks) id0 = 0;
-              if (id1 < 0 || id1 >= p.num_blocks) id1 = 0;
-            }
+            fetch(j + 1, next);
+#pragma unroll
+            for (int i = 0; i < KT / 16; ++i)
+              if (ids[i] < 0 || ids[i] >= p.num_blocks) {
+                raise_error(p.err, kErrBounds);
+                ids[i] = 0;  // a valid block; the output is then unspecified
+              }
             if (g >= kStages && !mbar_test_wait(&tail->k_empty[st], phase)) {
               // the stage may be waiting for products that wait for this Q
               ok = load_q(true) && mbar_wait(&tail->k_empty[st], phase, p.err) && !aborted(tail);
@@ -462,33 +430,34 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             load_q(false);
             uint8_t* dst = smem + S::kOffK + st * S::kStage;
             uint64_t* bar = &tail->k_full[st];
-            constexpr int kBytes = S::kStage + (F8 ? KT * 4 : 0);
-            if (!halves) {
-              const int y = (id0 << p.b_shift) + ((j * KT) & ((1 << p.b_shift) - 1));
-              mbar_arrive_expect_tx(bar, kBytes);
+            constexpr int kRowBytes = (kCols + 1) * 128 + (F8 ? 4 : 0);
+            if (parts == 1) {
+              const int y = (ids[0] << p.b_shift) + ((j * KT) & ((1 << p.b_shift) - 1));
+              mbar_arrive_expect_tx(bar, KT * kRowBytes);
               tc::tma_load_3d(dst, &tmap_c, 0, y, 0, bar);
               tc::tma_load_2d(dst + kCols * kChunk, &tmap_r, 0, y, bar);
               if (F8) bulk_g2s(tail->scale[st], p.scales + y, KT * 4, bar);
             } else {
-              const bool both = j * KT + 16 < pc.n_keys;
-              mbar_arrive_expect_tx(bar, both ? kBytes : kBytes / 2);
+              const int live = min(parts, (pc.n_keys - j * KT + (1 << part_shift) - 1) >> part_shift);
+              mbar_arrive_expect_tx(bar, (live << part_shift) * kRowBytes);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (i == 1 && !both) break;
-                const int y = (i ? id1 : id0) << 4;
+              for (int i = 0; i < KT / 16; ++i) {
+                if (i >= live) break;
+                const int y = ids[i] << p.b_shift, at = (i << part_shift) * 128;
 #pragma unroll
                 for (int c = 0; c < kCols; ++c)
-                  tc::tma_load_3d(dst + c * kChunk + i * 2048, &tmap_c, 0, y, c, bar);
-                tc::tma_load_2d(dst + kCols * kChunk + i * 2048, &tmap_r, 0, y, bar);
-                if (F8) bulk_g2s(tail->scale[st] + i * 16, p.scales + y, 64, bar);
+                  tc::tma_load_3d(dst + c * kChunk + at, &tmap_c, 0, y, c, bar);
+                tc::tma_load_2d(dst + kCols * kChunk + at, &tmap_r, 0, y, bar);
+                if (F8)
+                  bulk_g2s(tail->scale[st] + (i << part_shift), p.scales + y, 4 << part_shift, bar);
               }
             }
             if (++st == kStages) {
               st = 0;
               phase ^= 1;
             }
-            id0 = next0;
-            id1 = next1;
+#pragma unroll
+            for (int i = 0; i < KT / 16; ++i) ids[i] = next[i];
           }
           ok = ok && load_q(true);
           if (!ok) break;
@@ -556,20 +525,6 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
     } else if (warp == 2) {
       // ------------------------------------------------------------------ PV
       if (tc::elect_one()) {
-        // first the pass cut at this group's start, for the join: handled at its first cut
-        LatentJoin join{};
-        {
-          const Request q = load_request<NR>(p, tail->req, false);
-          const int pass = (begin - tail->base) / q.keys;
-          const unsigned a = tail->base + pass * q.keys;  // the pass's start
-          const int row0 = (pass * p.lanes + in_group) * NR;
-          if ((unsigned)begin > a && a / Q + 1 == (unsigned)group && row0 < q.rows) {
-            join.rows = min(q.rows - row0, NR);
-            join.pieces = (int32_t)((a + q.keys - 1) / Q - a / Q) + 1;
-            join.out_row = (int64_t)q.q_begin * p.Hq + row0;
-          }
-        }
-        p.joins[cta] = join;
         constexpr uint32_t idesc = tc::idesc_16bit_f32(128, NR, true, false, false);
         // A the codes, MN-major (bit 15); B E5M2 (type 1 in bits 10..)
         constexpr uint32_t idesc8 = tc::idesc_e4m3_f32(128, NR) | (1u << 15) | (1u << 10);
@@ -597,22 +552,25 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             }
             tc::fence_after_sync();
             const uint64_t vs = tc::desc_at(v_desc, st * S::kStage);
-            const uint64_t ps = tc::desc_at(p_desc, (g & 1) * S::kPTile);
             const bool add = j > pc.k0;
-            // products per 128-dim block: bf16, two of 16 keys each; codes, three,
-            // one for each part of the weights of all 32 keys
+            // a part of the weights after the other (bf16: one), 32 bytes of keys at
+            // a time: 16 bf16 or 32 codes
 #pragma unroll
             for (int m = 0; m < kBlocks; ++m)
 #pragma unroll
-              for (int k = 0; k < (F8 ? 3 : 2); ++k) {
-                const uint64_t pb = tc::desc_at(ps, k * 32);
-                if (F8)
-                  tc::mma_e4m3_ss(tmem + m * NR, tc::desc_at(vs, m * kChunk), pb, idesc8,
-                                  add || k > 0);
-                else
-                  tc::mma_bf16_ss(tmem + m * NR, tc::desc_at(vs, 2 * m * kChunk + k * 16 * 128),
-                                  pb, idesc, add || k > 0);
-              }
+              for (int part = 0; part < S::kPartsP; ++part)
+#pragma unroll
+                for (int k = 0; k < S::kPartBytes / 32; ++k) {
+                  const uint64_t pb = tc::desc_at(
+                      p_desc, ((g & 1) ? S::p_part(1, part) : S::p_part(0, part)) + k * 32);
+                  const bool acc = add || part > 0 || k > 0;
+                  if (F8)
+                    tc::mma_e4m3_ss(tmem + m * NR, tc::desc_at(vs, m * kChunk + k * 32 * 128), pb,
+                                    idesc8, acc);
+                  else
+                    tc::mma_bf16_ss(tmem + m * NR,
+                                    tc::desc_at(vs, 2 * m * kChunk + k * 16 * 128), pb, idesc, acc);
+                }
             tc::mma_commit(&tail->k_empty[st]);
             tc::mma_commit(&tail->pv_done[g & 1]);
             if (++st == kStages) st = 0;
@@ -627,12 +585,44 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       __syncwarp();
     } else if (warp == 3) {
       // -------------------------------------------------------------- pieces
-      Walk<NR> walk(begin, end, tail->req, tail->base, in_group);
+      // This group's range [begin, end) of the flat space, from the running sum of
+      // the weights, and the request that holds its first tile.
+      const int group = cta / p.lanes, in_group = cta - group * p.lanes;
+      const int groups = gridDim.x / p.lanes;
+      constexpr int kEach = kThreads / 32;
+      int32_t mine = 0;
+#pragma unroll 1
+      for (int i = 0; i < kEach; ++i) mine += weights[lane * kEach + i];
+      int32_t upto = mine;
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int W = __shfl_sync(0xffffffffu, upto, 31);
+      const unsigned Q = max(1u, ((unsigned)W + groups - 1) / groups);
+      const int begin = (int)min((unsigned)W, group * Q), end = (int)min((unsigned)W, begin + Q);
+      // the lane, its thread's sum, then the request
+      const int owner = __popc(__ballot_sync(0xffffffffu, upto <= begin)) & 31;
+      int base = __shfl_sync(0xffffffffu, upto - mine, owner);
+      int r = owner * kEach;
+#pragma unroll 1
+      while (r < owner * kEach + kEach - 1 && base + weights[r] <= begin) base += weights[r++];
+      r *= per_thread;
+      __syncwarp();
+      Walk<NR, KT> walk(begin, end, r, base, in_group);
       Piece pc;
+      Request q{};
+      bool first = true;
       int n = 0;
       bool ok = true;
       for (bool more = true; ok && more;) {
         more = walk.next(p, pc);
+        if (first) {  // the request that holds this group's first tile
+          first = false;
+          q = walk.q;
+          base = walk.base;
+        }
         if (!more) {
           pc.r = -1;
         } else if (pc.k0 >= pc.k1) {
@@ -647,11 +637,29 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&tail->piece_empty[n % kPieces],
                                                  (n / kPieces - 1) & 1, p.err));
         if (!ok) break;
+        // (the weights lie where the first copies will go)
+        if (n == 0) tc::fence_proxy_async_smem();
+        __syncwarp();
         if (lane == 0) {
           tail->piece[n % kPieces] = pc;
           mbar_arrive(&tail->piece_full[n % kPieces]);
         }
         __syncwarp();
+        if (n == 0) {
+          // the pass cut at this group's start, for the join: handled at its first cut
+          LatentJoin join{};
+          if (begin < end) {
+            const int at = begin - base, pass = at / q.keys;
+            const unsigned a = begin - (at - pass * q.keys);  // the pass's start
+            const int row0 = (pass * p.lanes + in_group) * NR;
+            if ((unsigned)begin > a && a / Q + 1 == (unsigned)group && row0 < q.rows) {
+              join.rows = min(q.rows - row0, NR);
+              join.pieces = (int32_t)((a + q.keys - 1) / Q - a / Q) + 1;
+              join.out_row = (int64_t)q.q_begin * p.Hq + row0;
+            }
+          }
+          if (lane == 0) p.joins[cta] = join;
+        }
         // a later piece's first tiles and queries, towards L2 while the ones
         // before are worked on (16 keys a lane)
         if (more && n > 0) {
@@ -744,56 +752,61 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         }
         const int lim_min = RT == 2 ? min(lim[0], lim[RT - 1]) : lim[0];
         for (int j = pc.k0; j < pc.k1; ++j, ++g) {
-          float x[RT][8];            // key 8 i + 2 (lane % 4) + b of the tile at [2 i + b]
+          float x[RT][VT];           // key 8 i + 2 (lane % 4) + b of the tile at [2 i + b]
           float alpha[RT];
 #pragma unroll
           for (int t = 0; t < RT; ++t) alpha[t] = 1.f;
-          float sc[8];               // E4M3: scales of those keys
+          float sc[VT];              // E4M3: scales of those keys
           const int key0 = j * KT;
           if (scores) {
             const int buf = g % kSBufs;
             if (!(ok = wait(&tail->s_full[buf], g / kSBufs))) break;
             tc::fence_after_sync();
-            uint32_t sr[16];
+            uint32_t sr[KT / 2];
             const float* s = reinterpret_cast<const float*>(sr);
-            tmem_ld_16x32(tmem + kTmemS + buf * KT + lanes, sr);
+#pragma unroll
+            for (int c = 0; c < KT; c += 32)
+              tmem_ld_16x32(tmem + kTmemS + buf * KT + c + lanes, sr + c / 2);
             if constexpr (F8) {
               // (the stage's scales came with its keys)
               if (!(ok = wait(&tail->k_full[g % kStages], g / kStages))) break;
-              uint32_t rr[16];
+              uint32_t rr[KT / 2];
               const float* rs = reinterpret_cast<const float*>(rr);
-              tmem_ld_16x32(tmem + kTmemR + buf * KT + lanes, rr);
+#pragma unroll
+              for (int c = 0; c < KT; c += 32)
+                tmem_ld_16x32(tmem + kTmemR + buf * KT + c + lanes, rr + c / 2);
               if (j == pc.k0) {
 #pragma unroll
-                for (int t = 0; t < RT; ++t) qs[t] = tail->q_scale[n % kPieces][row[t]];
+                for (int t = 0; t < RT; ++t)
+                  qs[t] = p.scale_log2 * tail->q_scale[n % kPieces][row[t]];
               }
               const float2* st = reinterpret_cast<const float2*>(tail->scale[g % kStages]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < VT / 2; ++i) {
                 const float2 v = st[4 * i + (lane & 3)];
                 sc[2 * i] = v.x;
                 sc[2 * i + 1] = v.y;
               }
               if (key0 + KT > pc.n_keys) {  // unwritten cells' scales may be anything
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < VT; ++i)
                   if (key0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1) >= pc.n_keys) sc[i] = 0.f;
               }
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < VT; ++i) {
                 const int a = (i >> 1) * 4 + (i & 1);
                 if constexpr (kStacked) {
-                  x[0][i] = p.scale_log2 * fmaf((s[a] + s[a + 2]) * qs[0], sc[i], rs[a]);
+                  x[0][i] = fmaf((s[a] + s[a + 2]) * qs[0], sc[i], rs[a] * p.scale_log2);
                 } else {
-                  x[0][i] = p.scale_log2 * fmaf(s[a] * qs[0], sc[i], rs[a]);
-                  x[RT - 1][i] = p.scale_log2 * fmaf(s[a + 2] * qs[RT - 1], sc[i], rs[a + 2]);
+                  x[0][i] = fmaf(s[a] * qs[0], sc[i], rs[a] * p.scale_log2);
+                  x[RT - 1][i] = fmaf(s[a + 2] * qs[RT - 1], sc[i], rs[a + 2] * p.scale_log2);
                 }
               }
             } else {
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < VT; ++i) {
                 x[0][i] = s[(i >> 1) * 4 + (i & 1)];
                 x[RT - 1][i] = s[(i >> 1) * 4 + (i & 1) + 2];
               }
@@ -802,7 +815,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
             if (key0 + KT > lim_min) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < VT; ++i) {
                 const int key = key0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1);
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
@@ -811,16 +824,17 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             }
             // the row's maximum (E4M3: of the weight p s, s by its exponent)
             float top[RT];
-            float lift[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              lift[i] = F8 ? (float)((int)(__float_as_uint(sc[i]) >> 23) - 127) : 0.f;
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-              float y[8];
+              float y[VT];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = F8 ? x[t][i] + lift[i] : x[t][i];
+              for (int i = 0; i < VT; ++i)
+                y[i] = F8 ? x[t][i] + (float)((int)(__float_as_uint(sc[i]) >> 23) - 127) : x[t][i];
               top[t] = fmax3(fmax3(y[0], y[1], y[2]), fmax3(y[3], y[4], y[5]), fmaxf(y[6], y[7]));
+#pragma unroll
+              for (int i = 8; i < VT; i += 8)
+                top[t] = fmax3(top[t], fmax3(y[i], y[i + 1], fmaxf(y[i + 2], y[i + 3])),
+                               fmax3(y[i + 4], y[i + 5], fmaxf(y[i + 6], y[i + 7])));
             }
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1)
@@ -839,33 +853,33 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                 m[t] = top[t];
               }
               const float neg = m[t] == -INFINITY ? 0.f : kTargetLog2<F8> - m[t];
-              float sum = 0.f;
+              float sum[2] = {0.f, 0.f};
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < VT; ++i) {
                 x[t][i] = ex2_ftz(F8 ? x[t][i] + neg : fmaf(x[t][i], p.scale_log2, neg));
-                sum += x[t][i];
+                sum[i & 1] += x[t][i];
               }
-              l[t] = l[t] * alpha[t] + sum;
+              l[t] = l[t] * alpha[t] + (sum[0] + sum[1]);
             }
           }
           // PV(g - 2) has read this half of P, and what was published with it
           if (g >= 2 && !(ok = wait(&tail->pv_done[g & 1], (g >> 1) - 1))) break;
           if (scores) {
             if constexpr (F8) {
-              // weights p s in three parts, 32 bytes of the row each
+              // weights p s in three parts, a byte a key
 #pragma unroll
               for (int t = 0; t < RT; ++t) {
-                uint8_t* prow = ps + (g & 1) * S::kPTile + row[t] * 128 + (lane & 3) * 2;
+                uint8_t* prow = ps + row[t] * 128 + (lane & 3) * 2;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < VT / 2; ++i) {
                   float a = x[t][2 * i] * sc[2 * i], b = x[t][2 * i + 1] * sc[2 * i + 1];
-                  uint8_t* at = prow + (i & 1) * 8;
 #pragma unroll
                   for (int part = 0; part < 3; ++part) {
                     const uint32_t code = e5m2_pair(a, b);
-                    const int gran = part * 2 + (i >> 1);  // 16 keys a granule
-                    *reinterpret_cast<uint16_t*>(at + ((gran ^ (row[t] & 7)) << 4)) =
-                        (uint16_t)code;
+                    const int off = (g & 1) ? S::p_part(1, part) : S::p_part(0, part);
+                    const int gran = (off >> 4 & 7) + (i >> 1);  // 16 keys a granule
+                    *reinterpret_cast<uint16_t*>(prow + (off & ~127) + (i & 1) * 8 +
+                                                 ((gran ^ (row[t] & 7)) << 4)) = (uint16_t)code;
                     const float2 v = e5m2_values(code);
                     a -= v.x;
                     b -= v.y;
@@ -875,10 +889,11 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             } else {
               const int mi = lane >> 3;  // the 8x8 matrix whose row this lane addresses
               const int prow = w4 * 16 + (mi & 1) * 8 + (lane & 7);
+              const int off = (g & 1) ? S::p_part(1, 0) : S::p_part(0, 0);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int gran = (g & 1) * 4 + 2 * i + (mi >> 1);
-                stmatrix_x4(ps + prow * 128 + ((gran ^ (prow & 7)) << 4),
+              for (int i = 0; i < KT / 16; ++i) {
+                const int gran = (off >> 4 & 7) + 2 * i + (mi >> 1);
+                stmatrix_x4(ps + prow * 128 + (off & ~127) + ((gran ^ (prow & 7)) << 4),
                             pack_bf16(x[0][4 * i], x[0][4 * i + 1]),
                             pack_bf16(x[RT - 1][4 * i], x[RT - 1][4 * i + 1]),
                             pack_bf16(x[0][4 * i + 2], x[0][4 * i + 3]),
@@ -1081,8 +1096,6 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       }
       if (!ok) tail->abort = 1;
     }
-  } else if (threadIdx.x == 64) {
-    p.joins[cta] = LatentJoin{};
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -1202,12 +1215,12 @@ pa_status launch(const LatentParams& p, const void* q, const pa_latent_pool* poo
   using S = Smem<L, NR, F8>;
   CUtensorMap tq, tc, tr;
   const int64_t cells = (int64_t)pool->num_blocks * pool->block_size;
-  const int box_rows = std::min(pool->block_size, KT);
+  const int box_rows = std::min(pool->block_size, S::KT);
   // (E4M3: the queries are converted, not copied)
   if (!encode_chunks(&tq, q, false, L / 64 + 1, (L + kRope) * 2, (int64_t)p.T * p.Hq, NR,
                      L / 64 + 1) ||
       !encode_chunks(&tc, pool->latent, F8, S::kCols, S::kCols * 128, cells, box_rows,
-                     box_rows == KT ? S::kCols : 1) ||
+                     box_rows == S::KT ? S::kCols : 1) ||
       !encode_rope(&tr, pool->rope, cells, box_rows))
     return PA_ERR_CUDA;
   if (cudaFuncSetAttribute(latent_attn_kernel<L, NR, F8>,
@@ -1270,6 +1283,7 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
   // rows are addressed by 32-bit tensor-map coordinates
   if ((int64_t)T * Hq > INT32_MAX - pa::kLatentRows) return PA_ERR_UNSUPPORTED;
 
+  const int KT = pa::latent_tile_keys(L, pool->dtype == PA_KV_FP8_E4M3);
   // Row tiles: the smallest of 16, 32 and 64 rows that covers the widest
   // request in one pass over its cells; 64 past that.
   int64_t widest = 0;
@@ -1288,7 +1302,7 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
       const int64_t rows = (int64_t)(qsl_host[r + 1] - qsl_host[r]) * Hq;
       if (rows > 0)
         w += ((rows + NR - 1) / NR + lanes - 1) / lanes *
-             ((seq_lens_host[r] + pa::kLatentKeys - 1) / pa::kLatentKeys);
+             ((seq_lens_host[r] + KT - 1) / KT);
     }
     const int64_t cost = w * std::max(1570, 1300 * lanes);
     if (lanes <= sms && cost < best) {
@@ -1296,9 +1310,11 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
       W = w;
       G = lanes;
     }
-    if (w > INT32_MAX) return PA_ERR_UNSUPPORTED;
     if (widest <= NR) break;  // one row tile each
   }
+  // the flat space stays within 31 bits whatever the device lengths are
+  const int64_t most = ((int64_t)T * Hq / NR + R) * (((int64_t)max_blocks * pool->block_size + KT - 1) / KT);
+  if (most > INT32_MAX) return PA_ERR_UNSUPPORTED;
   const int grid = G * (int)std::min<int64_t>(W, sms / G);
   if (workspace_bytes < pa::scratch_bytes(grid, NR, L)) return PA_ERR_INVALID;
 

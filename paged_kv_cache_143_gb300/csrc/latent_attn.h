@@ -8,14 +8,17 @@
 
 namespace pa {
 
-constexpr int kLatentKeys = 32;     // keys per tile
+// Keys per tile: 64 where that leaves several tiles of stages beside Q and P, else 32.
+constexpr int latent_tile_keys(int latent_dim, bool e4m3) {
+  return latent_dim == 512 && !e4m3 ? 32 : 64;
+}
 constexpr int kLatentRows = 64;     // most query rows (token, head) per row tile
 constexpr int kLatentMaxCtas = 1024;
 
-// The work of one call is laid out as one sequence of 32-key tiles, the "flat
+// The work of one call is laid out as one sequence of key tiles, the "flat
 // space". The grid is NG groups of G CTAs (G 1 or 2) that walk it side by
 // side: a pass (request r, row tiles i G .. i G + G - 1 of NR query rows, one to
-// each CTA of the group) takes the C_r = ceil(seq_len / 32) key tiles of the
+// each CTA of the group) takes the C_r = ceil(seq_len / KT) key tiles of the
 // request, at pref[r] + i C_r, pref the exclusive running sum of passes_r C_r.
 // Group b takes the tiles [b Q, b Q + Q), Q = ceil(W / NG): equal shares whatever
 // the lengths, and a cell that several row tiles need is read from HBM once,
