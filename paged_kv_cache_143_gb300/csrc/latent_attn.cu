@@ -32,6 +32,9 @@
 //   warps 4-7   softmax (S read as 16 x 256-bit fragments: a row in four lanes),
 //               P to shared memory; then the output
 //   warps 8-11  (E4M3) the query tile as E4M3 parts
+// The instruction cache is cold at launch and, once all SMs stream, a miss takes
+// microseconds: S, PV and softmax run once on whatever memory holds while the
+// first keys are on their way (S and O are overwritten by the first real products).
 // The softmax warps share nothing tile by tile. A warp that moves a row's
 // reference maximum says so beside P; warp 2 then asks all four to rescale
 // their dims of O before it issues that PV (rare: growth by more than 2^8).
@@ -149,6 +152,29 @@ struct Tail {
 };
 static_assert(sizeof(Tail<true>) <= 5120 && sizeof(Tail<false>) <= 2048, "Tail overruns its slot");
 
+// pa::mbar_wait without its timer: a cold line of instructions costs microseconds
+// once all SMs stream, and the timer's loop is one that every first wait would
+// fetch. Each try suspends the thread for at most about kTryNs, so the limit is
+// at least the pa::kWaitLimitNs that the tries add up to.
+constexpr unsigned kTryNs = 1000, kTries = 2000000;
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity, unsigned* err) {
+  const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
+  for (unsigned i = 0; i < kTries; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity), "r"(kTryNs)
+        : "memory");
+    if (ok) return true;
+  }
+  raise_error(err, kErrTimeout);
+  return false;
+}
+
 template <bool F8>
 __device__ __forceinline__ bool aborted(Tail<F8>* t) {
   return *reinterpret_cast<volatile int*>(&t->abort) != 0;
@@ -200,19 +226,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Two fp32 to E4M3 or E5M2 (nearest even), x in the low byte.
+// Two fp32 to E4M3 (nearest even), x in the low byte.
 __device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ uint32_t e5m2_pair(float x, float y) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E5M2);
-}
-// What two E5M2 codes stand for: the high bytes of two f16 numbers.
-__device__ __forceinline__ float2 e5m2_values(uint32_t pair) {
-  const uint32_t h = __byte_perm(pair, 0u, 0x1404);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
 // ------------------------------------------------------------ the flat space
 
 struct Request {
@@ -356,9 +373,11 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
   const uint32_t tmem = tail->tmem;
 
   // the next piece (n-th of the CTA) for one thread; r < 0 at the end
+  // (n = -1: a tile of nothing, for the instruction cache)
   auto piece = [&](int n, bool& ok) -> Piece {
-    Piece pc;
-    ok = mbar_wait(&tail->piece_full[n % kPieces], (n / kPieces) & 1, p.err);
+    Piece pc{0, 0, 1, KT, 0, -1, 0, -1, 0};
+    if (n < 0) return pc;
+    ok = bar_wait(&tail->piece_full[n % kPieces], (n / kPieces) & 1, p.err);
     if (ok)
       pc = tail->piece[n % kPieces];
     else
@@ -390,7 +409,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             if (n > 0) {
               uint64_t* bar = &tail->q_empty;
               if (may_wait) {
-                if (!mbar_wait(bar, (n - 1) & 1, p.err)) return false;
+                if (!bar_wait(bar, (n - 1) & 1, p.err)) return false;
               } else if (!mbar_test_wait(bar, (n - 1) & 1)) {
                 return true;
               }
@@ -424,7 +443,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               }
             if (g >= kStages && !mbar_test_wait(&tail->k_empty[st], phase)) {
               // the stage may be waiting for products that wait for this Q
-              ok = load_q(true) && mbar_wait(&tail->k_empty[st], phase, p.err) && !aborted(tail);
+              ok = load_q(true) && bar_wait(&tail->k_empty[st], phase, p.err) && !aborted(tail);
               if (!ok) break;
             }
             load_q(false);
@@ -438,7 +457,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               tc::tma_load_2d(dst + kCols * kChunk, &tmap_r, 0, y, bar);
               if (F8) bulk_g2s(tail->scale[st], p.scales + y, KT * 4, bar);
             } else {
-              const int live = min(parts, (pc.n_keys - j * KT + (1 << part_shift) - 1) >> part_shift);
+              const int live =
+                  min(parts, (pc.n_keys - j * KT + (1 << part_shift) - 1) >> part_shift);
               mbar_arrive_expect_tx(bar, (live << part_shift) * kRowBytes);
 #pragma unroll
               for (int i = 0; i < KT / 16; ++i) {
@@ -465,9 +485,9 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         }
         // every issued copy lands before the CTA may leave
         if (!ok) tail->abort = 1;
-        if (queries > 0) mbar_wait(&tail->q_full, (queries - 1) & 1, p.err);
+        if (queries > 0) bar_wait(&tail->q_full, (queries - 1) & 1, p.err);
         for (int i = max(0, g - kStages); i < g; ++i)
-          mbar_wait(&tail->k_full[i % kStages], (i / kStages) & 1, p.err);
+          bar_wait(&tail->k_full[i % kStages], (i / kStages) & 1, p.err);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -479,14 +499,18 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         const uint64_t k_desc = tc::smem_desc_sw128(smem + S::kOffK, 16, 1024);
         int g = 0, st = 0, phase = 0;
         bool ok = true;
-        for (int n = 0;; ++n) {
+#pragma unroll 1
+        for (int n = -1;; ++n) {
+          const bool live = n >= 0;
           const Piece pc = piece(n, ok);
           if (pc.r < 0) break;
-          if (!(ok = mbar_wait(&tail->q_full, n & 1, p.err))) break;
-          for (int j = pc.k0; j < pc.k1; ++j, ++g) {
+          if (live && !(ok = bar_wait(&tail->q_full, n & 1, p.err))) break;
+#pragma unroll 1
+          for (int j = pc.k0; j < pc.k1; ++j) {
             const int buf = g % kSBufs;
-            ok = (g < kSBufs || mbar_wait(&tail->s_empty[buf], (g / kSBufs - 1) & 1, p.err)) &&
-                 mbar_wait(&tail->k_full[st], phase, p.err);
+            ok = !live ||
+                 ((g < kSBufs || bar_wait(&tail->s_empty[buf], (g / kSBufs - 1) & 1, p.err)) &&
+                  bar_wait(&tail->k_full[st], phase, p.err));
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t ks = tc::desc_at(k_desc, st * S::kStage);
@@ -507,19 +531,22 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                 else
                   tc::mma_bf16_ss(d, qa, kb, idesc, true);
               }
+            if (!live) break;
             tc::mma_commit(&tail->s_full[buf]);
+            ++g;
             if (++st == kStages) {
               st = 0;
               phase ^= 1;
             }
           }
           if (!ok) break;
+          if (!live) continue;
           tc::mma_commit(&tail->q_empty);
           release(n);
         }
         if (!ok) tail->abort = 1;
         tc::mma_commit(&tail->final_mma);
-        mbar_wait(&tail->final_mma, 0, p.err);
+        bar_wait(&tail->final_mma, 0, p.err);
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -532,21 +559,24 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         const uint64_t v_desc = tc::smem_desc_sw128(smem + S::kOffK, kChunk, 1024);
         int g = 0, st = 0, fixes = 0;
         bool ok = true;
-        for (int n = 0;; ++n) {
+#pragma unroll 1
+        for (int n = -1;; ++n) {
+          const bool live = n >= 0;
           const Piece pc = piece(n, ok);
           if (pc.r < 0) break;
-          for (int j = pc.k0; j < pc.k1; ++j, ++g) {
-            if (!(ok = mbar_wait(&tail->p_full[g & 1], (g >> 1) & 1, p.err))) break;
+#pragma unroll 1
+          for (int j = pc.k0; j < pc.k1; ++j) {
+            if (live && !(ok = bar_wait(&tail->p_full[g & 1], (g >> 1) & 1, p.err))) break;
             if (j == pc.k0) {
               // the first product of a piece overwrites O: the last piece is out
-              if (n > 0 && !(ok = mbar_wait(&tail->o_empty, (n - 1) & 1, p.err))) break;
+              if (n > 0 && !(ok = bar_wait(&tail->o_empty, (n - 1) & 1, p.err))) break;
             } else if (*reinterpret_cast<volatile uint32_t*>(&tail->ask[g & 1][0]) != 0) {
               // rows of this tile have a new reference: O, complete up to the
               // tile before, is rescaled first
               *reinterpret_cast<volatile int32_t*>(&tail->fix_tile) = g;
-              ok = mbar_wait(&tail->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err);
+              ok = bar_wait(&tail->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err);
               mbar_arrive(&tail->fix);
-              ok = ok && mbar_wait(&tail->fixed, fixes & 1, p.err);
+              ok = ok && bar_wait(&tail->fixed, fixes & 1, p.err);
               if (!ok) break;
               ++fixes;
             }
@@ -571,16 +601,18 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                     tc::mma_bf16_ss(tmem + m * NR,
                                     tc::desc_at(vs, 2 * m * kChunk + k * 16 * 128), pb, idesc, acc);
                 }
+            if (!live) break;
             tc::mma_commit(&tail->k_empty[st]);
             tc::mma_commit(&tail->pv_done[g & 1]);
+            ++g;
             if (++st == kStages) st = 0;
           }
           if (!ok) break;
-          release(n);
+          if (live) release(n);
         }
         if (!ok) tail->abort = 1;
         tc::mma_commit(&tail->final_mma);
-        mbar_wait(&tail->final_mma, 0, p.err);
+        bar_wait(&tail->final_mma, 0, p.err);
       }
       __syncwarp();
     } else if (warp == 3) {
@@ -634,7 +666,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           continue;
         }
         if (n >= kPieces)
-          ok = __all_sync(0xffffffffu, mbar_wait(&tail->piece_empty[n % kPieces],
+          ok = __all_sync(0xffffffffu, bar_wait(&tail->piece_empty[n % kPieces],
                                                  (n / kPieces - 1) & 1, p.err));
         if (!ok) break;
         // (the weights lie where the first copies will go)
@@ -717,24 +749,19 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       };
       // Waits for a barrier, doing the rescales that are asked for meanwhile.
       auto wait = [&](uint64_t* bar, int parity) -> bool {
-        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
-        unsigned long long t0 = 0;
-        for (int spin = 1;; ++spin) {
-          if (__all_sync(0xffffffffu, mbar_test_wait(&tail->fix, fixes & 1))) rescale();
+#pragma unroll 1
+        for (unsigned i = 0; i < 64 * kTries; ++i) {
           if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
-          if ((spin & 1023) == 0) {
-            const unsigned long long now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitLimitNs) {
-              if (lane == 0) raise_error(p.err, kErrTimeout);
-              return false;
-            }
-          }
+          if (__all_sync(0xffffffffu, mbar_test_wait(&tail->fix, fixes & 1))) rescale();
         }
+        if (lane == 0) raise_error(p.err, kErrTimeout);
+        return false;
       };
       int g = 0;
       bool ok = true;
-      for (int n = 0;; ++n) {
+#pragma unroll 1
+      for (int n = -1;; ++n) {
+        const bool live = n >= 0;
         const Piece pc = piece(n, ok);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || pc.r < 0) break;
@@ -751,7 +778,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           qs[t] = 1.f;
         }
         const int lim_min = RT == 2 ? min(lim[0], lim[RT - 1]) : lim[0];
-        for (int j = pc.k0; j < pc.k1; ++j, ++g) {
+#pragma unroll 1
+        for (int j = pc.k0; j < pc.k1; ++j) {
           float x[RT][VT];           // key 8 i + 2 (lane % 4) + b of the tile at [2 i + b]
           float alpha[RT];
 #pragma unroll
@@ -760,7 +788,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           const int key0 = j * KT;
           if (scores) {
             const int buf = g % kSBufs;
-            if (!(ok = wait(&tail->s_full[buf], g / kSBufs))) break;
+            if (live && !(ok = wait(&tail->s_full[buf], g / kSBufs))) break;
             tc::fence_after_sync();
             uint32_t sr[KT / 2];
             const float* s = reinterpret_cast<const float*>(sr);
@@ -769,7 +797,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               tmem_ld_16x32(tmem + kTmemS + buf * KT + c + lanes, sr + c / 2);
             if constexpr (F8) {
               // (the stage's scales came with its keys)
-              if (!(ok = wait(&tail->k_full[g % kStages], g / kStages))) break;
+              if (live && !(ok = wait(&tail->k_full[g % kStages], g / kStages))) break;
               uint32_t rr[KT / 2];
               const float* rs = reinterpret_cast<const float*>(rr);
 #pragma unroll
@@ -778,7 +806,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               if (j == pc.k0) {
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-                  qs[t] = p.scale_log2 * tail->q_scale[n % kPieces][row[t]];
+                  qs[t] = tail->q_scale[n & (kPieces - 1)][row[t]];
               }
               const float2* st = reinterpret_cast<const float2*>(tail->scale[g % kStages]);
 #pragma unroll
@@ -797,10 +825,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               for (int i = 0; i < VT; ++i) {
                 const int a = (i >> 1) * 4 + (i & 1);
                 if constexpr (kStacked) {
-                  x[0][i] = fmaf((s[a] + s[a + 2]) * qs[0], sc[i], rs[a] * p.scale_log2);
+                  x[0][i] = fmaf((s[a] + s[a + 2]) * qs[0], sc[i], rs[a]);
                 } else {
-                  x[0][i] = fmaf(s[a] * qs[0], sc[i], rs[a] * p.scale_log2);
-                  x[RT - 1][i] = fmaf(s[a + 2] * qs[RT - 1], sc[i], rs[a + 2] * p.scale_log2);
+                  x[0][i] = fmaf(s[a] * qs[0], sc[i], rs[a]);
+                  x[RT - 1][i] = fmaf(s[a + 2] * qs[RT - 1], sc[i], rs[a + 2]);
                 }
               }
             } else {
@@ -812,7 +840,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               }
             }
             tc::fence_before_sync();
-            if (lane == 0) mbar_arrive(&tail->s_empty[buf]);
+            if (lane == 0 && live) mbar_arrive(&tail->s_empty[buf]);
             if (key0 + KT > lim_min) {
 #pragma unroll
               for (int i = 0; i < VT; ++i) {
@@ -829,7 +857,11 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               float y[VT];
 #pragma unroll
               for (int i = 0; i < VT; ++i)
-                y[i] = F8 ? x[t][i] + (float)((int)(__float_as_uint(sc[i]) >> 23) - 127) : x[t][i];
+                // (2^23 + n as a float holds n in its low bits)
+                y[i] = F8 ? fmaf(x[t][i], p.scale_log2,
+                                 __uint_as_float((__float_as_uint(sc[i]) >> 23) | 0x4B000000u) -
+                                     8388735.f)
+                          : x[t][i];
               top[t] = fmax3(fmax3(y[0], y[1], y[2]), fmax3(y[3], y[4], y[5]), fmaxf(y[6], y[7]));
 #pragma unroll
               for (int i = 8; i < VT; i += 8)
@@ -856,7 +888,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               float sum[2] = {0.f, 0.f};
 #pragma unroll
               for (int i = 0; i < VT; ++i) {
-                x[t][i] = ex2_ftz(F8 ? x[t][i] + neg : fmaf(x[t][i], p.scale_log2, neg));
+                x[t][i] = ex2_ftz(fmaf(x[t][i], p.scale_log2, neg));
                 sum[i & 1] += x[t][i];
               }
               l[t] = l[t] * alpha[t] + (sum[0] + sum[1]);
@@ -866,23 +898,26 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           if (g >= 2 && !(ok = wait(&tail->pv_done[g & 1], (g >> 1) - 1))) break;
           if (scores) {
             if constexpr (F8) {
-              // weights p s in three parts, a byte a key
+              // weights p s in three parts, a byte a key: an f16 number's high byte is
+              // its E5M2 truncation, so a part is the high byte after half a step is
+              // added to the magnitude, and what is left is exact in f16
 #pragma unroll
               for (int t = 0; t < RT; ++t) {
                 uint8_t* prow = ps + row[t] * 128 + (lane & 3) * 2;
 #pragma unroll
                 for (int i = 0; i < VT / 2; ++i) {
-                  float a = x[t][2 * i] * sc[2 * i], b = x[t][2 * i + 1] * sc[2 * i + 1];
+                  __half2 h = __floats2half2_rn(x[t][2 * i] * sc[2 * i],
+                                                x[t][2 * i + 1] * sc[2 * i + 1]);
 #pragma unroll
                   for (int part = 0; part < 3; ++part) {
-                    const uint32_t code = e5m2_pair(a, b);
+                    const uint32_t code =
+                        (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xFF00FF00u;
+                    h = __hsub2(h, *reinterpret_cast<const __half2*>(&code));
                     const int off = (g & 1) ? S::p_part(1, part) : S::p_part(0, part);
                     const int gran = (off >> 4 & 7) + (i >> 1);  // 16 keys a granule
                     *reinterpret_cast<uint16_t*>(prow + (off & ~127) + (i & 1) * 8 +
-                                                 ((gran ^ (row[t] & 7)) << 4)) = (uint16_t)code;
-                    const float2 v = e5m2_values(code);
-                    a -= v.x;
-                    b -= v.y;
+                                                 ((gran ^ (row[t] & 7)) << 4)) =
+                        (uint16_t)__byte_perm(code, 0u, 0x4431);
                   }
                 }
               }
@@ -933,12 +968,15 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               }
             }
           }
+          if (!live) break;
           tc::fence_proxy_async_smem();
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&tail->p_full[g & 1]);
+          ++g;
         }
         if (!ok) break;
+        if (!live) continue;
 
         // ---- the piece's rows: normalised to out, or a partial
         if (!(ok = wait(&tail->pv_done[(g - 1) & 1], (g - 1) >> 1))) break;
@@ -1024,7 +1062,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         const Piece pc = piece(n, ok);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || pc.r < 0) break;
-        if (n > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&tail->q_empty, (n - 1) & 1, p.err))))
+        if (n > 0 && !(ok = __all_sync(0xffffffffu, bar_wait(&tail->q_empty, (n - 1) & 1, p.err))))
           break;
 #pragma unroll 2
         for (int i = 0; i < NR / 4; ++i) {
@@ -1313,7 +1351,8 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
     if (widest <= NR) break;  // one row tile each
   }
   // the flat space stays within 31 bits whatever the device lengths are
-  const int64_t most = ((int64_t)T * Hq / NR + R) * (((int64_t)max_blocks * pool->block_size + KT - 1) / KT);
+  const int64_t most = ((int64_t)T * Hq / NR + R) *
+                       (((int64_t)max_blocks * pool->block_size + KT - 1) / KT);
   if (most > INT32_MAX) return PA_ERR_UNSUPPORTED;
   const int grid = G * (int)std::min<int64_t>(W, sms / G);
   if (workspace_bytes < pa::scratch_bytes(grid, NR, L)) return PA_ERR_INVALID;
