@@ -320,7 +320,6 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
   Tail<F8>* tail = reinterpret_cast<Tail<F8>*>(smem + S::kOffTail);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
-  launch_dependents();  // the join that follows may be scheduled now
 
   // ---- the weights of the requests, summed by thread over consecutive ones (the
   // ring is still empty). What runs before the first copy is kept short: cold
@@ -1137,15 +1136,21 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
+  // the join may be scheduled where this CTA leaves (not before: its CTAs would
+  // wait beside this one's; 1 us slower)
+  launch_dependents();
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-// Joins the partials of the row tiles cut at group boundaries: grid (attention CTAs,
-// row groups), one warp per row. o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-constexpr int kJoinWarps = 8;
+// Joins the partials of the row tiles cut at group boundaries: grid (attention
+// CTAs, row groups), one warp per row. o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// Bound by L2 (every partial is read back once, 2 KB a row at L 512) and by
+// latency: four partials are fetched at a time, beside the statistics and not
+// behind them (13 partials a row, one at a time, cost 12 us; so 5).
+constexpr int kJoinWarps = 8, kJoinBatch = 4;
 
 template <int L, int NR>
 __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const LatentParams p) {
@@ -1158,46 +1163,55 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
   // i - 1 groups on
   const int n = j.pieces;
   auto slot = [&](int i) -> int64_t { return 2 * (b + (i - 1) * p.lanes) + (i == 0 ? 1 : 0); };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    const float2 ml = p.part_ml[slot(i) * NR + row];
-    if (ml.y > 0.f) m = fmaxf(m, ml.x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   constexpr int kV = L / 128;
   float4 acc[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane < n) {
-      const float2 ml = p.part_ml[slot(i0 + lane) * NR + row];
-      if (ml.y > 0.f) {  // a piece without a visible key has no partial
-        w = ex2_ftz(ml.x - m);
-        l += w * ml.y;
+  float m = -INFINITY, l = 0.f;   // running reference and sum of the pieces so far
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kJoinBatch) {
+    float4 x[kJoinBatch][kV];
+    float2 ml[kJoinBatch];
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i0 + i < n) {
+        const int64_t at = slot(i0 + i) * NR + row;
+        ml[i] = __ldcg(p.part_ml + at);
+        // (a piece without a visible key has no partial: what is read is not used)
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+          x[i][v] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * L) + lane + v * 32);
       }
     }
-    const int cnt = min(32, n - i0);
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      if (wi == 0.f) continue;
-      const float4* src =
-          reinterpret_cast<const float4*>(p.part_o + (slot(i0 + i) * NR + row) * L) + lane;
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i)
+      if (ml[i].y > 0.f) top = fmaxf(top, ml[i].x);
+    const float keep = m == -INFINITY ? 0.f : ex2_ftz(m - top);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      acc[v].x *= keep;
+      acc[v].y *= keep;
+      acc[v].z *= keep;
+      acc[v].w *= keep;
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) {
+      if (!(ml[i].y > 0.f)) continue;
+      const float w = ex2_ftz(ml[i].x - m);
+      l = fmaf(w, ml[i].y, l);
 #pragma unroll
       for (int v = 0; v < kV; ++v) {
-        const float4 x = __ldcg(src + v * 32);
-        acc[v].x = fmaf(wi, x.x, acc[v].x);
-        acc[v].y = fmaf(wi, x.y, acc[v].y);
-        acc[v].z = fmaf(wi, x.z, acc[v].z);
-        acc[v].w = fmaf(wi, x.w, acc[v].w);
+        acc[v].x = fmaf(w, x[i][v].x, acc[v].x);
+        acc[v].y = fmaf(w, x[i][v].y, acc[v].y);
+        acc[v].z = fmaf(w, x[i][v].z, acc[v].z);
+        acc[v].w = fmaf(w, x[i][v].w, acc[v].w);
       }
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint2* dst = reinterpret_cast<uint2*>(p.out + (j.out_row + row) * L) + lane;
 #pragma unroll
@@ -1261,8 +1275,12 @@ pa_status launch(const LatentParams& p, const void* q, const pa_latent_pool* poo
                      box_rows == S::KT ? S::kCols : 1) ||
       !encode_rope(&tr, pool->rope, cells, box_rows))
     return PA_ERR_CUDA;
-  if (cudaFuncSetAttribute(latent_attn_kernel<L, NR, F8>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc) != cudaSuccess)
+  static OncePerDevice attribute;
+  if (!attribute.done([] {
+        return cudaFuncSetAttribute(latent_attn_kernel<L, NR, F8>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    S::kAlloc) == cudaSuccess;
+      }))
     return PA_ERR_CUDA;
   latent_attn_kernel<L, NR, F8><<<grid, S::kThreads, S::kAlloc, s>>>(tq, tc, tr, p);
   pa_status st = launch_status();

@@ -562,14 +562,17 @@ extern "C" pa_status pa_latent_prefill(
              !encode_heads(&tv, v, kV, H, Tk, vt, vh)) {
     return PA_ERR_CUDA;
   }
-  if (cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmem) != cudaSuccess)
-    return PA_ERR_CUDA;
   // the register split assumes that the block is launched with kLaunchRegs per
   // thread; refuse to launch a build that allocated fewer
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, latent_prefill_kernel) != cudaSuccess ||
-      fa.numRegs < (int)kLaunchRegs)
+  static OncePerDevice attribute;
+  if (!attribute.done([] {
+        cudaFuncAttributes fa;
+        return cudaFuncSetAttribute(latent_prefill_kernel,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmem) == cudaSuccess &&
+               cudaFuncGetAttributes(&fa, latent_prefill_kernel) == cudaSuccess &&
+               fa.numRegs >= (int)kLaunchRegs;
+      }))
     return PA_ERR_CUDA;
   latent_prefill_kernel<<<grid, kThreads, kSmem, as_stream(stream)>>>(tq, tk, tr, tv, p);
   return launch_status();

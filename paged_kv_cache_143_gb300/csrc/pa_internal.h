@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pa.h"
 
 namespace pa {
@@ -36,6 +38,26 @@ inline pa_status launch_status() {
   count_launches(1);
   return PA_OK;
 }
+
+// Does something once for each device (a kernel's attributes last as long as
+// its module): done(f) calls f on the first use of the current device and says
+// whether it has succeeded; a failure is tried again.
+class OncePerDevice {
+ public:
+  template <typename F>
+  bool done(F f) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return f();
+    const uint64_t bit = 1ull << dev;
+    if (mask_.load(std::memory_order_acquire) & bit) return true;
+    if (!f()) return false;
+    mask_.fetch_or(bit, std::memory_order_release);
+    return true;
+  }
+
+ private:
+  std::atomic<uint64_t> mask_{0};
+};
 
 // Shape checks shared by every entry point that takes a pool.
 pa_status check_pool(const pa_kv_pool* pool);
