@@ -200,50 +200,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ntk_all > 0) mbar_wait(&bars->q_full, 0, p.err);
       for (int i = max(0, issued - kSlots); i < issued; ++i)
         mbar_wait(&bars->full[i % kSlots], (i / kSlots) & 1, p.err);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && tc::elect_one()) {
       // --------------------------------------------------------- MMA issuer
+      // Descriptors are bases plus constants: computed anew for every product in
+      // a lane of its own they took 100 cycles a product, more than the product.
       constexpr uint32_t idesc_s = tc::idesc_16bit_f32(kM, kN, false, false, false);
       constexpr uint32_t idesc_o = tc::idesc_16bit_f32(kM, kV, false, true, false);
+      constexpr uint32_t idesc_h = tc::idesc_16bit_f32(kM, 64, false, true, false);
+      const uint64_t q_desc = tc::smem_desc_sw128(smem, 16, 1024);
+      const uint64_t k_desc = tc::smem_desc_sw128(smem + kOffRing, 16, 1024);
+      const uint64_t v_desc = tc::smem_desc_sw128(smem + kOffRing, kSlot, 1024);
       bool ok = ntk_all == 0 || mbar_wait(&bars->q_full, 0, p.err);
       auto landed = [&](int i) {
-        return mbar_wait(&bars->full[i % kSlots], (i / kSlots) & 1, p.err) && !aborted(bars);
+        return mbar_wait(&bars->full[i % kSlots], (i / kSlots) & 1, p.err);
       };
-      auto slot = [&](int i) { return smem + kOffRing + (i % kSlots) * kSlot; };
       auto issue_s = [&](int t, int j) -> bool {
-        const uint8_t* qs = smem + t * kQChunks * kSlot;
+        const uint64_t qt = tc::desc_at(q_desc, t * kQChunks * kSlot);
+        const uint32_t d = tmem + t * kN;
 #pragma unroll
         for (int c = 0; c < kKChunks; ++c) {
-          if (!landed(j * kTileChunks + c)) return false;
+          const int i = j * kTileChunks + c;
+          if (!landed(i)) return false;
           tc::fence_after_sync();
-          const uint8_t* ks = slot(j * kTileChunks + c);
+          const uint64_t ks = tc::desc_at(k_desc, (i % kSlots) * kSlot);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_ss(tmem + t * kN, tc::smem_desc_sw128(qs + c * kSlot + k * 32, 16, 1024),
-                            tc::smem_desc_sw128(ks + k * 32, 16, 1024), idesc_s, c > 0 || k > 0);
+            tc::mma_bf16_ss(d, tc::desc_at(qt, c * kSlot + k * 32), tc::desc_at(ks, k * 32),
+                            idesc_s, c > 0 || k > 0);
         }
         tc::mma_commit(&bars->s_full[t]);
         return true;
       };
       auto issue_pv = [&](int t, int j) -> bool {
         const int v = j * kTileChunks + kKChunks;
-        if (!mbar_wait(&bars->p_full[t], j & 1, p.err) || !landed(v) || !landed(v + 1)) return false;
+        if (!mbar_wait(&bars->p_full[t], j & 1, p.err) || !landed(v) || !landed(v + 1) ||
+            aborted(bars))
+          return false;
         tc::fence_after_sync();
-        // the two 64-column chunks of V may wrap around the ring, so each is a
+        const uint32_t d = tmem + 2 * kN + t * kV, pt = tmem + t * kN;
+        const uint64_t v0 = tc::desc_at(v_desc, (v % kSlots) * kSlot);
+        // the two 64-column chunks of V may wrap around the ring: then each is a
         // product of its own (64 columns of O)
-        constexpr uint32_t idesc_h = tc::idesc_16bit_f32(kM, 64, false, true, false);
-        if (slot(v + 1) == slot(v) + kSlot) {
+        if (v % kSlots != kSlots - 1) {
 #pragma unroll
           for (int k = 0; k < kN / 16; ++k)
-            tc::mma_bf16_ts(tmem + 2 * kN + t * kV, tmem + t * kN + k * 8,
-                            tc::smem_desc_sw128(slot(v) + k * 16 * 128, kSlot, 1024), idesc_o,
-                            j > 0 || k > 0);
+            tc::mma_bf16_ts(d, pt + k * 8, tc::desc_at(v0, k * 16 * 128), idesc_o, j > 0 || k > 0);
         } else {
 #pragma unroll
           for (int c = 0; c < kVChunks; ++c)
 #pragma unroll
             for (int k = 0; k < kN / 16; ++k)
-              tc::mma_bf16_ts(tmem + 2 * kN + t * kV + c * 64, tmem + t * kN + k * 8,
-                              tc::smem_desc_sw128(slot(v + c) + k * 16 * 128, kSlot, 1024), idesc_h,
+              tc::mma_bf16_ts(d + c * 64, pt + k * 8,
+                              tc::desc_at(c ? v_desc : v0, k * 16 * 128), idesc_h,
                               j > 0 || k > 0);
         }
         tc::mma_commit(&bars->pv_done[t]);
