@@ -5,9 +5,9 @@
 // the pair being dims (2i, 2i + 1) or (i, i + rot / 2). The work is one read
 // and one write of every element (HBM-bound when large, launch latency when
 // small); the angles depend on (token, pair) only, so a CTA computes its
-// tokens' cosines and sines once into shared memory, while the first vectors of
-// x are already on their way, and every head reuses them. fp32 arithmetic, one
-// rounding to bf16.
+// tokens' cosines and sines once into shared memory, while its vectors of x are
+// already on their way (four units of 16 or 32 bytes a thread), and every head
+// reuses them. fp32 arithmetic, one rounding to bf16.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "rope_angle.cuh"
@@ -15,10 +15,11 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 512;      // units a CTA aims at: two per thread, both loaded before the angles
+constexpr int kAhead = 4;        // units of a thread that are loaded before the angles
+constexpr int kUnits = kAhead * kThreads;  // units a CTA aims at
 constexpr int kMaxPairs = 128;   // rot_dim <= 256
 constexpr int kMaxTokens = 64;   // tokens of one CTA
-constexpr int kMaxAngles = 2048; // (token, pair) angles of one CTA
+constexpr int kMaxAngles = 1024; // (token, pair) angles of one CTA
 
 struct RopeParams {
   const __nv_bfloat16* x;
@@ -30,6 +31,7 @@ struct RopeParams {
   int32_t units;                   // units per head (rotated ones first, then copied ones)
   int32_t rot_units;
   int32_t tokens, heads;           // of one CTA
+  int32_t step_u, step_h;          // kThreads units on: units, and whole heads
   float factor;
 };
 
@@ -114,28 +116,35 @@ struct ScalarUnit {
 // grid (token groups, head groups). In place (out == x) is safe: a unit's dims
 // are read and written by one thread, and its loads come first.
 template <typename Unit>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
   __shared__ float2 cs[kMaxAngles];
   const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
   const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.H - h0);
   const int per_token = nh * p.units, n = nt * per_token;
-  auto place = [&](int i, int& t, int& h, int& u) {
-    t = i / per_token;
-    const int j = i - t * per_token;
-    h = j / p.units;
-    u = j - h * p.units;
-  };
-  auto src = [&](int t, int h) { return p.x + (t0 + t) * p.x_ts + (h0 + h) * p.x_hs; };
-  auto dst = [&](int t, int h) { return p.out + (t0 + t) * p.o_ts + (h0 + h) * p.o_hs; };
-  Unit first[2];
-  int t[2], h[2], u[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int i = threadIdx.x + k * kThreads;
-    if (i < n) {
-      place(i, t[k], h[k], u[k]);
-      first[k].load(p, src(t[k], h[k]), u[k]);
+  // the thread's unit, moved on by kThreads at a time without dividing
+  int t = threadIdx.x / per_token;
+  int u = threadIdx.x - t * per_token, h = u / p.units;
+  u -= h * p.units;
+  auto advance = [&]() {
+    u += p.step_u;
+    h += p.step_h;
+    if (u >= p.units) {
+      u -= p.units;
+      ++h;
     }
+    while (h >= nh) {
+      h -= nh;
+      ++t;
+    }
+  };
+  auto src = [&](int tok, int head) { return p.x + (t0 + tok) * p.x_ts + (h0 + head) * p.x_hs; };
+  auto dst = [&](int tok, int head) { return p.out + (t0 + tok) * p.o_ts + (h0 + head) * p.o_hs; };
+  Unit ahead[kAhead];
+  const int t_first = t, h_first = h, u_first = u;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    if ((int)threadIdx.x + k * kThreads < n) ahead[k].load(p, src(t, h), u);
+    advance();
   }
   for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
     const int tok = i / p.pairs;
@@ -145,16 +154,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     cs[i] = make_float2(c, s);
   }
   __syncthreads();
+  t = t_first, h = h_first, u = u_first;  // (walked again: registers are in-flight bytes)
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < kAhead; ++k) {
     if ((int)threadIdx.x + k * kThreads < n)
-      first[k].store(p, dst(t[k], h[k]), u[k], cs + t[k] * p.pairs);
-  for (int i = threadIdx.x + 2 * kThreads; i < n; i += kThreads) {
-    int tt, hh, uu;
-    place(i, tt, hh, uu);
+      ahead[k].store(p, dst(t, h), u, cs + t * p.pairs);
+    advance();
+  }
+  for (int i = threadIdx.x + kAhead * kThreads; i < n; i += kThreads) {
     Unit v;
-    v.load(p, src(tt, hh), uu);
-    v.store(p, dst(tt, hh), uu, cs + tt * p.pairs);
+    v.load(p, src(t, h), u);
+    v.store(p, dst(t, h), u, cs + t * p.pairs);
+    advance();
   }
 }
 
@@ -217,10 +228,12 @@ extern "C" pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_he
     p.tokens = (int)(kUnits / per_token);
     if (p.tokens > kMaxTokens) p.tokens = kMaxTokens;
     if (p.pairs > 0 && p.tokens > kMaxAngles / p.pairs) p.tokens = kMaxAngles / p.pairs;
-    // no fewer CTAs than SMs while there are tokens to spread
-    const int spread = (T + pa::num_sms() - 1) / pa::num_sms();
-    if (p.tokens > spread) p.tokens = spread;
+    // no fewer than two CTAs an SM while there are tokens to spread
+    const int spread = T / (2 * pa::num_sms());
+    if (p.tokens > spread) p.tokens = spread > 0 ? spread : 1;
   }
+  p.step_u = kThreads % p.units;
+  p.step_h = kThreads / p.units;
   const dim3 grid((unsigned)((T + p.tokens - 1) / p.tokens),
                   (unsigned)((num_heads + p.heads - 1) / p.heads));
   if (grid.y > 65535u) return PA_ERR_UNSUPPORTED;

@@ -221,7 +221,10 @@ def _dptr(t: Optional[torch.Tensor], dtype=None) -> Optional[int]:
 
 def _np_addr(a: np.ndarray) -> int:
     """Address of a contiguous numpy array's data (cheaper than .ctypes)."""
-    return a.__array_interface__["data"][0]
+    try:
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))
+    except (ValueError, TypeError):  # an empty or read-only array
+        return a.__array_interface__["data"][0]
 
 
 def _host_i32(a) -> np.ndarray:
@@ -689,13 +692,15 @@ def rope(x: torch.Tensor, out: torch.Tensor, positions: torch.Tensor, inv_freq: 
     if x.dim() != 3 or out.shape != x.shape:
         raise ValueError("x and out must be [T][H][D] of one shape")
     T, H, D = x.shape
+    pairs = inv_freq.numel()
     if positions.numel() != T:
         raise ValueError("positions must have one entry per token")
     dev = _device_of(x, "x")
+    px, po = _strided(x, "x", dev), _strided(out, "out", dev)
+    xs, os_ = x.stride(), out.stride()
     _check(lib().pa_rope(
-        _strided(x, "x", dev), x.stride(0), x.stride(1), _strided(out, "out", dev), out.stride(0),
-        out.stride(1), _flat(positions, "positions", dev, torch.int32), T, H, D,
-        _flat(inv_freq, "inv_freq", dev, torch.float32), 2 * inv_freq.numel(),
+        px, xs[0], xs[1], po, os_[0], os_[1], _flat(positions, "positions", dev, torch.int32), T, H,
+        D, _flat(inv_freq, "inv_freq", dev, torch.float32), 2 * pairs,
         PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor, _on(dev, stream)), "pa_rope")
 
 
