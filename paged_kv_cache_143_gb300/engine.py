@@ -22,6 +22,11 @@ completed; [MRV2 "재설계 3"] only diffs go to the device table; [MRV2
 
 There is no model: the caller provides the step's Q/K/V rows (token t of the
 batch is row t) and the sampled tokens.
+
+LatentEngine runs the same loop over a latent cache: pa_copy_latent_blocks,
+pa_write_latent (which turns the rotary keys by the positions that
+pa_prepare_inputs made) and, for the queries, pa_rope and pa_latent_forward
+take the places of the calls on keys and values.
 """
 from typing import Optional
 
@@ -36,7 +41,7 @@ class Engine:
                  max_blocks: int, max_tokens: int, scale: float, max_splits: int = 32,
                  device=None):
         self.sched, self.pool = sched, pool
-        self.B, self.Hq, self.D = pool.block_size, num_q_heads, pool.head_dim
+        self.B, self.Hq, self.D = pool.block_size, num_q_heads, self._out_dim(pool)
         self.max_reqs, self.max_blocks, self.max_tokens = max_reqs, max_blocks, max_tokens
         self.scale = scale
         dev = torch.device("cuda") if device is None else torch.device(device)
@@ -56,7 +61,7 @@ class Engine:
         self.done = [torch.cuda.Event(), torch.cuda.Event()]
         self.used = [False, False]
         self.dstage = torch.zeros(self.cap, **i32)
-        n = pa.forward_workspace_size(max_reqs, num_q_heads, self.D, max_splits)
+        n = self._workspace_bytes(max_splits)
         self.ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         self.mirror = np.full(max_reqs, -1, np.int64)  # stored-token count the device holds
         # each entry's last output row: gathered on the device, read back into
@@ -71,6 +76,25 @@ class Engine:
         self.steps = 0
         self.h2d_bytes = 0
         self.d2h_bytes = 0
+
+    # what a cache of another kind does otherwise
+    @staticmethod
+    def _out_dim(pool) -> int:
+        return pool.head_dim
+
+    def _workspace_bytes(self, max_splits: int) -> int:
+        return pa.forward_workspace_size(self.max_reqs, self.Hq, self.D, max_splits)
+
+    def _copy_blocks(self, src: torch.Tensor, dst: torch.Tensor, s) -> None:
+        pa.copy_blocks(self.pool, src, dst, stream=s)
+
+    def _store(self, k: torch.Tensor, v: torch.Tensor, T: int, s) -> None:
+        pa.write_kv(self.pool, k[:T], v[:T], self.slots[:T], stream=s)
+
+    def _attend(self, q: torch.Tensor, out: torch.Tensor, b: "pa.SchedBatch", R: int, T: int,
+                s) -> None:
+        pa.forward(q[:T], out[:T], self.qsl[:R + 1], self.seq[:R], b.query_start_loc, b.seq_lens,
+                   self.gathered[:R], self.pool, self.scale, 1, workspace=self.ws, stream=s)
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
              stream=None) -> "pa.SchedBatch":
@@ -117,14 +141,12 @@ class Engine:
             pa.apply_staged_writes(self.table, d[2], d[3], d[4], d[5], idx,
                                    self.gathered[:R], stream=s)
             if C:
-                pa.copy_blocks(self.pool, d[10], d[11], stream=s)
+                self._copy_blocks(d[10], d[11], s)
             pa.prepare_inputs(self.num_computed, self.table, self.B, self.pool.num_blocks, idx,
                               cnt, self.qsl[:R + 1], self.seq[:R], self.pos[:T],
                               self.slots[:T], stream=s)
-            pa.write_kv(self.pool, k[:T], v[:T], self.slots[:T], stream=s)
-            pa.forward(q[:T], out[:T], self.qsl[:R + 1], self.seq[:R], b.query_start_loc,
-                       b.seq_lens, self.gathered[:R], self.pool, self.scale, 1,
-                       workspace=self.ws, stream=s)
+            self._store(k, v, T, s)
+            self._attend(q, out, b, R, T, s)
             host = self.last_host[self.last_turn][:R]
             if R:
                 pa.gather_rows(out, d[12], self.last_dev[:R], stream=s)
@@ -140,3 +162,48 @@ class Engine:
 
     def sync(self) -> None:
         self.stream.synchronize()
+
+
+class LatentEngine(Engine):
+    """The serving loop over a latent cache (pa.LatentPool): step(q, latent,
+    k_rope, out) with q [T][Hq][L + 64] (the absorbed query, then its rotary
+    part), latent [T][L], k_rope [T][64] and out [T][Hq][L].
+
+    With inv_freq (and interleaved, factor, as pa.rope takes them) the rotary
+    parts come unturned: the keys' are turned as they are stored, the queries'
+    in place in q. Without, the caller has turned both."""
+
+    def __init__(self, sched: "pa.Scheduler", pool: "pa.LatentPool", num_q_heads: int,
+                 max_reqs: int, max_blocks: int, max_tokens: int, scale: float,
+                 inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 factor: float = 1.0, device=None):
+        super().__init__(sched, pool, num_q_heads, max_reqs, max_blocks, max_tokens, scale,
+                         device=device)
+        self.inv_freq = None if inv_freq is None else inv_freq.to(self.dev)
+        self.interleaved, self.factor = interleaved, factor
+
+    @staticmethod
+    def _out_dim(pool) -> int:
+        return pool.latent_dim
+
+    def _workspace_bytes(self, max_splits: int) -> int:
+        return pa.latent_workspace_size(self.Hq, self.D)
+
+    def _copy_blocks(self, src: torch.Tensor, dst: torch.Tensor, s) -> None:
+        pa.copy_latent_blocks(self.pool, src, dst, stream=s)
+
+    def _store(self, latent: torch.Tensor, k_rope: torch.Tensor, T: int, s) -> None:
+        turn = {} if self.inv_freq is None else dict(
+            positions=self.pos[:T], inv_freq=self.inv_freq, interleaved=self.interleaved,
+            factor=self.factor)
+        pa.write_latent(self.pool, latent[:T], k_rope[:T], self.slots[:T], stream=s, **turn)
+
+    def _attend(self, q: torch.Tensor, out: torch.Tensor, b: "pa.SchedBatch", R: int, T: int,
+                s) -> None:
+        if self.inv_freq is not None:
+            part = q[:T, :, self.D:]
+            pa.rope(part, part, self.pos[:T], self.inv_freq, interleaved=self.interleaved,
+                    factor=self.factor, stream=s)
+        pa.latent_forward(q[:T], out[:T], self.qsl[:R + 1], self.seq[:R], b.query_start_loc,
+                          b.seq_lens, self.gathered[:R], self.pool, self.scale, 1,
+                          workspace=self.ws, stream=s)
