@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
     }
     for (int s = 0; s < kSBufs; ++s) {
       mbar_init(&tail->s_full[s], 1);
-      mbar_init(&tail->s_empty[s], kScoreWarps);  // the warps that read S
+      mbar_init(&tail->s_empty[s], 4);  // the softmax warps
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tail->p_full[s], 4);   // one arrival per softmax warp
@@ -784,10 +784,11 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
 #pragma unroll
           for (int t = 0; t < RT; ++t) alpha[t] = 1.f;
           float sc[VT];              // E4M3: scales of those keys
-          const int key0 = j * KT;
+          const int key0 = j * KT, buf = g % kSBufs;
+          // (warps without rows wait too: all four release S, so that none can fall
+          // two phases of s_full behind, where a parity says nothing)
+          if (live && !(ok = wait(&tail->s_full[buf], g / kSBufs))) break;
           if (scores) {
-            const int buf = g % kSBufs;
-            if (live && !(ok = wait(&tail->s_full[buf], g / kSBufs))) break;
             tc::fence_after_sync();
             uint32_t sr[KT / 2];
             const float* s = reinterpret_cast<const float*>(sr);
@@ -893,6 +894,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               l[t] = l[t] * alpha[t] + (sum[0] + sum[1]);
             }
           }
+          if (!scores && lane == 0 && live) mbar_arrive(&tail->s_empty[buf]);
           // PV(g - 2) has read this half of P, and what was published with it
           if (g >= 2 && !(ok = wait(&tail->pv_done[g & 1], (g >> 1) - 1))) break;
           if (scores) {
@@ -945,8 +947,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           if (key0 + KT > pc.n_keys) {
             // the tile holds keys past the last visible one (unloaded blocks,
             // unwritten cells): zero them, so that P = 0 never meets a NaN (S of
-            // this tile has read them: every warp waits for it)
-            if (!scores && !(ok = wait(&tail->s_full[g % kSBufs], g / kSBufs))) break;
+            // this tile has read them)
             // the thread's chunk is (tid / 8) % kCols
             uint8_t* ks = smem + S::kOffK + (g % kStages) * S::kStage +
                           ((tid >> 3) & (kCols - 1)) * kChunk + (tid & 7) * 16;
