@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) bars->abort = 1;
     if (ok && !aborted(bars)) {
       tc::fence_after_sync();
-      // a row without a visible key is zero
-      const bool some = l_run > 0.f;
+      // a row without a visible key is zero (one with a NaN sum is not)
+      const bool some = l_run != 0.f;
       const float inv = some ? 1.f / l_run : 0.f;
       __nv_bfloat16* orow = p.out + ((int64_t)(q_begin + tok) * p.H + h) * kV;
 #pragma unroll 1

@@ -198,3 +198,21 @@ def test_device_starts_that_disagree_are_flagged(cuda_device):
     b.qsl_dev, b.ksl_dev = i32(b.qsl, dev), i32(b.ksl, dev)
     assert torch.equal(b.run().view(torch.int16), good.view(torch.int16))
     assert pa.get_error() == pa.PA_OK
+
+
+def test_rows_that_are_not_numbers(cuda_device):
+    """A NaN or an infinity in a query makes its own row NaN, and no other row
+    changes."""
+    c = Chunks([200, 3], [500, 40], 2, cuda_device, seed=31)
+    clean = c.run().clone()
+    bad = {(0, 0): (5, float("nan")), (150, 1): (DN + 2, float("inf")), (202, 0): (DN, float("nan"))}
+    for (t, h), (d, value) in bad.items():
+        c.q[t, h, d] = value
+    got = c.run()
+    assert pa.get_error() == pa.PA_OK
+    for t in range(203):
+        for h in range(2):
+            if (t, h) in bad:
+                assert torch.isnan(got[t, h]).all(), (t, h)
+            else:
+                assert torch.equal(got[t, h], clean[t, h]), (t, h)
