@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
 #pragma unroll
               for (int o = 1; o < 4; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
               if ((lane & 3) == 0) {
-                tail->l[n & 1][row[t]] = u > 0.f ? 1.f / u : 0.f;
+                tail->l[n & 1][row[t]] = u == 0.f ? 0.f : 1.f / u;  // (NaN stays NaN)
                 if (pc.slot >= 0)
                   p.part_ml[(int64_t)(2 * cta + pc.slot) * NR + row[t]] = make_float2(m[t], u);
               }
@@ -1123,7 +1123,9 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             *reinterpret_cast<uint4*>(smem + S::kOffQR + qrow * 128 +
                                       ((lane ^ (qrow & 7)) << 4)) = r;
           if (lane == 0)
-            tail->q_scale[n % kPieces][row] = __uint_as_float((uint32_t)(127 - e) << 23);
+            // (an infinity saturates as a code: the row's scores are NaN by its scale)
+            tail->q_scale[n % kPieces][row] =
+                __uint_as_float(ex == 128 ? 0x7FC00000u : (uint32_t)(127 - e) << 23);
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -1188,7 +1190,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     float top = m;
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i)
-      if (ml[i].y > 0.f) top = fmaxf(top, ml[i].x);
+      if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);  // (a NaN sum counts)
     const float keep = m == -INFINITY ? 0.f : ex2_ftz(m - top);
     m = top;
     l *= keep;
@@ -1201,7 +1203,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     }
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i) {
-      if (!(ml[i].y > 0.f)) continue;
+      if (ml[i].y == 0.f) continue;
       const float w = ex2_ftz(ml[i].x - m);
       l = fmaf(w, ml[i].y, l);
 #pragma unroll
@@ -1213,7 +1215,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2* dst = reinterpret_cast<uint2*>(p.out + (j.out_row + row) * L) + lane;
 #pragma unroll
   for (int v = 0; v < kV; ++v)

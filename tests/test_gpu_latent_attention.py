@@ -304,3 +304,40 @@ def test_bad_blocks_and_lengths_are_flagged(cuda_device):
     b.qsl_dev = i32(b.qsl, dev)
     assert torch.equal(b.run().view(torch.int16), good.view(torch.int16))
     assert pa.get_error() == pa.PA_OK
+
+
+@pytest.mark.parametrize("L", [256, 512])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_rows_that_are_not_numbers(cuda_device, fp8, L):
+    """A NaN or an infinity in a query makes its own row NaN, whether the row's
+    keys are cut over CTAs or not, and no other row changes."""
+    b = Batch([5000, 200, 40], [1, 3, 1], 20, L, 16, fp8, cuda_device, seed=21)
+    clean = b.run().clone()
+    bad = {(0, 3): (5, float("nan")), (1, 7): (L - 1, float("inf")),
+           (2, 0): (L + 3, float("nan")), (3, 19): (0, float("nan")),
+           (4, 19): (L + 63, float("-inf")), (0, 11): (17, float("-inf"))}
+    for (t, h), (d, value) in bad.items():
+        b.q[t, h, d] = value
+    got = b.run()
+    assert pa.get_error() == pa.PA_OK
+    for t in range(b.T):
+        for h in range(b.H):
+            if (t, h) in bad:
+                assert torch.isnan(got[t, h]).all(), (t, h)
+            else:
+                assert torch.equal(got[t, h], clean[t, h]), (t, h)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_a_key_of_infinite_score(cuda_device, fp8):
+    """An infinity in a key's rotary part: rows that it scores +inf are NaN, to
+    rows that it scores -inf it weighs nothing."""
+    b = Batch([3000, 90], [1, 1], 24, 512, 32, fp8, cuda_device, seed=22)
+    for r, key in ((0, 1234), (1, 50)):
+        slot = int(ref.slots_of(b.tab, r, b.seqs[r], b.B)[key])
+        b.pool.rope.view(-1, 64)[slot, 9] = float("inf")
+    got = b.run()
+    assert pa.get_error() == pa.PA_OK
+    up = b.q[:, :, 512 + 9] > 0
+    assert torch.isnan(got).all(-1)[up].all()
+    assert torch.isfinite(got)[~up].all()
