@@ -543,14 +543,24 @@ pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src,
  *                time (other streams, captured graphs that overlap) need
  *                workspaces of their own.
  *
- * Computed in fp32 (the softmax weights enter the second product rounded to
- * 16 bits), rounded once to bf16. Rows of requests with q_len == 0 and rows
+ * Computed in fp32 and rounded once to bf16; the softmax weights enter the
+ * second product rounded to bf16. On E4M3 pools the codes are multiplied as
+ * they are: the latent part of a query is taken to 2^-17 of its row's largest
+ * element, and a weight times its cell's scale to 2^-9 of itself or 2^-24 of
+ * the row's largest such product. Rows of requests with q_len == 0 and rows
  * past query_start_loc[num_reqs] are not touched.
+ * Cells past a request's seq_len may hold anything. A NaN or an infinity in a
+ * query stays in its own row of out; one in a visible latent row also reaches
+ * rows of the same request that do not see it yet (0 times it is NaN).
  * The work is divided from the device arrays at every launch; the host mirrors
  * only size the launch. A captured call therefore follows device lengths that
  * change between replays, with exact results, as long as query_start_loc
  * stays within num_tokens and each seq_len within max_blocks * block_size.
- * Host checks as pa_forward, and PA_ERR_INVALID for a workspace too small.
+ * Host checks as pa_forward, PA_ERR_INVALID for a workspace too small, and
+ * PA_ERR_UNSUPPORTED for shapes outside pa_latent_pool's and for batches past
+ * 32-bit bookkeeping: num_tokens * num_q_heads > 2^31 - 65, or
+ * (num_tokens * num_q_heads / 16 + num_reqs) * max_blocks * block_size / 32
+ * near 2^31.
  * Device checks: a request whose device entries leave those bounds (or with
  * q_len > seq_len) sets PA_ERR_DEVICE_BOUNDS and is skipped; a block id
  * outside the pool sets it too. Nothing is read or written outside the
@@ -580,8 +590,8 @@ pa_status pa_latent_forward(const void* q, void* out, const int32_t* query_start
  *   k_rope   dev bf16 [num_kv_tokens][rope_dim], shared by the heads
  *   v        dev bf16 [num_kv_tokens][num_heads][v_dim]
  *            16-byte aligned, innermost dims contiguous, token and head
- *            strides in elements, multiples of 8 (k_nope and v may be the
- *            two parts of one projection's output)
+ *            strides in elements, positive multiples of 8 (k_nope and v may
+ *            be the two parts of one projection's output)
  *   out      dev bf16 [num_tokens][num_heads][v_dim], contiguous, 16-byte aligned
  *   query_start_loc, kv_start_loc
  *            dev int32 [num_reqs+1], from 0, non-decreasing; qsl_host and
@@ -591,7 +601,10 @@ pa_status pa_latent_forward(const void* q, void* out, const int32_t* query_start
  *
  * Computed in fp32 (the softmax weights enter the second product rounded to
  * bf16), rounded once to bf16. Rows past query_start_loc[num_reqs] are not
- * touched. Supported: nope_dim 128, rope_dim 64, v_dim 128.
+ * touched; rows past kv_start_loc[num_reqs] may hold anything. A NaN or an
+ * infinity in v reaches every row of its request and head (0 times it is NaN
+ * where the row does not see it). Supported: nope_dim 128, rope_dim 64,
+ * v_dim 128. Needs no workspace.
  * Host checks: PA_ERR_INVALID (sizes, mirrors that do not end at num_tokens
  * and num_kv_tokens, strides, pointers), PA_ERR_UNSUPPORTED (other dims, more
  * than 32767 requests). Device checks: start arrays that leave the buffers or
