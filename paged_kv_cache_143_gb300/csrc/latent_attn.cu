@@ -51,9 +51,11 @@
 //     a long context's many small weights keep their share beside one large one.
 //     (Two E4M3 parts would do for weights within 2^-8 of the largest, but lose
 //     every weight below 2^-14 of it; PV is a fifth of the tensor time.)
-// For 32 rows or fewer the parts of q are stacked in the 64 rows of S: the lane
-// that reads a row's hi scores reads its lo scores too. The rotary part of q
-// and k stays bf16 and has S columns of its own, since s_n does not apply to it.
+// The parts of q are stacked in the rows of S (64, or 128 for 64 query rows),
+// those of hi above those of lo, 8 or 16 a softmax warp: the keys are read once for
+// both, and the thread that reads a row's hi scores reads its lo scores too. The
+// rotary part of q and k stays bf16 and has S columns of its own (64 rows), since
+// s_n does not apply to it.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -85,15 +87,13 @@ struct Smem {
   static constexpr int KT = latent_tile_keys(L, F8);
   static constexpr int kChunk = KT * 128;             // 128 bytes of each row of a key tile
   static constexpr int kSBufs = F8 ? 2 : 4;           // S buffers of KT columns
-  static constexpr bool kStacked = F8 && NR <= 32;    // hi and lo rows of q in one S
+  static constexpr int kM = F8 && NR > 32 ? 128 : 64; // rows of S: E4M3, hi and lo of q
   static constexpr int kCols = F8 ? L / 128 : L / 64; // 128-byte chunks of a latent row
-  static constexpr int kQRows = kStacked ? 2 * NR : NR;
-  static constexpr int kQChunk = kQRows * 128;
-  // bf16: the latent chunks, then the rotary part. E4M3: the chunks of hi (and
-  // lo, stacked), those of lo if apart, then the rotary part.
-  static constexpr int kQParts = F8 && !kStacked ? 2 : 1;
-  static constexpr int kOffQR = kQParts * kCols * kQChunk;
-  static constexpr int kQBytes = kOffQR + kQChunk;
+  // the latent chunks (E4M3: rows of hi and of lo), then the rotary part (64 rows
+  // of S at most)
+  static constexpr int kQChunk = (F8 ? 2 * NR : NR) * 128;
+  static constexpr int kOffQR = kCols * kQChunk;
+  static constexpr int kQBytes = kOffQR + (kM == 128 ? NR * 128 : kQChunk);
   static constexpr int kStage = (kCols + 1) * kChunk; // the last chunk is the rotary part
   // P of two tiles in 128-byte rows, a tile's part (bf16: all of it) in 64 bytes
   // of a row (bf16 with 64 keys: 128); part `i` of tile g starts at p_part
@@ -114,7 +114,7 @@ struct Smem {
   static_assert(kStages * KT >= 128 && kStages >= 3, "needs several key tiles in flight");
   static_assert(kAlloc <= 232448, "dynamic shared memory above the 227 KB per-block limit");
   static_assert(kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzled tiles start on 1024 bytes");
-  // S always reads 64 rows of Q: the rows past the tile's are whatever follows
+  // S reads at least 64 rows of Q: the rows past the tile's are whatever follows
   // in shared memory (their scores are never looked at)
   static_assert(kQBytes + 64 * 128 <= kAlloc - 1024, "Q over-read leaves the allocation");
 };
@@ -187,6 +187,18 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// 16 lanes x 16 columns, and the same 32 columns on: thread t has the 16 of row
+// t % 16 that start at column 32 (t / 16).
+__device__ __forceinline__ void tmem_ld_16x2x16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], 32;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
@@ -308,11 +320,11 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
   using S = Smem<L, NR, F8>;
   constexpr int kThreads = S::kThreads, kStages = S::kStages, kCols = S::kCols;
   constexpr int KT = S::KT, kChunk = S::kChunk, kSBufs = S::kSBufs;
-  constexpr int VT = KT / 4;                    // scores of a row in one thread
-  constexpr bool kStacked = S::kStacked;
   constexpr int kBlocks = L / 128;              // 128-dim blocks of O^T
-  constexpr int RT = kStacked ? 1 : 2;          // query rows of a softmax thread
-  constexpr int kWarpRows = 8 * RT;             // and of its warp
+  constexpr bool kWide = S::kM == 128;          // S: 16 rows of hi, their 16 of lo per warp
+  constexpr int RT = F8 ? 1 : 2;                // query rows of a softmax thread
+  constexpr int VT = kWide ? KT / 2 : KT / 4;   // and its scores of each
+  constexpr int kWarpRows = F8 && !kWide ? 8 : 16;  // query rows of a softmax warp
   constexpr int kScoreWarps = NR / kWarpRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -493,7 +505,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       // ------------------------------------------------------------------- S
       if (tc::elect_one()) {
         constexpr uint32_t idesc = tc::idesc_16bit_f32(64, KT, false, false, false);
-        constexpr uint32_t idesc8 = tc::idesc_e4m3_f32(64, KT);
+        constexpr uint32_t idesc8 = tc::idesc_e4m3_f32(S::kM, KT);
         const uint64_t q_desc = tc::smem_desc_sw128(smem, 16, 1024);
         const uint64_t k_desc = tc::smem_desc_sw128(smem + S::kOffK, 16, 1024);
         int g = 0, st = 0, phase = 0;
@@ -519,17 +531,14 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               tc::mma_bf16_ss(dr, tc::desc_at(q_desc, S::kOffQR + k * 32),
                               tc::desc_at(ks, kCols * kChunk + k * 32), idesc, k > 0);
 #pragma unroll
-            for (int q = 0; q < S::kQParts; ++q)
-#pragma unroll
-              for (int k = 0; k < kCols * 4; ++k) {
-                const uint64_t qa =
-                    tc::desc_at(q_desc, (q * kCols + (k >> 2)) * S::kQChunk + (k & 3) * 32);
-                const uint64_t kb = tc::desc_at(ks, (k >> 2) * kChunk + (k & 3) * 32);
-                if (F8)
-                  tc::mma_e4m3_ss(d, qa, kb, idesc8, q > 0 || k > 0);
-                else
-                  tc::mma_bf16_ss(d, qa, kb, idesc, true);
-              }
+            for (int k = 0; k < kCols * 4; ++k) {
+              const uint64_t qa = tc::desc_at(q_desc, (k >> 2) * S::kQChunk + (k & 3) * 32);
+              const uint64_t kb = tc::desc_at(ks, (k >> 2) * kChunk + (k & 3) * 32);
+              if (F8)
+                tc::mma_e4m3_ss(d, qa, kb, idesc8, k > 0);
+              else
+                tc::mma_bf16_ss(d, qa, kb, idesc, true);
+            }
             if (!live) break;
             tc::mma_commit(&tail->s_full[buf]);
             ++g;
@@ -718,7 +727,14 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       const bool scores = w4 < kScoreWarps;
       int row[RT];                               // the thread's rows of the tile
 #pragma unroll
-      for (int t = 0; t < RT; ++t) row[t] = w4 * kWarpRows + t * 8 + (lane >> 2);
+      for (int t = 0; t < RT; ++t)
+        row[t] = w4 * kWarpRows + (kWide ? lane & 15 : t * 8 + (lane >> 2));
+      // the key of the tile that score i of a thread belongs to; a row is in the
+      // threads whose numbers differ in kRowLanes
+      constexpr int kRowLanes = kWide ? 16 : 3;
+      auto key_of = [&](int i) {
+        return kWide ? (lane >> 4) * 32 + i : (i >> 1) * 8 + 2 * (lane & 3) + (i & 1);
+      };
       const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
       uint8_t* ps = smem + S::kOffP;
       const int tid = threadIdx.x - 128;
@@ -731,7 +747,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < kBlocks * NR; c += 16) {
           const int r = c % NR;  // the rows of softmax warp r / kWarpRows (and the next)
-          if (((asked >> (r / kWarpRows * 8)) & (RT == 1 ? 0xFFFF : 0xFF)) == 0) continue;
+          if (((asked >> (r / kWarpRows * 8)) & (kWarpRows == 8 ? 0xFFFF : 0xFF)) == 0) continue;
           uint32_t o[16];
           tmem_ld16(tmem + lanes + c, o);
           tc::tmem_wait_ld();
@@ -779,7 +795,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         const int lim_min = RT == 2 ? min(lim[0], lim[RT - 1]) : lim[0];
 #pragma unroll 1
         for (int j = pc.k0; j < pc.k1; ++j) {
-          float x[RT][VT];           // key 8 i + 2 (lane % 4) + b of the tile at [2 i + b]
+          float x[RT][VT];           // of keys key_of(0), ..
           float alpha[RT];
 #pragma unroll
           for (int t = 0; t < RT; ++t) alpha[t] = 1.f;
@@ -788,47 +804,72 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           // (warps without rows wait too: all four release S, so that none can fall
           // two phases of s_full behind, where a parity says nothing)
           if (live && !(ok = wait(&tail->s_full[buf], g / kSBufs))) break;
+          bool p_free = false;
           if (scores) {
+            // (a test of a barrier answers after about 200 cycles beside the products'
+            // reads of shared memory: they are asked ahead of their use)
+            bool keys_in = true;
+            if constexpr (F8) keys_in = mbar_test_wait(&tail->k_full[g % kStages],
+                                                       (g / kStages) & 1);
             tc::fence_after_sync();
             uint32_t sr[KT / 2];
             const float* s = reinterpret_cast<const float*>(sr);
+            const uint32_t ts = tmem + kTmemS + buf * KT + lanes;
+            const uint32_t tr = tmem + kTmemR + buf * KT + lanes;
 #pragma unroll
-            for (int c = 0; c < KT; c += 32)
-              tmem_ld_16x32(tmem + kTmemS + buf * KT + c + lanes, sr + c / 2);
+            for (int c = 0; c < KT; c += 32) {
+              if constexpr (kWide)  // 16 columns of hi, of lo
+                tmem_ld_16x2x16(ts + ((uint32_t)(c / 2) << 16), sr + c / 2);
+              else
+                tmem_ld_16x32(ts + c, sr + c / 2);
+            }
             if constexpr (F8) {
               // (the stage's scales came with its keys)
-              if (live && !(ok = wait(&tail->k_full[g % kStages], g / kStages))) break;
+              if (live && !__all_sync(0xffffffffu, keys_in) &&
+                  !(ok = wait(&tail->k_full[g % kStages], g / kStages)))
+                break;
               uint32_t rr[KT / 2];
               const float* rs = reinterpret_cast<const float*>(rr);
+              if constexpr (kWide) {
+                tmem_ld_16x2x16(tr, rr);
+              } else {
 #pragma unroll
-              for (int c = 0; c < KT; c += 32)
-                tmem_ld_16x32(tmem + kTmemR + buf * KT + c + lanes, rr + c / 2);
-              if (j == pc.k0) {
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-                  qs[t] = tail->q_scale[n & (kPieces - 1)][row[t]];
+                for (int c = 0; c < KT; c += 32) tmem_ld_16x32(tr + c, rr + c / 2);
               }
-              const float2* st = reinterpret_cast<const float2*>(tail->scale[g % kStages]);
+              if (j == pc.k0) qs[0] = tail->q_scale[n & (kPieces - 1)][row[0]];
+              const float* st = tail->scale[g % kStages];
+              if constexpr (kWide) {
 #pragma unroll
-              for (int i = 0; i < VT / 2; ++i) {
-                const float2 v = st[4 * i + (lane & 3)];
-                sc[2 * i] = v.x;
-                sc[2 * i + 1] = v.y;
+                for (int i = 0; i < VT; i += 4)
+                  *reinterpret_cast<float4*>(sc + i) =
+                      *reinterpret_cast<const float4*>(st + key_of(i));
+              } else {
+#pragma unroll
+                for (int i = 0; i < VT; i += 2)
+                  *reinterpret_cast<float2*>(sc + i) =
+                      *reinterpret_cast<const float2*>(st + key_of(i));
               }
               if (key0 + KT > pc.n_keys) {  // unwritten cells' scales may be anything
 #pragma unroll
                 for (int i = 0; i < VT; ++i)
-                  if (key0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1) >= pc.n_keys) sc[i] = 0.f;
+                  if (key0 + key_of(i) >= pc.n_keys) sc[i] = 0.f;
               }
               tc::tmem_wait_ld();
+              if constexpr (kWide) {
 #pragma unroll
-              for (int i = 0; i < VT; ++i) {
-                const int a = (i >> 1) * 4 + (i & 1);
-                if constexpr (kStacked) {
+                for (int i = 0; i < 16; ++i) x[0][i] = fmaf((s[i] + s[i + 16]) * qs[0], sc[i], rs[i]);
+                tmem_ld_16x2x16(ts + 16, sr);
+                tmem_ld_16x2x16(ts + 16 + (16u << 16), sr + 16);
+                tmem_ld_16x2x16(tr + 16, rr);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  x[0][VT - 16 + i] = fmaf((s[i] + s[i + 16]) * qs[0], sc[VT - 16 + i], rs[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < VT; ++i) {
+                  const int a = (i >> 1) * 4 + (i & 1);
                   x[0][i] = fmaf((s[a] + s[a + 2]) * qs[0], sc[i], rs[a]);
-                } else {
-                  x[0][i] = fmaf(s[a] * qs[0], sc[i], rs[a]);
-                  x[RT - 1][i] = fmaf(s[a + 2] * qs[RT - 1], sc[i], rs[a + 2]);
                 }
               }
             } else {
@@ -841,10 +882,13 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             }
             tc::fence_before_sync();
             if (lane == 0 && live) mbar_arrive(&tail->s_empty[buf]);
+            // (not for 64 bf16 rows: there PV(g - 2) is rarely done by now; 1.3% slower)
+            if ((F8 || NR <= 32) && g >= 2)
+              p_free = mbar_test_wait(&tail->pv_done[g & 1], ((g >> 1) - 1) & 1);
             if (key0 + KT > lim_min) {
 #pragma unroll
               for (int i = 0; i < VT; ++i) {
-                const int key = key0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1);
+                const int key = key0 + key_of(i);
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
                   if (key >= lim[t]) x[t][i] = -INFINITY;
@@ -869,7 +913,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                                fmax3(y[i + 4], y[i + 5], fmaxf(y[i + 6], y[i + 7])));
             }
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1)
+            for (int o = 1; o <= kRowLanes; o <<= 1)
+              if (o & kRowLanes)
 #pragma unroll
               for (int t = 0; t < RT; ++t)
                 top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], o));
@@ -896,31 +941,48 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           }
           if (!scores && lane == 0 && live) mbar_arrive(&tail->s_empty[buf]);
           // PV(g - 2) has read this half of P, and what was published with it
-          if (g >= 2 && !(ok = wait(&tail->pv_done[g & 1], (g >> 1) - 1))) break;
+          if (g >= 2 && !__all_sync(0xffffffffu, p_free) &&
+              !(ok = wait(&tail->pv_done[g & 1], (g >> 1) - 1)))
+            break;
           if (scores) {
             if constexpr (F8) {
               // weights p s in three parts, a byte a key: an f16 number's high byte is
               // its E5M2 truncation, so a part is the high byte after half a step is
               // added to the magnitude, and what is left is exact in f16
+              uint8_t* prow = ps + row[0] * 128 + (kWide ? 0 : (lane & 3) * 2);
+              uint32_t bytes[3][VT / 4];  // wide: the codes of 4 keys each
 #pragma unroll
-              for (int t = 0; t < RT; ++t) {
-                uint8_t* prow = ps + row[t] * 128 + (lane & 3) * 2;
+              for (int i = 0; i < VT / 2; ++i) {
+                __half2 h = __floats2half2_rn(x[0][2 * i] * sc[2 * i],
+                                              x[0][2 * i + 1] * sc[2 * i + 1]);
 #pragma unroll
-                for (int i = 0; i < VT / 2; ++i) {
-                  __half2 h = __floats2half2_rn(x[t][2 * i] * sc[2 * i],
-                                                x[t][2 * i + 1] * sc[2 * i + 1]);
-#pragma unroll
-                  for (int part = 0; part < 3; ++part) {
-                    const uint32_t code =
-                        (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xFF00FF00u;
-                    h = __hsub2(h, *reinterpret_cast<const __half2*>(&code));
+                for (int part = 0; part < 3; ++part) {
+                  const uint32_t code =
+                      (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xFF00FF00u;
+                  h = __hsub2(h, *reinterpret_cast<const __half2*>(&code));
+                  if constexpr (kWide) {
+                    bytes[part][i >> 1] =
+                        (i & 1) ? __byte_perm(bytes[part][i >> 1], code, 0x7531) : code;
+                  } else {
                     const int off = (g & 1) ? S::p_part(1, part) : S::p_part(0, part);
                     const int gran = (off >> 4 & 7) + (i >> 1);  // 16 keys a granule
                     *reinterpret_cast<uint16_t*>(prow + (off & ~127) + (i & 1) * 8 +
-                                                 ((gran ^ (row[t] & 7)) << 4)) =
+                                                 ((gran ^ (row[0] & 7)) << 4)) =
                         (uint16_t)__byte_perm(code, 0u, 0x4431);
                   }
                 }
+              }
+              if constexpr (kWide) {
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    const int off = (g & 1) ? S::p_part(1, part) : S::p_part(0, part);
+                    const int gran = (off >> 4 & 7) + (lane >> 4) * 2 + u;
+                    *reinterpret_cast<uint4*>(prow + (off & ~127) + ((gran ^ (row[0] & 7)) << 4)) =
+                        make_uint4(bytes[part][4 * u], bytes[part][4 * u + 1],
+                                   bytes[part][4 * u + 2], bytes[part][4 * u + 3]);
+                  }
               }
             } else {
               const int mi = lane >> 3;  // the 8x8 matrix whose row this lane addresses
@@ -938,8 +1000,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             }
           }
           const bool ask = __any_sync(0xffffffffu, alpha[0] < 1.f || alpha[RT - 1] < 1.f);
-          // (stacked: a rescale takes the rows of two warps, either may have asked)
-          if (scores && (ask || RT == 1) && (lane & 3) == 0) {
+          // (8 rows a warp: a rescale takes the rows of two, either may have asked)
+          if (scores && (ask || kWarpRows == 8) && (lane & kRowLanes) == 0) {
 #pragma unroll
             for (int t = 0; t < RT; ++t) tail->alpha[g & 1][row[t]] = alpha[t];
           }
@@ -960,8 +1022,9 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             for (int t = 0; t < RT; ++t) {
               float u = l[t];
 #pragma unroll
-              for (int o = 1; o < 4; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-              if ((lane & 3) == 0) {
+              for (int o = 1; o <= kRowLanes; o <<= 1)
+                if (o & kRowLanes) u += __shfl_xor_sync(0xffffffffu, u, o);
+              if ((lane & kRowLanes) == 0) {
                 tail->l[n & 1][row[t]] = u == 0.f ? 0.f : 1.f / u;  // (NaN stays NaN)
                 if (pc.slot >= 0)
                   p.part_ml[(int64_t)(2 * cta + pc.slot) * NR + row[t]] = make_float2(m[t], u);
@@ -1104,14 +1167,15 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               lo[k] |= e4m3_pair(x - hx, y - hy) << (16 * b);
             }
           }
-          const int qrow = kStacked ? (row >> 3) * 16 + (row & 7) : row;
-          const int lrow = kStacked ? qrow + 8 : row;
+          // a softmax warp's rows of hi, then of lo
+          const int qrow = row / kWarpRows * 2 * kWarpRows + row % kWarpRows;
+          const int lrow = qrow + kWarpRows, rrow = kWide ? row : qrow;
           const int block = lane * kPer / 128, byte = lane * kPer % 128;
           auto place = [&](int off, int at) {
             return smem + off + at * 128 + (((byte >> 4) ^ (at & 7)) << 4) + (byte & 15);
           };
           uint8_t* dh = place(block * S::kQChunk, qrow);
-          uint8_t* dl = place(((kStacked ? 0 : kCols) + block) * S::kQChunk, lrow);
+          uint8_t* dl = place(block * S::kQChunk, lrow);
           if constexpr (kPer == 16) {
             *reinterpret_cast<uint4*>(dh) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(dl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -1120,8 +1184,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             *reinterpret_cast<uint2*>(dl) = make_uint2(lo[0], lo[1]);
           }
           if (lane < 8)
-            *reinterpret_cast<uint4*>(smem + S::kOffQR + qrow * 128 +
-                                      ((lane ^ (qrow & 7)) << 4)) = r;
+            *reinterpret_cast<uint4*>(smem + S::kOffQR + rrow * 128 +
+                                      ((lane ^ (rrow & 7)) << 4)) = r;
           if (lane == 0)
             // (an infinity saturates as a code: the row's scores are NaN by its scale)
             tail->q_scale[n % kPieces][row] =
