@@ -31,11 +31,13 @@
 //               ring of four; it also asks L2 for a coming piece's first cells
 //   warps 4-7   softmax (S read as 16 x 256-bit fragments: a row in four lanes),
 //               P to shared memory; then the output
-//   warps 8-11  (E4M3) the query tile as E4M3 parts
+//   warps 8-11  (E4M3) the query tile as E4M3 parts; at L 256 then the softmax of
+//               the odd tiles, warps 4-7 that of the even ones
 // The instruction cache is cold at launch and, once all SMs stream, a miss takes
 // microseconds: S, PV and softmax run once on whatever memory holds while the
 // first keys are on their way (S and O are overwritten by the first real products).
-// The softmax warps share nothing tile by tile. A warp that moves a row's
+// The softmax warps of a group share nothing tile by tile (the two groups of E4M3
+// pools hand the rows' references on). A warp that moves a row's
 // reference maximum says so beside P; warp 2 then asks all four to rescale
 // their dims of O before it issues that PV (rare: growth by more than 2^8).
 // Every wait is bounded; a timeout sets the error word and the CTA unwinds.
@@ -88,6 +90,11 @@ struct Smem {
   static constexpr int kChunk = KT * 128;             // 128 bytes of each row of a key tile
   static constexpr int kSBufs = F8 ? 2 : 4;           // S buffers of KT columns
   static constexpr int kM = F8 && NR > 32 ? 128 : 64; // rows of S: E4M3, hi and lo of q
+  // E4M3: the warps that convert queries also take the softmax of odd tiles. With
+  // weights in three parts it takes one group 2500 cycles a tile; at L 256 the
+  // products take 1200 (152 x 4096 keys: 64 rows 103 us with one group, 84 with two,
+  // 16 rows 79 and 66), at L 512 as long as the softmax (119 and 122)
+  static constexpr bool kTwo = F8 && L == 256;
   static constexpr int kCols = F8 ? L / 128 : L / 64; // 128-byte chunks of a latent row
   // the latent chunks (E4M3: rows of hi and of lo), then the rotary part (64 rows
   // of S at most)
@@ -104,7 +111,7 @@ struct Smem {
     const int u = (g & 1) * kPartsP + part;
     return kPartBytes == 128 ? u * NR * 128 : (u >> 1) * NR * 128 + (u & 1) * 64;
   }
-  static constexpr int kTail = F8 ? 5120 : 2048;      // barriers, pieces, row statistics
+  static constexpr int kTail = F8 ? 8192 : 2048;      // barriers, pieces, row statistics
   static constexpr int kFit = (232448 - 1024 - kTail - kQBytes - kPBytes) / kStage;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kOffK = kQBytes;
@@ -140,17 +147,22 @@ struct Tail {
   uint64_t fix, fixed;           // O is to be rescaled for tile fix_tile; it has been
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t o_empty, final_mma;
+  // two softmax groups, by warp: the reference after an even / odd tile is
+  // there; the second group's sums of a piece are; and (all) 1 / sum is
+  uint64_t m_full[4][2], sum_full[4][kPieces], l_full;
   Piece piece[kPieces];
   alignas(16) float alpha[2][kLatentRows];   // by tile: factors of the rows of a warp that asks
   alignas(16) float l[2][kLatentRows];       // by piece: 1 / sum
   alignas(16) float scale[F8 ? kMaxStages : 1][64];      // E4M3: of the stage's keys
-  float q_scale[F8 ? kPieces : 1][kLatentRows];          // E4M3: 2^-e of the rows
+  float q_scale[F8 ? kPieces : 1][F8 ? kLatentRows : 1]; // E4M3: 2^-e of the rows
+  float m_ref[2][F8 ? kLatentRows : 1];                  // by tile: the rows' references
+  float2 sums[F8 ? kPieces : 1][F8 ? kLatentRows : 1];            // (reference, sum) of a piece
   alignas(4) uint8_t ask[2][4];  // by tile: softmax warps that ask for a rescale
   int32_t fix_tile;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Tail<true>) <= 5120 && sizeof(Tail<false>) <= 2048, "Tail overruns its slot");
+static_assert(sizeof(Tail<true>) <= 8192 && sizeof(Tail<false>) <= 2048, "Tail overruns its slot");
 
 // pa::mbar_wait without its timer: a cold line of instructions costs microseconds
 // once all SMs stream, and the timer's loop is one that every first wait would
@@ -325,6 +337,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
   constexpr int RT = F8 ? 1 : 2;                // query rows of a softmax thread
   constexpr int VT = kWide ? KT / 2 : KT / 4;   // and its scores of each
   constexpr int kWarpRows = F8 && !kWide ? 8 : 16;  // query rows of a softmax warp
+  constexpr bool kTwo = S::kTwo;                // two softmax groups
   constexpr int kScoreWarps = NR / kWarpRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -374,6 +387,13 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
     mbar_init(&tail->fixed, 4);
     mbar_init(&tail->o_empty, 4);
     mbar_init(&tail->final_mma, 2);
+    if (kTwo) {
+      for (int w = 0; w < 4; ++w) {
+        for (int s = 0; s < 2; ++s) mbar_init(&tail->m_full[w][s], 1);
+        for (int s = 0; s < kPieces; ++s) mbar_init(&tail->sum_full[w][s], 1);
+      }
+      mbar_init(&tail->l_full, 4);
+    }
     tail->abort = 0;
     fence_mbar_init();
   }
@@ -721,9 +741,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       }
       if (!ok && lane == 0) tail->abort = 1;
       __syncwarp();
-    } else if (warp < 8) {
+    } else {
       // ---------------------------------------------------- softmax and output
-      const int w4 = warp - 4;
+      const int w4 = warp & 3;
+      const bool second = F8 && warp >= 8;       // the group of the odd tiles
       const bool scores = w4 < kScoreWarps;
       int row[RT];                               // the thread's rows of the tile
 #pragma unroll
@@ -737,7 +758,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       };
       const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
       uint8_t* ps = smem + S::kOffP;
-      const int tid = threadIdx.x - 128;
+      const int tid = threadIdx.x & 127;
       int fixes = 0;
       // this warp's dims of O times the new factors of the rows that ask
       auto rescale = [&]() {
@@ -762,17 +783,90 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         if (lane == 0) mbar_arrive(&tail->fixed);
         ++fixes;
       };
-      // Waits for a barrier, doing the rescales that are asked for meanwhile.
+      // Waits for a barrier, doing the rescales that are asked for meanwhile (warps
+      // 4-7: they hold all lanes of O between them).
       auto wait = [&](uint64_t* bar, int parity) -> bool {
 #pragma unroll 1
         for (unsigned i = 0; i < 64 * kTries; ++i) {
           if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
-          if (__all_sync(0xffffffffu, mbar_test_wait(&tail->fix, fixes & 1))) rescale();
+          if (!second && __all_sync(0xffffffffu, mbar_test_wait(&tail->fix, fixes & 1)))
+            rescale();
         }
         if (lane == 0) raise_error(p.err, kErrTimeout);
         return false;
       };
-      int g = 0;
+      // E4M3: the rows of the piece's query tile as two parts (warps 8-11)
+      auto convert = [&](const Piece& pc, int n) {
+        constexpr int kPer = L / 32;             // dims of a lane: 16 or 8
+#pragma unroll 2
+        for (int i = 0; i < NR / 4; ++i) {
+          const int row = i * 4 + w4;
+          // (rows past the tile's are zeros)
+          uint4 v[kPer / 8], r = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < kPer / 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
+          if (row < pc.rows) {
+            const __nv_bfloat16* src = p.q + (int64_t)(pc.row + row) * (L + kRope);
+#pragma unroll
+            for (int k = 0; k < kPer / 8; ++k)
+              v[k] = __ldg(reinterpret_cast<const uint4*>(src + lane * kPer) + k);
+            if (lane < 8) r = __ldg(reinterpret_cast<const uint4*>(src + L) + lane);
+          }
+          float f[kPer], amax = 0.f;
+#pragma unroll
+          for (int k = 0; k < kPer / 8; ++k) bf16x8_to_f32(v[k], f + 8 * k);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) amax = fmaxf(amax, fabsf(f[k]));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // 2^e brings the largest magnitude to [2^7, 2^8); exact
+          const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+          const int e = amax > 0.f ? min(100, max(-120, 7 - ex)) : 0;
+          const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+          uint32_t hi[kPer / 4], lo[kPer / 4];
+#pragma unroll
+          for (int k = 0; k < kPer / 4; ++k) {
+            hi[k] = lo[k] = 0u;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float x = f[4 * k + 2 * b] * up, y = f[4 * k + 2 * b + 1] * up;
+              const uint32_t h = e4m3_pair(x, y);
+              float hx, hy;
+              e4m3x2_to_f32((uint16_t)h, hx, hy);
+              hi[k] |= h << (16 * b);
+              lo[k] |= e4m3_pair(x - hx, y - hy) << (16 * b);
+            }
+          }
+          // a softmax warp's rows of hi, then of lo
+          const int qrow = row / kWarpRows * 2 * kWarpRows + row % kWarpRows;
+          const int lrow = qrow + kWarpRows, rrow = kWide ? row : qrow;
+          const int block = lane * kPer / 128, byte = lane * kPer % 128;
+          auto place = [&](int off, int at) {
+            return smem + off + at * 128 + (((byte >> 4) ^ (at & 7)) << 4) + (byte & 15);
+          };
+          uint8_t* dh = place(block * S::kQChunk, qrow);
+          uint8_t* dl = place(block * S::kQChunk, lrow);
+          if constexpr (kPer == 16) {
+            *reinterpret_cast<uint4*>(dh) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint2*>(dh) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dl) = make_uint2(lo[0], lo[1]);
+          }
+          if (lane < 8)
+            *reinterpret_cast<uint4*>(smem + S::kOffQR + rrow * 128 +
+                                      ((lane ^ (rrow & 7)) << 4)) = r;
+          if (lane == 0)
+            // (an infinity saturates as a code: the row's scores are NaN by its scale)
+            tail->q_scale[n % kPieces][row] =
+                __uint_as_float(ex == 128 ? 0x7FC00000u : (uint32_t)(127 - e) << 23);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->q_full);
+      };
+      int g = second ? 1 : 0;  // tiles so far (the tile of nothing: one of the group's)
       bool ok = true;
 #pragma unroll 1
       for (int n = -1;; ++n) {
@@ -780,6 +874,16 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         const Piece pc = piece(n, ok);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || pc.r < 0) break;
+        if constexpr (F8) {
+          if (second && live) {
+            if (n > 0 && !(ok = wait(&tail->q_empty, n - 1))) break;
+            convert(pc, n);
+          }
+          if (second && !kTwo) {
+            if (live && lane == 0) release(n);
+            continue;
+          }
+        }
         int lim[RT];                 // keys the rows see
         float m[RT], l[RT], qs[RT];  // reference (log2), sum; E4M3: 2^-e of the query
 #pragma unroll
@@ -795,6 +899,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         const int lim_min = RT == 2 ? min(lim[0], lim[RT - 1]) : lim[0];
 #pragma unroll 1
         for (int j = pc.k0; j < pc.k1; ++j) {
+          if (kTwo && (g & 1) != (int)second) {  // the other group's tile
+            ++g;
+            continue;
+          }
           float x[RT][VT];           // of keys key_of(0), ..
           float alpha[RT];
 #pragma unroll
@@ -812,16 +920,18 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             if constexpr (F8) keys_in = mbar_test_wait(&tail->k_full[g % kStages],
                                                        (g / kStages) & 1);
             tc::fence_after_sync();
-            uint32_t sr[KT / 2];
+            uint32_t sr[kWide ? KT : KT / 2];
             const float* s = reinterpret_cast<const float*>(sr);
             const uint32_t ts = tmem + kTmemS + buf * KT + lanes;
             const uint32_t tr = tmem + kTmemR + buf * KT + lanes;
 #pragma unroll
             for (int c = 0; c < KT; c += 32) {
-              if constexpr (kWide)  // 16 columns of hi, of lo
-                tmem_ld_16x2x16(ts + ((uint32_t)(c / 2) << 16), sr + c / 2);
-              else
+              if constexpr (kWide) {  // 16 columns of hi, of lo
+                tmem_ld_16x2x16(ts + c / 2, sr + c);
+                tmem_ld_16x2x16(ts + c / 2 + (16u << 16), sr + c + 16);
+              } else {
                 tmem_ld_16x32(ts + c, sr + c / 2);
+              }
             }
             if constexpr (F8) {
               // (the stage's scales came with its keys)
@@ -832,11 +942,12 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               const float* rs = reinterpret_cast<const float*>(rr);
               if constexpr (kWide) {
                 tmem_ld_16x2x16(tr, rr);
+                tmem_ld_16x2x16(tr + 16, rr + 16);
               } else {
 #pragma unroll
                 for (int c = 0; c < KT; c += 32) tmem_ld_16x32(tr + c, rr + c / 2);
               }
-              if (j == pc.k0) qs[0] = tail->q_scale[n & (kPieces - 1)][row[0]];
+              if (j < pc.k0 + (kTwo ? 2 : 1)) qs[0] = tail->q_scale[n & (kPieces - 1)][row[0]];
               const float* st = tail->scale[g % kStages];
               if constexpr (kWide) {
 #pragma unroll
@@ -857,14 +968,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               tc::tmem_wait_ld();
               if constexpr (kWide) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[0][i] = fmaf((s[i] + s[i + 16]) * qs[0], sc[i], rs[i]);
-                tmem_ld_16x2x16(ts + 16, sr);
-                tmem_ld_16x2x16(ts + 16 + (16u << 16), sr + 16);
-                tmem_ld_16x2x16(tr + 16, rr);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  x[0][VT - 16 + i] = fmaf((s[i] + s[i + 16]) * qs[0], sc[VT - 16 + i], rs[i]);
+                for (int i = 0; i < VT; ++i) {
+                  const int a = (i & 16) * 2 + (i & 15);
+                  x[0][i] = fmaf((s[a] + s[a + 16]) * qs[0], sc[i], rs[i]);
+                }
               } else {
 #pragma unroll
                 for (int i = 0; i < VT; ++i) {
@@ -885,6 +992,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             // (not for 64 bf16 rows: there PV(g - 2) is rarely done by now; 1.3% slower)
             if ((F8 || NR <= 32) && g >= 2)
               p_free = mbar_test_wait(&tail->pv_done[g & 1], ((g >> 1) - 1) & 1);
+            bool m_there = false;
+            if constexpr (kTwo) {
+              if (g > 0) m_there = mbar_test_wait(&tail->m_full[w4][(g - 1) & 1], ((g - 1) >> 1) & 1);
+            }
             if (key0 + KT > lim_min) {
 #pragma unroll
               for (int i = 0; i < VT; ++i) {
@@ -918,6 +1029,17 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
 #pragma unroll
               for (int t = 0; t < RT; ++t)
                 top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], o));
+            float own[RT];                 // the reference that l is kept by
+            if constexpr (kTwo) {
+              // the tile before is the other group's: its warp of the same rows hands
+              // over the reference (waited for across pieces too, so that neither
+              // group can fall two tiles behind)
+              own[0] = m[0];
+              if (live && g > 0 && !__all_sync(0xffffffffu, m_there) &&
+                  !(ok = wait(&tail->m_full[w4][(g - 1) & 1], (g - 1) >> 1)))
+                break;
+              m[0] = j > pc.k0 ? tail->m_ref[(g - 1) & 1][row[0]] : -INFINITY;
+            }
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
               if (!F8) top[t] *= p.scale_log2;
@@ -929,6 +1051,11 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                 alpha[t] = ex2_ftz(m[t] - top[t]);
                 m[t] = top[t];
               }
+              if constexpr (kTwo) {
+                if ((lane & kRowLanes) == 0) tail->m_ref[g & 1][row[0]] = m[0];
+                __syncwarp();
+                if (lane == 0 && live) mbar_arrive(&tail->m_full[w4][g & 1]);
+              }
               const float neg = m[t] == -INFINITY ? 0.f : kTargetLog2<F8> - m[t];
               float sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -936,7 +1063,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                 x[t][i] = ex2_ftz(fmaf(x[t][i], p.scale_log2, neg));
                 sum[i & 1] += x[t][i];
               }
-              l[t] = l[t] * alpha[t] + (sum[0] + sum[1]);
+              const float keep = !kTwo ? alpha[t] : own[t] == m[t] ? 1.f : ex2_ftz(own[t] - m[t]);
+              l[t] = l[t] * keep + (sum[0] + sum[1]);
             }
           }
           if (!scores && lane == 0 && live) mbar_arrive(&tail->s_empty[buf]);
@@ -1016,7 +1144,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             for (int i = pc.n_keys - key0 + tid / (8 * kCols); i < KT; i += 16 / kCols)
               *reinterpret_cast<uint4*>(ks + i * 128) = make_uint4(0, 0, 0, 0);
           }
-          if (j == pc.k1 - 1 && scores) {
+          if (!kTwo && j == pc.k1 - 1 && scores) {
             // the piece's sums, before the arrival that its output waits behind
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
@@ -1039,7 +1167,43 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           ++g;
         }
         if (!ok) break;
-        if (!live) continue;
+        if (!live) {
+          g = 0;
+          continue;
+        }
+        if constexpr (kTwo) {
+          // the groups' sums of the piece, joined by the first
+          float u = l[0];
+#pragma unroll
+          for (int o = 1; o <= kRowLanes; o <<= 1)
+            if (o & kRowLanes) u += __shfl_xor_sync(0xffffffffu, u, o);
+          if (second) {
+            if (scores && (lane & kRowLanes) == 0)
+              tail->sums[n % kPieces][row[0]] = make_float2(m[0], u);
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&tail->sum_full[w4][n % kPieces]);
+              release(n);
+            }
+            continue;
+          }
+          // (released pieces bound how far the second group runs ahead)
+          if (!(ok = wait(&tail->sum_full[w4][n % kPieces], n / kPieces))) break;
+          if (scores) {
+            const float2 o = tail->sums[n % kPieces][row[0]];
+            const float top = fmaxf(m[0], o.x);
+            u = u * (m[0] == top ? 1.f : ex2_ftz(m[0] - top)) +
+                o.y * (o.x == top ? 1.f : ex2_ftz(o.x - top));
+            if ((lane & kRowLanes) == 0) {
+              tail->l[n & 1][row[0]] = u == 0.f ? 0.f : 1.f / u;  // (NaN stays NaN)
+              if (pc.slot >= 0)
+                p.part_ml[(int64_t)(2 * cta + pc.slot) * NR + row[0]] = make_float2(top, u);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tail->l_full);
+          if (!(ok = wait(&tail->l_full, n))) break;
+        }
 
         // ---- the piece's rows: normalised to out, or a partial
         if (!(ok = wait(&tail->pv_done[(g - 1) & 1], (g - 1) >> 1))) break;
@@ -1112,89 +1276,6 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&tail->o_empty);
-          release(n);
-        }
-      }
-      if (!ok) tail->abort = 1;
-    } else if constexpr (F8) {
-      // ------------------------------------------------------- query as E4M3
-      const int w4 = warp - 8;
-      bool ok = true;
-      constexpr int kPer = L / 32;               // dims of a lane: 16 or 8
-      for (int n = 0;; ++n) {
-        const Piece pc = piece(n, ok);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok || pc.r < 0) break;
-        if (n > 0 && !(ok = __all_sync(0xffffffffu, bar_wait(&tail->q_empty, (n - 1) & 1, p.err))))
-          break;
-#pragma unroll 2
-        for (int i = 0; i < NR / 4; ++i) {
-          const int row = i * 4 + w4;
-          // (rows past the tile's are zeros)
-          uint4 v[kPer / 8], r = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int k = 0; k < kPer / 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
-          if (row < pc.rows) {
-            const __nv_bfloat16* src = p.q + (int64_t)(pc.row + row) * (L + kRope);
-#pragma unroll
-            for (int k = 0; k < kPer / 8; ++k)
-              v[k] = __ldg(reinterpret_cast<const uint4*>(src + lane * kPer) + k);
-            if (lane < 8) r = __ldg(reinterpret_cast<const uint4*>(src + L) + lane);
-          }
-          float f[kPer], amax = 0.f;
-#pragma unroll
-          for (int k = 0; k < kPer / 8; ++k) bf16x8_to_f32(v[k], f + 8 * k);
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) amax = fmaxf(amax, fabsf(f[k]));
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // 2^e brings the largest magnitude to [2^7, 2^8); exact
-          const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-          const int e = amax > 0.f ? min(100, max(-120, 7 - ex)) : 0;
-          const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-          uint32_t hi[kPer / 4], lo[kPer / 4];
-#pragma unroll
-          for (int k = 0; k < kPer / 4; ++k) {
-            hi[k] = lo[k] = 0u;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const float x = f[4 * k + 2 * b] * up, y = f[4 * k + 2 * b + 1] * up;
-              const uint32_t h = e4m3_pair(x, y);
-              float hx, hy;
-              e4m3x2_to_f32((uint16_t)h, hx, hy);
-              hi[k] |= h << (16 * b);
-              lo[k] |= e4m3_pair(x - hx, y - hy) << (16 * b);
-            }
-          }
-          // a softmax warp's rows of hi, then of lo
-          const int qrow = row / kWarpRows * 2 * kWarpRows + row % kWarpRows;
-          const int lrow = qrow + kWarpRows, rrow = kWide ? row : qrow;
-          const int block = lane * kPer / 128, byte = lane * kPer % 128;
-          auto place = [&](int off, int at) {
-            return smem + off + at * 128 + (((byte >> 4) ^ (at & 7)) << 4) + (byte & 15);
-          };
-          uint8_t* dh = place(block * S::kQChunk, qrow);
-          uint8_t* dl = place(block * S::kQChunk, lrow);
-          if constexpr (kPer == 16) {
-            *reinterpret_cast<uint4*>(dh) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            *reinterpret_cast<uint2*>(dh) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dl) = make_uint2(lo[0], lo[1]);
-          }
-          if (lane < 8)
-            *reinterpret_cast<uint4*>(smem + S::kOffQR + rrow * 128 +
-                                      ((lane ^ (rrow & 7)) << 4)) = r;
-          if (lane == 0)
-            // (an infinity saturates as a code: the row's scores are NaN by its scale)
-            tail->q_scale[n % kPieces][row] =
-                __uint_as_float(ex == 128 ? 0x7FC00000u : (uint32_t)(127 - e) << 23);
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&tail->q_full);
           release(n);
         }
       }

@@ -114,6 +114,8 @@ SHAPES = [  # seq_lens, q_lens, H, L, B
     ([12000, 1, 1, 12000], [1, 1, 1, 3], 64, 512, 64),
     ([17] * 400, [1] * 400, 16, 256, 16),          # more requests than threads
     ([64] * 152 + [1], [1] * 153, 8, 512, 32),
+    ([64] * 450, [1] * 450, 40, 256, 64),          # pieces of one tile each
+    ([70, 1, 130, 200, 64] * 50, [1, 1, 2, 1, 1] * 50, 24, 256, 32),
 ]
 
 
