@@ -1494,9 +1494,10 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
   for (int r = 0; r < R; ++r)
     widest = std::max<int64_t>(widest, (int64_t)(qsl_host[r + 1] - qsl_host[r]) * Hq);
   const int NR = widest <= 16 ? 16 : widest <= 32 ? 32 : 64;
-  // CTAs side by side (LatentParams): a tile of keys costs a CTA about 1300
-  // cycles of products and HBM 1570 cycles of an SM's share; two CTAs on the same
-  // keys share the latter (more would gain nothing: the products then bound).
+  // CTAs side by side (LatentParams): two on the same keys read them from HBM once
+  // and then take 0.93 of the time for a pair of row tiles, but an odd one leaves a CTA
+  // idle: 32 requests x 4096 keys, 4 row tiles 116 us alone and 106 side by side, 5 132
+  // and 150 (more than two would gain nothing: the products bound).
   const int sms = std::min(pa::num_sms(), pa::kLatentMaxCtas);
   int64_t W = 0, best = INT64_MAX;
   int G = 1;
@@ -1508,7 +1509,7 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
         w += ((rows + NR - 1) / NR + lanes - 1) / lanes *
              ((seq_lens_host[r] + KT - 1) / KT);
     }
-    const int64_t cost = w * std::max(1570, 1300 * lanes);
+    const int64_t cost = w * (lanes == 1 ? 100 : 2 * 93);
     if (lanes <= sms && cost < best) {
       best = cost;
       W = w;
