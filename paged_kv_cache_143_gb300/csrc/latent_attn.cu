@@ -258,7 +258,7 @@ __device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
 
 struct Request {
   int32_t q_begin, q_len, seq, rows, keys;  // query rows, key tiles
-  int32_t weight;                           // passes * keys; 0 for one without work
+  int32_t weight;                           // passes * (skip + keys); 0 for one without work
 };
 
 // Reads request r; one whose device entries do not fit the buffers has no
@@ -278,7 +278,8 @@ __device__ __forceinline__ Request load_request(const LatentParams& p, int r, bo
   q.rows = q.q_len * p.Hq;  // (T * Hq fits 32 bits)
   q.keys = (q.seq + KT - 1) / KT;
   const int tiles = (q.rows + NR - 1) / NR;
-  q.weight = (p.lanes == 1 ? tiles : (tiles + 1) / 2) * q.keys;  // (the host bounds the sum)
+  // (the host bounds the sum)
+  q.weight = (p.lanes == 1 ? tiles : (tiles + 1) / 2) * (p.skip + q.keys);
   return q;
 }
 
@@ -303,12 +304,14 @@ struct Walk {
       if (++r >= p.R) return false;
       q = load_request<NR, KT>(p, r, false);
     }
-    const unsigned off = pos - base;
-    const int pass = (int)(off / (unsigned)q.keys), tile = pass * p.lanes + lane;
+    const unsigned off = pos - base, span = p.skip + q.keys;
+    const int pass = (int)(off / span), tile = pass * p.lanes + lane;
+    const int at = (int)(off - pass * span), stop = min((int)span, at + (end - pos));
+    pos += stop - at;
+    if (stop <= p.skip) return false;  // (the range ends before the pass's keys)
     out.r = r;
-    out.k0 = (int)off - pass * q.keys;
-    const int k1 = min(q.keys, out.k0 + (end - pos));
-    pos += k1 - out.k0;
+    out.k0 = max(0, at - p.skip);
+    const int k1 = stop - p.skip;
     out.slot = out.k0 > 0 ? 0 : k1 < q.keys ? 1 : -1;
     out.row = q.q_begin * p.Hq + tile * NR;
     out.rows = max(0, min(NR, q.rows - tile * NR));  // 0: the pass has fewer tiles
@@ -709,8 +712,9 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           // the pass cut at this group's start, for the join: handled at its first cut
           LatentJoin join{};
           if (begin < end) {
-            const int at = begin - base, pass = at / q.keys;
-            const unsigned a = begin - (at - pass * q.keys);  // the pass's start
+            const int at = begin - base, pass = at / (p.skip + q.keys);
+            // the pass's first tile
+            const unsigned a = begin - (at - pass * (p.skip + q.keys)) + p.skip;
             const int row0 = (pass * p.lanes + in_group) * NR;
             if ((unsigned)begin > a && a / Q + 1 == (unsigned)group && row0 < q.rows) {
               join.rows = min(q.rows - row0, NR);
@@ -721,10 +725,11 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           if (lane == 0) p.joins[cta] = join;
         }
         // a later piece's first tiles and queries, towards L2 while the ones
-        // before are worked on (16 keys a lane)
-        if (more && n > 0) {
+        // before are worked on (16 keys a lane; E4M3: queries of the first one too,
+        // which are read in two rounds)
+        if (more && (n > 0 || F8)) {
           const int key = pc.k0 * KT + lane * 16;
-          if (lane < 8 && key < pc.n_keys) {
+          if (n > 0 && lane < 8 && key < pc.n_keys) {
             const int32_t id = __ldg(p.block_tables + (int64_t)pc.r * p.max_blocks +
                                      (key >> p.b_shift));
             if (id >= 0 && id < p.num_blocks) {
@@ -798,69 +803,88 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       // E4M3: the rows of the piece's query tile as two parts (warps 8-11)
       auto convert = [&](const Piece& pc, int n) {
         constexpr int kPer = L / 32;             // dims of a lane: 16 or 8
-#pragma unroll 2
-        for (int i = 0; i < NR / 4; ++i) {
-          const int row = i * 4 + w4;
+        // Eight rows of a warp on their way at a time: once the keys stream, a load
+        // takes microseconds (two at a time, the first S came 15 us into the kernel)
+        constexpr int kBatch = NR / 4 < 8 ? NR / 4 : 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < NR / 4; i0 += kBatch) {
+          uint4 v[kBatch][kPer / 8], rot[kBatch / 4];  // rot: 8 lanes a row
+          const __nv_bfloat16* src = p.q + (int64_t)pc.row * (L + kRope);
           // (rows past the tile's are zeros)
-          uint4 v[kPer / 8], r = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int k = 0; k < kPer / 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
-          if (row < pc.rows) {
-            const __nv_bfloat16* src = p.q + (int64_t)(pc.row + row) * (L + kRope);
+          for (int b = 0; b < kBatch; ++b) {
+            const int row = (i0 + b) * 4 + w4;
 #pragma unroll
             for (int k = 0; k < kPer / 8; ++k)
-              v[k] = __ldg(reinterpret_cast<const uint4*>(src + lane * kPer) + k);
-            if (lane < 8) r = __ldg(reinterpret_cast<const uint4*>(src + L) + lane);
+              v[b][k] = row < pc.rows
+                            ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * (L + kRope) +
+                                                                   lane * kPer) + k)
+                            : make_uint4(0, 0, 0, 0);
           }
-          float f[kPer], amax = 0.f;
 #pragma unroll
-          for (int k = 0; k < kPer / 8; ++k) bf16x8_to_f32(v[k], f + 8 * k);
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) amax = fmaxf(amax, fabsf(f[k]));
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // 2^e brings the largest magnitude to [2^7, 2^8); exact
-          const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-          const int e = amax > 0.f ? min(100, max(-120, 7 - ex)) : 0;
-          const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-          uint32_t hi[kPer / 4], lo[kPer / 4];
-#pragma unroll
-          for (int k = 0; k < kPer / 4; ++k) {
-            hi[k] = lo[k] = 0u;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const float x = f[4 * k + 2 * b] * up, y = f[4 * k + 2 * b + 1] * up;
-              const uint32_t h = e4m3_pair(x, y);
-              float hx, hy;
-              e4m3x2_to_f32((uint16_t)h, hx, hy);
-              hi[k] |= h << (16 * b);
-              lo[k] |= e4m3_pair(x - hx, y - hy) << (16 * b);
-            }
+          for (int u = 0; u < kBatch / 4; ++u) {
+            const int row = (i0 + u * 4 + (lane >> 3)) * 4 + w4;
+            rot[u] = row < pc.rows
+                         ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * (L + kRope) + L) +
+                                 (lane & 7))
+                         : make_uint4(0, 0, 0, 0);
           }
           // a softmax warp's rows of hi, then of lo
-          const int qrow = row / kWarpRows * 2 * kWarpRows + row % kWarpRows;
-          const int lrow = qrow + kWarpRows, rrow = kWide ? row : qrow;
-          const int block = lane * kPer / 128, byte = lane * kPer % 128;
-          auto place = [&](int off, int at) {
-            return smem + off + at * 128 + (((byte >> 4) ^ (at & 7)) << 4) + (byte & 15);
-          };
-          uint8_t* dh = place(block * S::kQChunk, qrow);
-          uint8_t* dl = place(block * S::kQChunk, lrow);
-          if constexpr (kPer == 16) {
-            *reinterpret_cast<uint4*>(dh) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            *reinterpret_cast<uint2*>(dh) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dl) = make_uint2(lo[0], lo[1]);
+          auto hi_row = [&](int row) { return row / kWarpRows * 2 * kWarpRows + row % kWarpRows; };
+#pragma unroll
+          for (int u = 0; u < kBatch / 4; ++u) {
+            const int row = (i0 + u * 4 + (lane >> 3)) * 4 + w4, at = kWide ? row : hi_row(row);
+            *reinterpret_cast<uint4*>(smem + S::kOffQR + at * 128 +
+                                      (((lane & 7) ^ (at & 7)) << 4)) = rot[u];
           }
-          if (lane < 8)
-            *reinterpret_cast<uint4*>(smem + S::kOffQR + rrow * 128 +
-                                      ((lane ^ (rrow & 7)) << 4)) = r;
-          if (lane == 0)
-            // (an infinity saturates as a code: the row's scores are NaN by its scale)
-            tail->q_scale[n % kPieces][row] =
-                __uint_as_float(ex == 128 ? 0x7FC00000u : (uint32_t)(127 - e) << 23);
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int row = (i0 + b) * 4 + w4;
+            float f[kPer], amax = 0.f;
+#pragma unroll
+            for (int k = 0; k < kPer / 8; ++k) bf16x8_to_f32(v[b][k], f + 8 * k);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) amax = fmaxf(amax, fabsf(f[k]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // 2^e brings the largest magnitude to [2^7, 2^8); exact
+            const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+            const int e = amax > 0.f ? min(100, max(-120, 7 - ex)) : 0;
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            uint32_t hi[kPer / 4], lo[kPer / 4];
+#pragma unroll
+            for (int k = 0; k < kPer / 4; ++k) {
+              hi[k] = lo[k] = 0u;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float x = f[4 * k + 2 * h] * up, y = f[4 * k + 2 * h + 1] * up;
+                const uint32_t code = e4m3_pair(x, y);
+                float hx, hy;
+                e4m3x2_to_f32((uint16_t)code, hx, hy);
+                hi[k] |= code << (16 * h);
+                lo[k] |= e4m3_pair(x - hx, y - hy) << (16 * h);
+              }
+            }
+            const int qrow = hi_row(row), lrow = qrow + kWarpRows;
+            const int block = lane * kPer / 128, byte = lane * kPer % 128;
+            auto place = [&](int off, int at) {
+              return smem + off + at * 128 + (((byte >> 4) ^ (at & 7)) << 4) + (byte & 15);
+            };
+            uint8_t* dh = place(block * S::kQChunk, qrow);
+            uint8_t* dl = place(block * S::kQChunk, lrow);
+            if constexpr (kPer == 16) {
+              *reinterpret_cast<uint4*>(dh) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(dl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+              *reinterpret_cast<uint2*>(dh) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(dl) = make_uint2(lo[0], lo[1]);
+            }
+            if (lane == 0)
+              // (an infinity saturates as a code: the row's scores are NaN by its scale)
+              tail->q_scale[n % kPieces][row] =
+                  __uint_as_float(ex == 128 ? 0x7FC00000u : (uint32_t)(127 - e) << 23);
+          }
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -1499,27 +1523,34 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
   // idle: 32 requests x 4096 keys, 4 row tiles 116 us alone and 106 side by side, 5 132
   // and 150 (more than two would gain nothing: the products bound).
   const int sms = std::min(pa::num_sms(), pa::kLatentMaxCtas);
-  int64_t W = 0, best = INT64_MAX;
+  int64_t W = 0, passes = 0, best = INT64_MAX;
   int G = 1;
   for (int lanes = 1; lanes <= 2; ++lanes) {
-    int64_t w = 0;
+    int64_t w = 0, n = 0;
     for (int r = 0; r < R; ++r) {
       const int64_t rows = (int64_t)(qsl_host[r + 1] - qsl_host[r]) * Hq;
-      if (rows > 0)
-        w += ((rows + NR - 1) / NR + lanes - 1) / lanes *
-             ((seq_lens_host[r] + KT - 1) / KT);
+      if (rows == 0) continue;
+      const int64_t of_r = ((rows + NR - 1) / NR + lanes - 1) / lanes;
+      n += of_r;
+      w += of_r * ((seq_lens_host[r] + KT - 1) / KT);
     }
     const int64_t cost = w * (lanes == 1 ? 100 : 2 * 93);
     if (lanes <= sms && cost < best) {
       best = cost;
       W = w;
+      passes = n;
       G = lanes;
     }
     if (widest <= NR) break;  // one row tile each
   }
+  // A pass begins with its queries and ends with its output, which stalls its CTA
+  // for 2 to 4 us, 3 to 5 tiles: it counts as 4 tiles more in the shares (less where
+  // shares are small). 160 decodes 58.8 -> 56.5 us, 24 x 4 drafted tokens 30.2 -> 26.7.
+  const int skip = (int)std::min<int64_t>(4, W / (sms / G) / 2);
+  W += passes * skip;
   // the flat space stays within 31 bits whatever the device lengths are
   const int64_t most = ((int64_t)T * Hq / NR + R) *
-                       (((int64_t)max_blocks * pool->block_size + KT - 1) / KT);
+                       (skip + ((int64_t)max_blocks * pool->block_size + KT - 1) / KT);
   if (most > INT32_MAX) return PA_ERR_UNSUPPORTED;
   const int grid = G * (int)std::min<int64_t>(W, sms / G);
   if (workspace_bytes < pa::scratch_bytes(grid, NR, L)) return PA_ERR_INVALID;
@@ -1542,6 +1573,7 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
   p.b_shift = p.B == 16 ? 4 : p.B == 32 ? 5 : 6;
   p.causal = causal;
   p.lanes = G;
+  p.skip = skip;
   p.scale_log2 = scale * 1.4426950408889634f;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.joins = reinterpret_cast<pa::LatentJoin*>(ws);

@@ -19,7 +19,8 @@ constexpr int kLatentMaxCtas = 1024;
 // space". The grid is NG groups of G CTAs (G 1 or 2) that walk it side by
 // side: a pass (request r, row tiles i G .. i G + G - 1 of NR query rows, one to
 // each CTA of the group) takes the C_r = ceil(seq_len / KT) key tiles of the
-// request, at pref[r] + i C_r, pref the exclusive running sum of passes_r C_r.
+// request, behind S places without a tile (what a pass costs besides its tiles), at
+// pref[r] + i (S + C_r), pref the exclusive running sum of passes_r (S + C_r).
 // Group b takes the tiles [b Q, b Q + Q), Q = ceil(W / NG): equal shares whatever
 // the lengths, and a cell that several row tiles need is read from HBM once,
 // by the first of the group's CTAs that comes to it. A CTA's pieces are the parts
@@ -52,6 +53,7 @@ struct LatentParams {
   int32_t T, R, Hq, max_blocks, num_blocks, B, b_shift;  // B = 1 << b_shift
   int32_t causal;
   int32_t lanes;               // G
+  int32_t skip;                // S of the flat space
   float scale_log2;            // softmax scale * log2(e)
   LatentJoin* joins;           // [grid]
   float2* part_ml;             // [2 grid][NR] (max in log2 units, sum)
