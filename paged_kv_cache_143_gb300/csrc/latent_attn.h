@@ -35,9 +35,9 @@ constexpr int kLatentMaxCtas = 1024;
 // computed from the device arrays at every launch, so a captured call follows
 // lengths that change.
 struct LatentJoin {       // what the join needs of a CTA's first piece
-  int32_t rows;           // query rows of the tile cut at its start; 0: none, or
-                          // joined at an earlier cut
+  int32_t rows;           // query rows of the tile cut at its start; 0: none
   int32_t pieces;         // partials of that tile
+  int32_t cut;            // which of its cuts this is
   int64_t out_row;        // its first row in out
 };
 
