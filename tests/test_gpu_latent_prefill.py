@@ -77,6 +77,13 @@ SHAPES = [  # q_lens, k_lens, H
     ([700], [2100], 2),
     ([33, 520], [33, 520], 16),
     ([2] * 70, [3] * 70, 1),
+    # few units, split along their keys over a cluster of CTAs
+    ([5], [3000], 1),
+    ([40, 3], [2000, 9000], 2),
+    ([300], [5000], 1),
+    ([1, 2, 130], [4000, 10, 700], 3),
+    ([1500], [1450], 1),
+    ([257, 1], [2300, 1100], 8),
 ]
 
 
@@ -216,3 +223,31 @@ def test_rows_that_are_not_numbers(cuda_device):
                 assert torch.isnan(got[t, h]).all(), (t, h)
             else:
                 assert torch.equal(got[t, h], clean[t, h]), (t, h)
+
+
+def test_split_units_captured_flagged_and_beside_nan(cuda_device):
+    """Units that a cluster of CTAs shares: replayed from a graph, with device
+    starts that disagree, and with NaN in every row of nobody."""
+    dev = cuda_device
+    b = Chunks([30, 70], [2500, 1300], 2, dev, seed=41, spare=50)
+    first = b.run().clone()
+    b.check()
+    for t in (b.k, b.v, b.kr):
+        t[b.ksl[-1]:] = float("nan")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        b.run()
+    b.out.fill_(9.0)
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert pa.get_error() == pa.PA_OK
+    assert torch.equal(b.out[:100].view(torch.int16), first[:100].view(torch.int16))
+    assert (b.out[100:] == 9).all()
+    for q, k in (([0, 30, 151], None), ([0, -1, 100], None), (None, [0, 2500, 3851]),
+                 (None, [0, 3900, 3800])):
+        b.qsl_dev = i32(b.qsl if q is None else q, dev)
+        b.ksl_dev = i32(b.ksl if k is None else k, dev)
+        b.run()
+        assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS, (q, k)
