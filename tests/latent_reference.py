@@ -46,7 +46,8 @@ def e4m3_round(x):
     _, e = np.frexp(np.where(np.isfinite(x), x, 1.0))
     step = np.exp2(np.maximum(e - 4, -9).astype(np.float64))
     with np.errstate(invalid="ignore"):
-        return np.where(np.isinf(x), np.sign(x) * 448, np.clip(np.round(x / step) * step, -448, 448))
+        near = np.clip(np.round(x / step) * step, -448, 448)
+        return np.where(np.isinf(x), np.sign(x) * 448, near)
 
 
 def token_scale(row):
