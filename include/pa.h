@@ -437,7 +437,8 @@ pa_status pa_gather_rows(const void* src, int64_t src_rows, int64_t row_bytes,
  * Angles are exact to about 2^-24 of a turn at any position; fp32 arithmetic, one
  * rounding to bf16 (nearest-even). The inverse turn is the same call with
  * negated positions and 1 / factor. Errors: PA_ERR_INVALID (sizes, strides,
- * NULL or misaligned pointers), PA_ERR_UNSUPPORTED (odd rot_dim or above 256).
+ * NULL or misaligned pointers), PA_ERR_UNSUPPORTED (odd rot_dim or above 256,
+ * head_dim above 32768).
  */
 typedef enum pa_rope_layout { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
 

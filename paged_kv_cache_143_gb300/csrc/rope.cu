@@ -8,8 +8,9 @@
 // tokens' cosines and sines once into shared memory, while its vectors of x are
 // already on their way (four units of 16 or 32 bytes a thread), and every head
 // reuses them. fp32 arithmetic, one rounding to bf16. Measured: 8192 tokens x 32
-// heads x 128 dims (64 turned) in 28.8 us, 4650 GB/s (two units in flight 35 us, five
-// CTAs an SM instead of four 37); 256 x 64 x 64 interleaved in 3.6 us, a launch.
+// heads x 128 dims (64 turned, half layout) in 24.7 us, 5430 GB/s (bound by HBM and by
+// instructions about alike); x 128 heads x 64 dims, interleaved, 52 us, 5130 GB/s (three
+// units in flight and five CTAs an SM: 23.1 and 58); 256 x 64 x 64 in 3.6 us, a launch.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "rope_angle.cuh"
@@ -22,6 +23,7 @@ constexpr int kUnits = kAhead * kThreads;  // units a CTA aims at
 constexpr int kMaxPairs = 128;   // rot_dim <= 256
 constexpr int kMaxTokens = 64;   // tokens of one CTA
 constexpr int kMaxAngles = 1024; // (token, pair) angles of one CTA
+constexpr int kMaxDim = 32768;   // of a head, for the exact reciprocals
 
 struct RopeParams {
   const __nv_bfloat16* x;
@@ -30,12 +32,17 @@ struct RopeParams {
   const float* inv_freq;
   int64_t x_ts, x_hs, o_ts, o_hs;  // token and head strides, elements
   int32_t T, H, pairs, interleaved;
-  int32_t units;                   // units per head (rotated ones first, then copied ones)
-  int32_t rot_units;
+  int32_t rot_units, pass_units;   // units per head that are turned, and copied
   int32_t tokens, heads;           // of one CTA
-  int32_t step_u, step_h;          // kThreads units on: units, and whole heads
+  uint32_t by_rot, by_pass, by_heads;  // reciprocals of rot_units, pass_units and H
   float factor;
 };
+
+// i / d by d's reciprocal 2^32 / d + 1 (0 for d = 1), exact while i * d < 2^32.
+uint32_t reciprocal(int32_t d) { return d <= 1 ? 0u : (uint32_t)((1ull << 32) / d + 1); }
+__device__ __forceinline__ int divide(int i, uint32_t by) {
+  return by == 0u ? i : (int)__umulhi((uint32_t)i, by);
+}
 
 // A unit of the vector form: 8 dims (4 pairs) of the interleaved layout; 8 + 8
 // dims (8 pairs) of the half layout; 8 dims passed through.
@@ -70,19 +77,23 @@ struct VecUnit {
     float f[8];
     pa::bf16x8_to_f32(a, f);
     if (p.interleaved) {
+      const float4* cs2 = reinterpret_cast<const float4*>(cs + u * 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = cs[u * 4 + i];
-        pa::rope_turn(f[2 * i], f[2 * i + 1], t.x, t.y);
+      for (int i = 0; i < 2; ++i) {
+        const float4 t = cs2[i];
+        pa::rope_turn(f[4 * i], f[4 * i + 1], t.x, t.y);
+        pa::rope_turn(f[4 * i + 2], f[4 * i + 3], t.z, t.w);
       }
       *reinterpret_cast<uint4*>(dst) = pack(f);
     } else {
       float g[8];
       pa::bf16x8_to_f32(b, g);
+      const float4* cs2 = reinterpret_cast<const float4*>(cs + u * 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 t = cs[u * 8 + i];
-        pa::rope_turn(f[i], g[i], t.x, t.y);
+      for (int i = 0; i < 4; ++i) {
+        const float4 t = cs2[i];
+        pa::rope_turn(f[2 * i], g[2 * i], t.x, t.y);
+        pa::rope_turn(f[2 * i + 1], g[2 * i + 1], t.z, t.w);
       }
       *reinterpret_cast<uint4*>(dst) = pack(f);
       *reinterpret_cast<uint4*>(dst + p.pairs) = pack(g);
@@ -115,38 +126,37 @@ struct ScalarUnit {
   }
 };
 
-// grid (token groups, head groups). In place (out == x) is safe: a unit's dims
+// grid (token groups, head groups). A CTA's turned units come first, then its
+// copied ones, so that a warp does one of the two (mixed, a warp went through both:
+// 160 instructions for 16 bytes a lane). In place (out == x) is safe: a unit's dims
 // are read and written by one thread, and its loads come first.
 template <typename Unit>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
-  __shared__ float2 cs[kMaxAngles];
+  __shared__ alignas(16) float2 cs[kMaxAngles];
   const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
   const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.H - h0);
-  const int per_token = nh * p.units, n = nt * per_token;
-  // the thread's unit, moved on by kThreads at a time without dividing
-  int t = threadIdx.x / per_token;
-  int u = threadIdx.x - t * per_token, h = u / p.units;
-  u -= h * p.units;
-  auto advance = [&]() {
-    u += p.step_u;
-    h += p.step_h;
-    if (u >= p.units) {
-      u -= p.units;
-      ++h;
-    }
-    while (h >= nh) {
-      h -= nh;
-      ++t;
-    }
+  const int turned = nt * nh * p.rot_units, n = turned + nt * nh * p.pass_units;
+  struct Place {
+    int tok, head, unit;
   };
-  auto src = [&](int tok, int head) { return p.x + (t0 + tok) * p.x_ts + (h0 + head) * p.x_hs; };
-  auto dst = [&](int tok, int head) { return p.out + (t0 + tok) * p.o_ts + (h0 + head) * p.o_hs; };
+  auto place = [&](int i) {
+    const bool rot = i < turned;
+    const int j = rot ? i : i - turned;
+    const int at = divide(j, rot ? p.by_rot : p.by_pass);  // token by token, head by head
+    const int unit = j - at * (rot ? p.rot_units : p.pass_units) + (rot ? 0 : p.rot_units);
+    const int tok = p.tokens == 1 ? 0 : divide(at, p.by_heads);  // (then nh = H)
+    return Place{tok, at - tok * nh, unit};
+  };
+  const __nv_bfloat16* x = p.x + t0 * p.x_ts + h0 * p.x_hs;
+  __nv_bfloat16* out = p.out + t0 * p.o_ts + h0 * p.o_hs;
   Unit ahead[kAhead];
-  const int t_first = t, h_first = h, u_first = u;
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
-    if ((int)threadIdx.x + k * kThreads < n) ahead[k].load(p, src(t, h), u);
-    advance();
+    const int i = threadIdx.x + k * kThreads;
+    if (i < n) {
+      const Place at = place(i);
+      ahead[k].load(p, x + at.tok * p.x_ts + at.head * p.x_hs, at.unit);
+    }
   }
   for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
     const int tok = i / p.pairs;
@@ -156,18 +166,19 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
     cs[i] = make_float2(c, s);
   }
   __syncthreads();
-  t = t_first, h = h_first, u = u_first;  // (walked again: registers are in-flight bytes)
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
-    if ((int)threadIdx.x + k * kThreads < n)
-      ahead[k].store(p, dst(t, h), u, cs + t * p.pairs);
-    advance();
+    const int i = threadIdx.x + k * kThreads;
+    if (i < n) {
+      const Place at = place(i);  // (found again: registers are in-flight bytes)
+      ahead[k].store(p, out + at.tok * p.o_ts + at.head * p.o_hs, at.unit, cs + at.tok * p.pairs);
+    }
   }
   for (int i = threadIdx.x + kAhead * kThreads; i < n; i += kThreads) {
+    const Place at = place(i);
     Unit v;
-    v.load(p, src(t, h), u);
-    v.store(p, dst(t, h), u, cs + t * p.pairs);
-    advance();
+    v.load(p, x + at.tok * p.x_ts + at.head * p.x_hs, at.unit);
+    v.store(p, out + at.tok * p.o_ts + at.head * p.o_hs, at.unit, cs + at.tok * p.pairs);
   }
 }
 
@@ -182,7 +193,8 @@ extern "C" pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_he
     return PA_ERR_INVALID;
   if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_INVALID;
   if (!(factor > 0.f) || factor > 3.0e38f) return PA_ERR_INVALID;
-  if (rot_dim % 2 != 0 || rot_dim > 2 * kMaxPairs) return PA_ERR_UNSUPPORTED;
+  if (rot_dim % 2 != 0 || rot_dim > 2 * kMaxPairs || head_dim > kMaxDim)
+    return PA_ERR_UNSUPPORTED;
   if (T == 0) return PA_OK;
   if (!x || !out || !positions || (rot_dim > 0 && !inv_freq)) return PA_ERR_INVALID;
   // rows [token][head] of out must not share elements: heads inside tokens, or
@@ -217,10 +229,11 @@ extern "C" pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_he
                    (p.interleaved ? rot_dim : p.pairs) % 8 == 0;
   const int pass = x == out ? 0 : head_dim - rot_dim;  // dims copied
   p.rot_units = vec ? (p.interleaved ? rot_dim / 8 : p.pairs / 8) : p.pairs;
-  p.units = p.rot_units + (vec ? pass / 8 : pass);
-  if (p.units == 0) return PA_OK;  // in place, nothing turned
+  p.pass_units = vec ? pass / 8 : pass;
+  const int units = p.rot_units + p.pass_units;
+  if (units == 0) return PA_OK;  // in place, nothing turned
   // CTAs of about kUnits units: several tokens of few heads, or some heads of one token
-  const int64_t per_token = (int64_t)num_heads * p.units;
+  const int64_t per_token = (int64_t)num_heads * units;
   p.tokens = 1;
   p.heads = num_heads;
   if (per_token > kUnits) {
@@ -234,8 +247,9 @@ extern "C" pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_he
     const int spread = T / (2 * pa::num_sms());
     if (p.tokens > spread) p.tokens = spread > 0 ? spread : 1;
   }
-  p.step_u = kThreads % p.units;
-  p.step_h = kThreads / p.units;
+  p.by_rot = reciprocal(p.rot_units);
+  p.by_pass = reciprocal(p.pass_units);
+  p.by_heads = reciprocal(num_heads);
   const dim3 grid((unsigned)((T + p.tokens - 1) / p.tokens),
                   (unsigned)((num_heads + p.heads - 1) / p.heads));
   if (grid.y > 65535u) return PA_ERR_UNSUPPORTED;

@@ -94,6 +94,7 @@ def test_rope_refusals():
         assert call(**bad) == pa.PA_ERR_INVALID, bad
     assert call(rot=31) == pa.PA_ERR_UNSUPPORTED
     assert call(D=512, rot=258, xh=512, oh=512, xt=2048, ot=2048) == pa.PA_ERR_UNSUPPORTED
+    assert call(H=1, D=32776, xt=40000, ot=40000) == pa.PA_ERR_UNSUPPORTED
 
 
 def test_binding_checks_without_a_device():
