@@ -595,14 +595,18 @@ PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
 LATENT_ROPE_DIM = 64  # rotary dims of a latent cell
 
 
+# A decode step's calls are small enough for their Python to show, so the calls
+# below test everything about their tensors in one expression and look for the one
+# at fault (_explain) only where it fails. The current device and its stream come
+# from what torch.cuda.current_device() and current_stream() call themselves.
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
 def _device_of(t: torch.Tensor, what: str) -> int:
     """The current device, on which a call's first tensor must be."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    # (what torch.cuda.current_device() and, below, current_stream() return,
-    # without their Python layers: a decode step's calls are small enough for
-    # the difference to show)
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{what} is on {t.device}, not on the current device")
     return dev
@@ -615,33 +619,22 @@ def _on(dev: int, stream) -> int:
     return _stream(stream)
 
 
-def _refuse(t: torch.Tensor, what: str, dtype, dev: int) -> None:
-    if not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    raise ValueError(f"{what} is on {t.device}, the call on cuda:{dev}")
-
-
-def _strided(t: torch.Tensor, what: str, dev: int, dtype=torch.bfloat16) -> int:
-    """Device pointer of a tensor on device `dev` whose innermost dimension is
-    contiguous (0 for an empty one)."""
-    if t.get_device() != dev or t.dtype is not dtype:
-        _refuse(t, what, dtype, dev)
-    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
-        raise ValueError(f"{what}: the innermost dimension must be contiguous")
-    return t.data_ptr()
-
-
-def _flat(t: Optional[torch.Tensor], what: str, dev: int, dtype) -> Optional[int]:
-    """Device pointer of a contiguous tensor on device `dev` (None stays None)."""
-    if t is None:
-        return None
-    if t.get_device() != dev or t.dtype is not dtype:
-        _refuse(t, what, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor")
-    return t.data_ptr()
+def _explain(dev: int, *tensors) -> None:
+    """Raises for the first of the (tensor, name, dtype, flat) that is not on device
+    `dev`, of another type or not contiguous (flat; else in its last dimension)."""
+    for t, what, dtype, flat in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what}: expected a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what} is on {t.device}, the call on cuda:{dev}")
+        if flat and not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous tensor")
+        if not flat and t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+            raise ValueError(f"{what}: the innermost dimension must be contiguous")
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
@@ -689,19 +682,27 @@ def rope(x: torch.Tensor, out: torch.Tensor, positions: torch.Tensor, inv_freq: 
          interleaved: bool = False, factor: float = 1.0, stream=None) -> None:
     """Turns the first 2 * len(inv_freq) dims of every head of x [T][H][D] by
     positions * inv_freq into out (which may be x); the other dims are copied."""
-    if x.dim() != 3 or out.shape != x.shape:
+    shape = x.shape
+    if len(shape) != 3 or out.shape != shape:
         raise ValueError("x and out must be [T][H][D] of one shape")
-    T, H, D = x.shape
-    pairs = inv_freq.numel()
+    T, H, D = shape
     if positions.numel() != T:
         raise ValueError("positions must have one entry per token")
     dev = _device_of(x, "x")
-    px, po = _strided(x, "x", dev), _strided(out, "out", dev)
-    xs, os_ = x.stride(), out.stride()
-    _check(lib().pa_rope(
-        px, xs[0], xs[1], po, os_[0], os_[1], _flat(positions, "positions", dev, torch.int32), T, H,
-        D, _flat(inv_freq, "inv_freq", dev, torch.float32), 2 * pairs,
-        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor, _on(dev, stream)), "pa_rope")
+    xt, xh, xd = x.stride()
+    ot, oh, od = out.stride()
+    if not (xd == 1 == od and x.dtype is _BF16 is out.dtype and positions.dtype is _I32
+            and inv_freq.dtype is _F32
+            and out.get_device() == positions.get_device() == inv_freq.get_device() == dev
+            and positions.is_contiguous() and inv_freq.is_contiguous()):
+        _explain(dev, (x, "x", _BF16, False), (out, "out", _BF16, False),
+                 (positions, "positions", _I32, True), (inv_freq, "inv_freq", _F32, True))
+    st = (_lib or lib()).pa_rope(
+        x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, positions.data_ptr(), T, H, D,
+        inv_freq.data_ptr(), 2 * inv_freq.numel(),
+        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor, _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_rope")
 
 
 class LatentPool:
@@ -728,10 +729,12 @@ class LatentPool:
         self.rope_dim = rope.shape[2]
 
     def struct(self, dev: int) -> _LatentPool:
-        return _LatentPool(_flat(self.latent, "latent", dev, self.latent.dtype),
-                           _flat(self.rope, "rope", dev, torch.bfloat16),
-                           _flat(self.scales, "scales", dev, torch.float32), self.num_blocks,
-                           self.block_size, self.latent_dim, self.rope_dim, self.dtype)
+        _explain(dev, (self.latent, "latent", self.latent.dtype, True),
+                 (self.rope, "rope", _BF16, True), (self.scales, "scales", _F32, True))
+        return _LatentPool(self.latent.data_ptr(), self.rope.data_ptr(),
+                           None if self.scales is None else self.scales.data_ptr(),
+                           self.num_blocks, self.block_size, self.latent_dim, self.rope_dim,
+                           self.dtype)
 
     def ref(self, dev: int):
         """ctypes reference to the pool's C struct, built once per device and
@@ -749,13 +752,6 @@ class LatentPool:
         object.__setattr__(self, name, value)
 
 
-def _tokens(t: torch.Tensor, width: int, what: str) -> int:
-    """Token stride of rows [T][width]."""
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{what} must be [tokens][{width}]")
-    return t.stride(0) if t.shape[0] > 1 else (width + 7) // 8 * 8
-
-
 def write_latent(pool: LatentPool, latent: torch.Tensor, k_rope: torch.Tensor,
                  slot_mapping: torch.Tensor, positions: Optional[torch.Tensor] = None,
                  inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
@@ -763,24 +759,40 @@ def write_latent(pool: LatentPool, latent: torch.Tensor, k_rope: torch.Tensor,
     """Stores a step's latent rows and rotary keys by slot; with positions and
     inv_freq the rotary keys are turned first."""
     T = slot_mapping.numel()
-    ls, rs = _tokens(latent, pool.latent_dim, "latent"), _tokens(k_rope, pool.rope_dim, "k_rope")
-    if latent.shape[0] != T or k_rope.shape[0] != T or (positions is not None and
-                                                        positions.numel() != T):
-        raise ValueError("latent, k_rope and positions must have one row per slot")
-    if inv_freq is not None and 2 * inv_freq.numel() != pool.rope_dim:
-        raise ValueError("inv_freq must have rope_dim / 2 entries")
+    if latent.shape != (T, pool.latent_dim) or k_rope.shape != (T, pool.rope_dim) or (
+            positions is not None and positions.numel() != T):
+        raise ValueError("latent [T][latent_dim], k_rope [T][rope_dim] and positions must have "
+                         "one row per slot")
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq come together")
+    if inv_freq is not None and 2 * inv_freq.numel() != pool.rope_dim:
+        raise ValueError("inv_freq must have rope_dim / 2 entries")
     if T == 0:
         return
     dev = _device_of(pool.latent, "the pool")
-    _check(lib().pa_write_latent(
-        pool.ref(dev), _strided(latent, "latent", dev), ls, _strided(k_rope, "k_rope", dev), rs,
-        _flat(positions, "positions", dev, torch.int32),
-        _flat(inv_freq, "inv_freq", dev, torch.float32),
-        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor,
-        _flat(slot_mapping, "slot_mapping", dev, torch.int64), T, _on(dev, stream)),
-        "pa_write_latent")
+    ls, ld = latent.stride()
+    rs, rd = k_rope.stride()
+    if not (ld == 1 == rd and latent.dtype is _BF16 is k_rope.dtype
+            and slot_mapping.dtype is torch.int64
+            and latent.get_device() == k_rope.get_device() == slot_mapping.get_device() == dev
+            and slot_mapping.is_contiguous()
+            and (positions is None or (
+                positions.dtype is _I32 and inv_freq.dtype is _F32
+                and positions.get_device() == inv_freq.get_device() == dev
+                and positions.is_contiguous() and inv_freq.is_contiguous()))):
+        _explain(dev, (latent, "latent", _BF16, False), (k_rope, "k_rope", _BF16, False),
+                 (slot_mapping, "slot_mapping", torch.int64, True),
+                 (positions, "positions", _I32, True), (inv_freq, "inv_freq", _F32, True))
+    if T == 1:  # (the stride of a dimension of one entry may be anything)
+        ls, rs = pool.latent_dim, pool.rope_dim
+    st = (_lib or lib()).pa_write_latent(
+        pool.ref(dev), latent.data_ptr(), ls, k_rope.data_ptr(), rs,
+        None if positions is None else positions.data_ptr(),
+        None if inv_freq is None else inv_freq.data_ptr(),
+        PA_ROPE_INTERLEAVED if interleaved else PA_ROPE_HALF, factor, slot_mapping.data_ptr(), T,
+        _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_write_latent")
 
 
 def read_latent(pool: LatentPool, block_tables: torch.Tensor, kv_start_loc: torch.Tensor,
@@ -789,19 +801,32 @@ def read_latent(pool: LatentPool, block_tables: torch.Tensor, kv_start_loc: torc
     """Cached rows of the requests, ragged by kv_start_loc, widened to bf16."""
     R, max_blocks = block_tables.shape
     N = latent_out.shape[0]
-    ls, rs = _tokens(latent_out, pool.latent_dim, "latent_out"), _tokens(rope_out, pool.rope_dim,
-                                                                         "rope_out")
     if kv_start_loc.numel() != R + 1 or (first is not None and first.numel() != R):
         raise ValueError("kv_start_loc must have num_reqs + 1 entries and first num_reqs")
-    if rope_out.shape[0] != N:
-        raise ValueError("latent_out and rope_out must have the same rows")
+    if latent_out.shape != (N, pool.latent_dim) or rope_out.shape != (N, pool.rope_dim):
+        raise ValueError("latent_out [N][latent_dim] and rope_out [N][rope_dim] must have the same "
+                         "rows")
     dev = _device_of(pool.latent, "the pool")
-    _check(lib().pa_read_latent(
-        pool.ref(dev), _flat(block_tables, "block_tables", dev, torch.int32), max_blocks,
-        _flat(kv_start_loc, "kv_start_loc", dev, torch.int32),
-        _flat(first, "first", dev, torch.int32), R, N,
-        _strided(latent_out, "latent_out", dev), ls, _strided(rope_out, "rope_out", dev), rs,
-        _on(dev, stream)), "pa_read_latent")
+    ls, ld = latent_out.stride()
+    rs, rd = rope_out.stride()
+    if not (ld == 1 == rd and latent_out.dtype is _BF16 is rope_out.dtype
+            and block_tables.dtype is _I32 is kv_start_loc.dtype
+            and (latent_out.get_device() == rope_out.get_device() == block_tables.get_device()
+                 == kv_start_loc.get_device() == dev)
+            and block_tables.is_contiguous() and kv_start_loc.is_contiguous()
+            and (first is None or (first.dtype is _I32 and first.get_device() == dev
+                                   and first.is_contiguous()))):
+        _explain(dev, (block_tables, "block_tables", _I32, True),
+                 (kv_start_loc, "kv_start_loc", _I32, True), (first, "first", _I32, True),
+                 (latent_out, "latent_out", _BF16, False), (rope_out, "rope_out", _BF16, False))
+    if N <= 1:  # (the stride of a dimension of one entry may be anything)
+        ls, rs = pool.latent_dim, pool.rope_dim
+    st = (_lib or lib()).pa_read_latent(
+        pool.ref(dev), block_tables.data_ptr(), max_blocks, kv_start_loc.data_ptr(),
+        None if first is None else first.data_ptr(), R, N, latent_out.data_ptr(), ls,
+        rope_out.data_ptr(), rs, _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_read_latent")
 
 
 def copy_latent_blocks(pool: LatentPool, src: torch.Tensor, dst: torch.Tensor,
@@ -809,9 +834,9 @@ def copy_latent_blocks(pool: LatentPool, src: torch.Tensor, dst: torch.Tensor,
     if src.numel() != dst.numel():
         raise ValueError("src and dst must pair up")
     dev = _device_of(pool.latent, "the pool")
-    _check(lib().pa_copy_latent_blocks(
-        pool.ref(dev), _flat(src, "src", dev, torch.int32), _flat(dst, "dst", dev, torch.int32),
-        src.numel(), _on(dev, stream)), "pa_copy_latent_blocks")
+    _explain(dev, (src, "src", _I32, True), (dst, "dst", _I32, True))
+    _check(lib().pa_copy_latent_blocks(pool.ref(dev), src.data_ptr(), dst.data_ptr(), src.numel(),
+                                       _on(dev, stream)), "pa_copy_latent_blocks")
 
 
 def latent_workspace_size(num_q_heads: int, latent_dim: int) -> int:
@@ -834,17 +859,28 @@ def latent_forward(q: torch.Tensor, out: torch.Tensor, query_start_loc: torch.Te
         raise ValueError("q must be [T][H][latent_dim + rope_dim] and out [T][H][latent_dim]")
     if block_tables.dim() != 2 or block_tables.shape[0] != R:
         raise ValueError("block_tables must be [num_reqs][max_blocks]")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     dev = _device_of(q, "q")
-    st = lib().pa_latent_forward(
-        _flat(q, "q", dev, torch.bfloat16), _flat(out, "out", dev, torch.bfloat16),
-        _flat(query_start_loc, "query_start_loc", dev, torch.int32),
-        _flat(seq_lens, "seq_lens", dev, torch.int32), _np_addr(qh), _np_addr(sh),
-        _flat(block_tables, "block_tables", dev, torch.int32), block_tables.shape[1], R, T, H,
+    if not (q.dtype is _BF16 is out.dtype
+            and query_start_loc.dtype is _I32 is seq_lens.dtype and block_tables.dtype is _I32
+            and (out.get_device() == query_start_loc.get_device() == seq_lens.get_device()
+                 == block_tables.get_device() == dev)
+            and q.is_contiguous() and out.is_contiguous() and query_start_loc.is_contiguous()
+            and seq_lens.is_contiguous() and block_tables.is_contiguous()
+            and (workspace is None or (workspace.get_device() == dev
+                                       and workspace.is_contiguous()))):
+        _explain(dev, (q, "q", _BF16, True), (out, "out", _BF16, True),
+                 (query_start_loc, "query_start_loc", _I32, True),
+                 (seq_lens, "seq_lens", _I32, True), (block_tables, "block_tables", _I32, True),
+                 (workspace, "workspace", None if workspace is None else workspace.dtype, True))
+    st = (_lib or lib()).pa_latent_forward(
+        q.data_ptr(), out.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(),
+        _np_addr(qh), _np_addr(sh), block_tables.data_ptr(), block_tables.shape[1], R, T, H,
         pool.ref(dev), float(scale), int(causal),
-        None if workspace is None else _flat(workspace, "workspace", dev, workspace.dtype),
-        ws_bytes, _on(dev, stream))
-    _check(st, "pa_latent_forward")
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_latent_forward")
 
 
 def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
@@ -866,14 +902,27 @@ def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, 
         raise ValueError("q [T][H][Dn + Dr], k_nope [Tk][H][Dn], k_rope [Tk][Dr], v [Tk][H][Dv] "
                          "and out [T][H][Dv] must agree")
     dev = _device_of(q, "q")
-    st = lib().pa_latent_prefill(
-        _strided(q, "q", dev), q.stride(0), q.stride(1), _strided(k_nope, "k_nope", dev),
-        k_nope.stride(0), k_nope.stride(1), _strided(k_rope, "k_rope", dev), k_rope.stride(0),
-        _strided(v, "v", dev), v.stride(0), v.stride(1), _flat(out, "out", dev, torch.bfloat16),
-        _flat(query_start_loc, "query_start_loc", dev, torch.int32),
-        _flat(kv_start_loc, "kv_start_loc", dev, torch.int32), _np_addr(qh), _np_addr(kh), R, T,
-        Tk, H, Dn, Dr, Dv, float(scale), int(causal), _on(dev, stream))
-    _check(st, "pa_latent_prefill")
+    qt, qs, qd = q.stride()
+    kt, ks, kd = k_nope.stride()
+    vt, vs, vd = v.stride()
+    if not (qd == kd == vd == 1 and q.dtype is _BF16 is out.dtype
+            and k_nope.dtype is _BF16 is k_rope.dtype and v.dtype is _BF16
+            and query_start_loc.dtype is _I32 is kv_start_loc.dtype
+            and (k_nope.get_device() == k_rope.get_device() == v.get_device() == out.get_device()
+                 == query_start_loc.get_device() == kv_start_loc.get_device() == dev)
+            and out.is_contiguous() and query_start_loc.is_contiguous()
+            and kv_start_loc.is_contiguous() and k_rope.stride(1) == 1):
+        _explain(dev, (q, "q", _BF16, False), (k_nope, "k_nope", _BF16, False),
+                 (k_rope, "k_rope", _BF16, False), (v, "v", _BF16, False),
+                 (out, "out", _BF16, True), (query_start_loc, "query_start_loc", _I32, True),
+                 (kv_start_loc, "kv_start_loc", _I32, True))
+    st = (_lib or lib()).pa_latent_prefill(
+        q.data_ptr(), qt, qs, k_nope.data_ptr(), kt, ks, k_rope.data_ptr(), k_rope.stride(0),
+        v.data_ptr(), vt, vs, out.data_ptr(), query_start_loc.data_ptr(), kv_start_loc.data_ptr(),
+        _np_addr(qh), _np_addr(kh), R, T, Tk, H, Dn, Dr, Dv, float(scale), int(causal),
+        _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_latent_prefill")
 
 
 def selftest_wait_timeout(stream=None) -> None:
