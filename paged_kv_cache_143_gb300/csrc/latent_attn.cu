@@ -809,9 +809,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       // E4M3: the rows of the piece's query tile as two parts (warps 8-11)
       auto convert = [&](const Piece& pc, int n) {
         constexpr int kPer = L / 32;             // dims of a lane: 16 or 8
-        // Eight rows of a warp on their way at a time: once the keys stream, a load
-        // takes microseconds (two at a time, the first S came 15 us into the kernel)
-        constexpr int kBatch = NR / 4 < 8 ? NR / 4 : 8;
+        // Four rows of a warp on their way at a time: once the keys stream, a load takes
+        // microseconds (12 long contexts x 64 heads: two rows at a time 118.5 us, four
+        // 101.6; eight 103.2, for the code that is fetched cold)
+        constexpr int kBatch = 4;
 #pragma unroll 1
         for (int i0 = 0; i0 < NR / 4; i0 += kBatch) {
           uint4 v[kBatch][kPer / 8], rot[kBatch / 4];  // rot: 8 lanes a row
