@@ -551,8 +551,8 @@ pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src,
  * the row's largest such product. Rows of requests with q_len == 0 and rows
  * past query_start_loc[num_reqs] are not touched.
  * Cells past a request's seq_len may hold anything. A NaN or an infinity in a
- * query stays in its own row of out; one in a visible latent row also reaches
- * rows of the same request that do not see it yet (0 times it is NaN).
+ * query stays in its own row of out; one in a cell reaches the rows that see it
+ * and no others.
  * The work is divided from the device arrays at every launch; the host mirrors
  * only size the launch. A captured call therefore follows device lengths that
  * change between replays, with exact results, as long as query_start_loc
@@ -603,8 +603,9 @@ pa_status pa_latent_forward(const void* q, void* out, const int32_t* query_start
  * Computed in fp32 (the softmax weights enter the second product rounded to
  * bf16), rounded once to bf16. Rows past query_start_loc[num_reqs] are not
  * touched; rows past kv_start_loc[num_reqs] may hold anything. A NaN or an
- * infinity in v reaches every row of its request and head (0 times it is NaN
- * where the row does not see it). Supported: nope_dim 128, rope_dim 64,
+ * infinity in a query or in a key (and its value) reaches the rows that see it and
+ * no others; one in a value whose key is finite may reach every row of its
+ * request and head (0 times it is NaN). Supported: nope_dim 128, rope_dim 64,
  * v_dim 128. Needs no workspace.
  * Host checks: PA_ERR_INVALID (sizes, mirrors that do not end at num_tokens
  * and num_kv_tokens, strides, pointers), PA_ERR_UNSUPPORTED (other dims, more

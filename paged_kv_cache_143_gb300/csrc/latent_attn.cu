@@ -15,8 +15,9 @@
 // E4M3 16 heads 80 us, 64 117 (2750 cycles a 64-key tile, 2400 of them reads).
 // 160 decodes of 128 to 2048 keys x 32 heads: 56.5 us (35.3).
 //
-// One CTA per SM walks an equal share of all (row tile, 32-key tile) pairs
-// (pa::LatentParams). Both products run on the 5th-generation tensor cores:
+// One CTA per SM walks an equal share of all (row tile, key tile) pairs, a pass
+// over a request counting as four tiles more than it has (pa::LatentParams). Both
+// products run on the 5th-generation tensor cores:
 //   S [64 rows x 32 keys] = Q K^T     Q and the cells K-major in shared memory
 //   O^T [L x NR]        += c^T P^T    the same cells read again, MN-major, as
 //                                     the A operand; P from shared memory
@@ -29,7 +30,7 @@
 // their hand-overs) for 2700, and what HBM delivers a tile in is 1570.
 //   warp 0      TMA producer (one lane): the key tiles into a ring of stages, and
 //               the Q tile
-//   warp 1      TMEM and, one lane, S, up to four tiles ahead
+//   warp 1      TMEM and, one lane, S, up to four tiles ahead (E4M3: two)
 //   warp 2      one lane, PV. (One lane for both products spent a third of a
 //               tile's time between the two batches of them.)
 //   warp 3      the CTA's pieces, found once and handed to the others through a
@@ -57,7 +58,7 @@
 //     that of p s_n, placed at 2^7, so that is 2^-24 of the row's largest weight:
 //     a long context's many small weights keep their share beside one large one.
 //     (Two E4M3 parts would do for weights within 2^-8 of the largest, but lose
-//     every weight below 2^-14 of it; PV is a fifth of the tensor time.)
+//     every weight below 2^-14 of it.)
 // The parts of q are stacked in the rows of S (64, or 128 for 64 query rows),
 // those of hi above those of lo, 8 or 16 a softmax warp: the keys are read once for
 // both, and the thread that reads a row's hi scores reads its lo scores too. The
@@ -942,6 +943,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           // two phases of s_full behind, where a parity says nothing)
           if (live && !(ok = wait(&tail->s_full[buf], g / kSBufs))) break;
           bool p_free = false;
+          // rows of a chunk hide keys of this tile that others see; scores there that
+          // are no numbers
+          const bool hiding = pc.first >= 0 && key0 + KT > pc.sees;
+          bool odd = false;
           if (scores) {
             // (a test of a barrier answers after about 200 cycles beside the products'
             // reads of shared memory: they are asked ahead of their use)
@@ -1027,6 +1032,15 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                 m_there = mbar_test_wait(&tail->m_full[w4][(g - 1) & 1], ((g - 1) >> 1) & 1);
             }
             if (key0 + KT > lim_min) {
+              if (hiding) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                  float sum = 0.f;
+#pragma unroll
+                  for (int i = 0; i < VT; ++i) sum += x[t][i];
+                  odd |= lim[t] > 0 && !(fabsf(sum) < INFINITY);
+                }
+              }
 #pragma unroll
               for (int i = 0; i < VT; ++i) {
                 const int key = key0 + key_of(i);
@@ -1164,6 +1178,23 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             for (int t = 0; t < RT; ++t) tail->alpha[g & 1][row[t]] = alpha[t];
           }
           if (lane == 0) tail->ask[g & 1][w4] = ask;
+          if (__builtin_expect(hiding && __any_sync(0xffffffffu, odd), 0)) {  // rare
+            // A later token's cell may not be finite. Its score then is that for every
+            // row: those that see it are NaN already, and zeros keep it from the others
+            // (0 times it is NaN)
+            if (live && !(ok = wait(&tail->k_full[g % kStages], g / kStages))) break;
+            uint32_t* cells =
+                reinterpret_cast<uint32_t*>(smem + S::kOffK + (g % kStages) * S::kStage);
+#pragma unroll 1
+            for (int i = lane; i < kCols * kChunk / 4; i += 32) {
+              uint32_t w = cells[i];
+              constexpr uint32_t kField = F8 ? 0xFFu : 0xFFFFu, kOdd = F8 ? 0x7Fu : 0x7F80u;
+#pragma unroll 1
+              for (int b = 0; b < 32; b += F8 ? 8 : 16)
+                if ((w >> b & kOdd) == kOdd) w &= ~(kField << b);
+              cells[i] = w;
+            }
+          }
           if (key0 + KT > pc.n_keys) {
             // the tile holds keys past the last visible one (unloaded blocks,
             // unwritten cells): zero them, so that P = 0 never meets a NaN (S of

@@ -131,6 +131,17 @@ __device__ __forceinline__ bool aborted(Bars* b) {
   return *reinterpret_cast<volatile int*>(&b->abort) != 0;
 }
 
+// Zeros in the place of infinities and NaN in a chunk, by a warp.
+__device__ __noinline__ void clear_non_finite(uint8_t* chunk) {
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < kSlot / 4; i += 32) {
+    uint32_t x = reinterpret_cast<uint32_t*>(chunk)[i];
+    if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+    if ((x & 0x7F800000u) == 0x7F800000u) x &= 0xFFFFu;
+    reinterpret_cast<uint32_t*>(chunk)[i] = x;
+  }
+}
+
 template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -368,7 +379,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_wait_ld();
       float* s = reinterpret_cast<float*>(sr);
       const int key0 = (j0 + j) * kN;
+      bool odd = false;  // scores that are no numbers where this row hides keys
       if (key0 + kN > limit) {
+        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int k = 0; k < kN; k += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            sum2[u] = f2_add(sum2[u], f2_pack(s[k + 2 * u], s[k + 2 * u + 1]));
+        float lo, hi;
+        f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), lo, hi);
+        odd = valid && !(fabsf(lo + hi) < INFINITY);
 #pragma unroll
         for (int k = 0; k < kN; ++k)
           if (key0 + k >= limit) s[k] = -INFINITY;
@@ -438,6 +459,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_st32(tmem_s + c * 32, w);
       }
       tc::tmem_wait_st();
+      if (__any_sync(0xffffffffu, odd)) {
+        // A later key may not be finite. Its score then is that for every row: those
+        // that see it are NaN already, and zeros in its value keep it from the others
+        // (0 times it is NaN)
+        const int v = j * kTileChunks + kKChunks;
+        bool here = true;
+#pragma unroll
+        for (int c = 0; c < kVChunks; ++c)
+          here = here && mbar_wait(&bars->full[(v + c) % kSlots], ((v + c) / kSlots) & 1, p.err);
+        if (!__all_sync(0xffffffffu, here)) {
+          ok = false;
+          break;
+        }
+#pragma unroll 1
+        for (int c = 0; c < kVChunks; ++c)
+          clear_non_finite(smem + kOffRing + ((v + c) % kSlots) * kSlot);
+        tc::fence_proxy_async_smem();
+      }
       if (j == ntk_all - 1 && key0 + kN > n_kv_all) {
         // value rows past the last visible key (another request's, or past
         // the array) are zeroed, so that P = 0 never meets a NaN

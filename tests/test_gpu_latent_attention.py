@@ -343,3 +343,30 @@ def test_a_key_of_infinite_score(cuda_device, fp8):
     up = b.q[:, :, 512 + 9] > 0
     assert torch.isnan(got).all(-1)[up].all()
     assert torch.isfinite(got)[~up].all()
+
+
+@pytest.mark.parametrize("H,L", [(20, 256), (3, 512), (64, 512)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_later_tokens_that_are_not_numbers(cuda_device, fp8, H, L):
+    """A NaN or an infinity in a chunk's later cells leaves the rows that do not
+    see them as they are; rows that see a NaN are NaN."""
+    b = Batch([700, 40, 130], [9, 5, 130], H, L, 16, fp8, cuda_device, seed=23)
+    clean = b.run().clone()
+    first = {}                        # request -> first bad position
+    for r, keys in ((0, (697, 699)), (1, (38,)), (2, (64, 65, 100))):
+        first[r] = min(keys)
+        for i, key in enumerate(keys):
+            slot = int(ref.slots_of(b.tab, r, b.seqs[r], b.B)[key])
+            cell = b.pool.latent.view(-1, L)[slot]
+            if fp8:
+                cell[7 + 40 * i] = 0x7F
+            else:
+                cell[7 + 40 * i] = float("nan") if i != 1 else float("inf")
+    got = b.run()
+    assert pa.get_error() == pa.PA_OK
+    for r in range(3):
+        a, n = int(b.qsl[r]), b.q_lens[r]
+        hide = first[r] - (b.seqs[r] - n)        # rows before this one do not see it
+        assert 0 < hide < n
+        assert torch.equal(got[a:a + hide].view(torch.int16), clean[a:a + hide].view(torch.int16))
+        assert torch.isnan(got[a + hide:a + n]).any(-1).all()

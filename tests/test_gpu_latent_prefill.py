@@ -251,3 +251,24 @@ def test_split_units_captured_flagged_and_beside_nan(cuda_device):
         b.ksl_dev = i32(b.ksl if k is None else k, dev)
         b.run()
         assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS, (q, k)
+
+
+def test_later_keys_that_are_not_numbers(cuda_device):
+    """NaN and infinities in a chunk's later keys and values leave the rows that do
+    not see them as they are, whole units and split ones alike."""
+    for q_lens, k_lens, H in (([300, 70], [420, 70], 3), ([40], [3000], 1)):
+        b = Chunks(q_lens, k_lens, H, cuda_device, seed=51)
+        clean = b.run().clone()
+        for r, n in enumerate(q_lens):
+            bad = int(b.ksl[r]) + k_lens[r] - n + n // 2     # seen from row n / 2 on
+            b.k[bad, :, 3] = float("nan")
+            b.v[bad, :, 5] = float("inf")
+            b.kr[bad + 1, 7] = float("nan")
+            b.v[bad + 1] = float("nan")
+        got = b.run()
+        assert pa.get_error() == pa.PA_OK
+        for r, n in enumerate(q_lens):
+            a = int(b.qsl[r])
+            assert torch.equal(got[a:a + n // 2].view(torch.int16),
+                               clean[a:a + n // 2].view(torch.int16))
+            assert torch.isnan(got[a + n // 2:a + n]).all()
