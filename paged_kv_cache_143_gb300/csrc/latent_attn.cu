@@ -1037,7 +1037,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
                 for (int t = 0; t < RT; ++t) {
                   float sum = 0.f;
 #pragma unroll
-                  for (int i = 0; i < VT; ++i) sum += x[t][i];
+                  for (int i = 0; i < VT; ++i)  // (past n_keys lies anything)
+                    sum += key0 + key_of(i) < pc.n_keys ? x[t][i] : 0.f;
                   odd |= lim[t] > 0 && !(fabsf(sum) < INFINITY);
                 }
               }
