@@ -563,8 +563,9 @@ pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src,
  * (num_tokens * num_q_heads / 16 + num_reqs) * max_blocks * block_size / 32
  * near 2^31.
  * Device checks: a request whose device entries leave those bounds (or with
- * q_len > seq_len) sets PA_ERR_DEVICE_BOUNDS and is skipped; a block id
- * outside the pool sets it too. Nothing is read or written outside the
+ * q_len > seq_len) sets PA_ERR_DEVICE_BOUNDS and is skipped; where the others
+ * claim more work than the bound above (a query_start_loc that goes back and
+ * forth), all are; a block id outside the pool sets it too. Nothing is read or written outside the
  * buffers.
  */
 size_t pa_latent_workspace_size(int32_t num_q_heads, int32_t latent_dim);

@@ -262,6 +262,14 @@ __device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
 }
 // ------------------------------------------------------------ the flat space
 
+// Sums of weights stop here. The host refuses batches that could come this far with
+// a query_start_loc that only rises; one that goes back and forth on the device can,
+// its requests overlapping, and is then taken for an empty batch.
+constexpr int32_t kMaxWork = INT32_MAX;
+__device__ __forceinline__ int32_t add_work(int32_t a, int32_t b) {
+  return (int32_t)min((uint32_t)a + (uint32_t)b, (uint32_t)kMaxWork);
+}
+
 struct Request {
   int32_t q_begin, q_len, seq, rows, keys;  // query rows, key tiles
   int32_t weight;                           // passes * (skip + keys); 0 for one without work
@@ -284,7 +292,7 @@ __device__ __forceinline__ Request load_request(const LatentParams& p, int r, bo
   q.rows = q.q_len * p.Hq;  // (T * Hq fits 32 bits)
   q.keys = (q.seq + KT - 1) / KT;
   const int tiles = (q.rows + NR - 1) / NR;
-  // (the host bounds the sum)
+  // (within the host's bound on the sum, kMaxWork, for each request by itself)
   q.weight = (p.lanes == 1 ? tiles : (tiles + 1) / 2) * (p.skip + q.keys);
   return q;
 }
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
 #pragma unroll 1
     for (int i = 0; i < per_thread; ++i) {
       const int r = threadIdx.x * per_thread + i;
-      if (r < p.R) w += load_request<NR, KT>(p, r, cta == 0).weight;
+      if (r < p.R) w = add_work(w, load_request<NR, KT>(p, r, cta == 0).weight);
     }
     weights[threadIdx.x] = w;
   }
@@ -661,14 +669,18 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       constexpr int kEach = kThreads / 32;
       int32_t mine = 0;
 #pragma unroll 1
-      for (int i = 0; i < kEach; ++i) mine += weights[lane * kEach + i];
+      for (int i = 0; i < kEach; ++i) mine = add_work(mine, weights[lane * kEach + i]);
       int32_t upto = mine;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+        if (lane >= o) upto = add_work(upto, y);
       }
-      const int W = __shfl_sync(0xffffffffu, upto, 31);
+      int W = __shfl_sync(0xffffffffu, upto, 31);
+      if (W == kMaxWork) {
+        if (cta == 0 && lane == 0) raise_error(p.err, kErrBounds);
+        W = 0;
+      }
       const unsigned Q = max(1u, ((unsigned)W + groups - 1) / groups);
       const int begin = (int)min((unsigned)W, group * Q), end = (int)min((unsigned)W, begin + Q);
       // the lane, its thread's sum, then the request
@@ -1631,7 +1643,7 @@ extern "C" pa_status pa_latent_forward(const void* q, void* out, const int32_t* 
   // the flat space stays within 31 bits whatever the device lengths are
   const int64_t most = ((int64_t)T * Hq / NR + R) *
                        (skip + ((int64_t)max_blocks * pool->block_size + KT - 1) / KT);
-  if (most > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (most >= pa::kMaxWork) return PA_ERR_UNSUPPORTED;
   const int grid = G * (int)std::min<int64_t>(W, sms / G);
   if (workspace_bytes < pa::scratch_bytes(grid, NR, L)) return PA_ERR_INVALID;
 

@@ -370,3 +370,25 @@ def test_later_tokens_that_are_not_numbers(cuda_device, fp8, H, L):
         assert 0 < hide < n
         assert torch.equal(got[a:a + hide].view(torch.int16), clean[a:a + hide].view(torch.int16))
         assert torch.isnan(got[a + hide:a + n]).any(-1).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_starts_that_claim_more_than_32_bits_of_work(cuda_device, fp8):
+    """Device starts 0, T, 0, T, ..: half of the requests claim every row, each a
+    valid request by itself, and their passes together more key tiles than 32 bits
+    hold. The call is flagged and writes nothing."""
+    dev = cuda_device
+    T, H, L, B, R, ctx = 2048, 128, 256, 64, 1024, 1 << 18
+    # tiles of 64 rows and 64 keys, the rows' two by two
+    assert (R // 2) * (T * H // 64 // 2) * (ctx // 64) > 2 ** 31
+    pool = ref.new_pool(pa, 2, B, L, fp8, dev, poison=False)
+    q = torch.zeros(T, H, L + 64, dtype=torch.bfloat16, device=dev)
+    out = torch.full((T, H, L), 9.0, dtype=torch.bfloat16, device=dev)
+    table = torch.zeros(R, ctx // B, dtype=torch.int32, device=dev)
+    host = np.arange(R + 1, dtype=np.int32) * (T // R)
+    seq = np.full(R, ctx, np.int32)
+    ws = torch.empty(pa.latent_workspace_size(H, L), dtype=torch.uint8, device=dev)
+    starts = i32([0, T] * (R // 2) + [0], dev)
+    pa.latent_forward(q, out, starts, i32(seq, dev), host, seq, table, pool, 0.1, workspace=ws)
+    assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS
+    assert (out == 9).all()
