@@ -59,7 +59,7 @@ constexpr int kTileChunks = kKChunks + kVChunks;
 constexpr int kSlots = 8;
 constexpr int kOffRing = 2 * kQChunks * kSlot;
 constexpr int kOffBars = kOffRing + kSlots * kSlot;
-constexpr int kSmem = kOffBars + 512 + 1024;           // the base is rounded up to 1024 B
+constexpr int kSmem = kOffBars + 1024 + 1024;          // the base is rounded up to 1024 B
 static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB per-block limit");
 
 struct Bars {
@@ -69,8 +69,10 @@ struct Bars {
   uint64_t final_mma;
   uint32_t tmem;
   int abort;
+  int any_cleared;               // some value element was: rows past cleared[dim] get a NaN
+  int32_t cleared[kV];           // first key of the request whose element was, by dim
 };
-static_assert(sizeof(Bars) <= 512, "the mbarriers overrun their slot");
+static_assert(sizeof(Bars) <= 1024, "the mbarriers overrun their slot");
 
 constexpr int kMaxUnits = 1024;
 
@@ -131,15 +133,74 @@ __device__ __forceinline__ bool aborted(Bars* b) {
   return *reinterpret_cast<volatile int*>(&b->abort) != 0;
 }
 
-// Zeros in the place of infinities and NaN in a chunk, by a warp.
-__device__ __noinline__ void clear_non_finite(uint8_t* chunk) {
-#pragma unroll 1
-  for (int i = threadIdx.x & 31; i < kSlot / 4; i += 32) {
-    uint32_t x = reinterpret_cast<uint32_t*>(chunk)[i];
-    if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-    if ((x & 0x7F800000u) == 0x7F800000u) x &= 0xFFFFu;
-    reinterpret_cast<uint32_t*>(chunk)[i] = x;
+__device__ __forceinline__ bool non_finite_pair(uint32_t x) {  // either bf16
+  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+}
+
+// Zeros in the place of the infinities and NaN of one value row, by a warp; `key` is
+// its position in the request. Rows that see the key have the NaN put back when they
+// are written (0 or NaN times the element is that).
+__device__ __forceinline__ void clear_value(uint8_t* const (&chunk)[kVChunks], int row, int32_t key,
+                                         Bars* bars) {
+  const int lane = threadIdx.x & 31;
+  for (int c = 0; c < kVChunks; ++c) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(chunk[c] + row * 128) + lane;
+    uint32_t x = *w;
+    if (!non_finite_pair(x)) continue;
+    const int dim = c * 64 + (((lane >> 2) ^ (row & 7)) << 3) + (lane & 3) * 2;
+    for (int half = 0; half < 2; ++half) {
+      if ((x >> 16 * half & 0x7F80u) != 0x7F80u) continue;
+      x &= half ? 0xFFFFu : 0xFFFF0000u;
+      atomicMin(&bars->cleared[dim + half], key);
+    }
+    *w = x;
+    *reinterpret_cast<volatile int*>(&bars->any_cleared) = 1;
   }
+}
+
+// For a tile in which rows hide keys and score some of them with no number (limit >= 0:
+// this thread's row does; it sees the keys below limit): a later key may not be
+// finite, and 0 times its value then a NaN. The keys at fault are those that rows with a
+// finite query hide and score so; their values, and no others, are cleared. All lanes of
+// a warp, before S is overwritten; v is the ring position of the tile's first value chunk.
+__device__ __noinline__ bool clear_hidden(uint8_t* smem, Bars* bars, uint32_t tmem_s,
+                                          int query, int v, int key0, int limit, int n_kv,
+                                          unsigned* err) {
+  bool here = mbar_wait(&bars->q_full, 0, err);
+  uint8_t* chunk[kVChunks];
+#pragma unroll
+  for (int c = 0; c < kVChunks; ++c) {
+    here = here && mbar_wait(&bars->full[(v + c) % kSlots], ((v + c) / kSlots) & 1, err);
+    chunk[c] = smem + kOffRing + ((v + c) % kSlots) * kSlot;
+  }
+  if (!__all_sync(0xffffffffu, here)) return false;
+  bool finite = limit >= 0;
+#pragma unroll 1
+  for (int i = 0; i < kQChunks * 8; ++i) {
+    const uint4 x = *reinterpret_cast<const uint4*>(smem + query + (i >> 3) * kSlot + (i & 7) * 16);
+    if (non_finite_pair(x.x) || non_finite_pair(x.y) || non_finite_pair(x.z) ||
+        non_finite_pair(x.w))
+      finite = false;
+  }
+#pragma unroll 1
+  for (int c = 0; c < kN / 32; ++c) {
+    uint32_t x[32];
+    tc::tmem_ld32(tmem_s + c * 32, x);
+    tc::tmem_wait_ld();
+    uint32_t bad = 0u;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const int key = key0 + c * 32 + k;
+      if (key >= limit && key < n_kv && !(fabsf(__uint_as_float(x[k])) < INFINITY)) bad |= 1u << k;
+    }
+    bad = __reduce_or_sync(0xffffffffu, finite ? bad : 0u);
+    for (; bad != 0u; bad &= bad - 1) {
+      const int n = c * 32 + __ffs(bad) - 1;
+      clear_value(chunk, n, key0 + n, bars);
+    }
+  }
+  tc::fence_proxy_async_smem();
+  return true;
 }
 
 template <bool kSplit>
@@ -214,8 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bars->final_mma, 1);
     bars->abort = 0;
+    bars->any_cleared = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x < kV) bars->cleared[threadIdx.x] = INT32_MAX;
   if (warp == 1) {
     tc::tmem_alloc(&bars->tmem, kTmemCols);
     tc::tmem_relinquish();
@@ -364,6 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = (2 * pair + t) * kM + row;
     const bool valid = tok < q_len;
     const int limit = !valid ? 0 : p.causal ? max(0, min(P + tok + 1, k_len)) : k_len;
+    // keys that every row of the warp sees (rows past the chunk are never looked at)
+    const int least = __reduce_min_sync(0xffffffffu, valid ? limit : INT32_MAX);
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; ok && j < my_ntk; ++j) {
@@ -379,17 +444,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_wait_ld();
       float* s = reinterpret_cast<float*>(sr);
       const int key0 = (j0 + j) * kN;
-      bool odd = false;  // scores that are no numbers where this row hides keys
-      if (key0 + kN > limit) {
+      if (key0 + kN > least) {
+        // Scores that are no numbers in a tile where this row hides keys of its request
+        // (32 at a time up to the last such key; past it lies anything)
         uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int k = 0; k < kN; k += 8)
+        for (int k = 0; k < kN; k += 32)
+          if (key0 + k < n_kv_all) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            sum2[u] = f2_add(sum2[u], f2_pack(s[k + 2 * u], s[k + 2 * u + 1]));
+            for (int u = 0; u < 16; ++u)
+              sum2[u & 3] = f2_add(sum2[u & 3], f2_pack(s[k + 2 * u], s[k + 2 * u + 1]));
+          }
         float lo, hi;
         f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), lo, hi);
-        odd = valid && !(fabsf(lo + hi) < INFINITY);
+        const bool odd = limit > 0 && limit < min(key0 + kN, n_kv_all) &&
+                         !(fabsf(lo + hi) < INFINITY);
+        if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {  // rare
+          if (!__all_sync(0xffffffffu, clear_hidden(smem, bars, tmem_s,
+                                                    t * kQChunks * kSlot + row * 128,
+                                                    j * kTileChunks + kKChunks, key0,
+                                                    odd ? limit : -1, n_kv_all, p.err))) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int c = 0; c < kN / 32; ++c)
+            tc::tmem_ld32(tmem_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sr + c * 32));
+          tc::tmem_wait_ld();
+        }
 #pragma unroll
         for (int k = 0; k < kN; ++k)
           if (key0 + k >= limit) s[k] = -INFINITY;
@@ -459,24 +541,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_st32(tmem_s + c * 32, w);
       }
       tc::tmem_wait_st();
-      if (__any_sync(0xffffffffu, odd)) {
-        // A later key may not be finite. Its score then is that for every row: those
-        // that see it are NaN already, and zeros in its value keep it from the others
-        // (0 times it is NaN)
-        const int v = j * kTileChunks + kKChunks;
-        bool here = true;
-#pragma unroll
-        for (int c = 0; c < kVChunks; ++c)
-          here = here && mbar_wait(&bars->full[(v + c) % kSlots], ((v + c) / kSlots) & 1, p.err);
-        if (!__all_sync(0xffffffffu, here)) {
-          ok = false;
-          break;
-        }
-#pragma unroll 1
-        for (int c = 0; c < kVChunks; ++c)
-          clear_non_finite(smem + kOffRing + ((v + c) % kSlots) * kSlot);
-        tc::fence_proxy_async_smem();
-      }
       if (j == ntk_all - 1 && key0 + kN > n_kv_all) {
         // value rows past the last visible key (another request's, or past
         // the array) are zeroed, so that P = 0 never meets a NaN
@@ -507,6 +571,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], (my_ntk - 1) & 1, p.err)))
       ok = false;
     if (!ok) bars->abort = 1;
+    // NaN in the place of O's elements that a cleared value of a seen key belongs to
+    // (all clears are done: those that matter to a tile precede its last product)
+    const bool any_cleared = *reinterpret_cast<volatile int*>(&bars->any_cleared) != 0;
+    auto put_back = [&](int c, uint32_t (&o)[32]) {
+      if (__builtin_expect(any_cleared, 0)) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (limit > bars->cleared[c * 32 + k]) o[k] = 0x7FC00000u;
+      }
+    };
     if constexpr (kSplit) {
       // both tiles' products are done and every copy has landed: Q and the ring
       // make room for the partials
@@ -521,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (my_ntk > 0) {
           tc::tmem_ld32(tmem_o + c * 32, o);
           tc::tmem_wait_ld();
+          put_back(c, o);
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -584,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (my_ntk > 0) {
           tc::tmem_ld32(tmem_o + c * 32, o);
           tc::tmem_wait_ld();
+          put_back(c, o);
         }
         if (valid) {
 #pragma unroll

@@ -272,3 +272,67 @@ def test_later_keys_that_are_not_numbers(cuda_device):
             assert torch.equal(got[a:a + n // 2].view(torch.int16),
                                clean[a:a + n // 2].view(torch.int16))
             assert torch.isnan(got[a + n // 2:a + n]).all()
+
+
+@pytest.mark.parametrize("form", ["query", "later_key", "next_request"])
+@pytest.mark.parametrize("q_lens,k_lens,H", [([300, 70], [420, 70], 3), ([40, 30], [3000, 1500], 1)],
+                         ids=["whole", "split"])
+def test_a_visible_infinite_value_stays(cuda_device, q_lens, k_lens, H, form):
+    """An infinite value behind a finite key makes its dimension infinite in every
+    row that sees it, whatever else of the tile is no number: another row's query, a
+    key that the row hides, or the next request's keys (after the tile's last)."""
+    b = Chunks(q_lens, k_lens, H, cuda_device, seed=61)
+    last = []                       # the first row's own key: in a tile that hides keys
+    for r, n in enumerate(q_lens):
+        last.append(int(b.ksl[r]) + k_lens[r] - n)
+        b.v[last[r], :, 5] = float("inf")
+    clean = b.run().clone()
+    for r, n in enumerate(q_lens):
+        a = int(b.qsl[r])
+        assert (clean[a:a + n, :, 5] == float("inf")).all()
+        others = [d for d in range(DV) if d != 5]
+        assert torch.isfinite(clean[a:a + n][..., others]).all()
+    same = torch.ones(int(b.qsl[-1]), dtype=torch.bool, device=cuda_device)
+    if form == "query":
+        row = int(b.qsl[0]) + 7
+        b.q[row, :, 9] = float("nan")
+        same[row] = False
+    elif form == "later_key":
+        for r, n in enumerate(q_lens):
+            b.k[last[r] + n // 2, :, 3] = float("nan")       # seen from row n / 2 on
+            same[int(b.qsl[r]) + n // 2:int(b.qsl[r + 1])] = False
+    else:
+        b.k[b.ksl[1]:] = float("nan")
+        b.v[b.ksl[1]:] = float("nan")
+        same[b.qsl[1]:] = False
+    got = b.run()
+    assert pa.get_error() == pa.PA_OK
+    rows = got[:b.qsl[-1]]
+    assert torch.equal(rows[same].view(torch.int16), clean[:b.qsl[-1]][same].view(torch.int16))
+    assert torch.isnan(rows[~same]).all()
+
+
+def test_a_cleared_value_returns_to_the_rows_that_see_it(cuda_device):
+    """A key that its first rows hide, with an infinite rotary element and an
+    infinite value: the rows that see it with score -inf get 0 times infinity, a NaN,
+    in that dimension and nothing else from it."""
+    for q_lens, k_lens, H in (([300, 70], [420, 70], 3), ([40], [3000], 1)):
+        b = Chunks(q_lens, k_lens, H, cuda_device, seed=62)
+        b.q[..., DN + 7] = -b.q[..., DN + 7].abs() - 0.01     # every score of the key is -inf
+        clean = {}
+        for bad_value in (False, True):
+            for r, n in enumerate(q_lens):
+                key = int(b.ksl[r]) + k_lens[r] - n + n // 2  # seen from row n / 2 on
+                b.kr[key, 7] = float("inf")
+                if bad_value:
+                    b.v[key, :, 5] = float("inf")
+            clean[bad_value] = b.run().clone()
+        assert pa.get_error() == pa.PA_OK
+        assert torch.isfinite(clean[False]).all()
+        for r, n in enumerate(q_lens):
+            a = int(b.qsl[r])
+            want = clean[False][a:a + n].clone()
+            want[n // 2:, :, 5] = float("nan")
+            got = clean[True][a:a + n]
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
+            assert torch.equal(got.nan_to_num(), want.nan_to_num())
