@@ -607,7 +607,8 @@ pa_status pa_latent_forward(const void* q, void* out, const int32_t* query_start
  * infinity in a query or in a key (and its value) reaches the rows that see it and
  * no others; one in a value whose key is finite reaches those too and may, as
  * NaN (0 times it), reach every row of its request and head. A key that a row
- * scores -inf weighs 0 there, which its value is still multiplied by. Supported: nope_dim 128, rope_dim 64,
+ * scores -inf weighs 0 there, which its value is still multiplied by; a row that
+ * scores every visible key so is NaN. Supported: nope_dim 128, rope_dim 64,
  * v_dim 128. Needs no workspace.
  * Host checks: PA_ERR_INVALID (sizes, mirrors that do not end at num_tokens
  * and num_kv_tokens, strides, pointers), PA_ERR_UNSUPPORTED (other dims, more

@@ -203,6 +203,23 @@ __device__ __noinline__ bool clear_hidden(uint8_t* smem, Bars* bars, uint32_t tm
   return true;
 }
 
+// NaN in the place of the elements of this thread's row of O that a cleared value
+// of a key it sees (one below limit) belongs to. All lanes of a warp.
+__device__ __noinline__ void put_back(uint32_t tmem_o, int limit, const Bars* bars) {
+  tc::fence_after_sync();
+#pragma unroll 1
+  for (int c = 0; c < kV; c += 32) {
+    uint32_t o[32];
+    tc::tmem_ld32(tmem_o + c, o);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (limit > bars->cleared[c + k]) o[k] = 0x7FC00000u;
+    tc::tmem_st32(tmem_o + c, o);
+  }
+  tc::tmem_wait_st();
+}
+
 template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -571,16 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], (my_ntk - 1) & 1, p.err)))
       ok = false;
     if (!ok) bars->abort = 1;
-    // NaN in the place of O's elements that a cleared value of a seen key belongs to
     // (all clears are done: those that matter to a tile precede its last product)
-    const bool any_cleared = *reinterpret_cast<volatile int*>(&bars->any_cleared) != 0;
-    auto put_back = [&](int c, uint32_t (&o)[32]) {
-      if (__builtin_expect(any_cleared, 0)) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (limit > bars->cleared[c * 32 + k]) o[k] = 0x7FC00000u;
-      }
-    };
+    if (__builtin_expect(*reinterpret_cast<volatile int*>(&bars->any_cleared), 0) && ok &&
+        my_ntk > 0)
+      put_back(tmem_o, limit, bars);
     if constexpr (kSplit) {
       // both tiles' products are done and every copy has landed: Q and the ring
       // make room for the partials
@@ -588,14 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(0, kThreads);
       tc::fence_after_sync();
       float2* sums = reinterpret_cast<float2*>(smem + kOffSums);
-      sums[t * kM + row] = make_float2(m_run, my_ntk > 0 ? l_run : 0.f);
+      // (a sum of -1: the row sees no key of this CTA's)
+      sums[t * kM + row] = make_float2(m_run, my_ntk > 0 && limit > j0 * kN ? l_run : -1.f);
 #pragma unroll 1
       for (int c = 0; c < kV / 32; ++c) {
         uint32_t o[32];
         if (my_ntk > 0) {
           tc::tmem_ld32(tmem_o + c * 32, o);
           tc::tmem_wait_ld();
-          put_back(c, o);
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -617,28 +628,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4 x[kMaxSplit];
 #pragma unroll
         for (int k = 0; k < kMaxSplit; ++k) {
-          ml[k] = make_float2(-INFINITY, 0.f);
+          ml[k] = make_float2(-INFINITY, -1.f);
           if (k < split) {
             ml[k] = ld_cluster2(in_cta(sums + at, k));
-            x[k] = ld_cluster4(in_cta(piece, k));  // (not used where the sum is zero)
+            x[k] = ld_cluster4(in_cta(piece, k));  // (not used where the sum is -1)
           }
         }
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kMaxSplit; ++k)
-          if (ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
+          if (!(ml[k].y < 0.f)) top = fmaxf(top, ml[k].x);  // (a NaN sum counts)
+        bool some = false;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kMaxSplit; ++k) {
-          if (ml[k].y == 0.f) continue;
-          const float w = ex2_ftz(ml[k].x - top);
+          if (ml[k].y < 0.f) continue;
+          some = true;
+          // (scores of -inf alone weigh 0, which O may make a NaN)
+          const float w = ml[k].x == -INFINITY ? 0.f : ex2_ftz(ml[k].x - top);
           sum = fmaf(w, ml[k].y, sum);
           o.x = fmaf(w, x[k].x, o.x);
           o.y = fmaf(w, x[k].y, o.y);
           o.z = fmaf(w, x[k].z, o.z);
           o.w = fmaf(w, x[k].w, o.w);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        // zero without a visible key; NaN where every score is -inf
+        const float inv = some ? 1.f / sum : 0.f;
         __nv_bfloat162 lo2 = __floats2bfloat162_rn(o.x * inv, o.y * inv);
         __nv_bfloat162 hi2 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
         *reinterpret_cast<uint2*>(p.out + ((int64_t)(q_begin + tok_i) * p.H + h) * kV + lane * 4) =
@@ -649,8 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && !aborted(bars)) {
       tc::fence_after_sync();
-      // a row without a visible key is zero (one with a NaN sum is not)
-      const bool some = l_run != 0.f;
+      // a row without a visible key is zero; one whose scores are all -inf is NaN (its
+      // sum is 0)
+      const bool some = limit > 0;
       const float inv = some ? 1.f / l_run : 0.f;
       __nv_bfloat16* orow = p.out + ((int64_t)(q_begin + tok) * p.H + h) * kV;
 #pragma unroll 1
@@ -659,7 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (my_ntk > 0) {
           tc::tmem_ld32(tmem_o + c * 32, o);
           tc::tmem_wait_ld();
-          put_back(c, o);
         }
         if (valid) {
 #pragma unroll

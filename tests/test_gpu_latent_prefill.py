@@ -336,3 +336,43 @@ def test_a_cleared_value_returns_to_the_rows_that_see_it(cuda_device):
             got = clean[True][a:a + n]
             assert torch.equal(torch.isnan(got), torch.isnan(want))
             assert torch.equal(got.nan_to_num(), want.nan_to_num())
+
+
+@pytest.mark.parametrize("q_lens,k_lens,H", [([1, 300, 70], [1, 420, 70], 3), ([40, 2], [3000, 700], 1)],
+                         ids=["whole", "split"])
+def test_scores_of_minus_infinity_alone(cuda_device, q_lens, k_lens, H):
+    """A row whose query holds an infinity that scores every visible key -inf is NaN,
+    as the softmax of such scores is, and not zero."""
+    b = Chunks(q_lens, k_lens, H, cuda_device, seed=63)
+    b.kr[:, 7] = b.kr[:, 7].abs() + 0.01
+    clean = b.run().clone()
+    rows = [int(a) for a in b.qsl[:-1]] + [int(b.qsl[-1]) - 1]
+    for t in rows:
+        b.q[t, H - 1, DN + 7] = float("-inf")
+    got = b.run()
+    assert pa.get_error() == pa.PA_OK
+    for t in range(b.qsl[-1]):
+        for h in range(H):
+            if t in rows and h == H - 1:
+                assert torch.isnan(got[t, h]).all(), t
+            else:
+                assert torch.equal(got[t, h], clean[t, h]), (t, h)
+
+
+def test_a_piece_of_minus_infinity_scores(cuda_device):
+    """A unit that CTAs share, the first half of whose keys score -inf: they weigh
+    nothing, but an infinite value among them is 0 times infinity, a NaN."""
+    b = Chunks([40], [4000], 1, cuda_device, seed=64)
+    b.q[..., DN + 7] = -b.q[..., DN + 7].abs() - 0.01
+    b.kr[:2000, 7] = float("inf")
+    clean = b.run().clone()
+    assert torch.isfinite(clean).all()
+    half = Chunks([40], [2000], 1, cuda_device, seed=64)     # the other half alone
+    half.q, half.k, half.v, half.kr, half.out = b.q, b.k[2000:], b.v[2000:], b.kr[2000:], clean
+    half.check()
+    b.v[77, 0, 5] = float("inf")
+    got = b.run().clone()
+    assert pa.get_error() == pa.PA_OK
+    assert torch.isnan(got[..., 5]).all()
+    others = [d for d in range(DV) if d != 5]
+    assert torch.equal(got[..., others], clean[..., others])
