@@ -165,6 +165,7 @@ struct Tail {
   float2 sums[F8 ? kPieces : 1][F8 ? kLatentRows : 1];            // (reference, sum) of a piece
   alignas(4) uint8_t ask[2][4];  // by tile: softmax warps that ask for a rescale
   int32_t fix_tile;
+  int32_t cleared[2];            // by piece: the last one (+ 1) with a cell cleared
   uint32_t tmem;
   int abort;
 };
@@ -260,6 +261,61 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
+// Zeros in the place of infinities and NaN in the cells of a stage from row r0 on, by
+// a warp.
+template <bool F8, int KT, int kCols>
+__device__ __noinline__ void clear_cells(uint8_t* stage, int r0) {
+  constexpr uint32_t kField = F8 ? 0xFFu : 0xFFFFu, kOdd = F8 ? 0x7Fu : 0x7F80u;
+#pragma unroll 1
+  for (int i = r0 * kCols; i < KT * kCols; ++i) {
+    uint32_t* at = reinterpret_cast<uint32_t*>(stage + (i % kCols) * KT * 128 + i / kCols * 128) +
+                   (threadIdx.x & 31);
+    const uint32_t w = *at;
+    uint32_t keep = w;
+#pragma unroll 1
+    for (int b = 0; b < 32; b += F8 ? 8 : 16)
+      if ((w >> b & kOdd) == kOdd) keep &= ~(kField << b);
+    if (keep != w) *at = keep;
+  }
+}
+
+// NaN in the place of O's elements of the rows that see a cell in [key0, key1) which
+// is not finite in that dim (bf16 cells; all lanes of a warp, `dim` the lane's in the
+// first block of 128). The cells are read again: this is rare.
+template <int L, int NR>
+__device__ __noinline__ void put_back(uint32_t tmem_o, const uint8_t* latent, const int32_t* table,
+                                      int b_shift, int num_blocks, int dim, int key0, int key1,
+                                      int first, int sees, int heads) {
+  int32_t from[L / 128];  // the first such key, by block
+#pragma unroll
+  for (int b = 0; b < L / 128; ++b) from[b] = INT32_MAX;
+#pragma unroll 1
+  for (int key = key1 - 1; key >= key0; --key) {
+    const int32_t listed = __ldg(table + (key >> b_shift));
+    const int64_t id = listed < 0 || listed >= num_blocks ? 0 : listed;  // as the producer reads
+    const int64_t cell = (id << b_shift) + (key & ((1 << b_shift) - 1));
+    const uint16_t* c = reinterpret_cast<const uint16_t*>(latent) + cell * L + dim;
+#pragma unroll
+    for (int b = 0; b < L / 128; ++b)
+      if ((c[b * 128] & 0x7F80u) == 0x7F80u) from[b] = key;
+  }
+#pragma unroll 1
+  for (int i = 0; i < NR; i += 16) {
+#pragma unroll
+    for (int b = 0; b < L / 128; ++b) {
+      uint32_t o[16];
+      tmem_ld16(tmem_o + b * NR + i, o);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (sees + (int)((unsigned)(first + i + k) / (unsigned)heads) > from[b])
+          o[k] = 0x7FC00000u;
+      tmem_st16(tmem_o + b * NR + i, o);
+    }
+  }
+  tc::tmem_wait_st();
+}
+
 // ------------------------------------------------------------ the flat space
 
 // Sums of weights stop here. The host refuses batches that could come this far with
@@ -412,6 +468,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       mbar_init(&tail->l_full, 4);
     }
     tail->abort = 0;
+    tail->cleared[0] = tail->cleared[1] = 0;
     fence_mbar_init();
   }
   tc::fence_proxy_async_smem();
@@ -1192,21 +1249,17 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           }
           if (lane == 0) tail->ask[g & 1][w4] = ask;
           if (__builtin_expect(hiding && __any_sync(0xffffffffu, odd), 0)) {  // rare
-            // A later token's cell may not be finite. Its score then is that for every
-            // row: those that see it are NaN already, and zeros keep it from the others
-            // (0 times it is NaN)
+            // A later token's cell may not be finite, and 0 times it then a NaN: zeros
+            // keep it from the rows that hide it. Its score is no number for any row. One
+            // that sees it is NaN by that or, at -inf (no E4M3 code gives that), gets
+            // 0 times the element when it is written (put_back). Cells before the
+            // tile's first row's limit are seen by all rows and stay.
             if (live && !(ok = wait(&tail->k_full[g % kStages], g / kStages))) break;
-            uint32_t* cells =
-                reinterpret_cast<uint32_t*>(smem + S::kOffK + (g % kStages) * S::kStage);
-#pragma unroll 1
-            for (int i = lane; i < kCols * kChunk / 4; i += 32) {
-              uint32_t w = cells[i];
-              constexpr uint32_t kField = F8 ? 0xFFu : 0xFFFFu, kOdd = F8 ? 0x7Fu : 0x7F80u;
-#pragma unroll 1
-              for (int b = 0; b < 32; b += F8 ? 8 : 16)
-                if ((w >> b & kOdd) == kOdd) w &= ~(kField << b);
-              cells[i] = w;
-            }
+            const int seen = pc.sees + (int)((unsigned)pc.first / (unsigned)p.Hq);
+            clear_cells<F8, KT, kCols>(smem + S::kOffK + (g % kStages) * S::kStage,
+                                       max(0, seen - key0));
+            if (!F8 && lane == 0)
+              *reinterpret_cast<volatile int32_t*>(&tail->cleared[n & 1]) = n + 1;
           }
           if (key0 + KT > pc.n_keys) {
             // the tile holds keys past the last visible one (unloaded blocks,
@@ -1282,6 +1335,14 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         // ---- the piece's rows: normalised to out, or a partial
         if (!(ok = wait(&tail->pv_done[(g - 1) & 1], (g - 1) >> 1))) break;
         tc::fence_after_sync();
+        if constexpr (!F8) {
+          if (__builtin_expect(
+                  *reinterpret_cast<volatile int32_t*>(&tail->cleared[n & 1]) == n + 1, 0))
+            put_back<L, NR>(tmem + lanes, p.latent, p.block_tables + (int64_t)pc.r * p.max_blocks,
+                            p.b_shift, p.num_blocks, w4 * 32 + lane,
+                            max(pc.k0 * KT, pc.sees + (int)((unsigned)pc.first / (unsigned)p.Hq)),
+                            min(pc.k1 * KT, pc.n_keys), pc.first, pc.sees, p.Hq);
+        }
         if (pc.slot < 0) {
           // lane = dim, register = row: three exchanges between lanes whose
           // numbers differ in one bit leave 8 dims of two rows in each lane

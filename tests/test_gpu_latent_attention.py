@@ -392,3 +392,52 @@ def test_starts_that_claim_more_than_32_bits_of_work(cuda_device, fp8):
     pa.latent_forward(q, out, starts, i32(seq, dev), host, seq, table, pool, 0.1, workspace=ws)
     assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS
     assert (out == 9).all()
+
+
+def check_with_infinite_cells(b):
+    """b.out against the formula with its infinities (bf16 cells): a row is NaN where
+    a visible score is NaN or +inf or all are -inf; a key of score -inf weighs 0, and
+    0 times an element of it that is not finite is NaN. The rest within Batch.check's
+    tolerance, from the finite cells."""
+    lat, rot = ref.pool_rows(b.pool)
+    for r in range(len(b.seqs)):
+        at = ref.slots_of(b.tab, r, b.seqs[r], b.B)
+        c, kr = lat[at], rot[at]
+        k = np.concatenate((c, kr), -1)
+        for j in range(b.q_lens[r]):
+            t = int(b.qsl[r]) + j
+            n = b.seqs[r] - b.q_lens[r] + j + 1 if b.causal else b.seqs[r]
+            q = ref.f64(b.q[t])
+            with np.errstate(invalid="ignore"):
+                x = q @ k[:n].T * b.scale
+                row_nan = np.isnan(x).any(-1) | (x == np.inf).any(-1) | (x == -np.inf).all(-1)
+            good = np.isfinite(k[:n]).all(-1)
+            dims = ~np.isfinite(c[:n]).all(0)          # where some visible cell is not finite
+            got = ref.f64(b.out[t])
+            want_nan = row_nan[:, None] | dims[None]
+            np.testing.assert_array_equal(np.isnan(got), want_nan, err_msg=f"token {t}")
+            p = ref.softmax_rows(np.where(np.isfinite(x) & good, x, -np.inf))
+            v = np.where(good[:, None], c[:n], 0.0)
+            want, size = p @ v, p @ np.abs(v)
+            s_mag = b.scale * (np.abs(q)[:, :] @ np.abs(np.where(good[:, None], k[:n], 0.0)).T
+                               ).max(-1, keepdims=True)
+            tol = size * (ref.BF16_HALF + 2 * 2.0 ** -20 * s_mag) + ref.BF16_HALF * np.abs(want)
+            err = np.abs(np.where(want_nan, 0.0, got - want))
+            assert (err <= tol + 1e-30).all(), (t, (err / (tol + 1e-30)).max())
+
+
+@pytest.mark.parametrize("where", ["hidden", "seen"])
+@pytest.mark.parametrize("H,L,seqs,q_lens", [
+    (20, 256, [700, 40, 130], [9, 5, 130]), (3, 512, [700, 40, 130], [9, 5, 130]),
+    (64, 512, [300, 5000], [7, 4]), (16, 512, [20000], [3])])
+def test_an_infinite_element_of_either_score(cuda_device, H, L, seqs, q_lens, where):
+    """One infinite element in a cell, its scores +inf and -inf by the queries' signs:
+    the same result whether the tile also holds keys that some rows hide or not."""
+    b = Batch(seqs, q_lens, H, L, 16, False, cuda_device, seed=24)
+    for r, n in enumerate(q_lens):
+        key = b.seqs[r] - n + (n // 2 if where == "hidden" else 0) - (where == "seen")
+        slot = int(ref.slots_of(b.tab, r, b.seqs[r], b.B)[key])
+        b.pool.latent.view(-1, L)[slot, 130 + r] = float("inf") if r != 1 else float("-inf")
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    check_with_infinite_cells(b)
