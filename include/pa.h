@@ -553,7 +553,8 @@ pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src,
  * Cells past a request's seq_len may hold anything. A NaN or an infinity in a
  * query stays in its own row of out; one in a cell reaches the rows that see it
  * and no others. A cell that a row scores -inf weighs 0 there, which its elements
- * are still multiplied by (NaN where they are not finite).
+ * are still multiplied by (NaN where they are not finite); a row that scores
+ * every visible cell so is NaN.
  * The work is divided from the device arrays at every launch; the host mirrors
  * only size the launch. A captured call therefore follows device lengths that
  * change between replays, with exact results, as long as query_start_loc

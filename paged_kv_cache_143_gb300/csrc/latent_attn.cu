@@ -84,6 +84,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;   // S buffers from column 256 on
 constexpr uint32_t kTmemR = 384;   // E4M3: the rotary part of S from 384 on
 constexpr int kMaxStages = 8, kPieces = 4;
+constexpr float kNoKey = -1.f;     // as a partial's sum: the row sees none of its keys
 // The reference maximum moves when it grows by more than 2^kRescaleLog2; weights
 // of the maximum are placed at 2^kTargetLog2 (E5M2 weights must stay below 57344).
 template <bool F8> constexpr float kRescaleLog2 = F8 ? 7.f : 8.f;
@@ -764,10 +765,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         if (!more) {
           pc.r = -1;
         } else if (pc.k0 >= pc.k1) {
-          // no row of the tile sees these keys: sums of zero, which the join skips
+          // no row of the tile sees these keys: the join skips them
           if (pc.slot >= 0) {
             float2* ml = p.part_ml + (int64_t)(2 * cta + pc.slot) * NR;
-            for (int i = lane; i < NR; i += 32) ml[i] = make_float2(-INFINITY, 0.f);
+            for (int i = lane; i < NR; i += 32) ml[i] = make_float2(-INFINITY, kNoKey);
           }
           continue;
         }
@@ -1280,9 +1281,11 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               for (int o = 1; o <= kRowLanes; o <<= 1)
                 if (o & kRowLanes) u += __shfl_xor_sync(0xffffffffu, u, o);
               if ((lane & kRowLanes) == 0) {
-                tail->l[n & 1][row[t]] = u == 0.f ? 0.f : 1.f / u;  // (NaN stays NaN)
+                // (a row whose scores are all -inf has a sum of 0 and O 0 or NaN: NaN)
+                tail->l[n & 1][row[t]] = 1.f / u;
                 if (pc.slot >= 0)
-                  p.part_ml[(int64_t)(2 * cta + pc.slot) * NR + row[t]] = make_float2(m[t], u);
+                  p.part_ml[(int64_t)(2 * cta + pc.slot) * NR + row[t]] =
+                      make_float2(m[t], lim[t] > pc.k0 * KT ? u : kNoKey);
               }
             }
           }
@@ -1322,9 +1325,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             u = u * (m[0] == top ? 1.f : ex2_ftz(m[0] - top)) +
                 o.y * (o.x == top ? 1.f : ex2_ftz(o.x - top));
             if ((lane & kRowLanes) == 0) {
-              tail->l[n & 1][row[0]] = u == 0.f ? 0.f : 1.f / u;  // (NaN stays NaN)
+              tail->l[n & 1][row[0]] = 1.f / u;
               if (pc.slot >= 0)
-                p.part_ml[(int64_t)(2 * cta + pc.slot) * NR + row[0]] = make_float2(top, u);
+                p.part_ml[(int64_t)(2 * cta + pc.slot) * NR + row[0]] =
+                    make_float2(top, lim[0] > pc.k0 * KT ? u : kNoKey);
             }
           }
           __syncwarp();
@@ -1459,14 +1463,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
   float4 acc[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float m = -INFINITY, l = 0.f;   // running reference and sum of the pieces so far
+  float m = -INFINITY, l = kNoKey;  // running reference and sum of the pieces so far
 #pragma unroll 1
   for (int i0 = sub; live && i0 < n; i0 += kJoinBatch * share) {
     float4 x[kJoinBatch][kV];
     float2 ml[kJoinBatch];
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
+      ml[i] = make_float2(-INFINITY, kNoKey);
       if (i0 + i * share < n) {
         const int64_t at = slot(i0 + i * share) * NR + row;
         ml[i] = __ldcg(p.part_ml + at);
@@ -1479,10 +1483,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     float top = m;
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i)
-      if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);  // (a NaN sum counts)
+      if (!(ml[i].y < 0.f)) top = fmaxf(top, ml[i].x);  // (a NaN sum counts)
     const float keep = m == -INFINITY ? 0.f : ex2_ftz(m - top);
     m = top;
-    l *= keep;
+    if (l > 0.f) l *= keep;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       acc[v].x *= keep;
@@ -1492,9 +1496,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     }
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i) {
-      if (ml[i].y == 0.f) continue;
-      const float w = ex2_ftz(ml[i].x - m);
-      l = fmaf(w, ml[i].y, l);
+      if (ml[i].y < 0.f) continue;
+      // (scores of -inf alone weigh 0, which O may make a NaN)
+      const float w = ml[i].x == -INFINITY ? 0.f : ex2_ftz(ml[i].x - m);
+      l = fmaf(w, ml[i].y, l < 0.f ? 0.f : l);
 #pragma unroll
       for (int v = 0; v < kV; ++v) {
         acc[v].x = fmaf(w, x[i][v].x, acc[v].x);
@@ -1507,7 +1512,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
   uint2* dst = reinterpret_cast<uint2*>(p.out + (j.out_row + row) * L);
   if (share == 1) {
     if (!live) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l < 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int v = 0; v < kV; ++v)
       dst[lane + v * 32] = make_uint2(pack_bf16(acc[v].x * inv, acc[v].y * inv),
@@ -1523,25 +1528,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
   if (!live) return;
   const int w0 = warp - sub;
   float top = -INFINITY, sum = 0.f;
+  auto weight = [&](float x) { return x == -INFINITY ? 0.f : ex2_ftz(x - top); };
   for (int k = 0; k < share; ++k)
-    if (part_sum[w0 + k].y != 0.f) top = fmaxf(top, part_sum[w0 + k].x);
+    if (!(part_sum[w0 + k].y < 0.f)) top = fmaxf(top, part_sum[w0 + k].x);
   for (int k = 0; k < share; ++k)
-    if (part_sum[w0 + k].y != 0.f)
-      sum = fmaf(ex2_ftz(part_sum[w0 + k].x - top), part_sum[w0 + k].y, sum);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (!(part_sum[w0 + k].y < 0.f))
+      sum = fmaf(weight(part_sum[w0 + k].x), part_sum[w0 + k].y, sum);
+  const float inv = 1.f / sum;  // (every row sees a key)
   for (int q = sub * 32 + lane; q < L / 4; q += share * 32) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < share; ++k) {
       const float2 s = part_sum[w0 + k];
-      if (s.y == 0.f) continue;
-      const float w = ex2_ftz(s.x - top) * inv;
+      if (s.y < 0.f) continue;
+      const float w = weight(s.x);
       const float4 x = *reinterpret_cast<const float4*>(&part_acc[w0 + k][q * 4]);
       o.x = fmaf(w, x.x, o.x);
       o.y = fmaf(w, x.y, o.y);
       o.z = fmaf(w, x.z, o.z);
       o.w = fmaf(w, x.w, o.w);
     }
-    dst[q] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    dst[q] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   }
 }
 

@@ -441,3 +441,41 @@ def test_an_infinite_element_of_either_score(cuda_device, H, L, seqs, q_lens, wh
     b.run()
     assert pa.get_error() == pa.PA_OK
     check_with_infinite_cells(b)
+
+
+@pytest.mark.parametrize("L", [256, 512])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_scores_of_minus_infinity_alone(cuda_device, fp8, L):
+    """A row whose query holds an infinity that scores every visible key -inf is NaN,
+    as the softmax of such scores is, whether its keys are cut over CTAs or not."""
+    b = Batch([5000, 200, 1], [1, 3, 1], 20, L, 16, fp8, cuda_device, seed=25)
+    b.pool.rope[..., 7] = b.pool.rope[..., 7].abs() + 0.01      # (NaN cells stay NaN)
+    clean = b.run().clone()
+    bad = ((0, 3), (1, 7), (3, 19), (4, 0))
+    for t, h in bad:
+        b.q[t, h, L + 7] = float("-inf")
+    got = b.run()
+    assert pa.get_error() == pa.PA_OK
+    for t in range(b.T):
+        for h in range(b.H):
+            if (t, h) in bad:
+                assert torch.isnan(got[t, h]).all(), (t, h)
+            else:
+                assert torch.equal(got[t, h], clean[t, h]), (t, h)
+
+
+@pytest.mark.parametrize("seqs", [[20000], [5000, 7000], [300] * 160], ids=["one", "two", "many"])
+def test_pieces_of_minus_infinity_scores(cuda_device, seqs):
+    """Requests whose first half scores -inf: it weighs nothing, but an infinite
+    element among it is 0 times infinity, a NaN, in its dim; cut over CTAs and joined."""
+    b = Batch(seqs, [1] * len(seqs), 16, 512, 16, False, cuda_device, seed=26)
+    b.q[..., 512 + 7] = -b.q[..., 512 + 7].abs() - 0.01
+    for r, n in enumerate(seqs):
+        slots = torch.from_numpy(ref.slots_of(b.tab, r, n // 2, b.B)).to(cuda_device)
+        b.pool.rope.view(-1, 64)[slots, 7] = float("inf")
+        cell = b.pool.latent.view(-1, 512)[int(slots[n // 5])]
+        cell[99] = -float("inf")
+        b.q[r, :, 99] = b.q[r, :, 99].abs() + 0.01
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    check_with_infinite_cells(b)
