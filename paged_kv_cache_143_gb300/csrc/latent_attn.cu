@@ -1191,7 +1191,9 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             if constexpr (F8) {
               // weights p s in three parts, a byte a key: an f16 number's high byte is
               // its E5M2 truncation, so a part is the high byte after half a step is
-              // added to the magnitude, and what is left is exact in f16
+              // added to the magnitude, and what is left is exact in f16. (A NaN, 0x7FFF,
+              // becomes zeros: a hidden key's scale may be one; a row that sees it is NaN
+              // by its sum.)
               uint8_t* prow = ps + row[0] * 128 + (kWide ? 0 : (lane & 3) * 2);
               uint32_t bytes[3][VT / 4];  // wide: the codes of 4 keys each
 #pragma unroll

@@ -479,3 +479,24 @@ def test_pieces_of_minus_infinity_scores(cuda_device, seqs):
     b.run()
     assert pa.get_error() == pa.PA_OK
     check_with_infinite_cells(b)
+
+
+@pytest.mark.parametrize("H,L", [(20, 256), (3, 512), (64, 512)])
+def test_later_scales_that_are_not_numbers(cuda_device, H, L):
+    """A NaN or an infinity as the scale of a chunk's later E4M3 cell leaves the rows
+    that do not see it as they are; rows that see a NaN are NaN."""
+    b = Batch([700, 40, 130], [9, 5, 130], H, L, 16, True, cuda_device, seed=27)
+    clean = b.run().clone()
+    first = {}
+    for r, keys in ((0, (697, 699)), (1, (38,)), (2, (64, 65, 100))):
+        first[r] = min(keys)
+        for i, key in enumerate(keys):
+            slot = int(ref.slots_of(b.tab, r, b.seqs[r], b.B)[key])
+            b.pool.scales.view(-1)[slot] = float("nan") if i != 1 else float("inf")
+    got = b.run()
+    assert pa.get_error() == pa.PA_OK
+    for r in range(3):
+        a, n = int(b.qsl[r]), b.q_lens[r]
+        hide = first[r] - (b.seqs[r] - n)        # rows before this one do not see it
+        assert torch.equal(got[a:a + hide].view(torch.int16), clean[a:a + hide].view(torch.int16))
+        assert torch.isnan(got[a + hide:a + n]).all()
