@@ -434,8 +434,8 @@ pa_status pa_gather_rows(const void* src, int64_t src_rows, int64_t row_bytes,
  *                   PA_ROPE_INTERLEAVED: dims (2i, 2i + 1)
  *   factor          finite and positive (long-context scalings change inv_freq and this factor)
  *
- * Angles are exact to about 2^-24 of a turn at any position; fp32 arithmetic, one
- * rounding to bf16 (nearest-even). The inverse turn is the same call with
+ * Angles are off by less than 2^-25 of a turn at any position, for frequencies
+ * of magnitude up to 256; fp32 arithmetic, one rounding to bf16 (nearest-even). The inverse turn is the same call with
  * negated positions and 1 / factor. Errors: PA_ERR_INVALID (sizes, strides,
  * NULL or misaligned pointers), PA_ERR_UNSUPPORTED (odd rot_dim or above 256,
  * head_dim above 32768).

@@ -8,7 +8,7 @@
 // tokens' cosines and sines once into shared memory, while its vectors of x are
 // already on their way (four units of 16 or 32 bytes a thread), and every head
 // reuses them. fp32 arithmetic, one rounding to bf16. Measured: 8192 tokens x 32
-// heads x 128 dims (64 turned, half layout) in 24.7 us, 5430 GB/s (bound by HBM and by
+// heads x 128 dims (64 turned, half layout) in 24.9 us, 5390 GB/s (bound by HBM and by
 // instructions about alike); x 128 heads x 64 dims, interleaved, 52 us, 5130 GB/s (three
 // units in flight and five CTAs an SM: 23.1 and 58); 256 x 64 x 64 in 3.6 us, a launch.
 #include "pa_device.cuh"

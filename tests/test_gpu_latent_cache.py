@@ -108,6 +108,51 @@ def test_rope_turned_back(cuda_device):
     assert ((z.float() - x.float()).abs() <= pair * (2 * ref.BF16_HALF * 1.5 + 1e-5)).all()
 
 
+def exact_turns(pos, freq):
+    """pos * freq / (2 pi) in turns, within [-1/2, 1/2), by whole numbers: 1 / (2 pi) to
+    2^-200, freq a multiple of 2^-149."""
+    inv = 255752132986241185678408580023709873616295664310550962376831  # 2^200 / (2 pi)
+    t = (int(pos) * int(float(freq) * 2.0 ** 149) * inv) % (1 << 349)
+    return (t - (1 << 349) if t >> 348 else t) / 2.0 ** 349
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_angles_at_any_position(cuda_device, interleaved):
+    """Angles next to a whole number of half turns, where sin is small and its bf16
+    rounding with it: (1, 0) turned by theta is (cos, sin). The angle may be off by 2^-25
+    of a turn, sin by 2^-22 of itself (two fp32 steps), and both are rounded to bf16."""
+    rng = np.random.default_rng(6)
+    freq = np.concatenate((10.0 ** rng.uniform(-8, 0, 24), 2.0 ** rng.uniform(0, 8, 6),
+                           [1.0, -0.37])).astype(np.float32)
+    n, per = len(freq), 40
+    positions = []
+    for f in freq:                      # positions next to k / 2 turns, the nearest kept
+        top = 2 ** 31 - 1
+        k = rng.integers(-int(top * abs(f) / np.pi) - 1, int(top * abs(f) / np.pi) + 1, 4000)
+        p = np.clip(np.rint(k * np.pi / abs(float(f))), -top - 1, top).astype(np.int64)
+        off = [abs((2 * exact_turns(x, f) + 0.5) % 1 - 0.5) for x in p]
+        positions.append(p[np.argsort(off)[:per]])
+    pos = np.concatenate(positions)
+    x = torch.zeros(len(pos), 1, 2 * n, dtype=torch.bfloat16, device=cuda_device)
+    x[..., 0:2 * n:2 if interleaved else 1][..., :n] = 1.0
+    out = torch.empty_like(x)
+    pa.rope(x, out, i32(pos, cuda_device), torch.from_numpy(freq).to(cuda_device), interleaved)
+    assert pa.get_error() == pa.PA_OK
+    got = ref.f64(out)[:, 0]
+    small = 0
+    for i, f in enumerate(freq):
+        rows = range(per * i, per * i + per)
+        turns = np.array([exact_turns(pos[t], f) for t in rows])
+        c, s = (got[rows.start:rows.stop, j] for j in
+                ((2 * i, 2 * i + 1) if interleaved else (i, n + i)))
+        for value, want in ((c, np.cos(2 * np.pi * turns)), (s, np.sin(2 * np.pi * turns))):
+            tol = ref.BF16_HALF * np.abs(want) * (1 + 2.0 ** -20) + 2 * np.pi * 2.0 ** -25 \
+                + 2.0 ** -22 * np.abs(want)
+            assert (np.abs(value - want) <= tol).all(), (f, (np.abs(value - want) / tol).max())
+        small += int((np.abs(np.sin(2 * np.pi * turns)) < 2.0 ** -12).sum())
+    assert small > n * per // 2         # (the test's own inputs: most angles are such)
+
+
 ROWS = [(1, 16, 512), (5, 32, 256), (255, 64, 512), (256, 16, 256), (1030, 32, 512)]
 
 
