@@ -422,7 +422,7 @@ pa_status pa_gather_rows(const void* src, int64_t src_rows, int64_t row_bytes,
  *
  *   x, out          dev bf16 [T][num_heads][head_dim], innermost dims
  *                   contiguous, the token and head strides given in elements
- *                   (>= 0; x may repeat rows with stride 0, rows of out must
+ *                   (0 .. 2^38 - 1; x may repeat rows with stride 0, rows of out must
  *                   not overlap). out may be x itself, with the same strides
  *                   (then turned in place); otherwise the two must not overlap.
  *                   A rotary part at the end of a wider head is reached by
@@ -438,7 +438,7 @@ pa_status pa_gather_rows(const void* src, int64_t src_rows, int64_t row_bytes,
  * of magnitude up to 256; fp32 arithmetic, one rounding to bf16 (nearest-even). The inverse turn is the same call with
  * negated positions and 1 / factor. Errors: PA_ERR_INVALID (sizes, strides,
  * NULL or misaligned pointers), PA_ERR_UNSUPPORTED (odd rot_dim or above 256,
- * head_dim above 32768).
+ * head_dim above 32768, num_heads * head_dim above 2^31).
  */
 typedef enum pa_rope_layout { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
 

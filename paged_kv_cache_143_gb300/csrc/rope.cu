@@ -11,6 +11,8 @@
 // heads x 128 dims (64 turned, half layout) in 24.9 us, 5390 GB/s (bound by HBM and by
 // instructions about alike); x 128 heads x 64 dims, interleaved, 52 us, 5130 GB/s (three
 // units in flight and five CTAs an SM: 23.1 and 58); 256 x 64 x 64 in 3.6 us, a launch.
+#include <algorithm>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "rope_angle.cuh"
@@ -24,6 +26,8 @@ constexpr int kMaxPairs = 128;   // rot_dim <= 256
 constexpr int kMaxTokens = 64;   // tokens of one CTA
 constexpr int kMaxAngles = 1024; // (token, pair) angles of one CTA
 constexpr int kMaxDim = 32768;   // of a head, for the exact reciprocals
+constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements: more than any memory holds
+constexpr int kMaxHeadGroups = 65535;             // CTAs along the heads
 
 struct RopeParams {
   const __nv_bfloat16* x;
@@ -202,11 +206,14 @@ extern "C" pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_he
   // (the stride of a dimension of one entry is never used)
   const int64_t D = head_dim, xt = T > 1 ? x_token_stride : 0, ot = T > 1 ? out_token_stride : 0;
   const int64_t xh = num_heads > 1 ? x_head_stride : 0, oh = num_heads > 1 ? out_head_stride : 0;
-  if (xt < 0 || xh < 0 || ot < 0 || oh < 0) return PA_ERR_INVALID;
-  const bool heads_inside = (num_heads == 1 || oh >= D) &&
-                            (T == 1 || ot >= (num_heads - 1) * oh + D);
-  const bool tokens_inside = (T == 1 || ot >= D) &&
-                             (num_heads == 1 || oh >= (int64_t)(T - 1) * ot + D);
+  for (int64_t stride : {xt, xh, ot, oh})
+    if (stride < 0 || stride >= kMaxStride) return PA_ERR_INVALID;
+  // whether `outer` reaches past n rows of D that lie `inner` apart, by division
+  auto past = [&](int64_t outer, int64_t n, int64_t inner) {
+    return outer >= D && (n == 1 || inner <= (outer - D) / (n - 1));
+  };
+  const bool heads_inside = (num_heads == 1 || oh >= D) && (T == 1 || past(ot, num_heads, oh));
+  const bool tokens_inside = (T == 1 || ot >= D) && (num_heads == 1 || past(oh, T, ot));
   if (!heads_inside && !tokens_inside) return PA_ERR_INVALID;
   if (x == out && ((T > 1 && xt != ot) || (num_heads > 1 && xh != oh))) return PA_ERR_INVALID;
   if ((reinterpret_cast<uintptr_t>(x) & 1u) || (reinterpret_cast<uintptr_t>(out) & 1u) ||
@@ -237,8 +244,11 @@ extern "C" pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_he
   p.tokens = 1;
   p.heads = num_heads;
   if (per_token > kUnits) {
-    const int groups = (int)((per_token + kUnits - 1) / kUnits);
-    p.heads = (num_heads + groups - 1) / groups;
+    const int64_t groups = std::min<int64_t>((per_token + kUnits - 1) / kUnits, kMaxHeadGroups);
+    p.heads = (int)((num_heads + groups - 1) / groups);
+    // (then a token has 2^31 elements and more)
+    if ((int64_t)p.heads * units * units >= (int64_t)1 << 32 && p.heads > 1)
+      return PA_ERR_UNSUPPORTED;
   } else {
     p.tokens = (int)(kUnits / per_token);
     if (p.tokens > kMaxTokens) p.tokens = kMaxTokens;
@@ -250,9 +260,8 @@ extern "C" pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_he
   p.by_rot = reciprocal(p.rot_units);
   p.by_pass = reciprocal(p.pass_units);
   p.by_heads = reciprocal(num_heads);
-  const dim3 grid((unsigned)((T + p.tokens - 1) / p.tokens),
-                  (unsigned)((num_heads + p.heads - 1) / p.heads));
-  if (grid.y > 65535u) return PA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(((int64_t)T + p.tokens - 1) / p.tokens),
+                  (unsigned)(((int64_t)num_heads + p.heads - 1) / p.heads));
   if (vec)
     rope_kernel<VecUnit><<<grid, kThreads, 0, pa::as_stream(stream)>>>(p);
   else

@@ -153,6 +153,19 @@ def test_rope_angles_at_any_position(cuda_device, interleaved):
     assert small > n * per // 2         # (the test's own inputs: most angles are such)
 
 
+def test_rope_more_wide_heads_than_a_grid_has_rows(cuda_device):
+    """66000 heads of 8256 dims, each more than a CTA's work: one token of them."""
+    rng = np.random.default_rng(7)
+    H, D = 66000, 8256
+    x = randn(rng, (1, 1, D), cuda_device)
+    out = torch.empty(1, H, D, dtype=torch.bfloat16, device=cuda_device)
+    freq = pa.rope_frequencies(64)[0]
+    pa.rope(x.expand(1, H, D), out, i32([12345], cuda_device), freq.to(cuda_device))
+    check_turn(x, out[:, :1], [12345], freq.numpy(), False, 1.0)
+    assert torch.equal(out, out[:, :1].expand(1, H, D))
+    assert pa.get_error() == pa.PA_OK
+
+
 ROWS = [(1, 16, 512), (5, 32, 256), (255, 64, 512), (256, 16, 256), (1030, 32, 512)]
 
 

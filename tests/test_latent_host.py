@@ -97,6 +97,22 @@ def test_rope_refusals():
     assert call(H=1, D=32776, xt=40000, ot=40000) == pa.PA_ERR_UNSUPPORTED
 
 
+def test_rope_sizes_whose_products_pass_64_bits():
+    """Strides that no memory holds are refused, not multiplied; so are rows that
+    overlap by them."""
+    L = pa.lib()
+
+    def call(T, H, D, xt, xh, ot, oh):
+        return L.pa_rope(P, xt, xh, 32, ot, oh, P, T, H, D, P, 2, 0, 1.0, None)
+
+    top = 2 ** 31 - 1
+    for a in ((2, 3, 64, 64, 64, 64, 1 << 62), (3, 2, 64, 64, 64, 1 << 62, 64),
+              (2, 2, 64, 1 << 62, 64, 128, 64), (2, 2, 64, 128, 1 << 38, 128, 64),
+              (top, top, 1, 0, 0, (1 << 38) - 1, (1 << 38) - 1), (top, top, 1, 0, 0, top - 1, 1)):
+        assert call(*a) == pa.PA_ERR_INVALID, a
+    assert call(1, top, 32768, 0, 0, 0, 32768) == pa.PA_ERR_UNSUPPORTED
+
+
 def test_binding_checks_without_a_device():
     x = torch.zeros(2, 3, 8, dtype=torch.bfloat16)
     with pytest.raises(ValueError):  # not a CUDA tensor
