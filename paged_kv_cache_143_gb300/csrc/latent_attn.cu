@@ -72,6 +72,7 @@
 #include <cuda_fp8.h>
 
 #include "latent_attn.h"
+#include "mbar_poll.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "tc_ptx.cuh"
@@ -251,6 +252,11 @@ __device__ __forceinline__ void stmatrix_x4(void* row, uint32_t a, uint32_t b, u
                    smem_u32(row)),
                "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
+}
+
+// Asks L2 for `bytes` contiguous bytes (address and size multiples of 16).
+__device__ __forceinline__ void prefetch_l2(const void* gmem, unsigned bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gmem), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
