@@ -683,9 +683,10 @@ pa_status pa_forward_noalloc(const void* q, void* out, const int32_t* query_star
 /*
  * pa_selftest_wait_timeout — diagnostics, not part of the method on the pages.
  * Launches one small kernel that waits on a device barrier which nothing will
- * complete, through the same bounded wait that every kernel of this library
- * uses. The wait gives up after its limit (about 2 seconds), records the
- * timeout in the error word and returns: afterwards pa_get_error() reports
+ * complete, through the same bounded waits that the kernels of this library
+ * use, one after the other. Each gives up after its limit (2 seconds, so about
+ * 4 in all), the last records the timeout in the error word, and the kernel
+ * returns: afterwards pa_get_error() reports
  * PA_ERR_TIMEOUT. Lets callers and tests check the no-hang error path.
  */
 pa_status pa_selftest_wait_timeout(pa_stream_t stream);

@@ -173,29 +173,6 @@ struct Tail {
 };
 static_assert(sizeof(Tail<true>) <= 8192 && sizeof(Tail<false>) <= 2048, "Tail overruns its slot");
 
-// pa::mbar_wait without its timer: a cold line of instructions costs microseconds
-// once all SMs stream, and the timer's loop is one that every first wait would
-// fetch. Each try suspends the thread for at most about kTryNs, so the limit is
-// at least the pa::kWaitLimitNs that the tries add up to.
-constexpr unsigned kTryNs = 1000, kTries = 2000000;
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity, unsigned* err) {
-  const uint32_t addr = smem_u32(bar);
-#pragma unroll 1
-  for (unsigned i = 0; i < kTries; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(addr), "r"(parity), "r"(kTryNs)
-        : "memory");
-    if (ok) return true;
-  }
-  raise_error(err, kErrTimeout);
-  return false;
-}
-
 template <bool F8>
 __device__ __forceinline__ bool aborted(Tail<F8>* t) {
   return *reinterpret_cast<volatile int*>(&t->abort) != 0;
@@ -484,12 +461,17 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = tail->tmem;
 
+  // waits end early where another role has given up (not those for what is in flight
+  // when a role ends)
+  auto wait_for = [&](uint64_t* bar, unsigned parity) {
+    return mbar_wait_quiet(bar, parity, &tail->abort, p.err);
+  };
   // the next piece (n-th of the CTA) for one thread; r < 0 at the end
   // (n = -1: a tile of nothing, for the instruction cache)
   auto piece = [&](int n, bool& ok) -> Piece {
     Piece pc{0, 0, 1, KT, 0, -1, 0, -1, 0};
     if (n < 0) return pc;
-    ok = bar_wait(&tail->piece_full[n % kPieces], (n / kPieces) & 1, p.err);
+    ok = wait_for(&tail->piece_full[n % kPieces], (n / kPieces) & 1);
     if (ok)
       pc = tail->piece[n % kPieces];
     else
@@ -521,7 +503,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
             if (n > 0) {
               uint64_t* bar = &tail->q_empty;
               if (may_wait) {
-                if (!bar_wait(bar, (n - 1) & 1, p.err)) return false;
+                if (!wait_for(bar, (n - 1) & 1)) return false;
               } else if (!mbar_test_wait(bar, (n - 1) & 1)) {
                 return true;
               }
@@ -555,7 +537,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
               }
             if (g >= kStages && !mbar_test_wait(&tail->k_empty[st], phase)) {
               // the stage may be waiting for products that wait for this Q
-              ok = load_q(true) && bar_wait(&tail->k_empty[st], phase, p.err) && !aborted(tail);
+              ok = load_q(true) && wait_for(&tail->k_empty[st], phase) && !aborted(tail);
               if (!ok) break;
             }
             load_q(false);
@@ -597,9 +579,9 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         }
         // every issued copy lands before the CTA may leave
         if (!ok) tail->abort = 1;
-        if (queries > 0) bar_wait(&tail->q_full, (queries - 1) & 1, p.err);
+        if (queries > 0) mbar_wait_quiet(&tail->q_full, (queries - 1) & 1, nullptr, p.err);
         for (int i = max(0, g - kStages); i < g; ++i)
-          bar_wait(&tail->k_full[i % kStages], (i / kStages) & 1, p.err);
+          mbar_wait_quiet(&tail->k_full[i % kStages], (i / kStages) & 1, nullptr, p.err);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -616,13 +598,13 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           const bool live = n >= 0;
           const Piece pc = piece(n, ok);
           if (pc.r < 0) break;
-          if (live && !(ok = bar_wait(&tail->q_full, n & 1, p.err))) break;
+          if (live && !(ok = wait_for(&tail->q_full, n & 1))) break;
 #pragma unroll 1
           for (int j = pc.k0; j < pc.k1; ++j) {
             const int buf = g % kSBufs;
             ok = !live ||
-                 ((g < kSBufs || bar_wait(&tail->s_empty[buf], (g / kSBufs - 1) & 1, p.err)) &&
-                  bar_wait(&tail->k_full[st], phase, p.err));
+                 ((g < kSBufs || wait_for(&tail->s_empty[buf], (g / kSBufs - 1) & 1)) &&
+                  wait_for(&tail->k_full[st], phase));
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t ks = tc::desc_at(k_desc, st * S::kStage);
@@ -655,7 +637,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         }
         if (!ok) tail->abort = 1;
         tc::mma_commit(&tail->final_mma);
-        bar_wait(&tail->final_mma, 0, p.err);
+        mbar_wait_quiet(&tail->final_mma, 0, nullptr, p.err);
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -675,17 +657,17 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           if (pc.r < 0) break;
 #pragma unroll 1
           for (int j = pc.k0; j < pc.k1; ++j) {
-            if (live && !(ok = bar_wait(&tail->p_full[g & 1], (g >> 1) & 1, p.err))) break;
+            if (live && !(ok = wait_for(&tail->p_full[g & 1], (g >> 1) & 1))) break;
             if (j == pc.k0) {
               // the first product of a piece overwrites O: the last piece is out
-              if (n > 0 && !(ok = bar_wait(&tail->o_empty, (n - 1) & 1, p.err))) break;
+              if (n > 0 && !(ok = wait_for(&tail->o_empty, (n - 1) & 1))) break;
             } else if (*reinterpret_cast<volatile uint32_t*>(&tail->ask[g & 1][0]) != 0) {
               // rows of this tile have a new reference: O, complete up to the
               // tile before, is rescaled first
               *reinterpret_cast<volatile int32_t*>(&tail->fix_tile) = g;
-              ok = bar_wait(&tail->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err);
+              ok = wait_for(&tail->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
               mbar_arrive(&tail->fix);
-              ok = ok && bar_wait(&tail->fixed, fixes & 1, p.err);
+              ok = ok && wait_for(&tail->fixed, fixes & 1);
               if (!ok) break;
               ++fixes;
             }
@@ -721,7 +703,7 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         }
         if (!ok) tail->abort = 1;
         tc::mma_commit(&tail->final_mma);
-        bar_wait(&tail->final_mma, 0, p.err);
+        mbar_wait_quiet(&tail->final_mma, 0, nullptr, p.err);
       }
       __syncwarp();
     } else if (warp == 3) {
@@ -779,8 +761,8 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
           continue;
         }
         if (n >= kPieces)
-          ok = __all_sync(0xffffffffu, bar_wait(&tail->piece_empty[n % kPieces],
-                                                 (n / kPieces - 1) & 1, p.err));
+          ok = __all_sync(0xffffffffu, wait_for(&tail->piece_empty[n % kPieces],
+                                                 (n / kPieces - 1) & 1));
         if (!ok) break;
         // (the weights lie where the first copies will go)
         if (n == 0) tc::fence_proxy_async_smem();
@@ -874,13 +856,13 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
       // Waits for a barrier, doing the rescales that are asked for meanwhile (warps
       // 4-7: they hold all lanes of O between them).
       auto wait = [&](uint64_t* bar, int parity) -> bool {
+        WaitLimit limit;
 #pragma unroll 1
-        for (unsigned i = 0; i < 64 * kTries; ++i) {
+        do {
           if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
           if (!second && __all_sync(0xffffffffu, mbar_test_wait(&tail->fix, fixes & 1)))
             rescale();
-        }
-        if (lane == 0) raise_error(p.err, kErrTimeout);
+        } while (!__any_sync(0xffffffffu, limit.over(&tail->abort, p.err)));
         return false;
       };
       // E4M3: the rows of the piece's query tile as two parts (warps 8-11)

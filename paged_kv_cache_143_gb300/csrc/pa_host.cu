@@ -2,6 +2,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "mbar_poll.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -132,17 +133,24 @@ extern "C" uint64_t pa_kernel_launches(void) {
 }
 
 namespace {
-// Waits on a barrier that nothing completes, through the bounded wait every
-// kernel of the library uses: it gives up after pa::kWaitLimitNs, records
-// kErrTimeout and returns.
+// Waits on a barrier that nothing completes, in each form that the library's kernels
+// use. The polling one has to end at once where another role has given up, and after
+// pa::kWaitLimitNs (not much later) by itself; only then comes the plain one, which
+// gives up after as long, records kErrTimeout and returns.
 __global__ void wait_timeout_kernel(unsigned* err) {
   __shared__ uint64_t bar;
-  if (threadIdx.x == 0) {
-    pa::mbar_init(&bar, 1);
-    pa::fence_mbar_init();
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) pa::mbar_wait(&bar, 0, err);
+  if (threadIdx.x != 0) return;
+  pa::mbar_init(&bar, 1);
+  pa::fence_mbar_init();
+  const int given_up = 1, at_work = 0;
+  const unsigned long long t0 = pa::global_timer_ns();
+  bool as_stated = !pa::mbar_wait_quiet(&bar, 0, &given_up, nullptr);
+  const unsigned long long t1 = pa::global_timer_ns();
+  as_stated = as_stated && t1 - t0 < pa::kWaitLimitNs / 10;
+  as_stated = as_stated && !pa::mbar_wait_quiet(&bar, 0, &at_work, nullptr);
+  const unsigned long long took = pa::global_timer_ns() - t1;
+  if (as_stated && took >= pa::kWaitLimitNs && took < pa::kWaitLimitNs / 10 * 11)
+    pa::mbar_wait(&bar, 0, err);
 }
 }  // namespace
 

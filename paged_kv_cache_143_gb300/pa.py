@@ -926,8 +926,8 @@ def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, 
 
 
 def selftest_wait_timeout(stream=None) -> None:
-    """Runs the library's bounded device wait on a barrier nothing completes
-    (about 2 s); pa_get_error() afterwards reports PA_ERR_TIMEOUT."""
+    """Runs the library's bounded device waits on a barrier nothing completes
+    (about 4 s); pa_get_error() afterwards reports PA_ERR_TIMEOUT."""
     _check(lib().pa_selftest_wait_timeout(_stream(stream)), "pa_selftest_wait_timeout")
 
 

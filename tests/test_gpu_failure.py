@@ -153,3 +153,14 @@ def test_shared_prefix_device_mirror_errors_are_flagged_and_never_written(cuda_d
     assert (big[w.T:].view(torch.int16) == 0x1234).all()
     step.run(cascade=True)
     assert pa.get_error() == pa.PA_OK
+
+
+def test_every_form_of_the_bounded_wait_gives_up_in_time(cuda_device):
+    """The polling wait and the plain one each give up after 2 s, the first where it
+    polls, and the kernel raises no timeout if either leaves its limits."""
+    pa.selftest_wait_timeout()     # (modules are loaded)
+    pa.get_error()
+    t0 = time.time()
+    pa.selftest_wait_timeout()
+    assert pa.get_error() == pa.PA_ERR_TIMEOUT
+    assert 4.0 <= time.time() - t0 < 4.6
