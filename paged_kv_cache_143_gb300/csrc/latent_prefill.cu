@@ -203,21 +203,19 @@ __device__ __noinline__ bool clear_hidden(uint8_t* smem, Bars* bars, uint32_t tm
   return true;
 }
 
-// NaN in the place of the elements of this thread's row of O that a cleared value
-// of a key it sees (one below limit) belongs to. All lanes of a warp.
-__device__ __noinline__ void put_back(uint32_t tmem_o, int limit, const Bars* bars) {
-  tc::fence_after_sync();
+// NaN in the place of the elements of this thread's row (written by it before) that a
+// cleared value of a key it sees, one below limit, belongs to: in out, or in the shared
+// memory that the CTAs of a cluster join from.
+__device__ __noinline__ void put_back(__nv_bfloat16* out, float* piece, int row, int limit,
+                                      const Bars* bars) {
 #pragma unroll 1
-  for (int c = 0; c < kV; c += 32) {
-    uint32_t o[32];
-    tc::tmem_ld32(tmem_o + c, o);
-    tc::tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-      if (limit > bars->cleared[c + k]) o[k] = 0x7FC00000u;
-    tc::tmem_st32(tmem_o + c, o);
+  for (int d = 0; d < kV; ++d) {
+    if (limit <= bars->cleared[d]) continue;
+    if (out)
+      reinterpret_cast<uint16_t*>(out)[d] = 0x7FFFu;
+    else
+      piece[((d >> 2) ^ (row & 31)) * 4 + (d & 3)] = __uint_as_float(0x7FFFFFFFu);
   }
-  tc::tmem_wait_st();
 }
 
 template <bool kSplit>
@@ -588,10 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], (my_ntk - 1) & 1, p.err)))
       ok = false;
     if (!ok) bars->abort = 1;
-    // (all clears are done: those that matter to a tile precede its last product)
-    if (__builtin_expect(*reinterpret_cast<volatile int*>(&bars->any_cleared), 0) && ok &&
-        my_ntk > 0)
-      put_back(tmem_o, limit, bars);
+    // (all clears are done by now: those that matter to a tile precede its last product)
+    auto any_cleared = [&] {
+      return __builtin_expect(*reinterpret_cast<volatile int*>(&bars->any_cleared), 0) != 0;
+    };
     if constexpr (kSplit) {
       // both tiles' products are done and every copy has landed: Q and the ring
       // make room for the partials
@@ -615,6 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       (((c * 8 + q) ^ (row & 31)) << 4)) =
                 make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
       }
+      if (any_cleared() && my_ntk > 0)
+        put_back(nullptr, reinterpret_cast<float*>(smem) + (t * kM + row) * kV, row, limit, bars);
       tc::fence_before_sync();
       cluster_sync();
       // a warp joins a row: o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k
@@ -690,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (any_cleared() && valid) put_back(orow, nullptr, row, limit, bars);
     }
     tc::fence_before_sync();
     named_bar_sync(0, kThreads);
