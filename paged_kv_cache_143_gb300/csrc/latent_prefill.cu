@@ -246,11 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int npairs = (q_len + 2 * kM - 1) / (2 * kM);
   int pair;
   if (listed) {
-    // the device lengths may disagree with the mirrors that the list came
-    // from: a pair past the request's, or rows past its last listed pair
+    // the device lengths may disagree with the mirrors that the list came from: rows
+    // past the request's last listed pair are an error, a pair past its rows (a padded
+    // batch) is nothing to do
     pair = unit & 0x7FFF;
-    if ((pair >= npairs || ((unit & 0x8000) != 0 && pair != npairs - 1)) && reporter)
-      raise_error(p.err, kErrBounds);
+    if ((unit & 0x8000) != 0 && pair < npairs - 1 && reporter) raise_error(p.err, kErrBounds);
     if (pair >= npairs) return;
   } else {
     if (npairs > (int)gridDim.x && reporter) raise_error(p.err, kErrBounds);

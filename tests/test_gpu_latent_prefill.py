@@ -376,3 +376,15 @@ def test_a_piece_of_minus_infinity_scores(cuda_device):
     assert torch.isnan(got[..., 5]).all()
     others = [d for d in range(DV) if d != 5]
     assert torch.equal(got[..., others], clean[..., others])
+
+
+@pytest.mark.parametrize("q_lens,k_lens,spare", [
+    ([250], [250], 9), ([507, 3], [504, 80], 9), ([30, 1], [30, 40], 700), ([5], [3000], 300)])
+def test_padded_batches(cuda_device, q_lens, k_lens, spare):
+    """The mirrors plan for padding rows that end in a query tile of their own: the
+    batch is right, they stay as they are, and nothing is flagged."""
+    b = Chunks(q_lens, k_lens, 2, cuda_device, seed=71, spare=spare)
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check()
+    assert (b.out[b.qsl[-1]:] == 9).all()
