@@ -859,9 +859,12 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
         WaitLimit limit;
 #pragma unroll 1
         do {
-          if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
-          if (!second && __all_sync(0xffffffffu, mbar_test_wait(&tail->fix, fixes & 1)))
-            rescale();
+#pragma unroll 1
+          for (unsigned i = 0; i < kTries; ++i) {
+            if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
+            if (!second && __all_sync(0xffffffffu, mbar_test_wait(&tail->fix, fixes & 1)))
+              rescale();
+          }
         } while (!__any_sync(0xffffffffu, limit.over(&tail->abort, p.err)));
         return false;
       };

@@ -20,16 +20,16 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, unsigned parity) {
   return ok != 0;
 }
 
-// Bounds a loop of tries: told of every kTries-th failure, it says when to give up, which
-// is kWaitLimitNs after the first such or, with an `abort` flag, as soon as that is set
+// Bounds a wait: asked after every kTries failed tries, it says when to give up, which
+// is kWaitLimitNs after the first time or, with an `abort` flag, as soon as that is set
 // (another role has given up and raised the error). Reading the timer only then keeps it
 // out of the waits of a GPU at work: a cold line of instructions costs microseconds
-// once all SMs stream, and a timer's loop is one that every first wait would fetch.
+// once all SMs stream, and a timer's loop is one that every first wait would fetch. (A
+// loop of tries inside a loop of these, not one that counts: 2 to 3 % at latent 256.)
 constexpr unsigned kTries = 4096;
 class WaitLimit {
  public:
   __device__ __forceinline__ bool over(const int* abort, unsigned* err) {
-    if (++tries_ % kTries != 0) return false;
     since_ = check(since_, abort, err);
     return since_ == 0;
   }
@@ -44,7 +44,7 @@ class WaitLimit {
     raise_error(err, kErrTimeout);
     return 0;
   }
-  uint32_t tries_ = 0, since_ = 0;
+  uint32_t since_ = 0;
 };
 static_assert(kWaitLimitNs < 0xFFFFFFFFull - 1000000000ull, "the limit has to fit 32 bits of time");
 
@@ -57,15 +57,18 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, unsigned parity, 
   WaitLimit limit;
 #pragma unroll 1
   do {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(addr), "r"(parity), "r"(kTryNs)
-        : "memory");
-    if (ok) return true;
+#pragma unroll 1
+    for (unsigned i = 0; i < kTries; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(addr), "r"(parity), "r"(kTryNs)
+          : "memory");
+      if (ok) return true;
+    }
   } while (!limit.over(abort, err));
   return false;
 }
