@@ -453,7 +453,8 @@ pa_status pa_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, 
  *     latent[num_blocks][block_size][latent_dim]   bf16, or E4M3 codes
  *     rope  [num_blocks][block_size][rope_dim]     bf16
  *     scales[num_blocks][block_size]               fp32, E4M3 pools only
- * A code of token n stands for decode(code) * scales[n].
+ * A code of token n stands for decode(code) * scales[n]. pa_write_latent stores
+ * powers of two, 2^-60 and more; attention takes any scale from 2^-90 to 2^100.
  *
  * Supported: latent_dim in {256, 512}; rope_dim 64; block_size in {16, 32, 64}.
  */
@@ -547,7 +548,7 @@ pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src,
  * Computed in fp32 and rounded once to bf16; the softmax weights enter the
  * second product rounded to bf16. On E4M3 pools the codes are multiplied as
  * they are: the latent part of a query is taken to 2^-17 of its row's largest
- * element, and a weight times its cell's scale to 2^-9 of itself or 2^-24 of
+ * element (if that is 2^-119 at least), and a weight times its cell's scale to 2^-9 of itself or 2^-24 of
  * the row's largest such product. Rows of requests with q_len == 0 and rows
  * past query_start_loc[num_reqs] are not touched.
  * Cells past a request's seq_len may hold anything. A NaN or an infinity in a

@@ -915,9 +915,10 @@ __global__ void __launch_bounds__(Smem<L, NR, F8>::kThreads, 1)
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
               amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // 2^e brings the largest magnitude to [2^7, 2^8); exact
+            // 2^e brings the largest magnitude to [2^7, 2^8), if it is 2^-119 at least
+            // (2^-e is kept a normal number); exact
             const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-            const int e = amax > 0.f ? min(100, max(-120, 7 - ex)) : 0;
+            const int e = amax > 0.f ? min(126, 7 - ex) : 0;
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
             uint32_t hi[kPer / 4], lo[kPer / 4];
 #pragma unroll

@@ -500,3 +500,20 @@ def test_later_scales_that_are_not_numbers(cuda_device, H, L):
         hide = first[r] - (b.seqs[r] - n)        # rows before this one do not see it
         assert torch.equal(got[a:a + hide].view(torch.int16), clean[a:a + hide].view(torch.int16))
         assert torch.isnan(got[a + hide:a + n]).all()
+
+
+@pytest.mark.parametrize("H,L", [(20, 256), (16, 512), (64, 512)])
+@pytest.mark.parametrize("power", [105, -80])
+def test_small_queries_on_large_cells(cuda_device, H, L, power):
+    """E4M3 cells near the ends of the scales' range and queries as far the other way:
+    ordinary scores, whose query parts keep their bits."""
+    b = Batch([5, 9, 3, 200, 64], [1, 2, 1, 1, 4], H, L, 16, True, cuda_device, seed=28)
+    rng = np.random.default_rng(29)
+    for r, n in enumerate(b.seqs):
+        c = torch.from_numpy(rng.standard_normal((n, L)) * 2.0 ** power).to(cuda_device).bfloat16()
+        kr = torch.from_numpy(rng.standard_normal((n, 64))).to(cuda_device).bfloat16()
+        pa.write_latent(b.pool, c, kr, torch.from_numpy(ref.slots_of(b.tab, r, n, b.B)).to(cuda_device))
+    b.q[..., :L] *= 2.0 ** -power
+    b.run()
+    assert pa.get_error() == pa.PA_OK
+    b.check()
