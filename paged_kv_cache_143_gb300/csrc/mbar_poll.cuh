@@ -25,7 +25,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, unsigned parity) {
 // (another role has given up and raised the error). Reading the timer only then keeps it
 // out of the waits of a GPU at work: a cold line of instructions costs microseconds
 // once all SMs stream, and a timer's loop is one that every first wait would fetch. (A
-// loop of tries inside a loop of these, not one that counts: 2 to 3 % at latent 256.)
+// loop of tries inside a loop of these, not one that counts: up to 1.5 %.)
 constexpr unsigned kTries = 4096;
 class WaitLimit {
  public:

@@ -650,8 +650,12 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
                    `stretch` and the fastest not at all;
       "by_parts"   pairs that turn less than `slow` times over the original
                    context are divided by `stretch`, those that turn more than
-                   `fast` times are kept, a linear ramp between; the factor is
-                   1 + 0.1 ln(stretch).
+                   `fast` times are kept, and between the two a pair is mixed by
+                   its number of turns, linearly; the factor is 1 + 0.1 ln(stretch).
+                   Other implementations ramp linearly in the pair's index, between
+                   limits rounded to whole pairs, which gives the pairs between
+                   other frequencies: a model is to be served with the frequencies
+                   that it was trained with, which may be any tensor.
     """
     if rot_dim <= 0 or rot_dim % 2:
         raise ValueError("rot_dim must be positive and even")
