@@ -10,10 +10,10 @@
 // 2 (2 L + 64) operations on it; up to about 64 rows per request that is less
 // tensor time than the cell takes from HBM, so the design is laid out for streaming.
 // Measured, 152 requests x 4096 keys, L 512, blocks of 64 (HBM's share of the time
-// at 6783 GB/s 106 us; E4M3 59): 16 heads 117 us, 32 118, 64 126, 128 212 (there shared
+// at 6783 GB/s 106 us; E4M3 59): 16 heads 118 us, 32 120, 64 128, 128 215 (there shared
 // memory bounds: a 32-key tile takes 1450 cycles, 1250 of them the products' reads);
-// E4M3 16 heads 80 us, 64 117 (2750 cycles a 64-key tile, 2400 of them reads).
-// 160 decodes of 128 to 2048 keys x 32 heads: 56.5 us (35.3).
+// E4M3 16 heads 83 us, 64 117 (2750 cycles a 64-key tile, 2400 of them reads).
+// 160 decodes of 128 to 2048 keys x 32 heads: 57.0 us (35.3).
 //
 // One CTA per SM walks an equal share of all (row tile, key tile) pairs, a pass
 // over a request counting as four tiles more than it has (pa::LatentParams). Both

@@ -23,9 +23,10 @@
 // CTAs go out longest first from a host-planned list of (request, tile pair). Where
 // those are few, the keys of each are shared out over a cluster of CTAs, which join
 // their O, maxima and sums through each other's shared memory: no workspace, and
-// every output row still written once. 24 heads, 5 queries on 16000 keys: 258 -> 86 us.
-// Long chunks (4 of 1900 to 4096 queries behind up to 16000 keys, 24 heads) run at 1300
-// to 1354 TFLOP/s, 820 to 850 us: a pair of tiles takes 3500 cycles, the softmax chain
+// every output row still written once. 24 heads, 5 queries on 16000 keys: 258 -> 73 us.
+// Long chunks (4 of 1900 to 4096 queries behind up to 16000 keys, 24 heads) take 815 to
+// 850 us at 2.07 GHz (1375 to 1318 TFLOP/s) and 866 to 875 for seconds on end, under the
+// power cap: a pair of tiles takes 3500 cycles, the softmax chain
 // of one 3300 (S and P share TMEM columns), the products of both 2700.
 // Every wait is bounded; a timeout sets the error word and the CTA unwinds.
 #include <cudaTypedefs.h>
