@@ -630,6 +630,162 @@ pa_status pa_latent_prefill(const void* q, int64_t q_token_stride, int64_t q_hea
                             int32_t causal, pa_stream_t stream);
 
 /*
+ * Attention to a part of a long cache.
+ *
+ * Two ways to spend less on a long context, over the pools, tables and batches
+ * of pa_forward. They can be used alone or together.
+ *   fewer blocks read   each query token attends to k blocks, chosen for it by
+ *                       a cheap score: pa_update_block_bounds after pa_write_kv,
+ *                       then pa_score_blocks, pa_select_blocks and
+ *                       pa_sparse_forward in the place of pa_forward;
+ *   fewer tokens kept   a request's tokens that received the least attention
+ *                       leave the cache: pa_attention_mass beside pa_forward
+ *                       sums the weights, pa_select_tokens chooses and
+ *                       pa_compact_cache moves what stays.
+ * None of these calls but pa_attention_mass takes host mirrors: rows, lengths
+ * and work are found from the device arrays at every launch, so captured calls
+ * follow lengths that change between replays. Rows past
+ * query_start_loc[num_reqs] are not touched. Device entries that leave the
+ * buffers set PA_ERR_DEVICE_BOUNDS; what they would reach is skipped.
+ */
+
+/*
+ * pa_update_block_bounds — the least and the greatest key of each block that a
+ * step wrote to, dim by dim over the block's stored tokens.
+ *
+ *   bounds           dev bf16 [num_blocks][num_kv_heads][2][head_dim], 16-byte
+ *                    aligned: least, then greatest; those of blocks that the
+ *                    call does not reach are left as they are
+ *   query_start_loc  dev int32 [num_reqs+1]: request r's blocks from that of its
+ *                    first new token, (seq_len - q_len) / B, to its last are made
+ *                    anew. NULL: all blocks of every request (a compacted cache)
+ *   seq_lens         dev int32 [num_reqs]: stored tokens, this step's included
+ *   num_tokens       at least query_start_loc[num_reqs] (unused without it)
+ *
+ * Exact: bf16 keys as they are, E4M3 pools the decoded codes, without k_scale.
+ * A dim with a NaN key has NaN bounds; infinite keys count as the largest finite
+ * bf16. A block shared by several requests of one call has to hold the same
+ * number of stored tokens for each of them (full prefix blocks do).
+ */
+pa_status pa_update_block_bounds(const pa_kv_pool* pool, void* bounds,
+                                 const int32_t* query_start_loc, const int32_t* seq_lens,
+                                 const int32_t* block_tables, int32_t max_blocks,
+                                 int32_t num_reqs, int32_t num_tokens, pa_stream_t stream);
+
+/*
+ * pa_score_blocks — for each query token, kv head and block before it, the most
+ * that a key inside the block's bounds can score with any of the kv head's
+ * query heads:
+ *   scores[t][h][i] = k_scale * max over the query heads j of kv head h of
+ *       sum_d max(q[t][j][d], 0) * greatest[i][h][d]
+ *             + min(q[t][j][d], 0) * least[i][h][d]
+ * for the blocks i = 0 .. p / B, p the token's position (as pa_forward, causal).
+ *
+ *   q        dev bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned
+ *   bounds   as pa_update_block_bounds left them
+ *   scores   dev fp32 [num_tokens][num_kv_heads][max_blocks]; entries of blocks
+ *            past the token's own are left as they are
+ *   pool     sizes, type and k_scale (its keys are not read; k_scale counts for
+ *            E4M3 pools only)
+ *
+ * fp32 sums; NaN bounds or queries give NaN. The last block of a chunk's token
+ * is scored with all of its stored keys, also those after the token. At most 64
+ * query heads a kv head (PA_ERR_UNSUPPORTED).
+ */
+pa_status pa_score_blocks(const void* q, const void* bounds, float* scores,
+                          const int32_t* query_start_loc, const int32_t* seq_lens,
+                          const int32_t* block_tables, int32_t max_blocks, int32_t num_reqs,
+                          int32_t num_tokens, int32_t num_q_heads, const pa_kv_pool* pool,
+                          pa_stream_t stream);
+
+/*
+ * pa_select_blocks — of the c = p / B + 1 blocks that a token at position p may
+ * see, the first `first`, the last `last` and the ones with the greatest scores,
+ * k in all, for each kv head; all where c <= k.
+ *
+ *   scores     dev fp32 [num_tokens][num_kv_heads][max_blocks]
+ *   selected   dev int32 [num_tokens][num_kv_heads][k]: block indices in
+ *              ascending order, -1 behind them
+ *   first, last  0 or more, first + last <= k
+ *
+ * Exact: of equal scores the lower index is taken (0 and -0 are equal), NaN
+ * counts above every number.
+ */
+pa_status pa_select_blocks(const float* scores, const int32_t* query_start_loc,
+                           const int32_t* seq_lens, int32_t num_reqs, int32_t num_tokens,
+                           int32_t num_kv_heads, int32_t max_blocks, int32_t block_size,
+                           int32_t first, int32_t last, int32_t k, int32_t* selected,
+                           pa_stream_t stream);
+
+/*
+ * pa_sparse_forward — pa_forward (causal) in which a token's heads see only the
+ * blocks that its list for their kv head names:
+ *   out[t][h] = sum_n softmax_n(scale * q[t][h] . k_n) v_n
+ * over the keys n <= p of the blocks in selected[t][h / g].
+ *
+ *   selected  dev int32 [num_tokens][num_kv_heads][k]: logical blocks of the
+ *             request in any order; -1 names none; a block past the token names
+ *             no visible key. A block named twice counts twice.
+ *
+ * Computed in fp32 and rounded once to bf16; the softmax weights enter the
+ * second product rounded to 16 bits. A row without a visible key is zero; one
+ * that scores every visible key -inf, and one that meets a NaN, is NaN. Cells
+ * past a token's position may hold anything. The order of sums depends on the
+ * sizes of the call alone. Needs no workspace; any number of query heads a kv
+ * head. An entry below -1 or past max_blocks, or a block id outside the pool,
+ * sets PA_ERR_DEVICE_BOUNDS and is skipped.
+ */
+pa_status pa_sparse_forward(const void* q, void* out, const int32_t* query_start_loc,
+                            const int32_t* seq_lens, const int32_t* block_tables,
+                            int32_t max_blocks, int32_t num_reqs, int32_t num_tokens,
+                            int32_t num_q_heads, const int32_t* selected, int32_t k,
+                            const pa_kv_pool* pool, float scale, pa_stream_t stream);
+
+/*
+ * pa_select_tokens — of each request's n = seq_lens[r] stored tokens the first
+ * `first`, the last `last` and the ones with the greatest mass, k in all; all
+ * where n <= k. The rules are those of pa_select_blocks.
+ *
+ *   mass         dev fp32, row x at mass + x * mass_stride, max_reqs rows
+ *   idx_mapping  dev int32 [num_reqs]: request r's row; NULL: row r
+ *   kept         dev int32 [num_reqs][k]: token indices, ascending, -1 behind
+ *   kept_lens    dev int32 [num_reqs]: min(n, k)
+ */
+pa_status pa_select_tokens(const float* mass, int64_t mass_stride, int32_t max_reqs,
+                           const int32_t* idx_mapping, const int32_t* seq_lens, int32_t num_reqs,
+                           int32_t first, int32_t last, int32_t k, int32_t* kept,
+                           int32_t* kept_lens, pa_stream_t stream);
+
+/*
+ * pa_compact_cache — token kept[r][i] of request r becomes its token i, for
+ * i < kept_lens[r]: its keys and values move from the cell that src_tables gives
+ * to the one that dst_tables gives, its mass from place kept[r][i] of the
+ * request's row of mass_in to place i of its row of mass_out. Keys are moved as
+ * they are: rotary positions stay those of the tokens, so later queries go on
+ * from the true position, seq_lens and slots from the kept count.
+ *
+ *   src_tables  dev int32 [num_reqs][max_blocks]
+ *   dst_tables  dev int32 [num_reqs][dst_blocks]; at each place the block of
+ *               src_tables (moved in place) or one that no request of the call
+ *               reads. Blocks that others share are to be given new ones.
+ *   kept        dev int32 [num_reqs][k], strictly ascending
+ *   kept_lens   dev int32 [num_reqs], 0 .. k
+ *   mass_in, mass_out  dev fp32 rows as pa_select_tokens; may be the same array,
+ *               else they do not overlap; both NULL: none
+ *
+ * Copies of bits. Cells past kept_lens[r], and places of mass_out, are left as
+ * they are. The bounds of the moved blocks are made anew by
+ * pa_update_block_bounds without query_start_loc. A place outside its table, its
+ * row of mass or the pool sets PA_ERR_DEVICE_BOUNDS and is skipped. At most
+ * 65535 requests (PA_ERR_UNSUPPORTED).
+ */
+pa_status pa_compact_cache(const pa_kv_pool* pool, const int32_t* src_tables, int32_t max_blocks,
+                           const int32_t* dst_tables, int32_t dst_blocks, const int32_t* kept,
+                           int32_t k, const int32_t* kept_lens, int32_t num_reqs,
+                           const float* mass_in, float* mass_out, int64_t mass_stride,
+                           int32_t max_reqs, const int32_t* idx_mapping, pa_stream_t stream);
+
+/*
  * pa_get_error — synchronise `stream`, then return and clear the sticky
  * device error word of the current device: PA_ERR_TIMEOUT if a bounded wait
  * gave up, else PA_ERR_DEVICE_BOUNDS if an index was out of range, else

@@ -1,0 +1,57 @@
+// batch_rows.cuh — which request a row of a ragged batch belongs to, found on
+// the device from query_start_loc alone (no host mirror, so a captured call
+// follows device lengths that change between replays).
+#pragma once
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+// The last i of [0, n) with f(i) <= x, for f that does not fall (0 if there is
+// none). The lanes of a warp try 32 places at once: one round for up to 32
+// requests, two for 1024, each a load and a vote. All lanes get the answer.
+template <class F>
+__device__ __forceinline__ int warp_last_le(int n, int64_t x, F f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) >> 5;
+    const int64_t at = (int64_t)lane * step;
+    const bool le = at < len && (int64_t)f(lo + (int)at) <= x;
+    const int c = max(__popc(__ballot_sync(0xffffffffu, le)), 1);
+    const int skip = (c - 1) * step;
+    lo += skip;
+    len = min(step, len - skip);
+  }
+  return lo;
+}
+
+// Request r's rows and lengths, or false (with kErrBounds) where they leave the
+// batch's buffers.
+struct ReqSpan {
+  int q0, q_len, seq;
+};
+__device__ __forceinline__ bool request_span(const int32_t* qsl, const int32_t* seq_lens, int r,
+                                             int T, int64_t capacity, unsigned* err, ReqSpan& s) {
+  s.q0 = qsl[r];
+  const int end = qsl[r + 1];
+  s.seq = seq_lens[r];
+  s.q_len = end - s.q0;
+  if (s.q0 < 0 || end > T || s.q0 > end) {
+    raise_error(err, kErrBounds);
+    return false;
+  }
+  if (s.q_len > 0 && (s.seq < s.q_len || s.seq > capacity)) {
+    raise_error(err, kErrBounds);
+    return false;
+  }
+  return true;
+}
+
+// The request of row t, or -1 for a row behind the last sequence. The whole warp calls it.
+__device__ __forceinline__ int request_of_row(const int32_t* qsl, int R, int t) {
+  const int r = warp_last_le(R, t, [&](int i) { return __ldg(qsl + i); });
+  return t < qsl[r + 1] && t >= qsl[r] ? r : -1;
+}
+
+}  // namespace pa

@@ -30,6 +30,8 @@ EXPORTS = ("pa_write_kv", "pa_forward_workspace_size", "pa_forward", "pa_apply_s
            "pa_decode_graph_destroy", "pa_decode_graph_kernels",
            "pa_rope", "pa_write_latent", "pa_read_latent", "pa_copy_latent_blocks",
            "pa_latent_workspace_size", "pa_latent_forward", "pa_latent_prefill",
+           "pa_update_block_bounds", "pa_score_blocks", "pa_select_blocks", "pa_sparse_forward",
+           "pa_select_tokens", "pa_compact_cache",
            # include/pa_sched.h
            "pa_sched_create", "pa_sched_destroy", "pa_sched_add_request", "pa_sched_fork",
            "pa_sched_abort", "pa_sched_step", "pa_sched_commit", "pa_sched_get_stats",
@@ -142,6 +144,18 @@ def lib():
         L.pa_latent_prefill.restype = ctypes.c_int
         L.pa_latent_prefill.argtypes = [P, I64, I64, P, I64, I64, P, I64, P, I64, I64, P, P, P, P,
                                         P, I32, I32, I32, I32, I32, I32, I32, F32, I32, P]
+        L.pa_update_block_bounds.restype = ctypes.c_int
+        L.pa_update_block_bounds.argtypes = [PP, P, P, P, P, I32, I32, I32, P]
+        L.pa_score_blocks.restype = ctypes.c_int
+        L.pa_score_blocks.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, PP, P]
+        L.pa_select_blocks.restype = ctypes.c_int
+        L.pa_select_blocks.argtypes = [P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, P, P]
+        L.pa_sparse_forward.restype = ctypes.c_int
+        L.pa_sparse_forward.argtypes = [P, P, P, P, P, I32, I32, I32, I32, P, I32, PP, F32, P]
+        L.pa_select_tokens.restype = ctypes.c_int
+        L.pa_select_tokens.argtypes = [P, I64, I32, P, P, I32, I32, I32, I32, P, P, P]
+        L.pa_compact_cache.restype = ctypes.c_int
+        L.pa_compact_cache.argtypes = [PP, P, I32, P, I32, P, I32, P, I32, P, P, I64, I32, P, P]
         L.pa_get_error.restype = ctypes.c_int
         L.pa_get_error.argtypes = [P]
         L.pa_status_string.restype = ctypes.c_char_p
@@ -927,6 +941,232 @@ def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, 
         _on(dev, stream))
     if st:
         raise PaError(st, "pa_latent_prefill")
+
+
+# ------------------------------------------------- attention to a part of a cache
+
+def _pool_on(pool: KVPool, dev: int) -> None:
+    if pool.k.get_device() != dev or pool.v.get_device() != dev:
+        raise ValueError(f"the pool is on {pool.k.device}, the call on cuda:{dev}")
+
+
+def _batch_shapes(query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
+                  block_tables: torch.Tensor) -> int:
+    R = seq_lens.numel()
+    if query_start_loc.numel() != R + 1:
+        raise ValueError("query_start_loc must have num_reqs + 1 entries and seq_lens num_reqs")
+    if block_tables.dim() != 2 or block_tables.shape[0] != R:
+        raise ValueError("block_tables must be [num_reqs][max_blocks]")
+    return R
+
+
+def update_block_bounds(pool: KVPool, bounds: torch.Tensor, block_tables: torch.Tensor,
+                        seq_lens: torch.Tensor, query_start_loc: Optional[torch.Tensor] = None,
+                        num_tokens: Optional[int] = None, stream=None) -> None:
+    """The least and greatest key (bounds bf16 [num_blocks][Hkv][2][D]) of the
+    blocks that hold each request's new tokens, of which there are at most
+    num_tokens; without query_start_loc of all its blocks."""
+    R = seq_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != R:
+        raise ValueError("block_tables must be [num_reqs][max_blocks]")
+    if bounds.shape != (pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim):
+        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
+    if query_start_loc is not None:
+        if query_start_loc.numel() != R + 1:
+            raise ValueError("query_start_loc must have num_reqs + 1 entries")
+        if num_tokens is None:
+            raise ValueError("query_start_loc comes with num_tokens, the most that it may reach")
+    dev = _device_of(bounds, "bounds")
+    _pool_on(pool, dev)
+    if not (bounds.dtype is _BF16 and block_tables.dtype is _I32 is seq_lens.dtype
+            and block_tables.get_device() == seq_lens.get_device() == dev
+            and bounds.is_contiguous() and block_tables.is_contiguous()
+            and seq_lens.is_contiguous()
+            and (query_start_loc is None or (
+                query_start_loc.dtype is _I32 and query_start_loc.get_device() == dev
+                and query_start_loc.is_contiguous()))):
+        _explain(dev, (bounds, "bounds", _BF16, True), (block_tables, "block_tables", _I32, True),
+                 (seq_lens, "seq_lens", _I32, True),
+                 (query_start_loc, "query_start_loc", _I32, True))
+    st = (_lib or lib()).pa_update_block_bounds(
+        pool.ref(), bounds.data_ptr(),
+        None if query_start_loc is None else query_start_loc.data_ptr(), seq_lens.data_ptr(),
+        block_tables.data_ptr(), block_tables.shape[1], R,
+        0 if query_start_loc is None else num_tokens, _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_update_block_bounds")
+
+
+def score_blocks(q: torch.Tensor, bounds: torch.Tensor, scores: torch.Tensor,
+                 query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
+                 block_tables: torch.Tensor, pool: KVPool, stream=None) -> None:
+    """The most that a key inside each block's bounds can score with a token's
+    query heads: q [T][Hq][D], scores fp32 [T][Hkv][max_blocks]; entries of
+    blocks past a token's own are left as they are."""
+    R = _batch_shapes(query_start_loc, seq_lens, block_tables)
+    T, Hq, D = q.shape
+    if D != pool.head_dim or scores.shape != (T, pool.num_kv_heads, block_tables.shape[1]):
+        raise ValueError("q must be [T][Hq][head_dim] and scores [T][num_kv_heads][max_blocks]")
+    if bounds.shape != (pool.num_blocks, pool.num_kv_heads, 2, D):
+        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
+    dev = _device_of(q, "q")
+    _pool_on(pool, dev)
+    if not (q.dtype is _BF16 is bounds.dtype and scores.dtype is _F32
+            and query_start_loc.dtype is _I32 is seq_lens.dtype and block_tables.dtype is _I32
+            and (bounds.get_device() == scores.get_device() == query_start_loc.get_device()
+                 == seq_lens.get_device() == block_tables.get_device() == dev)
+            and q.is_contiguous() and bounds.is_contiguous() and scores.is_contiguous()
+            and query_start_loc.is_contiguous() and seq_lens.is_contiguous()
+            and block_tables.is_contiguous()):
+        _explain(dev, (q, "q", _BF16, True), (bounds, "bounds", _BF16, True),
+                 (scores, "scores", _F32, True), (query_start_loc, "query_start_loc", _I32, True),
+                 (seq_lens, "seq_lens", _I32, True), (block_tables, "block_tables", _I32, True))
+    st = (_lib or lib()).pa_score_blocks(
+        q.data_ptr(), bounds.data_ptr(), scores.data_ptr(), query_start_loc.data_ptr(),
+        seq_lens.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], R, T, Hq, pool.ref(),
+        _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_score_blocks")
+
+
+def select_blocks(scores: torch.Tensor, selected: torch.Tensor, query_start_loc: torch.Tensor,
+                  seq_lens: torch.Tensor, block_size: int, first: int = 1, last: int = 2,
+                  stream=None) -> None:
+    """Of the blocks that a token may see the first and last ones and those with
+    the greatest scores [T][Hkv][max_blocks], k in all: selected int32
+    [T][Hkv][k], ascending, -1 behind them."""
+    T, H, max_blocks = scores.shape
+    R = seq_lens.numel()
+    if query_start_loc.numel() != R + 1:
+        raise ValueError("query_start_loc must have num_reqs + 1 entries and seq_lens num_reqs")
+    if selected.dim() != 3 or selected.shape[:2] != (T, H):
+        raise ValueError("selected must be [T][num_kv_heads][k]")
+    dev = _device_of(scores, "scores")
+    if not (scores.dtype is _F32 and selected.dtype is _I32
+            and query_start_loc.dtype is _I32 is seq_lens.dtype
+            and (selected.get_device() == query_start_loc.get_device() == seq_lens.get_device()
+                 == dev)
+            and scores.is_contiguous() and selected.is_contiguous()
+            and query_start_loc.is_contiguous() and seq_lens.is_contiguous()):
+        _explain(dev, (scores, "scores", _F32, True), (selected, "selected", _I32, True),
+                 (query_start_loc, "query_start_loc", _I32, True),
+                 (seq_lens, "seq_lens", _I32, True))
+    st = (_lib or lib()).pa_select_blocks(
+        scores.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(), R, T, H, max_blocks,
+        int(block_size), int(first), int(last), selected.shape[2], selected.data_ptr(),
+        _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_select_blocks")
+
+
+def sparse_forward(q: torch.Tensor, out: torch.Tensor, query_start_loc: torch.Tensor,
+                   seq_lens: torch.Tensor, block_tables: torch.Tensor, selected: torch.Tensor,
+                   pool: KVPool, scale: float, stream=None) -> None:
+    """`forward` (causal) in which a token's heads see only the blocks that
+    selected int32 [T][Hkv][k] names for their kv head (-1: none)."""
+    R = _batch_shapes(query_start_loc, seq_lens, block_tables)
+    T, Hq, D = q.shape
+    if D != pool.head_dim or out.shape != q.shape:
+        raise ValueError("q and out must be [T][Hq][head_dim]")
+    if selected.dim() != 3 or selected.shape[:2] != (T, pool.num_kv_heads):
+        raise ValueError("selected must be [T][num_kv_heads][k]")
+    dev = _device_of(q, "q")
+    _pool_on(pool, dev)
+    if not (q.dtype is _BF16 is out.dtype and selected.dtype is _I32
+            and query_start_loc.dtype is _I32 is seq_lens.dtype and block_tables.dtype is _I32
+            and (out.get_device() == selected.get_device() == query_start_loc.get_device()
+                 == seq_lens.get_device() == block_tables.get_device() == dev)
+            and q.is_contiguous() and out.is_contiguous() and selected.is_contiguous()
+            and query_start_loc.is_contiguous() and seq_lens.is_contiguous()
+            and block_tables.is_contiguous()):
+        _explain(dev, (q, "q", _BF16, True), (out, "out", _BF16, True),
+                 (selected, "selected", _I32, True),
+                 (query_start_loc, "query_start_loc", _I32, True),
+                 (seq_lens, "seq_lens", _I32, True), (block_tables, "block_tables", _I32, True))
+    st = (_lib or lib()).pa_sparse_forward(
+        q.data_ptr(), out.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(),
+        block_tables.data_ptr(), block_tables.shape[1], R, T, Hq, selected.data_ptr(),
+        selected.shape[2], pool.ref(), float(scale), _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_sparse_forward")
+
+
+def _mass_shape(mass: torch.Tensor, idx_mapping: Optional[torch.Tensor], R: int) -> None:
+    if mass.dim() != 2:
+        raise ValueError("mass must be [max_reqs][places]")
+    if idx_mapping is None:
+        if mass.shape[0] < R:
+            raise ValueError("mass must have a row for each request")
+    elif idx_mapping.numel() != R:
+        raise ValueError("idx_mapping must have one entry per request")
+
+
+def select_tokens(mass: torch.Tensor, kept: torch.Tensor, kept_lens: torch.Tensor,
+                  seq_lens: torch.Tensor, idx_mapping: Optional[torch.Tensor] = None,
+                  first: int = 4, last: int = 64, stream=None) -> None:
+    """Of each request's stored tokens the first and last ones and those with the
+    greatest mass [max_reqs][places] (row idx_mapping[r], or r): kept int32
+    [R][k], ascending, -1 behind them, kept_lens[r] of them."""
+    R = seq_lens.numel()
+    _mass_shape(mass, idx_mapping, R)
+    if kept.dim() != 2 or kept.shape[0] != R or kept_lens.numel() != R:
+        raise ValueError("kept must be [num_reqs][k] and kept_lens have num_reqs entries")
+    dev = _device_of(mass, "mass")
+    if not (mass.dtype is _F32 and kept.dtype is _I32 is kept_lens.dtype
+            and seq_lens.dtype is _I32
+            and (kept.get_device() == kept_lens.get_device() == seq_lens.get_device() == dev)
+            and mass.is_contiguous() and kept.is_contiguous() and kept_lens.is_contiguous()
+            and seq_lens.is_contiguous()
+            and (idx_mapping is None or (
+                idx_mapping.dtype is _I32 and idx_mapping.get_device() == dev
+                and idx_mapping.is_contiguous()))):
+        _explain(dev, (mass, "mass", _F32, True), (kept, "kept", _I32, True),
+                 (kept_lens, "kept_lens", _I32, True), (seq_lens, "seq_lens", _I32, True),
+                 (idx_mapping, "idx_mapping", _I32, True))
+    st = (_lib or lib()).pa_select_tokens(
+        mass.data_ptr(), mass.shape[1], mass.shape[0],
+        None if idx_mapping is None else idx_mapping.data_ptr(), seq_lens.data_ptr(), R,
+        int(first), int(last), kept.shape[1], kept.data_ptr(), kept_lens.data_ptr(),
+        _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_select_tokens")
+
+
+def compact_cache(pool: KVPool, src_tables: torch.Tensor, dst_tables: torch.Tensor,
+                  kept: torch.Tensor, kept_lens: torch.Tensor,
+                  mass_in: Optional[torch.Tensor] = None, mass_out: Optional[torch.Tensor] = None,
+                  idx_mapping: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Token kept[r][i] of request r becomes its token i (i < kept_lens[r]): keys
+    and values move from the cells of src_tables to those of dst_tables (the same
+    blocks, or blocks that no request of the call reads), mass within the
+    request's row."""
+    R = kept_lens.numel()
+    if kept.dim() != 2 or kept.shape[0] != R:
+        raise ValueError("kept must be [num_reqs][k]")
+    for t in (src_tables, dst_tables):
+        if t.dim() != 2 or t.shape[0] != R:
+            raise ValueError("src_tables and dst_tables must be [num_reqs][blocks]")
+    if (mass_in is None) != (mass_out is None):
+        raise ValueError("mass_in and mass_out come together")
+    if mass_in is not None:
+        _mass_shape(mass_in, idx_mapping, R)
+        if mass_out.shape != mass_in.shape:
+            raise ValueError("mass_in and mass_out must have one shape")
+    dev = _device_of(kept, "kept")
+    _pool_on(pool, dev)
+    _explain(dev, (kept, "kept", _I32, True), (kept_lens, "kept_lens", _I32, True),
+             (src_tables, "src_tables", _I32, True), (dst_tables, "dst_tables", _I32, True),
+             (mass_in, "mass_in", _F32, True), (mass_out, "mass_out", _F32, True),
+             (idx_mapping, "idx_mapping", _I32, True))
+    rows, places = (0, 0) if mass_in is None else mass_in.shape
+    st = (_lib or lib()).pa_compact_cache(
+        pool.ref(), src_tables.data_ptr(), src_tables.shape[1], dst_tables.data_ptr(),
+        dst_tables.shape[1], kept.data_ptr(), kept.shape[1], kept_lens.data_ptr(), R,
+        None if mass_in is None else mass_in.data_ptr(),
+        None if mass_out is None else mass_out.data_ptr(), places, rows,
+        None if idx_mapping is None else idx_mapping.data_ptr(), _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_compact_cache")
 
 
 def selftest_wait_timeout(stream=None) -> None:
