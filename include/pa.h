@@ -742,6 +742,48 @@ pa_status pa_sparse_forward(const void* q, void* out, const int32_t* query_start
                             const pa_kv_pool* pool, float scale, pa_stream_t stream);
 
 /*
+ * pa_attention_mass — the attention that each stored token has received: for
+ * the tokens n < seq_lens[r] of request r, in its row of mass,
+ *   mass_out[n] = old[n] + sum over the last w query tokens of the step that see
+ *                 n and all query heads of softmax_n(scale * q . k_n),
+ *   old[n] = decay * mass_in[n] for tokens stored before this step, 0 for the
+ *            step's own (whatever mass_in holds there),
+ *   w = min(q_len, window), or q_len with window 0.
+ * The batch, the pool and causal visibility are those of pa_forward (causal 1);
+ * the step's keys are already written. Requests with q_len 0 are not touched,
+ * and places past seq_lens[r] are not.
+ *
+ *   mass_in, mass_out  dev fp32, row x at mass + x * mass_stride, max_reqs rows;
+ *                may be the same array, else they do not overlap
+ *   idx_mapping  dev int32 [num_reqs]: request r's row; NULL: row r. A row listed
+ *                twice is left unspecified
+ *   workspace    dev scratch of at least pa_attention_mass_workspace_size bytes
+ *                for the same mirrors and window, 16-byte aligned. Calls that may
+ *                run at the same time need workspaces of their own.
+ *
+ * fp32 scores, weights and sums, in an order that the sizes decide. The queries
+ * of E4M3 pools are taken to 2^-17 of their row's largest element. A NaN or an
+ * infinity in a query, or in a key that a query sees, makes that query's weights
+ * NaN where its softmax is. The mirrors plan the launch: a captured call follows
+ * device lengths that stay at or below them, request by request; others set
+ * PA_ERR_DEVICE_BOUNDS and are left out.
+ * PA_ERR_INVALID: mirrors as for pa_forward, a length above mass_stride, a
+ * workspace too small. PA_ERR_UNSUPPORTED: more than 65535 requests.
+ */
+size_t pa_attention_mass_workspace_size(const int32_t* qsl_host, const int32_t* seq_lens_host,
+                                        int32_t num_reqs, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t window);
+
+pa_status pa_attention_mass(const void* q, const float* mass_in, float* mass_out,
+                            int64_t mass_stride, int32_t max_reqs, const int32_t* idx_mapping,
+                            const int32_t* query_start_loc, const int32_t* seq_lens,
+                            const int32_t* qsl_host, const int32_t* seq_lens_host,
+                            const int32_t* block_tables, int32_t max_blocks, int32_t num_reqs,
+                            int32_t num_tokens, int32_t num_q_heads, const pa_kv_pool* pool,
+                            float scale, float decay, int32_t window, void* workspace,
+                            size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * pa_select_tokens — of each request's n = seq_lens[r] stored tokens the first
  * `first`, the last `last` and the ones with the greatest mass, k in all; all
  * where n <= k. The rules are those of pa_select_blocks.

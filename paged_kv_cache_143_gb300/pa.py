@@ -31,7 +31,8 @@ EXPORTS = ("pa_write_kv", "pa_forward_workspace_size", "pa_forward", "pa_apply_s
            "pa_rope", "pa_write_latent", "pa_read_latent", "pa_copy_latent_blocks",
            "pa_latent_workspace_size", "pa_latent_forward", "pa_latent_prefill",
            "pa_update_block_bounds", "pa_score_blocks", "pa_select_blocks", "pa_sparse_forward",
-           "pa_select_tokens", "pa_compact_cache",
+           "pa_attention_mass_workspace_size", "pa_attention_mass", "pa_select_tokens",
+           "pa_compact_cache",
            # include/pa_sched.h
            "pa_sched_create", "pa_sched_destroy", "pa_sched_add_request", "pa_sched_fork",
            "pa_sched_abort", "pa_sched_step", "pa_sched_commit", "pa_sched_get_stats",
@@ -152,6 +153,11 @@ def lib():
         L.pa_select_blocks.argtypes = [P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, P, P]
         L.pa_sparse_forward.restype = ctypes.c_int
         L.pa_sparse_forward.argtypes = [P, P, P, P, P, I32, I32, I32, I32, P, I32, PP, F32, P]
+        L.pa_attention_mass_workspace_size.restype = SZ
+        L.pa_attention_mass_workspace_size.argtypes = [P, P, I32, I32, I32, I32]
+        L.pa_attention_mass.restype = ctypes.c_int
+        L.pa_attention_mass.argtypes = [P, P, P, I64, I32, P, P, P, P, P, P, I32, I32, I32, I32,
+                                        PP, F32, F32, I32, P, SZ, P]
         L.pa_select_tokens.restype = ctypes.c_int
         L.pa_select_tokens.argtypes = [P, I64, I32, P, P, I32, I32, I32, I32, P, P, P]
         L.pa_compact_cache.restype = ctypes.c_int
@@ -1099,6 +1105,68 @@ def _mass_shape(mass: torch.Tensor, idx_mapping: Optional[torch.Tensor], R: int)
             raise ValueError("mass must have a row for each request")
     elif idx_mapping.numel() != R:
         raise ValueError("idx_mapping must have one entry per request")
+
+
+def attention_mass_workspace_size(qsl_host, seq_lens_host, num_q_heads: int, num_kv_heads: int,
+                                  window: int = 0) -> int:
+    """Bytes of the workspace that attention_mass needs for a batch like this."""
+    qh, sh = _host_i32(qsl_host), _host_i32(seq_lens_host)
+    if qh.size != sh.size + 1:
+        raise ValueError("qsl_host must have num_reqs + 1 entries")
+    return int(lib().pa_attention_mass_workspace_size(_np_addr(qh), _np_addr(sh), sh.size,
+                                                      num_q_heads, num_kv_heads, int(window)))
+
+
+def attention_mass(q: torch.Tensor, mass_in: torch.Tensor, mass_out: torch.Tensor,
+                   query_start_loc: torch.Tensor, seq_lens: torch.Tensor, qsl_host, seq_lens_host,
+                   block_tables: torch.Tensor, pool: KVPool, scale: float,
+                   idx_mapping: Optional[torch.Tensor] = None, decay: float = 1.0,
+                   window: int = 0, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """What each stored token has received: decay * mass_in for the tokens stored
+    before, plus the softmax weights of the step's last `window` queries (0: all)
+    of all heads. mass fp32 [max_reqs][places], row idx_mapping[r] (or r)."""
+    qh = _host_i32(qsl_host)
+    sh = _host_i32(seq_lens_host)
+    R = _batch_shapes(query_start_loc, seq_lens, block_tables)
+    if qh.size != R + 1 or sh.size != R:
+        raise ValueError("the host mirrors must have the entries of the device arrays")
+    T, Hq, D = q.shape
+    if D != pool.head_dim:
+        raise ValueError("q must be [T][Hq][head_dim]")
+    _mass_shape(mass_in, idx_mapping, R)
+    if mass_out.shape != mass_in.shape:
+        raise ValueError("mass_in and mass_out must have one shape")
+    dev = _device_of(q, "q")
+    _pool_on(pool, dev)
+    if not (q.dtype is _BF16 and mass_in.dtype is _F32 is mass_out.dtype
+            and query_start_loc.dtype is _I32 is seq_lens.dtype and block_tables.dtype is _I32
+            and (mass_in.get_device() == mass_out.get_device() == query_start_loc.get_device()
+                 == seq_lens.get_device() == block_tables.get_device() == dev)
+            and q.is_contiguous() and mass_in.is_contiguous() and mass_out.is_contiguous()
+            and query_start_loc.is_contiguous() and seq_lens.is_contiguous()
+            and block_tables.is_contiguous()
+            and (idx_mapping is None or (
+                idx_mapping.dtype is _I32 and idx_mapping.get_device() == dev
+                and idx_mapping.is_contiguous()))
+            and (workspace is None or (workspace.get_device() == dev
+                                       and workspace.is_contiguous()))):
+        _explain(dev, (q, "q", _BF16, True), (mass_in, "mass_in", _F32, True),
+                 (mass_out, "mass_out", _F32, True),
+                 (query_start_loc, "query_start_loc", _I32, True),
+                 (seq_lens, "seq_lens", _I32, True), (block_tables, "block_tables", _I32, True),
+                 (idx_mapping, "idx_mapping", _I32, True),
+                 (workspace, "workspace", None if workspace is None else workspace.dtype, True))
+    st = (_lib or lib()).pa_attention_mass(
+        q.data_ptr(), mass_in.data_ptr(), mass_out.data_ptr(), mass_in.shape[1],
+        mass_in.shape[0], None if idx_mapping is None else idx_mapping.data_ptr(),
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), _np_addr(qh), _np_addr(sh),
+        block_tables.data_ptr(), block_tables.shape[1], R, T, Hq, pool.ref(), float(scale),
+        float(decay), int(window), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _on(dev, stream))
+    if st:
+        raise PaError(st, "pa_attention_mass")
 
 
 def select_tokens(mass: torch.Tensor, kept: torch.Tensor, kept_lens: torch.Tensor,
