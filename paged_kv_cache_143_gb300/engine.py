@@ -26,7 +26,9 @@ batch is row t) and the sampled tokens.
 LatentEngine runs the same loop over a latent cache: pa_copy_latent_blocks,
 pa_write_latent (which turns the rotary keys by the positions that
 pa_prepare_inputs made) and, for the queries, pa_rope and pa_latent_forward
-take the places of the calls on keys and values.
+take the places of the calls on keys and values. SparseEngine runs it with
+attention to a part of each context: pa_update_block_bounds, pa_score_blocks,
+pa_select_blocks and pa_sparse_forward in the place of pa_forward.
 """
 from typing import Optional
 
@@ -207,3 +209,41 @@ class LatentEngine(Engine):
         pa.latent_forward(q[:T], out[:T], self.qsl[:R + 1], self.seq[:R], b.query_start_loc,
                           b.seq_lens, self.gathered[:R], self.pool, self.scale, 1,
                           workspace=self.ws, stream=s)
+
+
+class SparseEngine(Engine):
+    """The serving loop with attention to a part of each context: every token's
+    heads attend to `num_selected` blocks of their kv head, chosen by the bounds
+    of the blocks' keys (pa_score_blocks) with the first `first` and the newest
+    `last` among them. Contexts of no more blocks than that are attended to
+    whole, as Engine does."""
+
+    def __init__(self, sched: "pa.Scheduler", pool: "pa.KVPool", num_q_heads: int, max_reqs: int,
+                 max_blocks: int, max_tokens: int, scale: float, num_selected: int,
+                 first: int = 1, last: int = 2, device=None):
+        super().__init__(sched, pool, num_q_heads, max_reqs, max_blocks, max_tokens, scale,
+                         device=device)
+        self.first, self.last = first, last
+        H = pool.num_kv_heads
+        self.bounds = torch.zeros((pool.num_blocks, H, 2, pool.head_dim), dtype=torch.bfloat16,
+                                  device=self.dev)
+        self.scores = torch.empty((max_tokens, H, max_blocks), dtype=torch.float32,
+                                  device=self.dev)
+        self.selected = torch.empty((max_tokens, H, num_selected), dtype=torch.int32,
+                                    device=self.dev)
+
+    def _workspace_bytes(self, max_splits: int) -> int:
+        return 0
+
+    def _attend(self, q: torch.Tensor, out: torch.Tensor, b: "pa.SchedBatch", R: int, T: int,
+                s) -> None:
+        qsl, seq, tab = self.qsl[:R + 1], self.seq[:R], self.gathered[:R]
+        # a block that was copied on write is written to in the same step, so the bounds of
+        # every block that a request reads are those of its keys
+        pa.update_block_bounds(self.pool, self.bounds, tab, seq, query_start_loc=qsl,
+                               num_tokens=T, stream=s)
+        pa.score_blocks(q[:T], self.bounds, self.scores[:T], qsl, seq, tab, self.pool, stream=s)
+        pa.select_blocks(self.scores[:T], self.selected[:T], qsl, seq, self.B, first=self.first,
+                         last=self.last, stream=s)
+        pa.sparse_forward(q[:T], out[:T], qsl, seq, tab, self.selected[:T], self.pool, self.scale,
+                          stream=s)
