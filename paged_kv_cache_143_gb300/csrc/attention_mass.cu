@@ -33,7 +33,7 @@
 #include <utility>
 
 #include "batch_rows.cuh"
-#include "decode_rows.cuh"
+#include "cells.cuh"
 #include "mbar_poll.cuh"
 
 namespace pa {
@@ -56,7 +56,6 @@ struct MassParams {
   const int32_t* qsl;
   const int32_t* seq_lens;
   const int32_t* tables;
-  const uint8_t* k_pool;
   int max_reqs, max_blocks, R, T, Hq, Hkv, g, B, num_blocks, window;
   float decay, qk_scale;   // softmax scale * log2(e) (* k_scale)
   // streaming form
@@ -118,6 +117,13 @@ __device__ __forceinline__ int mass_row(const MassParams& p, int r) {
   return at >= 0 && at < p.max_reqs ? at : -1;
 }
 
+// (ref, sum) joined with another part's maximum and sum.
+__device__ __forceinline__ void join_stats(float& ref, float& sum, float m, float l) {
+  const float top = fmaxf(ref, m), base = top == -INFINITY ? 0.f : top;
+  sum = sum * ex2_ftz(ref - base) + l * ex2_ftz(m - base);
+  ref = top;
+}
+
 // ------------------------------------------------------------ streaming form
 
 constexpr int kNarrowWarps = 4;
@@ -131,10 +137,8 @@ struct NarrowTail {
 template <int D, bool FP8, int NH>
 __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
     mass_scores_kernel(const __grid_constant__ CUtensorMap tmap_k, MassParams p) {
-  using MK = MmaKeys<D, FP8>;
-  using G = Geo<D, FP8>;
-  constexpr int KS = MK::KS;
-  constexpr int kStages = kNarrowRing / G::kChunkBytes > 8 ? 8 : kNarrowRing / G::kChunkBytes;
+  using C = Cells<D, FP8>;
+  constexpr int kStages = kNarrowRing / C::kBytes > 8 ? 8 : kNarrowRing / C::kBytes;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
   NarrowTail* tail = reinterpret_cast<NarrowTail*>(ring + kNarrowWarps * kNarrowRing);
@@ -184,40 +188,27 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
     const int id = __shfl_sync(kFull, id_lane, i & 31);
     if (lane == 0) {
       const int row = (k0 + (i * kNarrowWarps + warp) * kChunk) % p.B;
-      uint8_t* dst = my_ring + (i % kStages) * G::kChunkBytes;
-      mbar_arrive_expect_tx(&full[i % kStages], G::kChunkBytes);
-      if constexpr (MK::kSw)
-        tc::tma_load_3d(dst, &tmap_k, 0, kvh * p.B + row, id, &full[i % kStages]);
-      else
-        bulk_g2s(dst, p.k_pool + (((int64_t)id * p.Hkv + kvh) * p.B + row) * G::kRowBytes,
-                 G::kChunkBytes, &full[i % kStages]);
+      mbar_arrive_expect_tx(&full[i % kStages], C::kBytes);
+      C::load(my_ring + (i % kStages) * C::kBytes, &tmap_k, kvh * p.B + row, id,
+              &full[i % kStages]);
     }
   };
   for (int i = 0; i < min(mine, kStages); ++i) issue(i);
-  uint32_t qb[NH][KS][2];
-  float sc[NH][2], mx[NH][2], l[NH][2];
+  QueryCols<D, FP8, NH> q;
+  q.load([&](int c) -> const __nv_bfloat16* {
+    return c < m.rows ? p.q + ((int64_t)(m.q0 + m.q_len - m.w + c / p.g) * p.Hq + kvh * p.g + c % p.g) * D
+                      : nullptr;
+  }, p.qk_scale, grp, tig);
+  float mx[NH][2], l[NH][2];
   int lim[NH][2];  // keys that the query of column 2 tig + e sees
 #pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    const int c = 8 * h + grp;
-    const __nv_bfloat16* rows[2] = {nullptr, nullptr};
-    if (c < m.rows)
-      rows[0] = p.q + ((int64_t)(m.q0 + m.q_len - m.w + c / p.g) * p.Hq + kvh * p.g + c % p.g) * D;
-    MK one;
-    one.load_q(rows, p.qk_scale, tig);
-#pragma unroll
-    for (int j = 0; j < KS; ++j) {
-      qb[h][j][0] = one.qb[j][0];
-      qb[h][j][1] = one.qb[j][1];
-    }
+  for (int h = 0; h < NH; ++h)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      sc[h][e] = one.sc[e];
       mx[h][e] = -INFINITY;
       l[h][e] = 0.f;
       lim[h][e] = m.seq - m.w + (8 * h + 2 * tig + e) / p.g + 1;
     }
-  }
   for (int i = 0; i < mine; ++i) {
     const int stage = i % kStages;
     if (!__all_sync(kFull, mbar_wait(&full[stage], (i / kStages) & 1, p.err))) {
@@ -226,27 +217,8 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
           mbar_wait(&full[x % kStages], (x / kStages) & 1, p.err);
       break;  // flagged
     }
-    const uint8_t* Ks = my_ring + stage * G::kChunkBytes;
-    float acc[NH][2][4];
-#pragma unroll
-    for (int h = 0; h < NH; ++h)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) acc[h][c][0] = acc[h][c][1] = acc[h][c][2] = acc[h][c][3] = 0.f;
-    const uint8_t* r0 = Ks + grp * G::kRowBytes;
-    const uint8_t* r1 = Ks + (grp + 8) * G::kRowBytes;
-#pragma unroll
-    for (int q = 0; q < KS / 2; ++q) {
-      uint32_t w0[4], w1[4];
-      MK::k_words(r0, grp, q, tig, w0);
-      MK::k_words(r1, grp + 8, q, tig, w1);
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        MmaRows<D, FP8>::mma(acc[h][q & 1], w0[0], w1[0], w0[1], w1[1], qb[h][2 * q][0],
-                             qb[h][2 * q][1]);
-        MmaRows<D, FP8>::mma(acc[h][q & 1], w0[2], w1[2], w0[3], w1[3], qb[h][2 * q + 1][0],
-                             qb[h][2 * q + 1][1]);
-      }
-    }
+    float s[NH][4];
+    q.scores(my_ring + stage * C::kBytes, s, grp, tig);
     __syncwarp();
     if (i + kStages < mine) issue(i + kStages);
     const int key = k0 + (i * kNarrowWarps + warp) * kChunk + grp;
@@ -255,8 +227,8 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int c = 8 * h + 2 * tig + e;
-        float x0 = (acc[h][0][e] + acc[h][1][e]) * sc[h][e];
-        float x1 = (acc[h][0][2 + e] + acc[h][1][2 + e]) * sc[h][e];
+        float x0 = s[h][e] * q.sc[h][e];
+        float x1 = s[h][2 + e] * q.sc[h][e];
         if (key >= lim[h][e]) x0 = -INFINITY;
         if (key + 8 >= lim[h][e]) x1 = -INFINITY;
         if (c < m.rows) {
@@ -278,9 +250,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         const float m2 = __shfl_xor_sync(kFull, mx[h][e], o), l2 = __shfl_xor_sync(kFull, l[h][e], o);
-        const float ref = fmaxf(mx[h][e], m2), base = ref == -INFINITY ? 0.f : ref;
-        l[h][e] = l[h][e] * ex2_ftz(mx[h][e] - base) + l2 * ex2_ftz(m2 - base);
-        mx[h][e] = ref;
+        join_stats(mx[h][e], l[h][e], m2, l2);
       }
       if (grp == 0) tail->stats[warp][8 * h + 2 * tig + e] = make_float2(mx[h][e], l[h][e]);
     }
@@ -325,10 +295,17 @@ __global__ void __launch_bounds__(kSumThreads) mass_sum_kernel(MassParams p) {
   }
   grid_dependency_wait();  // the scores and their statistics are complete
   const int rows = p.Hkv * m.rows, n_split = (m.seq + kSplitKeys - 1) / kSplitKeys;
-  for (int x = threadIdx.x; x < rows; x += kSumThreads)
-    lse[x] = lse_of(p.split_stats +
-                        ((int64_t)(r * (int64_t)p.Hkv + x / m.rows) * kNarrowRows + x % m.rows) * p.splits,
-                    n_split, 1);
+  for (int x = threadIdx.x >> 5; x < rows; x += kSumThreads / 32) {  // a warp for each row
+    const float2* part = p.split_stats +
+        ((int64_t)(r * (int64_t)p.Hkv + x / m.rows) * kNarrowRows + x % m.rows) * p.splits;
+    const int lane = threadIdx.x & 31;
+    float ref = -INFINITY, sum = 0.f;
+    for (int i = lane; i < n_split; i += 32) join_stats(ref, sum, part[i].x, part[i].y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      join_stats(ref, sum, __shfl_xor_sync(kFull, ref, o), __shfl_xor_sync(kFull, sum, o));
+    if (lane == 0) lse[x] = ref + log2f(sum);  // NaN for a row that scores -inf throughout
+  }
   __syncthreads();
   const int key = key0 + (int)threadIdx.x;
   if (key >= m.seq) return;
@@ -338,7 +315,7 @@ __global__ void __launch_bounds__(kSumThreads) mass_sum_kernel(MassParams p) {
   const int j0 = max(0, key - (m.seq - m.w));  // the first counted query that sees the key
   for (int h = 0; h < p.Hkv; ++h) {
     const int c0 = j0 * p.g;
-#pragma unroll 8
+#pragma unroll 16
     for (int c = c0; c < m.rows; ++c)
       sum += ex2_ftz(s[(int64_t)(h * m.rows + c) * stride] - lse[h * m.rows + c]);
   }
@@ -661,11 +638,13 @@ __global__ void __launch_bounds__(kWideThreads, 2)
       if (!WEIGHTS) {
         const int k0 = key0 + i * kTile;
         const bool whole = k0 + kTile <= sees;
+        uint32_t buf[2][32];
+        tc::tmem_ld32(s, buf[0]);
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) {
-          uint32_t v[32];
-          tc::tmem_ld32(s + c, v);
+          uint32_t(&v)[32] = buf[c / 32 & 1];
           tc::tmem_wait_ld();
+          if (c + 32 < kTile) tc::tmem_ld32(s + c + 32, buf[(c / 32 + 1) & 1]);
           float x[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -693,11 +672,13 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         // the tile's first row that sees the key (0: all do)
         const int64_t from = (int64_t)max(0, key - (m.seq - m.w)) * p.g - row0;
         float a[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t buf[2][32];
+        tc::tmem_ld32(s, buf[0]);
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) {
-          uint32_t v[32];
-          tc::tmem_ld32(s + c, v);
+          uint32_t(&v)[32] = buf[c / 32 & 1];
           tc::tmem_wait_ld();
+          if (c + 32 < kTile) tc::tmem_ld32(s + c + 32, buf[(c / 32 + 1) & 1]);
           if (__all_sync(kFull, from <= c && c + 32 <= rows)) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -897,7 +878,7 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
   CUtensorMap tmap{};
   pa_status st = PA_OK;
   if (pl.narrow) {
-    if (F8 && D == 128 && !key_map(&tmap, pool, kChunk)) return PA_ERR_CUDA;
+    if (!cell_map<D, F8>(&tmap, pool->k_pool, pool->num_blocks, p.Hkv * p.B)) return PA_ERR_CUDA;
     const dim3 grid((unsigned)pl.splits, (unsigned)p.Hkv, (unsigned)p.R);
     st = launch_after(pl.max_narrow_rows <= 8 ? mass_scores_kernel<D, F8, 1> : mass_scores_kernel<D, F8, 2>,
                       grid, kNarrowWarps * 32, narrow_smem, s, false, 1, tmap, p);
@@ -980,7 +961,6 @@ extern "C" pa_status pa_attention_mass(
   p.qsl = query_start_loc;
   p.seq_lens = seq_lens;
   p.tables = block_tables;
-  p.k_pool = static_cast<const uint8_t*>(pool->k_pool);
   p.max_reqs = max_reqs;
   p.max_blocks = max_blocks;
   p.R = num_reqs;

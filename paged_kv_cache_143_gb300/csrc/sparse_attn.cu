@@ -11,17 +11,17 @@
 //    no warp waits for another until the end. The list is read 32 entries at a
 //    time, one a lane, and turned into the cells that hold visible keys.
 //  - S^T = K Q^T and O^T += V^T P^T are warp-level m16n8k16 MMAs with the 16 keys
-//    of a cell as rows and the heads as columns (as the decode kernel's MmaKeys;
-//    g heads are far below the smallest tcgen05 tile), the running maximum and
-//    sum of the softmax per head in registers, in fp32; the weights are rounded
-//    to 16 bits for the second product.
+//    of a cell as rows and the heads as columns (cells.cuh; g heads are far below
+//    the smallest tcgen05 tile), the running maximum and sum of the softmax per
+//    head in registers, in fp32; the weights are rounded to 16 bits for the second
+//    product.
 //  - The warps join by log-sum-exp in shared memory. Where there are too few
 //    (token, kv head) pairs for the GPU, a cluster of 2, 4 or 8 CTAs shares each
 //    list and joins through distributed shared memory: no workspace, one launch.
 #include <cooperative_groups.h>
 
 #include "batch_rows.cuh"
-#include "decode_rows.cuh"
+#include "cells.cuh"
 
 namespace pa {
 namespace {
@@ -46,35 +46,21 @@ struct SparseParams {
   unsigned* err;
 };
 
-// One warp's heads (NH groups of eight) against 16-key cells: MmaKeys with NH
-// column tiles, K and V fragments loaded once for all, and a softmax whose
-// reference may stay at -inf (a cell that scores -inf throughout weighs 0).
+// One warp's heads (NH groups of eight) against 16-key cells: the softmax's running
+// maxima and sums and the unnormalised output in registers. The reference of a row
+// moves only when its maximum grows by more than 2^8 (MmaRows::rebase), and may stay
+// at -inf: a cell that scores -inf throughout weighs 0.
 template <int D, bool FP8, int NH>
 struct CellHeads {
-  using MK = MmaKeys<D, FP8>;
-  using G = Geo<D, FP8>;
-  static constexpr int KS = MK::KS, DG = MK::DG, MT = MK::MT;
-  static constexpr bool kSw = MK::kSw;
-  uint32_t qb[NH][KS][2];
-  float sc[NH][2];
-  float o[NH][MT][4];
+  using C = Cells<D, FP8>;
+  static constexpr int MT = C::MT;
+  QueryCols<D, FP8, NH> q;
+  float o[NH][MT][4];  // [mt]: (dim d, column 2 tig), (d, 2 tig + 1), (d + 1, ..), d = value_dim(mt, grp)
   float m[NH][2], l[NH][2];
 
-  __device__ __forceinline__ void load_q(const __nv_bfloat16* q, int heads, float q_scale, int grp,
-                                         int tig) {
+  __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      MK one;
-      const __nv_bfloat16* rows[2] = {8 * h + grp < heads ? q + (int64_t)(8 * h + grp) * D : nullptr,
-                                      nullptr};
-      one.load_q(rows, q_scale, tig);
-#pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        qb[h][j][0] = one.qb[j][0];
-        qb[h][j][1] = one.qb[j][1];
-      }
-      sc[h][0] = one.sc[0];
-      sc[h][1] = one.sc[1];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) o[h][mt][0] = o[h][mt][1] = o[h][mt][2] = o[h][mt][3] = 0.f;
       m[h][0] = m[h][1] = -INFINITY;
@@ -86,32 +72,7 @@ struct CellHeads {
   __device__ __forceinline__ void cell(const uint8_t* Ks, const uint8_t* Vs, int n, int grp,
                                        int tig) {
     float s[NH][4];
-    {
-      float acc[NH][2][4];
-#pragma unroll
-      for (int h = 0; h < NH; ++h)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) acc[h][c][0] = acc[h][c][1] = acc[h][c][2] = acc[h][c][3] = 0.f;
-      const uint8_t* r0 = Ks + grp * G::kRowBytes;
-      const uint8_t* r1 = Ks + (grp + 8) * G::kRowBytes;
-#pragma unroll
-      for (int q = 0; q < KS / 2; ++q) {
-        uint32_t w0[4], w1[4];
-        MK::k_words(r0, grp, q, tig, w0);
-        MK::k_words(r1, grp + 8, q, tig, w1);
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          MmaRows<D, FP8>::mma(acc[h][q & 1], w0[0], w1[0], w0[1], w1[1], qb[h][2 * q][0],
-                               qb[h][2 * q][1]);
-          MmaRows<D, FP8>::mma(acc[h][q & 1], w0[2], w1[2], w0[3], w1[3], qb[h][2 * q + 1][0],
-                               qb[h][2 * q + 1][1]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < NH; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[h][i] = acc[h][0][i] + acc[h][1][i];
-    }
+    q.scores(Ks, s, grp, tig);
     const bool whole = n >= 16;
     uint32_t pb[NH][2];
     bool rescale = false;
@@ -122,8 +83,8 @@ struct CellHeads {
       for (int e = 0; e < 2; ++e) {
         float& x0 = s[h][e];
         float& x1 = s[h][2 + e];
-        x0 = whole || grp < n ? x0 * sc[h][e] : -INFINITY;
-        x1 = whole || grp + 8 < n ? x1 * sc[h][e] : -INFINITY;
+        x0 = whole || grp < n ? x0 * q.sc[h][e] : -INFINITY;
+        x1 = whole || grp + 8 < n ? x1 * q.sc[h][e] : -INFINITY;
         float mx = fmaxf(x0, x1);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -146,8 +107,8 @@ struct CellHeads {
         pb[h][0] = *reinterpret_cast<uint32_t*>(&a);
         pb[h][1] = *reinterpret_cast<uint32_t*>(&b);
       }
-      MK::movtrans(pb[h][0]);
-      MK::movtrans(pb[h][1]);
+      MmaKeys<D, FP8>::movtrans(pb[h][0]);
+      MmaKeys<D, FP8>::movtrans(pb[h][1]);
     }
     if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
@@ -160,29 +121,14 @@ struct CellHeads {
           o[h][mt][3] *= alpha[h][1];
         }
     }
-    // V rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9 over dims DG grp .. DG grp + DG - 1
-    uint32_t vw[4][DG / 2];
+    uint32_t vw[4][C::kWords];  // rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int kr = 2 * tig + (i & 1) + 8 * (i >> 1);
-      if constexpr (kSw) {
-        const uint4 x =
-            *reinterpret_cast<const uint4*>(Vs + kr * G::kRowBytes + ((grp ^ (kr & 7)) << 4));
-        MmaRows<D, FP8>::widen8(x.x, x.y, &vw[i][0]);
-        MmaRows<D, FP8>::widen8(x.z, x.w, &vw[i][4]);
-      } else {
-        const uint8_t* vrow = Vs + kr * G::kRowBytes + DG * grp * G::kElt;
-#pragma unroll
-        for (int h = 0; h < DG / 8; ++h) {
-          uint32_t w4[4];
-          MmaRows<D, FP8>::load8(vrow + 8 * h * G::kElt, w4);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) vw[i][4 * h + w] = w4[w];
-        }
-      }
+      C::value_words(Vs, kr, grp, vw[i]);
       if (!whole && kr >= n)  // a hidden cell may hold NaN, which a weight of 0 must not meet
 #pragma unroll
-        for (int w = 0; w < DG / 2; ++w) vw[i][w] = 0u;
+        for (int w = 0; w < C::kWords; ++w) vw[i][w] = 0u;
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -214,21 +160,20 @@ struct CellHeads {
           cl[row] = sum;
         }
 #pragma unroll
-        for (int i = 0; i < DG / 4; ++i)
-          *reinterpret_cast<float4*>(comb + row * D + DG * grp + 4 * i) =
-              make_float4(o[h][2 * i][e], o[h][2 * i][2 + e], o[h][2 * i + 1][e],
-                          o[h][2 * i + 1][2 + e]);
+        for (int w = 0; w < MT; w += 2)
+          *reinterpret_cast<float4*>(comb + row * D + C::value_dim(w, grp)) =
+              make_float4(o[h][w][e], o[h][w][2 + e], o[h][w + 1][e], o[h][w + 1][2 + e]);
       }
   }
 };
 
 template <int D, bool FP8>
 struct SparseGeo {
-  using G = Geo<D, FP8>;
-  // cells of a warp's ring: 24 KB a warp, 96 KB a CTA, two CTAs on an SM
-  static constexpr int kStages = 24576 / G::kStageBytes > 8 ? 8 : 24576 / G::kStageBytes;
-  static constexpr int kWarpBytes = 24576;  // ring, later the warp's part of the join
-  static_assert(kStages * G::kStageBytes <= kWarpBytes, "ring");
+  static constexpr int kCell = 2 * Cells<D, FP8>::kBytes;  // keys, then values
+  // cells of a warp's ring: 16 KB a warp, 64 KB a CTA, three CTAs on an SM
+  static constexpr int kWarpBytes = 16384;  // ring, later the warp's part of the join
+  static constexpr int kStages = kWarpBytes / kCell > 8 ? 8 : kWarpBytes / kCell;
+  static_assert(kStages >= 2, "ring");
   static_assert((16 * D + 32) * 4 <= kWarpBytes, "join");
 };
 
@@ -241,12 +186,12 @@ struct SparseTail {
 };
 
 template <int D, bool FP8, int NH>
-__global__ void __launch_bounds__(kSparseThreads, 2)
+__global__ void __launch_bounds__(kSparseThreads, NH == 1 ? 3 : 2)
     sparse_attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, SparseParams p) {
   using CH = CellHeads<D, FP8, NH>;
   using SG = SparseGeo<D, FP8>;
-  using G = Geo<D, FP8>;
+  using C = Cells<D, FP8>;
   constexpr int kStages = SG::kStages;
   constexpr int kRows = 8 * NH;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -274,14 +219,15 @@ __global__ void __launch_bounds__(kSparseThreads, 2)
   }
   __syncwarp();
   CH st;
-  st.load_q(p.q + ((int64_t)t * p.Hq + hq0) * D, heads, p.q_scale, grp, tig);
+  st.q.load([&](int c) { return c < heads ? p.q + ((int64_t)t * p.Hq + hq0 + c) * D : nullptr; },
+            p.q_scale, grp, tig);
+  st.reset();
 
   uint8_t* my_ring = ring + warp * SG::kWarpBytes;
   uint64_t* full = tail->full[warp];
   uint2* cells = tail->cells[warp];
   const int32_t* list = p.selected + ((int64_t)t * p.Hkv + kvh) * p.k;
   const int32_t* table = p.tables + (int64_t)r * p.max_blocks;
-  const int64_t head_bytes = (int64_t)p.B * G::kRowBytes;
   const int lanes_of = kSparseWarps * p.split;  // warps that share the list
   const int first = rank * kSparseWarps + warp;
   uint32_t pos = 0;  // cells gone through: stage pos mod kStages, phase pos / kStages
@@ -289,18 +235,11 @@ __global__ void __launch_bounds__(kSparseThreads, 2)
   int seen = 0;
   auto issue = [&](uint32_t at, uint2 c) {  // one lane
     const uint32_t stage = at % kStages;
-    uint8_t* dst = my_ring + stage * G::kStageBytes;
-    mbar_arrive_expect_tx(&full[stage], G::kStageBytes);
-    const int row = (int)(c.y & 0xffu);
-    if constexpr (CH::kSw) {
-      tc::tma_load_3d(dst, &tmap_k, 0, kvh * p.B + row, (int)c.x, &full[stage]);
-      tc::tma_load_3d(dst + G::kChunkBytes, &tmap_v, 0, kvh * p.B + row, (int)c.x, &full[stage]);
-    } else {
-      const int64_t off =
-          ((int64_t)(int)c.x * p.Hkv + kvh) * head_bytes + (int64_t)row * G::kRowBytes;
-      bulk_g2s(dst, p.k_pool + off, G::kChunkBytes, &full[stage]);
-      bulk_g2s(dst + G::kChunkBytes, p.v_pool + off, G::kChunkBytes, &full[stage]);
-    }
+    uint8_t* dst = my_ring + stage * SG::kCell;
+    mbar_arrive_expect_tx(&full[stage], SG::kCell);
+    const int line = kvh * p.B + (int)(c.y & 0xffu);
+    C::load(dst, &tmap_k, line, (int)c.x, &full[stage]);
+    C::load(dst + C::kBytes, &tmap_v, line, (int)c.x, &full[stage]);
   };
   for (int64_t base = 0; base < p.k && ok; base += 32 * lanes_of) {
     const int64_t e = base + (int64_t)lane * lanes_of + first;
@@ -344,8 +283,8 @@ __global__ void __launch_bounds__(kSparseThreads, 2)
         __syncwarp();
         break;
       }
-      const uint8_t* Ks = my_ring + stage * G::kStageBytes;
-      st.cell(Ks, Ks + G::kChunkBytes, (int)(cells[c].y >> 8), grp, tig);
+      const uint8_t* Ks = my_ring + stage * SG::kCell;
+      st.cell(Ks, Ks + C::kBytes, (int)(cells[c].y >> 8), grp, tig);
       __syncwarp();
       if (lane == 0 && c + kStages < total) issue(at + kStages, cells[c + kStages]);
     }
@@ -444,14 +383,10 @@ pa_status launch_sparse(const SparseParams& p, int64_t ctas, cudaStream_t s) {
                                     (int)smem) == cudaSuccess;
       }))
     return PA_ERR_CUDA;
-  DecodeParams maps{};
-  maps.k_pool = p.k_pool;
-  maps.v_pool = p.v_pool;
-  maps.Hkv = p.Hkv;
-  maps.B = p.B;
-  maps.num_blocks = p.num_blocks;
   CUtensorMap tk, tv;
-  if (decode_maps<D, FP8>(maps, &tk, &tv) != cudaSuccess) return PA_ERR_CUDA;
+  if (!cell_map<D, FP8>(&tk, p.k_pool, p.num_blocks, p.Hkv * p.B) ||
+      !cell_map<D, FP8>(&tv, p.v_pool, p.num_blocks, p.Hkv * p.B))
+    return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kSparseThreads);
@@ -512,10 +447,16 @@ extern "C" pa_status pa_sparse_forward(const void* q, void* out, const int32_t* 
   p.v_scale = fp8 ? pool->v_scale : 1.f;
   p.err = error_word();
   if (!p.err) return PA_ERR_CUDA;
-  // CTAs share a list while two of them do not fill each SM and a warp keeps two blocks
+  // A cluster shares a list where that many CTAs still run at once (three on an SM, two
+  // for more than 8 heads), and two CTAs where the lists are one to two times as many as
+  // run at once and a second round would be short; each warp keeps two blocks. Lists of
+  // 128 blocks of 16 keys (bf16, 8 kv heads): 8 decodes 31 us alone, 23 by 2 or 4, 31 by 8;
+  // 24: 45, 43, 47, 61; 64: 119, 109, 111, 141; 300 tokens of a chunk (64 blocks): 164, 201.
   const int64_t units = (int64_t)num_tokens * p.Hkv * p.parts;
+  const int64_t at_once = (int64_t)(wide ? 2 : 3) * num_sms();
   p.split = 1;
-  while (p.split < 8 && units * p.split < 2 * num_sms() && k >= p.split * 2 * kSparseWarps * 2)
+  while (p.split < 8 && k >= 4 * kSparseWarps * p.split &&
+         (units * 2 * p.split <= at_once || (p.split == 1 && units > at_once && units < 2 * at_once)))
     p.split *= 2;
   if (units * p.split > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   const int64_t ctas = units * p.split;
