@@ -45,7 +45,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNarrowRows = 16;     // rows of the streaming form, at the most
 constexpr int kSplitKeys = 1024;    // keys of one of its CTAs
 constexpr int kTile = 128;          // rows, and keys, of a tcgen05 tile
-constexpr int kInfoBytes = 1024;    // behind an image: (score factor, lse) of its rows
+constexpr int kInfoBytes = 1024;    // behind an image: what its rows' scores are turned with
+// Of rows 2 i and 2 i + 1 four floats, (factor, factor, -lse, -lse), so that one load
+// feeds one packed multiply-add: the row's factor is at info_at(row), -lse 2 further.
+__device__ __forceinline__ int info_at(int row) { return (row >> 1) * 4 + (row & 1); }
 
 struct MassParams {
   const __nv_bfloat16* q;
@@ -312,12 +315,13 @@ __global__ void __launch_bounds__(kSumThreads) mass_sum_kernel(MassParams p) {
   const int stride = padded_keys(m.seq);
   const float* s = p.scores + at + key;
   float sum = 0.f;
-  const int j0 = max(0, key - (m.seq - m.w));  // the first counted query that sees the key
-  for (int h = 0; h < p.Hkv; ++h) {
-    const int c0 = j0 * p.g;
+  if (key <= m.seq - m.w) {  // seen by all counted queries
 #pragma unroll 16
-    for (int c = c0; c < m.rows; ++c)
-      sum += ex2_ftz(s[(int64_t)(h * m.rows + c) * stride] - lse[h * m.rows + c]);
+    for (int x = 0; x < rows; ++x) sum += ex2_ftz(s[(int64_t)x * stride] - lse[x]);
+  } else {
+    const int c0 = (key - (m.seq - m.w)) * p.g;  // the first row that sees the key
+    for (int x = 0; x < rows; ++x)
+      if (x % m.rows >= c0) sum += ex2_ftz(s[(int64_t)x * stride] - lse[x]);
   }
   const int64_t o = (int64_t)slot * p.mass_stride + key;
   p.mass_out[o] = (key < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + sum;
@@ -374,7 +378,13 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
       p.q + ((int64_t)(m.q0 + m.q_len - m.w + c / p.g) * p.Hq + kvh * p.g + c % p.g) * D);
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) v[i] = c < m.rows ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-  float sc = p.qk_scale;
+  float sc = fabsf(p.qk_scale);  // its sign goes to the query: greater products are greater scores
+  if (p.qk_scale < 0.f) {
+    constexpr uint32_t kSigns = 0x80008000u;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      v[i] = make_uint4(v[i].x ^ kSigns, v[i].y ^ kSigns, v[i].z ^ kSigns, v[i].w ^ kSigns);
+  }
   if constexpr (!F8) {
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -423,20 +433,47 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
       *reinterpret_cast<uint4*>(image + kTile * D + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
-  reinterpret_cast<float2*>(image + W::kTileBytes)[tid] = make_float2(sc, 0.f);
+  reinterpret_cast<float*>(image + W::kTileBytes)[info_at(tid)] = sc;
 }
 
 struct WideTail {
-  uint64_t fixed_full, fixed_empty;
-  uint64_t full[2], empty[2];      // stages of the streamed operand
+  uint64_t fixed_full[2], fixed_empty[2];
+  uint64_t full[4], empty[4];      // stages of the streamed operand
+  uint64_t info_full[8];           // WEIGHTS: what is behind a step's image
   uint64_t s_full[2], s_empty[2];  // accumulators
   uint32_t tmem;
   int abort;
-  float part[kTile];               // a CTA's sums, for its cluster
+  float2 part[kTile];              // a warpgroup's results, for the other one and the cluster
 };
 
-constexpr int kWideThreads = 192;  // warps 0-3: rows or keys; 4: copies; 5: MMAs
+// Warps 0-3 and 4-7: rows or keys, each group of four the accumulators of one stage
+// (every other step); 8: copies; 9: MMAs.
+constexpr int kWideThreads = 320;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
 constexpr uint32_t kWideCols = 2 * kTile;
+
+// Shared memory of a CTA, two of which run on an SM: the tile that stays (WEIGHTS: two
+// slots, the next kv head's keys arrive while this one's are multiplied), as many stages
+// of the stream as there is room for (a stage is free again as soon as its MMAs are
+// done), and a ring of eight steps' row factors. Two slots of 128 bf16 keys of 128 dims
+// leave room for 64 query rows a stage.
+template <int D, bool F8, bool WEIGHTS>
+struct WideSmem {
+  using W = WideGeo<D, F8>;
+  static constexpr int kRows = WEIGHTS && !F8 && D == 128 ? 64 : kTile;  // columns of a step
+  static constexpr int kKeys = kTile * D * (F8 ? 1 : 2);
+  static constexpr int kSlots = WEIGHTS ? 2 : 1;
+  static constexpr int kFixed = WEIGHTS ? kKeys : W::kImage;
+  static constexpr int kStage = WEIGHTS ? kRows * D * 2 : kKeys;
+  static constexpr int kRoom = (108 << 10) - kSlots * kFixed - 8 * kInfoBytes;
+  static constexpr int kStages = kRoom / kStage > 4 ? 4 : kRoom / kStage;
+  static constexpr int kOffStream = kSlots * kFixed;
+  static constexpr int kOffInfo = kOffStream + kStages * kStage;
+  static constexpr int kOffTail = kOffInfo + 8 * kInfoBytes;
+  static constexpr size_t kAlloc = 1024 + kOffTail + sizeof(WideTail);
+  static_assert(kStages >= 2 && kFixed % 1024 == 0 && kStage % 1024 == 0,
+                "swizzled tiles start on 1024-byte boundaries");
+};
 
 // A swizzled K-major operand tile of rows of SPAN bytes.
 template <int SPAN>
@@ -455,12 +492,13 @@ template <int D, bool F8, bool WEIGHTS>
 __global__ void __launch_bounds__(kWideThreads, 2)
     mass_tile_kernel(const __grid_constant__ CUtensorMap tmap_k, MassParams p) {
   using W = WideGeo<D, F8>;
-  constexpr int kSlot = W::kImage;  // of the tile that stays and of each stage
-  static_assert(kSlot % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+  using S = WideSmem<D, F8, WEIGHTS>;
+  constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* fixed = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* stream = fixed + kSlot;
-  WideTail* t = reinterpret_cast<WideTail*>(stream + 2 * kSlot);
+  uint8_t* stream = fixed + S::kOffStream;
+  uint8_t* infos = fixed + S::kOffInfo;
+  WideTail* t = reinterpret_cast<WideTail*>(fixed + S::kOffTail);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   launch_dependents();
@@ -492,26 +530,31 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     key0 = blockIdx.x * kTile;
     if (key0 >= m.seq) return;
     // row tiles whose last query comes before the tile's first key add nothing
-    ti0 = (int)((int64_t)max(0, key0 - (m.seq - m.w)) * p.g / kTile);
-    n_tiles = (m.rows + kTile - 1) / kTile - ti0;
+    ti0 = (int)((int64_t)max(0, key0 - (m.seq - m.w)) * p.g / S::kRows);
+    n_tiles = (m.rows + S::kRows - 1) / S::kRows - ti0;
     kvh0 = blockIdx.z;
     kvh_step = gridDim.z;
     n_steps = kvh0 < p.Hkv ? ((p.Hkv - kvh0 + kvh_step - 1) / kvh_step) * n_tiles : 0;
   }
 
   if (tid == 0) {
-    mbar_init(&t->fixed_full, 1);
-    mbar_init(&t->fixed_empty, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&t->fixed_full[i], 1);
+      mbar_init(&t->fixed_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&t->full[i], 1);
-      mbar_init(&t->empty[i], 5);  // the MMAs, and the four warps that read what is behind the tile
+      mbar_init(&t->empty[i], 1);
+    }
+    for (int i = 0; i < 8; ++i) mbar_init(&t->info_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&t->s_full[i], 1);
       mbar_init(&t->s_empty[i], 4);
     }
     t->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tc::tmem_alloc(&t->tmem, kWideCols);
     tc::tmem_relinquish();
   }
@@ -526,7 +569,7 @@ __global__ void __launch_bounds__(kWideThreads, 2)
   };
   float total = 0.f, low = 0.f, ref = -INFINITY;  // (WEIGHTS: the sum and what its roundings lost)
 
-  if (warp == 4) {
+  if (warp == kCopyWarp) {
     // ------------------------------------------------------------- copies
     constexpr int kCols = F8 ? 1 : D / 64;  // boxes across a key row
     const int32_t* table = p.tables + (int64_t)r * p.max_blocks;
@@ -548,55 +591,81 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         tc::tma_load_3d(dst + col * W::kHalf + blk * p.B * kBoxRow, &tmap_k, col * 64,
                         kvh * p.B, id, bar);
     };
-    auto load_rows = [&](uint8_t* dst, int tile, int kvh, uint64_t* bar) {
+    auto image_of = [&](int tile, int kvh) {
+      return p.images + ((int64_t)tile * p.Hkv + kvh) * W::kImage;
+    };
+    auto copy = [&](void* dst, const uint8_t* src, unsigned bytes, uint64_t* bar) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar, W::kImage);
-        bulk_g2s(dst, p.images + ((int64_t)tile * p.Hkv + kvh) * W::kImage, W::kImage, bar);
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_g2s(dst, src, bytes, bar);
       }
     };
     int i = 0, fixed_loads = 0;
     bool ok = true;
     for (; i < n_steps && ok; ++i) {
-      const int st = i & 1;
+      const int st = i % kStages;
       if (WEIGHTS ? i % n_tiles == 0 : i == 0) {
-        if (fixed_loads > 0) ok = __all_sync(kFull, wait(&t->fixed_empty, (fixed_loads - 1) & 1));
+        const int slot = fixed_loads & 1;
+        if (fixed_loads > 1) ok = __all_sync(kFull, wait(&t->fixed_empty[slot], (fixed_loads / 2 - 1) & 1));
         if (!ok) break;
         if (WEIGHTS)
-          load_keys(fixed, key0, kvh0 + i / n_tiles * kvh_step, &t->fixed_full);
+          load_keys(fixed + slot * S::kFixed, key0, kvh0 + i / n_tiles * kvh_step, &t->fixed_full[slot]);
         else
-          load_rows(fixed, tile0, kvh0, &t->fixed_full);
+          copy(fixed, image_of(tile0, kvh0), W::kImage, &t->fixed_full[0]);
         ++fixed_loads;
       }
-      if (i >= 2) ok = __all_sync(kFull, wait(&t->empty[st], ((i >> 1) - 1) & 1));
+      if (i >= kStages) ok = __all_sync(kFull, wait(&t->empty[st], (i / kStages - 1) & 1));
       if (!ok) break;
-      uint8_t* dst = stream + st * kSlot;
-      if (WEIGHTS)
-        load_rows(dst, tile0 + ti0 + i % n_tiles, kvh0 + i / n_tiles * kvh_step, &t->full[st]);
-      else
+      uint8_t* dst = stream + st * S::kStage;
+      if (WEIGHTS) {
+        constexpr int kParts = kTile / S::kRows;  // steps of an image
+        const int ti = ti0 + i % n_tiles;
+        const uint8_t* image = image_of(tile0 + ti / kParts, kvh0 + i / n_tiles * kvh_step);
+        if constexpr (kParts == 1) {
+          copy(dst, image, W::kTileBytes, &t->full[st]);
+        } else if (lane == 0) {  // its rows of both halves
+          constexpr int kPiece = S::kRows * 128;
+          mbar_arrive_expect_tx(&t->full[st], 2 * kPiece);
+          for (int h = 0; h < 2; ++h)
+            bulk_g2s(dst + h * kPiece, image + h * W::kHalf + ti % kParts * kPiece, kPiece, &t->full[st]);
+        }
+        // Slot i mod 8 has been read: the stage is free since step i - kStages' MMAs are done,
+        // and those waited until step i - kStages - 2, of the same accumulator, had been read.
+        static_assert(kStages + 2 <= 8, "the ring of row factors");
+        copy(infos + (i & 7) * kInfoBytes, image + W::kTileBytes + ti % kParts * S::kRows * 8,
+             S::kRows * 8, &t->info_full[i & 7]);
+      } else {
         load_keys(dst, key0 + i * kTile, kvh0, &t->full[st]);
+      }
     }
     if (!ok) {  // what is in flight lands before the CTA ends
-      if (fixed_loads > 0) mbar_wait(&t->fixed_full, (fixed_loads - 1) & 1, nullptr);
-      for (int x = max(0, i - 2); x < i; ++x) mbar_wait(&t->full[x & 1], (x >> 1) & 1, nullptr);
+      for (int x = max(0, fixed_loads - 2); x < fixed_loads; ++x)
+        mbar_wait(&t->fixed_full[x & 1], (x / 2) & 1, nullptr);
+      for (int x = max(0, i - kStages); x < i; ++x)
+        mbar_wait(&t->full[x % kStages], (x / kStages) & 1, nullptr);
+      if (WEIGHTS)
+        for (int x = max(0, i - 8); x < i; ++x) mbar_wait(&t->info_full[x & 7], (x >> 3) & 1, nullptr);
     }
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     // --------------------------------------------------------------- MMAs
     if (tc::elect_one()) {
       constexpr uint32_t idesc =
-          F8 ? tc::idesc_e4m3_f32(kTile, kTile) : tc::idesc_16bit_f32(kTile, kTile, false, false, false);
-      const uint64_t a0 = operand_desc<W::kRowSpan>(fixed);
+          F8 ? tc::idesc_e4m3_f32(kTile, S::kRows)
+             : tc::idesc_16bit_f32(kTile, S::kRows, false, false, false);
       int heads = 0;
       for (int i = 0; i < n_steps; ++i) {
-        const int st = i & 1;
+        const int st = i % kStages, buf = i & 1;
         if (WEIGHTS ? i % n_tiles == 0 : i == 0) {
-          if (!wait(&t->fixed_full, heads & 1)) break;
+          if (!wait(&t->fixed_full[heads & 1], (heads / 2) & 1)) break;
           ++heads;
         }
-        if (!wait(&t->full[st], (i >> 1) & 1)) break;
-        if (i >= 2 && !wait(&t->s_empty[st], ((i >> 1) - 1) & 1)) break;
+        const int slot = (heads - 1) & 1;
+        if (!wait(&t->full[st], (i / kStages) & 1)) break;
+        if (i >= 2 && !wait(&t->s_empty[buf], ((i >> 1) - 1) & 1)) break;
         tc::fence_after_sync();
-        const uint64_t b0 = operand_desc<W::kRowSpan>(stream + st * kSlot);
-        const uint32_t d = tmem + st * kTile;
+        const uint64_t a0 = operand_desc<W::kRowSpan>(fixed + slot * S::kFixed);
+        const uint64_t b0 = operand_desc<W::kRowSpan>(stream + st * S::kStage);
+        const uint32_t d = tmem + buf * kTile;
         if constexpr (F8) {
 #pragma unroll
           for (int part = 0; part < 2; ++part)
@@ -609,130 +678,154 @@ __global__ void __launch_bounds__(kWideThreads, 2)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             tc::mma_bf16_ss(d, tc::desc_at(a0, (k >> 2) * W::kHalf + (k & 3) * 32),
-                            tc::desc_at(b0, (k >> 2) * W::kHalf + (k & 3) * 32), idesc, k > 0);
+                            tc::desc_at(b0, (k >> 2) * (WEIGHTS ? S::kRows * 128 : W::kHalf) + (k & 3) * 32), idesc,
+                            k > 0);
         }
         tc::mma_commit(&t->empty[st]);
-        tc::mma_commit(&t->s_full[st]);
-        if (WEIGHTS && (i + 1) % n_tiles == 0) tc::mma_commit(&t->fixed_empty);
+        tc::mma_commit(&t->s_full[buf]);
+        if (WEIGHTS && (i + 1) % n_tiles == 0) tc::mma_commit(&t->fixed_empty[slot]);
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------ rows, or keys
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const int me = tid & (kTile - 1);  // the thread's row, or key, of the tile
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     float sc = 0.f;
     int sees = 0;  // !WEIGHTS: keys that the thread's row sees
     if (!WEIGHTS && n_steps > 0) {
-      if (wait(&t->fixed_full, 0))
-        sc = reinterpret_cast<const float2*>(fixed + W::kTileBytes)[tid].x;
-      sees = m.seq - m.w + min(ti0 * kTile + tid, m.rows - 1) / p.g + 1;
+      if (wait(&t->fixed_full[0], 0))
+        sc = reinterpret_cast<const float*>(fixed + W::kTileBytes)[info_at(me)];
+      sees = m.seq - m.w + min(ti0 * kTile + me, m.rows - 1) / p.g + 1;
     }
-    const int key = key0 + tid;  // WEIGHTS
-    for (int i = 0; i < n_steps; ++i) {
-      const int st = i & 1;
-      // (the stage's own barrier too: what the copy brought is read here)
-      if (!__all_sync(kFull, wait(&t->full[st], (i >> 1) & 1) && wait(&t->s_full[st], (i >> 1) & 1)))
+    const int key = key0 + me;  // WEIGHTS
+    const int buf = warp >> 2;
+    for (int i = buf; i < n_steps; i += 2) {
+      if (!__all_sync(kFull, (!WEIGHTS || wait(&t->info_full[i & 7], (i >> 3) & 1)) &&
+                                 wait(&t->s_full[buf], (i >> 1) & 1)))
         break;
       tc::fence_after_sync();
-      const uint32_t s = tmem + lane_base + st * kTile;
+      const uint32_t s = tmem + lane_base + buf * kTile;
       if (!WEIGHTS) {
         const int k0 = key0 + i * kTile;
-        const bool whole = k0 + kTile <= sees;
-        uint32_t buf[2][32];
-        tc::tmem_ld32(s, buf[0]);
+        const bool whole = __all_sync(kFull, k0 + kTile <= sees);
+        const uint64_t sc2 = f2_pack(sc, sc);
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) {
-          uint32_t(&v)[32] = buf[c / 32 & 1];
+          uint32_t v[32];
+          tc::tmem_ld32(s + c, v);
           tc::tmem_wait_ld();
-          if (c + 32 < kTile) tc::tmem_ld32(s + c + 32, buf[(c / 32 + 1) & 1]);
-          float x[32];
+          if (!whole)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            x[e] = __uint_as_float(v[e]) * sc;
-            if (!whole && k0 + c + e >= sees) x[e] = -INFINITY;
-          }
-          float mx = x[0];
+            for (int e = 0; e < 32; ++e)
+              if (k0 + c + e >= sees) v[e] = 0xff800000u;  // -inf
+          float mx = __uint_as_float(v[0]);
 #pragma unroll
-          for (int e = 1; e < 31; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
-          mx = fmaxf(mx, x[31]);
+          for (int e = 1; e < 31; e += 2)
+            mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          mx = fmaxf(mx, __uint_as_float(v[31])) * sc;  // sc is not negative
           if (mx > ref) {
             total *= ex2_ftz(ref - mx);
             ref = mx;
           }
           const float base = ref == -INFINITY ? 0.f : ref;
-          float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int e = 0; e < 32; ++e) a[e & 3] += ex2_ftz(x[e] - base);
-          total += (a[0] + a[1]) + (a[2] + a[3]);
-        }
-      } else {
-        const float2* info = reinterpret_cast<const float2*>(stream + st * kSlot + W::kTileBytes);
-        const int row0 = (ti0 + i % n_tiles) * kTile;
-        const int rows = min(kTile, m.rows - row0);
-        // the tile's first row that sees the key (0: all do)
-        const int64_t from = (int64_t)max(0, key - (m.seq - m.w)) * p.g - row0;
-        float a[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t buf[2][32];
-        tc::tmem_ld32(s, buf[0]);
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          uint32_t(&v)[32] = buf[c / 32 & 1];
-          tc::tmem_wait_ld();
-          if (c + 32 < kTile) tc::tmem_ld32(s + c + 32, buf[(c / 32 + 1) & 1]);
-          if (__all_sync(kFull, from <= c && c + 32 <= rows)) {
+          const uint64_t base2 = f2_pack(-base, -base);
+          uint64_t a[2] = {0ull, 0ull};
+          if (whole) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float4 f = *reinterpret_cast<const float4*>(info + c + e);
-              a[e & 3] += ex2_ftz(fmaf(__uint_as_float(v[e]), f.x, -f.y));
-              a[(e + 1) & 3] += ex2_ftz(fmaf(__uint_as_float(v[e + 1]), f.z, -f.w));
+              float x, y;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, base2), x, y);
+              a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(ex2_ftz(x), ex2_ftz(y)));
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float2 f = info[c + e];
-              const float w = ex2_ftz(fmaf(__uint_as_float(v[e]), f.x, -f.y));
-              a[e & 3] += c + e >= from && c + e < rows ? w : 0.f;
+            for (int e = 0; e < 32; e += 2) {
+              float x, y;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, base2), x, y);
+              x = k0 + c + e < sees ? ex2_ftz(x) : 0.f;  // (a factor of 0 times -inf is NaN)
+              y = k0 + c + e + 1 < sees ? ex2_ftz(y) : 0.f;
+              a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(x, y));
+            }
+          }
+          float a0, a1;
+          f2_unpack(f2_add(a[0], a[1]), a0, a1);
+          total += a0 + a1;
+        }
+      } else {
+        const float4* info = reinterpret_cast<const float4*>(infos + (i & 7) * kInfoBytes);
+        const int row0 = (ti0 + i % n_tiles) * S::kRows;
+        const int rows = min(S::kRows, m.rows - row0);
+        // the tile's first row that sees the key (0: all do)
+        const int64_t from = (int64_t)max(0, key - (m.seq - m.w)) * p.g - row0;
+        uint64_t a[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < S::kRows; c += 32) {
+          uint32_t v[32];
+          tc::tmem_ld32(s + c, v);
+          tc::tmem_wait_ld();
+          if (__all_sync(kFull, from <= c && c + 32 <= rows)) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float4 f = info[(c + e) >> 1];
+              float x, y;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                               f2_pack(f.x, f.y), f2_pack(f.z, f.w)), x, y);
+              a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(ex2_ftz(x), ex2_ftz(y)));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float4 f = info[(c + e) >> 1];
+              const float x = ex2_ftz(fmaf(__uint_as_float(v[e]), f.x, f.z));
+              const float y = ex2_ftz(fmaf(__uint_as_float(v[e + 1]), f.y, f.w));
+              a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1],
+                                       f2_pack(c + e >= from && c + e < rows ? x : 0.f,
+                                               c + e + 1 >= from && c + e + 1 < rows ? y : 0.f));
             }
           }
         }
         // one sum of up to millions of weights: the rounding of each addition is kept
-        const float add = ((a[0] + a[1]) + (a[2] + a[3])) + low;
+        float a0, a1;
+        f2_unpack(f2_add(a[0], a[1]), a0, a1);
+        const float add = (a0 + a1) + low;
         const float next = total + add;
         low = add - (next - total);
         total = next;
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&t->s_empty[st]);
-        mbar_arrive(&t->empty[st]);
-      }
+      if (lane == 0) mbar_arrive(&t->s_empty[buf]);
     }
+    if (WEIGHTS && isnan(low)) low = 0.f;  // (a NaN sum has no rounding to put back)
+    if (buf == 1) t->part[me] = WEIGHTS ? make_float2(total, low) : make_float2(ref, total);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 5) tc::tmem_dealloc(tmem, kWideCols);
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kWideCols);
   if (!WEIGHTS) {
-    if (warp < 4)
+    if (warp < 4) {
+      join_stats(ref, total, t->part[tid].x, t->part[tid].y);
       p.tile_stats[(((int64_t)tile0 * p.Hkv + kvh0) * p.parts + blockIdx.y) * kTile + tid] =
           make_float2(ref, total);
+    }
     return;
   }
-  if (isnan(low)) low = 0.f;  // (infinite or NaN sums have no rounding to put back)
+  if (warp < 4) total = (total + t->part[tid].x) + (low + t->part[tid].y);
   if (gridDim.z > 1) {
-    if (warp < 4) t->part[tid] = total + low;
+    if (warp < 4) t->part[tid].x = total;
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     if (blockIdx.z == 0 && warp < 4) {
-      total = low = 0.f;
-      for (unsigned c = 0; c < gridDim.z; ++c) total += *cluster.map_shared_rank(&t->part[tid], c);
+      total = 0.f;
+      for (unsigned c = 0; c < gridDim.z; ++c) total += cluster.map_shared_rank(&t->part[tid], c)->x;
     }
     cluster.sync();
   }
   if (blockIdx.z == 0 && warp < 4 && key0 + tid < m.seq) {
     const int64_t o = (int64_t)mass_row(p, r) * p.mass_stride + key0 + tid;
-    p.mass_out[o] = (key0 + tid < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + (total + low);
+    p.mass_out[o] = (key0 + tid < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + total;
   }
 }
 
@@ -747,16 +840,16 @@ __global__ void __launch_bounds__(kTile) mass_join_kernel(MassParams p) {
   if (who.x < 0 || who.x >= p.R || p.first_tile[who.x] < 0 || p.first_tile[who.x] + who.y != tile)
     return;
   const int n = min(p.parts, (p.seq_lens[who.x] + p.part_keys - 1) / p.part_keys);
-  float2* info =
-      reinterpret_cast<float2*>(p.images + (int64_t)blockIdx.x * W::kImage + W::kTileBytes);
-  info[threadIdx.x].y =
-      lse_of(p.tile_stats + (int64_t)blockIdx.x * p.parts * kTile + threadIdx.x, n, kTile);
+  float* info =
+      reinterpret_cast<float*>(p.images + (int64_t)blockIdx.x * W::kImage + W::kTileBytes);
+  info[info_at(threadIdx.x) + 2] =
+      -lse_of(p.tile_stats + (int64_t)blockIdx.x * p.parts * kTile + threadIdx.x, n, kTile);
 }
 
 // ------------------------------------------------------------------- planning
 
 struct MassPlan {
-  int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows;
+  int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows, sum_key_tiles;
   int splits, parts, part_keys, key_tiles, narrow_keys;
   size_t off_stats, off_tile_of, off_first, off_images, off_tile_stats, total;
 };
@@ -766,7 +859,7 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
                     MassPlan& pl) {
   pl = MassPlan{};
   const int64_t g = Hq / Hkv;
-  int64_t steps = 0;
+  int64_t steps = 0;  // of pass 1: row tiles x kv heads x key tiles
   int narrow_keys = 0, wide_keys = 0;
   for (int r = 0; r < R; ++r) {
     const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];
@@ -785,13 +878,15 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
       if (tiles > pl.max_tiles) pl.max_tiles = tiles;
       if (seq[r] > wide_keys) wide_keys = seq[r];
       steps += tiles * Hkv * ((seq[r] + kTile - 1) / kTile);
+      pl.sum_key_tiles += (seq[r] + kTile - 1) / kTile;
     }
   }
   pl.narrow_keys = narrow_keys;
   pl.splits = (narrow_keys + kSplitKeys - 1) / kSplitKeys;
   pl.key_tiles = (wide_keys + kTile - 1) / kTile;
-  // parts of the keys: four times the 152 SMs' worth of CTAs of pass 1, of 4 to 32 key tiles
-  int64_t per = (steps + 607) / 608;
+  // Parts of the keys in pass 1, of 4 to 32 key tiles: 1216 CTAs and more, of which 304 run
+  // at once on 152 SMs.
+  int64_t per = (steps + 1215) / 1216;
   per = per < 4 ? 4 : per > 32 ? 32 : per;
   pl.part_keys = (int)per * kTile;
   pl.parts = (wide_keys + pl.part_keys - 1) / pl.part_keys;
@@ -863,7 +958,7 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
                    cudaStream_t s) {
   static OncePerDevice once;
   constexpr size_t narrow_smem = 1024 + (size_t)kNarrowWarps * kNarrowRing + sizeof(NarrowTail);
-  constexpr size_t wide_smem = 1024 + 3 * (size_t)WideGeo<D, F8>::kImage + sizeof(WideTail);
+  constexpr size_t stats_smem = WideSmem<D, F8, false>::kAlloc, sum_smem = WideSmem<D, F8, true>::kAlloc;
   if (!once.done([] {
         auto set = [](const void* f, size_t n) {
           return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n) ==
@@ -871,8 +966,8 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
         };
         return set((const void*)mass_scores_kernel<D, F8, 1>, narrow_smem) &&
                set((const void*)mass_scores_kernel<D, F8, 2>, narrow_smem) &&
-               set((const void*)mass_tile_kernel<D, F8, false>, wide_smem) &&
-               set((const void*)mass_tile_kernel<D, F8, true>, wide_smem);
+               set((const void*)mass_tile_kernel<D, F8, false>, stats_smem) &&
+               set((const void*)mass_tile_kernel<D, F8, true>, sum_smem);
       }))
     return PA_ERR_CUDA;
   CUtensorMap tmap{};
@@ -893,16 +988,15 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
                     kTile, 0, s, false, 1, p);
   if (st != PA_OK) return st;
   st = launch_after(mass_tile_kernel<D, F8, false>, dim3((unsigned)(pl.n_tiles * p.Hkv), (unsigned)p.parts),
-                    kWideThreads, wide_smem, s, false, 1, tmap, p);
+                    kWideThreads, stats_smem, s, true, 1, tmap, p);
   if (st != PA_OK) return st;
-  st = launch_after(mass_join_kernel<D, F8>, dim3((unsigned)(pl.n_tiles * p.Hkv)), kTile, 0, s, false, 1, p);
+  st = launch_after(mass_join_kernel<D, F8>, dim3((unsigned)(pl.n_tiles * p.Hkv)), kTile, 0, s, true, 1, p);
   if (st != PA_OK) return st;
-  // the kv heads of a key tile go to a cluster while key tiles alone leave SMs idle
+  // a cluster shares the kv heads of a key tile while there are less than four rounds of CTAs
   unsigned share = 1;
-  while (share < 8 && (int)share * 2 <= p.Hkv && (int64_t)pl.key_tiles * p.R * share < 2 * num_sms())
-    share *= 2;
+  while (share < 8 && (int)share * 2 <= p.Hkv && pl.sum_key_tiles * share < 8 * num_sms()) share *= 2;
   return launch_after(mass_tile_kernel<D, F8, true>, dim3((unsigned)pl.key_tiles, (unsigned)p.R, share),
-                      kWideThreads, wide_smem, s, false, share, tmap, p);
+                      kWideThreads, sum_smem, s, true, share, tmap, p);
 }
 
 }  // namespace
