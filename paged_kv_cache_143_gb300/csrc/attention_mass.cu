@@ -68,7 +68,7 @@ struct MassParams {
   int splits;
   int narrow_rows;         // rows of a request of this form, at the most
   // tcgen05 form
-  int2* tile_of;           // [n_tiles] (request, row tile)
+  int4* tile_of;           // [n_tiles] (request or -1, row tile, keys, counted queries)
   int* first_tile;         // [R], -1: not of this form
   uint8_t* images;         // [n_tiles][Hkv][image]
   float2* tile_stats;      // [n_tiles][Hkv][parts][128]
@@ -337,6 +337,10 @@ struct WideGeo {
   static constexpr int kHalf = kTile * 128;                   // 64 bf16 columns of 128 rows
 };
 
+__device__ __forceinline__ int tiles_of(const MassReq& m) {
+  return m.rows > kNarrowRows ? (m.rows + kTile - 1) / kTile : 0;
+}
+
 // 16-byte piece c of row `row` in swizzled rows of SPAN (128 or 64) bytes.
 template <int SPAN>
 __device__ __forceinline__ int swizzled(int row, int c) {
@@ -351,26 +355,34 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
   const int ti = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
   const MassReq m = rows_of(p, r);
   const bool reporter = tid == 0 && ti == 0 && kvh == 0;
-  const int tiles = m.rows > kNarrowRows ? (m.rows + kTile - 1) / kTile : 0;
+  const int tiles = tiles_of(m);
   if (reporter && (bad_request(m) || (m.rows > 0 && !tiles && !p.scores))) raise_error(p.err, kErrBounds);
+  if (r == p.R - 1 && ti == 0 && kvh == 0) {  // entries past the device's rows
+    const int64_t end = before(p, r, [](const MassReq& x) -> int64_t { return tiles_of(x); }) + tiles;
+    for (int64_t x = end + tid; x < p.n_tiles; x += kTile) p.tile_of[x] = make_int4(-1, 0, 0, 0);
+  }
   if (!tiles) {
     if (reporter) p.first_tile[r] = -1;
     return;
   }
   if (ti >= tiles) return;
-  const int64_t first = before(p, r, [](const MassReq& x) -> int64_t {
-    return x.rows > kNarrowRows ? (x.rows + kTile - 1) / kTile : 0;
-  });
+  const int64_t first = before(p, r, [](const MassReq& x) -> int64_t { return tiles_of(x); });
   const bool fits = first + tiles <= p.n_tiles && tiles <= (int)gridDim.x &&
                     (m.seq + kTile - 1) / kTile <= p.key_tiles &&
-                    m.seq <= (int64_t)p.parts * p.part_keys;
+                    m.seq <= (int64_t)p.parts * p.part_keys && mass_row(p, r) >= 0;
   if (reporter) {
     p.first_tile[r] = fits ? (int)first : -1;
-    if (!fits || mass_row(p, r) < 0) raise_error(p.err, kErrBounds);
+    if (!fits) raise_error(p.err, kErrBounds);
+  }
+  if (tid == 0 && kvh == 0) {
+    if (first + ti < p.n_tiles) p.tile_of[first + ti] = make_int4(fits ? r : -1, ti, m.seq, m.w);
+    // (no CTA comes to tiles past the grid's)
+    if (ti == 0)
+      for (int64_t x = first + gridDim.x; x < first + tiles && x < p.n_tiles; ++x)
+        p.tile_of[x] = make_int4(-1, 0, 0, 0);
   }
   if (!fits) return;
   const int tile = (int)first + ti;
-  if (tid == 0 && kvh == 0) p.tile_of[tile] = make_int2(r, ti);
   uint8_t* image = p.images + ((int64_t)tile * p.Hkv + kvh) * W::kImage;
   const int c = ti * kTile + tid;
   uint4 v[D / 8];
@@ -443,7 +455,7 @@ struct WideTail {
   uint64_t s_full[2], s_empty[2];  // accumulators
   uint32_t tmem;
   int abort;
-  float2 part[kTile];              // a warpgroup's results, for the other one and the cluster
+  float part[2][kTile];            // results of the warpgroups, for each other and the cluster
 };
 
 // Warps 0-3 and 4-7: rows or keys, each group of four the accumulators of one stage
@@ -508,13 +520,13 @@ __global__ void __launch_bounds__(kWideThreads, 2)
   if (!WEIGHTS) {
     const int tile = blockIdx.x / p.Hkv;
     kvh0 = blockIdx.x - tile * p.Hkv;
-    const int2 who = p.tile_of[tile];
-    // an entry that this call did not write (the device has fewer rows than the mirrors)
-    if (who.x < 0 || who.x >= p.R || p.first_tile[who.x] < 0 || p.first_tile[who.x] + who.y != tile)
-      return;
+    const int4 who = p.tile_of[tile];
+    if (who.x < 0) return;
     r = who.x;
-    m = rows_of(p, r);
-    if (who.y < 0 || who.y >= (m.rows + kTile - 1) / kTile) return;
+    m.q0 = m.q_len = 0;  // (not needed here)
+    m.seq = who.z;
+    m.w = who.w;
+    m.rows = m.w * p.g;
     tile0 = tile;
     ti0 = who.y;
     key0 = blockIdx.y * p.part_keys;
@@ -522,10 +534,16 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     const int last = min(m.rows - 1, ti0 * kTile + kTile - 1) / p.g;
     const int end = min(m.seq - m.w + last + 1, key0 + p.part_keys);
     n_steps = max(0, (end - key0 + kTile - 1) / kTile);
+    if (n_steps == 0) {
+      if (tid < kTile)
+        p.tile_stats[(((int64_t)tile0 * p.Hkv + kvh0) * p.parts + blockIdx.y) * kTile + tid] =
+            make_float2(-INFINITY, 0.f);
+      return;
+    }
   } else {
     r = blockIdx.y;
     tile0 = p.first_tile[r];
-    if (tile0 < 0 || mass_row(p, r) < 0) return;
+    if (tile0 < 0) return;
     m = rows_of(p, r);
     key0 = blockIdx.x * kTile;
     if (key0 >= m.seq) return;
@@ -567,8 +585,7 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     if (!ok) *static_cast<volatile int*>(&t->abort) = 1;
     return ok;
   };
-  float total = 0.f, low = 0.f, ref = -INFINITY;  // (WEIGHTS: the sum and what its roundings lost)
-
+  float total = 0.f, ref = -INFINITY;
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------- copies
     constexpr int kCols = F8 ? 1 : D / 64;  // boxes across a key row
@@ -698,7 +715,11 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         sc = reinterpret_cast<const float*>(fixed + W::kTileBytes)[info_at(me)];
       sees = m.seq - m.w + min(ti0 * kTile + me, m.rows - 1) / p.g + 1;
     }
-    const int key = key0 + me;  // WEIGHTS
+    // WEIGHTS: a thread reads four keys of its warp's 32, me4 + 8 j, and of every eight
+    // columns two, so that what belongs to a column is loaded for four weights at once;
+    // their sums, and what the roundings of those lost
+    const int me4 = (warp & 3) * 32 + (lane >> 2), col2 = lane & 3;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
     const int buf = warp >> 2;
     for (int i = buf; i < n_steps; i += 2) {
       if (!__all_sync(kFull, (!WEIGHTS || wait(&t->info_full[i & 7], (i >> 3) & 1)) &&
@@ -756,49 +777,74 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         const float4* info = reinterpret_cast<const float4*>(infos + (i & 7) * kInfoBytes);
         const int row0 = (ti0 + i % n_tiles) * S::kRows;
         const int rows = min(S::kRows, m.rows - row0);
-        // the tile's first row that sees the key (0: all do)
-        const int64_t from = (int64_t)max(0, key - (m.seq - m.w)) * p.g - row0;
-        uint64_t a[2] = {0ull, 0ull};
+        // rows from which on the warp's last key is seen (0 and below: all keys by all rows)
+        const int after = key0 + (warp & 3) * 32 + 31 - (m.seq - m.w);
+        const int64_t from = (int64_t)max(0, after) * p.g - row0;
+        uint64_t a[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < S::kRows; c += 32) {
-          uint32_t v[32];
-          tc::tmem_ld32(s + c, v);
+          uint32_t v[2][16];
+          tc::tmem_ld16x256_x4(s + c, v[0]);
+          tc::tmem_ld16x256_x4(s + (16u << 16) + c, v[1]);
           tc::tmem_wait_ld();
-          if (__all_sync(kFull, from <= c && c + 32 <= rows)) {
+          if (from <= c && c + 32 <= rows) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float4 f = info[(c + e) >> 1];
-              float x, y;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
-                               f2_pack(f.x, f.y), f2_pack(f.z, f.w)), x, y);
-              a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(ex2_ftz(x), ex2_ftz(y)));
+            for (int n = 0; n < 4; ++n) {
+              const float4 f = info[(c >> 1) + 4 * n + col2];
+              const uint64_t factor = f2_pack(f.x, f.y), lse = f2_pack(f.z, f.w);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t* w = &v[j >> 1][4 * n + 2 * (j & 1)];
+                float x, y;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(w[0]), __uint_as_float(w[1])), factor, lse), x, y);
+                a[j] = f2_add(a[j], f2_pack(ex2_ftz(x), ex2_ftz(y)));
+              }
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float4 f = info[(c + e) >> 1];
-              const float x = ex2_ftz(fmaf(__uint_as_float(v[e]), f.x, f.z));
-              const float y = ex2_ftz(fmaf(__uint_as_float(v[e + 1]), f.y, f.w));
-              a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1],
-                                       f2_pack(c + e >= from && c + e < rows ? x : 0.f,
-                                               c + e + 1 >= from && c + e + 1 < rows ? y : 0.f));
+            for (int j = 0; j < 4; ++j) {
+              // the tile's first row that sees the key
+              const int64_t first64 = (int64_t)max(0, key0 + me4 + 8 * j - (m.seq - m.w)) * p.g - row0;
+              const int first = (int)min(first64, (int64_t)kTile);
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                const float4 f = info[(c >> 1) + 4 * n + col2];
+                const uint32_t* w = &v[j >> 1][4 * n + 2 * (j & 1)];
+                const int row = c + 8 * n + 2 * col2;
+                const float x = ex2_ftz(fmaf(__uint_as_float(w[0]), f.x, f.z));
+                const float y = ex2_ftz(fmaf(__uint_as_float(w[1]), f.y, f.w));
+                a[j] = f2_add(a[j], f2_pack(row >= first && row < rows ? x : 0.f,
+                                            row + 1 >= first && row + 1 < rows ? y : 0.f));
+              }
             }
           }
         }
         // one sum of up to millions of weights: the rounding of each addition is kept
-        float a0, a1;
-        f2_unpack(f2_add(a[0], a[1]), a0, a1);
-        const float add = (a0 + a1) + low;
-        const float next = total + add;
-        low = add - (next - total);
-        total = next;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float a0, a1;
+          f2_unpack(a[j], a0, a1);
+          const float add = (a0 + a1) + low[j];
+          const float next = sum[j] + add;
+          low[j] = add - (next - sum[j]);
+          sum[j] = next;
+        }
       }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&t->s_empty[buf]);
     }
-    if (WEIGHTS && isnan(low)) low = 0.f;  // (a NaN sum has no rounding to put back)
-    if (buf == 1) t->part[me] = WEIGHTS ? make_float2(total, low) : make_float2(ref, total);
+    if (!WEIGHTS) {
+      if (buf == 1) t->part[0][me] = ref, t->part[1][me] = total;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float x = sum[j] + (isnan(low[j]) ? 0.f : low[j]);  // (a NaN sum has lost no rounding)
+        x += __shfl_xor_sync(kFull, x, 1);
+        x += __shfl_xor_sync(kFull, x, 2);
+        if (col2 == 0) t->part[buf][me4 + 8 * j] = x;
+      }
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -806,20 +852,20 @@ __global__ void __launch_bounds__(kWideThreads, 2)
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kWideCols);
   if (!WEIGHTS) {
     if (warp < 4) {
-      join_stats(ref, total, t->part[tid].x, t->part[tid].y);
+      join_stats(ref, total, t->part[0][tid], t->part[1][tid]);
       p.tile_stats[(((int64_t)tile0 * p.Hkv + kvh0) * p.parts + blockIdx.y) * kTile + tid] =
           make_float2(ref, total);
     }
     return;
   }
-  if (warp < 4) total = (total + t->part[tid].x) + (low + t->part[tid].y);
+  if (warp < 4) total = t->part[0][tid] + t->part[1][tid];
   if (gridDim.z > 1) {
-    if (warp < 4) t->part[tid].x = total;
+    if (warp < 4) t->part[0][tid] = total;  // (read by this thread alone)
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     if (blockIdx.z == 0 && warp < 4) {
       total = 0.f;
-      for (unsigned c = 0; c < gridDim.z; ++c) total += cluster.map_shared_rank(&t->part[tid], c)->x;
+      for (unsigned c = 0; c < gridDim.z; ++c) total += *cluster.map_shared_rank(&t->part[0][tid], c);
     }
     cluster.sync();
   }
@@ -836,10 +882,9 @@ __global__ void __launch_bounds__(kTile) mass_join_kernel(MassParams p) {
   launch_dependents();
   grid_dependency_wait();
   const int tile = blockIdx.x / p.Hkv;
-  const int2 who = p.tile_of[tile];
-  if (who.x < 0 || who.x >= p.R || p.first_tile[who.x] < 0 || p.first_tile[who.x] + who.y != tile)
-    return;
-  const int n = min(p.parts, (p.seq_lens[who.x] + p.part_keys - 1) / p.part_keys);
+  const int4 who = p.tile_of[tile];
+  if (who.x < 0) return;
+  const int n = min(p.parts, (who.z + p.part_keys - 1) / p.part_keys);
   float* info =
       reinterpret_cast<float*>(p.images + (int64_t)blockIdx.x * W::kImage + W::kTileBytes);
   info[info_at(threadIdx.x) + 2] =
@@ -896,7 +941,7 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   pl.off_stats = at;
   if (pl.narrow) at = up(at + (size_t)R * Hkv * kNarrowRows * pl.splits * sizeof(float2));
   pl.off_tile_of = at;
-  at = up(at + (size_t)pl.n_tiles * sizeof(int2));
+  at = up(at + (size_t)pl.n_tiles * sizeof(int4));
   pl.off_first = at;
   if (pl.n_tiles) at = up(at + (size_t)R * sizeof(int));
   pl.off_images = at;
@@ -1074,7 +1119,7 @@ extern "C" pa_status pa_attention_mass(
   p.split_stats = reinterpret_cast<float2*>(ws + pl.off_stats);
   p.splits = pl.splits;
   p.narrow_rows = (int)pl.max_narrow_rows;
-  p.tile_of = reinterpret_cast<int2*>(ws + pl.off_tile_of);
+  p.tile_of = reinterpret_cast<int4*>(ws + pl.off_tile_of);
   p.first_tile = reinterpret_cast<int*>(ws + pl.off_first);
   p.images = ws + pl.off_images;
   p.tile_stats = reinterpret_cast<float2*>(ws + pl.off_tile_stats);
