@@ -12,8 +12,10 @@
 #include <cuda_fp16.h>
 
 #include "batch_rows.cuh"
+#include "mbar_poll.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "tc_ptx.cuh"
 
 namespace pa {
 namespace {
@@ -166,16 +168,6 @@ __global__ void __launch_bounds__(kBoundWarps * 32)
 }
 
 // ------------------------------------------------------------------ scores
-//
-// A warp takes 16 blocks as the rows of m16n8k16 MMAs and the (token, head)
-// pairs of a row tile as the columns, eight at a time. The blocks' bounds go
-// straight from memory to registers as A fragments (lane (grp, tig) holds dims
-// 32 j + 8 tig .. + 7 of rows grp and grp + 8, the same dims for both operands,
-// so that a fragment is a 16-byte load) and stay there for all columns; q+ and
-// q- are cut once by the CTA into B fragments in shared memory. The maximum
-// over the heads of a kv head is taken in registers.
-constexpr int kScoreWarps = 4;
-constexpr int kMaxColTiles = 8;  // n-tiles of a CTA's row tile
 
 struct ScoreParams {
   const __nv_bfloat16* q;
@@ -187,10 +179,31 @@ struct ScoreParams {
   int max_blocks, R, T, Hq, Hkv, g, B, num_blocks;
   int gp;         // columns that a token takes: g padded to 1, 2, 4 or a multiple of 8
   int tile;       // tokens of a row tile
-  int tiles;      // 16-block tiles that a warp goes through
+  int tiles;      // block tiles that a warp (of 16 blocks), or a CTA (of 128), goes through
   float k_scale;
   unsigned* err;
 };
+
+// The row tile of a CTA: slot x belongs to request r, whose slots begin at
+// qsl[r] / tile + r; false if it has no tokens or its blocks end before `first`.
+struct ScoreTile {
+  int r, t0, nt;   // request, first row of q, tokens
+  int pos0;        // position of the first token
+  int n_blocks;    // blocks that the last token sees
+};
+__device__ __forceinline__ bool score_tile(const ScoreParams& p, int slot, int64_t first,
+                                           ScoreTile& s) {
+  s.r = warp_last_le(p.R, slot, [&](int x) { return __ldg(p.qsl + x) / p.tile + x; });
+  ReqSpan q;
+  if (!request_span(p.qsl, p.seq_lens, s.r, p.T, (int64_t)p.max_blocks * p.B, p.err, q)) return false;
+  const int j0 = (slot - (q.q0 / p.tile + s.r)) * p.tile;
+  if (j0 < 0 || j0 >= q.q_len) return false;
+  s.t0 = q.q0 + j0;
+  s.nt = min(p.tile, q.q_len - j0);
+  s.pos0 = q.seq - q.q_len + j0;
+  s.n_blocks = (s.pos0 + s.nt - 1) / p.B + 1;
+  return first < s.n_blocks;
+}
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -218,112 +231,422 @@ __device__ __forceinline__ uint32_t negative(uint32_t x) {
   __nv_bfloat162 v = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&x), z);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+__device__ __forceinline__ uint4 positive(uint4 v) {
+  return make_uint4(positive(v.x), positive(v.y), positive(v.z), positive(v.w));
+}
+__device__ __forceinline__ uint4 negative(uint4 v) {
+  return make_uint4(negative(v.x), negative(v.y), negative(v.z), negative(v.w));
+}
+
+// Decodes (a row tile of at most 8 NH columns): the bounds are what costs, 4 D bytes
+// a (block, kv head) read once. A warp takes 16 blocks as the rows of m16n8k16 MMAs
+// and the (token, head) pairs as columns; q+ and q- stay in registers. Each block's
+// bounds are one bulk copy into the warp's ring of three 16-block stages (records 64
+// bytes apart in banks, so that the 16-byte fragment loads of a quarter-warp do not
+// collide); no warp waits for another. The maximum over the heads is taken in
+// registers.
+constexpr int kScoreWarps = 4;
+constexpr int kScoreStages = 3;
 
 template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(ScoreParams p) {
+struct ScoreRing {
+  static constexpr int kRecord = 4 * D;          // least and greatest key
+  static constexpr int kPitch = kRecord + 64;
+  static constexpr int kStage = 16 * kPitch;
+  static constexpr int kWarp = kScoreStages * kStage;
+  static constexpr size_t kAlloc = kScoreWarps * (kWarp + 8 * kScoreStages);
+};
+
+template <int D, int NH>
+__global__ void __launch_bounds__(kScoreWarps * 32, 2) block_score_kernel(ScoreParams p) {
+  using Rg = ScoreRing<D>;
   constexpr int KJ = D / 32;
-  extern __shared__ uint4 qfrag[];  // [n-tile][j][q+, q-][lane]
+  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 2, tig = lane & 3;
+  uint8_t* ring = smem + warp * Rg::kWarp;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kScoreWarps * Rg::kWarp) + warp * kScoreStages;
   const int kvh = blockIdx.x % p.Hkv;
-  const int slot = blockIdx.x / p.Hkv;
-  const int r = warp_last_le(p.R, slot, [&](int x) { return __ldg(p.qsl + x) / p.tile + x; });
-  ReqSpan s;
-  if (!request_span(p.qsl, p.seq_lens, r, p.T, (int64_t)p.max_blocks * p.B, p.err, s)) return;
-  const int j0 = (slot - (s.q0 / p.tile + r)) * p.tile;
-  if (j0 < 0 || j0 >= s.q_len) return;
-  const int nt = min(p.tile, s.q_len - j0);             // tokens of this tile
-  const int pos0 = s.seq - s.q_len + j0;                // position of its first token
-  const int n_blocks = (pos0 + nt - 1) / p.B + 1;       // blocks that its last token sees
   const int first = (int)blockIdx.y * kScoreWarps * p.tiles * 16;
-  if (first >= n_blocks) return;
-  const int n_col = (nt * p.gp + 7) / 8;                // n-tiles in use
-  for (int x = threadIdx.x; x < n_col * KJ * 32; x += kScoreWarps * 32) {
-    const int l = x & 31, j = (x >> 5) % KJ, c = x / (32 * KJ);
-    const int col = c * 8 + (l >> 2);
-    const int t = min(col / p.gp, nt - 1), h = min(col % p.gp, p.g - 1);
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-        p.q + ((int64_t)(s.q0 + j0 + t) * p.Hq + kvh * p.g + h) * D + 32 * j + 8 * (l & 3)));
-    uint4* dst = qfrag + ((c * KJ + j) * 2) * 32 + l;
-    dst[0] = make_uint4(positive(v.x), positive(v.y), positive(v.z), positive(v.w));
-    dst[32] = make_uint4(negative(v.x), negative(v.y), negative(v.z), negative(v.w));
+  ScoreTile s;
+  if (!score_tile(p, blockIdx.x / p.Hkv, first, s)) return;
+  if (lane == 0) {
+    for (int i = 0; i < kScoreStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
   }
-  __syncthreads();
-  const int32_t* table = p.tables + (int64_t)r * p.max_blocks;
-  for (int it = 0; it < p.tiles; ++it) {
-    const int b0 = first + (it * kScoreWarps + warp) * 16;
-    if (b0 >= n_blocks) break;
-    uint4 a[2][2][KJ];  // [lo, hi][row grp, row grp + 8]
+  __syncwarp();
+  const int32_t* table = p.tables + (int64_t)s.r * p.max_blocks;
+  // the warp's tiles are those of 16 blocks from first + 16 warp, 64 apart
+  const int end = min(s.n_blocks, first + kScoreWarps * p.tiles * 16);
+  const int mine = max(0, (end - first - 16 * warp + 63) / 64);
+  auto block_of = [&](int i) { return first + 16 * warp + 64 * i + (lane & 15); };
+  auto fetch = [&](int i) { return i < mine && lane < 16 && block_of(i) < end ? __ldg(table + block_of(i)) : 0; };
+  auto issue = [&](int i, int id) {
+    bool on = lane < 16 && block_of(i) < end;
+    if (on && (id < 0 || id >= p.num_blocks)) {
+      raise_error(p.err, kErrBounds);
+      on = false;
+    }
+    const unsigned n = __popc(__ballot_sync(kFull, on));
+    uint64_t* bar = &full[i % kScoreStages];
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * Rg::kRecord);
+    __syncwarp();
+    if (on)
+      bulk_g2s(ring + (i % kScoreStages) * Rg::kStage + lane * Rg::kPitch,
+               p.bounds + ((int64_t)id * p.Hkv + kvh) * 2 * D, Rg::kRecord, bar);
+  };
+  for (int i = 0; i < min(mine, kScoreStages); ++i) issue(i, fetch(i));
+  int next_id = fetch(kScoreStages);
+  uint4 qp[NH][KJ], qn[NH][KJ];  // lane (grp, tig): dims 32 j + 8 tig .. + 7 of column 8 h + grp
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    const int col = 8 * h + grp;
+    const int t = min(col / p.gp, s.nt - 1), head = min(col % p.gp, p.g - 1);
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.q + ((int64_t)(s.t0 + t) * p.Hq + kvh * p.g + head) * D + 8 * tig);
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) {
+      const uint4 v = __ldg(src + 4 * j);
+      qp[h][j] = positive(v);
+      qn[h][j] = negative(v);
+    }
+  }
+  for (int i = 0; i < mine; ++i) {
+    const int st = i % kScoreStages;
+    if (!__all_sync(kFull, mbar_wait(&full[st], (i / kScoreStages) & 1, p.err))) {
+      if (lane == 0)
+        for (int x = i + 1; x < min(mine, i + kScoreStages); ++x)
+          mbar_wait(&full[x % kScoreStages], (x / kScoreStages) & 1, p.err);
+      return;  // flagged
+    }
+    float acc[NH][2][4] = {};
+    const uint8_t* rec = ring + st * Rg::kStage + grp * Rg::kPitch + 16 * tig;
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) {
+      const uint4 l0 = *reinterpret_cast<const uint4*>(rec + 64 * j);
+      const uint4 l1 = *reinterpret_cast<const uint4*>(rec + 8 * Rg::kPitch + 64 * j);
+      const uint4 h0 = *reinterpret_cast<const uint4*>(rec + 2 * D + 64 * j);
+      const uint4 h1 = *reinterpret_cast<const uint4*>(rec + 8 * Rg::kPitch + 2 * D + 64 * j);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        mma_bf16(acc[h][1], h0.x, h1.x, h0.y, h1.y, qp[h][j].x, qp[h][j].y);
+        mma_bf16(acc[h][0], l0.x, l1.x, l0.y, l1.y, qn[h][j].x, qn[h][j].y);
+        mma_bf16(acc[h][1], h0.z, h1.z, h0.w, h1.w, qp[h][j].z, qp[h][j].w);
+        mma_bf16(acc[h][0], l0.z, l1.z, l0.w, l1.w, qn[h][j].z, qn[h][j].w);
+      }
+    }
+    __syncwarp();
+    if (i + kScoreStages < mine) {
+      issue(i + kScoreStages, next_id);
+      next_id = fetch(i + kScoreStages + 1);
+    }
+    const int b0 = first + 16 * warp + 64 * i;
+    float* out = p.scores + ((int64_t)s.t0 * p.Hkv + kvh) * p.max_blocks + b0 + grp;
+    const int64_t token = (int64_t)p.Hkv * p.max_blocks;
+    // columns 2 tig, 2 tig + 1 of rows grp (e = 0, 1) and grp + 8 (e = 2, 3)
+    if (p.gp == 1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 2 * tig + (e & 1), blk = b0 + grp + 8 * (e >> 1);
+        if (t < s.nt && (int64_t)blk * p.B <= s.pos0 + t)
+          out[t * token + 8 * (e >> 1)] = (acc[0][0][e] + acc[0][1][e]) * p.k_scale;
+      }
+      continue;
+    }
+    float m[NH][2];
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int ri = 0; ri < 2; ++ri) {
+        float x = max_nan(acc[h][0][2 * ri] + acc[h][1][2 * ri],
+                          acc[h][0][2 * ri + 1] + acc[h][1][2 * ri + 1]);
+        if (p.gp >= 4) x = max_nan(x, __shfl_xor_sync(kFull, x, 1));
+        if (p.gp >= 8) x = max_nan(x, __shfl_xor_sync(kFull, x, 2));
+        m[h][ri] = x;
+      }
+    const int t = NH == 1 ? 2 * tig / p.gp : 0;             // the token of this lane's columns
+    const int writer = NH == 1 ? tig & ~(p.gp / 2 - 1) : 0;  // and the lane that writes for it
 #pragma unroll
     for (int ri = 0; ri < 2; ++ri) {
-      const int i = b0 + grp + 8 * ri;
-      int id = i < n_blocks ? __ldg(table + i) : -1;
-      if (i < n_blocks && (id < 0 || id >= p.num_blocks)) {
-        raise_error(p.err, kErrBounds);
-        id = -1;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.bounds + (((int64_t)max(id, 0) * p.Hkv + kvh) * 2 + h) * D + 8 * tig);
-#pragma unroll
-        for (int j = 0; j < KJ; ++j)
-          a[h][ri][j] = id >= 0 ? __ldg(src + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
-      }
+      const int blk = b0 + grp + 8 * ri;
+      const float x = NH == 1 ? m[0][ri] : max_nan(m[0][ri], m[NH - 1][ri]);
+      if (tig == writer && t < s.nt && (int64_t)blk * p.B <= s.pos0 + t)
+        out[t * token + 8 * ri] = x * p.k_scale;
     }
-    float run[2] = {-INFINITY, -INFINITY};  // over the n-tiles of one token (gp > 8)
-    for (int c = 0; c < n_col; ++c) {
-      float acc[2][4] = {};
+  }
+}
+
+// Chunks: a matrix product of full size, [hi lo] (128 blocks) x [q+ q-] (256 columns)
+// on tcgen05. A CTA keeps q+ and q- of its row tile in shared memory as the operand of
+// 256 columns (N; cut to what is there) and streams the bounds of 128 blocks at a time,
+// their least keys, then their greatest, as the operand of 128 rows: a thread of the
+// copy warps brings 16 bytes by cp.async straight to their swizzled place. Four warps
+// read the accumulators (a thread owns a block and takes the maximum over the heads in
+// registers), so that neighbouring threads write neighbouring blocks' scores.
+constexpr int kChunkThreads = 288;  // warps 0-3: scores; 4-7: copies; 8: MMAs
+constexpr int kChunkCols = 256;
+constexpr int kChunkStages = 3;
+
+template <int D>
+struct ChunkSmem {
+  static constexpr int kHalf = 128 * 128;                 // 64 dims of 128 blocks
+  static constexpr int kStage = D / 64 * kHalf;
+  static constexpr int kColHalf = kChunkCols * 128;       // 64 dims of 256 columns
+  static constexpr int kOffRing = 2 * (D / 64) * kColHalf;  // q- (with the least keys), q+
+  static constexpr int kOffTail = kOffRing + kChunkStages * kStage;
+};
+struct ChunkTail {
+  uint64_t full[kChunkStages], empty[kChunkStages];
+  uint64_t q_ready, s_full[2], s_empty[2];
+  uint32_t tmem;
+  int abort;
+};
+template <int D>
+constexpr size_t chunk_alloc() {
+  return 1024 + ChunkSmem<D>::kOffTail + sizeof(ChunkTail);
+}
+
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(on ? 16u : 0u)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Scores of one block (a thread's TMEM lane) for the tokens of a row tile whose tokens
+// take GP columns (a power of two up to 8; 0: a multiple of 8 that is known at run time).
+template <int GP>
+__device__ __forceinline__ void write_scores(const ScoreParams& p, const ScoreTile& s, uint32_t tm,
+                                             float* out, int64_t token, int blk, int n_cols) {
+  const int from = max(0, (int)min((int64_t)blk * p.B - s.pos0, (int64_t)s.nt));  // first token that sees it
+  float run = 0.f;
+  int in_token = 0, t = 0;  // (GP 0) columns of the token that were gone through, and the token
+  for (int c = 0; c < n_cols; c += 32) {
+    uint32_t v[32];
+    tc::tmem_ld32(tm + c, v);
+    tc::tmem_wait_ld();
+    if constexpr (GP > 0) {
 #pragma unroll
-      for (int j = 0; j < KJ; ++j) {
-        const uint4 qp = qfrag[((c * KJ + j) * 2) * 32 + lane];
-        const uint4 qn = qfrag[((c * KJ + j) * 2 + 1) * 32 + lane];
-        mma_bf16(acc[1], a[1][0][j].x, a[1][1][j].x, a[1][0][j].y, a[1][1][j].y, qp.x, qp.y);
-        mma_bf16(acc[0], a[0][0][j].x, a[0][1][j].x, a[0][0][j].y, a[0][1][j].y, qn.x, qn.y);
-        mma_bf16(acc[1], a[1][0][j].z, a[1][1][j].z, a[1][0][j].w, a[1][1][j].w, qp.z, qp.w);
-        mma_bf16(acc[0], a[0][0][j].z, a[0][1][j].z, a[0][0][j].w, a[0][1][j].w, qn.z, qn.w);
+      for (int e = 0; e < 32; e += GP) {
+        float x = __uint_as_float(v[e]);
+#pragma unroll
+        for (int i = 1; i < GP; ++i) x = max_nan(x, __uint_as_float(v[e + i]));
+        const int tok = (c + e) / GP;
+        if (tok >= from && tok < s.nt) out[tok * token] = x * p.k_scale;
       }
-      // columns 2 tig, 2 tig + 1 of rows grp (e = 0, 1) and grp + 8 (e = 2, 3)
-      float v[4];
+    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (acc[0][e] + acc[1][e]) * p.k_scale;
-      if (p.gp == 1) {
+      for (int e = 0; e < 32; e += 8) {
+        float x = __uint_as_float(v[e]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = c * 8 + 2 * tig + (e & 1), i = b0 + grp + 8 * (e >> 1);
-          if (t < nt && i * p.B <= pos0 + t)
-            p.scores[((int64_t)(s.q0 + j0 + t) * p.Hkv + kvh) * p.max_blocks + i] = v[e];
+        for (int i = 1; i < 8; ++i) x = max_nan(x, __uint_as_float(v[e + i]));
+        run = in_token ? max_nan(run, x) : x;
+        in_token += 8;
+        if (in_token == p.gp) {
+          if (t >= from && t < s.nt) out[t * token] = run * p.k_scale;
+          ++t;
+          in_token = 0;
         }
-        continue;
-      }
-      float m[2] = {max_nan(v[0], v[1]), max_nan(v[2], v[3])};
-#pragma unroll
-      for (int ri = 0; ri < 2; ++ri) {
-        if (p.gp >= 4) m[ri] = max_nan(m[ri], __shfl_xor_sync(kFull, m[ri], 1));
-        if (p.gp >= 8) m[ri] = max_nan(m[ri], __shfl_xor_sync(kFull, m[ri], 2));
-      }
-      int t, writer;  // the token of this lane's columns, and the lane of its group that writes
-      if (p.gp > 8) {
-        const int part = c % (p.gp / 8);
-        run[0] = part ? max_nan(run[0], m[0]) : m[0];
-        run[1] = part ? max_nan(run[1], m[1]) : m[1];
-        if (part + 1 < p.gp / 8) continue;
-        m[0] = run[0];
-        m[1] = run[1];
-        t = c / (p.gp / 8);
-        writer = 0;
-      } else {
-        t = (c * 8 + 2 * tig) / p.gp;
-        writer = tig & ~(p.gp / 2 - 1);
-      }
-#pragma unroll
-      for (int ri = 0; ri < 2; ++ri) {
-        const int i = b0 + grp + 8 * ri;
-        if (tig == writer && t < nt && (int64_t)i * p.B <= pos0 + t)
-          p.scores[((int64_t)(s.q0 + j0 + t) * p.Hkv + kvh) * p.max_blocks + i] = m[ri];
       }
     }
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScoreParams p) {
+  using S = ChunkSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* cols = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* ring = cols + S::kOffRing;
+  ChunkTail* t = reinterpret_cast<ChunkTail*>(cols + S::kOffTail);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kvh = blockIdx.x % p.Hkv;
+  const int first = (int)blockIdx.y * p.tiles * 128;
+  ScoreTile s;
+  if (!score_tile(p, blockIdx.x / p.Hkv, first, s)) return;
+  const int n_tiles = min(p.tiles, (s.n_blocks - first + 127) / 128);
+  const int n_cols = (s.nt * p.gp + 15) & ~15;
+  if (tid == 0) {
+    for (int i = 0; i < kChunkStages; ++i) {
+      mbar_init(&t->full[i], 128);
+      mbar_init(&t->empty[i], 1);
+    }
+    mbar_init(&t->q_ready, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&t->s_full[i], 1);
+      mbar_init(&t->s_empty[i], 4);
+    }
+    t->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tc::tmem_alloc(&t->tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = t->tmem;
+  auto wait = [&](uint64_t* bar, unsigned parity) {
+    const bool ok = mbar_wait_quiet(bar, parity, &t->abort, p.err);
+    if (!ok) *static_cast<volatile int*>(&t->abort) = 1;
+    return ok;
+  };
+  constexpr int kPieces = D / 8;  // 16-byte pieces of a row of dims
+  if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------- copies
+    // a warp's lanes bring 32 / kPieces blocks at once; lane l knows block 32 w + l's id
+    constexpr int kAtOnce = 32 / kPieces;
+    const int w = warp - 4, piece = lane % kPieces;
+    const int32_t* table = p.tables + (int64_t)s.r * p.max_blocks;
+    auto fetch = [&](int i) {
+      const int blk = first + i * 128 + w * 32 + lane;
+      return i < n_tiles && blk < s.n_blocks ? __ldg(table + blk) : -1;
+    };
+    int id = fetch(0), next = -1;
+    bool ok = true;
+    int step = 0;
+    for (; step < 2 * n_tiles && ok; ++step) {
+      const int i = step >> 1, h = step & 1, st = step % kChunkStages;
+      if (step >= kChunkStages) ok = __all_sync(kFull, wait(&t->empty[st], (step / kChunkStages - 1) & 1));
+      if (!ok) break;
+      if (h == 0) next = fetch(i + 1);
+      bool good = id >= 0 && id < p.num_blocks;
+      if (!good && h == 0 && first + i * 128 + w * 32 + lane < s.n_blocks) raise_error(p.err, kErrBounds);
+      const int use = good ? id : -1;
+      uint8_t* dst = ring + st * S::kStage + (piece >> 3) * S::kHalf;
+#pragma unroll
+      for (int b = 0; b < 32; b += kAtOnce) {
+        const int mine = b + lane / kPieces;  // of the warp's 32 blocks
+        const int from = __shfl_sync(kFull, use, mine);
+        const int row = w * 32 + mine;
+        const __nv_bfloat16* src =
+            p.bounds + (((int64_t)max(from, 0) * p.Hkv + kvh) * 2 + h) * D + piece * 8;
+        cp_async16_or_zero(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4), src, from >= 0);
+      }
+      cp_async_commit();
+      if (step > 0) {  // the step before has landed: hand it over
+        cp_async_wait<1>();
+        tc::fence_proxy_async_smem();
+        mbar_arrive(&t->full[(step - 1) % kChunkStages]);
+      }
+      if (h == 1) id = next;
+    }
+    cp_async_wait<0>();
+    if (ok) {
+      tc::fence_proxy_async_smem();
+      mbar_arrive(&t->full[(step - 1) % kChunkStages]);
+    }
+  } else if (warp == 8) {
+    // --------------------------------------------------------------- MMAs
+    if (tc::elect_one()) {
+      const uint32_t idesc = tc::idesc_16bit_f32(128, 16, false, false, false) - (2u << 17) +
+                             ((uint32_t)(n_cols >> 3) << 17);
+      bool ok = wait(&t->q_ready, 0);
+      for (int step = 0; step < 2 * n_tiles && ok; ++step) {
+        const int i = step >> 1, h = step & 1, st = step % kChunkStages, buf = i & 1;
+        if (h == 0 && i >= 2) ok = wait(&t->s_empty[buf], ((i >> 1) - 1) & 1);
+        ok = ok && wait(&t->full[st], (step / kChunkStages) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t a = tc::smem_desc_sw128(ring + st * S::kStage, 16, 1024);
+        const uint64_t b = tc::smem_desc_sw128(cols + h * (D / 64) * S::kColHalf, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_bf16_ss(tmem + buf * kChunkCols, tc::desc_at(a, (k >> 2) * S::kHalf + (k & 3) * 32),
+                          tc::desc_at(b, (k >> 2) * S::kColHalf + (k & 3) * 32), idesc, h > 0 || k > 0);
+        tc::mma_commit(&t->empty[st]);
+        if (h == 1) tc::mma_commit(&t->s_full[buf]);
+      }
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------- columns first, then scores
+    for (int x = tid; x < n_cols * kPieces; x += 128) {
+      const int piece = x % kPieces, c = x / kPieces;
+      const int tok = min(c / p.gp, s.nt - 1), head = min(c % p.gp, p.g - 1);
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(
+          p.q + ((int64_t)(s.t0 + tok) * p.Hq + kvh * p.g + head) * D + piece * 8));
+      uint8_t* dst = cols + (piece >> 3) * S::kColHalf + c * 128 + (((piece & 7) ^ (c & 7)) << 4);
+      *reinterpret_cast<uint4*>(dst) = negative(v);
+      *reinterpret_cast<uint4*>(dst + (D / 64) * S::kColHalf) = positive(v);
+    }
+    tc::fence_proxy_async_smem();
+    mbar_arrive(&t->q_ready);
+    const int64_t token = (int64_t)p.Hkv * p.max_blocks;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int buf = i & 1;
+      if (!__all_sync(kFull, wait(&t->s_full[buf], (i >> 1) & 1))) break;
+      tc::fence_after_sync();
+      const int blk = first + i * 128 + tid;
+      const uint32_t tm = tmem + lanes + buf * kChunkCols;
+      float* out = p.scores + ((int64_t)s.t0 * p.Hkv + kvh) * p.max_blocks + blk;
+      switch (p.gp) {
+        case 1: write_scores<1>(p, s, tm, out, token, blk, n_cols); break;
+        case 2: write_scores<2>(p, s, tm, out, token, blk, n_cols); break;
+        case 4: write_scores<4>(p, s, tm, out, token, blk, n_cols); break;
+        case 8: write_scores<8>(p, s, tm, out, token, blk, n_cols); break;
+        default: write_scores<0>(p, s, tm, out, token, blk, n_cols);
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&t->s_empty[buf]);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D, int NH>
+bool score_attributes() {
+  static OncePerDevice once;
+  return once.done([] {
+    return cudaFuncSetAttribute(block_score_kernel<D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)ScoreRing<D>::kAlloc) == cudaSuccess;
+  });
+}
+template <int D>
+bool chunk_attributes() {
+  static OncePerDevice once;
+  return once.done([] {
+    return cudaFuncSetAttribute(chunk_score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)chunk_alloc<D>()) == cudaSuccess;
+  });
+}
+
+template <int D>
+pa_status launch_scores(ScoreParams& p, cudaStream_t stream) {
+  // At most one token a request on average and 16 columns a token: the streaming form, else
+  // the chunks' (which takes any batch: a single token costs it one small MMA more).
+  const bool decodes = p.T <= p.R && p.gp <= 16;
+  const int cols = decodes ? (p.gp <= 8 ? 8 : 16) : kChunkCols;
+  p.tile = cols / p.gp;
+  const int64_t slots = p.T / p.tile + (int64_t)p.R;
+  const int per = decodes ? kScoreWarps * 16 : 128;  // blocks of a tile of the CTA
+  const int64_t all = slots * p.Hkv * (((int64_t)p.max_blocks + per - 1) / per);
+  // a CTA goes through several tiles, as long as all SMs have a few CTAs
+  const int64_t want = all / ((decodes ? 4 : 3) * (int64_t)num_sms());
+  p.tiles = (int)(want < 1 ? 1 : want > 8 ? 8 : want);
+  const int64_t chunks = ((int64_t)p.max_blocks + per * p.tiles - 1) / (per * p.tiles);
+  if (slots * p.Hkv > 0x7fffffff || chunks > 65535) return PA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(slots * p.Hkv), (unsigned)chunks);
+  if (!decodes) {
+    if (!chunk_attributes<D>()) return PA_ERR_CUDA;
+    chunk_score_kernel<D><<<grid, kChunkThreads, chunk_alloc<D>(), stream>>>(p);
+  } else if (p.gp <= 8) {
+    if (!score_attributes<D, 1>()) return PA_ERR_CUDA;
+    block_score_kernel<D, 1><<<grid, kScoreWarps * 32, ScoreRing<D>::kAlloc, stream>>>(p);
+  } else {
+    if (!score_attributes<D, 2>()) return PA_ERR_CUDA;
+    block_score_kernel<D, 2><<<grid, kScoreWarps * 32, ScoreRing<D>::kAlloc, stream>>>(p);
+  }
+  return launch_status();
 }
 
 }  // namespace
@@ -392,21 +715,10 @@ extern "C" pa_status pa_score_blocks(const void* q, const void* bounds, float* s
   p.B = pool->block_size;
   p.num_blocks = pool->num_blocks;
   p.gp = p.g <= 1 ? 1 : p.g <= 2 ? 2 : p.g <= 4 ? 4 : (p.g + 7) / 8 * 8;
-  if (p.gp > 8 * kMaxColTiles) return PA_ERR_UNSUPPORTED;
-  p.tile = 8 * kMaxColTiles / p.gp;
-  p.tiles = 2;
+  if (p.g > 64) return PA_ERR_UNSUPPORTED;
   p.k_scale = pool->dtype == PA_KV_FP8_E4M3 ? pool->k_scale : 1.f;
   p.err = error_word();
   if (!p.err) return PA_ERR_CUDA;
-  const int64_t slots = num_tokens / p.tile + (int64_t)num_reqs;
-  const int per_cta = kScoreWarps * p.tiles * 16;
-  const int64_t chunks = ((int64_t)max_blocks + per_cta - 1) / per_cta;
-  if (slots * p.Hkv > 0x7fffffff || chunks > 65535) return PA_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(slots * p.Hkv), (unsigned)chunks);
-  const size_t smem = (size_t)kMaxColTiles * (pool->head_dim / 32) * 2 * 32 * sizeof(uint4);
-  if (pool->head_dim == 128)
-    block_score_kernel<128><<<grid, kScoreWarps * 32, smem, as_stream(stream)>>>(p);
-  else
-    block_score_kernel<64><<<grid, kScoreWarps * 32, smem, as_stream(stream)>>>(p);
-  return launch_status();
+  return pool->head_dim == 128 ? launch_scores<128>(p, as_stream(stream))
+                               : launch_scores<64>(p, as_stream(stream));
 }
