@@ -3,16 +3,22 @@
 // row's candidates the first and last ones and the greatest others, listed in
 // ascending order.
 //
-// One CTA per row. Scores become 32-bit keys in the order of the numbers (NaN
-// above all, forced candidates above NaN, -0 as 0), which each thread holds in
-// registers for a run of consecutive candidates. The k-th greatest key is found
-// bit by bit from the top: a bit stays set while at least k keys reach the
-// prefix with it, 32 votes of the CTA in all and no atomics, so nothing depends
-// on timing. Keys above the threshold are taken, and of those equal to it as
-// many as are left, from the lowest index: one scan of both counts gives every
-// thread the place of its candidates in the list.
-// Rows longer than the registers hold (32768 candidates) read their scores again
-// for every two bits.
+// Scores become 32-bit keys in the order of the numbers (NaN above all, forced
+// candidates above NaN, -0 as 0). The k-th greatest key is found eight bits at a time
+// from the top: of the keys that agree with what is found so far, a histogram in shared
+// memory counts the next eight bits, and the digit is the one in which the k-th falls.
+// Keys above the threshold are taken, and of those equal to it as many as are left,
+// from the lowest index: one running count of both gives each candidate its place in
+// the list. Counts are whole numbers, so nothing depends on the order of the atomics.
+//  - A CTA of 128 or 512 threads holds eight candidates a thread in registers; a row
+//    of more than 4096 is shared by a cluster of 2, 4 or 8 CTAs (histograms and counts
+//    joined through distributed shared memory), and of more than 32768 read again for
+//    every pass.
+//  - What is left is latency (a few hundred kilobytes for a whole batch): a pass is
+//    eight atomics a thread, one barrier, and the digit, which every warp works out for
+//    itself from the histogram.
+#include <cooperative_groups.h>
+
 #include "batch_rows.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -33,6 +39,7 @@ struct SelectParams {
   int R, T, H, unit;         // candidates are units of `unit` tokens
   int limit;                 // candidates that a row has room for
   int first, last, k;
+  int split;                 // CTAs (a cluster) a row
   int32_t* out;              // [rows][k]
   int32_t* counts;           // [R] or NULL
   unsigned* err;
@@ -45,43 +52,63 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive sums over the CTA's threads of two counts; the scratch is [2][32].
+constexpr int kEach = 8;  // candidates of a thread in a round
+constexpr int kBins = 256;
+
 template <int THREADS>
-__device__ __forceinline__ void scan2(int& a, int& b, int (*scratch)[32]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = a, y = b;
+struct SelectTail {
+  alignas(16) int hist[4][kBins];   // of this CTA, pass by pass
+  alignas(16) int total[kBins];     // of the cluster
+  int above[kEach][THREADS / 32];   // of a round: keys above the threshold, by place and warp
+  int equal[kEach][THREADS / 32];   // and equal to it
+  int cta_above, cta_equal;
+};
+
+// The digit into which the `left`-th key from the top falls, and which of that digit's
+// keys it is (from 1). The whole warp calls it; lane l has bins 255 - 8 l and below.
+__device__ __forceinline__ void find_digit(const int* hist, int& left, uint32_t& digit) {
+  const int lane = threadIdx.x & 31;
+  const int4 hi = *reinterpret_cast<const int4*>(hist + kBins - 4 - 8 * lane);
+  const int4 lo = *reinterpret_cast<const int4*>(hist + kBins - 8 - 8 * lane);
+  const int c[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += c[i];
+  int before = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(kFull, x, o), v = __shfl_up_sync(kFull, y, o);
-    if (lane >= o) {
-      x += u;
-      y += v;
-    }
+    const int y = __shfl_up_sync(kFull, before, o);
+    if (lane >= o) before += y;
   }
-  if (lane == 31) {
-    scratch[0][warp] = x;
-    scratch[1][warp] = y;
-  }
-  __syncthreads();
-  int before_x = 0, before_y = 0;
+  const unsigned reached = __ballot_sync(kFull, before >= left);
+  const int who = __ffs(reached) - 1;  // (left is at most the number of keys)
+  before -= sum;
+  int d = 0, rest = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w)
-    if (w < warp) {
-      before_x += scratch[0][w];
-      before_y += scratch[1][w];
+  for (int i = 0; i < 8; ++i) {
+    if (before < left && before + c[i] >= left) {
+      d = kBins - 1 - 8 * lane - i;
+      rest = left - before;
     }
-  a = before_x + x - a;
-  b = before_y + y - b;
+    before += c[i];
+  }
+  digit = (uint32_t)__shfl_sync(kFull, d, who);
+  left = __shfl_sync(kFull, rest, who);
 }
 
-template <int THREADS, int M>
+template <int THREADS>
 __global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
-  __shared__ int scratch[2][32];
-  __shared__ int votes[2][3];
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  namespace cg = cooperative_groups;
+  constexpr int kWarps = THREADS / 32, kRound = THREADS * kEach;
+  __shared__ SelectTail<THREADS> sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int split = p.split;
+  const int64_t row = blockIdx.x / split;
+  const int rank = (int)(blockIdx.x - row * split);
+  for (int i = tid; i < 4 * kBins; i += THREADS) (&sm.hist[0][0])[i] = 0;
   const float* src;
   int n;  // candidates
+  // (every CTA of a cluster takes the same way out)
   if (p.qsl) {
     const int t = (int)(row / p.H);
     const int r = request_of_row(p.qsl, p.R, t);
@@ -101,137 +128,166 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
     src = p.scores + (int64_t)at * p.stride;
   }
   int32_t* out = p.out + row * p.k;
-  if (p.counts && tid == 0) p.counts[row] = min(n, p.k);
+  if (p.counts && tid == 0 && rank == 0) p.counts[row] = min(n, p.k);
   if (n <= p.k) {
-    for (int i = tid; i < p.k; i += THREADS) out[i] = i < n ? i : -1;
+    for (int i = rank * THREADS + tid; i < p.k; i += THREADS * split) out[i] = i < n ? i : -1;
     return;
   }
+  // this CTA's run of candidates; of each round of 8 THREADS a thread has every THREADS-th
+  const int share = (n + split - 1) / split;
+  const int begin = min(n, rank * share), end = min(n, begin + share);
   const int tail = n - p.last;
-  auto key_at = [&](int i) -> uint32_t {
-    return i < p.first || i >= tail ? kForced : key_of(__ldg(src + i));
+  const bool one_round = share <= kRound;
+  uint32_t key[kEach];  // (0 where there is no candidate: the lowest key, of -inf, is greater)
+  auto read = [&](int base) {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int i = base + j * THREADS + tid;
+      key[j] = i >= end ? 0u : i < p.first || i >= tail ? kForced : key_of(__ldg(src + i));
+    }
   };
-  if (n <= THREADS * M) {
-    uint32_t key[M];
-    const int i0 = tid * M;
-    const bool wide = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
-#pragma unroll
-    for (int m = 0; m < M; m += 4) {
-      if (wide && i0 + m + 4 <= n) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(src + i0 + m));
-        key[m] = key_of(v.x);
-        key[m + 1] = key_of(v.y);
-        key[m + 2] = key_of(v.z);
-        key[m + 3] = key_of(v.w);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) key[m + e] = i0 + m + e < n ? key_of(__ldg(src + i0 + m + e)) : 0u;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i0 + m + e;
-        if (i < n && (i < p.first || i >= tail)) key[m + e] = kForced;
-      }
-    }
-    // places past n hold 0, below every candidate's key (the lowest, of -inf, is 0x007fffff)
-    uint32_t thr = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t want = thr | (1u << bit);
-      int c = 0;
-#pragma unroll
-      for (int m = 0; m < M; ++m) c += key[m] >= want;
-      c = __reduce_add_sync(kFull, c);
-      // one slot of `scratch` per warp, two rows in turn: the next bit's counts
-      // do not overtake the reading of this one's
-      if ((tid & 31) == 0) scratch[bit & 1][tid >> 5] = c;
-      __syncthreads();
-      int sum = (tid & 31) < THREADS / 32 ? scratch[bit & 1][tid & 31] : 0;
-      sum = __reduce_add_sync(kFull, sum);
-      if (sum >= p.k) thr = want;
-    }
-    int above = 0, equal = 0;
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      above += key[m] > thr;
-      equal += key[m] == thr && i0 + m < n;
-    }
-    const int mine = above;
-    __syncthreads();
-    int before = above, ties = equal;
-    scan2<THREADS>(before, ties, scratch);
-    // all keys above the threshold: the last thread's sums
-    if (tid == THREADS - 1) votes[0][0] = before + mine;
-    __syncthreads();
-    const int room = p.k - votes[0][0];  // ties that are taken
-    int at = before + min(ties, room);
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const bool tie = key[m] == thr && i0 + m < n;
-      if (key[m] > thr || (tie && ties < room)) out[at++] = i0 + m;
-      ties += tie;
-    }
-    return;
-  }
-  // A row too long for the registers.
+  read(begin);
+  cg::cluster_group cluster = cg::this_cluster();
   uint32_t thr = 0;
-  for (int bit = 30; bit >= 0; bit -= 2) {
-    int c[3] = {0, 0, 0};
-    for (int i = tid; i < n; i += THREADS) {
-      const uint32_t key = key_at(i);
+  int left = p.k;  // of the k, those among the keys that agree with thr so far
+  __syncthreads();
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    int* hist = sm.hist[pass];
+    for (int base = begin; base < end; base += kRound) {
+      if (!one_round) read(base);
 #pragma unroll
-      for (int v = 0; v < 3; ++v) c[v] += key >= (thr | ((uint32_t)(v + 1) << bit));
+      for (int j = 0; j < kEach; ++j)
+        if (key[j] != 0u && (pass == 0 || ((key[j] ^ thr) >> (shift + 8)) == 0u))
+          atomicAdd(&hist[(key[j] >> shift) & (kBins - 1)], 1);
     }
-    const int turn = (bit >> 1) & 1;
-    if (tid < 3) votes[turn][tid] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < 3; ++v) {
-      const int w = __reduce_add_sync(kFull, c[v]);
-      if ((tid & 31) == 0) atomicAdd(&votes[turn][v], w);  // whole numbers: any order
+    uint32_t digit;
+    if (split > 1) {
+      cluster.sync();
+      for (int i = tid; i < kBins; i += THREADS) {
+        int c = 0;
+        for (int o = 0; o < split; ++o) c += *cluster.map_shared_rank(&hist[i], o);
+        sm.total[i] = c;
+      }
+      __syncthreads();
+      find_digit(sm.total, left, digit);
+      __syncthreads();
+    } else {
+      __syncthreads();
+      find_digit(hist, left, digit);
     }
-    __syncthreads();
-    const uint32_t digit = (votes[turn][0] >= p.k) + (votes[turn][1] >= p.k) + (votes[turn][2] >= p.k);
-    thr |= digit << bit;
+    thr |= digit << shift;
   }
-  int done = 0;   // listed so far
-  int seen = 0;   // ties met so far
-  int above = 0;  // keys above the threshold in all
-  for (int i = tid; i < n; i += THREADS) above += key_at(i) > thr;
-  above = __reduce_add_sync(kFull, above);
-  __syncthreads();
-  if ((tid & 31) == 0) scratch[0][tid >> 5] = above;
-  __syncthreads();
-  above = (tid & 31) < THREADS / 32 ? scratch[0][tid & 31] : 0;
-  above = __reduce_add_sync(kFull, above);
-  const int room = p.k - above;
-  for (int base = 0; base < n; base += THREADS) {
-    const int i = base + tid;
-    const uint32_t key = i < n ? key_at(i) : 0u;
-    const int up = i < n && key > thr, tie = i < n && key == thr;
-    int a = up, e = tie;
+  // left: how many of the keys equal to thr are taken. First, what the CTAs before have.
+  int above0 = 0, equal0 = 0;
+  if (split > 1) {
+    int a = 0, e = 0;
+    for (int base = begin; base < end; base += kRound) {
+      if (!one_round) read(base);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        a += key[j] > thr;
+        e += key[j] == thr;
+      }
+    }
+    a = __reduce_add_sync(kFull, a);
+    e = __reduce_add_sync(kFull, e);
+    if (tid == 0) sm.cta_above = sm.cta_equal = 0;
     __syncthreads();
-    scan2<THREADS>(a, e, scratch);
-    const bool taken = up || (tie && seen + e < room);
-    if (taken) out[done + a + min(e, max(room - seen, 0))] = i;
-    if (tid == THREADS - 1) {
-      votes[0][0] = a + up;
-      votes[0][1] = e + tie;
+    if (lane == 0) {
+      atomicAdd(&sm.cta_above, a);
+      atomicAdd(&sm.cta_equal, e);
+    }
+    cluster.sync();
+    for (int o = 0; o < rank; ++o) {
+      above0 += *cluster.map_shared_rank(&sm.cta_above, o);
+      equal0 += *cluster.map_shared_rank(&sm.cta_equal, o);
+    }
+    cluster.sync();  // no CTA leaves while another reads its counts
+  }
+  for (int base = begin; base < end; base += kRound) {
+    if (!one_round) read(base);
+    unsigned up[kEach], tie[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      up[j] = __ballot_sync(kFull, key[j] > thr);
+      tie[j] = __ballot_sync(kFull, key[j] == thr);
+      if (lane == 0) {
+        sm.above[j][warp] = __popc(up[j]);
+        sm.equal[j][warp] = __popc(tie[j]);
+      }
     }
     __syncthreads();
-    done += votes[0][0] + min(votes[0][1], max(room - seen, 0));
-    seen += votes[0][1];
+    // exclusive sums over (j, warp), kEach * kWarps places, each warp for itself
+    constexpr int kPlaces = kEach * kWarps, kPer = kPlaces / 32;
+    int a[kPer], e[kPer], sa = 0, se = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      a[i] = (&sm.above[0][0])[lane * kPer + i];
+      e[i] = (&sm.equal[0][0])[lane * kPer + i];
+      sa += a[i];
+      se += e[i];
+    }
+    int ca = sa, ce = se;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, ca, o), z = __shfl_up_sync(kFull, ce, o);
+      if (lane >= o) {
+        ca += y;
+        ce += z;
+      }
+    }
+    const int round_above = __shfl_sync(kFull, ca, 31), round_equal = __shfl_sync(kFull, ce, 31);
+    ca -= sa;
+    ce -= se;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      // the sums before place (j, warp): lane (j kWarps + warp) / kPer has them
+      const int place = j * kWarps + warp, from = place / kPer;
+      int x = __shfl_sync(kFull, ca, from), y = __shfl_sync(kFull, ce, from);
+#pragma unroll
+      for (int i = 0; i < kPer - 1; ++i) {
+        const int u = __shfl_sync(kFull, a[i], from), v = __shfl_sync(kFull, e[i], from);
+        if (from * kPer + i < place) {
+          x += u;
+          y += v;
+        }
+      }
+      const unsigned lower = (1u << lane) - 1u;
+      x += above0 + __popc(up[j] & lower);
+      y += equal0 + __popc(tie[j] & lower);
+      const bool is_up = key[j] > thr;
+      if (is_up || (key[j] == thr && y < left)) out[x + min(y, left)] = base + j * THREADS + tid;
+    }
+    above0 += round_above;
+    equal0 += round_equal;
+    if (!one_round) __syncthreads();
   }
 }
 
 pa_status launch_select(SelectParams& p, int64_t rows, cudaStream_t s) {
-  if (rows > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+  const int threads = p.limit <= 1024 ? 128 : 512;
+  p.split = 1;
+  while (p.split < 8 && (int64_t)p.split * threads * kEach < p.limit) p.split *= 2;
+  if (rows * p.split > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   p.err = error_word();
   if (!p.err) return PA_ERR_CUDA;
-  if (p.limit <= 1024)
-    select_kernel<128, 8><<<(unsigned)rows, 128, 0, s>>>(p);
-  else if (p.limit <= 4096)
-    select_kernel<256, 16><<<(unsigned)rows, 256, 0, s>>>(p);
-  else
-    select_kernel<512, 64><<<(unsigned)rows, 512, 0, s>>>(p);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(rows * p.split));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)p.split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, threads == 128 ? select_kernel<128> : select_kernel<512>, p) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
   return launch_status();
 }
 
