@@ -10,13 +10,13 @@
 // Keys above the threshold are taken, and of those equal to it as many as are left,
 // from the lowest index: one running count of both gives each candidate its place in
 // the list. Counts are whole numbers, so nothing depends on the order of the atomics.
-//  - A CTA of 128 or 512 threads holds eight candidates a thread in registers; a row
-//    of more than 4096 is shared by a cluster of 2, 4 or 8 CTAs (histograms and counts
+//  - A CTA of 128 threads holds eight candidates a thread in registers, one of 256
+//    sixteen; a row of more than 4096 is shared by a cluster of 2, 4 or 8 CTAs (histograms and counts
 //    joined through distributed shared memory), and of more than 32768 read again for
 //    every pass.
 //  - What is left is latency (a few hundred kilobytes for a whole batch): a pass is
-//    eight atomics a thread, one barrier, and the digit, which every warp works out for
-//    itself from the histogram.
+//    an atomic a candidate, and the digit, which one warp works out for all (every warp
+//    for itself took more issue slots than the candidates).
 #include <cooperative_groups.h>
 
 #include "batch_rows.cuh"
@@ -52,17 +52,31 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kEach = 8;  // candidates of a thread in a round
 constexpr int kBins = 256;
 
-template <int THREADS>
+template <int THREADS, int EACH>
 struct SelectTail {
-  alignas(16) int hist[4][kBins];   // of this CTA, pass by pass
-  alignas(16) int total[kBins];     // of the cluster
-  int above[kEach][THREADS / 32];   // of a round: keys above the threshold, by place and warp
-  int equal[kEach][THREADS / 32];   // and equal to it
+  alignas(16) int hist[4][kBins];         // of this CTA, pass by pass
+  alignas(16) int total[kBins];           // of the cluster
+  int2 counts[EACH * THREADS / 32];  // of a round, by place and warp: keys above the threshold
+                                     // and equal to it; then the sums of those before
+  int2 round;                        // a round's counts
+  uint32_t digit;                    // a pass's digit, and which of its keys is wanted
+  int rest;
+  int row_state, row_n;              // what the row is: 0 nothing to do, 1 candidates
+  const float* row_src;
   int cta_above, cta_equal;
 };
+
+// One more in a bin, where `on`: predicated, so that a thread's candidates go out one
+// after the other (a branch for each costs several times as much).
+__device__ __forceinline__ void count_if(bool on, int* bin) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p red.shared::cta.add.u32 [%0], 1;\n\t}" ::"r"(smem_u32(bin)),
+      "r"((uint32_t)on)
+      : "memory");
+}
 
 // The digit into which the `left`-th key from the top falls, and which of that digit's
 // keys it is (from 1). The whole warp calls it; lane l has bins 255 - 8 l and below.
@@ -96,52 +110,61 @@ __device__ __forceinline__ void find_digit(const int* hist, int& left, uint32_t&
   left = __shfl_sync(kFull, rest, who);
 }
 
-template <int THREADS>
+template <int THREADS, int EACH>
 __global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
   namespace cg = cooperative_groups;
-  constexpr int kWarps = THREADS / 32, kRound = THREADS * kEach;
-  __shared__ SelectTail<THREADS> sm;
+  constexpr int kWarps = THREADS / 32, kRound = THREADS * EACH;
+  __shared__ SelectTail<THREADS, EACH> sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int split = p.split;
-  const int64_t row = blockIdx.x / split;
+  const unsigned row = blockIdx.x / (unsigned)split;
   const int rank = (int)(blockIdx.x - row * split);
   for (int i = tid; i < 4 * kBins; i += THREADS) (&sm.hist[0][0])[i] = 0;
-  const float* src;
-  int n;  // candidates
-  // (every CTA of a cluster takes the same way out)
-  if (p.qsl) {
-    const int t = (int)(row / p.H);
-    const int r = request_of_row(p.qsl, p.R, t);
-    if (r < 0) return;  // a row behind the last sequence
-    ReqSpan s;
-    if (!request_span(p.qsl, p.seq_lens, r, p.T, (int64_t)p.limit * p.unit, p.err, s)) return;
-    n = (s.seq - s.q_len + (t - s.q0)) / p.unit + 1;
-    src = p.scores + row * p.stride;
-  } else {
-    const int r = (int)row;
-    n = p.seq_lens[r];
-    const int at = p.idx ? p.idx[r] : r;
-    if (n < 0 || n > p.limit || at < 0 || at >= p.max_rows) {
-      if (tid == 0) raise_error(p.err, kErrBounds);
-      return;
+  if (warp == 0) {  // the row's candidates (every CTA of a cluster finds the same)
+    int n = 0;
+    const float* src = nullptr;
+    bool ok = true;
+    if (p.qsl) {
+      const int t = (int)(row / (unsigned)p.H);
+      const int r = request_of_row(p.qsl, p.R, t);
+      ReqSpan s;
+      ok = r >= 0 &&  // else a row behind the last sequence
+           request_span(p.qsl, p.seq_lens, r, p.T, (int64_t)p.limit * p.unit, p.err, s);
+      if (ok) n = (s.seq - s.q_len + (t - s.q0)) / p.unit + 1;
+      src = p.scores + (int64_t)row * p.stride;
+    } else {
+      n = p.seq_lens[row];
+      const int at = p.idx ? p.idx[row] : (int)row;
+      ok = n >= 0 && n <= p.limit && at >= 0 && at < p.max_rows;
+      if (!ok && lane == 0) raise_error(p.err, kErrBounds);
+      src = p.scores + (int64_t)at * p.stride;
     }
-    src = p.scores + (int64_t)at * p.stride;
+    if (lane == 0) {
+      sm.row_state = ok;
+      sm.row_n = n;
+      sm.row_src = src;
+    }
   }
-  int32_t* out = p.out + row * p.k;
+  __syncthreads();
+  if (!sm.row_state) return;
+  const int n = sm.row_n;
+  const float* src = sm.row_src;
+  int32_t* out = p.out + (int64_t)row * p.k;
   if (p.counts && tid == 0 && rank == 0) p.counts[row] = min(n, p.k);
   if (n <= p.k) {
     for (int i = rank * THREADS + tid; i < p.k; i += THREADS * split) out[i] = i < n ? i : -1;
     return;
   }
-  // this CTA's run of candidates; of each round of 8 THREADS a thread has every THREADS-th
+  // this CTA's run of candidates; of each round a thread has every THREADS-th, in `held` places
   const int share = (n + split - 1) / split;
   const int begin = min(n, rank * share), end = min(n, begin + share);
   const int tail = n - p.last;
   const bool one_round = share <= kRound;
-  uint32_t key[kEach];  // (0 where there is no candidate: the lowest key, of -inf, is greater)
+  const int held = min(EACH, (end - begin + THREADS - 1) / THREADS);
+  uint32_t key[EACH];  // (0 where there is no candidate: the lowest key, of -inf, is greater)
   auto read = [&](int base) {
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
+    for (int j = 0; j < EACH; ++j) {
       const int i = base + j * THREADS + tid;
       key[j] = i >= end ? 0u : i < p.first || i >= tail ? kForced : key_of(__ldg(src + i));
     }
@@ -158,11 +181,12 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
     for (int base = begin; base < end; base += kRound) {
       if (!one_round) read(base);
 #pragma unroll
-      for (int j = 0; j < kEach; ++j)
-        if (key[j] != 0u && (pass == 0 || ((key[j] ^ thr) >> (shift + 8)) == 0u))
-          atomicAdd(&hist[(key[j] >> shift) & (kBins - 1)], 1);
+      for (int j = 0; j < EACH; ++j) {
+        if (j % 4 == 0 && j >= held) break;
+        const bool agrees = key[j] != 0u && (pass == 0 || ((key[j] ^ thr) >> (shift + 8)) == 0u);
+        count_if(agrees, &hist[(key[j] >> shift) & (kBins - 1)]);
+      }
     }
-    uint32_t digit;
     if (split > 1) {
       cluster.sync();
       for (int i = tid; i < kBins; i += THREADS) {
@@ -170,13 +194,19 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
         for (int o = 0; o < split; ++o) c += *cluster.map_shared_rank(&hist[i], o);
         sm.total[i] = c;
       }
-      __syncthreads();
-      find_digit(sm.total, left, digit);
-      __syncthreads();
-    } else {
-      __syncthreads();
-      find_digit(hist, left, digit);
     }
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t digit;
+      find_digit(split > 1 ? sm.total : hist, left, digit);
+      if (lane == 0) {
+        sm.digit = digit;
+        sm.rest = left;
+      }
+    }
+    __syncthreads();
+    left = sm.rest;
+    const uint32_t digit = sm.digit;
     thr |= digit << shift;
   }
   // left: how many of the keys equal to thr are taken. First, what the CTAs before have.
@@ -186,7 +216,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
     for (int base = begin; base < end; base += kRound) {
       if (!one_round) read(base);
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) {
+      for (int j = 0; j < EACH; ++j) {
         a += key[j] > thr;
         e += key[j] == thr;
       }
@@ -208,68 +238,58 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
   }
   for (int base = begin; base < end; base += kRound) {
     if (!one_round) read(base);
-    unsigned up[kEach], tie[kEach];
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      up[j] = __ballot_sync(kFull, key[j] > thr);
-      tie[j] = __ballot_sync(kFull, key[j] == thr);
-      if (lane == 0) {
-        sm.above[j][warp] = __popc(up[j]);
-        sm.equal[j][warp] = __popc(tie[j]);
-      }
+    for (int j = 0; j < EACH; ++j) {
+      if (j >= held) break;
+      const unsigned up = __ballot_sync(kFull, key[j] > thr), tie = __ballot_sync(kFull, key[j] == thr);
+      if (lane == 0) sm.counts[j * kWarps + warp] = make_int2(__popc(up), __popc(tie));
     }
     __syncthreads();
-    // exclusive sums over (j, warp), kEach * kWarps places, each warp for itself
-    constexpr int kPlaces = kEach * kWarps, kPer = kPlaces / 32;
-    int a[kPer], e[kPer], sa = 0, se = 0;
+    if (warp == 0) {  // exclusive sums over (place, warp)
+      const int places = held * kWarps;
+      int ca = 0, ce = 0;  // of the 32 before
+      for (int i = lane; i < places + lane; i += 32) {
+        const int2 c = i < places ? sm.counts[i] : make_int2(0, 0);
+        int a = c.x, e = c.y;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      a[i] = (&sm.above[0][0])[lane * kPer + i];
-      e[i] = (&sm.equal[0][0])[lane * kPer + i];
-      sa += a[i];
-      se += e[i];
-    }
-    int ca = sa, ce = se;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, ca, o), z = __shfl_up_sync(kFull, ce, o);
-      if (lane >= o) {
-        ca += y;
-        ce += z;
-      }
-    }
-    const int round_above = __shfl_sync(kFull, ca, 31), round_equal = __shfl_sync(kFull, ce, 31);
-    ca -= sa;
-    ce -= se;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      // the sums before place (j, warp): lane (j kWarps + warp) / kPer has them
-      const int place = j * kWarps + warp, from = place / kPer;
-      int x = __shfl_sync(kFull, ca, from), y = __shfl_sync(kFull, ce, from);
-#pragma unroll
-      for (int i = 0; i < kPer - 1; ++i) {
-        const int u = __shfl_sync(kFull, a[i], from), v = __shfl_sync(kFull, e[i], from);
-        if (from * kPer + i < place) {
-          x += u;
-          y += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFull, a, o), z = __shfl_up_sync(kFull, e, o);
+          if (lane >= o) {
+            a += y;
+            e += z;
+          }
         }
+        if (i < places) sm.counts[i] = make_int2(ca + a - c.x, ce + e - c.y);
+        ca += __shfl_sync(kFull, a, 31);
+        ce += __shfl_sync(kFull, e, 31);
       }
-      const unsigned lower = (1u << lane) - 1u;
-      x += above0 + __popc(up[j] & lower);
-      y += equal0 + __popc(tie[j] & lower);
-      const bool is_up = key[j] > thr;
-      if (is_up || (key[j] == thr && y < left)) out[x + min(y, left)] = base + j * THREADS + tid;
+      if (lane == 0) sm.round = make_int2(ca, ce);
     }
-    above0 += round_above;
-    equal0 += round_equal;
-    if (!one_round) __syncthreads();
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+      if (j >= held) break;
+      const bool up = key[j] > thr, tie = key[j] == thr;
+      const unsigned ups = __ballot_sync(kFull, up), ties = __ballot_sync(kFull, tie);
+      if ((ups | ties) == 0u) continue;
+      const int2 c = sm.counts[j * kWarps + warp];
+      const unsigned lower = (1u << lane) - 1u;
+      const int x = above0 + c.x + __popc(ups & lower), y = equal0 + c.y + __popc(ties & lower);
+      if (up || (tie && y < left)) out[x + min(y, left)] = base + j * THREADS + tid;
+    }
+    if (!one_round) {
+      above0 += sm.round.x;
+      equal0 += sm.round.y;
+      __syncthreads();
+    }
   }
 }
 
 pa_status launch_select(SelectParams& p, int64_t rows, cudaStream_t s) {
-  const int threads = p.limit <= 1024 ? 128 : 512;
+  const bool small = p.limit <= 1024;
+  const int threads = small ? 128 : 512, each = 8;
   p.split = 1;
-  while (p.split < 8 && (int64_t)p.split * threads * kEach < p.limit) p.split *= 2;
+  while (p.split < 8 && (int64_t)p.split * threads * each < p.limit) p.split *= 2;
   if (rows * p.split > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   p.err = error_word();
   if (!p.err) return PA_ERR_CUDA;
@@ -283,7 +303,7 @@ pa_status launch_select(SelectParams& p, int64_t rows, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, threads == 128 ? select_kernel<128> : select_kernel<512>, p) !=
+  if (cudaLaunchKernelEx(&cfg, small ? select_kernel<128, 8> : select_kernel<512, 8>, p) !=
       cudaSuccess) {
     cudaGetLastError();
     return PA_ERR_CUDA;
