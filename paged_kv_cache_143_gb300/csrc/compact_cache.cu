@@ -6,7 +6,11 @@
 // the cells kept[0 .. i] have been read: one CTA goes through a request's cells
 // in order, a tile at a time, and reads tile x + 1 into registers before it
 // writes tile x. The CTAs divide what does not depend on each other: requests,
-// K and V, kv heads and, where those are few, the 16-byte pieces of a row.
+// K and V, kv heads and, where those leave SMs idle, the 16-byte pieces of a row
+// (a row's 64 to 256 bytes are what a gather brings at once: halves of them, read by
+// two CTAs at different times, take 57 us where whole rows take 50, for 16 requests cut
+// to 4096 tokens of 8 kv heads, E4M3). Where 1024 cells come from and go to is worked out once for all threads of a row
+// and kept in shared memory, the next 1024 cells' while these are moved.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -14,7 +18,9 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kDeep = 4;  // 16-byte pieces of a thread in flight
+constexpr int kDeep = 8;     // 16-byte pieces of a thread in flight, twice
+constexpr int kBatch = 1024;  // cells whose places are known at once
+constexpr uint32_t kNone = 0xffffffffu;
 
 struct CompactParams {
   uint8_t* k_pool;
@@ -30,22 +36,6 @@ struct CompactParams {
   int max_reqs, max_blocks, dst_blocks, R, k, Hkv, B, num_blocks, row_bytes, split;
   unsigned* err;
 };
-
-// The pool row of cell `n` of a request for a kv head, or -1 (flagged).
-__device__ __forceinline__ int64_t pool_row(const CompactParams& p, const int32_t* table,
-                                            int blocks, int n, int kvh) {
-  const int b = n / p.B;
-  if (n < 0 || b >= blocks) {
-    raise_error(p.err, kErrBounds);
-    return -1;
-  }
-  const int id = __ldg(table + b);
-  if (id < 0 || id >= p.num_blocks) {
-    raise_error(p.err, kErrBounds);
-    return -1;
-  }
-  return ((int64_t)id * p.Hkv + kvh) * p.B + (n - b * p.B);
-}
 
 __global__ void __launch_bounds__(kThreads) compact_kernel(CompactParams p) {
   const int r = blockIdx.y;
@@ -96,38 +86,95 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactParams p) {
   const int step = kThreads / pieces;                 // rows that the CTA moves at once
   const int row = (int)threadIdx.x / pieces;
   const int64_t byte = ((int)threadIdx.x % pieces + part * pieces) * 16;
+  // Places of a batch's cells: pool rows of the kv head (below 2^32: the pool fits the GPU)
+  // from which and to which they move, kNone where there is nothing to do.
+  __shared__ uint32_t from[2][kBatch], to[2][kBatch];
+  constexpr int kMine = kBatch / kThreads;  // cells whose places a thread works out
+  int place[kMine], id[2][kMine];
+  auto fetch_kept = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int i = base + u * kThreads + (int)threadIdx.x;
+      place[u] = i < n ? __ldg(kept + i) : 0;
+    }
+  };
+  auto fetch_ids = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int i = base + u * kThreads + (int)threadIdx.x;
+      const int a = place[u] / p.B, b = i / p.B;
+      id[0][u] = i < n && place[u] >= 0 && a < p.max_blocks ? __ldg(src + a) : -1;
+      id[1][u] = i < n && b < p.dst_blocks ? __ldg(dst + b) : -1;
+    }
+  };
+  auto settle = [&](int base, int turn) {
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int at = u * kThreads + (int)threadIdx.x, i = base + at;
+      uint32_t a = kNone, b = kNone;
+      if (id[0][u] >= 0 && id[0][u] < p.num_blocks && id[1][u] >= 0 && id[1][u] < p.num_blocks) {
+        a = (uint32_t)(((int64_t)id[0][u] * p.Hkv + kvh) * p.B + place[u] % p.B);
+        b = (uint32_t)(((int64_t)id[1][u] * p.Hkv + kvh) * p.B + i % p.B);
+        if (a == b) a = b = kNone;  // it stays where it is
+      } else if (i < n) {
+        raise_error(p.err, kErrBounds);
+      }
+      from[turn][at] = a;
+      to[turn][at] = b;
+    }
+  };
+  fetch_kept(0);
+  fetch_ids(0);
+  settle(0, 0);
+  __syncthreads();
   uint4 v[2][kDeep];
-  int64_t to[2][kDeep];
-  auto read = [&](int base, uint4 (&x)[kDeep], int64_t (&w)[kDeep]) {
-    int64_t from[kDeep];
+  const int tile = step * kDeep;  // divides kBatch: both are powers of two
+  auto read = [&](int base, uint4 (&x)[kDeep]) {
+    if (base >= n) return;
+    const uint32_t* f = from[(base / kBatch) & 1] + base % kBatch;
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
-      const int i = base + u * step + row;
-      from[u] = w[u] = -1;
-      if (i < n) {
-        from[u] = pool_row(p, src, p.max_blocks, __ldg(kept + i), kvh);
-        w[u] = pool_row(p, dst, p.dst_blocks, i, kvh);
-        if (from[u] < 0 || from[u] == w[u]) w[u] = -1;  // nothing to do
+      const uint32_t a = f[u * step + row];
+      if (a != kNone) x[u] = *reinterpret_cast<const uint4*>(pool + (int64_t)a * p.row_bytes + byte);
+    }
+  };
+  auto write = [&](int base, const uint4 (&x)[kDeep]) {
+    if (base >= n) return;
+    const uint32_t* t = to[(base / kBatch) & 1] + base % kBatch;
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const uint32_t b = t[u * step + row];
+      if (b != kNone) *reinterpret_cast<uint4*>(pool + (int64_t)b * p.row_bytes + byte) = x[u];
+    }
+  };
+  read(0, v[0]);
+  fetch_kept(kBatch);
+  // One tile a turn: the next one is read, then, when all threads have read theirs, this
+  // one written. In the first turn of a batch the next batch's places are worked out, in
+  // the halves of `from` and `to` that the batch before used, which is all written: after
+  // this turn's barrier, or where a batch has no third turn before they are read, ahead of it.
+  const bool early = 2 * tile >= kBatch;
+  auto turn = [&](int base, uint4 (&mine)[kDeep], uint4 (&other)[kDeep]) {
+    const bool opens = base % kBatch == 0;
+    if (opens) {
+      fetch_ids(base + kBatch);
+      if (early) {
+        __syncthreads();
+        settle(base + kBatch, (base / kBatch + 1) & 1);
+        __syncthreads();
       }
     }
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u)
-      if (w[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(pool + from[u] * p.row_bytes + byte);
-  };
-  auto write = [&](const uint4 (&x)[kDeep], const int64_t (&w)[kDeep]) {
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u)
-      if (w[u] >= 0) *reinterpret_cast<uint4*>(pool + w[u] * p.row_bytes + byte) = x[u];
-  };
-  const int tile = step * kDeep;
-  read(0, v[0], to[0]);
-  for (int base = 0; base < n; base += 2 * tile) {
-    read(base + tile, v[1], to[1]);
-    __syncthreads();  // what tile `base` overwrites has been read
-    write(v[0], to[0]);
-    read(base + 2 * tile, v[0], to[0]);
+    read(base + tile, other);
     __syncthreads();
-    write(v[1], to[1]);
+    write(base, mine);
+    if (opens) {
+      if (!early) settle(base + kBatch, (base / kBatch + 1) & 1);
+      fetch_kept(base + 2 * kBatch);
+    }
+  };
+  for (int base = 0; base < n; base += 2 * tile) {
+    turn(base, v[0], v[1]);
+    if (base + tile < n) turn(base + tile, v[1], v[0]);
   }
 }
 
@@ -151,7 +198,9 @@ extern "C" pa_status pa_compact_cache(const pa_kv_pool* pool, const int32_t* src
   if (!src_tables || !dst_tables || !kept || !kept_lens ||
       (reinterpret_cast<uintptr_t>(mass_in) & 3u) || (reinterpret_cast<uintptr_t>(mass_out) & 3u))
     return PA_ERR_INVALID;
-  if (num_reqs > 65535) return PA_ERR_UNSUPPORTED;
+  if (num_reqs > 65535 ||
+      (int64_t)pool->num_blocks * pool->num_kv_heads * pool->block_size >= 0xffffffffll)
+    return PA_ERR_UNSUPPORTED;
   CompactParams p{};
   p.k_pool = static_cast<uint8_t*>(pool->k_pool);
   p.v_pool = static_cast<uint8_t*>(pool->v_pool);
@@ -174,10 +223,9 @@ extern "C" pa_status pa_compact_cache(const pa_kv_pool* pool, const int32_t* src
   p.row_bytes = pool->head_dim * (pool->dtype == PA_KV_BF16 ? 2 : 1);
   p.err = error_word();
   if (!p.err) return PA_ERR_CUDA;
-  // rows in 32-byte pieces (a sector) at the least, while two CTAs do not fill each SM
+  // rows in 32-byte pieces (a sector) at the least, while SMs are idle
   p.split = 1;
-  while ((int64_t)num_reqs * p.Hkv * 2 * p.split < 2 * num_sms() && p.row_bytes / p.split > 32)
-    p.split *= 2;
+  while ((int64_t)num_reqs * p.Hkv * 2 * p.split < num_sms() && p.row_bytes / p.split > 32) p.split *= 2;
   const dim3 grid((unsigned)(p.Hkv * 2 * p.split + 1), (unsigned)num_reqs);
   compact_kernel<<<grid, kThreads, 0, as_stream(stream)>>>(p);
   return launch_status();
