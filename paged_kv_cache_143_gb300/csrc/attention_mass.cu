@@ -591,21 +591,24 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     constexpr int kCols = F8 ? 1 : D / 64;  // boxes across a key row
     const int32_t* table = p.tables + (int64_t)r * p.max_blocks;
     const int per_tile = kTile / p.B;
-    auto load_keys = [&](uint8_t* dst, int k0, int kvh, uint64_t* bar) {
-      const int blk = lane / kCols, col = lane % kCols;
-      const int lb = k0 / p.B + blk;
-      bool on = blk < per_tile && (int64_t)lb * p.B < m.seq;
-      int id = on ? __ldg(table + lb) : 0;
+    constexpr int kBoxRow = F8 ? D : 128;
+    // the block that this lane brings of the tile at key k0, -1 past the keys
+    const int my_blk = lane / kCols, my_col = lane % kCols;
+    auto block_at = [&](int64_t k0) {
+      const int64_t lb = k0 / p.B + my_blk;
+      return my_blk < per_tile && lb * p.B < m.seq ? __ldg(table + lb) : -1;
+    };
+    auto load_keys = [&](uint8_t* dst, int64_t k0, int id, int kvh, uint64_t* bar) {
+      bool on = my_blk < per_tile && (k0 / p.B + my_blk) * p.B < m.seq;
       if (on && (id < 0 || id >= p.num_blocks)) {
         raise_error(p.err, kErrBounds);
         on = false;
       }
       const unsigned boxes = __popc(__ballot_sync(kFull, on));
-      constexpr int kBoxRow = F8 ? D : 128;
       if (lane == 0) mbar_arrive_expect_tx(bar, boxes * (unsigned)(p.B * kBoxRow));
       __syncwarp();
       if (on)
-        tc::tma_load_3d(dst + col * W::kHalf + blk * p.B * kBoxRow, &tmap_k, col * 64,
+        tc::tma_load_3d(dst + my_col * W::kHalf + my_blk * p.B * kBoxRow, &tmap_k, my_col * 64,
                         kvh * p.B, id, bar);
     };
     auto image_of = [&](int tile, int kvh) {
@@ -619,25 +622,27 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     };
     int i = 0, fixed_loads = 0;
     bool ok = true;
+    int id = block_at(key0);  // of the next key tile (WEIGHTS: the only one)
+    int kvh = kvh0, ti = ti0, st = 0;
+    unsigned st_phase = 1;  // of the stage's empty barrier, once all have been filled
+    if (!WEIGHTS) {
+      copy(fixed, image_of(tile0, kvh0), W::kImage, &t->fixed_full[0]);
+      fixed_loads = 1;
+    }
     for (; i < n_steps && ok; ++i) {
-      const int st = i % kStages;
-      if (WEIGHTS ? i % n_tiles == 0 : i == 0) {
+      if (WEIGHTS && ti == ti0) {
         const int slot = fixed_loads & 1;
         if (fixed_loads > 1) ok = __all_sync(kFull, wait(&t->fixed_empty[slot], (fixed_loads / 2 - 1) & 1));
         if (!ok) break;
-        if (WEIGHTS)
-          load_keys(fixed + slot * S::kFixed, key0, kvh0 + i / n_tiles * kvh_step, &t->fixed_full[slot]);
-        else
-          copy(fixed, image_of(tile0, kvh0), W::kImage, &t->fixed_full[0]);
+        load_keys(fixed + slot * S::kFixed, key0, id, kvh, &t->fixed_full[slot]);
         ++fixed_loads;
       }
-      if (i >= kStages) ok = __all_sync(kFull, wait(&t->empty[st], (i / kStages - 1) & 1));
+      if (i >= kStages) ok = __all_sync(kFull, wait(&t->empty[st], st_phase));
       if (!ok) break;
       uint8_t* dst = stream + st * S::kStage;
       if (WEIGHTS) {
         constexpr int kParts = kTile / S::kRows;  // steps of an image
-        const int ti = ti0 + i % n_tiles;
-        const uint8_t* image = image_of(tile0 + ti / kParts, kvh0 + i / n_tiles * kvh_step);
+        const uint8_t* image = image_of(tile0 + ti / kParts, kvh);
         if constexpr (kParts == 1) {
           copy(dst, image, W::kTileBytes, &t->full[st]);
         } else if (lane == 0) {  // its rows of both halves
@@ -651,8 +656,19 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         static_assert(kStages + 2 <= 8, "the ring of row factors");
         copy(infos + (i & 7) * kInfoBytes, image + W::kTileBytes + ti % kParts * S::kRows * 8,
              S::kRows * 8, &t->info_full[i & 7]);
+        if (++ti == ti0 + n_tiles) {
+          ti = ti0;
+          kvh += kvh_step;
+        }
       } else {
-        load_keys(dst, key0 + i * kTile, kvh0, &t->full[st]);
+        const int64_t k0 = (int64_t)key0 + i * kTile;
+        const int next = i + 1 < n_steps ? block_at(k0 + kTile) : -1;
+        load_keys(dst, k0, id, kvh0, &t->full[st]);
+        id = next;
+      }
+      if (++st == kStages) {
+        st = 0;
+        st_phase ^= 1;
       }
     }
     if (!ok) {  // what is in flight lands before the CTA ends
@@ -669,15 +685,19 @@ __global__ void __launch_bounds__(kWideThreads, 2)
       constexpr uint32_t idesc =
           F8 ? tc::idesc_e4m3_f32(kTile, S::kRows)
              : tc::idesc_16bit_f32(kTile, S::kRows, false, false, false);
-      int heads = 0;
+      int heads = 0, left = 0, st = -1;  // left: steps with the tile that stays
+      unsigned st_phase = 1;
       for (int i = 0; i < n_steps; ++i) {
-        const int st = i % kStages, buf = i & 1;
-        if (WEIGHTS ? i % n_tiles == 0 : i == 0) {
+        const int buf = i & 1;
+        st = st + 1 == kStages ? 0 : st + 1;
+        if (st == 0) st_phase ^= 1;
+        if (left == 0) {
+          left = WEIGHTS ? n_tiles : n_steps;
           if (!wait(&t->fixed_full[heads & 1], (heads / 2) & 1)) break;
           ++heads;
         }
         const int slot = (heads - 1) & 1;
-        if (!wait(&t->full[st], (i / kStages) & 1)) break;
+        if (!wait(&t->full[st], st_phase)) break;
         if (i >= 2 && !wait(&t->s_empty[buf], ((i >> 1) - 1) & 1)) break;
         tc::fence_after_sync();
         const uint64_t a0 = operand_desc<W::kRowSpan>(fixed + slot * S::kFixed);
@@ -700,7 +720,7 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         }
         tc::mma_commit(&t->empty[st]);
         tc::mma_commit(&t->s_full[buf]);
-        if (WEIGHTS && (i + 1) % n_tiles == 0) tc::mma_commit(&t->fixed_empty[slot]);
+        if (--left == 0 && WEIGHTS) tc::mma_commit(&t->fixed_empty[slot]);
       }
     }
     __syncwarp();
@@ -721,6 +741,8 @@ __global__ void __launch_bounds__(kWideThreads, 2)
     const int me4 = (warp & 3) * 32 + (lane >> 2), col2 = lane & 3;
     float sum[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
     const int buf = warp >> 2;
+    int ti = ti0 + buf;  // WEIGHTS: the step's row tile
+    while (WEIGHTS && ti >= ti0 + n_tiles) ti -= n_tiles;
     for (int i = buf; i < n_steps; i += 2) {
       if (!__all_sync(kFull, (!WEIGHTS || wait(&t->info_full[i & 7], (i >> 3) & 1)) &&
                                  wait(&t->s_full[buf], (i >> 1) & 1)))
@@ -775,7 +797,9 @@ __global__ void __launch_bounds__(kWideThreads, 2)
         }
       } else {
         const float4* info = reinterpret_cast<const float4*>(infos + (i & 7) * kInfoBytes);
-        const int row0 = (ti0 + i % n_tiles) * S::kRows;
+        const int row0 = ti * S::kRows;
+        ti += 2;
+        while (ti >= ti0 + n_tiles) ti -= n_tiles;
         const int rows = min(S::kRows, m.rows - row0);
         // rows from which on the warp's last key is seen (0 and below: all keys by all rows)
         const int after = key0 + (warp & 3) * 32 + 31 - (m.seq - m.w);
