@@ -27,7 +27,6 @@
 // that bf16 has) after a power-of-two scale that puts its row's largest magnitude
 // into [2^7, 2^8): exact for elements down to 2^-8 of that one, off by 2^-18 of it
 // below.
-#include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
 #include <utility>
@@ -38,8 +37,6 @@
 
 namespace pa {
 namespace {
-
-namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNarrowRows = 16;     // rows of the streaming form, at the most
@@ -67,12 +64,16 @@ struct MassParams {
   float2* split_stats;     // [R][Hkv][16][splits] (maximum, sum)
   int splits;
   int narrow_rows;         // rows of a request of this form, at the most
-  // tcgen05 form
-  int4* tile_of;           // [n_tiles] (request or -1, row tile, keys, counted queries)
+  // tcgen05 form: a step is a row tile of a kv head and a key tile; request r's are the
+  // flat steps first_step[r] + (kvh * tiles + row tile) * key tiles + key tile
+  int4* tile_of;           // [n_tiles] (request or -1, row tile, the request's row and key tiles)
   int* first_tile;         // [R], -1: not of this form
+  int64_t* first_step;     // [R + 1]
   uint8_t* images;         // [n_tiles][Hkv][image]
-  float2* tile_stats;      // [n_tiles][Hkv][parts][128]
-  int n_tiles, parts, part_keys;
+  float2* tile_stats;      // [n_tiles][Hkv][pieces][4][128]
+  float* sums;             // [steps][128]: a step's weights, key by key
+  int64_t steps, per_cta;  // in all, and of a CTA
+  int n_tiles, pieces;
   int key_tiles;           // key tiles of the longest request
   unsigned* err;
 };
@@ -341,6 +342,10 @@ __device__ __forceinline__ int tiles_of(const MassReq& m) {
   return m.rows > kNarrowRows ? (m.rows + kTile - 1) / kTile : 0;
 }
 
+__device__ __forceinline__ int64_t steps_of(const MassParams& p, const MassReq& m) {
+  return (int64_t)tiles_of(m) * p.Hkv * ((m.seq + kTile - 1) / kTile);
+}
+
 // 16-byte piece c of row `row` in swizzled rows of SPAN (128 or 64) bytes.
 template <int SPAN>
 __device__ __forceinline__ int swizzled(int row, int c) {
@@ -357,30 +362,37 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
   const bool reporter = tid == 0 && ti == 0 && kvh == 0;
   const int tiles = tiles_of(m);
   if (reporter && (bad_request(m) || (m.rows > 0 && !tiles && !p.scores))) raise_error(p.err, kErrBounds);
-  if (r == p.R - 1 && ti == 0 && kvh == 0) {  // entries past the device's rows
-    const int64_t end = before(p, r, [](const MassReq& x) -> int64_t { return tiles_of(x); }) + tiles;
-    for (int64_t x = end + tid; x < p.n_tiles; x += kTile) p.tile_of[x] = make_int4(-1, 0, 0, 0);
+  const int64_t first = before(p, r, [](const MassReq& x) -> int64_t { return tiles_of(x); });
+  if (ti == 0 && kvh == 0) {
+    const int64_t step = before(p, r, [&](const MassReq& x) { return steps_of(p, x); });
+    if (tid == 0) p.first_step[r] = step;
+    if (r == p.R - 1) {  // the end, and entries past the device's rows
+      if (tid == 0) p.first_step[p.R] = step + steps_of(p, m);
+      for (int64_t x = first + tiles + tid; x < p.n_tiles; x += kTile)
+        p.tile_of[x] = make_int4(-1, 0, 0, 0);
+    }
   }
   if (!tiles) {
     if (reporter) p.first_tile[r] = -1;
     return;
   }
   if (ti >= tiles) return;
-  const int64_t first = before(p, r, [](const MassReq& x) -> int64_t { return tiles_of(x); });
-  const bool fits = first + tiles <= p.n_tiles && tiles <= (int)gridDim.x &&
-                    (m.seq + kTile - 1) / kTile <= p.key_tiles &&
-                    m.seq <= (int64_t)p.parts * p.part_keys && mass_row(p, r) >= 0;
-  if (reporter) {
-    p.first_tile[r] = fits ? (int)first : -1;
-    if (!fits) raise_error(p.err, kErrBounds);
-  }
-  if (tid == 0 && kvh == 0) {
-    if (first + ti < p.n_tiles) p.tile_of[first + ti] = make_int4(fits ? r : -1, ti, m.seq, m.w);
-    // (no CTA comes to tiles past the grid's)
-    if (ti == 0)
+  const int key_tiles = (m.seq + kTile - 1) / kTile;
+  bool fits = first + tiles <= p.n_tiles && tiles <= (int)gridDim.x && key_tiles <= p.key_tiles &&
+              mass_row(p, r) >= 0;
+  if (ti == 0 && kvh == 0) {
+    const int64_t step = before(p, r, [&](const MassReq& x) { return steps_of(p, x); });
+    fits = fits && step + steps_of(p, m) <= p.steps;
+    if (tid == 0) {
+      p.first_tile[r] = fits ? (int)first : -1;
+      if (!fits) raise_error(p.err, kErrBounds);
+      // (no CTA comes to tiles past the grid's)
       for (int64_t x = first + gridDim.x; x < first + tiles && x < p.n_tiles; ++x)
         p.tile_of[x] = make_int4(-1, 0, 0, 0);
+    }
   }
+  if (tid == 0 && kvh == 0 && first + ti < p.n_tiles)
+    p.tile_of[first + ti] = make_int4(fits ? r : -1, ti, tiles, key_tiles);
   if (!fits) return;
   const int tile = (int)first + ti;
   uint8_t* image = p.images + ((int64_t)tile * p.Hkv + kvh) * W::kImage;
@@ -448,42 +460,34 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
   reinterpret_cast<float*>(image + W::kTileBytes)[info_at(tid)] = sc;
 }
 
+// Warps 0-15: rows or keys, each group of four the accumulators of every fourth step;
+// 16: copies; 17: MMAs.
+constexpr int kGroups = 4;
+constexpr int kCopyWarp = 4 * kGroups, kMmaWarp = kCopyWarp + 1;
+constexpr int kWideThreads = 32 * (kMmaWarp + 1);
+constexpr uint32_t kWideCols = kGroups * kTile;  // all of tensor memory
+constexpr int kMaxKeyStages = 10;
+
 struct WideTail {
-  uint64_t fixed_full[2], fixed_empty[2];
-  uint64_t full[4], empty[4];      // stages of the streamed operand
-  uint64_t info_full[8];           // WEIGHTS: what is behind a step's image
-  uint64_t s_full[2], s_empty[2];  // accumulators
+  uint64_t image_full[2], image_empty[2];
+  uint64_t full[kMaxKeyStages], empty[kMaxKeyStages];
+  uint64_t s_full[kGroups], s_empty[kGroups];
   uint32_t tmem;
   int abort;
-  float part[2][kTile];            // results of the warpgroups, for each other and the cluster
 };
 
-// Warps 0-3 and 4-7: rows or keys, each group of four the accumulators of one stage
-// (every other step); 8: copies; 9: MMAs.
-constexpr int kWideThreads = 320;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
-constexpr uint32_t kWideCols = 2 * kTile;
-
-// Shared memory of a CTA, two of which run on an SM: the tile that stays (WEIGHTS: two
-// slots, the next kv head's keys arrive while this one's are multiplied), as many stages
-// of the stream as there is room for (a stage is free again as soon as its MMAs are
-// done), and a ring of eight steps' row factors. Two slots of 128 bf16 keys of 128 dims
-// leave room for 64 query rows a stage.
-template <int D, bool F8, bool WEIGHTS>
+// Shared memory of a CTA, one on an SM: two images, and as many stages of 128 keys as
+// there is room for.
+template <int D, bool F8>
 struct WideSmem {
   using W = WideGeo<D, F8>;
-  static constexpr int kRows = WEIGHTS && !F8 && D == 128 ? 64 : kTile;  // columns of a step
-  static constexpr int kKeys = kTile * D * (F8 ? 1 : 2);
-  static constexpr int kSlots = WEIGHTS ? 2 : 1;
-  static constexpr int kFixed = WEIGHTS ? kKeys : W::kImage;
-  static constexpr int kStage = WEIGHTS ? kRows * D * 2 : kKeys;
-  static constexpr int kRoom = (108 << 10) - kSlots * kFixed - 8 * kInfoBytes;
-  static constexpr int kStages = kRoom / kStage > 4 ? 4 : kRoom / kStage;
-  static constexpr int kOffStream = kSlots * kFixed;
-  static constexpr int kOffInfo = kOffStream + kStages * kStage;
-  static constexpr int kOffTail = kOffInfo + 8 * kInfoBytes;
+  static constexpr int kStage = kTile * D * (F8 ? 1 : 2);
+  static constexpr int kRoom = 232448 - 1024 - (int)sizeof(WideTail) - 2 * W::kImage;
+  static constexpr int kStages = kRoom / kStage > kMaxKeyStages ? kMaxKeyStages : kRoom / kStage;
+  static constexpr int kOffKeys = 2 * W::kImage;
+  static constexpr int kOffTail = kOffKeys + kStages * kStage;
   static constexpr size_t kAlloc = 1024 + kOffTail + sizeof(WideTail);
-  static_assert(kStages >= 2 && kFixed % 1024 == 0 && kStage % 1024 == 0,
+  static_assert(kStages >= 3 && W::kImage % 1024 == 0 && kStage % 1024 == 0 && kAlloc <= 232448,
                 "swizzled tiles start on 1024-byte boundaries");
 };
 
@@ -495,83 +499,75 @@ __device__ __forceinline__ uint64_t operand_desc(const void* smem) {
   return d;
 }
 
-// WEIGHTS false: the statistics of a row tile over one part of the keys (the row
-// tile stays in shared memory, the key tiles stream). WEIGHTS true: the mass of a
-// key tile (a kv head's keys stay, its row tiles stream), the kv heads shared by
-// the CTAs of a cluster. Both multiply the tile that stays (A, the lanes) with
-// each tile of the stream (B, the columns).
+// The part of a CTA's steps that one row tile of a kv head has, from flat step f on.
+struct Segment {
+  bool on;         // (false: of a request that was left out; nothing to do up to `next`)
+  int tile, ti, kvh;
+  int key_tile, n;  // first key tile, and how many
+  int piece;        // of the row tile's pieces
+  int64_t next;
+  MassReq m;
+  int r;
+};
+__device__ __forceinline__ Segment segment_at(const MassParams& p, int64_t f, int64_t end) {
+  Segment s;
+  s.r = warp_last_le(p.R, f, [&](int x) { return p.first_step[x]; });
+  const int64_t base = p.first_step[s.r], over = p.first_step[s.r + 1];
+  s.m = rows_of(p, s.r);
+  s.tile = p.first_tile[s.r];
+  const int tiles = tiles_of(s.m), keys = (s.m.seq + kTile - 1) / kTile;
+  s.on = s.tile >= 0 && tiles > 0;
+  s.next = min(end, over);
+  if (s.next <= f) s.next = end;  // (cannot be: f lies within the request)
+  if (!s.on) return s;
+  const int64_t unit = (f - base) / keys, start = base + unit * keys;
+  s.kvh = (int)(unit / tiles);
+  s.ti = (int)(unit - (int64_t)s.kvh * tiles);
+  s.tile += s.ti;
+  s.key_tile = (int)(f - start);
+  s.n = (int)min((int64_t)keys - s.key_tile, end - f);
+  s.piece = (int)(f / p.per_cta - start / p.per_cta);
+  s.next = f + s.n;
+  return s;
+}
+
+// One CTA per SM on an equal run of the call's steps. WEIGHTS false: each row tile's
+// statistics over the keys of the run (A, the lanes: query rows; B, the columns: keys).
+// WEIGHTS true: of each step the weights summed over the tile's rows, key by key (A: keys;
+// B: rows). A row tile's image stays in shared memory while its key tiles stream; the
+// next tile's arrives meanwhile, and nothing drains between them.
 template <int D, bool F8, bool WEIGHTS>
-__global__ void __launch_bounds__(kWideThreads, 2)
+__global__ void __launch_bounds__(kWideThreads, 1)
     mass_tile_kernel(const __grid_constant__ CUtensorMap tmap_k, MassParams p) {
   using W = WideGeo<D, F8>;
-  using S = WideSmem<D, F8, WEIGHTS>;
+  using S = WideSmem<D, F8>;
   constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* fixed = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* stream = fixed + S::kOffStream;
-  uint8_t* infos = fixed + S::kOffInfo;
-  WideTail* t = reinterpret_cast<WideTail*>(fixed + S::kOffTail);
+  uint8_t* images = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* keys = images + S::kOffKeys;
+  WideTail* t = reinterpret_cast<WideTail*>(images + S::kOffTail);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  launch_dependents();
-  grid_dependency_wait();  // the images (and, for WEIGHTS, the rows' lse) are complete
-  int r, tile0, n_steps, key0, n_tiles = 1, ti0 = 0, kvh0, kvh_step = 1;
-  MassReq m;
-  if (!WEIGHTS) {
-    const int tile = blockIdx.x / p.Hkv;
-    kvh0 = blockIdx.x - tile * p.Hkv;
-    const int4 who = p.tile_of[tile];
-    if (who.x < 0) return;
-    r = who.x;
-    m.q0 = m.q_len = 0;  // (not needed here)
-    m.seq = who.z;
-    m.w = who.w;
-    m.rows = m.w * p.g;
-    tile0 = tile;
-    ti0 = who.y;
-    key0 = blockIdx.y * p.part_keys;
-    // the keys that the tile's last row sees
-    const int last = min(m.rows - 1, ti0 * kTile + kTile - 1) / p.g;
-    const int end = min(m.seq - m.w + last + 1, key0 + p.part_keys);
-    n_steps = max(0, (end - key0 + kTile - 1) / kTile);
-    if (n_steps == 0) {
-      if (tid < kTile)
-        p.tile_stats[(((int64_t)tile0 * p.Hkv + kvh0) * p.parts + blockIdx.y) * kTile + tid] =
-            make_float2(-INFINITY, 0.f);
-      return;
-    }
-  } else {
-    r = blockIdx.y;
-    tile0 = p.first_tile[r];
-    if (tile0 < 0) return;
-    m = rows_of(p, r);
-    key0 = blockIdx.x * kTile;
-    if (key0 >= m.seq) return;
-    // row tiles whose last query comes before the tile's first key add nothing
-    ti0 = (int)((int64_t)max(0, key0 - (m.seq - m.w)) * p.g / S::kRows);
-    n_tiles = (m.rows + S::kRows - 1) / S::kRows - ti0;
-    kvh0 = blockIdx.z;
-    kvh_step = gridDim.z;
-    n_steps = kvh0 < p.Hkv ? ((p.Hkv - kvh0 + kvh_step - 1) / kvh_step) * n_tiles : 0;
-  }
-
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&t->fixed_full[i], 1);
-      mbar_init(&t->fixed_empty[i], 1);
+      mbar_init(&t->image_full[i], 1);
+      mbar_init(&t->image_empty[i], 1 + 4 * kGroups);  // the MMAs, and the warps that read its factors
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&t->full[i], 1);
       mbar_init(&t->empty[i], 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&t->info_full[i], 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&t->s_full[i], 1);
       mbar_init(&t->s_empty[i], 4);
     }
     t->abort = 0;
     fence_mbar_init();
   }
+  launch_dependents();
+  grid_dependency_wait();  // the images (and, for WEIGHTS, the rows' lse) are complete
+  const int64_t begin = (int64_t)blockIdx.x * p.per_cta;
+  const int64_t end = min(min(begin + p.per_cta, p.first_step[p.R]), p.steps);
+  if (begin >= end) return;
   if (warp == kMmaWarp) {
     tc::tmem_alloc(&t->tmem, kWideCols);
     tc::tmem_relinquish();
@@ -580,347 +576,321 @@ __global__ void __launch_bounds__(kWideThreads, 2)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = t->tmem;
-  auto wait = [&](uint64_t* bar, unsigned parity) {
-    const bool ok = mbar_wait_quiet(bar, parity, &t->abort, p.err);
+  auto wait = [&](uint64_t* bar, unsigned parity) {  // the whole warp
+    const bool ok = __all_sync(kFull, mbar_wait_quiet(bar, parity, &t->abort, p.err));
     if (!ok) *static_cast<volatile int*>(&t->abort) = 1;
     return ok;
   };
-  float total = 0.f, ref = -INFINITY;
+
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------- copies
     constexpr int kCols = F8 ? 1 : D / 64;  // boxes across a key row
-    const int32_t* table = p.tables + (int64_t)r * p.max_blocks;
-    const int per_tile = kTile / p.B;
     constexpr int kBoxRow = F8 ? D : 128;
-    // the block that this lane brings of the tile at key k0, -1 past the keys
-    const int my_blk = lane / kCols, my_col = lane % kCols;
-    auto block_at = [&](int64_t k0) {
-      const int64_t lb = k0 / p.B + my_blk;
-      return my_blk < per_tile && lb * p.B < m.seq ? __ldg(table + lb) : -1;
-    };
-    auto load_keys = [&](uint8_t* dst, int64_t k0, int id, int kvh, uint64_t* bar) {
-      bool on = my_blk < per_tile && (k0 / p.B + my_blk) * p.B < m.seq;
-      if (on && (id < 0 || id >= p.num_blocks)) {
-        raise_error(p.err, kErrBounds);
-        on = false;
-      }
-      const unsigned boxes = __popc(__ballot_sync(kFull, on));
-      if (lane == 0) mbar_arrive_expect_tx(bar, boxes * (unsigned)(p.B * kBoxRow));
-      __syncwarp();
-      if (on)
-        tc::tma_load_3d(dst + my_col * W::kHalf + my_blk * p.B * kBoxRow, &tmap_k, my_col * 64,
-                        kvh * p.B, id, bar);
-    };
-    auto image_of = [&](int tile, int kvh) {
-      return p.images + ((int64_t)tile * p.Hkv + kvh) * W::kImage;
-    };
-    auto copy = [&](void* dst, const uint8_t* src, unsigned bytes, uint64_t* bar) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, bytes);
-        bulk_g2s(dst, src, bytes, bar);
-      }
-    };
-    int i = 0, fixed_loads = 0;
+    const int per_tile = kTile / p.B;
+    const int my_blk = lane / kCols, my_col = lane % kCols;  // what this lane brings of a tile
+    int st = 0, segments = 0;
+    unsigned phase = 1;  // of a stage's empty barrier, once all have been filled
+    int64_t issued = 0;
     bool ok = true;
-    int id = block_at(key0);  // of the next key tile (WEIGHTS: the only one)
-    int kvh = kvh0, ti = ti0, st = 0;
-    unsigned st_phase = 1;  // of the stage's empty barrier, once all have been filled
-    if (!WEIGHTS) {
-      copy(fixed, image_of(tile0, kvh0), W::kImage, &t->fixed_full[0]);
-      fixed_loads = 1;
-    }
-    for (; i < n_steps && ok; ++i) {
-      if (WEIGHTS && ti == ti0) {
-        const int slot = fixed_loads & 1;
-        if (fixed_loads > 1) ok = __all_sync(kFull, wait(&t->fixed_empty[slot], (fixed_loads / 2 - 1) & 1));
-        if (!ok) break;
-        load_keys(fixed + slot * S::kFixed, key0, id, kvh, &t->fixed_full[slot]);
-        ++fixed_loads;
-      }
-      if (i >= kStages) ok = __all_sync(kFull, wait(&t->empty[st], st_phase));
+    for (int64_t f = begin; f < end && ok;) {
+      const Segment s = segment_at(p, f, end);
+      f = s.next;
+      if (!s.on) continue;
+      const int32_t* table = p.tables + (int64_t)s.r * p.max_blocks;
+      auto block_at = [&](int key_tile) {
+        const int64_t lb = (int64_t)key_tile * per_tile + my_blk;
+        return my_blk < per_tile && lb * p.B < s.m.seq ? __ldg(table + lb) : -1;
+      };
+      int id = block_at(s.key_tile);
+      const int slot = segments & 1;
+      if (segments > 1) ok = wait(&t->image_empty[slot], (segments / 2 - 1) & 1);
       if (!ok) break;
-      uint8_t* dst = stream + st * S::kStage;
-      if (WEIGHTS) {
-        constexpr int kParts = kTile / S::kRows;  // steps of an image
-        const uint8_t* image = image_of(tile0 + ti / kParts, kvh);
-        if constexpr (kParts == 1) {
-          copy(dst, image, W::kTileBytes, &t->full[st]);
-        } else if (lane == 0) {  // its rows of both halves
-          constexpr int kPiece = S::kRows * 128;
-          mbar_arrive_expect_tx(&t->full[st], 2 * kPiece);
-          for (int h = 0; h < 2; ++h)
-            bulk_g2s(dst + h * kPiece, image + h * W::kHalf + ti % kParts * kPiece, kPiece, &t->full[st]);
-        }
-        // Slot i mod 8 has been read: the stage is free since step i - kStages' MMAs are done,
-        // and those waited until step i - kStages - 2, of the same accumulator, had been read.
-        static_assert(kStages + 2 <= 8, "the ring of row factors");
-        copy(infos + (i & 7) * kInfoBytes, image + W::kTileBytes + ti % kParts * S::kRows * 8,
-             S::kRows * 8, &t->info_full[i & 7]);
-        if (++ti == ti0 + n_tiles) {
-          ti = ti0;
-          kvh += kvh_step;
-        }
-      } else {
-        const int64_t k0 = (int64_t)key0 + i * kTile;
-        const int next = i + 1 < n_steps ? block_at(k0 + kTile) : -1;
-        load_keys(dst, k0, id, kvh0, &t->full[st]);
-        id = next;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&t->image_full[slot], W::kImage);
+        bulk_g2s(images + slot * W::kImage, p.images + ((int64_t)s.tile * p.Hkv + s.kvh) * W::kImage,
+                 W::kImage, &t->image_full[slot]);
       }
-      if (++st == kStages) {
-        st = 0;
-        st_phase ^= 1;
+      ++segments;
+      for (int k = 0; k < s.n; ++k) {
+        const int next = k + 1 < s.n ? block_at(s.key_tile + k + 1) : -1;
+        if (issued >= kStages) ok = wait(&t->empty[st], phase);
+        if (!ok) break;
+        const int64_t lb = (int64_t)(s.key_tile + k) * per_tile + my_blk;
+        bool on = my_blk < per_tile && lb * p.B < s.m.seq;
+        if (on && (id < 0 || id >= p.num_blocks)) {
+          raise_error(p.err, kErrBounds);
+          on = false;
+        }
+        const unsigned boxes = __popc(__ballot_sync(kFull, on));
+        if (lane == 0) mbar_arrive_expect_tx(&t->full[st], boxes * (unsigned)(p.B * kBoxRow));
+        __syncwarp();
+        if (on)
+          tc::tma_load_3d(keys + st * S::kStage + my_col * W::kHalf + my_blk * p.B * kBoxRow, &tmap_k,
+                          my_col * 64, s.kvh * p.B, id, &t->full[st]);
+        id = next;
+        ++issued;
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
     }
     if (!ok) {  // what is in flight lands before the CTA ends
-      for (int x = max(0, fixed_loads - 2); x < fixed_loads; ++x)
-        mbar_wait(&t->fixed_full[x & 1], (x / 2) & 1, nullptr);
-      for (int x = max(0, i - kStages); x < i; ++x)
-        mbar_wait(&t->full[x % kStages], (x / kStages) & 1, nullptr);
-      if (WEIGHTS)
-        for (int x = max(0, i - 8); x < i; ++x) mbar_wait(&t->info_full[x & 7], (x >> 3) & 1, nullptr);
+      for (int x = max(0, segments - 2); x < segments; ++x)
+        mbar_wait(&t->image_full[x & 1], (x / 2) & 1, nullptr);
+      for (int64_t x = max((int64_t)0, issued - kStages); x < issued; ++x)
+        mbar_wait(&t->full[x % kStages], (unsigned)(x / kStages) & 1, nullptr);
     }
   } else if (warp == kMmaWarp) {
     // --------------------------------------------------------------- MMAs
-    if (tc::elect_one()) {
-      constexpr uint32_t idesc =
-          F8 ? tc::idesc_e4m3_f32(kTile, S::kRows)
-             : tc::idesc_16bit_f32(kTile, S::kRows, false, false, false);
-      int heads = 0, left = 0, st = -1;  // left: steps with the tile that stays
-      unsigned st_phase = 1;
-      for (int i = 0; i < n_steps; ++i) {
-        const int buf = i & 1;
-        st = st + 1 == kStages ? 0 : st + 1;
-        if (st == 0) st_phase ^= 1;
-        if (left == 0) {
-          left = WEIGHTS ? n_tiles : n_steps;
-          if (!wait(&t->fixed_full[heads & 1], (heads / 2) & 1)) break;
-          ++heads;
+    constexpr uint32_t idesc =
+        F8 ? tc::idesc_e4m3_f32(kTile, kTile) : tc::idesc_16bit_f32(kTile, kTile, false, false, false);
+    int st = 0, segments = 0;
+    unsigned phase = 0;
+    int64_t i = 0;
+    bool ok = true;
+    for (int64_t f = begin; f < end && ok;) {
+      const Segment s = segment_at(p, f, end);
+      f = s.next;
+      if (!s.on) continue;
+      const int slot = segments & 1;
+      ok = wait(&t->image_full[slot], (segments / 2) & 1);
+      ++segments;
+      const uint64_t rows = operand_desc<W::kRowSpan>(images + slot * W::kImage);
+      for (int k = 0; k < s.n && ok; ++k, ++i) {
+        const int buf = (int)i & (kGroups - 1);
+        ok = wait(&t->full[st], phase);
+        if (ok && i >= kGroups) ok = wait(&t->s_empty[buf], (unsigned)(i / kGroups - 1) & 1);
+        if (!ok) break;
+        if (tc::elect_one()) {
+          tc::fence_after_sync();
+          const uint64_t key = operand_desc<W::kRowSpan>(keys + st * S::kStage);
+          const uint32_t d = tmem + buf * kTile;
+          if constexpr (F8) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int x = 0; x < D / 32; ++x) {
+                const uint64_t q = tc::desc_at(rows, part * kTile * D + x * 32);
+                const uint64_t c = tc::desc_at(key, x * 32);
+                tc::mma_e4m3_ss(d, WEIGHTS ? c : q, WEIGHTS ? q : c, idesc, part > 0 || x > 0);
+              }
+          } else {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              const uint64_t q = tc::desc_at(rows, (x >> 2) * W::kHalf + (x & 3) * 32);
+              const uint64_t c = tc::desc_at(key, (x >> 2) * W::kHalf + (x & 3) * 32);
+              tc::mma_bf16_ss(d, WEIGHTS ? c : q, WEIGHTS ? q : c, idesc, x > 0);
+            }
+          }
+          tc::mma_commit(&t->empty[st]);
+          tc::mma_commit(&t->s_full[buf]);
+          if (k + 1 == s.n) tc::mma_commit(&t->image_empty[slot]);
         }
-        const int slot = (heads - 1) & 1;
-        if (!wait(&t->full[st], st_phase)) break;
-        if (i >= 2 && !wait(&t->s_empty[buf], ((i >> 1) - 1) & 1)) break;
-        tc::fence_after_sync();
-        const uint64_t a0 = operand_desc<W::kRowSpan>(fixed + slot * S::kFixed);
-        const uint64_t b0 = operand_desc<W::kRowSpan>(stream + st * S::kStage);
-        const uint32_t d = tmem + buf * kTile;
-        if constexpr (F8) {
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              tc::mma_e4m3_ss(d, tc::desc_at(a0, (WEIGHTS ? 0 : part * kTile * D) + k * 32),
-                              tc::desc_at(b0, (WEIGHTS ? part * kTile * D : 0) + k * 32), idesc,
-                              part > 0 || k > 0);
-        } else {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc::mma_bf16_ss(d, tc::desc_at(a0, (k >> 2) * W::kHalf + (k & 3) * 32),
-                            tc::desc_at(b0, (k >> 2) * (WEIGHTS ? S::kRows * 128 : W::kHalf) + (k & 3) * 32), idesc,
-                            k > 0);
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
         }
-        tc::mma_commit(&t->empty[st]);
-        tc::mma_commit(&t->s_full[buf]);
-        if (--left == 0 && WEIGHTS) tc::mma_commit(&t->fixed_empty[slot]);
       }
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------ rows, or keys
-    const int me = tid & (kTile - 1);  // the thread's row, or key, of the tile
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    float sc = 0.f;
-    int sees = 0;  // !WEIGHTS: keys that the thread's row sees
-    if (!WEIGHTS && n_steps > 0) {
-      if (wait(&t->fixed_full[0], 0))
-        sc = reinterpret_cast<const float*>(fixed + W::kTileBytes)[info_at(me)];
-      sees = m.seq - m.w + min(ti0 * kTile + me, m.rows - 1) / p.g + 1;
-    }
+    const int group = warp >> 2, me = tid & (kTile - 1);  // the row, or key, of the tile
+    const uint32_t acc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * kTile;
     // WEIGHTS: a thread reads four keys of its warp's 32, me4 + 8 j, and of every eight
-    // columns two, so that what belongs to a column is loaded for four weights at once;
-    // their sums, and what the roundings of those lost
+    // columns two, so that what belongs to a column is loaded for four weights at once
     const int me4 = (warp & 3) * 32 + (lane >> 2), col2 = lane & 3;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
-    const int buf = warp >> 2;
-    int ti = ti0 + buf;  // WEIGHTS: the step's row tile
-    while (WEIGHTS && ti >= ti0 + n_tiles) ti -= n_tiles;
-    for (int i = buf; i < n_steps; i += 2) {
-      if (!__all_sync(kFull, (!WEIGHTS || wait(&t->info_full[i & 7], (i >> 3) & 1)) &&
-                                 wait(&t->s_full[buf], (i >> 1) & 1)))
-        break;
-      tc::fence_after_sync();
-      const uint32_t s = tmem + lane_base + buf * kTile;
-      if (!WEIGHTS) {
-        const int k0 = key0 + i * kTile;
-        const bool whole = __all_sync(kFull, k0 + kTile <= sees);
-        const uint64_t sc2 = f2_pack(sc, sc);
+    int segments = 0;
+    int64_t i0 = 0;  // steps before the segment
+    bool ok = true;
+    for (int64_t f = begin; f < end && ok;) {
+      const Segment s = segment_at(p, f, end);
+      const int64_t f0 = f;
+      f = s.next;
+      if (!s.on) continue;
+      const int slot = segments & 1;
+      ok = wait(&t->image_full[slot], (segments / 2) & 1);
+      ++segments;
+      const float* factors = reinterpret_cast<const float*>(images + slot * W::kImage + W::kTileBytes);
+      const int first_row = s.ti * kTile;
+      const int seen_by_all = s.m.seq - s.m.w;  // the last key that all counted queries see
+      const float sc = factors[info_at(me)];
+      const uint64_t sc2 = f2_pack(sc, sc);
+      const int sees = seen_by_all + min(first_row + me, s.m.rows - 1) / p.g + 1;  // keys of the row
+      float total = 0.f, ref = -INFINITY;
+      for (int k = (int)((group - i0) & (kGroups - 1)); k < s.n; k += kGroups) {
+        if (!ok) break;
+        ok = wait(&t->s_full[group], (unsigned)((i0 + k) / kGroups) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const int k0 = (s.key_tile + k) * kTile;
+        if constexpr (!WEIGHTS) {
+          const bool whole = __all_sync(kFull, k0 + kTile <= sees);
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          uint32_t v[32];
-          tc::tmem_ld32(s + c, v);
-          tc::tmem_wait_ld();
-          if (!whole)
+          for (int c = 0; c < kTile; c += 32) {
+            uint32_t v[32];
+            tc::tmem_ld32(acc + c, v);
+            tc::tmem_wait_ld();
+            if (!whole)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (k0 + c + e >= sees) v[e] = 0xff800000u;  // -inf
-          float mx = __uint_as_float(v[0]);
+              for (int e = 0; e < 32; ++e)
+                if (k0 + c + e >= sees) v[e] = 0xff800000u;  // -inf
+            float mx4[4];
 #pragma unroll
-          for (int e = 1; e < 31; e += 2)
-            mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-          mx = fmaxf(mx, __uint_as_float(v[31])) * sc;  // sc is not negative
-          if (mx > ref) {
-            total *= ex2_ftz(ref - mx);
-            ref = mx;
-          }
-          const float base = ref == -INFINITY ? 0.f : ref;
-          const uint64_t base2 = f2_pack(-base, -base);
-          uint64_t a[2] = {0ull, 0ull};
-          if (whole) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x, y;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, base2), x, y);
-              a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(ex2_ftz(x), ex2_ftz(y)));
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t* w = v + 8 * e;
+              const float a = fmax3(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]));
+              const float b = fmax3(__uint_as_float(w[3]), __uint_as_float(w[4]), __uint_as_float(w[5]));
+              mx4[e] = fmaxf(fmax3(a, __uint_as_float(w[6]), __uint_as_float(w[7])), b);
             }
-          } else {
+            const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * sc;  // sc is not negative
+            if (mx > ref) {
+              total *= ex2_ftz(ref - mx);
+              ref = mx;
+            }
+            const float base = ref == -INFINITY ? 0.f : ref;
+            const uint64_t base2 = f2_pack(-base, -base);
+            uint64_t a[2] = {0ull, 0ull};
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float x, y;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, base2), x, y);
-              x = k0 + c + e < sees ? ex2_ftz(x) : 0.f;  // (a factor of 0 times -inf is NaN)
-              y = k0 + c + e + 1 < sees ? ex2_ftz(y) : 0.f;
+              x = ex2_ftz(x);
+              y = ex2_ftz(y);
+              if (!whole) {  // (a factor of 0 times -inf is NaN)
+                x = k0 + c + e < sees ? x : 0.f;
+                y = k0 + c + e + 1 < sees ? y : 0.f;
+              }
               a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(x, y));
             }
+            float a0, a1;
+            f2_unpack(f2_add(a[0], a[1]), a0, a1);
+            total += a0 + a1;
           }
-          float a0, a1;
-          f2_unpack(f2_add(a[0], a[1]), a0, a1);
-          total += a0 + a1;
-        }
-      } else {
-        const float4* info = reinterpret_cast<const float4*>(infos + (i & 7) * kInfoBytes);
-        const int row0 = ti * S::kRows;
-        ti += 2;
-        while (ti >= ti0 + n_tiles) ti -= n_tiles;
-        const int rows = min(S::kRows, m.rows - row0);
-        // rows from which on the warp's last key is seen (0 and below: all keys by all rows)
-        const int after = key0 + (warp & 3) * 32 + 31 - (m.seq - m.w);
-        const int64_t from = (int64_t)max(0, after) * p.g - row0;
-        uint64_t a[4] = {0ull, 0ull, 0ull, 0ull};
+        } else {
+          const float4* info = reinterpret_cast<const float4*>(factors);
+          const int rows = min(kTile, s.m.rows - first_row);
+          // rows from which on the warp's last key is seen (0 and below: all keys by all rows)
+          const int after = k0 + (warp & 3) * 32 + 31 - seen_by_all;
+          const int64_t from = (int64_t)max(0, after) * p.g - first_row;
+          uint64_t a[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < S::kRows; c += 32) {
-          uint32_t v[2][16];
-          tc::tmem_ld16x256_x4(s + c, v[0]);
-          tc::tmem_ld16x256_x4(s + (16u << 16) + c, v[1]);
-          tc::tmem_wait_ld();
-          if (from <= c && c + 32 <= rows) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const float4 f = info[(c >> 1) + 4 * n + col2];
-              const uint64_t factor = f2_pack(f.x, f.y), lse = f2_pack(f.z, f.w);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t* w = &v[j >> 1][4 * n + 2 * (j & 1)];
-                float x, y;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(w[0]), __uint_as_float(w[1])), factor, lse), x, y);
-                a[j] = f2_add(a[j], f2_pack(ex2_ftz(x), ex2_ftz(y)));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // the tile's first row that sees the key
-              const int64_t first64 = (int64_t)max(0, key0 + me4 + 8 * j - (m.seq - m.w)) * p.g - row0;
-              const int first = (int)min(first64, (int64_t)kTile);
+          for (int c = 0; c < kTile; c += 32) {
+            uint32_t v[2][16];
+            tc::tmem_ld16x256_x4(acc + c, v[0]);
+            tc::tmem_ld16x256_x4(acc + (16u << 16) + c, v[1]);
+            tc::tmem_wait_ld();
+            if (from <= c && c + 32 <= rows) {
 #pragma unroll
               for (int n = 0; n < 4; ++n) {
-                const float4 f = info[(c >> 1) + 4 * n + col2];
-                const uint32_t* w = &v[j >> 1][4 * n + 2 * (j & 1)];
-                const int row = c + 8 * n + 2 * col2;
-                const float x = ex2_ftz(fmaf(__uint_as_float(w[0]), f.x, f.z));
-                const float y = ex2_ftz(fmaf(__uint_as_float(w[1]), f.y, f.w));
-                a[j] = f2_add(a[j], f2_pack(row >= first && row < rows ? x : 0.f,
-                                            row + 1 >= first && row + 1 < rows ? y : 0.f));
+                const float4 q = info[(c >> 1) + 4 * n + col2];
+                const uint64_t factor = f2_pack(q.x, q.y), lse = f2_pack(q.z, q.w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t* w = &v[j >> 1][4 * n + 2 * (j & 1)];
+                  float x, y;
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(w[0]), __uint_as_float(w[1])), factor, lse), x, y);
+                  a[j] = f2_add(a[j], f2_pack(ex2_ftz(x), ex2_ftz(y)));
+                }
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                // the tile's first row that sees the key
+                const int64_t first64 = (int64_t)max(0, k0 + me4 + 8 * j - seen_by_all) * p.g - first_row;
+                const int first = (int)min(first64, (int64_t)kTile);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                  const float4 q = info[(c >> 1) + 4 * n + col2];
+                  const uint32_t* w = &v[j >> 1][4 * n + 2 * (j & 1)];
+                  const int row = c + 8 * n + 2 * col2;
+                  const float x = ex2_ftz(fmaf(__uint_as_float(w[0]), q.x, q.z));
+                  const float y = ex2_ftz(fmaf(__uint_as_float(w[1]), q.y, q.w));
+                  a[j] = f2_add(a[j], f2_pack(row >= first && row < rows ? x : 0.f,
+                                              row + 1 >= first && row + 1 < rows ? y : 0.f));
+                }
               }
             }
           }
-        }
-        // one sum of up to millions of weights: the rounding of each addition is kept
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float a0, a1;
-          f2_unpack(a[j], a0, a1);
-          const float add = (a0 + a1) + low[j];
-          const float next = sum[j] + add;
-          low[j] = add - (next - sum[j]);
-          sum[j] = next;
+          for (int j = 0; j < 4; ++j) {
+            float x, y;
+            f2_unpack(a[j], x, y);
+            x += y;
+            x += __shfl_xor_sync(kFull, x, 1);
+            x += __shfl_xor_sync(kFull, x, 2);
+            if (col2 == 0) p.sums[(f0 + k) * kTile + me4 + 8 * j] = x;
+          }
         }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t->s_empty[group]);
       }
-      tc::fence_before_sync();
+      i0 += s.n;
+      if (!WEIGHTS)
+        p.tile_stats[((((int64_t)s.tile * p.Hkv + s.kvh) * p.pieces + s.piece) * kGroups + group) * kTile +
+                     me] = make_float2(ref, total);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&t->s_empty[buf]);
-    }
-    if (!WEIGHTS) {
-      if (buf == 1) t->part[0][me] = ref, t->part[1][me] = total;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x = sum[j] + (isnan(low[j]) ? 0.f : low[j]);  // (a NaN sum has lost no rounding)
-        x += __shfl_xor_sync(kFull, x, 1);
-        x += __shfl_xor_sync(kFull, x, 2);
-        if (col2 == 0) t->part[buf][me4 + 8 * j] = x;
-      }
+      if (lane == 0) mbar_arrive(&t->image_empty[slot]);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kWideCols);
-  if (!WEIGHTS) {
-    if (warp < 4) {
-      join_stats(ref, total, t->part[0][tid], t->part[1][tid]);
-      p.tile_stats[(((int64_t)tile0 * p.Hkv + kvh0) * p.parts + blockIdx.y) * kTile + tid] =
-          make_float2(ref, total);
-    }
-    return;
-  }
-  if (warp < 4) total = t->part[0][tid] + t->part[1][tid];
-  if (gridDim.z > 1) {
-    if (warp < 4) t->part[0][tid] = total;  // (read by this thread alone)
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    if (blockIdx.z == 0 && warp < 4) {
-      total = 0.f;
-      for (unsigned c = 0; c < gridDim.z; ++c) total += *cluster.map_shared_rank(&t->part[0][tid], c);
-    }
-    cluster.sync();
-  }
-  if (blockIdx.z == 0 && warp < 4 && key0 + tid < m.seq) {
-    const int64_t o = (int64_t)mass_row(p, r) * p.mass_stride + key0 + tid;
-    p.mass_out[o] = (key0 + tid < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + total;
-  }
 }
 
-// The rows' lse into the images, from the parts' statistics.
+// The rows' lse into the images, from the pieces' statistics.
 template <int D, bool F8>
 __global__ void __launch_bounds__(kTile) mass_join_kernel(MassParams p) {
   using W = WideGeo<D, F8>;
   launch_dependents();
   grid_dependency_wait();
-  const int tile = blockIdx.x / p.Hkv;
+  const int tile = blockIdx.x / p.Hkv, kvh = blockIdx.x - tile * p.Hkv;
   const int4 who = p.tile_of[tile];
   if (who.x < 0) return;
-  const int n = min(p.parts, (who.z + p.part_keys - 1) / p.part_keys);
+  const int64_t start = p.first_step[who.x] + ((int64_t)kvh * who.z + who.y) * who.w;
+  const int n = (int)min((start + who.w - 1) / p.per_cta - start / p.per_cta + 1, (int64_t)p.pieces);
   float* info =
       reinterpret_cast<float*>(p.images + (int64_t)blockIdx.x * W::kImage + W::kTileBytes);
   info[info_at(threadIdx.x) + 2] =
-      -lse_of(p.tile_stats + (int64_t)blockIdx.x * p.parts * kTile + threadIdx.x, n, kTile);
+      -lse_of(p.tile_stats + (int64_t)blockIdx.x * p.pieces * kGroups * kTile + threadIdx.x, n * kGroups,
+              kTile);
+}
+
+// The steps' sums of each key, over the row tiles of all heads, into the mass.
+__global__ void __launch_bounds__(kSumThreads) mass_add_kernel(MassParams p) {
+  grid_dependency_wait();
+  const int r = blockIdx.y;
+  if (p.first_tile[r] < 0) return;
+  const MassReq m = rows_of(p, r);
+  const int key = blockIdx.x * kSumThreads + (int)threadIdx.x;
+  if (key >= m.seq) return;
+  const int key_tiles = (m.seq + kTile - 1) / kTile, units = tiles_of(m) * p.Hkv;
+  const float* s = p.sums + (p.first_step[r] + key / kTile) * kTile + key % kTile;
+  const int64_t step = (int64_t)key_tiles * kTile;
+  float sum = 0.f, low = 0.f;  // what the roundings of the sum lost is put back at the end
+  for (int u = 0; u < units; u += 16) {
+    float part = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (u + i < units) part += s[(u + i) * step];
+    const float add = part + low, next = sum + add;
+    low = add - (next - sum);
+    sum = next;
+  }
+  if (!isnan(low)) sum += low;  // (a NaN sum has lost no rounding)
+  const int64_t o = (int64_t)mass_row(p, r) * p.mass_stride + key;
+  p.mass_out[o] = (key < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + sum;
 }
 
 // ------------------------------------------------------------------- planning
 
 struct MassPlan {
-  int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows, sum_key_tiles;
-  int splits, parts, part_keys, key_tiles, narrow_keys;
-  size_t off_stats, off_tile_of, off_first, off_images, off_tile_stats, total;
+  int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows, steps, per_cta, ctas;
+  int splits, pieces, key_tiles, narrow_keys, wide_keys;
+  size_t off_stats, off_tile_of, off_first, off_steps, off_images, off_tile_stats, off_sums, total;
 };
 
 // What a batch needs, from its mirrors alone (head_dim 128's images serve 64 too).
@@ -928,7 +898,6 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
                     MassPlan& pl) {
   pl = MassPlan{};
   const int64_t g = Hq / Hkv;
-  int64_t steps = 0;  // of pass 1: row tiles x kv heads x key tiles
   int narrow_keys = 0, wide_keys = 0;
   for (int r = 0; r < R; ++r) {
     const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];
@@ -946,19 +915,17 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
       pl.n_tiles += tiles;
       if (tiles > pl.max_tiles) pl.max_tiles = tiles;
       if (seq[r] > wide_keys) wide_keys = seq[r];
-      steps += tiles * Hkv * ((seq[r] + kTile - 1) / kTile);
-      pl.sum_key_tiles += (seq[r] + kTile - 1) / kTile;
+      pl.steps += tiles * Hkv * (((int64_t)seq[r] + kTile - 1) / kTile);
     }
   }
   pl.narrow_keys = narrow_keys;
   pl.splits = (narrow_keys + kSplitKeys - 1) / kSplitKeys;
   pl.key_tiles = (wide_keys + kTile - 1) / kTile;
-  // Parts of the keys in pass 1, of 4 to 32 key tiles: 1216 CTAs and more, of which 304 run
-  // at once on 152 SMs.
-  int64_t per = (steps + 1215) / 1216;
-  per = per < 4 ? 4 : per > 32 ? 32 : per;
-  pl.part_keys = (int)per * kTile;
-  pl.parts = (wide_keys + pl.part_keys - 1) / pl.part_keys;
+  pl.wide_keys = wide_keys;
+  // an equal run of steps for each of 152 SMs, four at the least
+  pl.per_cta = (pl.steps + 151) / 152 < 4 ? 4 : (pl.steps + 151) / 152;
+  pl.ctas = (pl.steps + pl.per_cta - 1) / pl.per_cta;
+  pl.pieces = (int)((pl.key_tiles + pl.per_cta - 1) / pl.per_cta) + 1;
   if (pl.n_tiles > 0x7fffffff / (int64_t)Hkv || pl.max_tiles > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   auto up = [](size_t x) { return (x + 1023) & ~(size_t)1023; };
   size_t at = up((size_t)pl.score_floats * 4);
@@ -968,10 +935,14 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   at = up(at + (size_t)pl.n_tiles * sizeof(int4));
   pl.off_first = at;
   if (pl.n_tiles) at = up(at + (size_t)R * sizeof(int));
+  pl.off_steps = at;
+  if (pl.n_tiles) at = up(at + ((size_t)R + 1) * sizeof(int64_t));
   pl.off_images = at;
   at = up(at + (size_t)pl.n_tiles * Hkv * WideGeo<128, false>::kImage);
   pl.off_tile_stats = at;
-  at = up(at + (size_t)pl.n_tiles * Hkv * pl.parts * kTile * sizeof(float2));
+  at = up(at + (size_t)pl.n_tiles * Hkv * pl.pieces * kGroups * kTile * sizeof(float2));
+  pl.off_sums = at;
+  at = up(at + (size_t)pl.steps * kTile * sizeof(float));
   pl.total = at;
   return PA_OK;
 }
@@ -994,27 +965,21 @@ bool key_map(CUtensorMap* m, const pa_kv_pool* pool, int rows) {
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// dependent: the kernel may be scheduled before the one ahead of it has ended, and waits
+// for that itself.
 template <class... KArgs, class... Args>
 pa_status launch_after(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
-                       cudaStream_t s, bool dependent, unsigned cluster_z, Args&&... args) {
+                       cudaStream_t s, bool dependent, Args&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2] = {};
-  unsigned n = 0;
-  if (dependent) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster_z > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = attr[n].val.clusterDim.y = 1;
-    attr[n++].val.clusterDim.z = cluster_z;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) {
     cudaGetLastError();
     return PA_ERR_CUDA;
@@ -1027,7 +992,7 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
                    cudaStream_t s) {
   static OncePerDevice once;
   constexpr size_t narrow_smem = 1024 + (size_t)kNarrowWarps * kNarrowRing + sizeof(NarrowTail);
-  constexpr size_t stats_smem = WideSmem<D, F8, false>::kAlloc, sum_smem = WideSmem<D, F8, true>::kAlloc;
+  constexpr size_t wide_smem = WideSmem<D, F8>::kAlloc;
   if (!once.done([] {
         auto set = [](const void* f, size_t n) {
           return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n) ==
@@ -1035,8 +1000,8 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
         };
         return set((const void*)mass_scores_kernel<D, F8, 1>, narrow_smem) &&
                set((const void*)mass_scores_kernel<D, F8, 2>, narrow_smem) &&
-               set((const void*)mass_tile_kernel<D, F8, false>, stats_smem) &&
-               set((const void*)mass_tile_kernel<D, F8, true>, sum_smem);
+               set((const void*)mass_tile_kernel<D, F8, false>, wide_smem) &&
+               set((const void*)mass_tile_kernel<D, F8, true>, wide_smem);
       }))
     return PA_ERR_CUDA;
   CUtensorMap tmap{};
@@ -1045,27 +1010,26 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
     if (!cell_map<D, F8>(&tmap, pool->k_pool, pool->num_blocks, p.Hkv * p.B)) return PA_ERR_CUDA;
     const dim3 grid((unsigned)pl.splits, (unsigned)p.Hkv, (unsigned)p.R);
     st = launch_after(pl.max_narrow_rows <= 8 ? mass_scores_kernel<D, F8, 1> : mass_scores_kernel<D, F8, 2>,
-                      grid, kNarrowWarps * 32, narrow_smem, s, false, 1, tmap, p);
+                      grid, kNarrowWarps * 32, narrow_smem, s, false, tmap, p);
     if (st != PA_OK) return st;
     st = launch_after(mass_sum_kernel, dim3((unsigned)((pl.narrow_keys + kSumThreads - 1) / kSumThreads), (unsigned)p.R),
-                      kSumThreads, (size_t)p.Hkv * pl.max_narrow_rows * 4, s, true, 1, p);
+                      kSumThreads, (size_t)p.Hkv * pl.max_narrow_rows * 4, s, true, p);
     if (st != PA_OK) return st;
   }
   if (!pl.n_tiles) return PA_OK;
   if (!key_map(&tmap, pool, p.B)) return PA_ERR_CUDA;
   st = launch_after(mass_rows_kernel<D, F8>, dim3((unsigned)pl.max_tiles, (unsigned)p.Hkv, (unsigned)p.R),
-                    kTile, 0, s, false, 1, p);
+                    kTile, 0, s, false, p);
   if (st != PA_OK) return st;
-  st = launch_after(mass_tile_kernel<D, F8, false>, dim3((unsigned)(pl.n_tiles * p.Hkv), (unsigned)p.parts),
-                    kWideThreads, stats_smem, s, true, 1, tmap, p);
+  const dim3 ctas((unsigned)pl.ctas);
+  st = launch_after(mass_tile_kernel<D, F8, false>, ctas, kWideThreads, wide_smem, s, true, tmap, p);
   if (st != PA_OK) return st;
-  st = launch_after(mass_join_kernel<D, F8>, dim3((unsigned)(pl.n_tiles * p.Hkv)), kTile, 0, s, true, 1, p);
+  st = launch_after(mass_join_kernel<D, F8>, dim3((unsigned)(pl.n_tiles * p.Hkv)), kTile, 0, s, true, p);
   if (st != PA_OK) return st;
-  // a cluster shares the kv heads of a key tile while there are less than four rounds of CTAs
-  unsigned share = 1;
-  while (share < 8 && (int)share * 2 <= p.Hkv && pl.sum_key_tiles * share < 8 * num_sms()) share *= 2;
-  return launch_after(mass_tile_kernel<D, F8, true>, dim3((unsigned)pl.key_tiles, (unsigned)p.R, share),
-                      kWideThreads, sum_smem, s, true, share, tmap, p);
+  st = launch_after(mass_tile_kernel<D, F8, true>, ctas, kWideThreads, wide_smem, s, true, tmap, p);
+  if (st != PA_OK) return st;
+  return launch_after(mass_add_kernel, dim3((unsigned)((pl.wide_keys + kSumThreads - 1) / kSumThreads), (unsigned)p.R),
+                      kSumThreads, 0, s, true, p);
 }
 
 }  // namespace
@@ -1112,7 +1076,7 @@ extern "C" pa_status pa_attention_mass(
                                           seq_lens_host[r] > mass_stride))
       return PA_ERR_INVALID;
   if (!workspace || workspace_bytes < pl.total || !aligned16(workspace)) return PA_ERR_INVALID;
-  if (num_reqs > 65535 || pool->num_kv_heads > 65535 || pl.parts > 65535 ||
+  if (num_reqs > 65535 || pool->num_kv_heads > 65535 ||
       pool->num_kv_heads * pl.max_narrow_rows > 12288)
     return PA_ERR_UNSUPPORTED;
   MassParams p{};
@@ -1148,8 +1112,11 @@ extern "C" pa_status pa_attention_mass(
   p.images = ws + pl.off_images;
   p.tile_stats = reinterpret_cast<float2*>(ws + pl.off_tile_stats);
   p.n_tiles = (int)pl.n_tiles;
-  p.parts = pl.parts;
-  p.part_keys = pl.part_keys;
+  p.first_step = reinterpret_cast<int64_t*>(ws + pl.off_steps);
+  p.sums = reinterpret_cast<float*>(ws + pl.off_sums);
+  p.steps = pl.steps;
+  p.per_cta = pl.per_cta;
+  p.pieces = pl.pieces;
   p.key_tiles = pl.key_tiles;
   p.err = error_word();
   if (!p.err) return PA_ERR_CUDA;
