@@ -752,17 +752,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const float base = ref == -INFINITY ? 0.f : ref;
             const uint64_t base2 = f2_pack(-base, -base);
             uint64_t a[2] = {0ull, 0ull};
+            if (whole) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x, y;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, base2), x, y);
-              x = ex2_ftz(x);
-              y = ex2_ftz(y);
-              if (!whole) {  // (a factor of 0 times -inf is NaN)
-                x = k0 + c + e < sees ? x : 0.f;
-                y = k0 + c + e + 1 < sees ? y : 0.f;
+              for (int e = 0; e < 32; e += 2) {
+                float x, y;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, base2), x, y);
+                a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(ex2_ftz(x), ex2_ftz(y)));
               }
-              a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(x, y));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x, y;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, base2), x, y);
+                x = k0 + c + e < sees ? ex2_ftz(x) : 0.f;  // (a factor of 0 times -inf is NaN)
+                y = k0 + c + e + 1 < sees ? ex2_ftz(y) : 0.f;
+                a[(e >> 1) & 1] = f2_add(a[(e >> 1) & 1], f2_pack(x, y));
+              }
             }
             float a0, a1;
             f2_unpack(f2_add(a[0], a[1]), a0, a1);
