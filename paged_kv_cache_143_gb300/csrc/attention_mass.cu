@@ -299,16 +299,19 @@ __global__ void __launch_bounds__(kSumThreads) mass_sum_kernel(MassParams p) {
   }
   grid_dependency_wait();  // the scores and their statistics are complete
   const int rows = p.Hkv * m.rows, n_split = (m.seq + kSplitKeys - 1) / kSplitKeys;
-  for (int x = threadIdx.x >> 5; x < rows; x += kSumThreads / 32) {  // a warp for each row
-    const float2* part = p.split_stats +
-        ((int64_t)(r * (int64_t)p.Hkv + x / m.rows) * kNarrowRows + x % m.rows) * p.splits;
-    const int lane = threadIdx.x & 31;
+  // eight lanes for each row, all rows of up to 32 at once
+  for (int base = 0; base < rows; base += kSumThreads / 8) {
+    const int x = base + ((int)threadIdx.x >> 3), lane = threadIdx.x & 7;
     float ref = -INFINITY, sum = 0.f;
-    for (int i = lane; i < n_split; i += 32) join_stats(ref, sum, part[i].x, part[i].y);
+    if (x < rows) {
+      const float2* part = p.split_stats +
+          ((int64_t)(r * (int64_t)p.Hkv + x / m.rows) * kNarrowRows + x % m.rows) * p.splits;
+      for (int i = lane; i < n_split; i += 8) join_stats(ref, sum, part[i].x, part[i].y);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 4; o > 0; o >>= 1)
       join_stats(ref, sum, __shfl_xor_sync(kFull, ref, o), __shfl_xor_sync(kFull, sum, o));
-    if (lane == 0) lse[x] = ref + log2f(sum);  // NaN for a row that scores -inf throughout
+    if (lane == 0 && x < rows) lse[x] = ref + log2f(sum);  // NaN for a row that scores -inf throughout
   }
   __syncthreads();
   const int key = key0 + (int)threadIdx.x;
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kSumThreads) mass_sum_kernel(MassParams p) {
   const float* s = p.scores + at + key;
   float sum = 0.f;
   if (key <= m.seq - m.w) {  // seen by all counted queries
-#pragma unroll 16
+#pragma unroll 32
     for (int x = 0; x < rows; ++x) sum += ex2_ftz(s[(int64_t)x * stride] - lse[x]);
   } else {
     const int c0 = (key - (m.seq - m.w)) * p.g;  // the first row that sees the key
