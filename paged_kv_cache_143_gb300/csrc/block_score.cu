@@ -24,10 +24,14 @@ constexpr unsigned kFull = 0xffffffffu;
 
 // ------------------------------------------------------------------ bounds
 //
-// One warp per (block, kv head): its lanes read the block's key rows in
-// 16-byte pieces (a row in D * size / 16 lanes), eight loads in flight, keep
-// the least and greatest of their dims in packed 16-bit arithmetic (exact:
-// E4M3 codes widen to f16) and join by shuffles. HBM traffic is the keys once.
+// A warp takes a kv head of a block, or a few one after the other: its lanes read the key
+// rows in 16-byte pieces (a row in D * size / 16 lanes), eight loads in flight, and keep
+// the least and greatest of their dims in packed 16-bit arithmetic (exact: E4M3 codes
+// widen to f16). The lanes that hold the same dims join by halves: at each step a lane
+// hands the half of its dims to its partner that the partner keeps, so that in the end
+// every lane has, and writes, dims of its own (all dims to all lanes took two and a half
+// times the shuffles, and half of the time for blocks of 16 E4M3 keys). HBM traffic is
+// the keys once.
 // The blocks that a step touched are found from slots: request r owns the
 // slots from qsl[r] / B + 2 r on, which leaves room for the
 // (q_len - 1) / B + 2 blocks at most that q_len tokens reach.
@@ -56,12 +60,32 @@ __device__ __forceinline__ __half2 e4m3x2(uint32_t codes) {
   return *reinterpret_cast<__half2*>(&h);
 }
 
+// Of 2 KEEP pairs the lane keeps KEEP, joined with the partner M lanes away; then on to M / 2,
+// down to LAST.
+template <bool FP8, int M, int KEEP, int LAST, class V, int N>
+__device__ __forceinline__ void join_halves(V (&lo)[N], V (&hi)[N], int& pair, int lane) {
+  using P = Pack<FP8>;
+  const bool upper = lane & M;
+  pair += upper ? KEEP : 0;
+#pragma unroll
+  for (int p = 0; p < KEEP; ++p) {
+    auto share = [&](V& near, const V& far, auto join) {  // (by value: a choice of lvalues goes to memory)
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(&near), y = *reinterpret_cast<const uint32_t*>(&far);
+      const uint32_t got = __shfl_xor_sync(kFull, upper ? x : y, M), own = upper ? y : x;
+      near = join(*reinterpret_cast<const V*>(&own), *reinterpret_cast<const V*>(&got));
+    };
+    share(lo[p], lo[p + KEEP], [](V a, V b) { return P::least(a, b); });
+    share(hi[p], hi[p + KEEP], [](V a, V b) { return P::most(a, b); });
+  }
+  if constexpr (M > LAST) join_halves<FP8, M / 2, KEEP / 2, LAST>(lo, hi, pair, lane);
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kBoundWarps * 32)
     block_bounds_kernel(const uint8_t* __restrict__ k_pool, __nv_bfloat16* __restrict__ bounds,
                         const int32_t* __restrict__ qsl, const int32_t* __restrict__ seq_lens,
                         const int32_t* __restrict__ tables, int max_blocks, int R, int T, int Hkv,
-                        int B, int num_blocks, int64_t n_items, unsigned* err) {
+                        int B, int num_blocks, int per_warp, int64_t n_items, unsigned* err) {
   using P = Pack<FP8>;
   using V = typename P::T;
   constexpr int kRowBytes = D * (FP8 ? 1 : 2);
@@ -72,8 +96,9 @@ __global__ void __launch_bounds__(kBoundWarps * 32)
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
   if (item >= n_items) return;
-  const int64_t slot = item / Hkv;
-  const int kvh = (int)(item - slot * Hkv);
+  const int shares = (Hkv + per_warp - 1) / per_warp;
+  const int64_t slot = item / shares;
+  const int head0 = (int)(item - slot * shares) * per_warp, head1 = min(head0 + per_warp, Hkv);
   int r, i, n;  // request, logical block, the request's stored tokens
   if (qsl) {
     r = warp_last_le(R, slot, [&](int x) { return (int64_t)(__ldg(qsl + x) / B) + 2 * (int64_t)x; });
@@ -99,71 +124,64 @@ __global__ void __launch_bounds__(kBoundWarps * 32)
     return;
   }
   const int rows = min(B, n - i * B);
-  const uint8_t* src = k_pool + (((int64_t)id * Hkv + kvh) * B) * kRowBytes +
-                       (lane % kRowLanes) * 16;
-  V lo[kPairs] = {}, hi[kPairs] = {};
-  bool any = false;
-  for (int row0 = lane / kRowLanes; row0 < rows; row0 += kRows * kDeep) {
-    uint4 x[kDeep];
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u)
-      if (row0 + u * kRows < rows)
-        x[u] = *reinterpret_cast<const uint4*>(src + (int64_t)(row0 + u * kRows) * kRowBytes);
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u) {
-      if (row0 + u * kRows >= rows) break;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-      for (int p = 0; p < kPairs; ++p) {
-        V v;
-        if constexpr (FP8)
-          v = e4m3x2(w[p >> 1] >> (16 * (p & 1)));
-        else
-          v = *reinterpret_cast<const V*>(&w[p]);
-        lo[p] = any ? P::least(lo[p], v) : v;
-        hi[p] = any ? P::most(hi[p], v) : v;
-      }
-      any = true;
-    }
-  }
-#pragma unroll
-  for (int m = kRowLanes; m < 32; m <<= 1) {
-    const bool other = __shfl_xor_sync(kFull, any, m);
-#pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      uint32_t a = *reinterpret_cast<uint32_t*>(&lo[p]), b = *reinterpret_cast<uint32_t*>(&hi[p]);
-      a = __shfl_xor_sync(kFull, a, m);
-      b = __shfl_xor_sync(kFull, b, m);
-      const V va = *reinterpret_cast<V*>(&a), vb = *reinterpret_cast<V*>(&b);
-      if (other) {
-        lo[p] = any ? P::least(lo[p], va) : va;
-        hi[p] = any ? P::most(hi[p], vb) : vb;
-      }
-    }
-    any |= other;
-  }
-  if (lane >= kRowLanes) return;
   // infinite keys become the largest finite bounds, so that a query's zero still makes zero of them
   const __nv_bfloat162 top = __halves2bfloat162(__ushort_as_bfloat16(0x7F7F), __ushort_as_bfloat16(0x7F7F));
-  __nv_bfloat16* out = bounds + ((int64_t)id * Hkv + kvh) * 2 * D + lane * 2 * kPairs;
+  // (a lane without a row of its own takes the first, which changes nothing)
+  const int mine = lane / kRowLanes < rows ? lane / kRowLanes : 0;
+  const uint8_t* src = k_pool + (((int64_t)id * Hkv + head0) * B + mine) * kRowBytes + (lane % kRowLanes) * 16;
+  __nv_bfloat16* out = bounds + ((int64_t)id * Hkv + head0) * 2 * D;
+  for (int h = head0; h < head1; ++h, src += B * kRowBytes, out += 2 * D) {
+    V lo[kPairs], hi[kPairs];
+    for (int row0 = 0; row0 + mine < rows; row0 += kRows * kDeep) {
+      uint4 x[kDeep];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t w[kPairs];
+      for (int u = 0; u < kDeep; ++u)
+        if (row0 + mine + u * kRows < rows)
+          x[u] = *reinterpret_cast<const uint4*>(src + (row0 + u * kRows) * kRowBytes);
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      const V v = h ? hi[p] : lo[p];
-      __nv_bfloat162 o;
-      if constexpr (FP8) {
-        const float2 f = __half22float2(v);
-        o = __floats2bfloat162_rn(f.x, f.y);  // exact
-      } else {
-        o = __hmax2_nan(__hmin2_nan(v, top), __hneg2(top));
+      for (int u = 0; u < kDeep; ++u) {
+        if (row0 + mine + u * kRows >= rows) break;
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) {
+          V v;
+          if constexpr (FP8)
+            v = e4m3x2(w[p >> 1] >> (16 * (p & 1)));
+          else
+            v = *reinterpret_cast<const V*>(&w[p]);
+          const bool first = row0 == 0 && u == 0;
+          lo[p] = first ? v : P::least(lo[p], v);
+          hi[p] = first ? v : P::most(hi[p], v);
+        }
       }
-      w[p] = *reinterpret_cast<uint32_t*>(&o);
     }
+    __syncwarp();
+    int pair = 0;  // the first of the pairs that the lane keeps
+    join_halves<FP8, 16, kPairs / 2, kRowLanes>(lo, hi, pair, lane);
+    constexpr int kKept = kPairs * kRowLanes / 32;  // 1 or 2
+    uint32_t w[2][kKept];
 #pragma unroll
-    for (int p = 0; p < kPairs; p += 4)
-      *reinterpret_cast<uint4*>(out + h * D + 2 * p) = make_uint4(w[p], w[p + 1], w[p + 2], w[p + 3]);
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int p = 0; p < kKept; ++p) {
+        const V v = e ? hi[p] : lo[p];
+        __nv_bfloat162 o;
+        if constexpr (FP8) {
+          const float2 f = __half22float2(v);
+          o = __floats2bfloat162_rn(f.x, f.y);  // exact
+        } else {
+          o = __hmax2_nan(__hmin2_nan(v, top), __hneg2(top));
+        }
+        w[e][p] = *reinterpret_cast<uint32_t*>(&o);
+      }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(out) + (lane % kRowLanes) * kPairs + pair;
+    if constexpr (kKept == 2) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0][0], w[0][1]);
+      *reinterpret_cast<uint2*>(dst + D / 2) = make_uint2(w[1][0], w[1][1]);
+    } else {
+      dst[0] = w[0][0];
+      dst[D / 2] = w[1][0];
+    }
   }
 }
 
@@ -701,7 +719,13 @@ extern "C" pa_status pa_update_block_bounds(const pa_kv_pool* pool, void* bounds
   const int B = pool->block_size, D = pool->head_dim, Hkv = pool->num_kv_heads;
   const int64_t slots = query_start_loc ? num_tokens / B + 2 * (int64_t)num_reqs
                                         : (int64_t)num_reqs * max_blocks;
-  const int64_t items = slots * Hkv, ctas = (items + kBoundWarps - 1) / kBoundWarps;
+  // A warp takes heads of up to 128 keys in all, as long as every SM has 32 warps: finding
+  // its place costs a warp more than a head of 16 keys. (24 prompts of 15k to 20k tokens,
+  // E4M3, blocks of 16: 160 us one by one, 107 by 4, 100 by 8; blocks of 64: 84, 80, 78.)
+  const int64_t want = slots * Hkv / (32 * (int64_t)num_sms());
+  const int per_warp = (int)(want < 1 ? 1 : want > 128 / B ? 128 / B : want);
+  const int64_t items = slots * ((Hkv + per_warp - 1) / per_warp);
+  const int64_t ctas = (items + kBoundWarps - 1) / kBoundWarps;
   if (ctas > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   unsigned* err = error_word();
   if (!err) return PA_ERR_CUDA;
@@ -709,7 +733,7 @@ extern "C" pa_status pa_update_block_bounds(const pa_kv_pool* pool, void* bounds
     kernel<<<(unsigned)ctas, kBoundWarps * 32, 0, as_stream(stream)>>>(
         static_cast<const uint8_t*>(pool->k_pool), static_cast<__nv_bfloat16*>(bounds),
         query_start_loc, seq_lens, block_tables, max_blocks, num_reqs, num_tokens, Hkv, B,
-        pool->num_blocks, items, err);
+        pool->num_blocks, per_warp, items, err);
   };
   const bool fp8 = pool->dtype == PA_KV_FP8_E4M3;
   if (D == 128)
