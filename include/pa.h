@@ -665,7 +665,9 @@ pa_status pa_latent_prefill(const void* q, int64_t q_token_stride, int64_t q_hea
  * Exact: bf16 keys as they are, E4M3 pools the decoded codes, without k_scale.
  * A dim with a NaN key has NaN bounds; infinite keys count as the largest finite
  * bf16. A block shared by several requests of one call has to hold the same
- * number of stored tokens for each of them (full prefix blocks do).
+ * number of stored tokens for each of them (full prefix blocks do). pa_copy_blocks
+ * copies no bounds: a copied block's are made when it is next written to, which
+ * copy-on-write does in the same step.
  */
 pa_status pa_update_block_bounds(const pa_kv_pool* pool, void* bounds,
                                  const int32_t* query_start_loc, const int32_t* seq_lens,

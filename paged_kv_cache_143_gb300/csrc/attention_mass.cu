@@ -905,7 +905,8 @@ __global__ void __launch_bounds__(kSumThreads) mass_add_kernel(MassParams p) {
 
 struct MassPlan {
   int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows, steps, per_cta, ctas;
-  int splits, pieces, key_tiles, narrow_keys, wide_keys;
+  int64_t narrow_keys, wide_keys;
+  int splits, pieces, key_tiles;
   size_t off_stats, off_tile_of, off_first, off_steps, off_images, off_tile_stats, off_sums, total;
 };
 
@@ -914,7 +915,7 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
                     MassPlan& pl) {
   pl = MassPlan{};
   const int64_t g = Hq / Hkv;
-  int narrow_keys = 0, wide_keys = 0;
+  int64_t narrow_keys = 0, wide_keys = 0;
   for (int r = 0; r < R; ++r) {
     const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];
     if (q_len < 0 || (q_len > 0 && seq[r] < q_len)) return PA_ERR_INVALID;
@@ -935,9 +936,9 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
     }
   }
   pl.narrow_keys = narrow_keys;
-  pl.splits = (narrow_keys + kSplitKeys - 1) / kSplitKeys;
-  pl.key_tiles = (wide_keys + kTile - 1) / kTile;
   pl.wide_keys = wide_keys;
+  pl.splits = (int)((narrow_keys + kSplitKeys - 1) / kSplitKeys);
+  pl.key_tiles = (int)((wide_keys + kTile - 1) / kTile);
   // an equal run of steps for each of 152 SMs, four at the least
   pl.per_cta = (pl.steps + 151) / 152 < 4 ? 4 : (pl.steps + 151) / 152;
   pl.ctas = (pl.steps + pl.per_cta - 1) / pl.per_cta;

@@ -223,6 +223,8 @@ class SparseEngine(Engine):
                  first: int = 1, last: int = 2, device=None):
         super().__init__(sched, pool, num_q_heads, max_reqs, max_blocks, max_tokens, scale,
                          device=device)
+        if first < 0 or last < 0 or not 1 <= num_selected >= first + last:
+            raise ValueError("num_selected must be positive and hold the first and last blocks")
         self.first, self.last = first, last
         H = pool.num_kv_heads
         self.bounds = torch.zeros((pool.num_blocks, H, 2, pool.head_dim), dtype=torch.bfloat16,

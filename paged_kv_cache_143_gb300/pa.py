@@ -1211,9 +1211,9 @@ def compact_cache(pool: KVPool, src_tables: torch.Tensor, dst_tables: torch.Tens
     R = kept_lens.numel()
     if kept.dim() != 2 or kept.shape[0] != R:
         raise ValueError("kept must be [num_reqs][k]")
-    for t in (src_tables, dst_tables):
-        if t.dim() != 2 or t.shape[0] != R:
-            raise ValueError("src_tables and dst_tables must be [num_reqs][blocks]")
+    if src_tables.dim() != 2 or dst_tables.dim() != 2 or \
+            not src_tables.shape[0] == R == dst_tables.shape[0]:
+        raise ValueError("src_tables and dst_tables must be [num_reqs][blocks]")
     if (mass_in is None) != (mass_out is None):
         raise ValueError("mass_in and mass_out come together")
     if mass_in is not None:
@@ -1222,10 +1222,22 @@ def compact_cache(pool: KVPool, src_tables: torch.Tensor, dst_tables: torch.Tens
             raise ValueError("mass_in and mass_out must have one shape")
     dev = _device_of(kept, "kept")
     _pool_on(pool, dev)
-    _explain(dev, (kept, "kept", _I32, True), (kept_lens, "kept_lens", _I32, True),
-             (src_tables, "src_tables", _I32, True), (dst_tables, "dst_tables", _I32, True),
-             (mass_in, "mass_in", _F32, True), (mass_out, "mass_out", _F32, True),
-             (idx_mapping, "idx_mapping", _I32, True))
+    if not (kept.dtype is _I32 is kept_lens.dtype and src_tables.dtype is _I32 is dst_tables.dtype
+            and (kept_lens.get_device() == src_tables.get_device() == dst_tables.get_device()
+                 == dev)
+            and kept.is_contiguous() and kept_lens.is_contiguous()
+            and src_tables.is_contiguous() and dst_tables.is_contiguous()
+            and (mass_in is None or (
+                mass_in.dtype is _F32 is mass_out.dtype
+                and mass_in.get_device() == mass_out.get_device() == dev
+                and mass_in.is_contiguous() and mass_out.is_contiguous()))
+            and (idx_mapping is None or (
+                idx_mapping.dtype is _I32 and idx_mapping.get_device() == dev
+                and idx_mapping.is_contiguous()))):
+        _explain(dev, (kept, "kept", _I32, True), (kept_lens, "kept_lens", _I32, True),
+                 (src_tables, "src_tables", _I32, True), (dst_tables, "dst_tables", _I32, True),
+                 (mass_in, "mass_in", _F32, True), (mass_out, "mass_out", _F32, True),
+                 (idx_mapping, "idx_mapping", _I32, True))
     rows, places = (0, 0) if mass_in is None else mass_in.shape
     st = (_lib or lib()).pa_compact_cache(
         pool.ref(), src_tables.data_ptr(), src_tables.shape[1], dst_tables.data_ptr(),

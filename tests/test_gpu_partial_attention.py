@@ -214,6 +214,48 @@ def test_mass_long(cuda_device, D, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_mass_of_many_chunks(cuda_device, D, fp8):
+    """More row tiles than SMs, several of them in the run of one CTA, some cut by its
+    end, and decodes between them."""
+    rng = np.random.default_rng(24)
+    seqs = [int(x) for x in rng.integers(40, 400, 50)]
+    new = [int(x) for x in rng.integers(20, 41, 50)]
+    new[7] = new[20] = 1
+    new[31] = 0
+    check(*run_mass(cuda_device, rng, seqs, new, 12, 2, D, 16, fp8, window=30))
+    assert pa.get_error() == pa.PA_OK
+
+
+def test_mass_on_two_streams(cuda_device):
+    """Two calls at once, each with a workspace and a mass of its own."""
+    dev, B, Hkv, Hq, D = cuda_device, 16, 2, 8, 128
+    rng = np.random.default_rng(25)
+    jobs = []
+    for seqs, new in (([3000, 2000], [40, 64]), ([2500, 1800, 900], [1, 50, 2])):
+        table, qsl, blocks = batch(rng, seqs, new, B, dev)
+        pool = make_pool(rng, blocks, Hkv, B, D, False, dev)
+        q = torch.from_numpy(rng.standard_normal((int(qsl[-1]), Hq, D))).to(dev).bfloat16()
+        old = torch.rand((len(seqs), max(seqs)), device=dev)
+        qh, sh = np.array(qsl, np.int32), np.array(seqs, np.int32)
+        ws = torch.empty(pa.attention_mass_workspace_size(qh, sh, Hq, Hkv), dtype=torch.uint8,
+                         device=dev)
+        jobs.append((q, old, torch.zeros_like(old), i32(qsl, dev), i32(seqs, dev), qh, sh,
+                     i32(table, dev), pool, ws, table))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(3):
+        for s, (q, old, out, dq, ds, qh, sh, tab, pool, ws, _) in zip(streams, jobs):
+            pa.attention_mass(q, old, out, dq, ds, qh, sh, tab, pool, 0.1, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert pa.get_error() == pa.PA_OK
+    for q, old, out, dq, ds, qh, sh, tab, pool, ws, table in jobs:
+        check(ref.f64(out), *ref.mass(ref.f64(q), ref.cells(pool.k), ref.f64(old), range(len(sh)),
+                                      table, qh.tolist(), sh.tolist(), B, Hq // Hkv, 0.1, 1.0, 1.0,
+                                      0, np.zeros(old.shape), False))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("new", [3, 40], ids=["streamed", "tiles"])
 def test_mass_numbers_that_are_not_finite(cuda_device, new, fp8):
     """A row that meets a NaN gives NaN to every key that it sees, and to no other

@@ -166,6 +166,17 @@ def test_scores_long(cuda_device):
     assert (np.abs(got - want) <= tol).all()
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (4, 1), (16, 1), (20, 1)])
+def test_scores_of_chunks_among_empty_requests(cuda_device, Hq, Hkv):
+    """No more tokens than requests, most of them in one request."""
+    rng = np.random.default_rng(14)
+    new = [0, 11, 0, 0, 0, 0, 1, 0, 0, 0, 0, 0, 3]
+    seqs = [30, 200, 0, 5, 64, 0, 70, 1, 0, 16, 2, 0, 40]
+    got, want, tol = run_scores(cuda_device, rng, seqs, new, Hq, Hkv, 64, 16, False)
+    assert pa.get_error() == pa.PA_OK
+    assert (np.abs(got - want) <= tol).all()
+
+
 def test_scores_that_are_not_finite(cuda_device):
     """NaN of a query or a bound reaches what it takes part in; bounds are finite by
     construction, so an infinite query times a zero bound is the only other NaN."""
@@ -181,7 +192,7 @@ def test_scores_that_are_not_finite(cuda_device):
     fine = np.isfinite(want)
     assert np.array_equal(np.isnan(got), np.isnan(want)) and np.isnan(want).any()
     assert np.array_equal(got[~fine], want[~fine], equal_nan=True) and np.isinf(want).any()
-    assert (np.abs(got - want)[fine] <= tol[fine]).all()
+    assert (np.abs(got[fine] - want[fine]) <= tol[fine]).all()
 
 
 def test_scores_refuse_what_leaves_the_buffers(cuda_device):
@@ -239,6 +250,25 @@ def test_select_blocks(cuda_device, first, last, k, kind):
         for h in range(H):
             want = ref.pick(x[t, h], p // B + 1, first, last, k)
             assert np.array_equal(got[t, h], want), (t, h)
+
+
+@pytest.mark.parametrize("kind", ["plain", "ties", "special"])
+def test_select_blocks_of_long_contexts(cuda_device, kind):
+    """Rows that several CTAs share, and rows past what they hold at once."""
+    dev, B, H, k = cuda_device, 16, 2, 70
+    rng = np.random.default_rng(31)
+    for N in (5000, 40000):
+        seqs, new = [N * B, 17, N * B // 2], [2, 1, 1]
+        qsl = np.cumsum([0] + new)
+        x = spoiled(rng, (4, H, N), kind)
+        out = torch.full((4, H, k), 9, dtype=torch.int32, device=dev)
+        pa.select_blocks(torch.from_numpy(x).to(dev), out, i32(qsl, dev), i32(seqs, dev), B,
+                         first=2, last=3)
+        assert pa.get_error() == pa.PA_OK
+        for r, t, p in ref.rows_of(qsl, seqs):
+            for h in range(H):
+                assert np.array_equal(out[t, h].cpu().numpy(),
+                                      ref.pick(x[t, h], p // B + 1, 2, 3, k)), (N, t, h)
 
 
 @pytest.mark.parametrize("places", [7, 1000, 1024, 1025, 4096, 4097, 20000, 32768, 32769, 70001])
