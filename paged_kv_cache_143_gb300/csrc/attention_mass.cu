@@ -20,7 +20,7 @@
 //    and the order of every sum follows from the sizes alone.
 //    The query rows are laid out once per call as shared-memory images of 128
 //    rows, swizzled as the tensor cores read them, which one bulk copy fetches;
-//    behind each image its rows' score factors and, after pass 1, their lse.
+//    behind each image its rows' score factors.
 //
 // E4M3 pools: the codes are multiplied as they are. Up to 16 rows they widen to
 // f16; on tcgen05 a query is the sum of two E4M3 numbers (8 significant bits, all
@@ -42,7 +42,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNarrowRows = 16;     // rows of the streaming form, at the most
 constexpr int kSplitKeys = 1024;    // keys of one of its CTAs
 constexpr int kTile = 128;          // rows, and keys, of a tcgen05 tile
-constexpr int kInfoBytes = 1024;    // behind an image: what its rows' scores are turned with
+constexpr int kInfoBytes = 1024;    // behind an image: the score factors of its rows
 // Of rows 2 i and 2 i + 1 four floats, (factor, factor, -lse, -lse), so that one load
 // feeds one packed multiply-add: the row's factor is at info_at(row), -lse 2 further.
 __device__ __forceinline__ int info_at(int row) { return (row >> 1) * 4 + (row & 1); }
@@ -66,7 +66,6 @@ struct MassParams {
   int narrow_rows;         // rows of a request of this form, at the most
   // tcgen05 form: a step is a row tile of a kv head and a key tile; request r's are the
   // flat steps first_step[r] + (kvh * tiles + row tile) * key tiles + key tile
-  int4* tile_of;           // [n_tiles] (request or -1, row tile, the request's row and key tiles)
   int* first_tile;         // [R], -1: not of this form
   int64_t* first_step;     // [R + 1]
   uint8_t* images;         // [n_tiles][Hkv][image]
@@ -369,11 +368,7 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
   if (ti == 0 && kvh == 0) {
     const int64_t step = before(p, r, [&](const MassReq& x) { return steps_of(p, x); });
     if (tid == 0) p.first_step[r] = step;
-    if (r == p.R - 1) {  // the end, and entries past the device's rows
-      if (tid == 0) p.first_step[p.R] = step + steps_of(p, m);
-      for (int64_t x = first + tiles + tid; x < p.n_tiles; x += kTile)
-        p.tile_of[x] = make_int4(-1, 0, 0, 0);
-    }
+    if (tid == 0 && r == p.R - 1) p.first_step[p.R] = step + steps_of(p, m);
   }
   if (!tiles) {
     if (reporter) p.first_tile[r] = -1;
@@ -389,13 +384,8 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
     if (tid == 0) {
       p.first_tile[r] = fits ? (int)first : -1;
       if (!fits) raise_error(p.err, kErrBounds);
-      // (no CTA comes to tiles past the grid's)
-      for (int64_t x = first + gridDim.x; x < first + tiles && x < p.n_tiles; ++x)
-        p.tile_of[x] = make_int4(-1, 0, 0, 0);
     }
   }
-  if (tid == 0 && kvh == 0 && first + ti < p.n_tiles)
-    p.tile_of[first + ti] = make_int4(fits ? r : -1, ti, tiles, key_tiles);
   if (!fits) return;
   const int tile = (int)first + ti;
   uint8_t* image = p.images + ((int64_t)tile * p.Hkv + kvh) * W::kImage;
@@ -460,7 +450,7 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
       *reinterpret_cast<uint4*>(image + kTile * D + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
-  reinterpret_cast<float*>(image + W::kTileBytes)[info_at(tid)] = sc;
+  reinterpret_cast<float*>(image + W::kTileBytes)[tid] = sc;
 }
 
 // Warps 0-15: rows or keys, each group of four the accumulators of every fourth step;
@@ -480,6 +470,7 @@ struct WideTail {
   uint64_t s_full[kGroups], s_empty[kGroups];
   uint32_t tmem;
   int abort;
+  alignas(16) float factors[kGroups][2 * kTile];  // WEIGHTS: what a group turns scores with
 };
 
 // Shared memory of a CTA, one on an SM: two images, and as many stages of 128 keys as
@@ -510,7 +501,7 @@ struct Segment {
   bool on;         // (false: of a request that was left out; nothing to do up to `next`)
   int tile, ti, kvh;
   int key_tile, n;  // first key tile, and how many
-  int piece;        // of the row tile's pieces
+  int piece, pieces;  // of the row tile's pieces, and how many it has
   int64_t next;
   MassReq m;
   int r;
@@ -533,6 +524,7 @@ __device__ __forceinline__ Segment segment_at(const MassParams& p, int64_t f, in
   s.key_tile = (int)(f - start);
   s.n = (int)min((int64_t)keys - s.key_tile, end - f);
   s.piece = (int)(f / p.per_cta - start / p.per_cta);
+  s.pieces = (int)min((start + keys - 1) / p.per_cta - start / p.per_cta + 1, (int64_t)p.pieces);
   s.next = f + s.n;
   return s;
 }
@@ -720,13 +712,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int64_t f0 = f;
       f = s.next;
       if (!s.on) continue;
+      // (WEIGHTS: the warps of a group stop together, and none is still at the last segment's
+      // factors when they are overwritten)
+      if (WEIGHTS && named_bar_or(1 + group, kTile, !ok)) break;
       const int slot = segments & 1;
       ok = wait(&t->image_full[slot], (segments / 2) & 1);
       ++segments;
-      const float* factors = reinterpret_cast<const float*>(images + slot * W::kImage + W::kTileBytes);
       const int first_row = s.ti * kTile;
       const int seen_by_all = s.m.seq - s.m.w;  // the last key that all counted queries see
-      const float sc = factors[info_at(me)];
+      const float sc = reinterpret_cast<const float*>(images + slot * W::kImage + W::kTileBytes)[me];
+      const int64_t unit = (int64_t)s.tile * p.Hkv + s.kvh;
+      float* factors = t->factors[group];
+      if (WEIGHTS) {  // (score factor, -lse) of rows 2 i and 2 i + 1, from the pieces' statistics
+        const float2* part = p.tile_stats + unit * p.pieces * kGroups * kTile + me;
+        factors[info_at(me)] = sc;
+        factors[info_at(me) + 2] = -lse_of(part, s.pieces * kGroups, kTile);
+        named_bar_sync(1 + group, kTile);
+      }
       const uint64_t sc2 = f2_pack(sc, sc);
       const int sees = seen_by_all + min(first_row + me, s.m.rows - 1) / p.g + 1;  // keys of the row
       float total = 0.f, ref = -INFINITY;
@@ -845,8 +847,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       i0 += s.n;
       if (!WEIGHTS)
-        p.tile_stats[((((int64_t)s.tile * p.Hkv + s.kvh) * p.pieces + s.piece) * kGroups + group) * kTile +
-                     me] = make_float2(ref, total);
+        p.tile_stats[((unit * p.pieces + s.piece) * kGroups + group) * kTile + me] = make_float2(ref, total);
       __syncwarp();
       if (lane == 0) mbar_arrive(&t->image_empty[slot]);
     }
@@ -855,24 +856,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kWideCols);
-}
-
-// The rows' lse into the images, from the pieces' statistics.
-template <int D, bool F8>
-__global__ void __launch_bounds__(kTile) mass_join_kernel(MassParams p) {
-  using W = WideGeo<D, F8>;
-  launch_dependents();
-  grid_dependency_wait();
-  const int tile = blockIdx.x / p.Hkv, kvh = blockIdx.x - tile * p.Hkv;
-  const int4 who = p.tile_of[tile];
-  if (who.x < 0) return;
-  const int64_t start = p.first_step[who.x] + ((int64_t)kvh * who.z + who.y) * who.w;
-  const int n = (int)min((start + who.w - 1) / p.per_cta - start / p.per_cta + 1, (int64_t)p.pieces);
-  float* info =
-      reinterpret_cast<float*>(p.images + (int64_t)blockIdx.x * W::kImage + W::kTileBytes);
-  info[info_at(threadIdx.x) + 2] =
-      -lse_of(p.tile_stats + (int64_t)blockIdx.x * p.pieces * kGroups * kTile + threadIdx.x, n * kGroups,
-              kTile);
 }
 
 // The steps' sums of each key, over the row tiles of all heads, into the mass.
@@ -907,7 +890,7 @@ struct MassPlan {
   int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows, steps, per_cta, ctas;
   int64_t narrow_keys, wide_keys;
   int splits, pieces, key_tiles;
-  size_t off_stats, off_tile_of, off_first, off_steps, off_images, off_tile_stats, off_sums, total;
+  size_t off_stats, off_first, off_steps, off_images, off_tile_stats, off_sums, total;
 };
 
 // What a batch needs, from its mirrors alone (head_dim 128's images serve 64 too).
@@ -948,8 +931,6 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   size_t at = up((size_t)pl.score_floats * 4);
   pl.off_stats = at;
   if (pl.narrow) at = up(at + (size_t)R * Hkv * kNarrowRows * pl.splits * sizeof(float2));
-  pl.off_tile_of = at;
-  at = up(at + (size_t)pl.n_tiles * sizeof(int4));
   pl.off_first = at;
   if (pl.n_tiles) at = up(at + (size_t)R * sizeof(int));
   pl.off_steps = at;
@@ -1041,8 +1022,6 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
   const dim3 ctas((unsigned)pl.ctas);
   st = launch_after(mass_tile_kernel<D, F8, false>, ctas, kWideThreads, wide_smem, s, true, tmap, p);
   if (st != PA_OK) return st;
-  st = launch_after(mass_join_kernel<D, F8>, dim3((unsigned)(pl.n_tiles * p.Hkv)), kTile, 0, s, true, p);
-  if (st != PA_OK) return st;
   st = launch_after(mass_tile_kernel<D, F8, true>, ctas, kWideThreads, wide_smem, s, true, tmap, p);
   if (st != PA_OK) return st;
   return launch_after(mass_add_kernel, dim3((unsigned)((pl.wide_keys + kSumThreads - 1) / kSumThreads), (unsigned)p.R),
@@ -1124,7 +1103,6 @@ extern "C" pa_status pa_attention_mass(
   p.split_stats = reinterpret_cast<float2*>(ws + pl.off_stats);
   p.splits = pl.splits;
   p.narrow_rows = (int)pl.max_narrow_rows;
-  p.tile_of = reinterpret_cast<int4*>(ws + pl.off_tile_of);
   p.first_tile = reinterpret_cast<int*>(ws + pl.off_first);
   p.images = ws + pl.off_images;
   p.tile_stats = reinterpret_cast<float2*>(ws + pl.off_tile_stats);
