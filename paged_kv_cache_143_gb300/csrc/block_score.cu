@@ -394,23 +394,25 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 3) block_score_kernel(ScoreP
   }
 }
 
-// Chunks: a matrix product of full size, [hi lo] (128 blocks) x [q+ q-] (256 columns)
-// on tcgen05. A CTA keeps q+ and q- of its row tile in shared memory as the operand of
-// 256 columns (N; cut to what is there) and streams the bounds of 128 blocks at a time,
-// their least keys, then their greatest, as the operand of 128 rows: a thread of the
-// copy warps brings 16 bytes by cp.async straight to their swizzled place. Two groups
-// of four warps read the two accumulators in turn (a thread owns a block and takes the
-// maximum over the heads in registers), so that neighbouring threads write neighbouring
-// blocks' scores.
-constexpr int kChunkThreads = 416;  // warps 0-7: scores; 8-11: copies; 12: MMAs
-constexpr int kChunkCopy = 8, kChunkMma = 12;
-constexpr int kChunkCols = 256;
+// Chunks: a matrix product of full size, [lo hi] (128 blocks) x [q- q+] (112 columns)
+// on tcgen05. A CTA keeps q- and q+ of its row tile in shared memory as the operand of
+// up to 112 columns and streams the bounds of 128 blocks at a time, 64 dims a stage, as
+// the operand of 128 rows: a thread of the copy warps brings 16 bytes by cp.async
+// straight to their swizzled place. Four warps read the two accumulators in turn (a
+// thread owns a block and takes the maximum over the heads in registers), so that
+// neighbouring threads write neighbouring blocks' scores. What bounds it is a CTA's
+// start (its row tile, its columns, the first bounds: about 4 us for 5 to 9 us of work),
+// which the other CTA on the SM hides: 3 chunks on up to 33k tokens take 33 us, 37 with
+// one CTA of 256 columns, where the products alone would take 8.
+constexpr int kChunkThreads = 288;  // warps 0-3: scores; 4-7: copies; 8: MMAs
+constexpr int kChunkCopy = 4, kChunkMma = 8;
+constexpr int kChunkCols = 112;
 constexpr int kChunkStages = 3;
 
 template <int D>
 struct ChunkSmem {
-  static constexpr int kHalf = 128 * 128;                 // 64 dims of 128 blocks
-  static constexpr int kStage = D / 64 * kHalf;
+  static constexpr int kStage = 128 * 128;                // 64 dims of 128 blocks
+  static constexpr int kSteps = 2 * D / 64;               // of a tile: least keys, then greatest
   static constexpr int kColHalf = kChunkCols * 128;       // 64 dims of 256 columns
   static constexpr int kOffRing = 2 * (D / 64) * kColHalf;  // q- (with the least keys), q+
   static constexpr int kOffTail = kOffRing + kChunkStages * kStage;
@@ -509,7 +511,7 @@ __device__ __forceinline__ void write_scores(const ScoreParams& p, const ScoreTi
 }
 
 template <int D>
-__global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScoreParams p) {
+__global__ void __launch_bounds__(kChunkThreads, 2) chunk_score_kernel(ScoreParams p) {
   using S = ChunkSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* cols = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScorePara
       mbar_init(&t->full[i], 128);
       mbar_init(&t->empty[i], 1);
     }
-    mbar_init(&t->q_ready, 256);
+    mbar_init(&t->q_ready, 128);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&t->s_full[i], 1);
       mbar_init(&t->s_empty[i], 4);
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScorePara
     fence_mbar_init();
   }
   if (warp == kChunkMma) {
-    tc::tmem_alloc(&t->tmem, 512);
+    tc::tmem_alloc(&t->tmem, 256);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
@@ -551,39 +553,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScorePara
   constexpr int kPieces = D / 8;  // 16-byte pieces of a row of dims
   if (warp >= kChunkCopy && warp < kChunkMma) {
     // ------------------------------------------------------------- copies
-    // a warp's lanes bring 32 / kPieces blocks at once; lane l knows block 32 w + l's id
-    constexpr int kAtOnce = 32 / kPieces;
-    const int w = warp - kChunkCopy, piece = lane % kPieces;
+    // a warp's lanes bring 64 dims of four blocks at once; lane l knows block 32 w + l's id
+    const int w = warp - kChunkCopy, piece = lane & 7;
     const int32_t* table = p.tables + (int64_t)s.r * p.max_blocks;
     auto fetch = [&](int i) {
       const int blk = first + i * 128 + w * 32 + lane;
       return i < n_tiles && blk < s.n_blocks ? __ldg(table + blk) : -1;
     };
-    int id = fetch(0), next = -1;
+    int id = fetch(0), st = 0;
+    unsigned phase = 1;  // of a stage's empty barrier, once all have been filled
     bool ok = true;
-    int step = 0;
-    for (; step < 2 * n_tiles && ok; ++step) {
-      const int i = step >> 1, h = step & 1, st = step % kChunkStages;
-      if (step >= kChunkStages) ok = __all_sync(kFull, wait(&t->empty[st], (step / kChunkStages - 1) & 1));
-      if (!ok) break;
-      if (h == 0) next = fetch(i + 1);
+    for (int i = 0, step = 0; i < n_tiles && ok; ++i) {
+      const int next = fetch(i + 1);
       bool good = id >= 0 && id < p.num_blocks;
-      if (!good && h == 0 && first + i * 128 + w * 32 + lane < s.n_blocks) raise_error(p.err, kErrBounds);
+      if (!good && first + i * 128 + w * 32 + lane < s.n_blocks) raise_error(p.err, kErrBounds);
       const int use = good ? id : -1;
-      uint8_t* dst = ring + st * S::kStage + (piece >> 3) * S::kHalf;
+      for (int h = 0; h < S::kSteps; ++h, ++step) {
+        if (step >= kChunkStages) ok = __all_sync(kFull, wait(&t->empty[st], phase));
+        if (!ok) break;
+        uint8_t* dst = ring + st * S::kStage;
 #pragma unroll
-      for (int b = 0; b < 32; b += kAtOnce) {
-        const int mine = b + lane / kPieces;  // of the warp's 32 blocks
-        const int from = __shfl_sync(kFull, use, mine);
-        const int row = w * 32 + mine;
-        const __nv_bfloat16* src =
-            p.bounds + (((int64_t)max(from, 0) * p.Hkv + kvh) * 2 + h) * D + piece * 8;
-        cp_async16_or_zero(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4), src, from >= 0);
+        for (int b = 0; b < 32; b += 4) {
+          const int mine = b + lane / 8;  // of the warp's 32 blocks
+          const int from = __shfl_sync(kFull, use, mine);
+          const int row = w * 32 + mine;
+          const __nv_bfloat16* src =
+              p.bounds + ((int64_t)max(from, 0) * p.Hkv + kvh) * 2 * D + h * 64 + piece * 8;
+          cp_async16_or_zero(dst + row * 128 + ((piece ^ (row & 7)) << 4), src, from >= 0);
+        }
+        // an arrival of this thread once its copies have landed
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&t->full[st]))
+                     : "memory");
+        if (++st == kChunkStages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
-      // an arrival of this thread once its copies have landed
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&t->full[st]))
-                   : "memory");
-      if (h == 1) id = next;
+      id = next;
     }
     cp_async_wait_all();  // what is in flight lands before the CTA ends
   } else if (warp == kChunkMma) {
@@ -592,21 +598,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScorePara
       const uint32_t idesc = tc::idesc_16bit_f32(128, 16, false, false, false) - (2u << 17) +
                              ((uint32_t)(n_cols >> 3) << 17);
       bool ok = wait(&t->q_ready, 0);
-      for (int step = 0; step < 2 * n_tiles && ok; ++step) {
-        const int i = step >> 1, h = step & 1, st = step % kChunkStages, buf = i & 1;
-        if (h == 0 && i >= 2) ok = wait(&t->s_empty[buf], ((i >> 1) - 1) & 1);
-        ok = ok && wait(&t->full[st], (step / kChunkStages) & 1);
-        if (!ok) break;
-        tc::fence_proxy_async_smem();  // cp.async writes as threads do, the MMAs read as copies do
-        tc::fence_after_sync();
-        const uint64_t a = tc::smem_desc_sw128(ring + st * S::kStage, 16, 1024);
-        const uint64_t b = tc::smem_desc_sw128(cols + h * (D / 64) * S::kColHalf, 16, 1024);
+      int st = 0;
+      unsigned phase = 0;
+      for (int i = 0; i < n_tiles && ok; ++i) {
+        const int buf = i & 1;
+        if (i >= 2) ok = wait(&t->s_empty[buf], ((i >> 1) - 1) & 1);
+        for (int h = 0; h < S::kSteps && ok; ++h) {
+          ok = wait(&t->full[st], phase);
+          if (!ok) break;
+          tc::fence_proxy_async_smem();  // cp.async writes as threads do, the MMAs read as copies do
+          tc::fence_after_sync();
+          const uint64_t a = tc::smem_desc_sw128(ring + st * S::kStage, 16, 1024);
+          const uint64_t b = tc::smem_desc_sw128(cols + h * S::kColHalf, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_bf16_ss(tmem + buf * kChunkCols, tc::desc_at(a, (k >> 2) * S::kHalf + (k & 3) * 32),
-                          tc::desc_at(b, (k >> 2) * S::kColHalf + (k & 3) * 32), idesc, h > 0 || k > 0);
-        tc::mma_commit(&t->empty[st]);
-        if (h == 1) tc::mma_commit(&t->s_full[buf]);
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_ss(tmem + buf * 128, tc::desc_at(a, k * 32), tc::desc_at(b, k * 32), idesc,
+                            h > 0 || k > 0);
+          tc::mma_commit(&t->empty[st]);
+          if (++st == kChunkStages) {
+            st = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) tc::mma_commit(&t->s_full[buf]);
       }
     }
     __syncwarp();
@@ -630,12 +644,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScorePara
     mbar_arrive(&t->q_ready);
     const int64_t token = (int64_t)p.Hkv * p.max_blocks;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int buf = warp >> 2;
-    for (int i = buf; i < n_tiles; i += 2) {
+    for (int i = 0; i < n_tiles; ++i) {
+      const int buf = i & 1;
       if (!__all_sync(kFull, wait(&t->s_full[buf], (i >> 1) & 1))) break;
       tc::fence_after_sync();
-      const int blk = first + i * 128 + (tid & 127);
-      const uint32_t tm = tmem + lanes + buf * kChunkCols;
+      const int blk = first + i * 128 + tid;
+      const uint32_t tm = tmem + lanes + buf * 128;
       float* out = p.scores + ((int64_t)s.t0 * p.Hkv + kvh) * p.max_blocks + blk;
       switch (p.gp) {
         case 1: write_scores<1>(p, s, tm, out, token, blk, n_cols); break;
@@ -652,7 +666,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScorePara
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == kChunkMma) tc::tmem_dealloc(tmem, 512);
+  if (warp == kChunkMma) tc::tmem_dealloc(tmem, 256);
 }
 
 template <int D, int NH>
@@ -683,7 +697,7 @@ pa_status launch_scores(ScoreParams& p, cudaStream_t stream) {
   const int per = decodes ? kScoreWarps * 16 : 128;  // blocks of a tile of the CTA
   const int64_t all = slots * p.Hkv * (((int64_t)p.max_blocks + per - 1) / per);
   // A CTA goes through up to 8 tiles, as long as all SMs have a few CTAs (32 decodes on 9k to
-  // 65k tokens: 78 us with 2, 63 with 4, 59 with 8 and 12; 3 chunks on up to 33k: 47, 39, 33).
+  // 65k tokens: 78 us with 2, 63 with 4, 59 with 8 and 12; 3 chunks on up to 33k: 47, 39, 35).
   const int64_t want = all / ((decodes ? 4 : 2) * (int64_t)num_sms());
   p.tiles = (int)(want < 1 ? 1 : want > 8 ? 8 : want);
   const int64_t chunks = ((int64_t)p.max_blocks + per * p.tiles - 1) / (per * p.tiles);
