@@ -711,7 +711,7 @@ pa_status pa_score_blocks(const void* q, const void* bounds, float* scores,
  *   first, last  0 or more, first + last <= k
  *
  * Exact: of equal scores the lower index is taken (0 and -0 are equal), NaN
- * counts above every number.
+ * counts above every number. PA_ERR_UNSUPPORTED: k above 2^31 - 65536.
  */
 pa_status pa_select_blocks(const float* scores, const int32_t* query_start_loc,
                            const int32_t* seq_lens, int32_t num_reqs, int32_t num_tokens,
@@ -770,7 +770,8 @@ pa_status pa_sparse_forward(const void* q, void* out, const int32_t* query_start
  * device lengths that stay at or below them, request by request; others set
  * PA_ERR_DEVICE_BOUNDS and are left out.
  * PA_ERR_INVALID: mirrors as for pa_forward, a length above mass_stride, a
- * workspace too small. PA_ERR_UNSUPPORTED: more than 65535 requests.
+ * workspace too small. PA_ERR_UNSUPPORTED: more than 65535 requests, a length
+ * above 2^31 - 65536.
  */
 size_t pa_attention_mass_workspace_size(const int32_t* qsl_host, const int32_t* seq_lens_host,
                                         int32_t num_reqs, int32_t num_q_heads,
@@ -821,7 +822,7 @@ pa_status pa_select_tokens(const float* mass, int64_t mass_stride, int32_t max_r
  * they are. The bounds of the moved blocks are made anew by
  * pa_update_block_bounds without query_start_loc. A place outside its table, its
  * row of mass or the pool sets PA_ERR_DEVICE_BOUNDS and is skipped. At most
- * 65535 requests (PA_ERR_UNSUPPORTED).
+ * 65535 requests and 2^31 - 65536 places (PA_ERR_UNSUPPORTED).
  */
 pa_status pa_compact_cache(const pa_kv_pool* pool, const int32_t* src_tables, int32_t max_blocks,
                            const int32_t* dst_tables, int32_t dst_blocks, const int32_t* kept,

@@ -87,7 +87,7 @@ __device__ __forceinline__ MassReq rows_of(const MassParams& p, int q0, int end,
   m.q_len = end - q0;
   m.seq = seq;
   const bool fine = q0 >= 0 && end <= p.T && end >= q0 && seq >= m.q_len &&
-                    seq <= (int64_t)p.max_blocks * p.B && seq <= p.mass_stride;
+                    seq <= (int64_t)p.max_blocks * p.B && seq <= p.mass_stride && seq <= kMostTokens;
   m.w = fine ? (p.window > 0 ? min(m.q_len, p.window) : m.q_len) : 0;
   const int64_t rows = (int64_t)m.w * p.g;
   m.rows = rows > 0x3fffffff ? 0 : (int)rows;
@@ -904,7 +904,7 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
     if (q_len < 0 || (q_len > 0 && seq[r] < q_len)) return PA_ERR_INVALID;
     if (q_len == 0) continue;
     const int64_t rows = (window > 0 && q_len > window ? window : q_len) * g;
-    if (rows > 0x3fffffff) return PA_ERR_UNSUPPORTED;
+    if (rows > 0x3fffffff || seq[r] > kMostTokens) return PA_ERR_UNSUPPORTED;
     if (rows <= kNarrowRows) {
       ++pl.narrow;
       pl.score_floats += (int64_t)Hkv * rows * (((int64_t)seq[r] + 15) & ~15ll);

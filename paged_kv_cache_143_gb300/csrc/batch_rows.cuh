@@ -7,6 +7,10 @@
 
 namespace pa {
 
+// The longest list of tokens, candidates or places: below 2^31 by more than any loop here
+// goes past its end.
+constexpr int64_t kMostTokens = 0x7fff0000;
+
 // The last i of [0, n) with f(i) <= x, for f that does not fall (0 if there is
 // none). The lanes of a warp try 32 places at once: one round for up to 32
 // requests, two for 1024, each a load and a vote. All lanes get the answer.

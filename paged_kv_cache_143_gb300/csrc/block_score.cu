@@ -413,7 +413,7 @@ template <int D>
 struct ChunkSmem {
   static constexpr int kStage = 128 * 128;                // 64 dims of 128 blocks
   static constexpr int kSteps = 2 * D / 64;               // of a tile: least keys, then greatest
-  static constexpr int kColHalf = kChunkCols * 128;       // 64 dims of 256 columns
+  static constexpr int kColHalf = kChunkCols * 128;       // 64 dims of the columns
   static constexpr int kOffRing = 2 * (D / 64) * kColHalf;  // q- (with the least keys), q+
   static constexpr int kOffTail = kOffRing + kChunkStages * kStage;
 };

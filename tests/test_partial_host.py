@@ -234,3 +234,15 @@ def test_reference_pick():
     assert ref.pick(x, 7, 2, 1, 4).tolist() == [0, 1, 3, 6]
     assert ref.pick(x, 3, 0, 0, 5).tolist() == [0, 1, 2, -1, -1]
     assert ref.pick(x[5:], 2, 0, 0, 1).tolist() == [0]
+
+
+def test_lengths_at_the_end_of_int32():
+    """Lists of almost 2^31 entries, which loops over them would leave, are refused."""
+    U, most = pa.PA_ERR_UNSUPPORTED, 2 ** 31 - 1
+    L, c = pa.lib(), calls()
+    assert L.pa_select_blocks(P, P, P, 1, 1, 1, 4, 16, 1, 1, most, P, None) == U
+    assert L.pa_select_tokens(P, 4, 1, None, P, 1, 1, 1, most, P, P, None) == U
+    assert c["compact"](k=most) == U
+    seqs = np.array([most], np.int32)
+    assert c["mass"](sh=seqs, mb=2 ** 27, stride=2 ** 31) == U
+    assert pa.attention_mass_workspace_size([0, 1], seqs, 4, 2) == 0
