@@ -52,6 +52,48 @@ __device__ __forceinline__ bool request_span(const int32_t* qsl, const int32_t* 
   return true;
 }
 
+// A worker's run [begin, end) of a batch's units of work, of which request r has
+// units(r): the requests' units one after the other, equal runs for all workers. Unit
+// `begin` is request r's, whose first unit is `base`. Found from the device lengths by
+// each worker for itself (the whole warp calls it): every lane sums a part of the
+// requests, and the part that holds `begin` is gone through in the same way.
+struct BatchRun {
+  int64_t begin, end, base;
+  int r;
+};
+template <class F>
+__device__ __forceinline__ BatchRun batch_run(int R, int64_t workers, int64_t worker, F units) {
+  const int lane = threadIdx.x & 31;
+  BatchRun run{0, 0, 0, 0};
+  int lo = 0, len = R;
+  for (bool top = true; top || len > 1; top = false) {
+    const int step = (len + 31) >> 5;
+    const int from = (int)min((int64_t)lane * step, (int64_t)len), to = min(from + step, len);
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int i = from; i < to; ++i) mine += units(lo + i);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (top) {
+      const int64_t all = __shfl_sync(0xffffffffu, upto, 31), per = (all + workers - 1) / workers;
+      run.begin = min(worker * per, all);
+      run.end = min(run.begin + per, all);
+      if (run.begin == run.end) return run;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, run.base + upto > run.begin);
+    const int who = __ffs(past) - 1;  // (there is one: begin < the units up to the last lane's)
+    run.base += __shfl_sync(0xffffffffu, upto - mine, who);
+    lo += who * step;
+    len = min(step, len - who * step);
+  }
+  run.r = lo;
+  return run;
+}
+
 // The request of row t, or -1 for a row behind the last sequence. The whole warp calls it.
 __device__ __forceinline__ int request_of_row(const int32_t* qsl, int R, int t) {
   const int r = warp_last_le(R, t, [&](int i) { return __ldg(qsl + i); });

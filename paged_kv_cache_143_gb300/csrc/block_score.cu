@@ -11,6 +11,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "batch_rows.cuh"
 #include "mbar_poll.cuh"
 #include "pa_device.cuh"
@@ -202,31 +204,96 @@ struct ScoreParams {
   int max_blocks, R, T, Hq, Hkv, g, B, num_blocks;
   int gp;         // columns that a token takes: g padded to 1, 2, 4 or a multiple of 8
   int tile;       // tokens of a row tile
-  int tiles;      // block tiles that a warp (of 16 blocks), or a CTA (of 128), goes through
   float k_scale;
   unsigned* err;
 };
 
-// The row tile of a CTA: slot x belongs to request r, whose slots begin at
-// qsl[r] / tile + r; false if it has no tokens or its blocks end before `first`.
-struct ScoreTile {
-  int r, t0, nt;   // request, first row of q, tokens
-  int pos0;        // position of the first token
-  int n_blocks;    // blocks that the last token sees
+// A unit of work is UNIT blocks of a row tile (p.tile tokens of a request) of a kv head.
+// A request's are numbered by kv head, row tile and blocks, of which each row tile has as
+// many as the last; every worker has an equal run of the batch's (batch_run), whatever the
+// lengths. (A CTA for each row tile and 512 blocks: 64 decodes of up to 16k tokens 35 us
+// instead of 31, 32 of 9k to 65k 59 instead of 55.)
+struct ScoreReq {
+  int q0, q_len, seq;
+  int tiles, run;  // row tiles; units of one
 };
-__device__ __forceinline__ bool score_tile(const ScoreParams& p, int slot, int64_t first,
-                                           ScoreTile& s) {
-  s.r = warp_last_le(p.R, slot, [&](int x) { return __ldg(p.qsl + x) / p.tile + x; });
-  ReqSpan q;
-  if (!request_span(p.qsl, p.seq_lens, s.r, p.T, (int64_t)p.max_blocks * p.B, p.err, q)) return false;
-  const int j0 = (slot - (q.q0 / p.tile + s.r)) * p.tile;
-  if (j0 < 0 || j0 >= q.q_len) return false;
-  s.t0 = q.q0 + j0;
-  s.nt = min(p.tile, q.q_len - j0);
-  s.pos0 = q.seq - q.q_len + j0;
-  s.n_blocks = (s.pos0 + s.nt - 1) / p.B + 1;
-  return first < s.n_blocks;
+template <int UNIT>
+__device__ __forceinline__ ScoreReq score_request(const ScoreParams& p, int r, bool& bad) {
+  ScoreReq s;
+  s.q0 = __ldg(p.qsl + r);
+  const int end = __ldg(p.qsl + r + 1);
+  s.seq = __ldg(p.seq_lens + r);
+  s.q_len = end - s.q0;
+  const bool fine = s.q0 >= 0 && end <= p.T && s.q0 <= end &&
+                    (s.q_len == 0 || (s.seq >= s.q_len && s.seq <= (int64_t)p.max_blocks * p.B));
+  bad |= !fine;
+  if (!fine) s.q_len = 0;
+  s.tiles = (s.q_len + p.tile - 1) / p.tile;
+  s.run = s.q_len > 0 ? ((s.seq - 1) / p.B + UNIT) / UNIT : 0;
+  return s;
 }
+__device__ __forceinline__ int64_t score_units(const ScoreParams& p, const ScoreReq& s) {
+  return (int64_t)p.Hkv * s.tiles * s.run;
+}
+
+// The part of a worker's run that one row tile of a kv head has.
+struct ScoreTile {
+  int r, kvh, t0, nt;   // request, kv head, first row of q, tokens
+  int pos0;             // position of the first token
+  int first, n_blocks;  // first block, and where the part's blocks end
+};
+template <int UNIT>
+struct ScoreRun {
+  ScoreReq req;
+  int64_t left;               // units
+  int r, kvh, tile, blocks;   // request, kv head, row tile and block unit of the next one
+
+  // The whole warp calls it; false if there is nothing to do.
+  __device__ __forceinline__ bool start(const ScoreParams& p, int64_t workers, int64_t worker) {
+    bool bad = false;
+    const BatchRun run = batch_run(p.R, workers, worker, [&](int x) {
+      return score_units(p, score_request<UNIT>(p, x, bad));
+    });
+    if (bad) raise_error(p.err, kErrBounds);
+    left = run.end - run.begin;
+    if (left <= 0) return false;
+    r = run.r;
+    req = score_request<UNIT>(p, r, bad);
+    const int64_t at = run.begin - run.base, unit = at / req.run;
+    blocks = (int)(at - unit * req.run);
+    kvh = (int)(unit / req.tiles);
+    tile = (int)(unit - (int64_t)kvh * req.tiles);
+    return true;
+  }
+  // The next part, false at the end.
+  __device__ __forceinline__ bool next(const ScoreParams& p, ScoreTile& s) {
+    while (left > 0) {
+      if (kvh == p.Hkv || req.run == 0) {  // (without units: between the run's first and last request)
+        kvh = 0;
+        if (++r >= p.R) return false;  // (cannot be: a request has the unit)
+        bool bad = false;
+        req = score_request<UNIT>(p, r, bad);
+        if (req.run == 0) continue;
+      }
+      const int j0 = tile * p.tile, n = (int)min((int64_t)(req.run - blocks), left);
+      s.r = r;
+      s.kvh = kvh;
+      s.t0 = req.q0 + j0;
+      s.nt = min(p.tile, req.q_len - j0);
+      s.pos0 = req.seq - req.q_len + j0;
+      s.first = blocks * UNIT;
+      s.n_blocks = (int)min((int64_t)((s.pos0 + s.nt - 1) / p.B + 1), (int64_t)s.first + (int64_t)n * UNIT);
+      left -= n;
+      blocks = 0;
+      if (++tile == req.tiles) {
+        tile = 0;
+        ++kvh;
+      }
+      if (s.first < s.n_blocks) return true;
+    }
+    return false;
+  }
+};
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -241,6 +308,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Of N values, N 1, 2, 4 or 8.
+template <int N>
+__device__ __forceinline__ float max_nan(const uint32_t* v) {
+  float x = __uint_as_float(v[0]);
+  if constexpr (N == 2) x = max_nan(x, __uint_as_float(v[1]));
+#pragma unroll
+  for (int i = 1; i + 1 < N; i += 2) x = max_nan(x, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+  if constexpr (N > 2) x = max_nan(x, __uint_as_float(v[N - 1]));
+  return x;
 }
 
 // max(x, 0) and min(x, 0) of two bf16; NaN stays NaN in both
@@ -262,13 +344,15 @@ __device__ __forceinline__ uint4 negative(uint4 v) {
 }
 
 // Decodes (a row tile of at most 8 NH columns): the bounds are what costs, 4 D bytes
-// a (block, kv head) read once. A warp takes 16 blocks as the rows of m16n8k16 MMAs
-// and the (token, head) pairs as columns; q+ and q- stay in registers. The bounds of
-// a block come with one cp.async of the warp (16 bytes a lane) into its ring of two
-// 16-block stages (records 64 bytes apart in banks, so that the 16-byte fragment loads
-// of a quarter-warp do not collide); no warp waits for another. Three CTAs on an SM
-// hide each other's start: 32 decodes of 9k to 65k tokens (8 kv heads) take 59 us, 69
-// with three stages and two CTAs. The maximum over the heads is taken in registers.
+// a (block, kv head) read once. The workers are warps, none of which waits for another:
+// a warp takes 16 blocks as the rows of m16n8k16 MMAs and the (token, head) pairs as
+// columns; q+ and q- stay in registers. The bounds of a block come with one cp.async of
+// the warp (16 bytes a lane) into its ring of two 16-block stages (records 64 bytes apart
+// in banks, so that the 16-byte fragment loads of a quarter-warp do not collide). Three
+// CTAs of four warps run on an SM (two with three stages: 69 us where three took 59).
+// The maximum over the heads is taken in registers. 32 decodes of 9k to 65k tokens (8 kv
+// heads, blocks of 16): 55 us, 5.7 TB/s, 0.84 of the copy rate; 2 to 3 us are the
+// workers' start.
 constexpr int kScoreWarps = 4;
 constexpr int kScoreStages = 2;
 
@@ -289,125 +373,129 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 3) block_score_kernel(ScoreP
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 2, tig = lane & 3;
   uint8_t* ring = smem + warp * Rg::kWarp;
-  const int kvh = blockIdx.x % p.Hkv;
-  const int first = (int)blockIdx.y * kScoreWarps * p.tiles * 16;
-  ScoreTile s;
-  if (!score_tile(p, blockIdx.x / p.Hkv, first, s)) return;
-  const int32_t* table = p.tables + (int64_t)s.r * p.max_blocks;
-  // the warp's tiles are those of 16 blocks from first + 16 warp, 64 apart
-  const int end = min(s.n_blocks, first + kScoreWarps * p.tiles * 16);
-  const int mine = max(0, (end - first - 16 * warp + 63) / 64);
-  auto block_of = [&](int i) { return first + 16 * warp + 64 * i + (lane & 15); };
-  auto fetch = [&](int i) { return i < mine && lane < 16 && block_of(i) < end ? __ldg(table + block_of(i)) : 0; };
-  constexpr int kAtOnce = 512 / Rg::kRecord;  // records that the warp's lanes bring with one load
-  auto issue = [&](int i, int id) {  // (a group of copies for each tile, be there one or not)
-    if (i < mine) {
-      bool on = lane < 16 && block_of(i) < end;
-      if (on && (id < 0 || id >= p.num_blocks)) {
-        raise_error(p.err, kErrBounds);
-        on = false;
+  ScoreRun<16> work;
+  if (!work.start(p, (int64_t)gridDim.x * kScoreWarps, (int64_t)blockIdx.x * kScoreWarps + warp)) return;
+  for (ScoreTile s; work.next(p, s);) {
+    const int kvh = s.kvh, first = s.first, end = s.n_blocks;
+    const int32_t* table = p.tables + (int64_t)s.r * p.max_blocks;
+    const int mine = (end - first + 15) / 16;
+    auto block_of = [&](int i) { return first + 16 * i + (lane & 15); };
+    auto fetch = [&](int i) { return i < mine && lane < 16 && block_of(i) < end ? __ldg(table + block_of(i)) : 0; };
+    constexpr int kAtOnce = 512 / Rg::kRecord;  // records that the warp's lanes bring with one load
+    auto issue = [&](int i, int id) {  // (a group of copies for each tile, be there one or not)
+      if (i < mine) {
+        bool on = lane < 16 && block_of(i) < end;
+        if (on && (id < 0 || id >= p.num_blocks)) {
+          raise_error(p.err, kErrBounds);
+          on = false;
+        }
+        const int use = on ? id : -1, piece = lane % (32 / kAtOnce);
+        uint8_t* dst = ring + (i % kScoreStages) * Rg::kStage + piece * 16;
+#pragma unroll
+        for (int b = 0; b < 16; b += kAtOnce) {
+          const int rec = b + lane / (32 / kAtOnce);
+          const int from = __shfl_sync(kFull, use, rec);
+          if (from >= 0)
+            cp_async16(dst + rec * Rg::kPitch, p.bounds + ((int64_t)from * p.Hkv + kvh) * 2 * D + piece * 8);
+        }
       }
-      const int use = on ? id : -1, piece = lane % (32 / kAtOnce);
-      uint8_t* dst = ring + (i % kScoreStages) * Rg::kStage + piece * 16;
+      cp_async_commit();
+    };
+    for (int i = 0; i < kScoreStages; ++i) issue(i, fetch(i));
+    int next_id = fetch(kScoreStages);
+    uint4 qp[NH][KJ], qn[NH][KJ];  // lane (grp, tig): dims 32 j + 8 tig .. + 7 of column 8 h + grp
 #pragma unroll
-      for (int b = 0; b < 16; b += kAtOnce) {
-        const int rec = b + lane / (32 / kAtOnce);
-        const int from = __shfl_sync(kFull, use, rec);
-        if (from >= 0)
-          cp_async16(dst + rec * Rg::kPitch, p.bounds + ((int64_t)from * p.Hkv + kvh) * 2 * D + piece * 8);
-      }
-    }
-    cp_async_commit();
-  };
-  for (int i = 0; i < kScoreStages; ++i) issue(i, fetch(i));
-  int next_id = fetch(kScoreStages);
-  uint4 qp[NH][KJ], qn[NH][KJ];  // lane (grp, tig): dims 32 j + 8 tig .. + 7 of column 8 h + grp
+    for (int h = 0; h < NH; ++h) {
+      const int col = 8 * h + grp;
+      const int t = min(col / p.gp, s.nt - 1), head = min(col % p.gp, p.g - 1);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + ((int64_t)(s.t0 + t) * p.Hq + kvh * p.g + head) * D + 8 * tig);
 #pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    const int col = 8 * h + grp;
-    const int t = min(col / p.gp, s.nt - 1), head = min(col % p.gp, p.g - 1);
-    const uint4* src = reinterpret_cast<const uint4*>(
-        p.q + ((int64_t)(s.t0 + t) * p.Hq + kvh * p.g + head) * D + 8 * tig);
-#pragma unroll
-    for (int j = 0; j < KJ; ++j) {
-      const uint4 v = __ldg(src + 4 * j);
-      qp[h][j] = positive(v);
-      qn[h][j] = negative(v);
-    }
-  }
-  for (int i = 0; i < mine; ++i) {
-    const int st = i % kScoreStages;
-    cp_async_wait<kScoreStages - 1>();
-    __syncwarp();
-    float acc[NH][2][4] = {};
-    const uint8_t* rec = ring + st * Rg::kStage + grp * Rg::kPitch + 16 * tig;
-#pragma unroll
-    for (int j = 0; j < KJ; ++j) {
-      const uint4 l0 = *reinterpret_cast<const uint4*>(rec + 64 * j);
-      const uint4 l1 = *reinterpret_cast<const uint4*>(rec + 8 * Rg::kPitch + 64 * j);
-      const uint4 h0 = *reinterpret_cast<const uint4*>(rec + 2 * D + 64 * j);
-      const uint4 h1 = *reinterpret_cast<const uint4*>(rec + 8 * Rg::kPitch + 2 * D + 64 * j);
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        mma_bf16(acc[h][1], h0.x, h1.x, h0.y, h1.y, qp[h][j].x, qp[h][j].y);
-        mma_bf16(acc[h][0], l0.x, l1.x, l0.y, l1.y, qn[h][j].x, qn[h][j].y);
-        mma_bf16(acc[h][1], h0.z, h1.z, h0.w, h1.w, qp[h][j].z, qp[h][j].w);
-        mma_bf16(acc[h][0], l0.z, l1.z, l0.w, l1.w, qn[h][j].z, qn[h][j].w);
+      for (int j = 0; j < KJ; ++j) {
+        const uint4 v = __ldg(src + 4 * j);
+        qp[h][j] = positive(v);
+        qn[h][j] = negative(v);
       }
     }
-    __syncwarp();
-    issue(i + kScoreStages, next_id);
-    next_id = fetch(i + kScoreStages + 1);
-    const int b0 = first + 16 * warp + 64 * i;
-    float* out = p.scores + ((int64_t)s.t0 * p.Hkv + kvh) * p.max_blocks + b0 + grp;
-    const int64_t token = (int64_t)p.Hkv * p.max_blocks;
-    // columns 2 tig, 2 tig + 1 of rows grp (e = 0, 1) and grp + 8 (e = 2, 3)
-    if (p.gp == 1) {
+    for (int i = 0; i < mine; ++i) {
+      const int st = i % kScoreStages;
+      cp_async_wait<kScoreStages - 1>();
+      __syncwarp();
+      float acc[NH][2][4] = {};
+      const uint8_t* rec = ring + st * Rg::kStage + grp * Rg::kPitch + 16 * tig;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 2 * tig + (e & 1), blk = b0 + grp + 8 * (e >> 1);
-        if (t < s.nt && (int64_t)blk * p.B <= s.pos0 + t)
-          out[t * token + 8 * (e >> 1)] = (acc[0][0][e] + acc[0][1][e]) * p.k_scale;
+      for (int j = 0; j < KJ; ++j) {
+        const uint4 l0 = *reinterpret_cast<const uint4*>(rec + 64 * j);
+        const uint4 l1 = *reinterpret_cast<const uint4*>(rec + 8 * Rg::kPitch + 64 * j);
+        const uint4 h0 = *reinterpret_cast<const uint4*>(rec + 2 * D + 64 * j);
+        const uint4 h1 = *reinterpret_cast<const uint4*>(rec + 8 * Rg::kPitch + 2 * D + 64 * j);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          mma_bf16(acc[h][1], h0.x, h1.x, h0.y, h1.y, qp[h][j].x, qp[h][j].y);
+          mma_bf16(acc[h][0], l0.x, l1.x, l0.y, l1.y, qn[h][j].x, qn[h][j].y);
+          mma_bf16(acc[h][1], h0.z, h1.z, h0.w, h1.w, qp[h][j].z, qp[h][j].w);
+          mma_bf16(acc[h][0], l0.z, l1.z, l0.w, l1.w, qn[h][j].z, qn[h][j].w);
+        }
       }
-      continue;
-    }
-    float m[NH][2];
+      __syncwarp();
+      issue(i + kScoreStages, next_id);
+      next_id = fetch(i + kScoreStages + 1);
+      const int b0 = first + 16 * i;
+      float* out = p.scores + ((int64_t)s.t0 * p.Hkv + kvh) * p.max_blocks + b0 + grp;
+      const int64_t token = (int64_t)p.Hkv * p.max_blocks;
+      // columns 2 tig, 2 tig + 1 of rows grp (e = 0, 1) and grp + 8 (e = 2, 3)
+      if (p.gp == 1) {
 #pragma unroll
-    for (int h = 0; h < NH; ++h)
+        for (int e = 0; e < 4; ++e) {
+          const int t = 2 * tig + (e & 1), blk = b0 + grp + 8 * (e >> 1);
+          if (t < s.nt && (int64_t)blk * p.B <= s.pos0 + t)
+            out[t * token + 8 * (e >> 1)] = (acc[0][0][e] + acc[0][1][e]) * p.k_scale;
+        }
+        continue;
+      }
+      float m[NH][2];
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int ri = 0; ri < 2; ++ri) {
+          float x = max_nan(acc[h][0][2 * ri] + acc[h][1][2 * ri],
+                            acc[h][0][2 * ri + 1] + acc[h][1][2 * ri + 1]);
+          if (p.gp >= 4) x = max_nan(x, __shfl_xor_sync(kFull, x, 1));
+          if (p.gp >= 8) x = max_nan(x, __shfl_xor_sync(kFull, x, 2));
+          m[h][ri] = x;
+        }
+      const int t = NH == 1 ? 2 * tig / p.gp : 0;             // the token of this lane's columns
+      const int writer = NH == 1 ? tig & ~(p.gp / 2 - 1) : 0;  // and the lane that writes for it
 #pragma unroll
       for (int ri = 0; ri < 2; ++ri) {
-        float x = max_nan(acc[h][0][2 * ri] + acc[h][1][2 * ri],
-                          acc[h][0][2 * ri + 1] + acc[h][1][2 * ri + 1]);
-        if (p.gp >= 4) x = max_nan(x, __shfl_xor_sync(kFull, x, 1));
-        if (p.gp >= 8) x = max_nan(x, __shfl_xor_sync(kFull, x, 2));
-        m[h][ri] = x;
+        const int blk = b0 + grp + 8 * ri;
+        const float x = NH == 1 ? m[0][ri] : max_nan(m[0][ri], m[NH - 1][ri]);
+        if (tig == writer && t < s.nt && (int64_t)blk * p.B <= s.pos0 + t)
+          out[t * token + 8 * ri] = x * p.k_scale;
       }
-    const int t = NH == 1 ? 2 * tig / p.gp : 0;             // the token of this lane's columns
-    const int writer = NH == 1 ? tig & ~(p.gp / 2 - 1) : 0;  // and the lane that writes for it
-#pragma unroll
-    for (int ri = 0; ri < 2; ++ri) {
-      const int blk = b0 + grp + 8 * ri;
-      const float x = NH == 1 ? m[0][ri] : max_nan(m[0][ri], m[NH - 1][ri]);
-      if (tig == writer && t < s.nt && (int64_t)blk * p.B <= s.pos0 + t)
-        out[t * token + 8 * ri] = x * p.k_scale;
     }
   }
 }
 
-// Chunks: a matrix product of full size, [lo hi] (128 blocks) x [q- q+] (112 columns)
-// on tcgen05. A CTA keeps q- and q+ of its row tile in shared memory as the operand of
-// up to 112 columns and streams the bounds of 128 blocks at a time, 64 dims a stage, as
-// the operand of 128 rows: a thread of the copy warps brings 16 bytes by cp.async
-// straight to their swizzled place. Four warps read the two accumulators in turn (a
-// thread owns a block and takes the maximum over the heads in registers), so that
-// neighbouring threads write neighbouring blocks' scores. What bounds it is a CTA's
-// start (its row tile, its columns, the first bounds: about 4 us for 5 to 9 us of work),
-// which the other CTA on the SM hides: 3 chunks on up to 33k tokens take 33 us, 37 with
-// one CTA of 256 columns, where the products alone would take 8.
-constexpr int kChunkThreads = 288;  // warps 0-3: scores; 4-7: copies; 8: MMAs
-constexpr int kChunkCopy = 4, kChunkMma = 8;
-constexpr int kChunkCols = 112;
-constexpr int kChunkStages = 3;
+// Chunks: a matrix product of full size, [lo hi] (128 blocks) x [q- q+] (224 columns)
+// on tcgen05; the workers are CTAs, one on an SM. Seven warps keep q- and q+ of a row
+// tile in shared memory as the operand of up to 224 columns and have the next one's in
+// registers when its products begin; four bring the bounds of 128 blocks, 64 dims a
+// stage, as the operand of 128 rows: 16 bytes a thread by cp.async, straight to their
+// swizzled place. Four warps read the two accumulators in turn (a thread owns a block
+// and takes the maximum over the heads in registers), so that neighbouring threads
+// write neighbouring blocks' scores. What bounds it is shared memory: for a unit of 128
+// blocks the products read 114 KB of columns and 64 KB of bounds, which were written
+// there before, 1900 cycles of its 128 bytes (the products alone: 1800 at the rate that
+// is reached elsewhere); and 2 us a row tile until the next columns are written. 3 chunks
+// on up to 33k tokens (8 kv heads, blocks of 32): 31 us, 8 of them the ends of the launch;
+// 4 on up to 64k (blocks of 64): 75. Two CTAs an SM of 112 columns: 33 and 86. Eight
+// warps for the scores, or for the copies, or fewer fences for the copies: level.
+constexpr int kChunkThreads = 512;  // warps 0-3: scores; 4-7: copies; 8: MMAs; 9-15: columns
+constexpr int kChunkCopy = 4, kChunkMma = 8, kChunkColumn = 9;
+constexpr int kChunkCols = 224;
+constexpr int kChunkStages = 7;
+constexpr int kChunkBuf = 256;  // tensor memory columns of an accumulator
 
 template <int D>
 struct ChunkSmem {
@@ -419,7 +507,7 @@ struct ChunkSmem {
 };
 struct ChunkTail {
   uint64_t full[kChunkStages], empty[kChunkStages];
-  uint64_t q_ready, s_full[2], s_empty[2];
+  uint64_t q_ready, q_empty, s_full[2], s_empty[2];
   uint32_t tmem;
   int abort;
 };
@@ -452,29 +540,21 @@ struct BlockScores {
       if (seen && tok0 + 32 / GP <= nt) {
 #pragma unroll
         for (int e = 0; e < 32; e += GP) {
-          float x = __uint_as_float(v[e]);
-#pragma unroll
-          for (int i = 1; i < GP; ++i) x = max_nan(x, __uint_as_float(v[e + i]));
-          *out = x * k_scale;
+          *out = max_nan<GP>(v + e) * k_scale;
           out += token;
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 32; e += GP) {
-          float x = __uint_as_float(v[e]);
-#pragma unroll
-          for (int i = 1; i < GP; ++i) x = max_nan(x, __uint_as_float(v[e + i]));
           const int tok = tok0 + e / GP;
-          if (tok >= from && tok < nt) *out = x * k_scale;
+          if (tok >= from && tok < nt) *out = max_nan<GP>(v + e) * k_scale;
           out += token;
         }
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 32; e += 8) {
-        float x = __uint_as_float(v[e]);
-#pragma unroll
-        for (int i = 1; i < 8; ++i) x = max_nan(x, __uint_as_float(v[e + i]));
+        const float x = max_nan<8>(v + e);
         run = in_token ? max_nan(run, x) : x;
         in_token += 8;
         if (in_token == gp) {
@@ -511,25 +591,22 @@ __device__ __forceinline__ void write_scores(const ScoreParams& p, const ScoreTi
 }
 
 template <int D>
-__global__ void __launch_bounds__(kChunkThreads, 2) chunk_score_kernel(ScoreParams p) {
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_score_kernel(ScoreParams p) {
   using S = ChunkSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* cols = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* ring = cols + S::kOffRing;
   ChunkTail* t = reinterpret_cast<ChunkTail*>(cols + S::kOffTail);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kvh = blockIdx.x % p.Hkv;
-  const int first = (int)blockIdx.y * p.tiles * 128;
-  ScoreTile s;
-  if (!score_tile(p, blockIdx.x / p.Hkv, first, s)) return;
-  const int n_tiles = min(p.tiles, (s.n_blocks - first + 127) / 128);
-  const int n_cols = (s.nt * p.gp + 15) & ~15;
+  ScoreRun<128> work;
+  if (!work.start(p, gridDim.x, blockIdx.x)) return;  // (the same for all warps)
   if (tid == 0) {
     for (int i = 0; i < kChunkStages; ++i) {
       mbar_init(&t->full[i], 128);
       mbar_init(&t->empty[i], 1);
     }
-    mbar_init(&t->q_ready, 128);
+    mbar_init(&t->q_ready, kChunkCols);
+    mbar_init(&t->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&t->s_full[i], 1);
       mbar_init(&t->s_empty[i], 4);
@@ -538,7 +615,7 @@ __global__ void __launch_bounds__(kChunkThreads, 2) chunk_score_kernel(ScorePara
     fence_mbar_init();
   }
   if (warp == kChunkMma) {
-    tc::tmem_alloc(&t->tmem, 256);
+    tc::tmem_alloc(&t->tmem, 2 * kChunkBuf);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
@@ -555,118 +632,146 @@ __global__ void __launch_bounds__(kChunkThreads, 2) chunk_score_kernel(ScorePara
     // ------------------------------------------------------------- copies
     // a warp's lanes bring 64 dims of four blocks at once; lane l knows block 32 w + l's id
     const int w = warp - kChunkCopy, piece = lane & 7;
-    const int32_t* table = p.tables + (int64_t)s.r * p.max_blocks;
-    auto fetch = [&](int i) {
-      const int blk = first + i * 128 + w * 32 + lane;
-      return i < n_tiles && blk < s.n_blocks ? __ldg(table + blk) : -1;
-    };
-    int id = fetch(0), st = 0;
-    unsigned phase = 1;  // of a stage's empty barrier, once all have been filled
+    unsigned step = 0;
     bool ok = true;
-    for (int i = 0, step = 0; i < n_tiles && ok; ++i) {
-      const int next = fetch(i + 1);
-      bool good = id >= 0 && id < p.num_blocks;
-      if (!good && first + i * 128 + w * 32 + lane < s.n_blocks) raise_error(p.err, kErrBounds);
-      const int use = good ? id : -1;
-      for (int h = 0; h < S::kSteps; ++h, ++step) {
-        if (step >= kChunkStages) ok = __all_sync(kFull, wait(&t->empty[st], phase));
-        if (!ok) break;
-        uint8_t* dst = ring + st * S::kStage;
+    for (ScoreTile s; ok && work.next(p, s);) {
+      const int32_t* table = p.tables + (int64_t)s.r * p.max_blocks;
+      auto fetch = [&](int blk) { return blk < s.n_blocks ? __ldg(table + blk) : -1; };
+      int blk = s.first + w * 32 + lane;
+      int id = fetch(blk);
+      for (int b0 = s.first; b0 < s.n_blocks && ok; b0 += 128, blk += 128) {
+        const int next = fetch(blk + 128);
+        const bool good = id >= 0 && id < p.num_blocks;
+        if (!good && blk < s.n_blocks) raise_error(p.err, kErrBounds);
+        const int use = good ? id : -1;
+        const __nv_bfloat16* src[8];
+        unsigned there = 0;
 #pragma unroll
-        for (int b = 0; b < 32; b += 4) {
-          const int mine = b + lane / 8;  // of the warp's 32 blocks
-          const int from = __shfl_sync(kFull, use, mine);
-          const int row = w * 32 + mine;
-          const __nv_bfloat16* src =
-              p.bounds + ((int64_t)max(from, 0) * p.Hkv + kvh) * 2 * D + h * 64 + piece * 8;
-          cp_async16_or_zero(dst + row * 128 + ((piece ^ (row & 7)) << 4), src, from >= 0);
+        for (int b = 0; b < 8; ++b) {
+          const int from = __shfl_sync(kFull, use, 4 * b + lane / 8);  // of the warp's 32 blocks
+          src[b] = p.bounds + ((int64_t)max(from, 0) * p.Hkv + s.kvh) * 2 * D + piece * 8;
+          there |= (unsigned)(from >= 0) << b;
         }
-        // an arrival of this thread once its copies have landed
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&t->full[st]))
-                     : "memory");
-        if (++st == kChunkStages) {
-          st = 0;
-          phase ^= 1;
+#pragma unroll
+        for (int h = 0; h < S::kSteps; ++h, ++step) {
+          const unsigned st = step % kChunkStages, round = step / kChunkStages;
+          if (round > 0) ok = __all_sync(kFull, wait(&t->empty[st], (round - 1) & 1));
+          if (!ok) break;
+          uint8_t* dst = ring + st * S::kStage;
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const int row = w * 32 + 4 * b + lane / 8;
+            cp_async16_or_zero(dst + row * 128 + ((piece ^ (row & 7)) << 4), src[b] + h * 64,
+                               (there >> b) & 1);
+          }
+          // an arrival of this thread once its copies have landed
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                           smem_u32(&t->full[st]))
+                       : "memory");
         }
+        id = next;
       }
-      id = next;
     }
     cp_async_wait_all();  // what is in flight lands before the CTA ends
+  } else if (warp >= kChunkColumn) {
+    // ------------------------------------------------------------ columns
+    const int c = tid - kChunkColumn * 32;  // a column a thread, its loads all at once
+    bool ok = true;
+    unsigned part = 0;
+    for (ScoreTile s; ok && work.next(p, s); ++part) {
+      const bool mine = c < ((s.nt * p.gp + 15) & ~15);
+      const int tok = min(c / p.gp, s.nt - 1), head = min(c % p.gp, p.g - 1);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + ((int64_t)(s.t0 + tok) * p.Hq + s.kvh * p.g + head) * D);
+      uint4 v[kPieces];
+#pragma unroll
+      for (int x = 0; x < kPieces; ++x)
+        if (mine) v[x] = __ldg(src + x);
+      if (part > 0) ok = __all_sync(kFull, wait(&t->q_empty, (part - 1) & 1));
+      if (!ok) break;
+#pragma unroll
+      for (int x = 0; x < kPieces; ++x) {
+        uint8_t* dst = cols + (x >> 3) * S::kColHalf + c * 128 + (((x & 7) ^ (c & 7)) << 4);
+        if (mine) {
+          *reinterpret_cast<uint4*>(dst) = negative(v[x]);
+          *reinterpret_cast<uint4*>(dst + (D / 64) * S::kColHalf) = positive(v[x]);
+        }
+      }
+      tc::fence_proxy_async_smem();
+      mbar_arrive(&t->q_ready);
+    }
   } else if (warp == kChunkMma) {
     // --------------------------------------------------------------- MMAs
-    if (tc::elect_one()) {
+    bool ok = true;
+    unsigned step = 0, part = 0, i = 0;
+    auto all_wait = [&](uint64_t* bar, unsigned parity) { return __all_sync(kFull, wait(bar, parity)); };
+    for (ScoreTile s; ok && work.next(p, s); ++part) {
+      const int n_cols = (s.nt * p.gp + 15) & ~15;
       const uint32_t idesc = tc::idesc_16bit_f32(128, 16, false, false, false) - (2u << 17) +
                              ((uint32_t)(n_cols >> 3) << 17);
-      bool ok = wait(&t->q_ready, 0);
-      int st = 0;
-      unsigned phase = 0;
-      for (int i = 0; i < n_tiles && ok; ++i) {
-        const int buf = i & 1;
-        if (i >= 2) ok = wait(&t->s_empty[buf], ((i >> 1) - 1) & 1);
-        for (int h = 0; h < S::kSteps && ok; ++h) {
-          ok = wait(&t->full[st], phase);
-          if (!ok) break;
-          tc::fence_proxy_async_smem();  // cp.async writes as threads do, the MMAs read as copies do
-          tc::fence_after_sync();
-          const uint64_t a = tc::smem_desc_sw128(ring + st * S::kStage, 16, 1024);
-          const uint64_t b = tc::smem_desc_sw128(cols + h * S::kColHalf, 16, 1024);
+      ok = all_wait(&t->q_ready, part & 1);
+      for (int b0 = s.first; b0 < s.n_blocks && ok; b0 += 128, ++i) {
+        const unsigned buf = i & 1;
+        if (i >= 2) ok = all_wait(&t->s_empty[buf], ((i >> 1) - 1) & 1);
+        if (!ok) break;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_ss(tmem + buf * 128, tc::desc_at(a, k * 32), tc::desc_at(b, k * 32), idesc,
-                            h > 0 || k > 0);
-          tc::mma_commit(&t->empty[st]);
-          if (++st == kChunkStages) {
-            st = 0;
-            phase ^= 1;
+        for (int h = 0; h < S::kSteps; ++h, ++step) {
+          const unsigned st = step % kChunkStages;
+          ok = all_wait(&t->full[st], step / kChunkStages & 1);
+          if (!ok) break;
+          if (tc::elect_one()) {
+            tc::fence_proxy_async_smem();  // cp.async writes as threads do, the MMAs read as copies do
+            tc::fence_after_sync();
+            const uint64_t a = tc::smem_desc_sw128(ring + st * S::kStage, 16, 1024);
+            const uint64_t b = tc::smem_desc_sw128(cols + h * S::kColHalf, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16_ss(tmem + buf * kChunkBuf, tc::desc_at(a, k * 32), tc::desc_at(b, k * 32), idesc,
+                              h > 0 || k > 0);
+            tc::mma_commit(&t->empty[st]);
+            if (h == S::kSteps - 1) {
+              if (b0 + 128 >= s.n_blocks) tc::mma_commit(&t->q_empty);
+              tc::mma_commit(&t->s_full[buf]);
+            }
           }
+          __syncwarp();
         }
-        if (ok) tc::mma_commit(&t->s_full[buf]);
       }
     }
     __syncwarp();
   } else {
-    // -------------------------------------------- columns first, then scores
-    if (const int c = tid; c < n_cols) {  // a column a thread, its loads all at once
-      const int tok = min(c / p.gp, s.nt - 1), head = min(c % p.gp, p.g - 1);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((int64_t)(s.t0 + tok) * p.Hq + kvh * p.g + head) * D);
-      uint4 v[kPieces];
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) v[i] = __ldg(src + i);
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        uint8_t* dst = cols + (i >> 3) * S::kColHalf + c * 128 + (((i & 7) ^ (c & 7)) << 4);
-        *reinterpret_cast<uint4*>(dst) = negative(v[i]);
-        *reinterpret_cast<uint4*>(dst + (D / 64) * S::kColHalf) = positive(v[i]);
-      }
-    }
-    tc::fence_proxy_async_smem();
-    mbar_arrive(&t->q_ready);
+    // ------------------------------------------------------------- scores
     const int64_t token = (int64_t)p.Hkv * p.max_blocks;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    for (int i = 0; i < n_tiles; ++i) {
-      const int buf = i & 1;
-      if (!__all_sync(kFull, wait(&t->s_full[buf], (i >> 1) & 1))) break;
-      tc::fence_after_sync();
-      const int blk = first + i * 128 + tid;
-      const uint32_t tm = tmem + lanes + buf * 128;
-      float* out = p.scores + ((int64_t)s.t0 * p.Hkv + kvh) * p.max_blocks + blk;
-      switch (p.gp) {
-        case 1: write_scores<1>(p, s, tm, out, token, blk, n_cols); break;
-        case 2: write_scores<2>(p, s, tm, out, token, blk, n_cols); break;
-        case 4: write_scores<4>(p, s, tm, out, token, blk, n_cols); break;
-        case 8: write_scores<8>(p, s, tm, out, token, blk, n_cols); break;
-        default: write_scores<0>(p, s, tm, out, token, blk, n_cols);
+    unsigned i = 0;
+    bool ok = true;
+    for (ScoreTile s; ok && work.next(p, s);) {
+      const int n_cols = (s.nt * p.gp + 15) & ~15;
+      for (int b0 = s.first; b0 < s.n_blocks; b0 += 128, ++i) {
+        const unsigned buf = i & 1;
+        const int blk = b0 + tid;
+        ok = __all_sync(kFull, wait(&t->s_full[buf], (i >> 1) & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t tm = tmem + lanes + buf * kChunkBuf;
+        float* out = p.scores + ((int64_t)s.t0 * p.Hkv + s.kvh) * p.max_blocks + blk;
+        switch (p.gp) {
+          case 1: write_scores<1>(p, s, tm, out, token, blk, n_cols); break;
+          case 2: write_scores<2>(p, s, tm, out, token, blk, n_cols); break;
+          case 4: write_scores<4>(p, s, tm, out, token, blk, n_cols); break;
+          case 8: write_scores<8>(p, s, tm, out, token, blk, n_cols); break;
+          default: write_scores<0>(p, s, tm, out, token, blk, n_cols);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t->s_empty[buf]);
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&t->s_empty[buf]);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == kChunkMma) tc::tmem_dealloc(tmem, 256);
+  if (warp == kChunkMma) tc::tmem_dealloc(tmem, 2 * kChunkBuf);
 }
 
 template <int D, int NH>
@@ -693,16 +798,13 @@ pa_status launch_scores(ScoreParams& p, cudaStream_t stream) {
   const bool decodes = p.T <= p.R && p.gp <= 16;
   const int cols = decodes ? (p.gp <= 8 ? 8 : 16) : kChunkCols;
   p.tile = cols / p.gp;
+  // As many CTAs as run at once, or as there can be units (per) for.
   const int64_t slots = p.T / p.tile + (int64_t)p.R;
-  const int per = decodes ? kScoreWarps * 16 : 128;  // blocks of a tile of the CTA
-  const int64_t all = slots * p.Hkv * (((int64_t)p.max_blocks + per - 1) / per);
-  // A CTA goes through up to 8 tiles, as long as all SMs have a few CTAs (32 decodes on 9k to
-  // 65k tokens: 78 us with 2, 63 with 4, 59 with 8 and 12; 3 chunks on up to 33k: 47, 39, 35).
-  const int64_t want = all / ((decodes ? 4 : 2) * (int64_t)num_sms());
-  p.tiles = (int)(want < 1 ? 1 : want > 8 ? 8 : want);
-  const int64_t chunks = ((int64_t)p.max_blocks + per * p.tiles - 1) / (per * p.tiles);
-  if (slots * p.Hkv > 0x7fffffff || chunks > 65535) return PA_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(slots * p.Hkv), (unsigned)chunks);
+  const int per = decodes ? kScoreWarps * 16 : 128;
+  const int64_t chunks = ((int64_t)p.max_blocks + per - 1) / per;
+  const int64_t at_once = (decodes ? 3 : 1) * (int64_t)num_sms();
+  const unsigned grid =
+      (unsigned)(slots >= at_once || chunks >= at_once ? at_once : std::min(at_once, slots * chunks * p.Hkv));
   if (!decodes) {
     if (!chunk_attributes<D>()) return PA_ERR_CUDA;
     chunk_score_kernel<D><<<grid, kChunkThreads, chunk_alloc<D>(), stream>>>(p);

@@ -7,7 +7,7 @@
 // once and bound by HBM, or by L2 where neighbouring tokens list the same blocks.
 //  - A CTA of four warps serves one (token, kv head, up to 16 heads). Each warp
 //    takes every fourth listed block and has a ring of cells of its own in shared
-//    memory that its first lane fills with bulk (E4M3 at D = 128: tensor) copies:
+//    memory that its first lane fills with tensor copies:
 //    no warp waits for another until the end. The list is read 32 entries at a
 //    time, one a lane, and turned into the cells that hold visible keys.
 //  - S^T = K Q^T and O^T += V^T P^T are warp-level m16n8k16 MMAs with the 16 keys
