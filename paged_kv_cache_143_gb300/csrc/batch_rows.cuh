@@ -35,21 +35,19 @@ __device__ __forceinline__ int warp_last_le(int n, int64_t x, F f) {
 struct ReqSpan {
   int q0, q_len, seq;
 };
+__device__ __forceinline__ bool span_fits(const ReqSpan& s, int T, int64_t capacity, unsigned* err) {
+  if (s.q0 >= 0 && s.q_len >= 0 && (int64_t)s.q0 + s.q_len <= T &&
+      (s.q_len == 0 || (s.seq >= s.q_len && s.seq <= capacity)))
+    return true;
+  raise_error(err, kErrBounds);
+  return false;
+}
 __device__ __forceinline__ bool request_span(const int32_t* qsl, const int32_t* seq_lens, int r,
                                              int T, int64_t capacity, unsigned* err, ReqSpan& s) {
   s.q0 = qsl[r];
-  const int end = qsl[r + 1];
+  s.q_len = qsl[r + 1] - s.q0;
   s.seq = seq_lens[r];
-  s.q_len = end - s.q0;
-  if (s.q0 < 0 || end > T || s.q0 > end) {
-    raise_error(err, kErrBounds);
-    return false;
-  }
-  if (s.q_len > 0 && (s.seq < s.q_len || s.seq > capacity)) {
-    raise_error(err, kErrBounds);
-    return false;
-  }
-  return true;
+  return span_fits(s, T, capacity, err);
 }
 
 // A worker's run [begin, end) of a batch's units of work, of which request r has
@@ -94,10 +92,29 @@ __device__ __forceinline__ BatchRun batch_run(int R, int64_t workers, int64_t wo
   return run;
 }
 
-// The request of row t, or -1 for a row behind the last sequence. The whole warp calls it.
-__device__ __forceinline__ int request_of_row(const int32_t* qsl, int R, int t) {
-  const int r = warp_last_le(R, t, [&](int i) { return __ldg(qsl + i); });
-  return t < qsl[r + 1] && t >= qsl[r] ? r : -1;
+// The request of row t and its rows and lengths, or -1 for a row behind the last sequence.
+// The whole warp calls it. One trip to memory for up to 32 requests, and for row t of
+// request t (a batch of decodes); else the search after it.
+__device__ __forceinline__ int span_of_row(const int32_t* qsl, const int32_t* seq_lens, int R, int t,
+                                           ReqSpan& s) {
+  const int lane = threadIdx.x & 31;
+  const int at = R <= 32 ? min(lane, R - 1) : min(t, R - 1);
+  int q0 = __ldg(qsl + at), q1 = __ldg(qsl + at + 1), seq = __ldg(seq_lens + at), r = at;
+  if (R <= 32) {
+    r = max(__popc(__ballot_sync(0xffffffffu, lane < R && q0 <= t)) - 1, 0);
+    q0 = __shfl_sync(0xffffffffu, q0, r);
+    q1 = __shfl_sync(0xffffffffu, q1, r);
+    seq = __shfl_sync(0xffffffffu, seq, r);
+  } else if (t < q0 || t >= q1) {
+    r = warp_last_le(R, t, [&](int i) { return __ldg(qsl + i); });
+    q0 = __ldg(qsl + r);
+    q1 = __ldg(qsl + r + 1);
+    seq = __ldg(seq_lens + r);
+  }
+  s.q0 = q0;
+  s.q_len = q1 - q0;
+  s.seq = seq;
+  return t >= q0 && t < q1 ? r : -1;
 }
 
 }  // namespace pa

@@ -6,20 +6,25 @@
 // Scores become 32-bit keys in the order of the numbers (NaN above all, forced
 // candidates above NaN, -0 as 0). The k-th greatest key is found eight bits at a time
 // from the top: of the keys that agree with what is found so far, a histogram in shared
-// memory counts the next eight bits, and the digit is the one in which the k-th falls.
-// Keys above the threshold are taken, and of those equal to it as many as are left,
-// from the lowest index: one running count of both gives each candidate its place in
-// the list. Counts are whole numbers, so nothing depends on the order of the atomics.
-//  - A CTA of 128 threads (512 for more than 1024 candidates) holds eight candidates a
-//    thread in registers; a row of more than 4096 is shared by a cluster of 2, 4 or 8
-//    CTAs (histograms and counts joined through distributed shared memory), and one of
-//    more than 32768 read again for every pass.
-//  - What bounds it is latency (a few hundred kilobytes for a whole batch): a pass is
-//    an atomic a candidate, and the digit, which one warp works out for all (every warp
-//    for itself took more issue slots than the candidates). Replayed from a graph, 256
-//    rows of up to 900, 2300 and 4063 candidates take 7.2, 8.3 and 9.9 us, 24 rows of
-//    32000 14.1, one of 100000 50, rows that are taken whole 2.5 to 3. 256 threads of
-//    sixteen candidates and 1024 of four: slower by 1 to 3 us.
+// memory counts the next eight bits, and the digit is the one in which the k-th falls
+// (the search ends early where all keys of the digit are taken). Keys above the threshold
+// are taken, and of those equal to it as many as are left, from the lowest index: one
+// running count of both gives each candidate its place in the list. Counts are whole
+// numbers, so nothing depends on the order of the atomics.
+//  - A CTA of 128 threads (256 for more than 1024 candidates, 512 for more than 2048)
+//    holds eight candidates a thread in registers, a warp a run of them in the row, so
+//    that places follow from votes and one sum over the warps; a row of more than 4096
+//    is shared by a cluster of 2, 4 or 8 CTAs (histograms joined through distributed
+//    shared memory, with them what the CTAs before take), and one of more than 32768
+//    read again for every pass.
+//  - What bounds it is latency (a few hundred kilobytes for a whole batch): two trips to
+//    memory until the keys are there, and a pass is an atomic a candidate and the digit,
+//    which one warp works out for all (every warp for itself took more issue slots than
+//    the candidates): 1450 cycles, 2900 in a cluster. Replayed from a graph, 256 rows of
+//    up to 900, 2300 and 4063 candidates take 6.4, 7.5 and 8.4 us, 24 rows of 32000
+//    12, one of 100000 38, rows that are taken whole 2 to 3; 16000 rows of 900 68.
+//    1024 bins between the least and the greatest key, and the last few ranked one by
+//    one: 9.2 and 17.
 #include <cooperative_groups.h>
 
 #include "batch_rows.cuh"
@@ -56,19 +61,17 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 constexpr int kBins = 256;
+constexpr int kThreadsAtOnce = 1536;  // of an SM
 
-template <int THREADS, int EACH>
+template <int THREADS>
 struct SelectTail {
-  alignas(16) int hist[4][kBins];         // of this CTA, pass by pass
-  alignas(16) int total[kBins];           // of the cluster
-  int2 counts[EACH * THREADS / 32];  // of a round, by place and warp: keys above the threshold
-                                     // and equal to it; then the sums of those before
-  int2 round;                        // a round's counts
-  uint32_t digit;                    // a pass's digit, and which of its keys is wanted
-  int rest;
-  int row_state, row_n;              // what the row is: 0 nothing to do, 1 candidates
+  alignas(16) int hist[4][kBins];  // of this CTA, pass by pass
+  alignas(16) int total[kBins];    // of the cluster
+  int digit, rest, in_bin;         // a pass's digit, which of its keys is wanted, and of how many
+  int2 ahead[THREADS / 32];        // of a warp's bins: keys that the CTAs before take, and ties
+  int2 counts[THREADS / 32];       // of a warp's keys of a round: those above the threshold, and equal to it
+  int row_state, row_n;            // what the row is: 0 nothing to do, 1 candidates
   const float* row_src;
-  int cta_above, cta_equal;
 };
 
 // One more in a bin, where `on`: predicated, so that a thread's candidates go out one
@@ -82,8 +85,9 @@ __device__ __forceinline__ void count_if(bool on, int* bin) {
 }
 
 // The digit into which the `left`-th key from the top falls, and which of that digit's
-// keys it is (from 1). The whole warp calls it; lane l has bins 255 - 8 l and below.
-__device__ __forceinline__ void find_digit(const int* hist, int& left, uint32_t& digit) {
+// keys it is (from 1), of how many. The whole warp calls it; lane l has bins 255 - 8 l and
+// below.
+__device__ __forceinline__ void find_digit(const int* hist, int& left, int& digit, int& in_bin) {
   const int lane = threadIdx.x & 31;
   const int4 hi = *reinterpret_cast<const int4*>(hist + kBins - 4 - 8 * lane);
   const int4 lo = *reinterpret_cast<const int4*>(hist + kBins - 8 - 8 * lane);
@@ -100,39 +104,42 @@ __device__ __forceinline__ void find_digit(const int* hist, int& left, uint32_t&
   const unsigned reached = __ballot_sync(kFull, before >= left);
   const int who = __ffs(reached) - 1;  // (left is at most the number of keys)
   before -= sum;
-  int d = 0, rest = 0;
+  int d = 0, rest = 0, size = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (before < left && before + c[i] >= left) {
       d = kBins - 1 - 8 * lane - i;
       rest = left - before;
+      size = c[i];
     }
     before += c[i];
   }
-  digit = (uint32_t)__shfl_sync(kFull, d, who);
+  digit = __shfl_sync(kFull, d, who);
+  in_bin = __shfl_sync(kFull, size, who);
   left = __shfl_sync(kFull, rest, who);
 }
 
 template <int THREADS, int EACH>
-__global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
+__global__ void __launch_bounds__(THREADS, kThreadsAtOnce / THREADS) select_kernel(SelectParams p) {
   namespace cg = cooperative_groups;
   constexpr int kWarps = THREADS / 32, kRound = THREADS * EACH;
-  __shared__ SelectTail<THREADS, EACH> sm;
+  __shared__ SelectTail<THREADS> sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int split = p.split;
   const unsigned row = blockIdx.x / (unsigned)split;
   const int rank = (int)(blockIdx.x - row * split);
-  for (int i = tid; i < 4 * kBins; i += THREADS) (&sm.hist[0][0])[i] = 0;
+  for (int i = tid; i < 4 * kBins / 4; i += THREADS)
+    reinterpret_cast<int4*>(sm.hist)[i] = make_int4(0, 0, 0, 0);
   if (warp == 0) {  // the row's candidates (every CTA of a cluster finds the same)
     int n = 0;
     const float* src = nullptr;
     bool ok = true;
     if (p.qsl) {
       const int t = (int)(row / (unsigned)p.H);
-      const int r = request_of_row(p.qsl, p.R, t);
       ReqSpan s;
+      const int r = span_of_row(p.qsl, p.seq_lens, p.R, t, s);
       ok = r >= 0 &&  // else a row behind the last sequence
-           request_span(p.qsl, p.seq_lens, r, p.T, (int64_t)p.limit * p.unit, p.err, s);
+           span_fits(s, p.T, (int64_t)p.limit * p.unit, p.err);
       if (ok) n = (s.seq - s.q_len + (t - s.q0)) / p.unit + 1;
       src = p.scores + (int64_t)row * p.stride;
     } else {
@@ -158,142 +165,134 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectParams p) {
     for (int i = rank * THREADS + tid; i < p.k; i += THREADS * split) out[i] = i < n ? i : -1;
     return;
   }
-  // this CTA's run of candidates; of each round a thread has every THREADS-th, in `held` places
+  cg::cluster_group cluster = cg::this_cluster();
+  // This CTA's run of candidates. Of a round a warp has `held` times 32 in a row, a thread
+  // every 32nd of them.
   const int share = (n + split - 1) / split;
   const int begin = min(n, rank * share), end = min(n, begin + share);
   const int tail = n - p.last;
   const bool one_round = share <= kRound;
   const int held = min(EACH, (end - begin + THREADS - 1) / THREADS);
   uint32_t key[EACH];  // (0 where there is no candidate: the lowest key, of -inf, is greater)
+  auto index = [&](int base, int j) { return base + (warp * held + j) * 32 + lane; };
   auto read = [&](int base) {
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-      const int i = base + j * THREADS + tid;
-      key[j] = i >= end ? 0u : i < p.first || i >= tail ? kForced : key_of(__ldg(src + i));
+      const int i = index(base, j);
+      key[j] = j >= held || i >= end ? 0u : i < p.first || i >= tail ? kForced : key_of(__ldg(src + i));
+    }
+  };
+  // Each round's keys in turn: those of the one round stay where they are.
+  auto rounds = [&](auto f) {
+    for (int base = begin; base < end; base += kRound) {
+      if (!one_round) read(base);
+      f(base);
     }
   };
   read(begin);
-  cg::cluster_group cluster = cg::this_cluster();
   uint32_t thr = 0;
   int left = p.k;  // of the k, those among the keys that agree with thr so far
-  __syncthreads();
+  // (of a cluster, the first 256 threads:) keys of the thread's bins that the CTAs before
+  // this one take, and of ties that they have
+  int ahead = 0, ahead_ties = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     int* hist = sm.hist[pass];
-    for (int base = begin; base < end; base += kRound) {
-      if (!one_round) read(base);
+    rounds([&](int) {
 #pragma unroll
       for (int j = 0; j < EACH; ++j) {
         if (j % 4 == 0 && j >= held) break;
         const bool agrees = key[j] != 0u && (pass == 0 || ((key[j] ^ thr) >> (shift + 8)) == 0u);
         count_if(agrees, &hist[(key[j] >> shift) & (kBins - 1)]);
       }
-    }
+    });
+    int before = 0;
     if (split > 1) {
       cluster.sync();
-      for (int i = tid; i < kBins; i += THREADS) {
+      if (tid < kBins) {
         int c = 0;
-        for (int o = 0; o < split; ++o) c += *cluster.map_shared_rank(&hist[i], o);
-        sm.total[i] = c;
+#pragma unroll
+        for (int o = 0; o < 8; ++o) {
+          const int x = o < split ? *cluster.map_shared_rank(&hist[tid], o) : 0;
+          c += x;
+          before += o < rank ? x : 0;
+        }
+        sm.total[tid] = c;
       }
     }
     __syncthreads();
     if (warp == 0) {
-      uint32_t digit;
-      find_digit(split > 1 ? sm.total : hist, left, digit);
+      int digit, in_bin;
+      find_digit(split > 1 ? sm.total : hist, left, digit, in_bin);
       if (lane == 0) {
         sm.digit = digit;
         sm.rest = left;
+        sm.in_bin = in_bin;
       }
     }
     __syncthreads();
     left = sm.rest;
-    const uint32_t digit = sm.digit;
-    thr |= digit << shift;
+    const int digit = sm.digit;
+    const bool all = left == sm.in_bin;  // of this digit: no need to tell them apart
+    thr |= (uint32_t)digit << shift;
+    ahead += tid > digit || (all && tid == digit) ? before : 0;
+    if (all) {
+      thr = max(thr, 1u) - 1u;  // (all keys are above 0)
+      left = 0;
+      break;
+    }
+    if (pass == 3 && tid == digit) ahead_ties = before;
   }
-  // left: how many of the keys equal to thr are taken. First, what the CTAs before have.
+  // Keys above thr are taken, and `left` of those equal to it.
   int above0 = 0, equal0 = 0;
   if (split > 1) {
-    int a = 0, e = 0;
-    for (int base = begin; base < end; base += kRound) {
-      if (!one_round) read(base);
-#pragma unroll
-      for (int j = 0; j < EACH; ++j) {
-        a += key[j] > thr;
-        e += key[j] == thr;
-      }
-    }
-    a = __reduce_add_sync(kFull, a);
-    e = __reduce_add_sync(kFull, e);
-    if (tid == 0) sm.cta_above = sm.cta_equal = 0;
+    cluster.barrier_arrive();
+    ahead = __reduce_add_sync(kFull, ahead);
+    ahead_ties = __reduce_add_sync(kFull, ahead_ties);
+    if (lane == 0) sm.ahead[warp] = make_int2(ahead, ahead_ties);
     __syncthreads();
-    if (lane == 0) {
-      atomicAdd(&sm.cta_above, a);
-      atomicAdd(&sm.cta_equal, e);
-    }
-    cluster.sync();
-    for (int o = 0; o < rank; ++o) {
-      above0 += *cluster.map_shared_rank(&sm.cta_above, o);
-      equal0 += *cluster.map_shared_rank(&sm.cta_equal, o);
-    }
-    cluster.sync();  // no CTA leaves while another reads its counts
+    const int2 c = lane < kWarps ? sm.ahead[lane] : make_int2(0, 0);
+    above0 = __reduce_add_sync(kFull, c.x);
+    equal0 = __reduce_add_sync(kFull, c.y);
   }
-  for (int base = begin; base < end; base += kRound) {
-    if (!one_round) read(base);
+  rounds([&](int base) {
+    unsigned ups[EACH], ties[EACH];
+    int a = 0, e = 0;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-      if (j >= held) break;
-      const unsigned up = __ballot_sync(kFull, key[j] > thr), tie = __ballot_sync(kFull, key[j] == thr);
-      if (lane == 0) sm.counts[j * kWarps + warp] = make_int2(__popc(up), __popc(tie));
+      ups[j] = __ballot_sync(kFull, key[j] > thr);
+      ties[j] = __ballot_sync(kFull, key[j] == thr);
+      a += __popc(ups[j]);
+      e += __popc(ties[j]);
     }
+    if (lane == 0) sm.counts[warp] = make_int2(a, e);
     __syncthreads();
-    if (warp == 0) {  // exclusive sums over (place, warp)
-      const int places = held * kWarps;
-      int ca = 0, ce = 0;  // of the 32 before
-      for (int i = lane; i < places + lane; i += 32) {
-        const int2 c = i < places ? sm.counts[i] : make_int2(0, 0);
-        int a = c.x, e = c.y;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(kFull, a, o), z = __shfl_up_sync(kFull, e, o);
-          if (lane >= o) {
-            a += y;
-            e += z;
-          }
-        }
-        if (i < places) sm.counts[i] = make_int2(ca + a - c.x, ce + e - c.y);
-        ca += __shfl_sync(kFull, a, 31);
-        ce += __shfl_sync(kFull, e, 31);
-      }
-      if (lane == 0) sm.round = make_int2(ca, ce);
-    }
-    __syncthreads();
+    const int2 c = lane < kWarps ? sm.counts[lane] : make_int2(0, 0);
+    int x = above0 + __reduce_add_sync(kFull, lane < warp ? c.x : 0);
+    int y = equal0 + __reduce_add_sync(kFull, lane < warp ? c.y : 0);
+    const unsigned lower = (1u << lane) - 1u;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-      if (j >= held) break;
-      const bool up = key[j] > thr, tie = key[j] == thr;
-      const unsigned ups = __ballot_sync(kFull, up), ties = __ballot_sync(kFull, tie);
-      if ((ups | ties) == 0u) continue;
-      const int2 c = sm.counts[j * kWarps + warp];
-      const unsigned lower = (1u << lane) - 1u;
-      const int x = above0 + c.x + __popc(ups & lower), y = equal0 + c.y + __popc(ties & lower);
-      if (up || (tie && y < left)) out[x + min(y, left)] = base + j * THREADS + tid;
+      const int up = x + __popc(ups[j] & lower), tie = y + __popc(ties[j] & lower);
+      if (key[j] > thr || (key[j] == thr && tie < left)) out[up + min(tie, left)] = index(base, j);
+      x += __popc(ups[j]);
+      y += __popc(ties[j]);
     }
     if (!one_round) {
-      above0 += sm.round.x;
-      equal0 += sm.round.y;
+      above0 += __reduce_add_sync(kFull, c.x);
+      equal0 += __reduce_add_sync(kFull, c.y);
       __syncthreads();
     }
-  }
+  });
+  if (split > 1) cluster.barrier_wait();  // no CTA leaves while another reads its bins
 }
 
 pa_status launch_select(SelectParams& p, int64_t rows, cudaStream_t s) {
   if (p.k > kMostTokens) return PA_ERR_UNSUPPORTED;
   if (p.limit > kMostTokens) p.limit = (int)kMostTokens;  // (a longer row is flagged)
-  // 128 threads hold 1024 candidates: four such CTAs run where one of 512 does
-  const bool small = p.limit <= 1024;
-  const int threads = small ? 128 : 512, each = 8;
+  // (16000 rows of 1000 candidates: 68 us by 128 threads, 109 by 256, 247 by 512)
+  const int threads = p.limit <= 1024 ? 128 : p.limit <= 2048 ? 256 : 512, each = 8;
   p.split = 1;
   while (p.split < 8 && (int64_t)p.split * threads * each < p.limit) p.split *= 2;
   if (rows * p.split > 0x7fffffff) return PA_ERR_UNSUPPORTED;
@@ -309,8 +308,10 @@ pa_status launch_select(SelectParams& p, int64_t rows, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, small ? select_kernel<128, 8> : select_kernel<512, 8>, p) !=
-      cudaSuccess) {
+  auto kernel = threads == 128   ? select_kernel<128, 8>
+                : threads == 256 ? select_kernel<256, 8>
+                                 : select_kernel<512, 8>;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
     cudaGetLastError();
     return PA_ERR_CUDA;
   }

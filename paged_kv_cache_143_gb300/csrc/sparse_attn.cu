@@ -210,10 +210,10 @@ __global__ void __launch_bounds__(kSparseThreads, NH == 1 ? 3 : 2)
   const int hq0 = kvh * p.g + part * kRows;
   const int heads = min(kRows, p.g - part * kRows);
   // every CTA of a cluster takes the same way out here
-  const int r = request_of_row(p.qsl, p.R, t);
-  if (r < 0) return;  // a row behind the last sequence
   ReqSpan sp;
-  if (!request_span(p.qsl, p.seq_lens, r, p.T, (int64_t)p.max_blocks * p.B, p.err, sp)) return;
+  const int r = span_of_row(p.qsl, p.seq_lens, p.R, t, sp);
+  if (r < 0) return;  // a row behind the last sequence
+  if (!span_fits(sp, p.T, (int64_t)p.max_blocks * p.B, p.err)) return;
   const int sees = sp.seq - sp.q_len + (t - sp.q0) + 1;  // keys that the token may see
 
   if (lane == 0) {
