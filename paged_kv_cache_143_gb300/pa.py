@@ -956,14 +956,24 @@ def _pool_on(pool: KVPool, dev: int) -> None:
         raise ValueError(f"the pool is on {pool.k.device}, the call on cuda:{dev}")
 
 
+def _shape(t: torch.Tensor, dims: int, what: str):
+    """A tensor's `dims` sizes."""
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(what)
+    return shape
+
+
 def _batch_shapes(query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
-                  block_tables: torch.Tensor) -> int:
+                  block_tables: torch.Tensor):
+    """num_reqs and max_blocks."""
     R = seq_lens.numel()
     if query_start_loc.numel() != R + 1:
         raise ValueError("query_start_loc must have num_reqs + 1 entries and seq_lens num_reqs")
-    if block_tables.dim() != 2 or block_tables.shape[0] != R:
+    rows, max_blocks = _shape(block_tables, 2, "block_tables must be [num_reqs][max_blocks]")
+    if rows != R:
         raise ValueError("block_tables must be [num_reqs][max_blocks]")
-    return R
+    return R, max_blocks
 
 
 def update_block_bounds(pool: KVPool, bounds: torch.Tensor, block_tables: torch.Tensor,
@@ -973,7 +983,8 @@ def update_block_bounds(pool: KVPool, bounds: torch.Tensor, block_tables: torch.
     blocks that hold each request's new tokens, of which there are at most
     num_tokens; without query_start_loc of all its blocks."""
     R = seq_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != R:
+    rows, max_blocks = _shape(block_tables, 2, "block_tables must be [num_reqs][max_blocks]")
+    if rows != R:
         raise ValueError("block_tables must be [num_reqs][max_blocks]")
     if bounds.shape != (pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim):
         raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
@@ -997,8 +1008,8 @@ def update_block_bounds(pool: KVPool, bounds: torch.Tensor, block_tables: torch.
     st = (_lib or lib()).pa_update_block_bounds(
         pool.ref(), bounds.data_ptr(),
         None if query_start_loc is None else query_start_loc.data_ptr(), seq_lens.data_ptr(),
-        block_tables.data_ptr(), block_tables.shape[1], R,
-        0 if query_start_loc is None else num_tokens, _on(dev, stream))
+        block_tables.data_ptr(), max_blocks, R, 0 if query_start_loc is None else num_tokens,
+        _on(dev, stream))
     if st:
         raise PaError(st, "pa_update_block_bounds")
 
@@ -1009,9 +1020,9 @@ def score_blocks(q: torch.Tensor, bounds: torch.Tensor, scores: torch.Tensor,
     """The most that a key inside each block's bounds can score with a token's
     query heads: q [T][Hq][D], scores fp32 [T][Hkv][max_blocks]; entries of
     blocks past a token's own are left as they are."""
-    R = _batch_shapes(query_start_loc, seq_lens, block_tables)
+    R, max_blocks = _batch_shapes(query_start_loc, seq_lens, block_tables)
     T, Hq, D = q.shape
-    if D != pool.head_dim or scores.shape != (T, pool.num_kv_heads, block_tables.shape[1]):
+    if D != pool.head_dim or scores.shape != (T, pool.num_kv_heads, max_blocks):
         raise ValueError("q must be [T][Hq][head_dim] and scores [T][num_kv_heads][max_blocks]")
     if bounds.shape != (pool.num_blocks, pool.num_kv_heads, 2, D):
         raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
@@ -1029,7 +1040,7 @@ def score_blocks(q: torch.Tensor, bounds: torch.Tensor, scores: torch.Tensor,
                  (seq_lens, "seq_lens", _I32, True), (block_tables, "block_tables", _I32, True))
     st = (_lib or lib()).pa_score_blocks(
         q.data_ptr(), bounds.data_ptr(), scores.data_ptr(), query_start_loc.data_ptr(),
-        seq_lens.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], R, T, Hq, pool.ref(),
+        seq_lens.data_ptr(), block_tables.data_ptr(), max_blocks, R, T, Hq, pool.ref(),
         _on(dev, stream))
     if st:
         raise PaError(st, "pa_score_blocks")
@@ -1045,7 +1056,8 @@ def select_blocks(scores: torch.Tensor, selected: torch.Tensor, query_start_loc:
     R = seq_lens.numel()
     if query_start_loc.numel() != R + 1:
         raise ValueError("query_start_loc must have num_reqs + 1 entries and seq_lens num_reqs")
-    if selected.dim() != 3 or selected.shape[:2] != (T, H):
+    rows, heads, k = _shape(selected, 3, "selected must be [T][num_kv_heads][k]")
+    if rows != T or heads != H:
         raise ValueError("selected must be [T][num_kv_heads][k]")
     dev = _device_of(scores, "scores")
     if not (scores.dtype is _F32 and selected.dtype is _I32
@@ -1059,7 +1071,7 @@ def select_blocks(scores: torch.Tensor, selected: torch.Tensor, query_start_loc:
                  (seq_lens, "seq_lens", _I32, True))
     st = (_lib or lib()).pa_select_blocks(
         scores.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(), R, T, H, max_blocks,
-        int(block_size), int(first), int(last), selected.shape[2], selected.data_ptr(),
+        int(block_size), int(first), int(last), k, selected.data_ptr(),
         _on(dev, stream))
     if st:
         raise PaError(st, "pa_select_blocks")
@@ -1070,11 +1082,13 @@ def sparse_forward(q: torch.Tensor, out: torch.Tensor, query_start_loc: torch.Te
                    pool: KVPool, scale: float, stream=None) -> None:
     """`forward` (causal) in which a token's heads see only the blocks that
     selected int32 [T][Hkv][k] names for their kv head (-1: none)."""
-    R = _batch_shapes(query_start_loc, seq_lens, block_tables)
-    T, Hq, D = q.shape
-    if D != pool.head_dim or out.shape != q.shape:
+    R, max_blocks = _batch_shapes(query_start_loc, seq_lens, block_tables)
+    shape = q.shape
+    T, Hq, D = shape
+    if D != pool.head_dim or out.shape != shape:
         raise ValueError("q and out must be [T][Hq][head_dim]")
-    if selected.dim() != 3 or selected.shape[:2] != (T, pool.num_kv_heads):
+    rows, heads, k = _shape(selected, 3, "selected must be [T][num_kv_heads][k]")
+    if rows != T or heads != pool.num_kv_heads:
         raise ValueError("selected must be [T][num_kv_heads][k]")
     dev = _device_of(q, "q")
     _pool_on(pool, dev)
@@ -1091,20 +1105,21 @@ def sparse_forward(q: torch.Tensor, out: torch.Tensor, query_start_loc: torch.Te
                  (seq_lens, "seq_lens", _I32, True), (block_tables, "block_tables", _I32, True))
     st = (_lib or lib()).pa_sparse_forward(
         q.data_ptr(), out.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(),
-        block_tables.data_ptr(), block_tables.shape[1], R, T, Hq, selected.data_ptr(),
-        selected.shape[2], pool.ref(), float(scale), _on(dev, stream))
+        block_tables.data_ptr(), max_blocks, R, T, Hq, selected.data_ptr(), k, pool.ref(),
+        float(scale), _on(dev, stream))
     if st:
         raise PaError(st, "pa_sparse_forward")
 
 
-def _mass_shape(mass: torch.Tensor, idx_mapping: Optional[torch.Tensor], R: int) -> None:
-    if mass.dim() != 2:
-        raise ValueError("mass must be [max_reqs][places]")
+def _mass_shape(mass: torch.Tensor, idx_mapping: Optional[torch.Tensor], R: int):
+    """Rows and places."""
+    shape = _shape(mass, 2, "mass must be [max_reqs][places]")
     if idx_mapping is None:
-        if mass.shape[0] < R:
+        if shape[0] < R:
             raise ValueError("mass must have a row for each request")
     elif idx_mapping.numel() != R:
         raise ValueError("idx_mapping must have one entry per request")
+    return shape
 
 
 def attention_mass_workspace_size(qsl_host, seq_lens_host, num_q_heads: int, num_kv_heads: int,
@@ -1128,14 +1143,14 @@ def attention_mass(q: torch.Tensor, mass_in: torch.Tensor, mass_out: torch.Tenso
     of all heads. mass fp32 [max_reqs][places], row idx_mapping[r] (or r)."""
     qh = _host_i32(qsl_host)
     sh = _host_i32(seq_lens_host)
-    R = _batch_shapes(query_start_loc, seq_lens, block_tables)
+    R, max_blocks = _batch_shapes(query_start_loc, seq_lens, block_tables)
     if qh.size != R + 1 or sh.size != R:
         raise ValueError("the host mirrors must have the entries of the device arrays")
     T, Hq, D = q.shape
     if D != pool.head_dim:
         raise ValueError("q must be [T][Hq][head_dim]")
-    _mass_shape(mass_in, idx_mapping, R)
-    if mass_out.shape != mass_in.shape:
+    rows, places = shape = _mass_shape(mass_in, idx_mapping, R)
+    if mass_out.shape != shape:
         raise ValueError("mass_in and mass_out must have one shape")
     dev = _device_of(q, "q")
     _pool_on(pool, dev)
@@ -1158,11 +1173,11 @@ def attention_mass(q: torch.Tensor, mass_in: torch.Tensor, mass_out: torch.Tenso
                  (idx_mapping, "idx_mapping", _I32, True),
                  (workspace, "workspace", None if workspace is None else workspace.dtype, True))
     st = (_lib or lib()).pa_attention_mass(
-        q.data_ptr(), mass_in.data_ptr(), mass_out.data_ptr(), mass_in.shape[1],
-        mass_in.shape[0], None if idx_mapping is None else idx_mapping.data_ptr(),
+        q.data_ptr(), mass_in.data_ptr(), mass_out.data_ptr(), places, rows,
+        None if idx_mapping is None else idx_mapping.data_ptr(),
         query_start_loc.data_ptr(), seq_lens.data_ptr(), _np_addr(qh), _np_addr(sh),
-        block_tables.data_ptr(), block_tables.shape[1], R, T, Hq, pool.ref(), float(scale),
-        float(decay), int(window), None if workspace is None else workspace.data_ptr(),
+        block_tables.data_ptr(), max_blocks, R, T, Hq, pool.ref(), float(scale), float(decay),
+        int(window), None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _on(dev, stream))
     if st:
@@ -1176,8 +1191,9 @@ def select_tokens(mass: torch.Tensor, kept: torch.Tensor, kept_lens: torch.Tenso
     greatest mass [max_reqs][places] (row idx_mapping[r], or r): kept int32
     [R][k], ascending, -1 behind them, kept_lens[r] of them."""
     R = seq_lens.numel()
-    _mass_shape(mass, idx_mapping, R)
-    if kept.dim() != 2 or kept.shape[0] != R or kept_lens.numel() != R:
+    rows, places = _mass_shape(mass, idx_mapping, R)
+    lists, k = _shape(kept, 2, "kept must be [num_reqs][k]")
+    if lists != R or kept_lens.numel() != R:
         raise ValueError("kept must be [num_reqs][k] and kept_lens have num_reqs entries")
     dev = _device_of(mass, "mass")
     if not (mass.dtype is _F32 and kept.dtype is _I32 is kept_lens.dtype
@@ -1192,9 +1208,8 @@ def select_tokens(mass: torch.Tensor, kept: torch.Tensor, kept_lens: torch.Tenso
                  (kept_lens, "kept_lens", _I32, True), (seq_lens, "seq_lens", _I32, True),
                  (idx_mapping, "idx_mapping", _I32, True))
     st = (_lib or lib()).pa_select_tokens(
-        mass.data_ptr(), mass.shape[1], mass.shape[0],
-        None if idx_mapping is None else idx_mapping.data_ptr(), seq_lens.data_ptr(), R,
-        int(first), int(last), kept.shape[1], kept.data_ptr(), kept_lens.data_ptr(),
+        mass.data_ptr(), places, rows, None if idx_mapping is None else idx_mapping.data_ptr(),
+        seq_lens.data_ptr(), R, int(first), int(last), k, kept.data_ptr(), kept_lens.data_ptr(),
         _on(dev, stream))
     if st:
         raise PaError(st, "pa_select_tokens")
@@ -1209,16 +1224,17 @@ def compact_cache(pool: KVPool, src_tables: torch.Tensor, dst_tables: torch.Tens
     blocks, or blocks that no request of the call reads), mass within the
     request's row."""
     R = kept_lens.numel()
-    if kept.dim() != 2 or kept.shape[0] != R:
-        raise ValueError("kept must be [num_reqs][k]")
-    if src_tables.dim() != 2 or dst_tables.dim() != 2 or \
-            not src_tables.shape[0] == R == dst_tables.shape[0]:
-        raise ValueError("src_tables and dst_tables must be [num_reqs][blocks]")
+    lists, k = _shape(kept, 2, "kept must be [num_reqs][k]")
+    from_rows, src_blocks = _shape(src_tables, 2, "src_tables must be [num_reqs][blocks]")
+    to_rows, dst_blocks = _shape(dst_tables, 2, "dst_tables must be [num_reqs][blocks]")
+    if not lists == from_rows == to_rows == R:
+        raise ValueError("kept, src_tables and dst_tables must have a row for each request")
     if (mass_in is None) != (mass_out is None):
         raise ValueError("mass_in and mass_out come together")
+    rows = places = 0
     if mass_in is not None:
-        _mass_shape(mass_in, idx_mapping, R)
-        if mass_out.shape != mass_in.shape:
+        rows, places = shape = _mass_shape(mass_in, idx_mapping, R)
+        if mass_out.shape != shape:
             raise ValueError("mass_in and mass_out must have one shape")
     dev = _device_of(kept, "kept")
     _pool_on(pool, dev)
@@ -1238,10 +1254,9 @@ def compact_cache(pool: KVPool, src_tables: torch.Tensor, dst_tables: torch.Tens
                  (src_tables, "src_tables", _I32, True), (dst_tables, "dst_tables", _I32, True),
                  (mass_in, "mass_in", _F32, True), (mass_out, "mass_out", _F32, True),
                  (idx_mapping, "idx_mapping", _I32, True))
-    rows, places = (0, 0) if mass_in is None else mass_in.shape
     st = (_lib or lib()).pa_compact_cache(
-        pool.ref(), src_tables.data_ptr(), src_tables.shape[1], dst_tables.data_ptr(),
-        dst_tables.shape[1], kept.data_ptr(), kept.shape[1], kept_lens.data_ptr(), R,
+        pool.ref(), src_tables.data_ptr(), src_blocks, dst_tables.data_ptr(), dst_blocks,
+        kept.data_ptr(), k, kept_lens.data_ptr(), R,
         None if mass_in is None else mass_in.data_ptr(),
         None if mass_out is None else mass_out.data_ptr(), places, rows,
         None if idx_mapping is None else idx_mapping.data_ptr(), _on(dev, stream))
