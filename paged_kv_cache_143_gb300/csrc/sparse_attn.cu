@@ -209,6 +209,15 @@ __global__ void __launch_bounds__(kSparseThreads, NH == 1 ? 3 : 2)
   const int t = (int)(unit / p.parts / p.Hkv);
   const int hq0 = kvh * p.g + part * kRows;
   const int heads = min(kRows, p.g - part * kRows);
+  const int32_t* list = p.selected + ((int64_t)t * p.Hkv + kvh) * p.k;
+  const int lanes_of = kSparseWarps * p.split;  // warps that share the list
+  const int first = rank * kSparseWarps + warp;
+  // the list's entries of a round, one a lane; the first ones come with the row's lengths
+  auto entry = [&](int64_t base) {
+    const int64_t e = base + (int64_t)lane * lanes_of + first;
+    return e < p.k ? __ldg(list + e) : -1;
+  };
+  int b = entry(0);
   // every CTA of a cluster takes the same way out here
   ReqSpan sp;
   const int r = span_of_row(p.qsl, p.seq_lens, p.R, t, sp);
@@ -222,17 +231,12 @@ __global__ void __launch_bounds__(kSparseThreads, NH == 1 ? 3 : 2)
   }
   __syncwarp();
   CH st;
-  st.q.load([&](int c) { return c < heads ? p.q + ((int64_t)t * p.Hq + hq0 + c) * D : nullptr; },
-            p.q_scale, grp, tig);
   st.reset();
 
   uint8_t* my_ring = ring + warp * SG::kWarpBytes;
   uint64_t* full = tail->full[warp];
   uint2* cells = tail->cells[warp];
-  const int32_t* list = p.selected + ((int64_t)t * p.Hkv + kvh) * p.k;
   const int32_t* table = p.tables + (int64_t)r * p.max_blocks;
-  const int lanes_of = kSparseWarps * p.split;  // warps that share the list
-  const int first = rank * kSparseWarps + warp;
   uint32_t pos = 0;  // cells gone through: stage pos mod kStages, phase pos / kStages
   bool ok = true;
   int seen = 0;
@@ -245,21 +249,18 @@ __global__ void __launch_bounds__(kSparseThreads, NH == 1 ? 3 : 2)
     C::load(dst + C::kBytes, &tmap_v, line, (int)c.x, &full[stage]);
   };
   for (int64_t base = 0; base < p.k && ok; base += 32 * lanes_of) {
-    const int64_t e = base + (int64_t)lane * lanes_of + first;
     int n_cells = 0, id = 0, keys = 0;
-    if (e < p.k) {
-      const int b = __ldg(list + e);
-      if (b < -1 || b >= p.max_blocks) {
+    if (b < -1 || b >= p.max_blocks) {
+      raise_error(p.err, kErrBounds);
+    } else if (b >= 0 && (int64_t)b * p.B < sees) {
+      id = __ldg(table + b);
+      keys = min(p.B, sees - b * p.B);
+      if (id < 0 || id >= p.num_blocks)
         raise_error(p.err, kErrBounds);
-      } else if (b >= 0 && (int64_t)b * p.B < sees) {
-        id = __ldg(table + b);
-        keys = min(p.B, sees - b * p.B);
-        if (id < 0 || id >= p.num_blocks)
-          raise_error(p.err, kErrBounds);
-        else
-          n_cells = (keys + kChunk - 1) / kChunk;
-      }
+      else
+        n_cells = (keys + kChunk - 1) / kChunk;
     }
+    b = entry(base + 32 * lanes_of);
     int end = n_cells;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -276,6 +277,9 @@ __global__ void __launch_bounds__(kSparseThreads, NH == 1 ? 3 : 2)
     seen |= total > 0;
     if (lane == 0)
       for (int c = 0; c < min(total, kStages); ++c) issue(pos + c, cells[c]);
+    if (base == 0)  // (while the first cells are on their way)
+      st.q.load([&](int c) { return c < heads ? p.q + ((int64_t)t * p.Hq + hq0 + c) * D : nullptr; },
+                p.q_scale, grp, tig);
     for (int c = 0; c < total; ++c) {
       const uint32_t at = pos + c, stage = at % kStages;
       if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], (at / kStages) & 1, p.err))) {
@@ -456,7 +460,7 @@ extern "C" pa_status pa_sparse_forward(const void* q, void* out, const int32_t* 
   // 128 blocks of 16 keys (bf16, 8 kv heads), by the time of an earlier inner loop: 8
   // decodes 31 us alone, 23 by 2 or 4, 31 by 8; 24: 45, 43, 47, 61; 64: 119, 109, 111,
   // 141; 300 tokens of a chunk (64 blocks): 164, 201. As it is now, by this rule: 20.5,
-  // 41, 92, 90.
+  // 39, 92, 90.
   const int64_t units = (int64_t)num_tokens * p.Hkv * p.parts;
   const int64_t at_once = (int64_t)(wide ? 2 : 3) * num_sms();
   p.split = 1;
