@@ -6,7 +6,8 @@
 // has two passes over the scores. A request's rows for one kv head are its
 // counted queries times the g heads that share the kv head; two forms:
 //
-//  - up to 16 rows (decodes, drafted tokens): the keys are what costs. One pass
+//  - up to 16 rows (decodes, drafted tokens; up to 64, 16 at a time, in small calls
+//    without longer requests): the keys are what costs. One pass
 //    streams them once (warps with rings of 16-key cells, S^T = K Q^T by
 //    warp-level MMAs with the keys as rows, as pa_sparse_forward), writes the
 //    scores (4 g bytes a key against 2 D or D bytes of the key) to the
@@ -24,13 +25,14 @@
 //    rows, swizzled as the tensor cores read them, which one bulk copy fetches;
 //    behind each image its rows' score factors.
 //
-// E4M3 pools: the codes are multiplied as they are. Up to 16 rows they widen to
+// E4M3 pools: the codes are multiplied as they are. In the streaming form they widen to
 // f16; on tcgen05 a query is the sum of two E4M3 numbers (8 significant bits, all
 // that bf16 has) after a power-of-two scale that puts its row's largest magnitude
 // into [2^7, 2^8): exact for elements down to 2^-8 of that one, off by 2^-18 of it
 // below.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <utility>
 
 #include "batch_rows.cuh"
@@ -41,13 +43,19 @@ namespace pa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kNarrowRows = 16;     // rows of the streaming form, at the most
+constexpr int kNarrowRows = 16;     // rows that a CTA of the streaming form takes
+constexpr int kStreamRows = 64;     // rows of a request of that form, at the most
+constexpr int kStreamUnits = 608;   // its CTAs, where they are to spare the tcgen05 form
+constexpr int kSumRows = 12288;     // rows of all kv heads whose sums are at hand in shared memory
 constexpr int kSplitKeys = 1024;    // keys of one of its CTAs
 constexpr int kTile = 128;          // rows, and keys, of a tcgen05 tile
 constexpr int kInfoBytes = 1024;    // behind an image: the score factors of its rows
 // Of rows 2 i and 2 i + 1 four floats, (factor, factor, -lse, -lse), so that one load
 // feeds one packed multiply-add: the row's factor is at info_at(row), -lse 2 further.
 __device__ __forceinline__ int info_at(int row) { return (row >> 1) * 4 + (row & 1); }
+
+constexpr int kAllNarrow = 0, kAllWide = 1, kByBits = 2;
+constexpr int kMixedReqs = 4096;  // requests of a call with both forms, at the most
 
 struct MassParams {
   const __nv_bfloat16* q;
@@ -63,9 +71,11 @@ struct MassParams {
   // streaming form
   float* scores;           // request after request: [Hkv * rows][keys rounded up to 16]
   int64_t score_floats;
-  float2* split_stats;     // [R][Hkv][16][splits] (maximum, sum)
+  float2* split_stats;     // [R][Hkv][groups][16][splits] (maximum, sum)
   int splits;
   int narrow_rows;         // rows of a request of this form, at the most
+  int groups;              // of 16 rows
+  int sum_keys;            // keys of a CTA of the sums
   // tcgen05 form: a step is a row tile of a kv head and a key tile; request r's are the
   // flat steps first_step[r] + (kvh * tiles + row tile) * key tiles + key tile
   int* first_tile;         // [R], -1: not of this form
@@ -77,26 +87,30 @@ struct MassParams {
   int n_tiles, pieces;
   int key_tiles;           // key tiles of the longest request
   unsigned* err;
+  // Which form a request takes is the mirrors' choice, so that a captured call whose
+  // device lengths shrink finds the room that was planned for it.
+  int forms;               // kAllNarrow, kAllWide, kByBits
+  uint32_t wide[kMixedReqs / 32];
 };
 
 struct MassReq {
   int q0, q_len, seq, w, rows;  // w counted queries, rows = w * g
+  bool wide;                    // of the tcgen05 form
 };
 
-__device__ __forceinline__ MassReq rows_of(const MassParams& p, int q0, int end, int seq) {
+__device__ __forceinline__ MassReq rows_of(const MassParams& p, int r) {
+  const int q0 = p.qsl[r], end = p.qsl[r + 1], seq = p.seq_lens[r];
   MassReq m;
   m.q0 = q0;
   m.q_len = end - q0;
   m.seq = seq;
+  m.wide = p.forms == kAllWide || (p.forms == kByBits && ((p.wide[r >> 5] >> (r & 31)) & 1u));
   const bool fine = q0 >= 0 && end <= p.T && end >= q0 && seq >= m.q_len &&
                     seq <= (int64_t)p.max_blocks * p.B && seq <= p.mass_stride && seq <= kMostTokens;
   m.w = fine ? (p.window > 0 ? min(m.q_len, p.window) : m.q_len) : 0;
   const int64_t rows = (int64_t)m.w * p.g;
   m.rows = rows > 0x3fffffff ? 0 : (int)rows;
   return m;
-}
-__device__ __forceinline__ MassReq rows_of(const MassParams& p, int r) {
-  return rows_of(p, p.qsl[r], p.qsl[r + 1], p.seq_lens[r]);
 }
 // Whether request r was left out for entries that leave the buffers.
 __device__ __forceinline__ bool bad_request(const MassReq& m) { return m.rows == 0 && m.q_len != 0; }
@@ -114,7 +128,7 @@ __device__ __forceinline__ int64_t before(const MassParams& p, int r, F f) {
 }
 
 __device__ __forceinline__ int64_t score_floats_of(const MassParams& p, const MassReq& m) {
-  return m.rows > 0 && m.rows <= kNarrowRows ? (int64_t)p.Hkv * m.rows * padded_keys(m.seq) : 0;
+  return !m.wide && m.rows <= p.narrow_rows ? (int64_t)p.Hkv * m.rows * padded_keys(m.seq) : 0;
 }
 
 __device__ __forceinline__ int mass_row(const MassParams& p, int r) {
@@ -141,7 +155,7 @@ struct NarrowTail {
 
 template <int D, bool FP8, int NH>
 __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
-    mass_scores_kernel(const __grid_constant__ CUtensorMap tmap_k, MassParams p) {
+    mass_scores_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ MassParams p) {
   using C = Cells<D, FP8>;
   constexpr int kStages = kNarrowRing / C::kBytes > 8 ? 8 : kNarrowRing / C::kBytes;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -150,18 +164,18 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
   launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = lane >> 2, tig = lane & 3;
-  const int split = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z;
+  const int split = blockIdx.x, kvh = blockIdx.y / p.groups, r = blockIdx.z;
+  const int row0 = (blockIdx.y - kvh * p.groups) * kNarrowRows;  // the first of the CTA's 16 rows
   const MassReq m = rows_of(p, r);
-  const bool reporter = tid == 0 && split == 0 && kvh == 0;
-  if (bad_request(m) || (m.rows > kNarrowRows && p.n_tiles == 0) ||
-      (m.rows > 0 && mass_row(p, r) < 0)) {
-    if (reporter) raise_error(p.err, kErrBounds);
+  const bool reporter = tid == 0 && split == 0 && blockIdx.y == 0;
+  if (m.wide) return;
+  if (bad_request(m) || m.rows > p.narrow_rows || (m.rows > 0 && mass_row(p, r) < 0)) {
+    if (reporter) raise_error(p.err, kErrBounds);  // (or more rows than the mirrors said)
     return;
   }
-  if (m.rows == 0 || m.rows > kNarrowRows) return;
+  if (m.rows <= row0) return;
   const int64_t at = before(p, r, [&](const MassReq& x) { return score_floats_of(p, x); });
-  if (at + score_floats_of(p, m) > p.score_floats || m.seq > (int64_t)p.splits * kSplitKeys ||
-      m.rows > p.narrow_rows) {
+  if (at + score_floats_of(p, m) > p.score_floats || m.seq > (int64_t)p.splits * kSplitKeys) {
     if (reporter) raise_error(p.err, kErrBounds);  // more than the mirrors said
     return;
   }
@@ -169,7 +183,8 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
   if (k0 >= m.seq) return;
   const int n_cells = (min(m.seq - k0, kSplitKeys) + kChunk - 1) / kChunk;
   const int stride = padded_keys(m.seq);
-  float* out = p.scores + at + (int64_t)kvh * m.rows * stride;
+  const int n_rows = min(kNarrowRows, m.rows - row0);
+  float* out = p.scores + at + ((int64_t)kvh * m.rows + row0) * stride;
   const int32_t* table = p.tables + (int64_t)r * p.max_blocks;
   uint8_t* my_ring = ring + warp * kNarrowRing;
   uint64_t* full = tail->full[warp];
@@ -201,8 +216,9 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
   for (int i = 0; i < min(mine, kStages); ++i) issue(i);
   QueryCols<D, FP8, NH> q;
   q.load([&](int c) -> const __nv_bfloat16* {
-    return c < m.rows ? p.q + ((int64_t)(m.q0 + m.q_len - m.w + c / p.g) * p.Hq + kvh * p.g + c % p.g) * D
-                      : nullptr;
+    if (c >= n_rows) return nullptr;
+    c += row0;
+    return p.q + ((int64_t)(m.q0 + m.q_len - m.w + c / p.g) * p.Hq + kvh * p.g + c % p.g) * D;
   }, p.qk_scale, grp, tig);
   float mx[NH][2], l[NH][2];
   int lim[NH][2];  // keys that the query of column 2 tig + e sees
@@ -212,7 +228,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
     for (int e = 0; e < 2; ++e) {
       mx[h][e] = -INFINITY;
       l[h][e] = 0.f;
-      lim[h][e] = m.seq - m.w + (8 * h + 2 * tig + e) / p.g + 1;
+      lim[h][e] = m.seq - m.w + (row0 + 8 * h + 2 * tig + e) / p.g + 1;
     }
   for (int i = 0; i < mine; ++i) {
     const int stage = i % kStages;
@@ -236,7 +252,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
         float x1 = s[h][2 + e] * q.sc[h][e];
         if (key >= lim[h][e]) x0 = -INFINITY;
         if (key + 8 >= lim[h][e]) x1 = -INFINITY;
-        if (c < m.rows) {
+        if (c < n_rows) {
           float* dst = out + (int64_t)c * stride + key;
           dst[0] = x0;
           dst[8] = x1;
@@ -260,7 +276,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
       if (grp == 0) tail->stats[warp][8 * h + 2 * tig + e] = make_float2(mx[h][e], l[h][e]);
     }
   __syncthreads();
-  if (tid < m.rows) {
+  if (tid < n_rows) {
     float ref = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kNarrowWarps; ++w) ref = fmaxf(ref, tail->stats[w][tid].x);
@@ -268,7 +284,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
 #pragma unroll
     for (int w = 0; w < kNarrowWarps; ++w)
       sum += tail->stats[w][tid].y * ex2_ftz(tail->stats[w][tid].x - base);
-    p.split_stats[(((int64_t)r * p.Hkv + kvh) * kNarrowRows + tid) * p.splits + split] =
+    p.split_stats[(((int64_t)r * gridDim.y + blockIdx.y) * kNarrowRows + tid) * p.splits + split] =
         make_float2(ref, sum);
   }
 }
@@ -282,14 +298,39 @@ __device__ __forceinline__ float lse_of(const float2* s, int n, int64_t step) {
   return ref + log2f(sum);  // NaN for a row that scores -inf throughout
 }
 
+// A long sum of parts: what the roundings of the sum lost is put back at the end.
+struct Total {
+  float sum = 0.f, low = 0.f;
+  __device__ __forceinline__ void add(float part) {
+    const float x = part + low, next = sum + x;
+    low = x - (next - sum);
+    sum = next;
+  }
+  // (a NaN sum, or an infinite one, has lost no rounding)
+  __device__ __forceinline__ float get() const { return isnan(low) ? sum : sum + low; }
+};
+
+// *src, or 0: predicated, so that loads go out one after the other.
+__device__ __forceinline__ float load_if(bool on, const float* src) {
+  float x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t"
+      "@p ld.global.f32 %0, [%1];\n\t}"
+      : "=f"(x)
+      : "l"(src), "r"((uint32_t)on)
+      : "memory");
+  return x;
+}
+
 constexpr int kSumThreads = 256;
 
-__global__ void __launch_bounds__(kSumThreads) mass_sum_kernel(MassParams p) {
+// A CTA takes p.sum_keys keys, all of whose rows a thread adds up, or a part of them.
+__global__ void __launch_bounds__(kSumThreads, 5) mass_sum_kernel(const __grid_constant__ MassParams p) {
   extern __shared__ float lse[];  // [Hkv * rows]
   const int r = blockIdx.y;
   const MassReq m = rows_of(p, r);
-  if (m.rows == 0 || m.rows > p.narrow_rows || m.seq > (int64_t)p.splits * kSplitKeys) return;
-  const int key0 = blockIdx.x * kSumThreads;
+  if (m.wide || m.rows == 0 || m.rows > p.narrow_rows || m.seq > (int64_t)p.splits * kSplitKeys) return;
+  const int key0 = blockIdx.x * p.sum_keys;
   if (key0 >= m.seq) return;
   const int64_t at = before(p, r, [&](const MassReq& x) { return score_floats_of(p, x); });
   if (at + score_floats_of(p, m) > p.score_floats) return;
@@ -305,8 +346,9 @@ __global__ void __launch_bounds__(kSumThreads) mass_sum_kernel(MassParams p) {
     const int x = base + ((int)threadIdx.x >> 3), lane = threadIdx.x & 7;
     float ref = -INFINITY, sum = 0.f;
     if (x < rows) {
+      const int kvh = x / m.rows, row = x - kvh * m.rows;
       const float2* part = p.split_stats +
-          ((int64_t)(r * (int64_t)p.Hkv + x / m.rows) * kNarrowRows + x % m.rows) * p.splits;
+          (((int64_t)r * p.Hkv + kvh) * p.groups * kNarrowRows + row) * p.splits;
       for (int i = lane; i < n_split; i += 8) join_stats(ref, sum, part[i].x, part[i].y);
     }
 #pragma unroll
@@ -315,21 +357,48 @@ __global__ void __launch_bounds__(kSumThreads) mass_sum_kernel(MassParams p) {
     if (lane == 0 && x < rows) lse[x] = ref + log2f(sum);  // NaN for a row that scores -inf throughout
   }
   __syncthreads();
-  const int key = key0 + (int)threadIdx.x;
-  if (key >= m.seq) return;
+  const int part = (int)threadIdx.x / p.sum_keys, key = key0 + (int)threadIdx.x % p.sum_keys;
+  const int per = (rows * p.sum_keys + kSumThreads - 1) / kSumThreads;  // rows of a thread
+  const int x1 = key < m.seq ? min(rows, (part + 1) * per) : 0;
   const int stride = padded_keys(m.seq);
-  const float* s = p.scores + at + key;
-  float sum = 0.f;
-  if (key <= m.seq - m.w) {  // seen by all counted queries
-#pragma unroll 32
-    for (int x = 0; x < rows; ++x) sum += ex2_ftz(s[(int64_t)x * stride] - lse[x]);
-  } else {
-    const int c0 = (key - (m.seq - m.w)) * p.g;  // the first row that sees the key
-    for (int x = 0; x < rows; ++x)
-      if (x % m.rows >= c0) sum += ex2_ftz(s[(int64_t)x * stride] - lse[x]);
+  const float* s = p.scores + at + (int64_t)part * per * stride + key;
+  const int c0 = max(0, key - (m.seq - m.w)) * p.g;  // the first row that sees the key
+  Total total;
+  int x0 = part * per;
+  if (c0 == 0)
+    for (; x0 + 32 <= x1; x0 += 32, s += (int64_t)32 * stride) {
+      float sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 32; ++x) sum += ex2_ftz(s[x * (int64_t)stride] - lse[x0 + x]);
+      total.add(sum);
+    }
+  for (; x0 < x1; x0 += 16) {  // (without a branch, which would make a load wait for the one before)
+    float v[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x, s += stride) v[x] = load_if(x0 + x < x1, s);
+    float sum = 0.f;
+    int row = x0 % m.rows;  // of the kv head
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const float y = ex2_ftz(v[x] - lse[min(x0 + x, rows - 1)]);
+      sum += x0 + x < x1 && row >= c0 ? y : 0.f;
+      if (++row == m.rows) row = 0;
+    }
+    total.add(sum);
   }
+  float got = total.get();
+  if (p.sum_keys < kSumThreads) {
+    __shared__ float sums[kSumThreads];
+    sums[threadIdx.x] = got;
+    __syncthreads();
+    if (part > 0) return;
+    Total all;
+    for (int i = 0; i < kSumThreads; i += p.sum_keys) all.add(sums[i + threadIdx.x]);
+    got = all.get();
+  }
+  if (key >= m.seq) return;
   const int64_t o = (int64_t)slot * p.mass_stride + key;
-  p.mass_out[o] = (key < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + sum;
+  p.mass_out[o] = (key < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + got;
 }
 
 // -------------------------------------------------------------- tcgen05 form
@@ -343,7 +412,7 @@ struct WideGeo {
 };
 
 __device__ __forceinline__ int tiles_of(const MassReq& m) {
-  return m.rows > kNarrowRows ? (m.rows + kTile - 1) / kTile : 0;
+  return m.wide ? (m.rows + kTile - 1) / kTile : 0;
 }
 
 __device__ __forceinline__ int64_t steps_of(const MassParams& p, const MassReq& m) {
@@ -358,14 +427,14 @@ __device__ __forceinline__ int swizzled(int row, int c) {
 
 // One CTA per (row tile, kv head, request): the image of its 128 query rows.
 template <int D, bool F8>
-__global__ void __launch_bounds__(kTile) mass_rows_kernel(MassParams p) {
+__global__ void __launch_bounds__(kTile) mass_rows_kernel(const __grid_constant__ MassParams p) {
   using W = WideGeo<D, F8>;
   launch_dependents();
   const int ti = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
   const MassReq m = rows_of(p, r);
   const bool reporter = tid == 0 && ti == 0 && kvh == 0;
   const int tiles = tiles_of(m);
-  if (reporter && (bad_request(m) || (m.rows > 0 && !tiles && !p.scores))) raise_error(p.err, kErrBounds);
+  if (reporter && m.wide && bad_request(m)) raise_error(p.err, kErrBounds);
   const int64_t first = before(p, r, [](const MassReq& x) -> int64_t { return tiles_of(x); });
   if (ti == 0 && kvh == 0) {
     const int64_t step = before(p, r, [&](const MassReq& x) { return steps_of(p, x); });
@@ -550,7 +619,7 @@ __device__ __forceinline__ Segment segment_at(const MassParams& p, int64_t f, in
 // under way at once, which is all of tensor memory.
 template <int D, bool F8, bool WEIGHTS>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    mass_tile_kernel(const __grid_constant__ CUtensorMap tmap_k, MassParams p) {
+    mass_tile_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ MassParams p) {
   using W = WideGeo<D, F8>;
   using S = WideSmem<D, F8>;
   constexpr int kStages = S::kStages;
@@ -881,7 +950,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 }
 
 // The steps' sums of each key, over the row tiles of all heads, into the mass.
-__global__ void __launch_bounds__(kSumThreads) mass_add_kernel(MassParams p) {
+__global__ void __launch_bounds__(kSumThreads) mass_add_kernel(const __grid_constant__ MassParams p) {
   grid_dependency_wait();
   const int r = blockIdx.y;
   if (p.first_tile[r] < 0) return;
@@ -891,19 +960,16 @@ __global__ void __launch_bounds__(kSumThreads) mass_add_kernel(MassParams p) {
   const int key_tiles = (m.seq + kTile - 1) / kTile, units = tiles_of(m) * p.Hkv;
   const float* s = p.sums + (p.first_step[r] + key / kTile) * kTile + key % kTile;
   const int64_t step = (int64_t)key_tiles * kTile;
-  float sum = 0.f, low = 0.f;  // what the roundings of the sum lost is put back at the end
+  Total total;
   for (int u = 0; u < units; u += 16) {
     float part = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (u + i < units) part += s[(u + i) * step];
-    const float add = part + low, next = sum + add;
-    low = add - (next - sum);
-    sum = next;
+    total.add(part);
   }
-  if (!isnan(low)) sum += low;  // (a NaN sum has lost no rounding)
   const int64_t o = (int64_t)mass_row(p, r) * p.mass_stride + key;
-  p.mass_out[o] = (key < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + sum;
+  p.mass_out[o] = (key < m.seq - m.q_len ? p.decay * p.mass_in[o] : 0.f) + total.get();
 }
 
 // ------------------------------------------------------------------- planning
@@ -911,23 +977,48 @@ __global__ void __launch_bounds__(kSumThreads) mass_add_kernel(MassParams p) {
 struct MassPlan {
   int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows, steps, per_cta, ctas;
   int64_t narrow_keys, wide_keys;
-  int splits, pieces, key_tiles;
+  int splits, pieces, key_tiles, groups, forms;
   size_t off_stats, off_first, off_steps, off_images, off_tile_stats, off_sums, total;
 };
 
-// What a batch needs, from its mirrors alone (head_dim 128's images serve 64 too).
+// What a batch needs, from its mirrors alone (head_dim 128's images serve 64 too), and
+// which requests take the tcgen05 form (`wide`, if given).
 pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int Hkv, int window,
-                    MassPlan& pl) {
+                    MassPlan& pl, uint32_t* wide = nullptr) {
   pl = MassPlan{};
   const int64_t g = Hq / Hkv;
   int64_t narrow_keys = 0, wide_keys = 0;
+  // The rows up to which keys are streamed, 16 rows at a time: 16, or 64 where no request
+  // has more and what has more than 16 makes no more than two rounds of CTAs, so that the
+  // four launches of the tcgen05 form do not run: 3 x 2 to 7 tokens of 40 heads on 130 tokens
+  // 14 us instead of 46, 13 x 6 of 32 heads on 210 13 instead of 37.
+  int64_t stream_rows = kNarrowRows, units = 0, most = 0;
+  for (int r = 0; r < R; ++r) {
+    const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];
+    const int64_t rows = (window > 0 && q_len > window ? window : q_len) * g;
+    if (rows > most) most = rows;
+    if (rows > kNarrowRows)
+      units += (rows + kNarrowRows - 1) / kNarrowRows * Hkv * ((seq[r] + (int64_t)kSplitKeys - 1) / kSplitKeys);
+  }
+  if (most <= kStreamRows && units <= kStreamUnits && Hkv * (int64_t)kStreamRows <= kSumRows)
+    stream_rows = kStreamRows;
+  int64_t wide_reqs = 0, with_rows = 0;
+  for (int r = 0; r < R; ++r) {
+    const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];
+    if (q_len > 0) ++with_rows;
+    if ((window > 0 && q_len > window ? window : q_len) * g > stream_rows) ++wide_reqs;
+  }
+  // (more of them than a call's bits: all by the tcgen05 form, which takes any row)
+  pl.forms = wide_reqs == 0 ? kAllNarrow : wide_reqs == with_rows || R > kMixedReqs ? kAllWide : kByBits;
+  if (pl.forms == kAllWide) stream_rows = 0;
   for (int r = 0; r < R; ++r) {
     const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];
     if (q_len < 0 || (q_len > 0 && seq[r] < q_len)) return PA_ERR_INVALID;
     if (q_len == 0) continue;
     const int64_t rows = (window > 0 && q_len > window ? window : q_len) * g;
     if (rows > 0x3fffffff || seq[r] > kMostTokens) return PA_ERR_UNSUPPORTED;
-    if (rows <= kNarrowRows) {
+    if (rows > stream_rows && wide && pl.forms == kByBits) wide[r >> 5] |= 1u << (r & 31);
+    if (rows <= stream_rows) {
       ++pl.narrow;
       pl.score_floats += (int64_t)Hkv * rows * (((int64_t)seq[r] + 15) & ~15ll);
       if (seq[r] > narrow_keys) narrow_keys = seq[r];
@@ -944,15 +1035,18 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   pl.wide_keys = wide_keys;
   pl.splits = (int)((narrow_keys + kSplitKeys - 1) / kSplitKeys);
   pl.key_tiles = (int)((wide_keys + kTile - 1) / kTile);
-  // an equal run of steps for each of 152 SMs, four at the least
-  pl.per_cta = (pl.steps + 151) / 152 < 4 ? 4 : (pl.steps + 151) / 152;
+  // An equal run of steps for each of 152 SMs, but four at the least where that keeps the
+  // pieces of a row tile, whose statistics are joined, below ten.
+  const int64_t least = (pl.key_tiles + 7) / 8 < 4 ? (pl.key_tiles + 7) / 8 : 4;
+  pl.per_cta = std::max((pl.steps + 151) / 152, std::max(least, (int64_t)1));
+  pl.groups = (int)((pl.max_narrow_rows + kNarrowRows - 1) / kNarrowRows);
   pl.ctas = (pl.steps + pl.per_cta - 1) / pl.per_cta;
   pl.pieces = (int)((pl.key_tiles + pl.per_cta - 1) / pl.per_cta) + 1;
   if (pl.n_tiles > 0x7fffffff / (int64_t)Hkv || pl.max_tiles > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   auto up = [](size_t x) { return (x + 1023) & ~(size_t)1023; };
   size_t at = up((size_t)pl.score_floats * 4);
   pl.off_stats = at;
-  if (pl.narrow) at = up(at + (size_t)R * Hkv * kNarrowRows * pl.splits * sizeof(float2));
+  if (pl.narrow) at = up(at + (size_t)R * Hkv * pl.groups * kNarrowRows * pl.splits * sizeof(float2));
   pl.off_first = at;
   if (pl.n_tiles) at = up(at + (size_t)R * sizeof(int));
   pl.off_steps = at;
@@ -1028,11 +1122,11 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
   pa_status st = PA_OK;
   if (pl.narrow) {
     if (!cell_map<D, F8>(&tmap, pool->k_pool, pool->num_blocks, p.Hkv * p.B)) return PA_ERR_CUDA;
-    const dim3 grid((unsigned)pl.splits, (unsigned)p.Hkv, (unsigned)p.R);
+    const dim3 grid((unsigned)pl.splits, (unsigned)(p.Hkv * pl.groups), (unsigned)p.R);
     st = launch_after(pl.max_narrow_rows <= 8 ? mass_scores_kernel<D, F8, 1> : mass_scores_kernel<D, F8, 2>,
                       grid, kNarrowWarps * 32, narrow_smem, s, false, tmap, p);
     if (st != PA_OK) return st;
-    st = launch_after(mass_sum_kernel, dim3((unsigned)((pl.narrow_keys + kSumThreads - 1) / kSumThreads), (unsigned)p.R),
+    st = launch_after(mass_sum_kernel, dim3((unsigned)((pl.narrow_keys + p.sum_keys - 1) / p.sum_keys), (unsigned)p.R),
                       kSumThreads, (size_t)p.Hkv * pl.max_narrow_rows * 4, s, true, p);
     if (st != PA_OK) return st;
   }
@@ -1087,7 +1181,8 @@ extern "C" pa_status pa_attention_mass(
     return PA_ERR_INVALID;
   if (qsl_host[0] != 0 || qsl_host[num_reqs] != num_tokens) return PA_ERR_INVALID;
   MassPlan pl;
-  st = plan_mass(qsl_host, seq_lens_host, num_reqs, num_q_heads, pool->num_kv_heads, window, pl);
+  MassParams p{};
+  st = plan_mass(qsl_host, seq_lens_host, num_reqs, num_q_heads, pool->num_kv_heads, window, pl, p.wide);
   if (st != PA_OK) return st;
   for (int r = 0; r < num_reqs; ++r)
     if (qsl_host[r + 1] > qsl_host[r] && (seq_lens_host[r] > (int64_t)max_blocks * pool->block_size ||
@@ -1095,9 +1190,8 @@ extern "C" pa_status pa_attention_mass(
       return PA_ERR_INVALID;
   if (!workspace || workspace_bytes < pl.total || !aligned16(workspace)) return PA_ERR_INVALID;
   if (num_reqs > 65535 || pool->num_kv_heads > 65535 ||
-      pool->num_kv_heads * pl.max_narrow_rows > 12288)
+      pool->num_kv_heads * pl.max_narrow_rows > kSumRows)
     return PA_ERR_UNSUPPORTED;
-  MassParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.mass_in = mass_in;
   p.mass_out = mass_out;
@@ -1125,6 +1219,12 @@ extern "C" pa_status pa_attention_mass(
   p.split_stats = reinterpret_cast<float2*>(ws + pl.off_stats);
   p.splits = pl.splits;
   p.narrow_rows = (int)pl.max_narrow_rows;
+  p.groups = pl.groups;
+  p.forms = pl.forms;
+  // Eight threads a key where a thread a key would leave SMs idle (3 decodes of 128 heads on
+  // 200 tokens 9.6 us instead of 12.2, 13 x 4 to 6 tokens of 32 heads on 210 13 instead of
+  // 28); else one, which joins the rows' statistics for more keys.
+  p.sum_keys = (pl.narrow_keys + kSumThreads - 1) / kSumThreads * num_reqs <= num_sms() ? kSumThreads / 8 : kSumThreads;
   p.first_tile = reinterpret_cast<int*>(ws + pl.off_first);
   p.images = ws + pl.off_images;
   p.tile_stats = reinterpret_cast<float2*>(ws + pl.off_tile_stats);

@@ -501,3 +501,48 @@ def test_captured_calls_follow_the_device(cuda_device):
         for r in range(R):
             assert np.array_equal(kept[r].cpu().numpy(),
                                   ref.pick(mass[r].cpu().numpy(), seq[r], 2, 8, 50))
+
+
+MASS_FORMS = [  # new tokens and lengths of a batch; Hq, Hkv
+    ([1, 9, 40, 3, 0, 100], [300, 40, 150, 3, 20, 260], 4, 2),  # 2, 18, 80, 6, 200 rows a kv head
+    ([9, 20, 1, 21], [1100, 20, 700, 130], 6, 2),               # 27, 60, 3, 63: streamed in parts of 16
+    ([16, 1, 11], [16, 2100, 300], 4, 1),                       # 64, 4, 44
+    ([8] * 20, list(range(60, 160, 5)), 64, 8),                 # 64 rows each, too much to stream
+    ([17, 40], [500, 90], 8, 2),                                # none to stream
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("case", range(len(MASS_FORMS)))
+def test_mass_forms(cuda_device, case, fp8):
+    new, seqs, Hq, Hkv = MASS_FORMS[case]
+    rng = np.random.default_rng(600 + case)
+    check(*run_mass(cuda_device, rng, seqs, new, Hq, Hkv, 128 if case % 2 else 64, 16, fp8))
+
+
+@pytest.mark.parametrize("new,less", [
+    ([20, 1, 30, 12], [1, 1, 30, 2]), ([12, 1, 15], [2, 0, 15]), ([20, 30], [1, 2]),
+    ([20, 30, 1], [3, 0, 1]), ([20, 30, 1], [0, 18, 0])], ids=str)
+def test_mass_device_lengths_below_the_mirrors(cuda_device, new, less):
+    """Whatever form the mirrors planned for a request, fewer rows and tokens of it are
+    summed right."""
+    dev, B, Hkv, Hq, D = cuda_device, 16, 2, 8, 64
+    rng = np.random.default_rng(31)
+    R = len(new)
+    seqs = [int(n) for n in rng.integers(200, 400, size=R)]
+    fewer = [int(rng.integers(max(less[r], 1), seqs[r])) for r in range(R)]
+    table, qsl, blocks = batch(rng, seqs, new, B, dev, wide=1)
+    pool = make_pool(rng, blocks, Hkv, B, D, False, dev)
+    q = torch.from_numpy(rng.standard_normal((int(qsl[-1]), Hq, D))).to(dev).bfloat16()
+    qh, sh = np.array(qsl, np.int32), np.array(seqs, np.int32)
+    dev_qsl = np.concatenate([[0], np.cumsum(less)])
+    old = torch.rand((R, 420), device=dev)
+    ws = torch.empty(pa.attention_mass_workspace_size(qh, sh, Hq, Hkv), dtype=torch.uint8, device=dev)
+    out = torch.full_like(old, 7.0)
+    pa.attention_mass(q, old, out, i32(dev_qsl, dev), i32(fewer, dev), qh, sh, i32(table, dev), pool,
+                      0.125, workspace=ws)
+    assert pa.get_error() == pa.PA_OK
+    want, tol = ref.mass(ref.f64(q), ref.cells(pool.k), ref.f64(old), list(range(R)), table,
+                         dev_qsl.tolist(), fewer, B, Hq // Hkv, 0.125, 1.0, 1.0, 0,
+                         np.full((R, 420), 7.0), False)
+    check(ref.f64(out), want, tol)

@@ -130,7 +130,7 @@ def test_mass_workspace():
     assert size([0, 1, 2], [1000, 500], 8, 2) > size([0, 1], [1000], 8, 2)
     rows = 64 * 8
     assert size([0, 64], [1000], 8, 2) >= rows * 128 * 2
-    assert size([0, 64], [1000], 8, 2, window=16) < size([0, 64], [1000], 8, 2)
+    assert size([0, 64], [1000], 8, 2, window=4) < size([0, 64], [1000], 8, 2, window=16)
     assert size([0, 0], [1000], 8, 2) == 0
     assert size([0, 5], [4], 8, 2) == 0 and size([0, 5], [9], 7, 2) == 0
     with pytest.raises(ValueError):
