@@ -45,7 +45,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNarrowRows = 16;     // rows that a CTA of the streaming form takes
 constexpr int kStreamRows = 64;     // rows of a request of that form, at the most
-constexpr int kStreamUnits = 608;   // its CTAs, where they are to spare the tcgen05 form
+constexpr int kStreamUnits = 304;   // its CTAs, where they are to spare the tcgen05 form: one round
 constexpr int kSumRows = 12288;     // rows of all kv heads whose sums are at hand in shared memory
 constexpr int kSplitKeys = 1024;    // keys of one of its CTAs
 constexpr int kTile = 128;          // rows, and keys, of a tcgen05 tile
@@ -989,9 +989,11 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   const int64_t g = Hq / Hkv;
   int64_t narrow_keys = 0, wide_keys = 0;
   // The rows up to which keys are streamed, 16 rows at a time: 16, or 64 where no request
-  // has more and what has more than 16 makes no more than two rounds of CTAs, so that the
-  // four launches of the tcgen05 form do not run: 3 x 2 to 7 tokens of 40 heads on 130 tokens
-  // 14 us instead of 46, 13 x 6 of 32 heads on 210 13 instead of 37.
+  // has more and what has more than 16 makes no more than a round of CTAs, so that the four
+  // launches of the tcgen05 form do not run: 3 x 2 to 7 tokens of 40 heads on 130 tokens 14 us
+  // instead of 46, 13 x 6 of 32 heads on 210 13 instead of 37. (Up to 128 rows and two rounds:
+  // 2 x 16 tokens of 16 heads on 16 tokens 12 instead of 16, but 5 x 64 of 16 heads on 551 to
+  // 1802, where the scores are written and read again, 60 instead of 26.)
   int64_t stream_rows = kNarrowRows, units = 0, most = 0;
   for (int r = 0; r < R; ++r) {
     const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];

@@ -522,7 +522,8 @@ def test_mass_forms(cuda_device, case, fp8):
 
 @pytest.mark.parametrize("new,less", [
     ([20, 1, 30, 12], [1, 1, 30, 2]), ([12, 1, 15], [2, 0, 15]), ([20, 30], [1, 2]),
-    ([20, 30, 1], [3, 0, 1]), ([20, 30, 1], [0, 18, 0])], ids=str)
+    ([20, 30, 1], [3, 0, 1]), ([20, 30, 1], [0, 18, 0]), ([40, 1, 30, 12], [1, 1, 30, 2]),
+    ([40, 50], [1, 2]), ([40, 1, 3], [4, 0, 3])], ids=str)
 def test_mass_device_lengths_below_the_mirrors(cuda_device, new, less):
     """Whatever form the mirrors planned for a request, fewer rows and tokens of it are
     summed right."""
