@@ -18,8 +18,9 @@
 //  - more rows (the last queries of a prompt): scores are made twice on tcgen05,
 //    128 x 128 at a time, never leaving the SM. Pass 1 has query rows as the
 //    accumulator's lanes, so that a thread owns a row and its running maximum
-//    and sum; pass 2 has keys as lanes, S^T = K Q^T, so that a thread owns a key
-//    and adds its weights in registers, over all rows of all heads: no atomics,
+//    and sum; pass 2 has keys as lanes, S^T = K Q^T, so that the weights of a key
+//    are added in the registers of four threads, over the rows of a tile, and over
+//    tiles by a last kernel: no atomics,
 //    and the order of every sum follows from the sizes alone.
 //    The query rows are laid out once per call as shared-memory images of 128
 //    rows, swizzled as the tensor cores read them, which one bulk copy fetches;

@@ -547,3 +547,11 @@ def test_mass_device_lengths_below_the_mirrors(cuda_device, new, less):
                          dev_qsl.tolist(), fewer, B, Hq // Hkv, 0.125, 1.0, 1.0, 0,
                          np.full((R, 420), 7.0), False)
     check(ref.f64(out), want, tol)
+
+
+@pytest.mark.parametrize("most", [1, 3])
+def test_sparse_of_many_requests(cuda_device, most):
+    rng = np.random.default_rng(90 + most)
+    new = rng.integers(0, most + 1, size=300)
+    seqs = (new + rng.integers(0, 60, size=300)).tolist()
+    check(*attend(cuda_device, rng, seqs, new.tolist(), 4, 1, 64, 16, 3, False))

@@ -308,3 +308,26 @@ def test_select_refuses_what_leaves_the_buffers(cuda_device):
     assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS
     assert (out[0] == 9).all()
     assert np.array_equal(out[1, 0].cpu().numpy(), ref.pick(s[1, 0].cpu().numpy(), 2, 0, 0, 2))
+
+
+@pytest.mark.parametrize("R,most", [(33, 1), (1100, 1), (1100, 3), (2100, 1)])
+def test_rows_of_many_requests(cuda_device, R, most):
+    """More requests than a warp's lanes, and than their square: which request a row or a
+    unit of work belongs to."""
+    dev, B, Hkv = cuda_device, 16, 1
+    rng = np.random.default_rng(R + most)
+    new = rng.integers(0, most + 1, size=R)
+    seqs = (new + rng.integers(0, 70, size=R)).tolist()
+    got, want, tol = run_scores(dev, rng, seqs, new.tolist(), 4, Hkv, 64, B, False)
+    assert pa.get_error() == pa.PA_OK
+    assert (np.abs(got - want) <= tol).all()
+    qsl = np.cumsum([0] + new.tolist())
+    x = rng.standard_normal((int(qsl[-1]) + 2, Hkv, 5)).astype(np.float32)
+    selected = torch.full((x.shape[0], Hkv, 3), 7, dtype=torch.int32, device=dev)
+    pa.select_blocks(torch.from_numpy(x).to(dev), selected, i32(qsl, dev), i32(seqs, dev), B,
+                     first=0, last=1)
+    out = np.full((x.shape[0], Hkv, 3), 7)
+    for r, t, p in ref.rows_of(qsl.tolist(), seqs):
+        out[t, 0] = ref.pick(x[t, 0], p // B + 1, 0, 1, 3)
+    assert pa.get_error() == pa.PA_OK
+    assert np.array_equal(selected.cpu().numpy(), out)
