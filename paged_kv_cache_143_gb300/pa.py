@@ -950,6 +950,13 @@ def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, 
 
 
 # ------------------------------------------------- attention to a part of a cache
+#
+# Most of these calls take a few microseconds on the device, less than a dozen Python
+# calls, so what _device_of, _pool_on and _on do is written out where it succeeds.
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 
 def _pool_on(pool: KVPool, dev: int) -> None:
     if pool.k.get_device() != dev or pool.v.get_device() != dev:
@@ -993,15 +1000,18 @@ def update_block_bounds(pool: KVPool, bounds: torch.Tensor, block_tables: torch.
             raise ValueError("query_start_loc must have num_reqs + 1 entries")
         if num_tokens is None:
             raise ValueError("query_start_loc comes with num_tokens, the most that it may reach")
-    dev = _device_of(bounds, "bounds")
-    _pool_on(pool, dev)
-    if not (bounds.dtype is _BF16 and block_tables.dtype is _I32 is seq_lens.dtype
+    dev = bounds.get_device()
+    if dev < 0 or dev != _current_device():
+        _device_of(bounds, "bounds")
+    if not (pool.k.get_device() == pool.v.get_device() == dev
+            and bounds.dtype is _BF16 and block_tables.dtype is _I32 is seq_lens.dtype
             and block_tables.get_device() == seq_lens.get_device() == dev
             and bounds.is_contiguous() and block_tables.is_contiguous()
             and seq_lens.is_contiguous()
             and (query_start_loc is None or (
                 query_start_loc.dtype is _I32 and query_start_loc.get_device() == dev
                 and query_start_loc.is_contiguous()))):
+        _pool_on(pool, dev)
         _explain(dev, (bounds, "bounds", _BF16, True), (block_tables, "block_tables", _I32, True),
                  (seq_lens, "seq_lens", _I32, True),
                  (query_start_loc, "query_start_loc", _I32, True))
@@ -1009,7 +1019,7 @@ def update_block_bounds(pool: KVPool, bounds: torch.Tensor, block_tables: torch.
         pool.ref(), bounds.data_ptr(),
         None if query_start_loc is None else query_start_loc.data_ptr(), seq_lens.data_ptr(),
         block_tables.data_ptr(), max_blocks, R, 0 if query_start_loc is None else num_tokens,
-        _on(dev, stream))
+        _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(st, "pa_update_block_bounds")
 
@@ -1026,22 +1036,25 @@ def score_blocks(q: torch.Tensor, bounds: torch.Tensor, scores: torch.Tensor,
         raise ValueError("q must be [T][Hq][head_dim] and scores [T][num_kv_heads][max_blocks]")
     if bounds.shape != (pool.num_blocks, pool.num_kv_heads, 2, D):
         raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim]")
-    dev = _device_of(q, "q")
-    _pool_on(pool, dev)
-    if not (q.dtype is _BF16 is bounds.dtype and scores.dtype is _F32
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        _device_of(q, "q")
+    if not (pool.k.get_device() == pool.v.get_device() == dev
+            and q.dtype is _BF16 is bounds.dtype and scores.dtype is _F32
             and query_start_loc.dtype is _I32 is seq_lens.dtype and block_tables.dtype is _I32
             and (bounds.get_device() == scores.get_device() == query_start_loc.get_device()
                  == seq_lens.get_device() == block_tables.get_device() == dev)
             and q.is_contiguous() and bounds.is_contiguous() and scores.is_contiguous()
             and query_start_loc.is_contiguous() and seq_lens.is_contiguous()
             and block_tables.is_contiguous()):
+        _pool_on(pool, dev)
         _explain(dev, (q, "q", _BF16, True), (bounds, "bounds", _BF16, True),
                  (scores, "scores", _F32, True), (query_start_loc, "query_start_loc", _I32, True),
                  (seq_lens, "seq_lens", _I32, True), (block_tables, "block_tables", _I32, True))
     st = (_lib or lib()).pa_score_blocks(
         q.data_ptr(), bounds.data_ptr(), scores.data_ptr(), query_start_loc.data_ptr(),
         seq_lens.data_ptr(), block_tables.data_ptr(), max_blocks, R, T, Hq, pool.ref(),
-        _on(dev, stream))
+        _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(st, "pa_score_blocks")
 
@@ -1059,7 +1072,9 @@ def select_blocks(scores: torch.Tensor, selected: torch.Tensor, query_start_loc:
     rows, heads, k = _shape(selected, 3, "selected must be [T][num_kv_heads][k]")
     if rows != T or heads != H:
         raise ValueError("selected must be [T][num_kv_heads][k]")
-    dev = _device_of(scores, "scores")
+    dev = scores.get_device()
+    if dev < 0 or dev != _current_device():
+        _device_of(scores, "scores")
     if not (scores.dtype is _F32 and selected.dtype is _I32
             and query_start_loc.dtype is _I32 is seq_lens.dtype
             and (selected.get_device() == query_start_loc.get_device() == seq_lens.get_device()
@@ -1072,7 +1087,7 @@ def select_blocks(scores: torch.Tensor, selected: torch.Tensor, query_start_loc:
     st = (_lib or lib()).pa_select_blocks(
         scores.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(), R, T, H, max_blocks,
         int(block_size), int(first), int(last), k, selected.data_ptr(),
-        _on(dev, stream))
+        _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(st, "pa_select_blocks")
 
@@ -1090,15 +1105,18 @@ def sparse_forward(q: torch.Tensor, out: torch.Tensor, query_start_loc: torch.Te
     rows, heads, k = _shape(selected, 3, "selected must be [T][num_kv_heads][k]")
     if rows != T or heads != pool.num_kv_heads:
         raise ValueError("selected must be [T][num_kv_heads][k]")
-    dev = _device_of(q, "q")
-    _pool_on(pool, dev)
-    if not (q.dtype is _BF16 is out.dtype and selected.dtype is _I32
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        _device_of(q, "q")
+    if not (pool.k.get_device() == pool.v.get_device() == dev
+            and q.dtype is _BF16 is out.dtype and selected.dtype is _I32
             and query_start_loc.dtype is _I32 is seq_lens.dtype and block_tables.dtype is _I32
             and (out.get_device() == selected.get_device() == query_start_loc.get_device()
                  == seq_lens.get_device() == block_tables.get_device() == dev)
             and q.is_contiguous() and out.is_contiguous() and selected.is_contiguous()
             and query_start_loc.is_contiguous() and seq_lens.is_contiguous()
             and block_tables.is_contiguous()):
+        _pool_on(pool, dev)
         _explain(dev, (q, "q", _BF16, True), (out, "out", _BF16, True),
                  (selected, "selected", _I32, True),
                  (query_start_loc, "query_start_loc", _I32, True),
@@ -1106,7 +1124,7 @@ def sparse_forward(q: torch.Tensor, out: torch.Tensor, query_start_loc: torch.Te
     st = (_lib or lib()).pa_sparse_forward(
         q.data_ptr(), out.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(),
         block_tables.data_ptr(), max_blocks, R, T, Hq, selected.data_ptr(), k, pool.ref(),
-        float(scale), _on(dev, stream))
+        float(scale), _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(st, "pa_sparse_forward")
 
@@ -1152,9 +1170,11 @@ def attention_mass(q: torch.Tensor, mass_in: torch.Tensor, mass_out: torch.Tenso
     rows, places = shape = _mass_shape(mass_in, idx_mapping, R)
     if mass_out.shape != shape:
         raise ValueError("mass_in and mass_out must have one shape")
-    dev = _device_of(q, "q")
-    _pool_on(pool, dev)
-    if not (q.dtype is _BF16 and mass_in.dtype is _F32 is mass_out.dtype
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        _device_of(q, "q")
+    if not (pool.k.get_device() == pool.v.get_device() == dev
+            and q.dtype is _BF16 and mass_in.dtype is _F32 is mass_out.dtype
             and query_start_loc.dtype is _I32 is seq_lens.dtype and block_tables.dtype is _I32
             and (mass_in.get_device() == mass_out.get_device() == query_start_loc.get_device()
                  == seq_lens.get_device() == block_tables.get_device() == dev)
@@ -1166,6 +1186,7 @@ def attention_mass(q: torch.Tensor, mass_in: torch.Tensor, mass_out: torch.Tenso
                 and idx_mapping.is_contiguous()))
             and (workspace is None or (workspace.get_device() == dev
                                        and workspace.is_contiguous()))):
+        _pool_on(pool, dev)
         _explain(dev, (q, "q", _BF16, True), (mass_in, "mass_in", _F32, True),
                  (mass_out, "mass_out", _F32, True),
                  (query_start_loc, "query_start_loc", _I32, True),
@@ -1179,7 +1200,7 @@ def attention_mass(q: torch.Tensor, mass_in: torch.Tensor, mass_out: torch.Tenso
         block_tables.data_ptr(), max_blocks, R, T, Hq, pool.ref(), float(scale), float(decay),
         int(window), None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _on(dev, stream))
+        _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(st, "pa_attention_mass")
 
@@ -1195,7 +1216,9 @@ def select_tokens(mass: torch.Tensor, kept: torch.Tensor, kept_lens: torch.Tenso
     lists, k = _shape(kept, 2, "kept must be [num_reqs][k]")
     if lists != R or kept_lens.numel() != R:
         raise ValueError("kept must be [num_reqs][k] and kept_lens have num_reqs entries")
-    dev = _device_of(mass, "mass")
+    dev = mass.get_device()
+    if dev < 0 or dev != _current_device():
+        _device_of(mass, "mass")
     if not (mass.dtype is _F32 and kept.dtype is _I32 is kept_lens.dtype
             and seq_lens.dtype is _I32
             and (kept.get_device() == kept_lens.get_device() == seq_lens.get_device() == dev)
@@ -1210,7 +1233,7 @@ def select_tokens(mass: torch.Tensor, kept: torch.Tensor, kept_lens: torch.Tenso
     st = (_lib or lib()).pa_select_tokens(
         mass.data_ptr(), places, rows, None if idx_mapping is None else idx_mapping.data_ptr(),
         seq_lens.data_ptr(), R, int(first), int(last), k, kept.data_ptr(), kept_lens.data_ptr(),
-        _on(dev, stream))
+        _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(st, "pa_select_tokens")
 
@@ -1236,9 +1259,12 @@ def compact_cache(pool: KVPool, src_tables: torch.Tensor, dst_tables: torch.Tens
         rows, places = shape = _mass_shape(mass_in, idx_mapping, R)
         if mass_out.shape != shape:
             raise ValueError("mass_in and mass_out must have one shape")
-    dev = _device_of(kept, "kept")
-    _pool_on(pool, dev)
-    if not (kept.dtype is _I32 is kept_lens.dtype and src_tables.dtype is _I32 is dst_tables.dtype
+    dev = kept.get_device()
+    if dev < 0 or dev != _current_device():
+        _device_of(kept, "kept")
+    if not (pool.k.get_device() == pool.v.get_device() == dev
+            and kept.dtype is _I32 is kept_lens.dtype
+            and src_tables.dtype is _I32 is dst_tables.dtype
             and (kept_lens.get_device() == src_tables.get_device() == dst_tables.get_device()
                  == dev)
             and kept.is_contiguous() and kept_lens.is_contiguous()
@@ -1250,6 +1276,7 @@ def compact_cache(pool: KVPool, src_tables: torch.Tensor, dst_tables: torch.Tens
             and (idx_mapping is None or (
                 idx_mapping.dtype is _I32 and idx_mapping.get_device() == dev
                 and idx_mapping.is_contiguous()))):
+        _pool_on(pool, dev)
         _explain(dev, (kept, "kept", _I32, True), (kept_lens, "kept_lens", _I32, True),
                  (src_tables, "src_tables", _I32, True), (dst_tables, "dst_tables", _I32, True),
                  (mass_in, "mass_in", _F32, True), (mass_out, "mass_out", _F32, True),
@@ -1259,7 +1286,8 @@ def compact_cache(pool: KVPool, src_tables: torch.Tensor, dst_tables: torch.Tens
         kept.data_ptr(), k, kept_lens.data_ptr(), R,
         None if mass_in is None else mass_in.data_ptr(),
         None if mass_out is None else mass_out.data_ptr(), places, rows,
-        None if idx_mapping is None else idx_mapping.data_ptr(), _on(dev, stream))
+        None if idx_mapping is None else idx_mapping.data_ptr(),
+        _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(st, "pa_compact_cache")
 
