@@ -13,8 +13,10 @@
 //  - S^T = K Q^T and O^T += V^T P^T are warp-level m16n8k16 MMAs with the 16 keys
 //    of a cell as rows and the heads as columns (cells.cuh; g heads are far below
 //    the smallest tcgen05 tile), the running maximum and sum of the softmax per
-//    head in registers, in fp32; the weights are rounded to 16 bits for the second
-//    product.
+//    head in registers, in fp32. The second product takes each weight as the sum of
+//    two 16-bit numbers (bf16 alone is off by 2^-9 of each weight, as much as the output's
+//    own rounding; with the second, decodes take what they took, 300 tokens of a chunk
+//    96 us instead of 90).
 //  - The warps join by log-sum-exp in shared memory. Where there are too few
 //    (token, kv head) pairs for the GPU, a cluster of 2, 4 or 8 CTAs shares each
 //    list and joins through distributed shared memory: no workspace, one launch.
@@ -71,13 +73,37 @@ struct CellHeads {
     }
   }
 
+  // 2^x, x a score less its reference (up to 8); for f16 parts, exact to 2^-25 at the best,
+  // times 2^7, which makes that 2^-32 of the reference's weight.
+  static __device__ __forceinline__ float weight(float x) { return ex2_ftz(FP8 ? x + 7.f : x); }
+
+  // Two weights as sums of two 16-bit numbers, hi + lo. f16 (E4M3 pools): both rounded, off by
+  // 2^-23. bf16: hi is cut off below the weight, so that lo is positive like hi and an
+  // infinite value keeps its sign; off by (2^-7 + 2^-10) 2^-9, just above 2^-16.
+  static __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+    if constexpr (FP8) {
+      const __half2 a = __floats2half2_rn(x, y);
+      const float2 f = __half22float2(a);
+      const __half2 b = __floats2half2_rn(x - f.x, y - f.y);
+      hi = *reinterpret_cast<const uint32_t*>(&a);
+      lo = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      constexpr float kBelow = 1.f - 0x1p-10f;
+      const uint32_t a = __float_as_uint(x * kBelow) & 0xffff0000u;
+      const uint32_t b = __float_as_uint(y * kBelow) & 0xffff0000u;
+      const __nv_bfloat162 rest = __floats2bfloat162_rn(x - __uint_as_float(a), y - __uint_as_float(b));
+      hi = (a >> 16) | b;
+      lo = *reinterpret_cast<const uint32_t*>(&rest);
+    }
+  }
+
   // The cell's keys Ks and values Vs, of which the first n are visible (1..16).
   __device__ __forceinline__ void cell(const uint8_t* Ks, const uint8_t* Vs, int n, int grp,
                                        int tig) {
     float s[NH][4];
     q.scores(Ks, s, grp, tig);
     const bool whole = n >= 16;
-    uint32_t pb[NH][2];
+    uint32_t pb[NH][2], pl[NH][2];  // the weights, and what their rounding left
     bool rescale = false;
     float alpha[NH][2];
 #pragma unroll
@@ -94,24 +120,19 @@ struct CellHeads {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
         const float ref = MmaRows<D, FP8>::rebase(m[h][e], mx, alpha[h][e]);
         const float base = ref == -INFINITY ? 0.f : ref;  // (-inf minus -inf would be NaN)
-        x0 = ex2_ftz(x0 - base);
-        x1 = ex2_ftz(x1 - base);
+        x0 = weight(x0 - base);
+        x1 = weight(x1 - base);
         l[h][e] = l[h][e] * alpha[h][e] + (x0 + x1);
         m[h][e] = ref;
         rescale |= alpha[h][e] != 1.f;
       }
-      if (FP8) {
-        __half2 a = __floats2half2_rn(s[h][0], s[h][1]), b = __floats2half2_rn(s[h][2], s[h][3]);
-        pb[h][0] = *reinterpret_cast<uint32_t*>(&a);
-        pb[h][1] = *reinterpret_cast<uint32_t*>(&b);
-      } else {
-        __nv_bfloat162 a = __floats2bfloat162_rn(s[h][0], s[h][1]);
-        __nv_bfloat162 b = __floats2bfloat162_rn(s[h][2], s[h][3]);
-        pb[h][0] = *reinterpret_cast<uint32_t*>(&a);
-        pb[h][1] = *reinterpret_cast<uint32_t*>(&b);
+      split(s[h][0], s[h][1], pb[h][0], pl[h][0]);
+      split(s[h][2], s[h][3], pb[h][1], pl[h][1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        MmaKeys<D, FP8>::movtrans(pb[h][i]);
+        MmaKeys<D, FP8>::movtrans(pl[h][i]);
       }
-      MmaKeys<D, FP8>::movtrans(pb[h][0]);
-      MmaKeys<D, FP8>::movtrans(pb[h][1]);
     }
     if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
@@ -141,7 +162,10 @@ struct CellHeads {
       asm("prmt.b32 %0, %1, %2, 0x5410;" : "=r"(a2) : "r"(vw[2][mt]), "r"(vw[3][mt]));
       asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(a3) : "r"(vw[2][mt]), "r"(vw[3][mt]));
 #pragma unroll
-      for (int h = 0; h < NH; ++h) MmaRows<D, FP8>::mma(o[h][mt], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+      for (int h = 0; h < NH; ++h) {
+        MmaRows<D, FP8>::mma(o[h][mt], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+        MmaRows<D, FP8>::mma(o[h][mt], a0, a1, a2, a3, pl[h][0], pl[h][1]);
+      }
     }
   }
 
@@ -460,7 +484,7 @@ extern "C" pa_status pa_sparse_forward(const void* q, void* out, const int32_t* 
   // 128 blocks of 16 keys (bf16, 8 kv heads), by the time of an earlier inner loop: 8
   // decodes 31 us alone, 23 by 2 or 4, 31 by 8; 24: 45, 43, 47, 61; 64: 119, 109, 111,
   // 141; 300 tokens of a chunk (64 blocks): 164, 201. As it is now, by this rule: 20.5,
-  // 39, 92, 90.
+  // 41, 92, 96.
   const int64_t units = (int64_t)num_tokens * p.Hkv * p.parts;
   const int64_t at_once = (int64_t)(wide ? 2 : 3) * num_sms();
   p.split = 1;

@@ -1,0 +1,108 @@
+"""GPU tests of the calls on a part of a cache at their edges: what is left after
+values cancel, device lengths above the mirrors, many heads, bad block ids."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_143_gb300 import pa
+from tests import partial_reference as ref
+from tests.test_gpu_partial_attention import check
+from tests.test_gpu_partial_select import batch, i32, make_pool
+
+pytestmark = pytest.mark.gpu
+
+
+def code(x, fp8):
+    """The nearest bf16, or E4M3 code."""
+    x = torch.as_tensor(x)
+    return x.float().to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x.bfloat16()
+
+
+def cancelling(dev, rng, Hkv, g, D, fp8, k):
+    """One token on 40 keys: eight whose weights fall by about e^2 from one to the next, the
+    others' below e^-100. In every dim the values of the eight are chosen one after the other
+    to cancel what stands, so that of weights of about 1 hardly anything is left."""
+    B, n, scale = 16, 40, 1.0
+    pool = make_pool(rng, 5, Hkv, B, D, fp8, dev)
+    unit, unit_v = pool.k_scale, pool.v_scale
+    q = torch.zeros((1, Hkv * g, D), device=dev)
+    q[..., 0] = 8.0
+    table = np.array([[3, 0, 4]])
+    for h in range(Hkv):
+        s = np.full(n, -17.0)
+        order = rng.permutation(n)[:8]
+        s[order] = -(2.1 * np.arange(8) + rng.random(8) * 0.5) / 8
+        ks = code(s / unit, fp8)
+        cells = [(int(table[0, i // B]), i % B) for i in range(n)]
+        for i, (b, o) in enumerate(cells):
+            pool.k[b, h, o, 0] = ks[i].to(dev)
+        x = 8.0 * unit * ref.cells(ks.reshape(1, -1))[0]
+        w = np.exp(x - x.max())
+        w /= w.sum()
+        rest = np.array([w[i] for i in range(n) if i not in order])
+        assert rest.max() < np.exp(-100.0)
+        left = np.zeros(D)
+        for j, i in enumerate(order):
+            v = (rng.random(D) + 0.5 if j == 0 else -left / w[i]) / unit_v
+            c = code(v, fp8)
+            b, o = cells[i]
+            pool.v[b, h, o] = c.to(dev)
+            left += w[i] * ref.cells(c.reshape(1, -1))[0] * unit_v
+    sel = np.full((1, Hkv, k), -1)
+    sel[0, :, rng.permutation(k)[:3]] = np.array([0, 1, 2])[:, None]
+    out = torch.zeros((1, Hkv * g, D), dtype=torch.bfloat16, device=dev)
+    q = q.bfloat16()
+    pa.sparse_forward(q, out, i32([0, 1], dev), i32([n], dev), i32(table, dev), i32(sel, dev), pool,
+                      scale)
+    assert pa.get_error() == pa.PA_OK
+    K, V = ref.cells(pool.k), ref.cells(pool.v)
+    want, _ = ref.sparse(ref.f64(q), K, V, table, sel, [0, 1], [n], B, g, scale, unit, unit_v, fp8)
+    # A score is one product: its factor (three roundings), the product and the difference to the
+    # reference, each half a step of at most 25 in units of log 2, for the weight and for the sum.
+    # A weight is off by 2^-15 (f16: 2^-22) in the second product, by 2^-20 from exp2 and sums;
+    # the output is rounded to bf16.
+    rel = 2 * 5 * 25 * 2.0 ** -24 * np.log(2) + 2.0 ** -20 + 2.0 ** (-22 if fp8 else -15)
+    tol = np.zeros(want.shape)
+    for h in range(Hkv):
+        Kh = ref.context(K, table[0], n, B, h) * unit
+        Vh = np.abs(ref.context(V, table[0], n, B, h)) * unit_v
+        x = scale * Kh @ ref.f64(q)[0, h * g]
+        w = np.exp(x - x.max())
+        tol[0, h * g:(h + 1) * g] = (w / w.sum()) @ Vh * rel
+    assert (np.abs(want) < 2.0 ** -10).all()
+    check(ref.f64(out), want, tol + 2.0 ** -8 * (np.abs(want) + tol))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("g", [1, 4, 12])
+@pytest.mark.parametrize("k", [3, 200], ids=["one CTA", "cluster"])
+def test_sparse_where_values_cancel(cuda_device, k, g, D, fp8):
+    """Weights enter the second product with more bits than a 16-bit number has."""
+    cancelling(cuda_device, np.random.default_rng(g + D + k), 8, g, D, fp8, k)
+
+
+def test_sparse_infinite_values(cuda_device):
+    """An infinite value that a row sees gives an infinity of its sign, whatever bits of the
+    weight the second product takes one by one; two of different signs give NaN."""
+    dev, B, D = cuda_device, 16, 64
+    rng = np.random.default_rng(3)
+    pool = make_pool(rng, 4, 1, B, D, False, dev)
+    pool.v[1, 0, 3, 5] = float("inf")
+    pool.v[1, 0, 7, 6] = float("-inf")
+    pool.v[2, 0, 0, 7] = float("inf")
+    pool.v[2, 0, 1, 7] = float("-inf")
+    pool.v[2, 0, 9, 8] = float("inf")  # behind the token
+    q = torch.from_numpy(rng.standard_normal((1, 4, D))).to(dev).bfloat16()
+    q[0, 3] = 0  # equal weights, powers of two: nothing is left of them
+    sel = np.array([[[1, 0]]])
+    out = torch.zeros_like(q)
+    pa.sparse_forward(q, out, i32([0, 1], dev), i32([24], dev), i32([[1, 2]], dev), i32(sel, dev),
+                      pool, 0.125)
+    assert pa.get_error() == pa.PA_OK
+    want, tol = ref.sparse(ref.f64(q), ref.cells(pool.k), ref.cells(pool.v), [[1, 2]], sel, [0, 1],
+                           [24], B, 4, 0.125, 1.0, 1.0, False)
+    got = ref.f64(out)
+    assert (got[0, :, 5] == np.inf).all() and (got[0, :, 6] == -np.inf).all()
+    assert np.isnan(got[0, :, 7]).all() and np.isfinite(got[0, :, 8]).all()
+    check(got, want, tol)
