@@ -55,8 +55,7 @@ constexpr int kInfoBytes = 1024;    // behind an image: the score factors of its
 // feeds one packed multiply-add: the row's factor is at info_at(row), -lse 2 further.
 __device__ __forceinline__ int info_at(int row) { return (row >> 1) * 4 + (row & 1); }
 
-constexpr int kAllNarrow = 0, kAllWide = 1, kByBits = 2;
-constexpr int kMixedReqs = 4096;  // requests of a call with both forms, at the most
+constexpr int kFewReqs = 64;        // whose mirrors come with the launch
 
 struct MassParams {
   const __nv_bfloat16* q;
@@ -66,15 +65,14 @@ struct MassParams {
   const int32_t* idx;
   const int32_t* qsl;
   const int32_t* seq_lens;
+  const int2* mirrors;     // [R] the mirrors' new and stored tokens, of more than kFewReqs
   const int32_t* tables;
   int max_reqs, max_blocks, R, T, Hq, Hkv, g, B, num_blocks, window;
   float decay, qk_scale;   // softmax scale * log2(e) (* k_scale)
   // streaming form
   float* scores;           // request after request: [Hkv * rows][keys rounded up to 16]
-  int64_t score_floats;
   float2* split_stats;     // [R][Hkv][groups][16][splits] (maximum, sum)
   int splits;
-  int narrow_rows;         // rows of a request of this form, at the most
   int groups;              // of 16 rows
   int sum_keys;            // keys of a CTA of the sums
   // tcgen05 form: a step is a row tile of a kv head and a key tile; request r's are the
@@ -85,13 +83,10 @@ struct MassParams {
   float2* tile_stats;      // [n_tiles][Hkv][pieces][4][128]
   float* sums;             // [steps][128]: a step's weights, key by key
   int64_t steps, per_cta;  // in all, and of a CTA
-  int n_tiles, pieces;
-  int key_tiles;           // key tiles of the longest request
+  int pieces;
   unsigned* err;
-  // Which form a request takes is the mirrors' choice, so that a captured call whose
-  // device lengths shrink finds the room that was planned for it.
-  int forms;               // kAllNarrow, kAllWide, kByBits
-  uint32_t wide[kMixedReqs / 32];
+  int stream_rows;         // rows, by its mirror, up to which a request is streamed (-1: none is)
+  int2 few[kFewReqs];      // the mirrors of up to as many requests
 };
 
 struct MassReq {
@@ -99,18 +94,24 @@ struct MassReq {
   bool wide;                    // of the tcgen05 form
 };
 
+// Request r as the device has it; without rows where an entry leaves the buffers, or its
+// mirror, whose room is planned: what the requests before r take is then never more than
+// planned either, so that every request finds its own. The form that it takes is the
+// mirror's choice, so that a captured call whose lengths shrink finds it planned. (Mirrors
+// that come with every launch need no launch of their own: a decode on 3000 tokens 16.4 us
+// instead of 17.4.)
 __device__ __forceinline__ MassReq rows_of(const MassParams& p, int r) {
   const int q0 = p.qsl[r], end = p.qsl[r + 1], seq = p.seq_lens[r];
+  const int2 most = p.R <= kFewReqs ? p.few[r] : __ldcg(p.mirrors + r);
   MassReq m;
   m.q0 = q0;
   m.q_len = end - q0;
   m.seq = seq;
-  m.wide = p.forms == kAllWide || (p.forms == kByBits && ((p.wide[r >> 5] >> (r & 31)) & 1u));
-  const bool fine = q0 >= 0 && end <= p.T && end >= q0 && seq >= m.q_len &&
-                    seq <= (int64_t)p.max_blocks * p.B && seq <= p.mass_stride && seq <= kMostTokens;
+  m.wide = (int64_t)(p.window > 0 ? min(most.x, p.window) : most.x) * p.g > p.stream_rows;
+  // (the mirrors' tokens fit the table, the mass and 32 bits)
+  const bool fine = q0 >= 0 && end <= p.T && end >= q0 && seq >= m.q_len && m.q_len <= most.x && seq <= most.y;
   m.w = fine ? (p.window > 0 ? min(m.q_len, p.window) : m.q_len) : 0;
-  const int64_t rows = (int64_t)m.w * p.g;
-  m.rows = rows > 0x3fffffff ? 0 : (int)rows;
+  m.rows = m.w * p.g;
   return m;
 }
 // Whether request r was left out for entries that leave the buffers.
@@ -129,7 +130,7 @@ __device__ __forceinline__ int64_t before(const MassParams& p, int r, F f) {
 }
 
 __device__ __forceinline__ int64_t score_floats_of(const MassParams& p, const MassReq& m) {
-  return !m.wide && m.rows <= p.narrow_rows ? (int64_t)p.Hkv * m.rows * padded_keys(m.seq) : 0;
+  return m.wide ? 0 : (int64_t)p.Hkv * m.rows * padded_keys(m.seq);
 }
 
 __device__ __forceinline__ int mass_row(const MassParams& p, int r) {
@@ -142,6 +143,17 @@ __device__ __forceinline__ void join_stats(float& ref, float& sum, float m, floa
   const float top = fmaxf(ref, m), base = top == -INFINITY ? 0.f : top;
   sum = sum * ex2_ftz(ref - base) + l * ex2_ftz(m - base);
   ref = top;
+}
+
+// The mirrors as the kernels after it read them: passed by value, so that a captured call
+// keeps its own. 4 KB of parameters a launch.
+constexpr int kMirrorsAtOnce = 480;
+struct Mirrors {
+  int2 v[kMirrorsAtOnce];
+};
+__global__ void mass_mirrors_kernel(int2* out, int n, const __grid_constant__ Mirrors m) {
+  launch_dependents();
+  if ((int)threadIdx.x < n) out[threadIdx.x] = m.v[threadIdx.x];
 }
 
 // ------------------------------------------------------------ streaming form
@@ -162,6 +174,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
   NarrowTail* tail = reinterpret_cast<NarrowTail*>(ring + kNarrowWarps * kNarrowRing);
+  grid_dependency_wait();  // the mirrors are there (also for the kernel after this one)
   launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = lane >> 2, tig = lane & 3;
@@ -170,18 +183,13 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
   const MassReq m = rows_of(p, r);
   const bool reporter = tid == 0 && split == 0 && blockIdx.y == 0;
   if (m.wide) return;
-  if (bad_request(m) || m.rows > p.narrow_rows || (m.rows > 0 && mass_row(p, r) < 0)) {
-    if (reporter) raise_error(p.err, kErrBounds);  // (or more rows than the mirrors said)
-    return;
-  }
-  if (m.rows <= row0) return;
-  const int64_t at = before(p, r, [&](const MassReq& x) { return score_floats_of(p, x); });
-  if (at + score_floats_of(p, m) > p.score_floats || m.seq > (int64_t)p.splits * kSplitKeys) {
-    if (reporter) raise_error(p.err, kErrBounds);  // more than the mirrors said
+  if (bad_request(m) || (m.rows > 0 && mass_row(p, r) < 0)) {
+    if (reporter) raise_error(p.err, kErrBounds);
     return;
   }
   const int k0 = split * kSplitKeys;
-  if (k0 >= m.seq) return;
+  if (m.rows <= row0 || k0 >= m.seq) return;
+  const int64_t at = before(p, r, [&](const MassReq& x) { return score_floats_of(p, x); });
   const int n_cells = (min(m.seq - k0, kSplitKeys) + kChunk - 1) / kChunk;
   const int stride = padded_keys(m.seq);
   const int n_rows = min(kNarrowRows, m.rows - row0);
@@ -330,16 +338,12 @@ __global__ void __launch_bounds__(kSumThreads, 5) mass_sum_kernel(const __grid_c
   extern __shared__ float lse[];  // [Hkv * rows]
   const int r = blockIdx.y;
   const MassReq m = rows_of(p, r);
-  if (m.wide || m.rows == 0 || m.rows > p.narrow_rows || m.seq > (int64_t)p.splits * kSplitKeys) return;
+  if (m.wide || m.rows == 0) return;
   const int key0 = blockIdx.x * p.sum_keys;
   if (key0 >= m.seq) return;
-  const int64_t at = before(p, r, [&](const MassReq& x) { return score_floats_of(p, x); });
-  if (at + score_floats_of(p, m) > p.score_floats) return;
   const int slot = mass_row(p, r);
-  if (slot < 0) {
-    if (threadIdx.x == 0) raise_error(p.err, kErrBounds);
-    return;
-  }
+  if (slot < 0) return;  // (flagged)
+  const int64_t at = before(p, r, [&](const MassReq& x) { return score_floats_of(p, x); });
   grid_dependency_wait();  // the scores and their statistics are complete
   const int rows = p.Hkv * m.rows, n_split = (m.seq + kSplitKeys - 1) / kSplitKeys;
   // eight lanes for each row, all rows of up to 32 at once
@@ -430,6 +434,7 @@ __device__ __forceinline__ int swizzled(int row, int c) {
 template <int D, bool F8>
 __global__ void __launch_bounds__(kTile) mass_rows_kernel(const __grid_constant__ MassParams p) {
   using W = WideGeo<D, F8>;
+  grid_dependency_wait();  // the mirrors are there
   launch_dependents();
   const int ti = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
   const MassReq m = rows_of(p, r);
@@ -447,18 +452,12 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(const __grid_constant_
     return;
   }
   if (ti >= tiles) return;
-  const int key_tiles = (m.seq + kTile - 1) / kTile;
-  bool fits = first + tiles <= p.n_tiles && tiles <= (int)gridDim.x && key_tiles <= p.key_tiles &&
-              mass_row(p, r) >= 0;
-  if (ti == 0 && kvh == 0) {
-    const int64_t step = before(p, r, [&](const MassReq& x) { return steps_of(p, x); });
-    fits = fits && step + steps_of(p, m) <= p.steps;
-    if (tid == 0) {
-      p.first_tile[r] = fits ? (int)first : -1;
-      if (!fits) raise_error(p.err, kErrBounds);
-    }
+  const bool has_row = mass_row(p, r) >= 0;
+  if (reporter) {
+    p.first_tile[r] = has_row ? (int)first : -1;
+    if (!has_row) raise_error(p.err, kErrBounds);
   }
-  if (!fits) return;
+  if (!has_row) return;
   const int tile = (int)first + ti;
   uint8_t* image = p.images + ((int64_t)tile * p.Hkv + kvh) * W::kImage;
   const int c = ti * kTile + tid;
@@ -978,14 +977,13 @@ __global__ void __launch_bounds__(kSumThreads) mass_add_kernel(const __grid_cons
 struct MassPlan {
   int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows, steps, per_cta, ctas;
   int64_t narrow_keys, wide_keys;
-  int splits, pieces, key_tiles, groups, forms;
-  size_t off_stats, off_first, off_steps, off_images, off_tile_stats, off_sums, total;
+  int splits, pieces, key_tiles, groups, stream_rows;
+  size_t off_mirrors, off_stats, off_first, off_steps, off_images, off_tile_stats, off_sums, total;
 };
 
-// What a batch needs, from its mirrors alone (head_dim 128's images serve 64 too), and
-// which requests take the tcgen05 form (`wide`, if given).
+// What a batch needs, from its mirrors alone (head_dim 128's images serve 64 too).
 pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int Hkv, int window,
-                    MassPlan& pl, uint32_t* wide = nullptr) {
+                    MassPlan& pl) {
   pl = MassPlan{};
   const int64_t g = Hq / Hkv;
   int64_t narrow_keys = 0, wide_keys = 0;
@@ -1011,16 +1009,15 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
     if (q_len > 0) ++with_rows;
     if ((window > 0 && q_len > window ? window : q_len) * g > stream_rows) ++wide_reqs;
   }
-  // (more of them than a call's bits: all by the tcgen05 form, which takes any row)
-  pl.forms = wide_reqs == 0 ? kAllNarrow : wide_reqs == with_rows || R > kMixedReqs ? kAllWide : kByBits;
-  if (pl.forms == kAllWide) stream_rows = 0;
+  // (with them the requests without new tokens, so that one form flags what the device has of them)
+  if (wide_reqs == with_rows) stream_rows = -1;
+  pl.stream_rows = (int)stream_rows;
   for (int r = 0; r < R; ++r) {
     const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];
     if (q_len < 0 || (q_len > 0 && seq[r] < q_len)) return PA_ERR_INVALID;
     if (q_len == 0) continue;
     const int64_t rows = (window > 0 && q_len > window ? window : q_len) * g;
     if (rows > 0x3fffffff || seq[r] > kMostTokens) return PA_ERR_UNSUPPORTED;
-    if (rows > stream_rows && wide && pl.forms == kByBits) wide[r >> 5] |= 1u << (r & 31);
     if (rows <= stream_rows) {
       ++pl.narrow;
       pl.score_floats += (int64_t)Hkv * rows * (((int64_t)seq[r] + 15) & ~15ll);
@@ -1048,6 +1045,8 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   if (pl.n_tiles > 0x7fffffff / (int64_t)Hkv || pl.max_tiles > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   auto up = [](size_t x) { return (x + 1023) & ~(size_t)1023; };
   size_t at = up((size_t)pl.score_floats * 4);
+  pl.off_mirrors = at;
+  if (with_rows && R > kFewReqs) at = up(at + (size_t)R * sizeof(int2));
   pl.off_stats = at;
   if (pl.narrow) at = up(at + (size_t)R * Hkv * pl.groups * kNarrowRows * pl.splits * sizeof(float2));
   pl.off_first = at;
@@ -1104,9 +1103,20 @@ pa_status launch_after(void (*kernel)(KArgs...), dim3 grid, int threads, size_t 
   return launch_status();
 }
 
+pa_status set_mirrors(int2* out, const int32_t* qsl, const int32_t* seq, int R, cudaStream_t s) {
+  for (int r0 = 0; r0 < R; r0 += kMirrorsAtOnce) {
+    Mirrors m;
+    const int n = std::min(R - r0, kMirrorsAtOnce);
+    for (int i = 0; i < n; ++i) m.v[i] = make_int2(qsl[r0 + i + 1] - qsl[r0 + i], seq[r0 + i]);
+    mass_mirrors_kernel<<<1, (n + 31) & ~31, 0, s>>>(out + r0, n, m);
+    if (launch_status() != PA_OK) return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
 template <int D, bool F8>
 pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* pool,
-                   cudaStream_t s) {
+                   const int32_t* qsl_host, const int32_t* seq_host, cudaStream_t s) {
   static OncePerDevice once;
   constexpr size_t narrow_smem = 1024 + (size_t)kNarrowWarps * kNarrowRing + sizeof(NarrowTail);
   constexpr size_t wide_smem = WideSmem<D, F8>::kAlloc;
@@ -1121,27 +1131,30 @@ pa_status run_mass(const MassParams& p, const MassPlan& pl, const pa_kv_pool* po
                set((const void*)mass_tile_kernel<D, F8, true>, wide_smem);
       }))
     return PA_ERR_CUDA;
-  CUtensorMap tmap{};
-  pa_status st = PA_OK;
+  CUtensorMap tmap{}, tmap_tile{};
+  if ((pl.narrow && !cell_map<D, F8>(&tmap, pool->k_pool, pool->num_blocks, p.Hkv * p.B)) ||
+      (pl.n_tiles && !key_map(&tmap_tile, pool, p.B)))
+    return PA_ERR_CUDA;
+  const bool many = p.R > kFewReqs;
+  pa_status st = many ? set_mirrors(const_cast<int2*>(p.mirrors), qsl_host, seq_host, p.R, s) : PA_OK;
+  if (st != PA_OK) return st;
   if (pl.narrow) {
-    if (!cell_map<D, F8>(&tmap, pool->k_pool, pool->num_blocks, p.Hkv * p.B)) return PA_ERR_CUDA;
     const dim3 grid((unsigned)pl.splits, (unsigned)(p.Hkv * pl.groups), (unsigned)p.R);
     st = launch_after(pl.max_narrow_rows <= 8 ? mass_scores_kernel<D, F8, 1> : mass_scores_kernel<D, F8, 2>,
-                      grid, kNarrowWarps * 32, narrow_smem, s, false, tmap, p);
+                      grid, kNarrowWarps * 32, narrow_smem, s, many, tmap, p);
     if (st != PA_OK) return st;
     st = launch_after(mass_sum_kernel, dim3((unsigned)((pl.narrow_keys + p.sum_keys - 1) / p.sum_keys), (unsigned)p.R),
                       kSumThreads, (size_t)p.Hkv * pl.max_narrow_rows * 4, s, true, p);
     if (st != PA_OK) return st;
   }
   if (!pl.n_tiles) return PA_OK;
-  if (!key_map(&tmap, pool, p.B)) return PA_ERR_CUDA;
   st = launch_after(mass_rows_kernel<D, F8>, dim3((unsigned)pl.max_tiles, (unsigned)p.Hkv, (unsigned)p.R),
-                    kTile, 0, s, false, p);
+                    kTile, 0, s, many && !pl.narrow, p);
   if (st != PA_OK) return st;
   const dim3 ctas((unsigned)pl.ctas);
-  st = launch_after(mass_tile_kernel<D, F8, false>, ctas, kWideThreads, wide_smem, s, true, tmap, p);
+  st = launch_after(mass_tile_kernel<D, F8, false>, ctas, kWideThreads, wide_smem, s, true, tmap_tile, p);
   if (st != PA_OK) return st;
-  st = launch_after(mass_tile_kernel<D, F8, true>, ctas, kWideThreads, wide_smem, s, true, tmap, p);
+  st = launch_after(mass_tile_kernel<D, F8, true>, ctas, kWideThreads, wide_smem, s, true, tmap_tile, p);
   if (st != PA_OK) return st;
   return launch_after(mass_add_kernel, dim3((unsigned)((pl.wide_keys + kSumThreads - 1) / kSumThreads), (unsigned)p.R),
                       kSumThreads, 0, s, true, p);
@@ -1185,7 +1198,7 @@ extern "C" pa_status pa_attention_mass(
   if (qsl_host[0] != 0 || qsl_host[num_reqs] != num_tokens) return PA_ERR_INVALID;
   MassPlan pl;
   MassParams p{};
-  st = plan_mass(qsl_host, seq_lens_host, num_reqs, num_q_heads, pool->num_kv_heads, window, pl, p.wide);
+  st = plan_mass(qsl_host, seq_lens_host, num_reqs, num_q_heads, pool->num_kv_heads, window, pl);
   if (st != PA_OK) return st;
   for (int r = 0; r < num_reqs; ++r)
     if (qsl_host[r + 1] > qsl_host[r] && (seq_lens_host[r] > (int64_t)max_blocks * pool->block_size ||
@@ -1218,12 +1231,13 @@ extern "C" pa_status pa_attention_mass(
   p.qk_scale = scale * 1.44269504088896340736f * (f8 ? pool->k_scale : 1.f);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.scores = pl.narrow ? reinterpret_cast<float*>(ws) : nullptr;
-  p.score_floats = pl.score_floats;
+  p.mirrors = reinterpret_cast<const int2*>(ws + pl.off_mirrors);
   p.split_stats = reinterpret_cast<float2*>(ws + pl.off_stats);
   p.splits = pl.splits;
-  p.narrow_rows = (int)pl.max_narrow_rows;
   p.groups = pl.groups;
-  p.forms = pl.forms;
+  p.stream_rows = pl.stream_rows;
+  for (int r = 0; r < num_reqs && num_reqs <= kFewReqs; ++r)
+    p.few[r] = make_int2(qsl_host[r + 1] - qsl_host[r], seq_lens_host[r]);
   // Eight threads a key where a thread a key would leave SMs idle (3 decodes of 128 heads on
   // 200 tokens 9.6 us instead of 12.2, 13 x 4 to 6 tokens of 32 heads on 210 13 instead of
   // 28); else one, which joins the rows' statistics for more keys.
@@ -1231,17 +1245,15 @@ extern "C" pa_status pa_attention_mass(
   p.first_tile = reinterpret_cast<int*>(ws + pl.off_first);
   p.images = ws + pl.off_images;
   p.tile_stats = reinterpret_cast<float2*>(ws + pl.off_tile_stats);
-  p.n_tiles = (int)pl.n_tiles;
   p.first_step = reinterpret_cast<int64_t*>(ws + pl.off_steps);
   p.sums = reinterpret_cast<float*>(ws + pl.off_sums);
   p.steps = pl.steps;
   p.per_cta = pl.per_cta;
   p.pieces = pl.pieces;
-  p.key_tiles = pl.key_tiles;
   p.err = error_word();
   if (!p.err) return PA_ERR_CUDA;
   cudaStream_t s = as_stream(stream);
-  if (pool->head_dim == 128)
-    return f8 ? run_mass<128, true>(p, pl, pool, s) : run_mass<128, false>(p, pl, pool, s);
-  return f8 ? run_mass<64, true>(p, pl, pool, s) : run_mass<64, false>(p, pl, pool, s);
+  auto run = [&](auto kernels) { return kernels(p, pl, pool, qsl_host, seq_lens_host, s); };
+  if (pool->head_dim == 128) return f8 ? run(run_mass<128, true>) : run(run_mass<128, false>);
+  return f8 ? run(run_mass<64, true>) : run(run_mass<64, false>);
 }

@@ -106,3 +106,73 @@ def test_sparse_infinite_values(cuda_device):
     assert (got[0, :, 5] == np.inf).all() and (got[0, :, 6] == -np.inf).all()
     assert np.isnan(got[0, :, 7]).all() and np.isfinite(got[0, :, 8]).all()
     check(got, want, tol)
+
+
+# ------------------------------------------------- device lengths above the mirrors
+
+def mass_of(dev, rng, new, seqs, dev_new, dev_seqs, Hq, Hkv, D, B, fp8=False, window=0):
+    """One call planned for (new, seqs) on the device's lengths; what it wrote, and what it has
+    to write: nothing for the requests that are above their mirrors."""
+    R, most = len(new), [max(a, b) for a, b in zip(seqs, dev_seqs)]
+    table, _, blocks = batch(rng, most, most, B, dev)
+    pool = make_pool(rng, blocks, Hkv, B, D, fp8, dev)
+    qsl, dq = (np.cumsum([0] + list(x)).astype(np.int32) for x in (new, dev_new))
+    T = int(qsl[-1])
+    assert int(dq[-1]) <= T
+    q = torch.from_numpy(rng.standard_normal((T, Hq, D))).to(dev).bfloat16()
+    old = torch.rand((R, max(most) + 2), device=dev)
+    out = torch.full_like(old, 7.0)
+    sh = np.array(seqs, np.int32)
+    ws = torch.empty(pa.attention_mass_workspace_size(qsl, sh, Hq, Hkv, window), dtype=torch.uint8,
+                     device=dev)
+    ws.fill_(0xFF)
+    pa.attention_mass(q, old, out, i32(dq, dev), i32(dev_seqs, dev), qsl, sh, i32(table, dev), pool,
+                      0.125, workspace=ws, window=window)
+    above = [bool(a and (a > b or c > d)) for a, b, c, d in zip(dev_new, new, dev_seqs, seqs)]
+    assert pa.get_error() == (pa.PA_ERR_DEVICE_BOUNDS if any(above) else pa.PA_OK)
+    blank = np.full(old.shape, 7.0)
+    want, tol = ref.mass(ref.f64(q), ref.cells(pool.k), ref.f64(old), range(R), table, dq.tolist(),
+                         dev_seqs, B, Hq // Hkv, 0.125, pool.k_scale, 1.0, window, blank.copy(), fp8)
+    want[above] = 7.0
+    return ref.f64(out), want, tol
+
+
+@pytest.mark.parametrize("new,seqs,dev_new,dev_seqs", [
+    # a little more of one request where the other left room: none of it is written
+    ([1, 1], [900, 900], [1, 1], [1000, 500]),
+    ([40, 40], [900, 900], [40, 40], [1000, 500]),
+    ([40, 1], [500, 900], [40, 1], [510, 900]),
+    # an earlier request's excess takes nothing from those within their mirrors
+    ([1, 1, 1], [300, 300, 300], [1, 1, 1], [310, 300, 300]),
+    ([40, 30, 50], [300, 700, 300], [40, 30, 50], [700, 700, 300]),
+    ([40, 1, 50, 2], [300, 700, 300, 90], [40, 1, 50, 2], [300, 701, 300, 90]),
+    ([40, 1, 50, 2], [300, 700, 300, 90], [40, 1, 50, 2], [600, 700, 300, 90]),
+    # more new tokens than the mirror's, in either form and of a request that had none
+    ([1, 2, 1], [300, 300, 300], [2, 1, 1], [300, 300, 300]),
+    ([30, 40, 30], [300, 300, 300], [40, 30, 30], [300, 300, 300]),
+    ([0, 3, 2], [300, 300, 300], [1, 2, 2], [300, 300, 300]),
+    ([0, 60, 30], [300, 300, 300], [20, 40, 30], [300, 300, 300]),
+    ([1, 40, 1], [300, 300, 300], [20, 20, 1], [300, 300, 300]),
+], ids=str)
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_mass_above_the_mirrors(cuda_device, new, seqs, dev_new, dev_seqs, fp8):
+    """Flagged and left out request by request."""
+    check(*mass_of(cuda_device, np.random.default_rng(7), new, seqs, dev_new, dev_seqs, 8, 2, 64,
+                   16, fp8))
+
+
+def test_mass_above_the_window(cuda_device):
+    """Rows that the window cuts to the mirror's number do not make a request fit."""
+    check(*mass_of(cuda_device, np.random.default_rng(8), [20, 30], [300, 300], [30, 20],
+                   [300, 300], 4, 2, 64, 16, window=2))
+
+
+@pytest.mark.parametrize("R", [64, 65, 480, 481, 1300, 4200])
+@pytest.mark.parametrize("most", [1, 6])
+def test_mass_mirrors_of_many_requests(cuda_device, R, most):
+    """Mirrors that come with the launch, or by one or more of their own; every seventh request above its own."""
+    rng = np.random.default_rng(R + most)
+    new = rng.integers(0, most + 1, size=R).tolist()
+    seqs = [int(n + s) for n, s in zip(new, rng.integers(1, 60, size=R))]
+    dev_seqs = [s + (r % 7 == 3) for r, s in enumerate(seqs)]
+    check(*mass_of(cuda_device, rng, new, seqs, new, dev_seqs, 4, 1, 64, 16))
