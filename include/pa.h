@@ -770,8 +770,9 @@ pa_status pa_sparse_forward(const void* q, void* out, const int32_t* query_start
  * device lengths that stay at or below them, request by request; others set
  * PA_ERR_DEVICE_BOUNDS and are left out.
  * PA_ERR_INVALID: mirrors as for pa_forward, a length above mass_stride, a
- * workspace too small. PA_ERR_UNSUPPORTED: more than 65535 requests, a length
- * above 2^31 - 65536.
+ * workspace too small. PA_ERR_UNSUPPORTED: more than 65535 requests or kv heads,
+ * a length above 2^31 - 65536, 2^30 rows (counted queries times the heads of a kv
+ * head) of a request.
  */
 size_t pa_attention_mass_workspace_size(const int32_t* qsl_host, const int32_t* seq_lens_host,
                                         int32_t num_reqs, int32_t num_q_heads,

@@ -47,7 +47,9 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNarrowRows = 16;     // rows that a CTA of the streaming form takes
 constexpr int kStreamRows = 64;     // rows of a request of that form, at the most
 constexpr int kStreamUnits = 304;   // its CTAs, where they are to spare the tcgen05 form: one round
-constexpr int kSumRows = 12288;     // rows of all kv heads whose sums are at hand in shared memory
+// Rows of all kv heads whose sums are at hand in shared memory: 48 KB but for the 1 KB that
+// mass_sum_kernel has beside them.
+constexpr int kSumRows = (49152 - 1024) / 4;
 constexpr int kSplitKeys = 1024;    // keys of one of its CTAs
 constexpr int kTile = 128;          // rows, and keys, of a tcgen05 tile
 constexpr int kInfoBytes = 1024;    // behind an image: the score factors of its rows
@@ -394,6 +396,7 @@ __global__ void __launch_bounds__(kSumThreads, 5) mass_sum_kernel(const __grid_c
   float got = total.get();
   if (p.sum_keys < kSumThreads) {
     __shared__ float sums[kSumThreads];
+    static_assert(4 * kSumRows + sizeof(sums) <= 49152, "what a kernel has without asking for more");
     sums[threadIdx.x] = got;
     __syncthreads();
     if (part > 0) return;
@@ -993,7 +996,8 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   // instead of 46, 13 x 6 of 32 heads on 210 13 instead of 37. (Up to 128 rows and two rounds:
   // 2 x 16 tokens of 16 heads on 16 tokens 12 instead of 16, but 5 x 64 of 16 heads on 551 to
   // 1802, where the scores are written and read again, 60 instead of 26.)
-  int64_t stream_rows = kNarrowRows, units = 0, most = 0;
+  // (Of more kv heads than kSumRows / 16, fewer.)
+  int64_t stream_rows = std::min((int64_t)kNarrowRows, kSumRows / (int64_t)Hkv), units = 0, most = 0;
   for (int r = 0; r < R; ++r) {
     const int64_t q_len = (int64_t)qsl[r + 1] - qsl[r];
     const int64_t rows = (window > 0 && q_len > window ? window : q_len) * g;
@@ -1205,9 +1209,7 @@ extern "C" pa_status pa_attention_mass(
                                           seq_lens_host[r] > mass_stride))
       return PA_ERR_INVALID;
   if (!workspace || workspace_bytes < pl.total || !aligned16(workspace)) return PA_ERR_INVALID;
-  if (num_reqs > 65535 || pool->num_kv_heads > 65535 ||
-      pool->num_kv_heads * pl.max_narrow_rows > kSumRows)
-    return PA_ERR_UNSUPPORTED;
+  if (num_reqs > 65535 || pool->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.mass_in = mass_in;
   p.mass_out = mass_out;
