@@ -691,8 +691,9 @@ pa_status pa_update_block_bounds(const pa_kv_pool* pool, void* bounds,
  *            E4M3 pools only)
  *
  * fp32 sums; NaN bounds or queries give NaN. The last block of a chunk's token
- * is scored with all of its stored keys, also those after the token. At most 64
- * query heads a kv head (PA_ERR_UNSUPPORTED).
+ * is scored with all of its stored keys, also those after the token. A block id
+ * outside the pool sets PA_ERR_DEVICE_BOUNDS and scores as bounds of zeros. At most
+ * 64 query heads a kv head (PA_ERR_UNSUPPORTED).
  */
 pa_status pa_score_blocks(const void* q, const void* bounds, float* scores,
                           const int32_t* query_start_loc, const int32_t* seq_lens,

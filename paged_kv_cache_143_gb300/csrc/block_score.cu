@@ -194,6 +194,13 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// (a block id outside the pool: bounds of zeros)
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(on ? 16u : 0u)
+               : "memory");
+}
+
 struct ScoreParams {
   const __nv_bfloat16* q;
   const __nv_bfloat16* bounds;
@@ -395,8 +402,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 3) block_score_kernel(ScoreP
         for (int b = 0; b < 16; b += kAtOnce) {
           const int rec = b + lane / (32 / kAtOnce);
           const int from = __shfl_sync(kFull, use, rec);
-          if (from >= 0)
-            cp_async16(dst + rec * Rg::kPitch, p.bounds + ((int64_t)from * p.Hkv + kvh) * 2 * D + piece * 8);
+          cp_async16_or_zero(dst + rec * Rg::kPitch,
+                             p.bounds + ((int64_t)max(from, 0) * p.Hkv + kvh) * 2 * D + piece * 8, from >= 0);
         }
       }
       cp_async_commit();
@@ -514,12 +521,6 @@ struct ChunkTail {
 template <int D>
 constexpr size_t chunk_alloc() {
   return 1024 + ChunkSmem<D>::kOffTail + sizeof(ChunkTail);
-}
-
-__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(on ? 16u : 0u)
-               : "memory");
 }
 
 // Scores of one block (a thread's TMEM lane) for the tokens of a row tile whose tokens

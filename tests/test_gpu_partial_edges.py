@@ -186,3 +186,27 @@ def test_mass_of_many_heads(cuda_device, Hq, Hkv):
     got, want, tol = mass_of(cuda_device, np.random.default_rng(Hkv), [1], [18], [1], [18], Hq, Hkv,
                              64, 16)
     check(got, want, tol)
+
+
+# ---------------------------------------------------- block ids outside the pool
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 2), (9, 1)])
+@pytest.mark.parametrize("chunks", [False, True], ids=["decodes", "chunks"])
+def test_scores_of_blocks_outside_the_pool(cuda_device, chunks, Hq, Hkv):
+    """Such a block scores 0 in either form; every other block as it does."""
+    dev, B, D, blocks = cuda_device, 16, 128, 50
+    rng = np.random.default_rng(Hq)
+    seqs = [700, 900, 40] if chunks else rng.integers(30000, 60000, 30).tolist()
+    qsl = np.cumsum([0] + ([1, 60, 2] if chunks else [1] * 30))
+    table = rng.integers(0, blocks, (len(seqs), -(-max(seqs) // B)))  # (shared: bounds alone are read)
+    pool = make_pool(rng, blocks, Hkv, B, D, False, dev, fill=True)
+    bnd = torch.from_numpy(np.sort(rng.standard_normal((blocks, Hkv, 2, D)), axis=2)).to(dev).bfloat16()
+    q = torch.from_numpy(rng.standard_normal((int(qsl[-1]), Hq, D))).to(dev).bfloat16()
+    bad = rng.random(table.shape) < 0.1
+    asked = np.where(bad, rng.choice([-1, -5, blocks, blocks + 1, 2 ** 31 - 1], table.shape), table)
+    out = torch.full((int(qsl[-1]), Hkv, table.shape[1]), 7.0, device=dev)
+    pa.score_blocks(q, bnd, out, i32(qsl, dev), i32(seqs, dev), i32(asked, dev), pool)
+    assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS
+    with_zeros = np.concatenate([ref.f64(bnd), np.zeros((1, Hkv, 2, D))])
+    check(ref.f64(out), *ref.scores(ref.f64(q), with_zeros, np.where(bad, blocks, table), qsl, seqs,
+                                    B, Hq // Hkv, 1.0, np.full(out.shape, 7.0)))
