@@ -646,7 +646,8 @@ pa_status pa_latent_prefill(const void* q, int64_t q_token_stride, int64_t q_hea
  * and work are found from the device arrays at every launch, so captured calls
  * follow lengths that change between replays. Rows past
  * query_start_loc[num_reqs] are not touched. Device entries that leave the
- * buffers set PA_ERR_DEVICE_BOUNDS; what they would reach is skipped.
+ * buffers set PA_ERR_DEVICE_BOUNDS; what they would reach is neither read nor
+ * written.
  */
 
 /*
@@ -767,7 +768,8 @@ pa_status pa_sparse_forward(const void* q, void* out, const int32_t* query_start
  * fp32 scores, weights and sums, in an order that the sizes decide. The queries
  * of E4M3 pools are taken to 2^-17 of their row's largest element. A NaN or an
  * infinity in a query, or in a key that a query sees, makes that query's weights
- * NaN where its softmax is. The mirrors plan the launch: a captured call follows
+ * NaN where its softmax is. A block id outside the pool sets PA_ERR_DEVICE_BOUNDS
+ * and its keys count as zeros. The mirrors plan the launch: a captured call follows
  * device lengths that stay at or below them, request by request; others set
  * PA_ERR_DEVICE_BOUNDS and are left out.
  * PA_ERR_INVALID: mirrors as for pa_forward, a length above mass_stride, a

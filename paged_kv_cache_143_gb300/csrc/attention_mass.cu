@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
     id_lane = __ldg(table + (k0 + (lane * kNarrowWarps + warp) * kChunk) / p.B);
     if (id_lane < 0 || id_lane >= p.num_blocks) {
       raise_error(p.err, kErrBounds);
-      id_lane = 0;  // a valid block; the request's mass is then unspecified
+      id_lane = p.num_blocks;  // past the tensor map: keys of zeros
     }
   }
   auto issue = [&](int i) {  // the warp's i-th cell
@@ -700,10 +700,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (issued >= kStages) ok = wait(&t->empty[st], phase);
         if (!ok) break;
         const int64_t lb = (int64_t)(s.key_tile + k) * per_tile + my_blk;
-        bool on = my_blk < per_tile && lb * p.B < s.m.seq;
+        const bool on = my_blk < per_tile && lb * p.B < s.m.seq;
         if (on && (id < 0 || id >= p.num_blocks)) {
           raise_error(p.err, kErrBounds);
-          on = false;
+          id = p.num_blocks;  // past the tensor map: keys of zeros
         }
         const unsigned boxes = __popc(__ballot_sync(kFull, on));
         if (lane == 0) mbar_arrive_expect_tx(&t->full[st], boxes * (unsigned)(p.B * kBoxRow));

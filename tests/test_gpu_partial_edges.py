@@ -210,3 +210,31 @@ def test_scores_of_blocks_outside_the_pool(cuda_device, chunks, Hq, Hkv):
     with_zeros = np.concatenate([ref.f64(bnd), np.zeros((1, Hkv, 2, D))])
     check(ref.f64(out), *ref.scores(ref.f64(q), with_zeros, np.where(bad, blocks, table), qsl, seqs,
                                     B, Hq // Hkv, 1.0, np.full(out.shape, 7.0)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [[1, 2, 0, 1], [40, 30, 0, 70], [50, 1, 0, 3]],
+                         ids=["streamed", "tiles", "both"])
+def test_mass_of_blocks_outside_the_pool(cuda_device, new, fp8, D):
+    """The keys of such a block count as zeros, whichever form its request takes."""
+    dev, B, Hq, Hkv = cuda_device, 16, 8, 2
+    rng = np.random.default_rng(D + fp8)
+    seqs = [2100, 700, 300, 200]
+    table, qsl, blocks = batch(rng, seqs, new, B, dev)
+    pool = make_pool(rng, blocks, Hkv, B, D, fp8, dev)
+    q = torch.from_numpy(rng.standard_normal((int(qsl[-1]), Hq, D))).to(dev).bfloat16()
+    bad = (rng.random(table.shape) < 0.1) & (table >= 0)
+    bad[0, 0] = bad[1, 43] = bad[2, 0] = True
+    asked = np.where(bad, rng.choice([-1, -5, blocks, blocks + 1, 2 ** 31 - 1], table.shape), table)
+    old = torch.rand((4, 2200), device=dev)
+    out = torch.full_like(old, 7.0)
+    qh, sh = np.array(qsl, np.int32), np.array(seqs, np.int32)
+    ws = torch.empty(pa.attention_mass_workspace_size(qh, sh, Hq, Hkv), dtype=torch.uint8, device=dev)
+    pa.attention_mass(q, old, out, i32(qsl, dev), i32(seqs, dev), qh, sh, i32(asked, dev), pool, 0.125,
+                      workspace=ws)
+    assert pa.get_error() == pa.PA_ERR_DEVICE_BOUNDS
+    keys = ref.cells(pool.k)
+    check(ref.f64(out), *ref.mass(ref.f64(q), np.concatenate([keys, np.zeros_like(keys[:1])]),
+                                  ref.f64(old), range(4), np.where(bad, blocks, table), qsl, seqs, B,
+                                  Hq // Hkv, 0.125, pool.k_scale, 1.0, 0, np.full(old.shape, 7.0), fp8))
