@@ -479,18 +479,19 @@ extern "C" pa_status pa_sparse_forward(const void* q, void* out, const int32_t* 
   p.err = error_word();
   if (!p.err) return PA_ERR_CUDA;
   // A cluster shares a list where that many CTAs still run at once (three on an SM, two
-  // for more than 8 heads), and two CTAs where the lists are one to two times as many as
-  // run at once and a second round would be short; each warp keeps two blocks. Lists of
-  // 128 blocks of 16 keys (bf16, 8 kv heads), by the time of an earlier inner loop: 8
-  // decodes 31 us alone, 23 by 2 or 4, 31 by 8; 24: 45, 43, 47, 61; 64: 119, 109, 111,
-  // 141; 300 tokens of a chunk (64 blocks): 164, 201. As it is now, by this rule: 20.5,
-  // 41, 92, 96.
+  // for more than 8 heads), each warp keeping two blocks; and two CTAs share one of 128
+  // blocks or more where the lists are up to a third more than run at once, so that the
+  // second round is half as long. Lists of 128 blocks of 16 keys (bf16, 8 kv heads), us by
+  // 1, 2, 4 and 8 CTAs: 8 decodes 27, 22, 20, 27; 16: 31, 31, 37, 39; 40: 57, 61, 65, 78. Up
+  // to a third more than at once, by 1 and 2: 64 decodes on 128 blocks 96 and 94, on 256 184
+  // and 166, E4M3 117 and 111, on 32 blocks 33 and 39; 46 of 16 heads a kv head on 256 160
+  // and 143. Beyond: 80 decodes on 128 104 and 111, 100 E4M3 76 and 86, 300 tokens of a chunk
+  // (64 blocks) 96 and 133.
   const int64_t units = (int64_t)num_tokens * p.Hkv * p.parts;
   const int64_t at_once = (int64_t)(wide ? 2 : 3) * num_sms();
   p.split = 1;
-  while (p.split < 8 && k >= 4 * kSparseWarps * p.split &&
-         (units * 2 * p.split <= at_once || (p.split == 1 && units > at_once && units < 2 * at_once)))
-    p.split *= 2;
+  while (p.split < 8 && k >= 4 * kSparseWarps * p.split && units * 2 * p.split <= at_once) p.split *= 2;
+  if (k >= 128 && units > at_once && 3 * units <= 4 * at_once) p.split = 2;
   if (units * p.split > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   const int64_t ctas = units * p.split;
   cudaStream_t s = as_stream(stream);
