@@ -29,8 +29,8 @@
 // E4M3 pools: the codes are multiplied as they are. In the streaming form they widen to
 // f16; on tcgen05 a query is the sum of two E4M3 numbers (8 significant bits, all
 // that bf16 has) after a power-of-two scale that puts its row's largest magnitude
-// into [2^7, 2^8): exact for elements down to 2^-8 of that one, off by 2^-18 of it
-// below.
+// into [2^7, 2^8): exact for elements down to 2^-8 of that one, off by 2^-17 of it
+// at the most below. (Half a step of 2^-9, the smallest of E4M3, of 2^7.)
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -306,7 +306,7 @@ __device__ __forceinline__ float lse_of(const float2* s, int n, int64_t step) {
   for (int i = 0; i < n; ++i) ref = fmaxf(ref, s[i * step].x);
   const float base = ref == -INFINITY ? 0.f : ref;
   for (int i = 0; i < n; ++i) sum += s[i * step].y * ex2_ftz(s[i * step].x - base);
-  return ref + log2f(sum);  // NaN for a row that scores -inf throughout
+  return ref + log2f(sum);  // (-inf for a row that scores -inf throughout: its weights are then NaN)
 }
 
 // A long sum of parts: what the roundings of the sum lost is put back at the end.
@@ -317,8 +317,8 @@ struct Total {
     low = x - (next - sum);
     sum = next;
   }
-  // (a NaN sum, or an infinite one, has lost no rounding)
-  __device__ __forceinline__ float get() const { return isnan(low) ? sum : sum + low; }
+  // (of a sum that is not finite nothing is put back)
+  __device__ __forceinline__ float get() const { return isfinite(low) ? sum + low : sum; }
 };
 
 // *src, or 0: predicated, so that loads go out one after the other.
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kSumThreads, 5) mass_sum_kernel(const __grid_c
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1)
       join_stats(ref, sum, __shfl_xor_sync(kFull, ref, o), __shfl_xor_sync(kFull, sum, o));
-    if (lane == 0 && x < rows) lse[x] = ref + log2f(sum);  // NaN for a row that scores -inf throughout
+    if (lane == 0 && x < rows) lse[x] = ref + log2f(sum);  // (as lse_of)
   }
   __syncthreads();
   const int part = (int)threadIdx.x / p.sum_keys, key = key0 + (int)threadIdx.x % p.sum_keys;
@@ -1039,7 +1039,8 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   pl.wide_keys = wide_keys;
   pl.splits = (int)((narrow_keys + kSplitKeys - 1) / kSplitKeys);
   pl.key_tiles = (int)((wide_keys + kTile - 1) / kTile);
-  // An equal run of steps for each of 152 SMs, but four at the least where that keeps the
+  // An equal run of steps for each of 152 SMs (whatever the device has: the workspace's size
+  // is asked for without one), but four at the least where that keeps the
   // pieces of a row tile, whose statistics are joined, below ten.
   const int64_t least = (pl.key_tiles + 7) / 8 < 4 ? (pl.key_tiles + 7) / 8 : 4;
   pl.per_cta = std::max((pl.steps + 151) / 152, std::max(least, (int64_t)1));
