@@ -238,3 +238,65 @@ def test_mass_of_blocks_outside_the_pool(cuda_device, new, fp8, D):
     check(ref.f64(out), *ref.mass(ref.f64(q), np.concatenate([keys, np.zeros_like(keys[:1])]),
                                   ref.f64(old), range(4), np.where(bad, blocks, table), qsl, seqs, B,
                                   Hq // Hkv, 0.125, pool.k_scale, 1.0, 0, np.full(old.shape, 7.0), fp8))
+
+
+# ------------------------------------------------------- long contexts, captured calls
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [[1, 2, 1], [30, 40, 1]], ids=["streamed", "tiles and streamed"])
+def test_mass_of_long_contexts(cuda_device, new, fp8):
+    """Many splits and key tiles, row tiles cut into pieces for many CTAs."""
+    seqs = [40000, 9000, 17001]
+    check(*mass_of(cuda_device, np.random.default_rng(11), new, seqs, new, seqs, 6, 2, 128, 64, fp8))
+
+
+@pytest.mark.parametrize("R", [6, 70])
+def test_captured_mass_of_e4m3_pools(cuda_device, R):
+    """A captured call keeps the mirrors that it was captured with, whatever becomes of the host
+    arrays, and follows device lengths up to them; one above its own is flagged and left out."""
+    dev, B, Hq, Hkv, D = cuda_device, 16, 8, 2, 64
+    rng = np.random.default_rng(R)
+    new = [int(x) for x in rng.choice([1, 2, 5, 20], R)]
+    seqs = [int(x) for x in rng.integers(200, 400, R)]
+    table, qsl, blocks = batch(rng, [n + 16 for n in seqs], new, B, dev)
+    pool = make_pool(rng, blocks, Hkv, B, D, True, dev)
+    tab, dq, ds = i32(table, dev), i32(qsl, dev), i32(seqs, dev)
+    q = torch.zeros((int(qsl[-1]), Hq, D), dtype=torch.bfloat16, device=dev)
+    old, out = torch.rand((R, 420), device=dev), torch.zeros((R, 420), device=dev)
+    qh, sh = np.array(qsl, np.int32), np.array(seqs, np.int32)
+    ws = torch.empty(pa.attention_mass_workspace_size(qh, sh, Hq, Hkv), dtype=torch.uint8, device=dev)
+
+    def call():
+        pa.attention_mass(q, old, out, dq, ds, qh, sh, tab, pool, 0.125, decay=0.5, workspace=ws)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        call()
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        call()
+    qh[:], sh[:] = 0, 0
+    for turn in range(4):
+        some = [int(rng.integers(0, n + 1)) for n in new] if turn else new
+        lens = [int(rng.integers(max(a, 1), n + 1)) for a, n in zip(some, seqs)] if turn else list(seqs)
+        above = []
+        if turn == 3:
+            above = [r for r in range(0, R, 5) if some[r]]
+            for r in above:
+                lens[r] = seqs[r] + 1 + r % 16
+        qs = np.cumsum([0] + some)
+        dq.copy_(i32(qs, dev))
+        ds.copy_(i32(lens, dev))
+        q.copy_(torch.from_numpy(rng.standard_normal(tuple(q.shape))).to(dev).bfloat16())
+        ws.fill_(0xFF)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert pa.get_error() == (pa.PA_ERR_DEVICE_BOUNDS if above else pa.PA_OK)
+        want, tol = ref.mass(ref.f64(q), ref.cells(pool.k), ref.f64(old), range(R), table, qs.tolist(),
+                             lens, B, Hq // Hkv, 0.125, pool.k_scale, 0.5, 0, np.full((R, 420), 7.0),
+                             True)
+        want[above] = 7.0
+        check(ref.f64(out), want, tol)
