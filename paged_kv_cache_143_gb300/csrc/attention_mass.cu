@@ -116,6 +116,18 @@ __device__ __forceinline__ MassReq rows_of(const MassParams& p, int r) {
   m.rows = m.w * p.g;
   return m;
 }
+// The same of a request that mass_rows_kernel gave tiles, and so has held against its mirror
+// (whose place in the parameters would be one more first access, 1 us of each pass).
+__device__ __forceinline__ MassReq tiled_rows_of(const MassParams& p, int r) {
+  MassReq m;
+  m.q0 = p.qsl[r];
+  m.q_len = p.qsl[r + 1] - m.q0;
+  m.seq = p.seq_lens[r];
+  m.w = p.window > 0 ? min(m.q_len, p.window) : m.q_len;
+  m.rows = m.w * p.g;
+  m.wide = true;
+  return m;
+}
 // Whether request r was left out for entries that leave the buffers.
 __device__ __forceinline__ bool bad_request(const MassReq& m) { return m.rows == 0 && m.q_len != 0; }
 
@@ -591,10 +603,10 @@ __device__ __forceinline__ Segment segment_at(const MassParams& p, int64_t f, in
   Segment s;
   s.r = warp_last_le(p.R, f, [&](int x) { return p.first_step[x]; });
   const int64_t base = p.first_step[s.r], over = p.first_step[s.r + 1];
-  s.m = rows_of(p, s.r);
+  s.m = tiled_rows_of(p, s.r);
   s.tile = p.first_tile[s.r];
   const int tiles = tiles_of(s.m), keys = (s.m.seq + kTile - 1) / kTile;
-  s.on = s.tile >= 0 && tiles > 0;
+  s.on = s.tile >= 0;
   s.next = min(end, over);
   if (s.next <= f) s.next = end;  // (cannot be: f lies within the request)
   if (!s.on) return s;
@@ -957,7 +969,7 @@ __global__ void __launch_bounds__(kSumThreads) mass_add_kernel(const __grid_cons
   grid_dependency_wait();
   const int r = blockIdx.y;
   if (p.first_tile[r] < 0) return;
-  const MassReq m = rows_of(p, r);
+  const MassReq m = tiled_rows_of(p, r);
   const int key = blockIdx.x * kSumThreads + (int)threadIdx.x;
   if (key >= m.seq) return;
   const int key_tiles = (m.seq + kTile - 1) / kTile, units = tiles_of(m) * p.Hkv;
