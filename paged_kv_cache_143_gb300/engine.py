@@ -216,7 +216,9 @@ class SparseEngine(Engine):
     heads attend to `num_selected` blocks of their kv head, chosen by the bounds
     of the blocks' keys (pa_score_blocks) with the first `first` and the newest
     `last` among them. Contexts of no more blocks than that are attended to
-    whole, as Engine does."""
+    whole, as Engine does (a token at a time: long chunks on short contexts are
+    Engine's work). Keeps the scores of max_tokens tokens for all of max_blocks:
+    4 * max_tokens * num_kv_heads * max_blocks bytes."""
 
     def __init__(self, sched: "pa.Scheduler", pool: "pa.KVPool", num_q_heads: int, max_reqs: int,
                  max_blocks: int, max_tokens: int, scale: float, num_selected: int,
