@@ -79,7 +79,7 @@ struct MassParams {
   int sum_keys;            // keys of a CTA of the sums
   // tcgen05 form: a step is a row tile of a kv head and a key tile; request r's are the
   // flat steps first_step[r] + (kvh * tiles + row tile) * key tiles + key tile
-  int* first_tile;         // [R], -1: not of this form
+  int4* tiled;             // [R]: first tile (-1: none), first row of q, new tokens, stored tokens
   int64_t* first_step;     // [R + 1]
   uint8_t* images;         // [n_tiles][Hkv][image]
   float2* tile_stats;      // [n_tiles][Hkv][pieces][4][128]
@@ -116,13 +116,12 @@ __device__ __forceinline__ MassReq rows_of(const MassParams& p, int r) {
   m.rows = m.w * p.g;
   return m;
 }
-// The same of a request that mass_rows_kernel gave tiles, and so has held against its mirror
-// (whose place in the parameters would be one more first access, 1 us of each pass).
-__device__ __forceinline__ MassReq tiled_rows_of(const MassParams& p, int r) {
+// The same of a request as mass_rows_kernel has held it against its mirror and put it down.
+__device__ __forceinline__ MassReq tiled_rows_of(const MassParams& p, const int4& t) {
   MassReq m;
-  m.q0 = p.qsl[r];
-  m.q_len = p.qsl[r + 1] - m.q0;
-  m.seq = p.seq_lens[r];
+  m.q0 = t.y;
+  m.q_len = t.z;
+  m.seq = t.w;
   m.w = p.window > 0 ? min(m.q_len, p.window) : m.q_len;
   m.rows = m.w * p.g;
   m.wide = true;
@@ -463,13 +462,13 @@ __global__ void __launch_bounds__(kTile) mass_rows_kernel(const __grid_constant_
     if (tid == 0 && r == p.R - 1) p.first_step[p.R] = step + steps_of(p, m);
   }
   if (!tiles) {
-    if (reporter) p.first_tile[r] = -1;
+    if (reporter) p.tiled[r] = make_int4(-1, 0, 0, 0);
     return;
   }
   if (ti >= tiles) return;
   const bool has_row = mass_row(p, r) >= 0;
   if (reporter) {
-    p.first_tile[r] = has_row ? (int)first : -1;
+    p.tiled[r] = make_int4(has_row ? (int)first : -1, m.q0, m.q_len, m.seq);
     if (!has_row) raise_error(p.err, kErrBounds);
   }
   if (!has_row) return;
@@ -603,8 +602,9 @@ __device__ __forceinline__ Segment segment_at(const MassParams& p, int64_t f, in
   Segment s;
   s.r = warp_last_le(p.R, f, [&](int x) { return p.first_step[x]; });
   const int64_t base = p.first_step[s.r], over = p.first_step[s.r + 1];
-  s.m = tiled_rows_of(p, s.r);
-  s.tile = p.first_tile[s.r];
+  const int4 t = p.tiled[s.r];
+  s.m = tiled_rows_of(p, t);
+  s.tile = t.x;
   const int tiles = tiles_of(s.m), keys = (s.m.seq + kTile - 1) / kTile;
   s.on = s.tile >= 0;
   s.next = min(end, over);
@@ -968,8 +968,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 __global__ void __launch_bounds__(kSumThreads) mass_add_kernel(const __grid_constant__ MassParams p) {
   grid_dependency_wait();
   const int r = blockIdx.y;
-  if (p.first_tile[r] < 0) return;
-  const MassReq m = tiled_rows_of(p, r);
+  const int4 t = p.tiled[r];
+  if (t.x < 0) return;
+  const MassReq m = tiled_rows_of(p, t);
   const int key = blockIdx.x * kSumThreads + (int)threadIdx.x;
   if (key >= m.seq) return;
   const int key_tiles = (m.seq + kTile - 1) / kTile, units = tiles_of(m) * p.Hkv;
@@ -993,7 +994,7 @@ struct MassPlan {
   int64_t score_floats, narrow, n_tiles, max_tiles, max_narrow_rows, steps, per_cta, ctas;
   int64_t narrow_keys, wide_keys;
   int splits, pieces, key_tiles, groups, stream_rows;
-  size_t off_mirrors, off_stats, off_first, off_steps, off_images, off_tile_stats, off_sums, total;
+  size_t off_mirrors, off_stats, off_tiled, off_steps, off_images, off_tile_stats, off_sums, total;
 };
 
 // What a batch needs, from its mirrors alone (head_dim 128's images serve 64 too).
@@ -1066,8 +1067,8 @@ pa_status plan_mass(const int32_t* qsl, const int32_t* seq, int R, int Hq, int H
   if (with_rows && R > kFewReqs) at = up(at + (size_t)R * sizeof(int2));
   pl.off_stats = at;
   if (pl.narrow) at = up(at + (size_t)R * Hkv * pl.groups * kNarrowRows * pl.splits * sizeof(float2));
-  pl.off_first = at;
-  if (pl.n_tiles) at = up(at + (size_t)R * sizeof(int));
+  pl.off_tiled = at;
+  if (pl.n_tiles) at = up(at + (size_t)R * sizeof(int4));
   pl.off_steps = at;
   if (pl.n_tiles) at = up(at + ((size_t)R + 1) * sizeof(int64_t));
   pl.off_images = at;
@@ -1257,7 +1258,7 @@ extern "C" pa_status pa_attention_mass(
   // 200 tokens 9.6 us instead of 12.2, 13 x 4 to 6 tokens of 32 heads on 210 13 instead of
   // 28); else one, which joins the rows' statistics for more keys.
   p.sum_keys = (pl.narrow_keys + kSumThreads - 1) / kSumThreads * num_reqs <= num_sms() ? kSumThreads / 8 : kSumThreads;
-  p.first_tile = reinterpret_cast<int*>(ws + pl.off_first);
+  p.tiled = reinterpret_cast<int4*>(ws + pl.off_tiled);
   p.images = ws + pl.off_images;
   p.tile_stats = reinterpret_cast<float2*>(ws + pl.off_tile_stats);
   p.first_step = reinterpret_cast<int64_t*>(ws + pl.off_steps);
