@@ -732,12 +732,12 @@ pa_status pa_select_blocks(const float* scores, const int32_t* query_start_loc,
  *             no visible key. A block named twice counts twice.
  *
  * Computed in fp32 and rounded once to bf16; the softmax weights enter the
- * second product as sums of two 16-bit numbers, off by 2^-15 at the most. A row without a visible key is zero; one
- * that scores every visible key -inf, and one that meets a NaN, is NaN. Cells
- * past a token's position may hold anything. The order of sums depends on the
- * sizes of the call alone. Needs no workspace; any number of query heads a kv
- * head. An entry below -1 or past max_blocks, or a block id outside the pool,
- * sets PA_ERR_DEVICE_BOUNDS and is skipped.
+ * second product as sums of two 16-bit numbers, off by 2^-15 at the most. A row
+ * without a visible key is zero; one that scores every visible key -inf, and one
+ * that meets a NaN, is NaN. Cells past a token's position may hold anything. The
+ * order of sums depends on the sizes of the call alone. Needs no workspace; any
+ * number of query heads a kv head. An entry below -1 or past max_blocks, or a
+ * block id outside the pool, sets PA_ERR_DEVICE_BOUNDS and is skipped.
  */
 pa_status pa_sparse_forward(const void* q, void* out, const int32_t* query_start_loc,
                             const int32_t* seq_lens, const int32_t* block_tables,
